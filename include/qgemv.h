@@ -74,7 +74,9 @@ typedef enum {
     QG_ERR_UNSUPPORTED = 3,     /* valid request this build does not handle  */
     QG_ERR_WORKSPACE = 4,       /* workspace missing or too small            */
     QG_ERR_CUDA = 5,            /* a CUDA runtime call or launch failed      */
-    QG_ERR_DEVICE_TIMEOUT = 6   /* a kernel's bounded wait gave up           */
+    QG_ERR_DEVICE_TIMEOUT = 6,  /* a kernel's bounded wait gave up           */
+    QG_ERR_BAD_INDEX = 7        /* a kernel met a slot or block id outside   */
+                                /* the cache and skipped it                  */
 } qg_status;
 
 /* Static, human-readable name of a status. Never NULL. */
@@ -530,6 +532,178 @@ QG_API qg_status gemm_w8a8_hadamard(const uint16_t *x_bf16, const uint32_t *sign
 QG_API size_t qg_w8a8_hadamard_workspace_size(int M, int K);
 
 /*
+ * The decode step around the products: a paged key/value cache held in 8 bits
+ * (its block plan, the append, the attention over it) and the residual RMS
+ * norm. The pages leave these out ("Krill Teardown", "Core mechanisms", names
+ * the paged cache; the Uzu article, "Producing several tokens from one model
+ * pass", the tree verification); the formulas are stated here.
+ *
+ * The cache. Tokens live in blocks of block_size slots; a block holds every
+ * key/value head of its tokens:
+ *   k_cache, v_cache  8-bit codes [num_blocks][Hkv][block_size][D], int8
+ *                     (QG_KV_I8, codes -127..127) or e4m3 (QG_KV_E4M3);
+ *   scales            fp32 [num_blocks][Hkv][2]: one scale per block and head,
+ *                     [0] of its keys, [1] of its values; >= 0.
+ *   value = scale * code. block_size is a multiple of 16, 16..1024.
+ * A request's block_table row lists its blocks: token p is slot
+ * table[p / block_size] * block_size + p % block_size. Table rows hold
+ * max_blocks entries; entries past a request's last block are not read.
+ * Sizes whose products pass 2^31 are addressed in 64 bits;
+ * num_blocks * block_size < 2^31 (slots are int32).
+ */
+typedef enum { QG_KV_I8 = 0, QG_KV_E4M3 = 1 } qg_kv_format;
+typedef enum { QG_DT_BF16 = 0, QG_DT_F32 = 1 } qg_dtype;
+
+/*
+ * kv8_block_plan -- grows and shrinks the requests' block lists on the GPU and
+ * maps the new tokens to slots, from the requests' lengths alone.
+ *
+ *   old_lens, new_lens  int32 [R]: tokens of each request before and after; R
+ *                1..4096. new > old: the request grows (a decode step, drafts,
+ *                a prompt); new < old: it gives back the blocks past
+ *                ceil(new / block_size) (rejected drafts; 0 = it ends).
+ *   block_table  int32 [R][max_blocks] (in/out): the entries of blocks taken
+ *                are written, nothing else.
+ *   free_list    int32 [num_blocks] (in/out), a stack: entries 0..count-1 are
+ *                free block ids. With released blocks ranked in (request,
+ *                block) order, rank j goes to free_list[top - 1 - j], top =
+ *                count + released; blocks taken, ranked the same way, come
+ *                from free_list[top - 1 - j]. So shrinking back what was
+ *                grown restores the stack.
+ *   free_count   int32 [1]: count. free_count_out int32 [1] (output): top -
+ *                taken; may be the same address as free_count.
+ *   cu_new       int32 [R + 1] (output): prefix sums of max(new - old, 0).
+ *   slot_map     int32 [max_tokens] (output): slot of each new token, in
+ *                request order; -1 past the last.
+ *   positions    int32 [max_tokens] (output): its position in the request; -1
+ *                past the last.
+ *   info         int32 [4] (output): new tokens, blocks taken, blocks
+ *                released, state: 0 done; otherwise nothing is taken or
+ *                released, cu_new is 0 and slot_map and positions are -1
+ *                everywhere: 1 too few free blocks, 2 a request outgrows
+ *                max_blocks, 3 more than max_tokens new tokens, 4 a negative
+ *                length or a free_count outside 0..num_blocks (or a release
+ *                that would pass num_blocks).
+ *   workspace    qg_kv8_plan_workspace_size() bytes, 16-byte aligned,
+ *                zero-filled before its first use; every call leaves it at
+ *                zero, so calls ordered on one stream may share it.
+ * One launch; capturable in a CUDA graph.
+ */
+QG_API qg_status kv8_block_plan(const int32_t *old_lens, const int32_t *new_lens, int R, int block_size,
+                                int32_t *block_table, int max_blocks, int32_t *free_list, int num_blocks,
+                                const int32_t *free_count, int32_t *free_count_out, int32_t *cu_new,
+                                int32_t *slot_map, int32_t *positions, int max_tokens, int32_t *info,
+                                void *workspace, size_t ws_bytes, void *stream);
+QG_API size_t qg_kv8_plan_workspace_size(void);
+
+/*
+ * kv8_append -- quantizes the new tokens' keys and values into their slots.
+ *
+ *   k, v         [T][Hkv][D], bf16 or fp32 (dtype), token t at element
+ *                t * k_stride (v_stride) (>= Hkv * D, a multiple of 8): the
+ *                projections' outputs, also as slices of a fused q/k/v row.
+ *                Finite values.
+ *   slot_map     int32 [T]; a negative slot is skipped (padding); one outside
+ *                the cache is skipped and reported (qg_device_error). The
+ *                slots of one block are consecutive in T and ascending by 1
+ *                (as kv8_block_plan gives them): a run.
+ *   T >= 1, 1 <= Hkv <= 1024, D a multiple of 16 in 16..256.
+ * Per run (first slot f of its block), head and cache, in fp32 with IEEE
+ * rounding, qmax = 127 (int8) or 448 (e4m3):
+ *   s0 = f > 0 ? scale : 0;  s = max(s0, max|x| / qmax)  becomes the scale;
+ *   slots before f: code = round(code * (s0 / s)) when s > s0;
+ *   the run: code = round(x / s) (to nearest even, clamped to +-qmax);
+ *   f = 0 (a new block): the slots after the run are set to 0.
+ *   s = 0 (all values 0) gives codes 0. Other slots keep their codes. So a
+ *   block's scale only grows while it fills, and each growth rounds its earlier
+ *   codes once more (by at most half a step of the new scale).
+ * Results are exact functions of the inputs (no sums are formed).
+ */
+QG_API qg_status kv8_append(const void *k, const void *v, int dtype, int64_t k_stride, int64_t v_stride,
+                            const int32_t *slot_map, int T, int Hkv, int D, int block_size, int num_blocks,
+                            int format, void *k_cache, void *v_cache, float *scales, void *stream);
+
+/*
+ * kv8_read -- blocks back as the values they stand for: for saving or moving a
+ * prefix, and for checks.
+ *   block_ids    int32 [B], B >= 1 (an id outside the cache gives zeros and is
+ *                reported by qg_device_error).
+ *   k, v         bf16 [B][Hkv][block_size][D] (outputs): scale * code, rounded
+ *                to nearest even.
+ *   scales_out   fp32 [B][Hkv][2] (output): the blocks' scales.
+ */
+QG_API qg_status kv8_read(const int32_t *block_ids, int B, int Hkv, int D, int block_size, int num_blocks,
+                          int format, const void *k_cache, const void *v_cache, const float *scales,
+                          uint16_t *k, uint16_t *v, float *scales_out, void *stream);
+
+/*
+ * attn_kv8_paged -- attention of the step's query tokens over the cache.
+ *
+ *   q_bf16       bf16 [T][Hq][D], token t at element t * q_stride (>= Hq * D,
+ *                a multiple of 8).
+ *   cu_q         int32 [R + 1]: request r's query tokens are cu_q[r] ..
+ *                cu_q[r+1] - 1 (none is allowed); 0 <= cu_q <= T, ascending.
+ *   ctx_lens     int32 [R]: tokens of request r in the cache, its n query
+ *                tokens (the last n) among them; at most max_blocks *
+ *                block_size (longer ones are cut there and reported).
+ *   block_table  int32 [R][max_blocks]; a block id outside the cache is
+ *                skipped (its tokens count as unseen) and reported.
+ *   tree_mask    NULL: query token i of n sees the tokens 0 .. ctx - n + i.
+ *                Otherwise uint32 [T]: it sees the tokens 0 .. ctx - n - 1, and
+ *                token ctx - n + j (j < 32) where bit j of its word is set (an
+ *                ancestor in a draft tree, or itself); requests of more than
+ *                32 query tokens ignore it.
+ *   out_bf16     bf16 [T][Hq][D] (output), Hq a multiple of Hkv, kv head =
+ *                hq / (Hq / Hkv):
+ *                sum_j p_j v_j, p = softmax over the seen tokens j of
+ *                softmax_scale * q . k_j; 0 where no token is seen. Rows of T
+ *                past cu_q[R] are not written.
+ *   R 1..1024, T >= 1, D a multiple of 16 in 16..256 (64, 128 and 256 run on
+ *   the tensor cores, the others on a plain kernel), Hq <= 1024.
+ *   workspace    qg_attn_kv8_workspace_size(Hq, Hkv, D) bytes, 16-byte aligned,
+ *                zero-filled before its first use: its counters are left at
+ *                zero by every call, the rest is scratch. Calls that may
+ *                overlap need separate workspaces.
+ * Scores, maxima and sums are fp32, probabilities enter the value product as
+ * fp16 (relative rounding 2^-11); the split of a context over the GPU, and so
+ * the order of the sums, depends on the shapes and lengths alone.
+ */
+QG_API qg_status attn_kv8_paged(const uint16_t *q_bf16, int64_t q_stride, const void *k_cache,
+                                const void *v_cache, const float *scales, const int32_t *block_table,
+                                const int32_t *ctx_lens, const int32_t *cu_q, const uint32_t *tree_mask, int R,
+                                int T, int Hq, int Hkv, int D, int block_size, int num_blocks, int max_blocks,
+                                int format, float softmax_scale, uint16_t *out_bf16, void *workspace,
+                                size_t ws_bytes, void *stream);
+QG_API size_t qg_attn_kv8_workspace_size(int Hq, int Hkv, int D);
+
+/*
+ * rmsnorm_residual / rmsnorm_residual_i8 -- the residual addition and the RMS
+ * norm before a product, as bf16 (the W4A16 products) or as int8 codes with a
+ * scale per row (the W8A8 products).
+ *
+ *   x            [M][K], bf16 or fp32 (x_dtype): the last product's output.
+ *   residual     [M][K], bf16 or fp32 (res_dtype), or NULL for 0.
+ *   residual_out [M][K] (output), res_dtype: h = x + residual rounded to
+ *                nearest even; may be the same address as residual; NULL only
+ *                if residual is NULL too (then h = x, which is not stored).
+ *   weight       [K], bf16 or fp32 (w_dtype).
+ *   y = (h * rsqrt(mean(h^2) + eps)) * weight in fp32, h as stored.
+ *   rmsnorm_residual:     out_bf16 [M][K] = y, rounded to nearest even.
+ *   rmsnorm_residual_i8:  z = y, or with sign_bits (uint32 [K/32], may be
+ *                NULL) the randomized Hadamard transform of y's 32-blocks
+ *                exactly as in hadamard32_quant_i8; scale[m] = max|z| / 127,
+ *                q = clamp(rint(z / scale), -127, 127); an all-zero row gives
+ *                scale 0 and codes 0. The codes feed gemm_w8a8_i32.
+ *   M >= 1; K a multiple of 32, at most 32768; eps >= 0; finite values.
+ */
+QG_API qg_status rmsnorm_residual(const void *x, int x_dtype, const void *residual, int res_dtype,
+                                  const void *weight, int w_dtype, float eps, int M, int K, void *residual_out,
+                                  uint16_t *out_bf16, void *stream);
+QG_API qg_status rmsnorm_residual_i8(const void *x, int x_dtype, const void *residual, int res_dtype,
+                                     const void *weight, int w_dtype, float eps, const uint32_t *sign_bits, int M,
+                                     int K, void *residual_out, int8_t *q, float *scale, void *stream);
+
+/*
  * qg_workspace_size -- the single workspace query of the boundary: device
  * bytes the operation `op` needs for the given shape, group size 64 where
  * the operation has one (M, N, K for the W4A16 and W8A8 products; T, E,
@@ -562,8 +736,10 @@ QG_API void qg_set_pdl(int enable);
 /*
  * qg_device_error -- the sticky device-side error word of the current device:
  * 0 when no kernel has given up a bounded wait, otherwise a nonzero code
- * naming where it gave up. Synchronizes the device. With clear != 0 the word
- * is reset to 0. Returns QG_ERR_DEVICE_TIMEOUT when the word was nonzero.
+ * naming where it gave up (0x6xx: where a kernel of the paged cache met a slot
+ * or block id outside the cache, or a length past its table, and skipped it).
+ * Synchronizes the device. With clear != 0 the word is reset to 0. Returns
+ * QG_ERR_DEVICE_TIMEOUT when the word was nonzero, QG_ERR_BAD_INDEX for 0x6xx.
  */
 QG_API qg_status qg_device_error(uint32_t *code, int clear);
 

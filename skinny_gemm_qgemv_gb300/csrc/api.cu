@@ -86,6 +86,7 @@ const char* qg_status_string(qg_status s) {
     case QG_ERR_UNSUPPORTED: return "QG_ERR_UNSUPPORTED: valid request this build does not handle";
     case QG_ERR_WORKSPACE: return "QG_ERR_WORKSPACE: workspace missing or too small";
     case QG_ERR_CUDA: return "QG_ERR_CUDA: a CUDA runtime call or kernel launch failed";
+    case QG_ERR_BAD_INDEX: return "QG_ERR_BAD_INDEX: a slot or block id outside the cache was skipped";
     case QG_ERR_DEVICE_TIMEOUT: return "QG_ERR_DEVICE_TIMEOUT: a kernel's bounded wait gave up";
   }
   return "QG_ERR_UNKNOWN";
@@ -459,6 +460,143 @@ qg_status qg_selftest_wait_timeout(int kind, uint32_t limit, void* stream) {
 
 const char* qg_last_cuda_error_string(void) { return cudaGetErrorString(t_last_cuda); }
 
+// The paged 8-bit cache: sizes shared by its entry points
+static qg_status check_kv8(int Hkv, int D, int block_size, int num_blocks, int format) {
+  if (Hkv < 1 || Hkv > 1024 || D < 16 || D > 256 || D % 16 != 0) return QG_ERR_INVALID_ARG;
+  if (block_size < 16 || block_size > 1024 || block_size % 16 != 0 || num_blocks < 1) return QG_ERR_INVALID_ARG;
+  if ((long long)num_blocks * block_size >= (1LL << 31)) return QG_ERR_INVALID_ARG;
+  if ((long long)num_blocks * Hkv >= (1LL << 31)) return QG_ERR_INVALID_ARG;
+  if (format != QG_KV_I8 && format != QG_KV_E4M3) return QG_ERR_INVALID_ARG;
+  return QG_OK;
+}
+
+size_t qg_kv8_plan_workspace_size(void) { return 16; }
+
+qg_status kv8_block_plan(const int32_t* old_lens, const int32_t* new_lens, int R, int block_size,
+                         int32_t* block_table, int max_blocks, int32_t* free_list, int num_blocks,
+                         const int32_t* free_count, int32_t* free_count_out, int32_t* cu_new, int32_t* slot_map,
+                         int32_t* positions, int max_tokens, int32_t* info, void* workspace, size_t ws_bytes,
+                         void* stream) {
+  if (!old_lens || !new_lens || !block_table || !free_list || !free_count || !free_count_out || !cu_new ||
+      !slot_map || !positions || !info)
+    return QG_ERR_INVALID_ARG;
+  if (R < 1 || R > 4096 || max_blocks < 1 || max_tokens < 1 || max_tokens > (1 << 30)) return QG_ERR_INVALID_ARG;
+  qg_status st = check_kv8(1, 16, block_size, num_blocks, QG_KV_I8);
+  if (st != QG_OK) return st;
+  if ((long long)max_blocks * block_size > (1LL << 31) - 2048 || (long long)R * max_blocks >= (1LL << 31))
+    return QG_ERR_INVALID_ARG;
+  if (!aligned16(old_lens) || !aligned16(new_lens) || !aligned16(block_table) || !aligned16(free_list) ||
+      !aligned16(free_count) || !aligned16(free_count_out) || !aligned16(cu_new) || !aligned16(slot_map) ||
+      !aligned16(positions) || !aligned16(info) || !aligned16(workspace))
+    return QG_ERR_MISALIGNED;
+  if (!workspace || ws_bytes < qg_kv8_plan_workspace_size()) return QG_ERR_WORKSPACE;
+  const qg::PlanArgs a = {old_lens,   new_lens, R,        block_size, block_table, max_blocks, free_list, num_blocks,
+                          free_count, free_count_out, cu_new, slot_map, positions, max_tokens, info,
+                          static_cast<unsigned*>(workspace)};
+  return from_cuda(qg::launch_kv8_plan(a, static_cast<cudaStream_t>(stream), g_pdl));
+}
+
+qg_status kv8_append(const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride,
+                     const int32_t* slot_map, int T, int Hkv, int D, int block_size, int num_blocks, int format,
+                     void* k_cache, void* v_cache, float* scales, void* stream) {
+  if (!k || !v || !slot_map || !k_cache || !v_cache || !scales) return QG_ERR_INVALID_ARG;
+  if (T < 1 || (dtype != QG_DT_BF16 && dtype != QG_DT_F32)) return QG_ERR_INVALID_ARG;
+  qg_status st = check_kv8(Hkv, D, block_size, num_blocks, format);
+  if (st != QG_OK) return st;
+  if (k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return QG_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(slot_map) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(scales))
+    return QG_ERR_MISALIGNED;
+  uint32_t* err = err_word();
+  if (!err) return QG_ERR_CUDA;
+  const qg::AppendArgs a = {k, v, dtype == QG_DT_F32, k_stride, v_stride, slot_map, T, Hkv, D, block_size,
+                            num_blocks, k_cache, v_cache, scales, err, 1};
+  return from_cuda(qg::launch_kv8_append(a, format, static_cast<cudaStream_t>(stream), g_pdl));
+}
+
+qg_status kv8_read(const int32_t* block_ids, int B, int Hkv, int D, int block_size, int num_blocks, int format,
+                   const void* k_cache, const void* v_cache, const float* scales, uint16_t* k, uint16_t* v,
+                   float* scales_out, void* stream) {
+  if (!block_ids || !k_cache || !v_cache || !scales || !k || !v || !scales_out || B < 1) return QG_ERR_INVALID_ARG;
+  qg_status st = check_kv8(Hkv, D, block_size, num_blocks, format);
+  if (st != QG_OK) return st;
+  if (!aligned16(block_ids) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(scales) || !aligned16(k) ||
+      !aligned16(v) || !aligned16(scales_out))
+    return QG_ERR_MISALIGNED;
+  uint32_t* err = err_word();
+  if (!err) return QG_ERR_CUDA;
+  const qg::ReadArgs a = {block_ids, B, Hkv, D, block_size, num_blocks, k_cache, v_cache, scales, k, v, scales_out,
+                          err};
+  return from_cuda(qg::launch_kv8_read(a, format, static_cast<cudaStream_t>(stream), g_pdl));
+}
+
+size_t qg_attn_kv8_workspace_size(int Hq, int Hkv, int D) {
+  if (Hq < 1 || Hq > 1024 || Hkv < 1 || Hq % Hkv != 0 || D < 16 || D > 256 || D % 16 != 0) return 0;
+  return qg::attn_kv8_workspace_size(Hq, Hkv, D);
+}
+
+qg_status attn_kv8_paged(const uint16_t* q_bf16, int64_t q_stride, const void* k_cache, const void* v_cache,
+                         const float* scales, const int32_t* block_table, const int32_t* ctx_lens,
+                         const int32_t* cu_q, const uint32_t* tree_mask, int R, int T, int Hq, int Hkv, int D,
+                         int block_size, int num_blocks, int max_blocks, int format, float softmax_scale,
+                         uint16_t* out_bf16, void* workspace, size_t ws_bytes, void* stream) {
+  if (!q_bf16 || !k_cache || !v_cache || !scales || !block_table || !ctx_lens || !cu_q || !out_bf16)
+    return QG_ERR_INVALID_ARG;
+  qg_status st = check_kv8(Hkv, D, block_size, num_blocks, format);
+  if (st != QG_OK) return st;
+  if (R < 1 || R > 1024 || T < 1 || Hq < 1 || Hq > 1024 || Hq % Hkv != 0 || max_blocks < 1) return QG_ERR_INVALID_ARG;
+  if ((long long)max_blocks * block_size > (1LL << 31) - 2048 || (long long)T * Hq >= (1LL << 31))
+    return QG_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)Hq * D || q_stride % 8 != 0) return QG_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f)) return QG_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(scales) ||
+      !aligned16(block_table) || !aligned16(ctx_lens) || !aligned16(cu_q) || !aligned16(tree_mask) ||
+      !aligned16(out_bf16) || !aligned16(workspace))
+    return QG_ERR_MISALIGNED;
+  const size_t need = qg_attn_kv8_workspace_size(Hq, Hkv, D);
+  if (ws_bytes < need || (need && !workspace)) return QG_ERR_WORKSPACE;
+  uint32_t* err = err_word();
+  if (!err) return QG_ERR_CUDA;
+  const qg::AttnArgs a = {q_bf16, q_stride, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tree_mask, R, T,
+                          Hq, Hkv, D, block_size, num_blocks, max_blocks, softmax_scale * 1.4426950408889634f,
+                          out_bf16, workspace, err};
+  return from_cuda(qg::launch_attn_kv8(a, format, static_cast<cudaStream_t>(stream), g_pdl));
+}
+
+static qg_status check_norm(const qg::NormArgs& a, int x_dtype, int res_dtype, int w_dtype) {
+  if (!a.x || !a.w || !a.out || (a.res && !a.res_out)) return QG_ERR_INVALID_ARG;
+  for (int dt : {x_dtype, res_dtype, w_dtype})
+    if (dt != QG_DT_BF16 && dt != QG_DT_F32) return QG_ERR_INVALID_ARG;
+  if (a.M < 1 || a.K < 32 || a.K > 32768 || a.K % 32 != 0) return QG_ERR_INVALID_ARG;
+  if (!(a.eps >= 0.f)) return QG_ERR_INVALID_ARG;
+  if (!aligned16(a.x) || !aligned16(a.res) || !aligned16(a.w) || !aligned16(a.sign_bits) || !aligned16(a.res_out) ||
+      !aligned16(a.out) || !aligned16(a.scale))
+    return QG_ERR_MISALIGNED;
+  return QG_OK;
+}
+
+qg_status rmsnorm_residual(const void* x, int x_dtype, const void* residual, int res_dtype, const void* weight,
+                           int w_dtype, float eps, int M, int K, void* residual_out, uint16_t* out_bf16,
+                           void* stream) {
+  const qg::NormArgs a = {x, x_dtype == QG_DT_F32, residual, res_dtype == QG_DT_F32, weight, w_dtype == QG_DT_F32,
+                          eps, nullptr, M, K, residual_out, out_bf16, nullptr};
+  qg_status st = check_norm(a, x_dtype, res_dtype, w_dtype);
+  if (st != QG_OK) return st;
+  return from_cuda(qg::launch_rmsnorm(a, static_cast<cudaStream_t>(stream), g_pdl));
+}
+
+qg_status rmsnorm_residual_i8(const void* x, int x_dtype, const void* residual, int res_dtype, const void* weight,
+                              int w_dtype, float eps, const uint32_t* sign_bits, int M, int K, void* residual_out,
+                              int8_t* q, float* scale, void* stream) {
+  if (!scale) return QG_ERR_INVALID_ARG;
+  const qg::NormArgs a = {x, x_dtype == QG_DT_F32, residual, res_dtype == QG_DT_F32, weight, w_dtype == QG_DT_F32,
+                          eps, sign_bits, M, K, residual_out, q, scale};
+  qg_status st = check_norm(a, x_dtype, res_dtype, w_dtype);
+  if (st != QG_OK) return st;
+  return from_cuda(qg::launch_rmsnorm(a, static_cast<cudaStream_t>(stream), g_pdl));
+}
+
 qg_status qg_device_error(uint32_t* code, int clear) {
   uint32_t* p = err_word();
   if (!p) return QG_ERR_CUDA;
@@ -469,6 +607,7 @@ qg_status qg_device_error(uint32_t* code, int clear) {
     if (cudaMemcpy(p, &z, sizeof z, cudaMemcpyHostToDevice) != cudaSuccess) return QG_ERR_CUDA;
   }
   if (code) *code = v;
+  if (v >> 8 == 6) return QG_ERR_BAD_INDEX;
   return v ? QG_ERR_DEVICE_TIMEOUT : QG_OK;
 }
 

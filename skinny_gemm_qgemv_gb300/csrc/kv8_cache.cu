@@ -1,0 +1,353 @@
+// The paged 8-bit key/value cache: the block plan, the append and the read.
+//
+// kv8_plan_kernel. The lengths of all requests fit in one CTA's shared memory,
+// so every CTA forms the prefix sums of the blocks taken, the blocks released
+// and the new tokens by itself and then writes its share of the table, the
+// stack and the slots. No CTA waits for another one's writes: a block taken at
+// stack place p is free_list[p] below the old count, which nothing overwrites,
+// and above it a block released in this call, found through the prefix sums in
+// the releasing request's row, which nothing overwrites either.
+//
+// kv8_append_kernel. One CTA per run of slots, head and cache (keys or values):
+// the run's maximum decides the block's scale, the earlier codes of the block
+// are rounded to a grown scale, the run is quantized. All IEEE fp32 operations
+// on single values, so the codes do not depend on the work's order.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "kv8.cuh"
+#include "qg_common.cuh"
+#include "qg_internal.h"
+
+namespace qg {
+namespace {
+
+constexpr int kPlanThreads = 512;
+
+// take and rel are bounded by R * max_blocks < 2^31, the tokens only by their check
+struct PlanSums {
+  int take, rel;
+  long long tok;
+};
+
+// exclusive prefix sums over the CTA; `total` gets the sums of all threads
+__device__ __forceinline__ PlanSums plan_scan(PlanSums v, PlanSums* part, PlanSums& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  PlanSums s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, s.take, o), b = __shfl_up_sync(0xffffffffu, s.rel, o);
+    const long long c = __shfl_up_sync(0xffffffffu, s.tok, o);
+    if (lane >= o) s.take += a, s.rel += b, s.tok += c;
+  }
+  if (lane == 31) part[warp] = s;
+  __syncthreads();
+  PlanSums before = {0, 0, 0};
+  total = {0, 0, 0};
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before.take += part[w].take, before.rel += part[w].rel, before.tok += part[w].tok;
+    total.take += part[w].take, total.rel += part[w].rel, total.tok += part[w].tok;
+  }
+  return {before.take + s.take - v.take, before.rel + s.rel - v.rel, before.tok + s.tok - v.tok};
+}
+
+// largest r in [0, n) with a[r] <= v, for ascending a with a[0] <= v
+__device__ __forceinline__ int last_not_above(const int* a, int n, int v) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= v)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
+  extern __shared__ int sm[];
+  int* take_ex = sm;              // [R + 1]
+  int* rel_ex = sm + a.R + 1;     // [R + 1]
+  int* tok_ex = sm + 2 * a.R + 2; // [R + 1]
+  __shared__ PlanSums part[kPlanThreads / 32];
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int per = (a.R + kPlanThreads - 1) / kPlanThreads;
+  const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+  const int count = *a.free_count;
+  bool neg = false, outgrown = false;
+  PlanSums mine = {0, 0, 0};
+  for (int r = r0; r < r1; ++r) {
+    const int o = a.old_lens[r], n = a.new_lens[r];
+    if (o < 0 || n < 0) {
+      neg = true;
+    } else if (max(o, n) > a.max_blocks * a.bs) {
+      outgrown = true;
+    } else {
+      const int have = (o + a.bs - 1) / a.bs, need = (n + a.bs - 1) / a.bs;
+      mine.take += max(0, need - have);
+      mine.rel += max(0, have - need);
+      mine.tok += max(0, n - o);
+    }
+  }
+  const bool any_neg = __syncthreads_or(neg), any_out = __syncthreads_or(outgrown);
+  PlanSums total;
+  PlanSums ex = plan_scan(mine, part, total);
+  const int top = count + total.rel;
+  int state = 0;
+  if (any_neg || count < 0 || count > a.num_blocks || total.rel > a.num_blocks - count)
+    state = 4;
+  else if (any_out)
+    state = 2;
+  else if (total.tok > a.max_tokens)
+    state = 3;
+  else if (total.take > top)
+    state = 1;
+  if (state) total = {0, 0, 0};
+  if (state == 0) {
+    for (int r = r0; r < r1; ++r) {
+      const int o = a.old_lens[r], n = a.new_lens[r];
+      const int have = (o + a.bs - 1) / a.bs, need = (n + a.bs - 1) / a.bs;
+      take_ex[r] = ex.take, rel_ex[r] = ex.rel, tok_ex[r] = (int)ex.tok;
+      ex.take += max(0, need - have), ex.rel += max(0, have - need), ex.tok += max(0, n - o);
+    }
+    if (tid == 0) take_ex[a.R] = total.take, rel_ex[a.R] = total.rel, tok_ex[a.R] = (int)total.tok;
+  }
+  __syncthreads();
+  // the block of rank j among those taken
+  auto taken = [&](int j) {
+    const int p = top - 1 - j;
+    if (p < count) return a.free_list[p];
+    const int k = top - 1 - p;  // rank among the released
+    const int r = last_not_above(rel_ex, a.R, k);
+    return a.table[(size_t)r * a.max_blocks + (a.new_lens[r] + a.bs - 1) / a.bs + (k - rel_ex[r])];
+  };
+  const int nthreads = gridDim.x * kPlanThreads, gid = blockIdx.x * kPlanThreads + tid;
+  for (int j = gid; j < total.take; j += nthreads) {
+    const int r = last_not_above(take_ex, a.R, j);
+    a.table[(size_t)r * a.max_blocks + (a.old_lens[r] + a.bs - 1) / a.bs + (j - take_ex[r])] = taken(j);
+  }
+  for (int k = gid; k < total.rel; k += nthreads) {
+    const int r = last_not_above(rel_ex, a.R, k);
+    a.free_list[top - 1 - k] =
+        a.table[(size_t)r * a.max_blocks + (a.new_lens[r] + a.bs - 1) / a.bs + (k - rel_ex[r])];
+  }
+  for (int t0 = 4 * gid; t0 < a.max_tokens; t0 += 4 * nthreads) {
+    int slot[4], pos[4];
+    const int tokens = (int)total.tok;
+    int r = t0 < tokens ? last_not_above(tok_ex, a.R, t0) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + i;
+      slot[i] = pos[i] = -1;
+      if (t < tokens) {
+        while (tok_ex[r + 1] <= t) ++r;
+        const int old = a.old_lens[r], p = old + t - tok_ex[r], b = p / a.bs, have = (old + a.bs - 1) / a.bs;
+        const int blk = b < have ? a.table[(size_t)r * a.max_blocks + b] : taken(take_ex[r] + b - have);
+        slot[i] = blk * a.bs + p % a.bs;
+        pos[i] = p;
+      }
+    }
+    if (t0 + 4 <= a.max_tokens) {
+      *reinterpret_cast<int4*>(a.slot_map + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t0 + i < a.max_tokens) a.slot_map[t0 + i] = slot[i], a.positions[t0 + i] = pos[i];
+      }
+    }
+  }
+  if (blockIdx.x == 0) {
+    for (int r = tid; r <= a.R; r += kPlanThreads) a.cu_new[r] = state ? 0 : tok_ex[r];
+    if (tid == 0) a.info[0] = (int)total.tok, a.info[1] = total.take, a.info[2] = total.rel, a.info[3] = state;
+  }
+  // free_count_out may be free_count: the CTA that read it last writes it (no one waits)
+  if (tid == 0) {
+    unsigned seen;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.ticket) : "memory");
+    if (seen == gridDim.x - 1) {
+      *a.free_count_out = state ? count : top - total.take;
+      *a.ticket = 0;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+constexpr int kAppendThreads = 128;
+constexpr int kAppendKeep = 8;  // steps of 8 elements kept in registers between the maximum and the codes
+
+__device__ __forceinline__ void load8_in(const void* p, int f32, size_t elem, float (&v)[8]) {
+  if (f32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + elem);
+    const float4 a = __ldg(s), b = __ldg(s + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + elem));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(const float (&v)[8]) {
+  return make_uint2(kv8_encode4<FMT>(v[0], v[1], v[2], v[3]), kv8_encode4<FMT>(v[4], v[5], v[6], v[7]));
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a) {
+  __shared__ int run_len;
+  __shared__ float part[kAppendThreads / 32];
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int which = blockIdx.y & 1, head = blockIdx.y >> 1;
+  const void* x = which ? a.v : a.k;
+  const long long stride = which ? a.v_stride : a.k_stride;
+  uint8_t* cache = static_cast<uint8_t*>(which ? a.v_cache : a.k_cache);
+  const int d8 = a.D / 8;
+  const int t_end = min(a.T, (int)(blockIdx.x + 1) * a.window);
+  for (int t0 = blockIdx.x * a.window; t0 < t_end; ++t0) {
+    const int slot = __ldg(a.slot_map + t0);
+    if (slot < 0) continue;
+    if (slot >= a.num_blocks * a.bs) {
+      if (tid == 0) report_error(a.err, kErrKvSlot);
+      continue;
+    }
+    const int f = slot % a.bs, blk = slot / a.bs;
+    // the first token of its block in this call? (slots of a block ascend by one)
+    if (f > 0 && t0 > 0 && __ldg(a.slot_map + t0 - 1) == slot - 1) continue;
+    __syncthreads();
+    if (tid == 0) run_len = a.bs - f;
+    __syncthreads();
+    for (int i = tid; i < a.bs - f; i += kAppendThreads)
+      if (t0 + i >= a.T || __ldg(a.slot_map + t0 + i) != slot + i) atomicMin(&run_len, i);
+    __syncthreads();
+    const int chunks = run_len * d8;
+    float keep[kAppendKeep][8];
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < kAppendKeep; ++c) {
+      const int i = tid + c * kAppendThreads;
+      if (i < chunks) {
+        load8_in(x, a.f32, (t0 + i / d8) * stride + head * a.D + (i % d8) * 8, keep[c]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(keep[c][j]));
+      }
+    }
+    for (int i = tid + kAppendKeep * kAppendThreads; i < chunks; i += kAppendThreads) {
+      float v[8];
+      load8_in(x, a.f32, (t0 + i / d8) * stride + head * a.D + (i % d8) * 8, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((tid & 31) == 0) part[tid >> 5] = amax;
+    float* sp = a.scales + 2 * ((size_t)blk * a.Hkv + head) + which;
+    const float s0 = f > 0 ? *sp : 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, part[w]);
+    const float s1 = __fdiv_rn(amax, kv8_qmax<FMT>());
+    const float s = fmaxf(s0, s1);
+    if (tid == 0) *sp = s;  // every thread read the old one before the barrier
+    uint8_t* page = cache + ((size_t)blk * a.Hkv + head) * a.bs * a.D;
+    if (f > 0 && s > s0) {
+      // the earlier codes, rounded to the grown scale
+      const float ratio = __fdiv_rn(s0, s);
+      for (int i = tid; i < f * d8; i += kAppendThreads) {
+        uint2* p = reinterpret_cast<uint2*>(page) + i;
+        const uint2 old = *p;
+        float v[8];
+        kv8_decode4<FMT>(old.x, v[0], v[1], v[2], v[3]);
+        kv8_decode4<FMT>(old.y, v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], ratio);
+        *p = encode8<FMT>(v);
+      }
+    }
+    uint2* dst = reinterpret_cast<uint2*>(page + (size_t)f * a.D);
+    auto store = [&](int i, float(&v)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = s > 0.f ? __fdiv_rn(v[j], s) : 0.f;
+      dst[i] = encode8<FMT>(v);
+    };
+#pragma unroll
+    for (int c = 0; c < kAppendKeep; ++c)
+      if (tid + c * kAppendThreads < chunks) store(tid + c * kAppendThreads, keep[c]);
+    for (int i = tid + kAppendKeep * kAppendThreads; i < chunks; i += kAppendThreads) {
+      float v[8];
+      load8_in(x, a.f32, (t0 + i / d8) * stride + head * a.D + (i % d8) * 8, v);
+      store(i, v);
+    }
+    if (f == 0)
+      for (int i = tid + chunks; i < a.bs * d8; i += kAppendThreads) dst[i] = make_uint2(0u, 0u);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// read
+// ---------------------------------------------------------------------------
+template <int FMT>
+__global__ void __launch_bounds__(256) kv8_read_kernel(ReadArgs a) {
+  pdl_wait();
+  const int which = blockIdx.z, head = blockIdx.y;
+  const int per = a.bs * a.D / 8;
+  const int id = __ldg(a.ids + blockIdx.x);
+  const bool ok = id >= 0 && id < a.num_blocks;
+  if (!ok && threadIdx.x == 0) report_error(a.err, kErrKvBlock);
+  const size_t page = ((size_t)(ok ? id : 0) * a.Hkv + head);
+  const size_t dst = ((size_t)blockIdx.x * a.Hkv + head);
+  const float s = ok ? __ldg(a.scales + 2 * page + which) : 0.f;
+  if (threadIdx.x == 0) a.scales_out[2 * dst + which] = s;
+  const uint2* src = reinterpret_cast<const uint2*>(which ? a.v_cache : a.k_cache) + page * per;
+  uint4* out = reinterpret_cast<uint4*>(which ? a.v : a.k) + dst * per;
+  for (int i = threadIdx.x; i < per; i += blockDim.x) {
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    if (ok) {
+      const uint2 c = __ldg(src + i);
+      float v[8];
+      kv8_decode4<FMT>(c.x, v[0], v[1], v[2], v[3]);
+      kv8_decode4<FMT>(c.y, v[4], v[5], v[6], v[7]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= s;
+      o = make_uint4(f32_to_bf16x2(v[0], v[1]), f32_to_bf16x2(v[2], v[3]), f32_to_bf16x2(v[4], v[5]),
+                     f32_to_bf16x2(v[6], v[7]));
+    }
+    out[i] = o;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_plan(const PlanArgs& a, cudaStream_t stream, bool pdl) {
+  const int ctas = std::min(device_sm_count(), std::max(1, (a.max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads)));
+  const size_t smem = 3 * sizeof(int) * (a.R + 1);
+  if (smem > 40 << 10) {
+    cudaError_t e = allow_max_smem(kv8_plan_kernel);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(kv8_plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, stream, pdl, a);
+}
+
+cudaError_t launch_kv8_append(AppendArgs a, int format, cudaStream_t stream, bool pdl) {
+  const long long items = (long long)a.T * a.Hkv * 2;
+  a.window = (int)std::min<long long>(a.bs, std::max<long long>(1, (items + 2431) / 2432));
+  const dim3 grid((a.T + a.window - 1) / a.window, 2 * a.Hkv);
+  auto k = format == QG_KV_I8 ? kv8_append_kernel<QG_KV_I8> : kv8_append_kernel<QG_KV_E4M3>;
+  return launch_kernel(k, grid, dim3(kAppendThreads), 0, stream, pdl, a);
+}
+
+cudaError_t launch_kv8_read(const ReadArgs& a, int format, cudaStream_t stream, bool pdl) {
+  auto k = format == QG_KV_I8 ? kv8_read_kernel<QG_KV_I8> : kv8_read_kernel<QG_KV_E4M3>;
+  return launch_kernel(k, dim3(a.B, a.Hkv, 2), dim3(256), 0, stream, pdl, a);
+}
+
+}  // namespace qg

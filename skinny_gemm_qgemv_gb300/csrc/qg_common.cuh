@@ -32,6 +32,10 @@ enum DeviceError : uint32_t {
   kErrW8FusedBarrier = 0x405,
   kErrSelftestBarrier = 0x501,
   kErrSelftestFlag = 0x502,
+  kErrKvSlot = 0x601,    // 0x6xx: an index outside the paged cache, skipped
+  kErrKvBlock = 0x602,
+  kErrKvLength = 0x603,
+  kErrAttnWait = 0x701,
 };
 
 // Upper bound on polls of one mbarrier phase before a kernel reports a timeout

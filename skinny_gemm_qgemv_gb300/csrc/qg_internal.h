@@ -222,6 +222,75 @@ cudaError_t launch_affine_generic(const uint32_t* wq, int bits, const uint16_t* 
 cudaError_t launch_w8a16_gemv(const int8_t* wq, const float* scales, const uint16_t* x, float* y, int N, int K,
                               cudaStream_t stream, bool pdl);
 
+// The decode step around the products: paged 8-bit key/value cache
+// (kv8_cache.cu), attention over it (attn_kv8.cu), residual RMS norm (rmsnorm.cu)
+struct PlanArgs {
+  const int32_t *old_lens, *new_lens;
+  int R, bs;
+  int32_t* table;
+  int max_blocks;
+  int32_t* free_list;
+  int num_blocks;
+  const int32_t* free_count;
+  int32_t *free_count_out, *cu_new, *slot_map, *positions;
+  int max_tokens;
+  int32_t* info;
+  unsigned* ticket;  // zero before and after every call
+};
+struct AppendArgs {
+  const void *k, *v;
+  int f32;
+  long long k_stride, v_stride;
+  const int32_t* slot_map;
+  int T, Hkv, D, bs, num_blocks;
+  void *k_cache, *v_cache;
+  float* scales;
+  uint32_t* err;
+  int window;  // tokens whose runs one CTA takes (set by the launcher)
+};
+struct ReadArgs {
+  const int32_t* ids;
+  int B, Hkv, D, bs, num_blocks;
+  const void *k_cache, *v_cache;
+  const float* scales;
+  uint16_t *k, *v;
+  float* scales_out;
+  uint32_t* err;
+};
+struct AttnArgs {
+  const uint16_t* q;
+  long long q_stride;
+  const void *k_cache, *v_cache;
+  const float* scales;
+  const int32_t *table, *ctx_lens, *cu_q;
+  const uint32_t* tree;
+  int R, T, Hq, Hkv, D, bs, num_blocks, max_blocks;
+  float scale_log2;  // softmax_scale * log2(e)
+  uint16_t* out;
+  void* ws;
+  uint32_t* err;
+};
+struct NormArgs {
+  const void* x;
+  int x_f32;
+  const void* res;
+  int res_f32;
+  const void* w;
+  int w_f32;
+  float eps;
+  const uint32_t* sign_bits;
+  int M, K;
+  void* res_out;
+  void* out;
+  float* scale;  // null: bf16 output
+};
+cudaError_t launch_kv8_plan(const PlanArgs& a, cudaStream_t stream, bool pdl);
+cudaError_t launch_kv8_append(AppendArgs a, int format, cudaStream_t stream, bool pdl);
+cudaError_t launch_kv8_read(const ReadArgs& a, int format, cudaStream_t stream, bool pdl);
+size_t attn_kv8_workspace_size(int Hq, int Hkv, int D);
+cudaError_t launch_attn_kv8(const AttnArgs& a, int format, cudaStream_t stream, bool pdl);
+cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t stream, bool pdl);
+
 // MXFP4 MoE (moe_mxfp4.cu, moe_mx_mma.cu)
 constexpr int kMxTC = 8;                // pairs of one virtual expert: the N = 8 columns of one MMA
 // upper bound of the virtual experts of a batch: every active expert once, plus

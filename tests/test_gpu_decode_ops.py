@@ -1,0 +1,677 @@
+"""GPU parity of the decode step's operators against the 64-bit oracle.
+
+Tolerances (fixed before the first run):
+  * block plan, cache codes and scales, read-back values: equal, bit for bit.
+  * attention: |o - ref| <= 2^-8 |ref| (the bf16 result) + (2^-11 + 2 d +
+    n 2^-24) sum p|v| + n 2^-25 max|v|, n the seen tokens: the probabilities'
+    fp16 rounding, the scores' fp32 error d = (D + 8) 2^-23 max sum|q k| in
+    both numerator and denominator, the fp32 sums, and probabilities below
+    fp16's normal range.
+  * norm: bf16 2^-8 |ref| + 2^-18 |ref| (fp32 sums and products); int8: the
+    scale and the codes' values off by e = 48 * 2^-24 sum|y| of the value's
+    32-block (or of |y|), the code by half a step more; a row's scale
+    additionally by that error of its largest value.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import decode as od
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+FMT = {"i8": od.I8, "e4m3": od.E4M3}
+DT = {"i8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
+@pytest.fixture(scope="module")
+def q():
+    from skinny_gemm_qgemv_gb300 import build
+    build.build()
+    import skinny_gemm_qgemv_gb300 as qq
+    qq.lib()
+    qq.device_error(clear=True)
+    yield qq
+    assert qq.device_error(clear=True) == 0
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x, dtype=np.int64).astype(np.uint32).view(np.int32) if np.asarray(x).size else
+                        np.zeros(0, np.int32), device=DEV)
+
+
+def bits(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+# --------------------------------------------------------------------------
+# block plan
+# --------------------------------------------------------------------------
+
+def plan_state(rng, R, bs, top, grow, spare):
+    old = rng.integers(0, top + 1, R)
+    new = np.where(rng.random(R) < 0.2, rng.integers(0, old + 1), old + rng.integers(0, grow + 1, R))
+    have, need = -(-old // bs), -(-new // bs)
+    free = int(np.maximum(need - have, 0).sum()) + spare
+    N, maxb = free + int(have.sum()), int(max(have.max(), need.max(), 1))
+    ids = rng.permutation(N).astype(np.int32)
+    table, at = np.full((R, maxb), -7, np.int32), free
+    for r in range(R):
+        table[r, :have[r]] = ids[at:at + have[r]]
+        at += have[r]
+    return old, new, table, ids, free
+
+
+def run_plan(q, old, new, table, free, count, bs, max_tokens, inplace=False):
+    t, f, c = i32(table), i32(free), i32([count])
+    got = q.kv8_block_plan(i32(old), i32(new), t, f, c, bs, max_tokens, free_count_out=c if inplace else None)
+    torch.cuda.synchronize()
+    return [x.cpu().numpy() for x in (t, f, *got)], (t, f, got[0])
+
+
+@pytest.mark.parametrize("R,bs,top,grow", [(1, 16, 0, 1), (1, 64, 100, 5000), (3, 16, 40, 1), (32, 16, 500, 1),
+                                           (33, 48, 100, 70), (513, 32, 90, 33), (1000, 1024, 5000, 3000),
+                                           (4096, 16, 40, 9)])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_plan(q, R, bs, top, grow, inplace):
+    rng = np.random.default_rng(R + bs)
+    old, new, table, free, count = plan_state(rng, R, bs, top, grow, 3)
+    tokens = int(np.maximum(new - old, 0).sum())
+    for max_tokens in {max(1, tokens), tokens + 1 + R % 7}:
+        got, dev = run_plan(q, old, new, table, free, count, bs, max_tokens, inplace)
+        want = od.block_plan(old, new, table, free, count, bs, max_tokens)
+        for g, w, name in zip(got, want, ("table", "free_list", "count", "cu", "slots", "positions", "info")):
+            assert np.array_equal(g.reshape(-1), np.asarray(w).reshape(-1)), name
+        assert want[-1][3] == 0
+    # back again: the stack below the count is what it was
+    t, f, c = dev
+    back = q.kv8_block_plan(i32(new), i32(old), t, f, c, bs, max(1, int(np.maximum(old - new, 0).sum())))
+    want = od.block_plan(new, old, *[x for x in want[:3]], bs, max(1, int(np.maximum(old - new, 0).sum())))
+    torch.cuda.synchronize()
+    assert back[4][3].item() == 0 and back[0].item() == count
+    assert np.array_equal(f.cpu().numpy(), want[1])
+
+
+def test_plan_states(q):
+    rng = np.random.default_rng(9)
+    old, new, table, free, count = plan_state(rng, 20, 16, 100, 40, 0)
+    tokens = int(np.maximum(new - old, 0).sum())
+    grown = np.maximum(old, new)
+    cases = [(old, grown, 0, tokens, 1), (old, new + 100000, count, tokens, 2), (old, new, count, tokens - 1, 3),
+             (old, np.where(np.arange(20) == 7, -1, new), count, tokens, 4), (old, new, -1, tokens, 4),
+             (old, new, len(free) + 1, tokens, 4), (old, np.zeros(20, int), len(free), tokens, 4),
+             (old, np.full(20, 2 ** 31 - 1), count, tokens, 2)]
+    for o, n, c, mt, state in cases:
+        got, _ = run_plan(q, o, n, table, free, c, 16, mt)
+        want = od.block_plan(o, n, table, free, c, 16, mt)
+        assert got[-1].tolist() == [0, 0, 0, state] == want[-1].tolist()
+        for g, w in zip(got, want):
+            assert np.array_equal(g.reshape(-1), np.asarray(w).reshape(-1)), state
+
+
+# --------------------------------------------------------------------------
+# cache
+# --------------------------------------------------------------------------
+
+def random_cache(rng, nb, H, bs, D, fmt, device=DEV):
+    """Random codes (every int8 code but -128, every finite e4m3 code) and scales."""
+    c = rng.integers(0, 256, (2, nb, H, bs, D), dtype=np.uint8)
+    if fmt == "i8":
+        c[c == 128] = 7
+    else:
+        c[(c & 0x7F) == 0x7F] ^= 0x10
+    scales = (rng.random((nb, H, 2)) * 2.0 / float(od.QMAX[FMT[fmt]]) + 1e-4).astype(np.float32)
+    return c[0], c[1], scales
+
+
+def to_cache(c, fmt):
+    return torch.from_numpy(c.copy()).to(DEV).view(DT[fmt])
+
+
+def check_append(q, fmt, dtype, k, v, slots, kc, vc, sc, nb, bs, kt=None, vt=None):
+    """k, v: fp32 tensors (already rounded to dtype); kt, vt: what is passed."""
+    kd, vd, sd = to_cache(kc, fmt), to_cache(vc, fmt), torch.from_numpy(sc.copy()).to(DEV)
+    q.kv8_append(k.to(dtype).to(DEV) if kt is None else kt, v.to(dtype).to(DEV) if vt is None else vt, i32(slots), kd,
+                 vd, sd)
+    torch.cuda.synchronize()
+    wk, s0 = od.append(k.numpy(), slots, kc, sc[..., 0], FMT[fmt], nb, bs)
+    wv, s1 = od.append(v.numpy(), slots, vc, sc[..., 1], FMT[fmt], nb, bs)
+    assert np.array_equal(sd.cpu().numpy(), np.stack((s0, s1), -1))
+    assert np.array_equal(bits(kd), wk) and np.array_equal(bits(vd), wv)
+    return kd, vd, sd, wk, wv, np.stack((s0, s1), -1)
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,D,bs,runs", [
+    (1, 16, 16, [(0, 1)]), (2, 64, 16, [(3, 5), (0, 16), (15, 1)]), (8, 128, 16, [(i % 16, 1) for i in range(32)]),
+    (3, 80, 48, [(0, 48), (0, 48), (0, 7)]), (1, 256, 64, [(1, 63), (0, 64)]), (2, 128, 256, [(0, 200), (31, 225)]),
+    (2, 64, 1024, [(1000, 24), (0, 1024)]), (1, 128, 32, [(31, 1), (0, 31)])])
+def test_append(q, fmt, dtype, H, D, bs, runs):
+    rng = np.random.default_rng(H * D + bs)
+    nb = len(runs) + 2
+    kc, vc, sc = random_cache(rng, nb, H, bs, D, fmt)
+    blocks = rng.permutation(nb)[:len(runs)]
+    slots = np.concatenate([b * bs + f + np.arange(n) for b, (f, n) in zip(blocks, runs)])
+    T = len(slots)
+    g = torch.Generator().manual_seed(T)
+    # some tokens raise their block's scale, some do not, some are zero
+    size = torch.tensor([0.0, 0.01, 1.0, 30.0])[torch.randint(0, 4, (T, 1, 1), generator=g)]
+    k, v = ((torch.randn((T, H, D), generator=g) * size).to(dtype).float() for _ in range(2))
+    kd, vd, sd, wk, wv, ws = check_append(q, fmt, dtype, k, v, slots, kc, vc, sc, nb, bs)
+    ids = rng.permutation(nb)
+    rk, rv, rs = q.kv8_read(i32(ids), kd, vd, sd)
+    torch.cuda.synchronize()
+    assert np.array_equal(rs.cpu().numpy(), ws[ids])
+    for got, w, which in ((rk, wk, 0), (rv, wv, 1)):
+        want = (torch.from_numpy(od.decode(w[ids], FMT[fmt]).astype(np.float32)) *
+                torch.from_numpy(ws[ids][..., which])[..., None, None]).to(torch.bfloat16)
+        assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_append_steps_fill_a_block(q, fmt):
+    """Sixteen one-token appends into one block, each step checked: the scale grows and the codes are rounded again."""
+    rng = np.random.default_rng(3)
+    kc, vc, sc = random_cache(rng, 3, 2, 16, 64, fmt)
+    g = torch.Generator().manual_seed(4)
+    for s in range(16):
+        k, v = (torch.randn((1, 2, 64), generator=g) * (1 + 0.5 * s) for _ in range(2))
+        _, _, _, kc, vc, sc = check_append(q, fmt, torch.float32, k, v, [16 + s], kc, vc, sc, 3, 16)
+
+
+def test_append_strided_padded_and_zero(q):
+    rng = np.random.default_rng(5)
+    H, D, bs, nb, T = 4, 64, 16, 6, 23
+    kc, vc, sc = random_cache(rng, nb, H, bs, D, "i8")
+    # slices of a fused q/k/v row; padding slots before, between and after the runs
+    fused = torch.randn((T, 3 * H * D + 8), generator=torch.Generator().manual_seed(6))
+    fused[5:9] = 0
+    fd = fused.to(DEV)
+    kt = fd[:, H * D:2 * H * D].unflatten(1, (H, D))
+    vt = fd[:, 2 * H * D:3 * H * D].unflatten(1, (H, D))
+    slots = np.array([-1, -1] + list(range(80, 88)) + [-1] + list(range(32, 42)) + [-5, -1])
+    check_append(q, "i8", torch.float32, kt.cpu().contiguous(), vt.cpu().contiguous(), slots, kc, vc, sc, nb, bs, kt, vt)
+    # a new block of zeros: scale 0, codes 0
+    z = torch.zeros((16, H, D))
+    _, _, sd, wk, _, ws = check_append(q, "i8", torch.float32, z, z, np.arange(16), kc, vc, sc, nb, bs)
+    assert not ws[0].any() and not wk[0].any()
+
+
+def test_bad_slots_and_blocks_are_skipped_and_reported(q):
+    rng = np.random.default_rng(7)
+    kc, vc, sc = random_cache(rng, 4, 2, 16, 64, "i8")
+    k = torch.randn((3, 2, 64), generator=torch.Generator().manual_seed(8))
+    check_append(q, "i8", torch.float32, k, k, [64, 5, 2 ** 31 - 1], kc, vc, sc, 4, 16)
+    assert q.device_error(clear=True) == 0x601
+    rk, rv, rs = q.kv8_read(i32([4, 1, 2 ** 32 - 1]), to_cache(kc, "i8"), to_cache(vc, "i8"), torch.from_numpy(sc).to(DEV))
+    torch.cuda.synchronize()
+    assert not rk[0].any() and not rv[2].any() and not rs[0].any() and rk[1].any()
+    assert q.lib().qg_device_error(None, 1) == 7
+
+
+# --------------------------------------------------------------------------
+# attention
+# --------------------------------------------------------------------------
+
+def attn_case(rng, nq, ctx, Hq, Hkv, D, bs, fmt, tree, qstd=1.0):
+    R = len(nq)
+    need = [-(-max(c, 0) // bs) for c in ctx]
+    nb, maxb = sum(need) + 2, max(max(need), 1)
+    kc, vc, sc = random_cache(rng, nb, Hkv, bs, D, fmt)
+    ids = rng.permutation(nb)
+    table, at = np.full((R, maxb), -1, np.int64), 0
+    for r in range(R):
+        table[r, :need[r]] = ids[at:at + need[r]]
+        at += need[r]
+        if need[r] and ctx[r] % bs:
+            # slots past the context: anything, also codes that are not numbers
+            for c in (kc, vc):
+                c[table[r, need[r] - 1], :, ctx[r] % bs:] = 0x7F if fmt == "e4m3" else 0x80
+    cu = np.concatenate(([0], np.cumsum(nq)))
+    T = int(cu[-1]) + 3                                  # rows past the last request stay as they are
+    x = (torch.randn((T, Hq, D), generator=torch.Generator().manual_seed(int(rng.integers(1 << 30)))) * qstd).to(
+        torch.bfloat16)
+    masks = None
+    if tree:
+        masks = np.zeros(T, np.int64)
+        for r in range(R):
+            for i in range(nq[r]):
+                parent = int(rng.integers(-1, i)) if i else -1
+                masks[cu[r] + i] = (masks[cu[r] + parent] if parent >= 0 else 0) | (1 << (i % 32))
+    return dict(x=x, kc=kc, vc=vc, sc=sc, table=table, ctx=np.asarray(ctx), cu=cu, masks=masks, fmt=fmt)
+
+
+def run_attn(q, c, x=None, **kw):
+    out = torch.full(c["x"].shape, 7.0, device=DEV, dtype=torch.bfloat16)
+    q.attn_kv8_paged(c["x"].to(DEV) if x is None else x, to_cache(c["kc"], c["fmt"]), to_cache(c["vc"], c["fmt"]),
+                     torch.from_numpy(c["sc"]).to(DEV), i32(c["table"]), i32(c["ctx"]), i32(c["cu"]),
+                     tree_mask=None if c["masks"] is None else i32(c["masks"]), out=out, **kw)
+    torch.cuda.synchronize()
+    return out.cpu()
+
+
+def check_attn(out, c, scale=None):
+    D = c["x"].shape[2]
+    ref, mag, qk, n, vmax = od.attention(c["x"].float().numpy(), c["kc"], c["vc"], c["sc"], c["table"], c["ctx"],
+                                         c["cu"], FMT[c["fmt"]], D ** -0.5 if scale is None else scale, c["masks"])
+    last = int(c["cu"][-1])
+    assert bool((out[last:] == 7.0).all())
+    o = out[:last].double().numpy()
+    assert np.isfinite(o).all()
+    ref, mag, qk, n, vmax = ref[:last], mag[:last], qk[:last, :, None], n[:last, :, None], vmax[:last, :, None]
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * (D + 8) * 2.0 ** -23 * qk + n * 2.0 ** -24) * mag + \
+        n * 2.0 ** -25 * vmax
+    bad = np.abs(o - ref) > tol
+    assert not bad.any(), f"{bad.sum()} of {bad.size}; worst {np.max(np.abs(o - ref) / np.maximum(tol, 1e-300)):.3g}x"
+    assert not o[np.broadcast_to(n == 0, o.shape)].any()
+
+
+CASES = [
+    # query tokens, context lengths, Hq, Hkv, D, block, tree
+    ([1], [1], 4, 1, 128, 16, False),
+    ([1], [37], 32, 8, 128, 16, False),
+    ([1], [700], 8, 8, 128, 64, False),
+    ([1, 1, 1, 1, 1], [1, 16, 17, 0, 1000], 8, 2, 128, 16, False),
+    ([1, 0, 3, 2, 1], [50, 90, 3, 1, 333], 10, 2, 64, 32, False),
+    ([1] * 33, [(i * 97) % 400 for i in range(33)], 6, 2, 64, 16, False),
+    ([4, 5, 1], [129, 64, 80], 16, 2, 128, 48, False),
+    ([16], [2063], 32, 8, 128, 64, True),
+    ([16, 1, 32, 7], [16, 1, 32, 200], 8, 2, 128, 16, True),
+    ([32], [515], 7, 1, 64, 32, True),
+    ([40, 33], [40, 300], 4, 2, 128, 16, True),
+    ([100], [1000], 4, 1, 128, 128, False),
+    ([1, 2], [300, 45], 8, 2, 256, 16, False),
+    ([16, 3], [90, 600], 8, 1, 256, 64, True),
+    ([1, 6], [77, 140], 6, 3, 80, 16, False),
+    ([5], [64], 4, 4, 16, 16, True),
+    ([1], [5000], 5, 1, 64, 1024, False),
+    ([1, 1], [70, 40], 64, 2, 128, 16, False),
+    ([2], [260], 48, 1, 64, 48, False),
+]
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("nq,ctx,Hq,Hkv,D,bs,tree", CASES)
+def test_attention(q, fmt, nq, ctx, Hq, Hkv, D, bs, tree):
+    rng = np.random.default_rng(sum(ctx) + D + Hq)
+    c = attn_case(rng, nq, ctx, Hq, Hkv, D, bs, fmt, tree)
+    out = run_attn(q, c)
+    check_attn(out, c)
+    assert torch.equal(run_attn(q, c), out)  # the same bits again
+
+
+def test_attention_masks_that_leave_nothing(q):
+    # drafts without any earlier token, their words empty or naming tokens past the drafts
+    rng = np.random.default_rng(21)
+    c = attn_case(rng, [4, 3], [4, 3], 8, 2, 128, 16, "i8", True)
+    c["masks"][:] = [0, 0b1, 0, 0xFFFFFFF0, 0b111, 0, 0x80000000, 0, 0, 0]
+    out = run_attn(q, c)
+    check_attn(out, c)
+    assert not out[0].any() and not out[2].any() and not out[5].any() and not out[6].any() and out[1].any()
+    # a context shorter than the query tokens: the first ones see nothing
+    c = attn_case(rng, [6], [2], 8, 2, 128, 16, "e4m3", False)
+    out = run_attn(q, c)
+    check_attn(out, c)
+    assert not out[:4].any() and out[4].any()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_attention_scales_of_all_sizes(q, D, fmt):
+    """Blocks of zero scale, and scales that differ by 2^30; large and tiny queries."""
+    rng = np.random.default_rng(22)
+    c = attn_case(rng, [1, 4], [400, 333], 8, 2, D, 16, fmt, False)
+    c["sc"][::3, :, 1] = 0.0
+    c["sc"][1::3, :, 1] *= np.float32(2.0 ** -30)
+    c["sc"][::5, :, 0] = 0.0
+    c["x"][1] *= 1e-6
+    c["x"][2] *= 40.0
+    check_attn(run_attn(q, c), c)
+    c["sc"][..., 1] = 0.0
+    assert not run_attn(q, c)[:5].any()
+    c["sc"][..., 1] = np.float32(2.0 ** 40)
+    check_attn(run_attn(q, c), c)
+
+
+def test_attention_peaked_scores_and_softmax_scale(q):
+    rng = np.random.default_rng(23)
+    c = attn_case(rng, [3], [900], 8, 2, 128, 32, "i8", False, qstd=30.0)
+    check_attn(run_attn(q, c), c)
+    check_attn(run_attn(q, c, softmax_scale=1.7), c, 1.7)
+    check_attn(run_attn(q, c, softmax_scale=1e-6), c, 1e-6)
+
+
+def test_attention_strided_queries(q):
+    rng = np.random.default_rng(24)
+    c = attn_case(rng, [2, 1], [30, 99], 8, 2, 64, 16, "i8", False)
+    T = c["x"].shape[0]
+    fused = torch.zeros((T, 12 * 64), dtype=torch.bfloat16, device=DEV)
+    fused[:, 128:128 + 8 * 64] = c["x"].reshape(T, -1).to(DEV)
+    check_attn(run_attn(q, c, x=fused[:, 128:128 + 8 * 64].unflatten(1, (8, 64))), c)
+
+
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+def test_attention_bad_blocks_and_lengths(q, D):
+    rng = np.random.default_rng(25)
+    c = attn_case(rng, [1, 2], [200, 90], 4, 2, D, 16, "i8", False)
+    c["table"][0, 3], c["table"][0, 7], c["table"][1, 0] = -1, c["kc"].shape[0], 2 ** 31 - 1
+    out = run_attn(q, c)
+    check_attn(out, c)
+    assert q.device_error(clear=True) == 0x602
+    c["table"][0, 3], c["table"][0, 7], c["table"][1, 0] = 0, 1, 2
+    c["ctx"][0] = 10 ** 6                                # past its table: cut there
+    out = run_attn(q, c)
+    check_attn(out, c)
+    assert q.device_error(clear=True) == 0x603
+    assert q.lib().qg_device_error(None, 1) == 0
+
+
+def test_attention_long_context(q):
+    rng = np.random.default_rng(26)
+    c = attn_case(rng, [1], [70001], 4, 1, 128, 64, "i8", False)
+    check_attn(run_attn(q, c), c)
+
+
+def test_attention_offsets_past_32_bits(q):
+    """A cache of more than 2^32 bytes, its far end used."""
+    bs, D, Hkv = 64, 128, 2
+    nb = (1 << 32) // (Hkv * bs * D) + 9
+    kd = torch.zeros((nb, Hkv, bs, D), device=DEV, dtype=torch.int8)
+    vd = torch.zeros((nb, Hkv, bs, D), device=DEV, dtype=torch.int8)
+    sd = torch.full((nb, Hkv, 2), 0.01, device=DEV)
+    rng = np.random.default_rng(27)
+    c = attn_case(rng, [1, 2], [300, 100], 8, Hkv, D, bs, "i8", False)
+    small = c["kc"].shape[0]
+    kd[nb - small:] = to_cache(c["kc"], "i8")
+    vd[nb - small:] = to_cache(c["vc"], "i8")
+    sd[nb - small:] = torch.from_numpy(c["sc"]).to(DEV)
+    table = np.where(c["table"] >= 0, c["table"] + nb - small, -1)
+    out = torch.full(c["x"].shape, 7.0, device=DEV, dtype=torch.bfloat16)
+    q.attn_kv8_paged(c["x"].to(DEV), kd, vd, sd, i32(table), i32(c["ctx"]), i32(c["cu"]), out=out)
+    check_attn(out.cpu(), c)
+    # and an append and a read there
+    k = torch.randn((2, Hkv, D), generator=torch.Generator().manual_seed(1))
+    slots = [(nb - 1) * bs, (nb - 1) * bs + 1]
+    q.kv8_append(k.to(DEV), k.to(DEV), i32(slots), kd, vd, sd)
+    rk, rv, rs = q.kv8_read(i32([nb - 1]), kd, vd, sd)
+    assert torch.equal(rk, rv)
+    scale = k.abs().amax((0, 2)) / 127
+    assert torch.equal(rs[0, :, 0].cpu(), scale)
+    assert bool(((rk[0, :, :2].float().cpu().transpose(0, 1) - k).abs() <= scale[:, None] * 0.51 + 2.0 ** -8 * k.abs()
+                 ).all())
+
+
+def test_attention_on_another_stream_and_in_a_graph(q):
+    rng = np.random.default_rng(28)
+    c = attn_case(rng, [1, 2, 1], [100, 400, 37], 8, 2, 128, 16, "i8", False)
+    want = run_attn(q, c)
+    dev = [c["x"].to(DEV), to_cache(c["kc"], "i8"), to_cache(c["vc"], "i8"), torch.from_numpy(c["sc"]).to(DEV),
+           i32(c["table"]), i32(c["ctx"]), i32(c["cu"])]
+    out = torch.full(c["x"].shape, 7.0, device=DEV, dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        q.attn_kv8_paged(*dev, out=out)
+    st.synchronize()
+    assert torch.equal(out.cpu(), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.attn_kv8_paged(*dev, out=out)
+    # the lengths and tables are read by the replay
+    dev[5].copy_(i32([64, 5, 37]))
+    for _ in range(3):
+        out.fill_(7.0)
+        g.replay()
+    torch.cuda.synchronize()
+    c["ctx"] = np.array([64, 5, 37])
+    check_attn(out.cpu(), c)
+
+
+def test_decode_ops_back_to_back_with_pdl(q):
+    """plan -> append -> attention on one stream, launched with programmatic dependent launch: the same bits."""
+    rng = np.random.default_rng(29)
+    R, bs, Hkv, D = 5, 16, 2, 128
+    old = np.array([0, 15, 16, 33, 200])
+    new = old + np.array([3, 1, 1, 4, 2])
+    need = -(-old // bs)
+    nb, maxb = int(need.sum()) + 9, 14
+    ids = rng.permutation(nb)
+    table = np.full((R, maxb), -1)
+    at = 9
+    for r in range(R):
+        table[r, :need[r]] = ids[at:at + need[r]]
+        at += need[r]
+    kc, vc, sc = random_cache(rng, nb, Hkv, bs, D, "e4m3")
+    T = int((new - old).sum())
+    g = torch.Generator().manual_seed(2)
+    k, v, x = (torch.randn((T, h, D), generator=g).to(torch.bfloat16) for h in (Hkv, Hkv, 8))
+    outs = []
+    for pdl in (False, True):
+        q.set_pdl(pdl)
+        try:
+            t, kd, vd, sd = i32(table), to_cache(kc, "e4m3"), to_cache(vc, "e4m3"), torch.from_numpy(sc.copy()).to(DEV)
+            free, count, od_, nd = i32(ids), i32([9]), i32(old), i32(new)
+            kk, vv, xx = k.to(DEV), v.to(DEV), x.to(DEV)
+            torch.cuda.synchronize()
+            _, cu, slots, _, info = q.kv8_block_plan(od_, nd, t, free, count, bs, T)
+            q.kv8_append(kk, vv, slots, kd, vd, sd)
+            out = q.attn_kv8_paged(xx, kd, vd, sd, t, nd, cu)
+            torch.cuda.synchronize()
+        finally:
+            q.set_pdl(False)
+        assert info[3].item() == 0
+        outs.append((out.cpu(), bits(kd), bits(vd), sd.cpu(), t.cpu().numpy(), cu.cpu().numpy()))
+    assert torch.equal(outs[0][0], outs[1][0]) and np.array_equal(outs[0][1], outs[1][1])
+    out, kb, vb, sb, tb, cub = outs[0]
+    c = dict(x=torch.cat((x, x[:1])), kc=kb, vc=vb, sc=sb.numpy(), table=tb, ctx=new, cu=cub, masks=None, fmt="e4m3")
+    check_attn(torch.cat((out, torch.full_like(out[:1], 7.0))), c)
+
+
+# --------------------------------------------------------------------------
+# norm
+# --------------------------------------------------------------------------
+
+TD = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def norm_inputs(M, K, xd, rd, wd, seed):
+    x = synth.normal_f32((M, K), 1.0, seed, 0).to(TD[xd])
+    r = None if rd is None else (synth.normal_f32((M, K), 3.0, seed, 1)).to(TD[rd])
+    if r is not None:
+        r[:, ::61] *= 20
+    w = (1 + synth.normal_f32((K,), 0.3, seed, 2)).to(TD[wd])
+    h = x.float() if r is None else (x.float() + r.float()).to(TD[rd]).float()
+    return x, r, w, h
+
+
+NORM = [(1, 32, "f32", "f32", "bf16"), (1, 4096, "f32", "f32", "bf16"), (3, 4096, "bf16", "bf16", "f32"),
+        (16, 7168, "bf16", "f32", "bf16"), (5, 12288, "f32", "bf16", "bf16"), (2, 32768, "f32", "f32", "f32"),
+        (33, 96, "bf16", "bf16", "bf16"), (2, 8224, "bf16", None, "bf16"), (4, 16416, "f32", "f32", "bf16"),
+        (700, 2080, "f32", "bf16", "bf16")]
+
+
+@pytest.mark.parametrize("M,K,xd,rd,wd", NORM)
+def test_norm_bf16(q, M, K, xd, rd, wd):
+    x, r, w, h = norm_inputs(M, K, xd, rd, wd, 31)
+    y, ho = q.rmsnorm_residual(x.to(DEV), w.to(DEV), residual=None if r is None else r.to(DEV), eps=1e-5)
+    torch.cuda.synchronize()
+    if r is None:
+        assert ho is None
+    else:
+        assert torch.equal(ho.float().cpu(), h)
+    ref, _ = od.rmsnorm(h.double().numpy(), w.double().numpy(), 1e-5)
+    assert np.all(np.abs(y.double().cpu().numpy() - ref) <= (2.0 ** -8 + 2.0 ** -18) * np.abs(ref))
+
+
+@pytest.mark.parametrize("had", [False, True])
+@pytest.mark.parametrize("M,K,xd,rd,wd", NORM)
+def test_norm_i8(q, M, K, xd, rd, wd, had):
+    x, r, w, h = norm_inputs(M, K, xd, rd, wd, 37)
+    if M > 2:
+        x[1] = 0
+        h[1] = 0
+        if r is not None:
+            r[1] = 0
+    sb = synth.sign_bits(K, 38, 0) if had else None
+    qd, sd, ho = q.rmsnorm_residual_i8(x.to(DEV), w.to(DEV), residual=None if r is None else r.to(DEV), eps=1e-5,
+                                       sign_bits=None if sb is None else sb.to(DEV))
+    torch.cuda.synchronize()
+    if r is not None:
+        assert torch.equal(ho.float().cpu(), h)
+    z, mag = od.rmsnorm(h.double().numpy(), w.double().numpy(), 1e-5, None if sb is None else sb.numpy())
+    err = 48 * 2.0 ** -24 * mag
+    amax, emax = np.abs(z).max(-1), err.max(-1)
+    s = sd.double().cpu().numpy()
+    assert np.all(np.abs(s - amax / 127) <= emax / 127 + 2.0 ** -23 * amax / 127)
+    codes = qd.double().cpu().numpy()
+    assert np.abs(codes).max() <= 127
+    live = s > 0
+    assert np.array_equal(live, amax > 0) and not codes[~live].any()
+    step = s[live, None]
+    off = np.abs(codes[live] * step - z[live])
+    assert np.all(off <= step * 0.5 + err[live] + 127 * 2.0 ** -23 * step)
+
+
+def test_norm_in_place_and_transform_agree_with_the_quantizer(q):
+    M, K = 16, 4096
+    x, r, w, h = norm_inputs(M, K, "f32", "f32", "bf16", 41)
+    sb = synth.sign_bits(K, 41, 5).to(DEV)
+    xd, rd, wd = x.to(DEV), r.to(DEV), w.to(DEV)
+    y, ho = q.rmsnorm_residual(xd, wd, residual=rd.clone())
+    res = rd.clone()
+    y2, same = q.rmsnorm_residual(xd, wd, residual=res, residual_out=res)
+    assert same is res and torch.equal(y, y2) and torch.equal(res, ho)
+    # a weight that makes y a bf16 number: the codes are the quantizer's own, bit for bit
+    yb, _ = q.rmsnorm_residual(xd, wd, residual=rd)
+    one = torch.ones(K, device=DEV)
+    xs = (torch.randint(-7, 8, (M, K), generator=torch.Generator().manual_seed(3)).float() * 8).to(DEV)
+    xs[:, 0] = 8
+    unit = xs / xs.square().mean(-1, keepdim=True).sqrt()
+    q8, s8, _ = q.rmsnorm_residual_i8(unit, one, sign_bits=sb, eps=0.0)
+    qr, sr = q.hadamard32_quant_i8(xs.to(torch.bfloat16), sb)
+    torch.cuda.synchronize()
+    assert (q8.int() - qr.int()).abs().max().item() <= 1  # the rows differ by a factor, rounded once
+    assert yb.dtype == torch.bfloat16
+
+
+def test_norm_feeds_the_int8_product(q):
+    """norm -> codes -> exact int8 product against the float64 product of the codes."""
+    M, K, N = 8, 1024, 192
+    x, r, w, h = norm_inputs(M, K, "f32", "f32", "bf16", 43)
+    sb = synth.sign_bits(K, 43, 5)
+    qa, sa, _ = q.rmsnorm_residual_i8(x.to(DEV), w.to(DEV), residual=r.to(DEV), sign_bits=sb.to(DEV))
+    w8 = torch.randint(-127, 128, (N, K), generator=torch.Generator().manual_seed(4), dtype=torch.int8)
+    c = q.gemm_w8a8_i32(qa, w8.to(DEV))
+    torch.cuda.synchronize()
+    assert np.array_equal(c.cpu().numpy(), (qa.cpu().double() @ w8.double().T).to(torch.int32).numpy())
+
+
+def test_python_refusals(q):
+    z = torch.zeros
+    kc = z((2, 2, 16, 64), device=DEV, dtype=torch.int8)
+    sc = z((2, 2, 2), device=DEV)
+    x = z((1, 2, 64), device=DEV, dtype=torch.bfloat16)
+    one = i32([1])
+    tab = i32([[0, 1]])
+    cu = i32([0, 1])
+    with pytest.raises(ValueError):
+        q.attn_kv8_paged(x, kc, kc.view(torch.float8_e4m3fn), sc, tab, one, cu)
+    with pytest.raises(ValueError):
+        q.attn_kv8_paged(x.float(), kc, kc, sc, tab, one, cu)
+    with pytest.raises(ValueError):
+        q.attn_kv8_paged(x, kc, kc, sc, tab.long(), one, cu)
+    with pytest.raises(ValueError):
+        q.attn_kv8_paged(x, kc, kc, sc[:1], tab, one, cu)
+    with pytest.raises(ValueError):
+        q.attn_kv8_paged(x, kc, kc, sc, tab, one, i32([0, 1, 1]))
+    with pytest.raises(q.QGError):
+        q.attn_kv8_paged(z((1, 3, 64), device=DEV, dtype=torch.bfloat16), kc, kc, sc, tab, one, cu)
+    with pytest.raises(ValueError):
+        q.kv8_append(x, x[:, :1], one, kc, kc, sc)
+    with pytest.raises(ValueError):
+        q.kv8_append(x.half(), x.half(), one, kc, kc, sc)
+    with pytest.raises(ValueError):
+        q.kv8_append(x.transpose(1, 2), x.transpose(1, 2), one, kc, kc, sc)
+    with pytest.raises(ValueError):
+        q.kv8_read(torch.zeros(1, device=DEV, dtype=torch.int64), kc, kc, sc)
+    with pytest.raises(ValueError):
+        q.kv8_block_plan(one, i32([1, 2]), tab, one, one, 16, 4)
+    with pytest.raises(q.QGError):
+        q.rmsnorm_residual(z((1, 33), device=DEV), z(33, device=DEV))
+    with pytest.raises(ValueError):
+        q.rmsnorm_residual(z((1, 64), device=DEV), z(32, device=DEV))
+    with pytest.raises(ValueError):
+        q.rmsnorm_residual(z((1, 64), device=DEV, dtype=torch.float16), z(64, device=DEV))
+
+
+# --------------------------------------------------------------------------
+# guard bands
+# --------------------------------------------------------------------------
+
+BAND = 4096
+
+
+def banded(shape, dtype):
+    """A tensor between two bands of a fixed byte pattern, and the whole buffer."""
+    n = math.prod(shape) * torch.empty(0, dtype=dtype).element_size()
+    buf = torch.full((2 * BAND + n + 64,), 0xA5, device=DEV, dtype=torch.uint8)
+    return buf[BAND:BAND + n].view(dtype).view(shape), (buf, n)
+
+
+def intact(band):
+    buf, n = band
+    return bool((buf[:BAND] == 0xA5).all()) and bool((buf[BAND + n:] == 0xA5).all())
+
+
+def test_writes_stay_inside(q):
+    rng = np.random.default_rng(51)
+    bands = []
+
+    def make(shape, dtype):
+        t, b = banded(shape, dtype)
+        bands.append(b)
+        return t
+    # plan
+    old, new, table, free, count = plan_state(rng, 37, 16, 90, 30, 1)
+    tokens = int(np.maximum(new - old, 0).sum())
+    t = make(table.shape, torch.int32).copy_(i32(table))
+    f = make(free.shape, torch.int32).copy_(i32(free))
+    out = dict(free_count_out=make((1,), torch.int32), cu_new=make((38,), torch.int32),
+               slot_map=make((tokens + 1,), torch.int32), positions=make((tokens + 1,), torch.int32),
+               info=make((4,), torch.int32), workspace=make((16,), torch.uint8).zero_())
+    q.kv8_block_plan(i32(old), i32(new), t, f, i32([count]), 16, tokens + 1, **out)
+    # append and attention
+    for D, bs, fmt in ((128, 16, "i8"), (64, 48, "e4m3"), (256, 32, "i8"), (48, 16, "e4m3")):
+        H, nb = 3, 4
+        kc, vc, sc = random_cache(rng, nb, H, bs, D, fmt)
+        kd = make(kc.shape, DT[fmt])
+        vd = make(vc.shape, DT[fmt])
+        kd.view(torch.uint8).copy_(torch.from_numpy(kc))
+        vd.view(torch.uint8).copy_(torch.from_numpy(vc))
+        sd = make(sc.shape, torch.float32).copy_(torch.from_numpy(sc))
+        slots = list(range(bs - 3, bs)) + list(range((nb - 1) * bs, nb * bs))
+        k = torch.randn((len(slots), H, D), device=DEV)
+        q.kv8_append(k, k, i32(slots), kd, vd, sd)
+        x = torch.randn((5, 9, D), device=DEV).to(torch.bfloat16)
+        need = q.lib().qg_attn_kv8_workspace_size(9, H, D)
+        ws = make((max(16, need),), torch.uint8).zero_()
+        o = make((5, 9, D), torch.bfloat16)
+        q.attn_kv8_paged(x, kd, vd, sd, i32([[3, 0, 1, 2], [1, 2, 0, 3]]), i32([4 * bs, bs + 1]), i32([0, 3, 5]), out=o,
+                         workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.isfinite(o).all()
+    # norm
+    for M, K in ((3, 96), (2, 8224)):
+        x = torch.randn((M, K), device=DEV)
+        w = torch.ones(K, device=DEV)
+        ro = make((M, K), torch.float32)
+        q.rmsnorm_residual(x, w, residual=x, residual_out=ro, out=make((M, K), torch.bfloat16))
+        q.rmsnorm_residual_i8(x, w, residual=x, residual_out=ro, q=make((M, K), torch.int8),
+                              scale=make((M,), torch.float32))
+    torch.cuda.synchronize()
+    assert all(intact(b) for b in bands)
