@@ -532,68 +532,30 @@ def gemm_w8a8_i32(a, w, c=None, stream=None):
 
 KV_I8, KV_E4M3 = 0, 1
 DT_BF16, DT_F32 = 0, 1
-_KV_FORMAT = {torch.int8: KV_I8, torch.float8_e4m3fn: KV_E4M3}
-_DTYPE = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+
+_bind = None
 
 
-def _dtype(t, name):
-    dt = _DTYPE.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"{name} must be bfloat16 or float32")
-    return dt
+def _raise(status, where):
+    _check(status, where)
 
 
-def _ints(t, name, *shape):
-    """An int32 CUDA tensor, contiguous, of this shape (None: any extent)."""
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name} must be int32")
-    _need(t, 4, name)
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-
-
-def _cache_shape(k_cache, v_cache, scales):
-    """(num_blocks, Hkv, block_size, D, format) of a cache, checked."""
-    fmt = _KV_FORMAT.get(k_cache.dtype)
-    if fmt is None or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must both be int8 or both float8_e4m3fn")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape [num_blocks][Hkv][block_size][D]")
-    nb, Hkv, bs, D = k_cache.shape
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, 1, n)
-    _need(scales, 4, "scales")
-    if scales.dtype != torch.float32 or scales.shape != (nb, Hkv, 2):
-        raise ValueError("scales must be float32 [num_blocks][Hkv][2]")
-    return nb, Hkv, bs, D, fmt
-
-
-def _token_stride(t, name):
-    """Elements between the tokens of a [T][heads][D] tensor whose tokens are dense."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
-        raise ValueError(f"{name} must be [T][heads][D] with dense tokens")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-_ZEROED = {}
-
-
-def _zeroed_workspace(what, nbytes, device, stream):
-    """A workspace that every call leaves as it found it (counters at zero),
-    cached per (use, device, stream): calls on one stream are ordered, so they
-    may share it. Inside a stream capture a fresh one is made and not cached."""
-    st = torch.cuda.current_stream(device) if stream is None else stream
-    key = (what, device, st.cuda_stream)
-    ws = _ZEROED.get(key)
-    if ws is None or ws.numel() < nbytes:
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(nbytes, device=device, dtype=torch.uint8)
-        with torch.cuda.stream(st):
-            ws = torch.zeros(nbytes, device=device, dtype=torch.uint8)
-        _ZEROED[key] = ws
-    return ws
+def _binding():
+    """The compiled half of the binding (_qgbind.so, built by build.py)."""
+    global _bind
+    if _bind is None:
+        import importlib.util
+        lib()
+        path = os.path.join(_HERE, "_qgbind.so")
+        if not os.path.exists(path):
+            raise ImportError(f"_qgbind.so is not built ({path}); run "
+                              "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("_qgbind", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.set_raise(_raise)
+        _bind = m
+    return _bind
 
 
 def kv8_block_plan(old_lens, new_lens, block_table, free_list, free_count, block_size, max_tokens,
@@ -603,59 +565,25 @@ def kv8_block_plan(old_lens, new_lens, block_table, free_list, free_count, block
     (int32 [R]); block_table int32 [R][max_blocks] and free_list int32
     [num_blocks] are updated in place. Returns (free_count_out, cu_new,
     slot_map, positions, info); info = [new tokens, taken, released, state],
-    state 0 unless nothing was done (see the header)."""
-    R = old_lens.numel()
-    _ints(old_lens, "old_lens", R)
-    _ints(new_lens, "new_lens", R)
-    _ints(block_table, "block_table", R, None)
-    _ints(free_list, "free_list", None)
-    _ints(free_count, "free_count", 1)
-    dev, i32 = old_lens.device, torch.int32
-    if free_count_out is None:
-        free_count_out = torch.empty(1, device=dev, dtype=i32)
-    if cu_new is None:
-        cu_new = torch.empty(R + 1, device=dev, dtype=i32)
-    if slot_map is None:
-        slot_map = torch.empty(max_tokens, device=dev, dtype=i32)
-    if positions is None:
-        positions = torch.empty(max_tokens, device=dev, dtype=i32)
-    if info is None:
-        info = torch.empty(4, device=dev, dtype=i32)
-    if workspace is None:
-        workspace = _zeroed_workspace("plan", 256, dev, stream)
-    _check(lib().kv8_block_plan(_p(old_lens), _p(new_lens), R, block_size, _p(block_table), block_table.shape[1],
-                                _p(free_list), free_list.numel(), _p(free_count), _p(free_count_out), _p(cu_new),
-                                _p(slot_map), _p(positions), max_tokens, _p(info), _p(workspace), workspace.numel(),
-                                _stream(stream)), "kv8_block_plan")
-    return free_count_out, cu_new, slot_map, positions, info
+    state 0 unless nothing was done (see the header). free_count_out may be
+    free_count. The zeroed workspace is kept per (device, stream)."""
+    return (_bind or _binding()).block_plan(old_lens, new_lens, block_table, free_list, free_count, block_size,
+                                            max_tokens, free_count_out, cu_new, slot_map, positions, info, workspace,
+                                            stream)
 
 
 def kv8_append(k, v, slot_map, k_cache, v_cache, scales, stream=None):
     """Quantize the new tokens' k, v ([T][Hkv][D], bf16 or fp32, tokens dense,
-    any token stride) into their slots of the cache, in place."""
-    nb, Hkv, bs, D, fmt = _cache_shape(k_cache, v_cache, scales)
-    T = k.shape[0]
-    ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
-    if k.shape != (T, Hkv, D) or v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must have one type and shape [T][Hkv][D]")
-    _ints(slot_map, "slot_map", T)
-    _check(lib().kv8_append(_p(k), _p(v), _dtype(k, "k"), ks, vs, _p(slot_map), T, Hkv, D, bs, nb, fmt, _p(k_cache),
-                            _p(v_cache), _p(scales), _stream(stream)), "kv8_append")
+    any token stride) into their slots of the cache (int8 or float8_e4m3fn
+    [num_blocks][Hkv][block_size][D], scales fp32 [num_blocks][Hkv][2]), in
+    place."""
+    (_bind or _binding()).append(k, v, slot_map, k_cache, v_cache, scales, stream)
 
 
 def kv8_read(block_ids, k_cache, v_cache, scales, stream=None):
     """Blocks as the values they stand for: (k, v bf16 [B][Hkv][block_size][D],
     their scales fp32 [B][Hkv][2])."""
-    nb, Hkv, bs, D, fmt = _cache_shape(k_cache, v_cache, scales)
-    B = block_ids.numel()
-    _ints(block_ids, "block_ids", B)
-    dev = k_cache.device
-    k = torch.empty((B, Hkv, bs, D), device=dev, dtype=torch.bfloat16)
-    v = torch.empty((B, Hkv, bs, D), device=dev, dtype=torch.bfloat16)
-    s = torch.empty((B, Hkv, 2), device=dev, dtype=torch.float32)
-    _check(lib().kv8_read(_p(block_ids), B, Hkv, D, bs, nb, fmt, _p(k_cache), _p(v_cache), _p(scales), _p(k), _p(v),
-                          _p(s), _stream(stream)), "kv8_read")
-    return k, v, s
+    return (_bind or _binding()).read(block_ids, k_cache, v_cache, scales, stream)
 
 
 def attn_kv8_paged(q, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tree_mask=None, softmax_scale=None,
@@ -664,66 +592,17 @@ def attn_kv8_paged(q, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tre
     paged cache: request r's queries are rows cu_q[r] .. cu_q[r + 1] - 1, the
     last of its ctx_lens[r] tokens; causal, or by tree_mask (int32 [T], bit j:
     query token j of the request is seen). softmax_scale defaults to D ** -0.5.
-    Returns out, bf16 [T][Hq][D]."""
-    nb, Hkv, bs, D, fmt = _cache_shape(k_cache, v_cache, scales)
-    stride = _token_stride(q, "q")
-    T, Hq = q.shape[0], q.shape[1]
-    if q.dtype != torch.bfloat16 or q.shape[2] != D:
-        raise ValueError("q must be bfloat16 [T][Hq][D] with the cache's D")
-    R = ctx_lens.numel()
-    _ints(ctx_lens, "ctx_lens", R)
-    _ints(cu_q, "cu_q", R + 1)
-    _ints(block_table, "block_table", R, None)
-    if tree_mask is not None:
-        _ints(tree_mask, "tree_mask", T)
-    if out is None:
-        out = torch.empty((T, Hq, D), device=q.device, dtype=torch.bfloat16)
-    else:
-        _need(out, 2, "out")
-        if out.dtype != torch.bfloat16 or out.shape != q.shape:
-            raise ValueError("out must be bfloat16 [T][Hq][D]")
-    L = lib()
-    if workspace is None:
-        need = L.qg_attn_kv8_workspace_size(Hq, Hkv, D)
-        if need:
-            workspace = _zeroed_workspace("attn", need, q.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(L.attn_kv8_paged(_p(q), stride, _p(k_cache), _p(v_cache), _p(scales), _p(block_table), _p(ctx_lens),
-                            _p(cu_q), _p(tree_mask), R, T, Hq, Hkv, D, bs, nb, block_table.shape[1], fmt,
-                            D ** -0.5 if softmax_scale is None else softmax_scale, _p(out), _p(workspace), ws_bytes,
-                            _stream(stream)), "attn_kv8_paged")
-    return out
-
-
-def _norm_args(x, weight, residual, residual_out):
-    M, K = x.shape
-    _need(x, x.element_size(), "x")
-    _need(weight, weight.element_size(), "weight")
-    if weight.shape != (K,):
-        raise ValueError("weight must be [K]")
-    if residual is not None:
-        _need(residual, residual.element_size(), "residual")
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
-    if residual_out is not None:
-        _need(residual_out, residual_out.element_size(), "residual_out")
-        if residual_out.shape != x.shape or (residual is not None and (
-                residual.shape != x.shape or residual.dtype != residual_out.dtype)):
-            raise ValueError("residual and residual_out must be [M][K] of one type")
-    res_dt = DT_F32 if residual_out is None else _dtype(residual_out, "residual")
-    return M, K, _dtype(x, "x"), res_dt, _dtype(weight, "weight"), residual_out
+    Returns out, bf16 [T][Hq][D]. The zeroed workspace is kept per (device,
+    stream)."""
+    return (_bind or _binding()).attention(q, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tree_mask,
+                                           softmax_scale, out, workspace, stream)
 
 
 def rmsnorm_residual(x, weight, residual=None, eps=1e-6, residual_out=None, out=None, stream=None):
     """h = x + residual, y = h rsqrt(mean(h^2) + eps) weight: returns (y bf16
-    [M][K], h in the residual's type). x, residual, weight bf16 or fp32;
-    residual_out may be residual (in place)."""
-    M, K, xd, rd, wd, residual_out = _norm_args(x, weight, residual, residual_out)
-    if out is None:
-        out = torch.empty((M, K), device=x.device, dtype=torch.bfloat16)
-    _check(lib().rmsnorm_residual(_p(x), xd, _p(residual), rd, _p(weight), wd, eps, M, K, _p(residual_out), _p(out),
-                                  _stream(stream)), "rmsnorm_residual")
-    return out, residual_out
+    [M][K], h in the residual's type, None without one). x, residual, weight
+    bf16 or fp32; residual_out may be residual (in place)."""
+    return (_bind or _binding()).norm_bf16(x, weight, residual, eps, residual_out, out, stream)
 
 
 def rmsnorm_residual_i8(x, weight, residual=None, sign_bits=None, eps=1e-6, residual_out=None, q=None, scale=None,
@@ -731,13 +610,4 @@ def rmsnorm_residual_i8(x, weight, residual=None, sign_bits=None, eps=1e-6, resi
     """As rmsnorm_residual, the result as int8 codes with a scale per row, after
     the randomized Hadamard transform when sign_bits (int32 [K/32]) are given:
     returns (q int8 [M][K], scale fp32 [M], h)."""
-    M, K, xd, rd, wd, residual_out = _norm_args(x, weight, residual, residual_out)
-    if sign_bits is not None:
-        _ints(sign_bits, "sign_bits", K // 32)
-    if q is None:
-        q = torch.empty((M, K), device=x.device, dtype=torch.int8)
-    if scale is None:
-        scale = torch.empty(M, device=x.device, dtype=torch.float32)
-    _check(lib().rmsnorm_residual_i8(_p(x), xd, _p(residual), rd, _p(weight), wd, eps, _p(sign_bits), M, K,
-                                     _p(residual_out), _p(q), _p(scale), _stream(stream)), "rmsnorm_residual_i8")
-    return q, scale, residual_out
+    return (_bind or _binding()).norm_i8(x, weight, residual, sign_bits, eps, residual_out, q, scale, stream)

@@ -1,8 +1,10 @@
-"""Build libqgemv.so (sm_103a) in-tree with nvcc.
+"""Build libqgemv.so (sm_103a) in-tree with nvcc, and the compiled half of its
+Python binding with g++.
 
 Every .cu under csrc/ is compiled in parallel for sm_103a only
 (-gencode arch=compute_103a,code=sm_103a, -lineinfo, no fast-math) and linked
-into skinny_gemm_qgemv_gb300/libqgemv.so next to this file.
+into skinny_gemm_qgemv_gb300/libqgemv.so next to this file; csrc/binding.cpp
+becomes _qgbind.so beside it, which finds libqgemv.so in its own folder.
 """
 from __future__ import annotations
 
@@ -19,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(HERE, "libqgemv.so")
+BINDING = os.path.join(HERE, "_qgbind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -49,23 +52,64 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(OBJDIR, "binding.o")
+    deps = [src, os.path.join(INCLUDE, "qgemv.h"), torch.__file__]
+    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(d) for d in deps):
+        return obj
+    tinc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", src, "-o", obj, "-I", INCLUDE,
+           "-I", tinc, "-I", os.path.join(tinc, "torch", "csrc", "api", "include"), "-I",
+           os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str, force: bool) -> None:
+    import torch
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= os.path.getmtime(obj) and not force:
+        return
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libqgemv.so", "-Wl,-rpath,$ORIGIN", "-L", tlib,
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     if force:
         for o in glob.glob(os.path.join(OBJDIR, "*.o")):
             os.remove(o)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        bobj = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        bobj = bobj.result()
+    _link(objs, force)
+    _link_binding(bobj, force)
+    return LIB
+
+
+def _link(objs, force: bool) -> None:
     if os.path.exists(LIB) and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs) and not force:
-        return LIB
+        return
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
