@@ -118,11 +118,691 @@ __global__ void __launch_bounds__(32 * kPlainWarps) attn_kv8_plain_kernel(AttnAr
   }
 }
 
+// ---------------------------------------------------------------------------
+// The tensor-core kernel: D = 64, 128 or 256
+// ---------------------------------------------------------------------------
+constexpr int kAttnWarps = 8;
+constexpr int kUnit = 16;                       // tokens of one ring stage: one block, one scale pair
+constexpr float kNoMax = -1e30f;                // running maximum before any seen token
+constexpr float kSlack = 8.f;                   // log2: probabilities stay below 2^8 (fp16 holds 2^15)
+constexpr float kMinScale = 5.4210109e-20f;     // 2^-64
+constexpr size_t kAttnCounterBytes = 4096;      // one counter per CTA
+
+// bytes of the partial results of one CTA's piece: fp32 outputs, then (max, sum) per row
+__host__ __device__ constexpr size_t attn_piece_bytes(int rows, int D) { return (size_t)rows * (D * 4 + 8); }
+
+template <int D, int NT, int FMT>
+struct AttnShape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kSubs = D > 128 ? D / 128 : 1;  // 128-byte column blocks of a token
+  static constexpr int kRowBytes = D > 128 ? 128 : D;
+  static constexpr int kHalves = D / 64;               // 64-byte steps of q . k
+  static constexpr int kMt = D / 16;                   // 16-row tiles of the output's transpose
+  static constexpr int kVB = D == 64 ? 8 : 16;         // bytes of a value row that a lane holds
+  static constexpr int kStage = 2 * kUnit * D;         // a unit's keys, then its values
+  static constexpr int kNB = NT > 2 ? 2 : NT;          // 8-row tiles combined at a time
+  static constexpr int kPassNt = D == 256 ? 1 : kNB;
+  static constexpr int kBuf = kAttnWarps * kMt * kPassNt * 32 * 16;
+  static constexpr int kQ = kHalves * 4 * NT * 32 * 8;
+};
+
+// Token of MMA row i of a unit. Rows of the swizzled stage that one shared-memory
+// phase touches together must differ in the address bits that the swizzle does
+// not already spread: D >= 128 (128-byte rows, chunk ^= row & 7) pairs rows
+// that differ by 4, D = 64 (64-byte rows, chunk ^= row / 2 & 3) pairs odd with even.
+template <int D>
+__device__ __forceinline__ int unit_token(int i) {
+  const int b0 = i & 1, b1 = i >> 1 & 1, b2 = i >> 2 & 1;
+  const int t = D == 64 ? (b2 << 2 | b1 << 1 | (b0 ^ b1)) : ((b0 ^ b2) << 2 | b1 << 1 | b2);
+  return t | (i & 8);
+}
+
+// byte offset of 16-byte chunk `ch` of token row `row` in a swizzled [16][kRowBytes] tile
+template <int D>
+__device__ __forceinline__ uint32_t tile_offset(int row, int ch) {
+  return D == 64 ? row * 64 + ((ch ^ (row >> 1 & 3)) << 4) : row * 128 + ((ch ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+__device__ __forceinline__ uint32_t hsub2_1152(uint32_t a) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x64806480u));
+  return r;
+}
+// codes (b0, b1) and (b2, b3) of a word as f16 pairs, exact. int8: b ^ 0x80 =
+// b + 128 under the exponent byte 0x64 is fp16 1024 + 128 + b.
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == QG_KV_I8) {
+    const uint32_t u = w ^ 0x80808080u;
+    lo = hsub2_1152(prmt(u, 0x64646464u, 0x4140u));
+    hi = hsub2_1152(prmt(u, 0x64646464u, 0x4342u));
+  } else {
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The CTA's view of the batch: requests, their steps and where a step lies.
+// A request has one item per key/value head and tile of kRows query rows, an
+// item has ceil(units / warps) steps.
+struct AttnBatch {
+  const long long* first;  // [R + 1] steps before the request
+  const int* ctx;          // [R]
+  const int* cu;           // [R + 1]
+  int R, G;
+};
+struct AttnPlace {
+  int r, h, rt;   // request, key/value head, row tile
+  int s, steps;   // step within its item, steps of the item
+};
+__device__ __forceinline__ int attn_steps(int ctx) {
+  return max(1, (ctx + kUnit * kAttnWarps - 1) / (kUnit * kAttnWarps));
+}
+template <int ROWS>
+__device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, long long step) {
+  int lo = 0, hi = b.R;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (b.first[mid] <= step)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  AttnPlace p;
+  p.r = lo;
+  p.steps = attn_steps(b.ctx[lo]);
+  const int tiles = ((b.cu[lo + 1] - b.cu[lo]) * b.G + ROWS - 1) / ROWS;
+  const long long rem = step - b.first[lo];
+  const int item = (int)(rem / p.steps);
+  p.s = (int)(rem - (long long)item * p.steps);
+  p.h = item / tiles;
+  p.rt = item - p.h * tiles;
+  return p;
+}
+
+template <int D, int NT, int FMT>
+__global__ void __launch_bounds__(32 * kAttnWarps, 1)
+    attn_kv8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
+                    int stages, uint32_t ring_offset) {
+  using S = AttnShape<D, NT, FMT>;
+  constexpr int NW = kAttnWarps, ROWS = S::kRows;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // layout: ring | combine buffer | q fragments | rows | warp maxima and sums | meta | barriers | batch
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  uint8_t* ring = smem;
+  uint8_t* p = smem + (size_t)ring_offset;
+  float4* buf = reinterpret_cast<float4*>(p);
+  p += S::kBuf;
+  uint2* qfrag = reinterpret_cast<uint2*>(p);  // [half * 4 + word][nt][lane]
+  p += S::kQ;
+  float* row_factor = reinterpret_cast<float*>(p);             // [ROWS]
+  int* row_limit = reinterpret_cast<int*>(p + 4 * ROWS);       // [ROWS] tokens below it are seen
+  uint32_t* row_bits = reinterpret_cast<uint32_t*>(p + 8 * ROWS);  // [ROWS] draft tokens seen beyond it
+  p += 12 * ROWS;
+  float* wmax = reinterpret_cast<float*>(p);  // [NW][ROWS]
+  p += 4 * NW * ROWS;
+  float* wsum = reinterpret_cast<float*>(p);  // [NW][ROWS]
+  p += 4 * NW * ROWS;
+  float4* meta = reinterpret_cast<float4*>(p);  // [NW][stages] key scale, log2 and inverse of the value scale, kind
+  p += 16 * NW * stages;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(p);  // [NW][stages]
+  p += 8 * NW * stages;
+  long long* first = reinterpret_cast<long long*>(p);  // [R + 1]
+  int* ctxs = reinterpret_cast<int*>(first + a.R + 1);  // [R]
+  int* cus = ctxs + a.R;                               // [R + 1]
+  __shared__ long long scan_part[NW];
+  __shared__ unsigned arrived;
+
+  if (lane == 0)
+    for (int s = 0; s < stages; ++s) mbar_init(bars + warp * stages + s, 1);
+  fence_mbar_init();
+  pdl_wait();
+
+  // ---- the batch's steps ----
+  const int G = a.Hq / a.Hkv;
+  const AttnBatch batch = {first, ctxs, cus, a.R, G};
+  {
+    const int per = (a.R + 32 * NW - 1) / (32 * NW);
+    const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
+    const int most = a.max_blocks * a.bs;
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) {
+      const int q0 = min(max(a.cu_q[r], 0), a.T), q1 = min(max(a.cu_q[r + 1], 0), a.T);
+      int ctx = max(0, a.ctx_lens[r]);
+      if (ctx > most) {
+        ctx = most;
+        if (blockIdx.x == 0) report_error(a.err, kErrKvLength);
+      }
+      ctxs[r] = ctx;
+      cus[r] = q0;
+      if (r == a.R - 1) cus[a.R] = q1;
+      first[r] = mine;
+      mine += (long long)attn_steps(ctx) * a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS);
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) scan_part[warp] = inc;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before += scan_part[w];
+      total += scan_part[w];
+    }
+    for (int r = r0; r < r1; ++r) first[r] += before;
+    if (threadIdx.x == 0) first[a.R] = total;
+    __syncthreads();
+  }
+  const long long W = first[a.R];
+  const long long A = min((long long)gridDim.x, W);  // CTAs with work
+  if (blockIdx.x >= A) return;
+  const long long c0 = blockIdx.x * W / A, c1 = (blockIdx.x + 1) * W / A;
+  const int n = (int)(c1 - c0);
+
+  // ---- producer side of the warp's ring: lane l looks after step 32 b + l of batch b ----
+  uint64_t* bar = bars + warp * stages;
+  float4* my_meta = meta + warp * stages;
+  uint8_t* my_ring = ring + (size_t)warp * stages * S::kStage;
+  int page = -1, row = 0;
+  float ks = 0.f, vs = 0.f;
+  int n_blk = -1, n_head = 0, n_row = 0;  // of the following batch
+  float2 n_scale = make_float2(0.f, 0.f);
+  auto look_table = [&](int b) {
+    n_blk = -1;
+    const long long step = c0 + 32LL * b + lane;
+    if (step < c1) {
+      const AttnPlace at = attn_locate<ROWS>(batch, step);
+      const int tok = (at.s * NW + warp) * kUnit;
+      if (tok < ctxs[at.r]) {
+        n_blk = __ldg(a.table + (size_t)at.r * a.max_blocks + tok / a.bs);
+        n_head = at.h;
+        n_row = tok % a.bs;
+        if (n_blk < 0 || n_blk >= a.num_blocks) {
+          report_error(a.err, kErrKvBlock);
+          n_blk = -1;
+        }
+      }
+    }
+  };
+  auto look_scale = [&]() {
+    if (n_blk >= 0)
+      n_scale = __ldg(reinterpret_cast<const float2*>(a.scales) + (size_t)n_blk * a.Hkv + n_head);
+  };
+  auto next_batch = [&]() {
+    page = n_blk >= 0 ? n_blk * a.Hkv + n_head : -1;
+    row = n_row;
+    ks = n_scale.x;
+    vs = n_scale.y;
+  };
+  auto issue = [&](int i, int slot) {
+    const int l = i & 31;
+    if (l == 0 && i > 0) next_batch();
+    if (l == 0) look_table((i >> 5) + 1);
+    if (l == 16) look_scale();
+    if (lane == l) {
+      const bool ok = page >= 0;
+      // a value scale below 2^-64 counts as 2^-64: what it adds to an output is below 2^-55; of a block of
+      // zero scale only the probabilities count
+      const float v = vs < kMinScale ? kMinScale : vs;
+      my_meta[slot] = make_float4(ks, log2f(v), 1.f / v, !ok ? 0.f : vs == 0.f ? 2.f : 1.f);
+      if (ok) {
+        mbar_arrive_expect_tx(bar + slot, S::kStage);
+        const uint32_t dst = smem_u32(my_ring + (size_t)slot * S::kStage);
+#pragma unroll
+        for (int sub = 0; sub < S::kSubs; ++sub) {
+          tma_load_3d(dst + sub * kUnit * S::kRowBytes, &kmap, sub * 128, row, page, bar + slot);
+          tma_load_3d(dst + kUnit * D + sub * kUnit * S::kRowBytes, &vmap, sub * 128, row, page, bar + slot);
+        }
+      } else {
+        mbar_arrive(bar + slot);
+      }
+    }
+  };
+  look_table(0);
+  look_scale();
+  next_batch();
+  {
+    const int k = min(stages, n);
+    for (int i = 0; i < k; ++i) issue(i, i);
+  }
+
+  // ---- consumer ----
+  float acc[NT][S::kMt][4];
+  float m[NT][2], l[NT][2], rf[NT][2];
+  constexpr bool kQRegs = NT * S::kHalves <= 4;
+  uint2 qr[kQRegs ? S::kHalves * 4 : 1][kQRegs ? NT : 1];
+  AttnPlace item = {};
+  long long seg_end = c0;
+  int ctx = 0, nq = 0, q0 = 0, base = 0;
+  bool ok = true;
+
+  auto begin_segment = [&](long long step) {
+    item = attn_locate<ROWS>(batch, step);
+    seg_end = min(c1, step - item.s + item.steps);
+    ctx = ctxs[item.r];
+    q0 = cus[item.r];
+    nq = cus[item.r + 1] - q0;
+    base = ctx - nq;
+    // q as the B operand: warp w prepares 8-row tile w % NT, half w / NT, ...; 2^-sigma q in fp16, exact
+    const bool tree = a.tree && nq <= 32;
+    for (int nt = warp; nt < NT; nt += NW) {
+      const int rho = item.rt * ROWS + nt * 8 + g;
+      const bool live = rho < nq * G;
+      const int t = q0 + rho / G, hq = item.h * G + rho % G;
+      const uint16_t* src = a.q + (live ? t * a.q_stride + (size_t)hq * D + 16 * c : 0);
+      uint4 raw[S::kHalves][2];
+      float amax = 0.f;
+#pragma unroll
+      for (int hf = 0; hf < S::kHalves; ++hf) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          raw[hf][k] = live ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {raw[hf][k].x, raw[hf][k].y, raw[hf][k].z, raw[hf][k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+        }
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int sigma = fp16_prescale_exp(amax);
+      const float down = pow2f(-sigma);
+#pragma unroll
+      for (int hf = 0; hf < S::kHalves; ++hf) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint4 u = raw[hf][w >> 1];
+          const uint32_t x = w & 1 ? u.z : u.x, y = w & 1 ? u.w : u.y;
+          qfrag[((hf * 4 + w) * NT + nt) * 32 + lane] =
+              make_uint2(f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down),
+                         f16x2(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xFFFF0000u) * down));
+        }
+      }
+      if (c == 0) {
+        row_factor[nt * 8 + g] = a.scale_log2 * pow2f(sigma);
+        row_limit[nt * 8 + g] = !live ? 0 : tree ? base : base + rho / G + 1;
+        row_bits[nt * 8 + g] = live && tree ? a.tree[t] & (0xFFFFFFFFu >> (32 - nq)) : 0u;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        rf[nt][j] = row_factor[nt * 8 + 2 * c + j];
+        m[nt][j] = kNoMax;
+        l[nt][j] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < S::kMt; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[nt][mt][j] = 0.f;
+      if (kQRegs) {
+#pragma unroll
+        for (int k = 0; k < S::kHalves * 4; ++k) qr[k][nt] = qfrag[(k * NT + nt) * 32 + lane];
+      }
+    }
+  };
+
+  // one unit of 16 tokens whose first is `tok`, landed at `stage`
+  auto compute = [&](uint32_t stage, const float4 mt_, int tok) {
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+    // S^T = K q^T: lane (g, c) holds tokens g, g + 8 and 16-byte chunk c of each 64 bytes
+    const int t0 = unit_token<D>(g), t1 = t0 + 8;
+#pragma unroll
+    for (int hf = 0; hf < S::kHalves; ++hf) {
+      const uint32_t tile = stage + (hf >> 1) * kUnit * S::kRowBytes;
+      const int ch = D == 64 ? c : c + 4 * (hf & 1);
+      const uint4 k0 = lds128(tile + tile_offset<D>(t0, ch)), k1 = lds128(tile + tile_offset<D>(t1, ch));
+      const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t f[4];
+        codes_to_f16<FMT>(w0[w], f[0], f[2]);
+        codes_to_f16<FMT>(w1[w], f[1], f[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 b = kQRegs ? qr[hf * 4 + w][nt] : qfrag[((hf * 4 + w) * NT + nt) * 32 + lane];
+          mma16816(s[nt], f, b.x, b.y);
+        }
+      }
+    }
+    // t = log2 of (probability times value scale); lane: tokens t0, t1 of rows 2 c, 2 c + 1
+    const bool edge = tok + kUnit > base;  // some row may not see some token
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(s[nt][j], mt_.x * rf[nt][j & 1], mt_.y);
+      if (edge) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = tok + (j < 2 ? t0 : t1), rr = nt * 8 + 2 * c + (j & 1);
+          const unsigned d = (unsigned)(at - base);
+          const bool seen = at < row_limit[rr] || (d < 32u && (row_bits[rr] >> d & 1u));
+          if (!seen) s[nt][j] = -INFINITY;
+        }
+      }
+      grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kSlack || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kSlack;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = fmaxf(s[nt][j], s[nt][j + 2]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = fmaxf(m[nt][j], x), f = ex2(m[nt][j] - mn);
+          m[nt][j] = mn;
+          l[nt][j] *= f;
+#pragma unroll
+          for (int mt = 0; mt < S::kMt; ++mt) acc[nt][mt][j] *= f, acc[nt][mt][j + 2] *= f;
+        }
+      }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float e[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = ex2(s[nt][j] - m[nt][j & 1]);
+      l[nt][0] = fmaf(e[0] + e[2], mt_.z, l[nt][0]);
+      l[nt][1] = fmaf(e[1] + e[3], mt_.z, l[nt][1]);
+      // (token, row) -> (row, token): the B operand of the value product
+      pb[nt][0] = transpose8x8(f16x2(e[0], e[1]));
+      pb[nt][1] = transpose8x8(f16x2(e[2], e[3]));
+    }
+    if (mt_.w == 2.f) return;
+    // O^T += V^T p^T: lane (g, c) holds kVB bytes of the tokens of MMA columns 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+    const int r0 = unit_token<D>(2 * c), r1 = unit_token<D>(2 * c + 1);
+#pragma unroll
+    for (int sub = 0; sub < S::kSubs; ++sub) {
+      const uint32_t tile = stage + kUnit * D + sub * kUnit * S::kRowBytes;
+      uint32_t v[4][S::kVB / 4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rr = (k & 1 ? r1 : r0) + (k & 2 ? 8 : 0);
+        if (D == 64) {
+          const uint2 x = lds64(tile + tile_offset<D>(rr, g >> 1) + 8 * (g & 1));
+          v[k][0] = x.x, v[k][1] = x.y;
+        } else {
+          const uint4 x = lds128(tile + tile_offset<D>(rr, g));
+          v[k][0] = x.x, v[k][1] = x.y, v[k][S::kVB / 4 - 2] = x.z, v[k][S::kVB / 4 - 1] = x.w;
+        }
+        if (FMT == QG_KV_E4M3 && edge && tok + rr >= ctx) {
+          // slots past the context may hold codes that are not numbers
+#pragma unroll
+          for (int w = 0; w < S::kVB / 4; ++w) v[k][w] = 0u;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < S::kVB / 4; ++w) {
+        // bytes (2 i, 2 i + 1) of a word: output rows 2 i (MMA row g) and 2 i + 1 (row g + 8) of a tile
+        uint32_t f[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          codes_to_f16<FMT>(prmt(v[2 * k][w], v[2 * k + 1][w], 0x5140u), f[0][2 * k], f[0][2 * k + 1]);
+          codes_to_f16<FMT>(prmt(v[2 * k][w], v[2 * k + 1][w], 0x7362u), f[1][2 * k], f[1][2 * k + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(acc[nt][sub * (S::kVB / 2) + 2 * w + i], f[i], pb[nt][0], pb[nt][1]);
+      }
+    }
+  };
+
+  // result of tile (mt, nt): lane (g, c) holds elements d, d + 1 of rows 2 c, 2 c + 1 as {d r0, d r1, d+1 r0, d+1 r1}
+  auto write_out = [&](int nt, int mt, const float4 o, float l0, float l1) {
+    const int d = mt / (S::kVB / 2) * 128 + S::kVB * g + 2 * (mt % (S::kVB / 2));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int rho = item.rt * ROWS + nt * 8 + 2 * c + j;
+      if (rho < nq * G) {
+        const float L = j ? l1 : l0, x = j ? o.y : o.x, y = j ? o.w : o.z;
+        const size_t t = q0 + rho / G, hq = item.h * G + rho % G;
+        // no token seen: 0
+        *reinterpret_cast<uint32_t*>(a.out + (t * a.Hq + hq) * D + d) =
+            L == 0.f ? 0u : f32_to_bf16x2(x / L, y / L);
+      }
+    }
+  };
+
+  auto end_segment = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+        l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+        l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+        if (g == 0) {
+          wmax[warp * ROWS + nt * 8 + 2 * c + j] = m[nt][j];
+          wsum[warp * ROWS + nt * 8 + 2 * c + j] = l[nt][j];
+        }
+      }
+    }
+    const long long item_first = seg_end - 1 - ((seg_end - 1 - first[item.r]) % item.steps);
+    const bool whole = item_first >= c0 && item_first + item.steps <= c1;
+    const int slot = item_first < c0 ? 0 : 1;
+    uint8_t* ws = static_cast<uint8_t*>(a.ws) + kAttnCounterBytes;
+    uint8_t* mine = ws + (size_t)(2 * blockIdx.x + slot) * attn_piece_bytes(ROWS, D);
+    float2* stat = reinterpret_cast<float2*>(mine + (size_t)ROWS * D * 4);
+    __syncthreads();
+#pragma unroll
+    for (int n0 = 0; n0 < NT; n0 += S::kPassNt) {
+#pragma unroll
+      for (int k = 0; k < S::kPassNt; ++k) {
+        const int nt = n0 + k;
+        float f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float mm = kNoMax;
+          for (int w = 0; w < NW; ++w) mm = fmaxf(mm, wmax[w * ROWS + nt * 8 + 2 * c + j]);
+          f[j] = ex2(m[nt][j] - mm);
+        }
+#pragma unroll
+        for (int mt = 0; mt < S::kMt; ++mt)
+          buf[((warp * S::kPassNt + k) * S::kMt + mt) * 32 + lane] =
+              make_float4(acc[nt][mt][0] * f[0], acc[nt][mt][1] * f[1], acc[nt][mt][2] * f[0], acc[nt][mt][3] * f[1]);
+      }
+      __syncthreads();
+      for (int q = warp; q < S::kPassNt * S::kMt; q += NW) {
+        const int k = q / S::kMt, mt = q - k * S::kMt, nt = n0 + k;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float mm[2] = {kNoMax, kNoMax}, ll[2] = {0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float4 x = buf[((w * S::kPassNt + k) * S::kMt + mt) * 32 + lane];
+          o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) mm[j] = fmaxf(mm[j], wmax[w * ROWS + nt * 8 + 2 * c + j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          for (int w = 0; w < NW; ++w)
+            ll[j] += wsum[w * ROWS + nt * 8 + 2 * c + j] * ex2(wmax[w * ROWS + nt * 8 + 2 * c + j] - mm[j]);
+        if (whole) {
+          write_out(nt, mt, o, ll[0], ll[1]);
+        } else {
+          reinterpret_cast<float4*>(mine)[(nt * S::kMt + mt) * 32 + lane] = o;
+          if (mt == 0 && g == 0) {
+            stat[nt * 8 + 2 * c] = make_float2(mm[0], ll[0]);
+            stat[nt * 8 + 2 * c + 1] = make_float2(mm[1], ll[1]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (whole) return;
+    // the CTA that brings an item's last piece adds the pieces up, in the order of the CTAs
+    const int f = (int)(((item_first + 1) * A - 1) / W), e = (int)(((item_first + item.steps) * A - 1) / W);
+    unsigned* count = static_cast<unsigned*>(a.ws) + f;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(arrived) : "l"(count) : "memory");
+      if (arrived == (unsigned)(e - f)) *count = 0u;  // the next call finds it as this one did
+    }
+    __syncthreads();
+    const bool last = arrived == (unsigned)(e - f);
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    for (int q = warp; q < NT * S::kMt; q += NW) {
+      const int nt = q / S::kMt, mt = q - nt * S::kMt;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float mm[2] = {kNoMax, kNoMax}, ll[2] = {0.f, 0.f};
+      for (int i = f; i <= e; ++i) {
+        const uint8_t* piece = ws + (size_t)(2 * i + (i == f && item_first >= i * W / A ? 1 : 0)) * attn_piece_bytes(ROWS, D);
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(piece) + (nt * S::kMt + mt) * 32 + lane);
+        const float4 st = __ldcg(reinterpret_cast<const float4*>(piece + (size_t)ROWS * D * 4) + (nt * 8 + 2 * c) / 2);
+        const float pm[2] = {st.x, st.z}, pl[2] = {st.y, st.w};
+        float fo[2], fn[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float mn = fmaxf(mm[j], pm[j]);
+          fo[j] = ex2(mm[j] - mn), fn[j] = ex2(pm[j] - mn);
+          mm[j] = mn;
+          ll[j] = ll[j] * fo[j] + pl[j] * fn[j];
+        }
+        o.x = o.x * fo[0] + x.x * fn[0], o.y = o.y * fo[1] + x.y * fn[1];
+        o.z = o.z * fo[0] + x.z * fn[0], o.w = o.w * fo[1] + x.w * fn[1];
+      }
+      write_out(nt, mt, o, ll[0], ll[1]);
+    }
+  };
+
+  int slot = 0;
+  uint32_t phase = 0;
+  for (int i = 0; i < n; ++i) {
+    if (c0 + i == seg_end) {
+      if (i > 0) end_segment();
+      begin_segment(c0 + i);
+    }
+    if (ok) ok = mbar_wait(bar + slot, phase, a.err, kErrAttnWait);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      const float4 mt_ = my_meta[slot];
+      if (mt_.w != 0.f) {
+        const int s = (int)(c0 + i - (seg_end - 1 - ((seg_end - 1 - first[item.r]) % item.steps)));
+        compute(smem_u32(my_ring + (size_t)slot * S::kStage), mt_, (s * NW + warp) * kUnit);
+      }
+      __syncwarp();
+      if (i + stages < n) issue(i + stages, slot);
+    }
+    if (++slot == stages) slot = 0, phase ^= 1u;
+  }
+  end_segment();
+  if (!ok)  // the copies still in flight land before the shared memory is given up (bounded waits)
+    for (int s = 0; s < stages; ++s) mbar_wait_n(bar + s, phase, nullptr, 0, 1u << 16);
+}
+
+struct AttnLaunch {
+  int stages;
+  uint32_t ring;
+  size_t smem;
+};
+template <int D, int NT, int FMT>
+AttnLaunch attn_smem(int R) {
+  using S = AttnShape<D, NT, FMT>;
+  const size_t fixed = S::kBuf + S::kQ + 12 * S::kRows + 8 * kAttnWarps * S::kRows + 16 * (size_t)(R + 2);
+  const size_t budget = (size_t)device_max_smem_optin() - 1024 - fixed;
+  const size_t per = (size_t)kAttnWarps * (S::kStage + 24);
+  AttnLaunch l;
+  l.stages = (int)std::min<size_t>(8, budget / per);
+  l.ring = (uint32_t)((size_t)l.stages * kAttnWarps * S::kStage);
+  l.smem = fixed + per * l.stages;
+  return l;
+}
+
+template <int D, int NT, int FMT>
+cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
+  using S = AttnShape<D, NT, FMT>;
+  CUtensorMap km, vm;
+  const auto sw = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  for (int i = 0; i < 2; ++i)
+    if (!tmap_3d(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? a.v_cache : a.k_cache, D, a.bs,
+                 (uint64_t)a.num_blocks * a.Hkv, D, (uint64_t)a.bs * D, S::kRowBytes, kUnit, 1, sw))
+      return cudaErrorInvalidValue;
+  auto k = attn_kv8_kernel<D, NT, FMT>;
+  cudaError_t e = allow_max_smem(k);
+  if (e != cudaSuccess) return e;
+  const AttnLaunch l = attn_smem<D, NT, FMT>(a.R);
+  return launch_kernel(k, dim3(device_sm_count()), dim3(32 * kAttnWarps), l.smem, stream, pdl, km, vm, a, l.stages,
+                       l.ring);
+}
+
+// 8-row tiles per item: the least that hold an average request's query rows (more than 32 rows take several
+// items; D = 256 keeps 16 rows' outputs in registers at most)
+template <int FMT>
+cudaError_t launch_by_shape(const AttnArgs& a, cudaStream_t stream, bool pdl) {
+  const int rows = (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv);
+  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  switch (a.D) {
+    case 64:
+      return nt == 1   ? launch_mma<64, 1, FMT>(a, stream, pdl)
+             : nt == 2 ? launch_mma<64, 2, FMT>(a, stream, pdl)
+                       : launch_mma<64, 4, FMT>(a, stream, pdl);
+    case 128:
+      return nt == 1   ? launch_mma<128, 1, FMT>(a, stream, pdl)
+             : nt == 2 ? launch_mma<128, 2, FMT>(a, stream, pdl)
+                       : launch_mma<128, 4, FMT>(a, stream, pdl);
+    default: return nt == 1 ? launch_mma<256, 1, FMT>(a, stream, pdl) : launch_mma<256, 2, FMT>(a, stream, pdl);
+  }
+}
+
+bool attn_mma_dim(int D) { return D == 64 || D == 128 || D == 256; }
+
 }  // namespace
 
-size_t attn_kv8_workspace_size(int, int, int) { return 0; }
+size_t attn_kv8_workspace_size(int, int, int D) {
+  if (!attn_mma_dim(D)) return 0;
+  return kAttnCounterBytes + 2 * (size_t)device_sm_count() * attn_piece_bytes(D == 256 ? 16 : 32, D);
+}
 
 cudaError_t launch_attn_kv8(const AttnArgs& a, int format, cudaStream_t stream, bool pdl) {
+  if (attn_mma_dim(a.D))
+    return format == QG_KV_I8 ? launch_by_shape<QG_KV_I8>(a, stream, pdl)
+                              : launch_by_shape<QG_KV_E4M3>(a, stream, pdl);
   auto k = format == QG_KV_I8 ? attn_kv8_plain_kernel<QG_KV_I8> : attn_kv8_plain_kernel<QG_KV_E4M3>;
   return launch_kernel(k, dim3(a.T, a.Hq), dim3(32 * kPlainWarps), 0, stream, pdl, a);
 }

@@ -205,7 +205,7 @@ bool tmap_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t 
              uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
 bool tmap_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t rows,
              uint64_t chunks, uint64_t row_bytes, uint64_t chunk_bytes, uint32_t box_inner, uint32_t box_rows,
-             uint32_t box_chunks);
+             uint32_t box_chunks, CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // affine codes at 2, 3, 4, 5, 6 or 8 bits, groups 32/64/128 (affine_gemv.cu):
 // 1 <= M <= 4 on 32-code chunks (affine_fast_ok says which shapes), and the
