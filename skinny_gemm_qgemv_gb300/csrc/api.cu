@@ -460,6 +460,10 @@ qg_status qg_selftest_wait_timeout(int kind, uint32_t limit, void* stream) {
 
 const char* qg_last_cuda_error_string(void) { return cudaGetErrorString(t_last_cuda); }
 
+// The decode step's operators always launch with programmatic dependent launch:
+// their kernels touch nothing in memory before the dependency wait, so only the
+// launch itself overlaps the previous kernel (qg_set_pdl has no say in it).
+
 // The paged 8-bit cache: sizes shared by its entry points
 static qg_status check_kv8(int Hkv, int D, int block_size, int num_blocks, int format) {
   if (Hkv < 1 || Hkv > 1024 || D < 16 || D > 256 || D % 16 != 0) return QG_ERR_INVALID_ARG;
@@ -493,7 +497,7 @@ qg_status kv8_block_plan(const int32_t* old_lens, const int32_t* new_lens, int R
   const qg::PlanArgs a = {old_lens,   new_lens, R,        block_size, block_table, max_blocks, free_list, num_blocks,
                           free_count, free_count_out, cu_new, slot_map, positions, max_tokens, info,
                           static_cast<unsigned*>(workspace)};
-  return from_cuda(qg::launch_kv8_plan(a, static_cast<cudaStream_t>(stream), g_pdl));
+  return from_cuda(qg::launch_kv8_plan(a, static_cast<cudaStream_t>(stream), true));
 }
 
 qg_status kv8_append(const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride,
@@ -512,7 +516,7 @@ qg_status kv8_append(const void* k, const void* v, int dtype, int64_t k_stride, 
   if (!err) return QG_ERR_CUDA;
   const qg::AppendArgs a = {k, v, dtype == QG_DT_F32, k_stride, v_stride, slot_map, T, Hkv, D, block_size,
                             num_blocks, k_cache, v_cache, scales, err, 1};
-  return from_cuda(qg::launch_kv8_append(a, format, static_cast<cudaStream_t>(stream), g_pdl));
+  return from_cuda(qg::launch_kv8_append(a, format, static_cast<cudaStream_t>(stream), true));
 }
 
 qg_status kv8_read(const int32_t* block_ids, int B, int Hkv, int D, int block_size, int num_blocks, int format,
@@ -528,7 +532,7 @@ qg_status kv8_read(const int32_t* block_ids, int B, int Hkv, int D, int block_si
   if (!err) return QG_ERR_CUDA;
   const qg::ReadArgs a = {block_ids, B, Hkv, D, block_size, num_blocks, k_cache, v_cache, scales, k, v, scales_out,
                           err};
-  return from_cuda(qg::launch_kv8_read(a, format, static_cast<cudaStream_t>(stream), g_pdl));
+  return from_cuda(qg::launch_kv8_read(a, format, static_cast<cudaStream_t>(stream), true));
 }
 
 size_t qg_attn_kv8_workspace_size(int Hq, int Hkv, int D) {
@@ -561,7 +565,8 @@ qg_status attn_kv8_paged(const uint16_t* q_bf16, int64_t q_stride, const void* k
   const qg::AttnArgs a = {q_bf16, q_stride, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tree_mask, R, T,
                           Hq, Hkv, D, block_size, num_blocks, max_blocks, softmax_scale * 1.4426950408889634f,
                           out_bf16, workspace, err};
-  return from_cuda(qg::launch_attn_kv8(a, format, static_cast<cudaStream_t>(stream), g_pdl));
+  if (!qg::attn_kv8_ok(a)) return QG_ERR_UNSUPPORTED;
+  return from_cuda(qg::launch_attn_kv8(a, format, static_cast<cudaStream_t>(stream), true));
 }
 
 static qg_status check_norm(const qg::NormArgs& a, int x_dtype, int res_dtype, int w_dtype) {
@@ -583,7 +588,7 @@ qg_status rmsnorm_residual(const void* x, int x_dtype, const void* residual, int
                           eps, nullptr, M, K, residual_out, out_bf16, nullptr};
   qg_status st = check_norm(a, x_dtype, res_dtype, w_dtype);
   if (st != QG_OK) return st;
-  return from_cuda(qg::launch_rmsnorm(a, static_cast<cudaStream_t>(stream), g_pdl));
+  return from_cuda(qg::launch_rmsnorm(a, static_cast<cudaStream_t>(stream), true));
 }
 
 qg_status rmsnorm_residual_i8(const void* x, int x_dtype, const void* residual, int res_dtype, const void* weight,
@@ -594,7 +599,7 @@ qg_status rmsnorm_residual_i8(const void* x, int x_dtype, const void* residual, 
                           eps, sign_bits, M, K, residual_out, q, scale};
   qg_status st = check_norm(a, x_dtype, res_dtype, w_dtype);
   if (st != QG_OK) return st;
-  return from_cuda(qg::launch_rmsnorm(a, static_cast<cudaStream_t>(stream), g_pdl));
+  return from_cuda(qg::launch_rmsnorm(a, static_cast<cudaStream_t>(stream), true));
 }
 
 qg_status qg_device_error(uint32_t* code, int clear) {

@@ -121,18 +121,19 @@ __global__ void __launch_bounds__(32 * kPlainWarps) attn_kv8_plain_kernel(AttnAr
 // ---------------------------------------------------------------------------
 // The tensor-core kernel: D = 64, 128 or 256
 // ---------------------------------------------------------------------------
-constexpr int kAttnWarps = 8;
 constexpr int kUnit = 16;                       // tokens of one ring stage: one block, one scale pair
 constexpr float kNoMax = -1e30f;                // running maximum before any seen token
 constexpr float kSlack = 8.f;                   // log2: probabilities stay below 2^8 (fp16 holds 2^15)
 constexpr float kMinScale = 5.4210109e-20f;     // 2^-64
 constexpr size_t kAttnCounterBytes = 4096;      // one counter per CTA
+constexpr int kMaxCtas = 256;                   // pieces of an item whose factors fit the combine buffer
 
 // bytes of the partial results of one CTA's piece: fp32 outputs, then (max, sum) per row
 __host__ __device__ constexpr size_t attn_piece_bytes(int rows, int D) { return (size_t)rows * (D * 4 + 8); }
 
 template <int D, int NT, int FMT>
 struct AttnShape {
+  static constexpr int kWarps = (D <= 128 && NT == 1) ? 16 : 8;
   static constexpr int kRows = 8 * NT;
   static constexpr int kSubs = D > 128 ? D / 128 : 1;  // 128-byte column blocks of a token
   static constexpr int kRowBytes = D > 128 ? 128 : D;
@@ -140,9 +141,8 @@ struct AttnShape {
   static constexpr int kMt = D / 16;                   // 16-row tiles of the output's transpose
   static constexpr int kVB = D == 64 ? 8 : 16;         // bytes of a value row that a lane holds
   static constexpr int kStage = 2 * kUnit * D;         // a unit's keys, then its values
-  static constexpr int kNB = NT > 2 ? 2 : NT;          // 8-row tiles combined at a time
-  static constexpr int kPassNt = D == 256 ? 1 : kNB;
-  static constexpr int kBuf = kAttnWarps * kMt * kPassNt * 32 * 16;
+  static constexpr int kPass = kWarps == 16 ? 4 : 8;   // 16 x 8 output tiles that the warps' results are added up of at a time
+  static constexpr int kBuf = kWarps * kPass * 32 * 16;
   static constexpr int kQ = kHalves * 4 * NT * 32 * 8;
 };
 
@@ -214,7 +214,7 @@ __device__ __forceinline__ float ex2(float x) {
 // A request has one item per key/value head and tile of kRows query rows, an
 // item has ceil(units / warps) steps.
 struct AttnBatch {
-  const long long* first;  // [R + 1] steps before the request
+  const int* first;        // [R + 1] steps before the request
   const int* ctx;          // [R]
   const int* cu;           // [R + 1]
   int R, G;
@@ -223,11 +223,12 @@ struct AttnPlace {
   int r, h, rt;   // request, key/value head, row tile
   int s, steps;   // step within its item, steps of the item
 };
+template <int NW>
 __device__ __forceinline__ int attn_steps(int ctx) {
-  return max(1, (ctx + kUnit * kAttnWarps - 1) / (kUnit * kAttnWarps));
+  return max(1, (ctx + kUnit * NW - 1) / (kUnit * NW));
 }
-template <int ROWS>
-__device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, long long step) {
+template <int ROWS, int NW>
+__device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, int step) {
   int lo = 0, hi = b.R;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -238,22 +239,21 @@ __device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, long long s
   }
   AttnPlace p;
   p.r = lo;
-  p.steps = attn_steps(b.ctx[lo]);
+  p.steps = attn_steps<NW>(b.ctx[lo]);
   const int tiles = ((b.cu[lo + 1] - b.cu[lo]) * b.G + ROWS - 1) / ROWS;
-  const long long rem = step - b.first[lo];
-  const int item = (int)(rem / p.steps);
-  p.s = (int)(rem - (long long)item * p.steps);
+  const int rem = step - b.first[lo], item = rem / p.steps;
+  p.s = rem - item * p.steps;
   p.h = item / tiles;
   p.rt = item - p.h * tiles;
   return p;
 }
 
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(32 * kAttnWarps, 1)
+__global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     attn_kv8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
                     int stages, uint32_t ring_offset) {
   using S = AttnShape<D, NT, FMT>;
-  constexpr int NW = kAttnWarps, ROWS = S::kRows;
+  constexpr int NW = S::kWarps, ROWS = S::kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   // layout: ring | combine buffer | q fragments | rows | warp maxima and sums | meta | barriers | batch
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -275,16 +275,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
   p += 16 * NW * stages;
   uint64_t* bars = reinterpret_cast<uint64_t*>(p);  // [NW][stages]
   p += 8 * NW * stages;
-  long long* first = reinterpret_cast<long long*>(p);  // [R + 1]
-  int* ctxs = reinterpret_cast<int*>(first + a.R + 1);  // [R]
-  int* cus = ctxs + a.R;                               // [R + 1]
-  __shared__ long long scan_part[NW];
+  int* first = reinterpret_cast<int*>(p);  // [R + 1]
+  int* ctxs = first + a.R + 1;             // [R]
+  int* cus = ctxs + a.R;                   // [R + 1]
+  __shared__ int scan_part[NW];
   __shared__ unsigned arrived;
 
   if (lane == 0)
     for (int s = 0; s < stages; ++s) mbar_init(bars + warp * stages + s, 1);
   fence_mbar_init();
   pdl_wait();
+  pdl_launch_dependents();
 
   // ---- the batch's steps ----
   const int G = a.Hq / a.Hkv;
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
     const int per = (a.R + 32 * NW - 1) / (32 * NW);
     const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
     const int most = a.max_blocks * a.bs;
-    long long mine = 0;
+    int mine = 0;  // the host has checked that the steps of all requests stay below 2^31
     for (int r = r0; r < r1; ++r) {
       const int q0 = min(max(a.cu_q[r], 0), a.T), q1 = min(max(a.cu_q[r + 1], 0), a.T);
       int ctx = max(0, a.ctx_lens[r]);
@@ -305,17 +306,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
       cus[r] = q0;
       if (r == a.R - 1) cus[a.R] = q1;
       first[r] = mine;
-      mine += (long long)attn_steps(ctx) * a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS);
+      mine += attn_steps<NW>(ctx) * a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS);
     }
-    long long inc = mine;
+    int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
     if (lane == 31) scan_part[warp] = inc;
     __syncthreads();
-    long long before = inc - mine, total = 0;
+    int before = inc - mine, total = 0;
     for (int w = 0; w < NW; ++w) {
       if (w < warp) before += scan_part[w];
       total += scan_part[w];
@@ -324,11 +325,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
     if (threadIdx.x == 0) first[a.R] = total;
     __syncthreads();
   }
-  const long long W = first[a.R];
-  const long long A = min((long long)gridDim.x, W);  // CTAs with work
-  if (blockIdx.x >= A) return;
-  const long long c0 = blockIdx.x * W / A, c1 = (blockIdx.x + 1) * W / A;
-  const int n = (int)(c1 - c0);
+  const int W = first[a.R];
+  const int A = min((int)gridDim.x, W);  // CTAs with work: the first W % A take a step more than the others
+  if ((int)blockIdx.x >= A) return;
+  const int share = W / A, more = W % A;
+  const int c0 = blockIdx.x * share + min((int)blockIdx.x, more);
+  const int n = share + ((int)blockIdx.x < more ? 1 : 0), c1 = c0 + n;
+  auto cta_of = [&](int step) {
+    const int big = more * (share + 1);
+    return step < big ? step / (share + 1) : more + (step - big) / share;
+  };
 
   // ---- producer side of the warp's ring: lane l looks after step 32 b + l of batch b ----
   uint64_t* bar = bars + warp * stages;
@@ -340,9 +346,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
   float2 n_scale = make_float2(0.f, 0.f);
   auto look_table = [&](int b) {
     n_blk = -1;
-    const long long step = c0 + 32LL * b + lane;
+    const int step = c0 + 32 * b + lane;
     if (step < c1) {
-      const AttnPlace at = attn_locate<ROWS>(batch, step);
+      const AttnPlace at = attn_locate<ROWS, NW>(batch, step);
       const int tok = (at.s * NW + warp) * kUnit;
       if (tok < ctxs[at.r]) {
         n_blk = __ldg(a.table + (size_t)at.r * a.max_blocks + tok / a.bs);
@@ -372,10 +378,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
     if (l == 16) look_scale();
     if (lane == l) {
       const bool ok = page >= 0;
-      // a value scale below 2^-64 counts as 2^-64: what it adds to an output is below 2^-55; of a block of
-      // zero scale only the probabilities count
-      const float v = vs < kMinScale ? kMinScale : vs;
-      my_meta[slot] = make_float4(ks, log2f(v), 1.f / v, !ok ? 0.f : vs == 0.f ? 2.f : 1.f);
       if (ok) {
         mbar_arrive_expect_tx(bar + slot, S::kStage);
         const uint32_t dst = smem_u32(my_ring + (size_t)slot * S::kStage);
@@ -387,6 +389,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
       } else {
         mbar_arrive(bar + slot);
       }
+      // a value scale below 2^-64 counts as 2^-64: what it adds to an output is below 2^-55; of a block of
+      // zero scale only the probabilities count. (The warp reads this after a barrier of its own.)
+      const float v = vs < kMinScale ? kMinScale : vs;
+      my_meta[slot] = make_float4(ks, __log2f(v), 1.f / v, !ok ? 0.f : vs == 0.f ? 2.f : 1.f);
     }
   };
   look_table(0);
@@ -403,13 +409,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
   constexpr bool kQRegs = NT * S::kHalves <= 4;
   uint2 qr[kQRegs ? S::kHalves * 4 : 1][kQRegs ? NT : 1];
   AttnPlace item = {};
-  long long seg_end = c0;
+  int seg_end = c0, item_first = c0;
   int ctx = 0, nq = 0, q0 = 0, base = 0;
   bool ok = true;
 
-  auto begin_segment = [&](long long step) {
-    item = attn_locate<ROWS>(batch, step);
-    seg_end = min(c1, step - item.s + item.steps);
+  auto begin_segment = [&](int step) {
+    item = attn_locate<ROWS, NW>(batch, step);
+    item_first = step - item.s;
+    seg_end = min(c1, item_first + item.steps);
     ctx = ctxs[item.r];
     q0 = cus[item.r];
     nq = cus[item.r + 1] - q0;
@@ -477,11 +484,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
 
   // one unit of 16 tokens whose first is `tok`, landed at `stage`
   auto compute = [&](uint32_t stage, const float4 mt_, int tok) {
-    float s[NT][4];
+    // two chains of products where there are few, so that they do not wait for each other
+    constexpr int CH = NT <= 2 ? 2 : 1;
+    float sc[CH][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int k = 0; k < CH; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[k][nt][j] = 0.f;
     // S^T = K q^T: lane (g, c) holds tokens g, g + 8 and 16-byte chunk c of each 64 bytes
     const int t0 = unit_token<D>(g), t1 = t0 + 8;
 #pragma unroll
@@ -498,10 +509,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint2 b = kQRegs ? qr[hf * 4 + w][nt] : qfrag[((hf * 4 + w) * NT + nt) * 32 + lane];
-          mma16816(s[nt], f, b.x, b.y);
+          mma16816(sc[w % CH][nt], f, b.x, b.y);
         }
       }
     }
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[nt][j] = CH == 2 ? sc[0][nt][j] + sc[CH - 1][nt][j] : sc[0][nt][j];
     // t = log2 of (probability times value scale); lane: tokens t0, t1 of rows 2 c, 2 c + 1
     const bool edge = tok + kUnit > base;  // some row may not see some token
     bool grow = false;
@@ -620,38 +636,39 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
         }
       }
     }
-    const long long item_first = seg_end - 1 - ((seg_end - 1 - first[item.r]) % item.steps);
     const bool whole = item_first >= c0 && item_first + item.steps <= c1;
     const int slot = item_first < c0 ? 0 : 1;
     uint8_t* ws = static_cast<uint8_t*>(a.ws) + kAttnCounterBytes;
     uint8_t* mine = ws + (size_t)(2 * blockIdx.x + slot) * attn_piece_bytes(ROWS, D);
     float2* stat = reinterpret_cast<float2*>(mine + (size_t)ROWS * D * 4);
     __syncthreads();
+    float down[NT][2];
 #pragma unroll
-    for (int n0 = 0; n0 < NT; n0 += S::kPassNt) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int k = 0; k < S::kPassNt; ++k) {
-        const int nt = n0 + k;
-        float f[2];
+      for (int j = 0; j < 2; ++j) {
+        float mm = kNoMax;
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, wmax[w * ROWS + nt * 8 + 2 * c + j]);
+        down[nt][j] = ex2(m[nt][j] - mm);
+      }
+    }
+    // S::kPass tiles at a time (tile = nt * kMt + mt): all warps' parts into shared memory, then one warp per tile
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float mm = kNoMax;
-          for (int w = 0; w < NW; ++w) mm = fmaxf(mm, wmax[w * ROWS + nt * 8 + 2 * c + j]);
-          f[j] = ex2(m[nt][j] - mm);
-        }
+    for (int t0 = 0; t0 < NT * S::kMt; t0 += S::kPass) {
 #pragma unroll
-        for (int mt = 0; mt < S::kMt; ++mt)
-          buf[((warp * S::kPassNt + k) * S::kMt + mt) * 32 + lane] =
-              make_float4(acc[nt][mt][0] * f[0], acc[nt][mt][1] * f[1], acc[nt][mt][2] * f[0], acc[nt][mt][3] * f[1]);
+      for (int k = 0; k < S::kPass; ++k) {
+        const int nt = (t0 + k) / S::kMt, mt = (t0 + k) % S::kMt;
+        buf[(warp * S::kPass + k) * 32 + lane] = make_float4(acc[nt][mt][0] * down[nt][0], acc[nt][mt][1] * down[nt][1],
+                                                             acc[nt][mt][2] * down[nt][0], acc[nt][mt][3] * down[nt][1]);
       }
       __syncthreads();
-      for (int q = warp; q < S::kPassNt * S::kMt; q += NW) {
-        const int k = q / S::kMt, mt = q - k * S::kMt, nt = n0 + k;
+      if (warp < S::kPass) {
+        const int nt = (t0 + warp) / S::kMt, mt = (t0 + warp) % S::kMt;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float mm[2] = {kNoMax, kNoMax}, ll[2] = {0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          const float4 x = buf[((w * S::kPassNt + k) * S::kMt + mt) * 32 + lane];
+          const float4 x = buf[(w * S::kPass + warp) * 32 + lane];
           o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
 #pragma unroll
           for (int j = 0; j < 2; ++j) mm[j] = fmaxf(mm[j], wmax[w * ROWS + nt * 8 + 2 * c + j]);
@@ -674,7 +691,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
     }
     if (whole) return;
     // the CTA that brings an item's last piece adds the pieces up, in the order of the CTAs
-    const int f = (int)(((item_first + 1) * A - 1) / W), e = (int)(((item_first + item.steps) * A - 1) / W);
+    const int f = cta_of(item_first), e = cta_of(item_first + item.steps - 1);
     unsigned* count = static_cast<unsigned*>(a.ws) + f;
     __threadfence();
     __syncthreads();
@@ -687,48 +704,74 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1)
     __syncthreads();
     if (!last) return;
     __threadfence();
-    for (int q = warp; q < NT * S::kMt; q += NW) {
-      const int nt = q / S::kMt, mt = q - nt * S::kMt;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float mm[2] = {kNoMax, kNoMax}, ll[2] = {0.f, 0.f};
-      for (int i = f; i <= e; ++i) {
-        const uint8_t* piece = ws + (size_t)(2 * i + (i == f && item_first >= i * W / A ? 1 : 0)) * attn_piece_bytes(ROWS, D);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(piece) + (nt * S::kMt + mt) * 32 + lane);
-        const float4 st = __ldcg(reinterpret_cast<const float4*>(piece + (size_t)ROWS * D * 4) + (nt * 8 + 2 * c) / 2);
-        const float pm[2] = {st.x, st.z}, pl[2] = {st.y, st.w};
-        float fo[2], fn[2];
+    // factors of the pieces, a row per warp; then a tile per warp (or several warps, each a part of the pieces)
+    float* factor = reinterpret_cast<float*>(buf);  // [pieces][ROWS]
+    auto piece = [&](int i) {
+      return ws + (size_t)(2 * (f + i) + (i == 0 ? 1 : 0)) * attn_piece_bytes(ROWS, D);
+    };
+    const int pieces = e - f + 1;
+    for (int rr = warp; rr < ROWS; rr += NW) {
+      float mm = kNoMax;
+      for (int i = lane; i < pieces; i += 32)
+        mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr).x);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float mn = fmaxf(mm[j], pm[j]);
-          fo[j] = ex2(mm[j] - mn), fn[j] = ex2(pm[j] - mn);
-          mm[j] = mn;
-          ll[j] = ll[j] * fo[j] + pl[j] * fn[j];
-        }
-        o.x = o.x * fo[0] + x.x * fn[0], o.y = o.y * fo[1] + x.y * fn[1];
-        o.z = o.z * fo[0] + x.z * fn[0], o.w = o.w * fo[1] + x.w * fn[1];
+      for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+      float ll = 0.f;
+      for (int i = lane; i < pieces; i += 32) {
+        const float2 st = __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr);
+        const float x = ex2(st.x - mm);
+        factor[i * ROWS + rr] = x;
+        ll = fmaf(st.y, x, ll);
       }
-      write_out(nt, mt, o, ll[0], ll[1]);
+      ll = warp_sum(ll);
+      if (lane == 0) wsum[rr] = ll;
     }
+    __syncthreads();
+    constexpr int kTiles = NT * S::kMt, kParts = kTiles < NW ? NW / kTiles : 1;
+    for (int q = warp % kTiles; q < kTiles; q += NW) {
+      const int nt = q / S::kMt, mt = q - nt * S::kMt, part = kParts > 1 ? warp / kTiles : 0;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int i = part; i < pieces; i += kParts) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(piece(i)) + q * 32 + lane);
+        const float2 fa = *reinterpret_cast<const float2*>(factor + i * ROWS + nt * 8 + 2 * c);
+        o.x = fmaf(x.x, fa.x, o.x), o.y = fmaf(x.y, fa.y, o.y);
+        o.z = fmaf(x.z, fa.x, o.z), o.w = fmaf(x.w, fa.y, o.w);
+      }
+      if (kParts > 1) {
+        __syncthreads();
+        buf[warp * 32 + lane] = o;
+        __syncthreads();
+        if (part) break;
+        for (int k = 1; k < kParts; ++k) {
+          const float4 x = buf[(warp + k * kTiles) * 32 + lane];
+          o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+        }
+      }
+      write_out(nt, mt, o, wsum[nt * 8 + 2 * c], wsum[nt * 8 + 2 * c + 1]);
+    }
+    __syncthreads();
   };
 
-  int slot = 0;
+  int slot = 0, tok = 0;
   uint32_t phase = 0;
   for (int i = 0; i < n; ++i) {
     if (c0 + i == seg_end) {
       if (i > 0) end_segment();
       begin_segment(c0 + i);
+      tok = (item.s * NW + warp) * kUnit;
     }
     if (ok) ok = mbar_wait(bar + slot, phase, a.err, kErrAttnWait);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       const float4 mt_ = my_meta[slot];
       if (mt_.w != 0.f) {
-        const int s = (int)(c0 + i - (seg_end - 1 - ((seg_end - 1 - first[item.r]) % item.steps)));
-        compute(smem_u32(my_ring + (size_t)slot * S::kStage), mt_, (s * NW + warp) * kUnit);
+        compute(smem_u32(my_ring + (size_t)slot * S::kStage), mt_, tok);
       }
       __syncwarp();
       if (i + stages < n) issue(i + stages, slot);
     }
+    tok += NW * kUnit;
     if (++slot == stages) slot = 0, phase ^= 1u;
   }
   end_segment();
@@ -744,14 +787,20 @@ struct AttnLaunch {
 template <int D, int NT, int FMT>
 AttnLaunch attn_smem(int R) {
   using S = AttnShape<D, NT, FMT>;
-  const size_t fixed = S::kBuf + S::kQ + 12 * S::kRows + 8 * kAttnWarps * S::kRows + 16 * (size_t)(R + 2);
+  const size_t fixed = S::kBuf + S::kQ + 12 * S::kRows + 8 * S::kWarps * S::kRows + 12 * (size_t)(R + 2);
   const size_t budget = (size_t)device_max_smem_optin() - 1024 - fixed;
-  const size_t per = (size_t)kAttnWarps * (S::kStage + 24);
+  const size_t per = (size_t)S::kWarps * (S::kStage + 24);
   AttnLaunch l;
   l.stages = (int)std::min<size_t>(8, budget / per);
-  l.ring = (uint32_t)((size_t)l.stages * kAttnWarps * S::kStage);
+  l.ring = (uint32_t)((size_t)l.stages * S::kWarps * S::kStage);
   l.smem = fixed + per * l.stages;
   return l;
+}
+
+// steps of all items, at most (8 rows, 128 tokens); the kernel counts them in 32 bits
+long long attn_most_steps(const AttnArgs& a) {
+  const long long tiles = ((long long)a.T * (a.Hq / a.Hkv)) / 8 + 2LL * a.R;
+  return tiles * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128 + 1);
 }
 
 template <int D, int NT, int FMT>
@@ -767,7 +816,7 @@ cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   cudaError_t e = allow_max_smem(k);
   if (e != cudaSuccess) return e;
   const AttnLaunch l = attn_smem<D, NT, FMT>(a.R);
-  return launch_kernel(k, dim3(device_sm_count()), dim3(32 * kAttnWarps), l.smem, stream, pdl, km, vm, a, l.stages,
+  return launch_kernel(k, dim3(std::min(device_sm_count(), kMaxCtas)), dim3(32 * S::kWarps), l.smem, stream, pdl, km, vm, a, l.stages,
                        l.ring);
 }
 
@@ -796,8 +845,10 @@ bool attn_mma_dim(int D) { return D == 64 || D == 128 || D == 256; }
 
 size_t attn_kv8_workspace_size(int, int, int D) {
   if (!attn_mma_dim(D)) return 0;
-  return kAttnCounterBytes + 2 * (size_t)device_sm_count() * attn_piece_bytes(D == 256 ? 16 : 32, D);
+  return kAttnCounterBytes + 2 * (size_t)std::min(device_sm_count(), kMaxCtas) * attn_piece_bytes(D == 256 ? 16 : 32, D);
 }
+
+bool attn_kv8_ok(const AttnArgs& a) { return !attn_mma_dim(a.D) || attn_most_steps(a) < (1LL << 31); }
 
 cudaError_t launch_attn_kv8(const AttnArgs& a, int format, cudaStream_t stream, bool pdl) {
   if (attn_mma_dim(a.D))

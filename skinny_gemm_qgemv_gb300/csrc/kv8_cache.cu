@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
   int* tok_ex = sm + 2 * a.R + 2; // [R + 1]
   __shared__ PlanSums part[kPlanThreads / 32];
   pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
   const int per = (a.R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
   __shared__ int run_len;
   __shared__ float part[kAppendThreads / 32];
   pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
   const int which = blockIdx.y & 1, head = blockIdx.y >> 1;
   const void* x = which ? a.v : a.k;
@@ -298,6 +300,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
 template <int FMT>
 __global__ void __launch_bounds__(256) kv8_read_kernel(ReadArgs a) {
   pdl_wait();
+  pdl_launch_dependents();
   const int which = blockIdx.z, head = blockIdx.y;
   const int per = a.bs * a.D / 8;
   const int id = __ldg(a.ids + blockIdx.x);

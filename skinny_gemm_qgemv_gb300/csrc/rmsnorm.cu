@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const void* __restrict__ 
                                                        void* __restrict__ out, float* __restrict__ scale) {
   __shared__ float part[2][32];
   pdl_wait();
+  pdl_launch_dependents();
   const int n8 = K / 8;
   const size_t row = (size_t)blockIdx.x * n8;
   float h[C][8];
