@@ -143,7 +143,9 @@ struct AttnShape {
   static constexpr int kStage = 2 * kUnit * D;         // a unit's keys, then its values
   static constexpr int kPass = kWarps == 16 ? 4 : 8;   // 16 x 8 output tiles that the warps' results are added up of at a time
   static constexpr int kBuf = kWarps * kPass * 32 * 16;
-  static constexpr int kQ = kHalves * 4 * NT * 32 * 8;
+  static constexpr bool kQRegs = NT * kHalves <= 4;    // the query fragments stay in registers
+  static constexpr int kQ = kQRegs ? 0 : kHalves * 4 * NT * 32 * 8;
+  static constexpr int kRaw = 2 * kRows * D * 2;
 };
 
 // Token of MMA row i of a unit. Rows of the swizzled stage that one shared-memory
@@ -212,41 +214,69 @@ __device__ __forceinline__ float ex2(float x) {
 
 // The CTA's view of the batch: requests, their steps and where a step lies.
 // A request has one item per key/value head and tile of kRows query rows, an
-// item has ceil(units / warps) steps.
+// item has ceil(units / warps) steps. Shares are cut on a scale on which an
+// item also costs kItemCost steps before its first one: what beginning and
+// ending it takes (a batch of 32 requests of 1..8192 tokens, where one CTA can
+// meet 20 short items: 82 -> XX us).
 struct AttnBatch {
-  const int* first;        // [R + 1] steps before the request
-  const int* ctx;          // [R]
-  const int* cu;           // [R + 1]
+  const int* first;  // [R + 1] steps before the request
+  const int* cost;   // [R + 1] the same with every item's kItemCost
+  const int* ctx;    // [R]
+  const int* cu;     // [R + 1]
   int R, G;
 };
 struct AttnPlace {
   int r, h, rt;   // request, key/value head, row tile
   int s, steps;   // step within its item, steps of the item
 };
+constexpr int kItemCost = 2;
 template <int NW>
 __device__ __forceinline__ int attn_steps(int ctx) {
   return max(1, (ctx + kUnit * NW - 1) / (kUnit * NW));
 }
-template <int ROWS, int NW>
-__device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, int step) {
-  int lo = 0, hi = b.R;
+// largest r in [0, n) with v[r] <= x
+__device__ __forceinline__ int attn_find(const int* v, int n, int x) {
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (b.first[mid] <= step)
+    if (v[mid] <= x)
       lo = mid;
     else
       hi = mid;
   }
+  return lo;
+}
+template <int ROWS, int NW>
+__device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, int step) {
   AttnPlace p;
-  p.r = lo;
-  p.steps = attn_steps<NW>(b.ctx[lo]);
-  const int tiles = ((b.cu[lo + 1] - b.cu[lo]) * b.G + ROWS - 1) / ROWS;
-  const int rem = step - b.first[lo], item = rem / p.steps;
+  p.r = attn_find(b.first, b.R, step);
+  p.steps = attn_steps<NW>(b.ctx[p.r]);
+  const int tiles = ((b.cu[p.r + 1] - b.cu[p.r]) * b.G + ROWS - 1) / ROWS;
+  const int rem = step - b.first[p.r], item = rem / p.steps;
   p.s = rem - item * p.steps;
   p.h = item / tiles;
   p.rt = item - p.h * tiles;
   return p;
 }
+// first step at or after place x of the cost scale, and the place of a step
+template <int NW>
+__device__ __forceinline__ int attn_step_at(const AttnBatch& b, int x) {
+  if (x >= b.cost[b.R]) return b.first[b.R];
+  const int r = attn_find(b.cost, b.R, x), steps = attn_steps<NW>(b.ctx[r]);
+  const int rem = x - b.cost[r], item = rem / (steps + kItemCost);
+  return b.first[r] + item * steps + max(0, rem - item * (steps + kItemCost) - kItemCost);
+}
+template <int NW>
+__device__ __forceinline__ int attn_cost_of(const AttnBatch& b, int step) {
+  const int r = attn_find(b.first, b.R, step), steps = attn_steps<NW>(b.ctx[r]);
+  const int rem = step - b.first[r], item = rem / steps;
+  return b.cost[r] + rem + (item + 1) * kItemCost;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <int D, int NT, int FMT>
 __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
@@ -263,10 +293,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   p += S::kBuf;
   uint2* qfrag = reinterpret_cast<uint2*>(p);  // [half * 4 + word][nt][lane]
   p += S::kQ;
-  float* row_factor = reinterpret_cast<float*>(p);             // [ROWS]
-  int* row_limit = reinterpret_cast<int*>(p + 4 * ROWS);       // [ROWS] tokens below it are seen
-  uint32_t* row_bits = reinterpret_cast<uint32_t*>(p + 8 * ROWS);  // [ROWS] draft tokens seen beyond it
-  p += 12 * ROWS;
+  uint8_t* qraw = p;  // [2][ROWS][D] bf16: this segment's queries and the next one's
+  p += S::kRaw;
+  int2* row_seen = reinterpret_cast<int2*>(p) + warp * ROWS;  // tokens below .x are seen, and draft tokens by .y's bits
+  p += 8 * NW * ROWS;
   float* wmax = reinterpret_cast<float*>(p);  // [NW][ROWS]
   p += 4 * NW * ROWS;
   float* wsum = reinterpret_cast<float*>(p);  // [NW][ROWS]
@@ -276,10 +306,12 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(p);  // [NW][stages]
   p += 8 * NW * stages;
   int* first = reinterpret_cast<int*>(p);  // [R + 1]
-  int* ctxs = first + a.R + 1;             // [R]
-  int* cus = ctxs + a.R;                   // [R + 1]
-  __shared__ int scan_part[NW];
+  int* cost = first + a.R + 1;             // [R + 1]
+  int* cus = cost + a.R + 1;               // [R + 1]
+  int* ctxs = cus + a.R + 1;               // [R]
+  __shared__ int2 scan_part[NW];
   __shared__ unsigned arrived;
+  __shared__ float row_factor[ROWS];
 
   if (lane == 0)
     for (int s = 0; s < stages; ++s) mbar_init(bars + warp * stages + s, 1);
@@ -289,12 +321,12 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
 
   // ---- the batch's steps ----
   const int G = a.Hq / a.Hkv;
-  const AttnBatch batch = {first, ctxs, cus, a.R, G};
+  const AttnBatch batch = {first, cost, ctxs, cus, a.R, G};
   {
     const int per = (a.R + 32 * NW - 1) / (32 * NW);
     const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
     const int most = a.max_blocks * a.bs;
-    int mine = 0;  // the host has checked that the steps of all requests stay below 2^31
+    int2 mine = make_int2(0, 0);  // the host has checked that both stay below 2^31
     for (int r = r0; r < r1; ++r) {
       const int q0 = min(max(a.cu_q[r], 0), a.T), q1 = min(max(a.cu_q[r + 1], 0), a.T);
       int ctx = max(0, a.ctx_lens[r]);
@@ -305,43 +337,62 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       ctxs[r] = ctx;
       cus[r] = q0;
       if (r == a.R - 1) cus[a.R] = q1;
-      first[r] = mine;
-      mine += attn_steps<NW>(ctx) * a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS);
+      first[r] = mine.x;
+      cost[r] = mine.y;
+      const int items = a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS), steps = attn_steps<NW>(ctx);
+      mine.x += items * steps;
+      mine.y += items * (steps + kItemCost);
     }
-    int inc = mine;
+    int2 inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
+      if (lane >= o) inc.x += x, inc.y += y;
     }
     if (lane == 31) scan_part[warp] = inc;
     __syncthreads();
-    int before = inc - mine, total = 0;
+    int2 before = make_int2(inc.x - mine.x, inc.y - mine.y), total = make_int2(0, 0);
     for (int w = 0; w < NW; ++w) {
-      if (w < warp) before += scan_part[w];
-      total += scan_part[w];
+      const int2 x = scan_part[w];
+      if (w < warp) before.x += x.x, before.y += x.y;
+      total.x += x.x, total.y += x.y;
     }
-    for (int r = r0; r < r1; ++r) first[r] += before;
-    if (threadIdx.x == 0) first[a.R] = total;
+    for (int r = r0; r < r1; ++r) first[r] += before.x, cost[r] += before.y;
+    if (threadIdx.x == 0) first[a.R] = total.x, cost[a.R] = total.y;
     __syncthreads();
   }
-  const int W = first[a.R];
-  const int A = min((int)gridDim.x, W);  // CTAs with work: the first W % A take a step more than the others
+  const int W = cost[a.R];
+  const int A = min((int)gridDim.x, W);  // CTAs with a share: the first W % A take one place more than the others
   if ((int)blockIdx.x >= A) return;
   const int share = W / A, more = W % A;
-  const int c0 = blockIdx.x * share + min((int)blockIdx.x, more);
-  const int n = share + ((int)blockIdx.x < more ? 1 : 0), c1 = c0 + n;
+  const int x0 = blockIdx.x * share + min((int)blockIdx.x, more);
+  const int c0 = attn_step_at<NW>(batch, x0), c1 = attn_step_at<NW>(batch, x0 + share + ((int)blockIdx.x < more ? 1 : 0));
+  const int n = c1 - c0;
+  if (n == 0) return;
   auto cta_of = [&](int step) {
-    const int big = more * (share + 1);
-    return step < big ? step / (share + 1) : more + (step - big) / share;
+    const int x = attn_cost_of<NW>(batch, step), big = more * (share + 1);
+    return x < big ? x / (share + 1) : more + (x - big) / share;
   };
+
+  // the queries of the item that `at` lies in, to buffer `b` (asynchronous)
+  auto fetch_q = [&](const AttnPlace& at, int b) {
+    const int q_first = cus[at.r], rows = (cus[at.r + 1] - q_first) * G;
+    for (int i = threadIdx.x; i < ROWS * (D / 8); i += 32 * NW) {
+      const int rr = i / (D / 8), rho = at.rt * ROWS + rr;
+      const bool live = rho < rows;
+      const uint16_t* src = a.q;
+      if (live) src += (q_first + rho / G) * a.q_stride + (size_t)(at.h * G + rho % G) * D + 8 * (i % (D / 8));
+      cp_async16(smem_u32(qraw + (size_t)b * ROWS * D * 2 + 16 * i), src, live);
+    }
+  };
+  fetch_q(attn_locate<ROWS, NW>(batch, c0), 0);
 
   // ---- producer side of the warp's ring: lane l looks after step 32 b + l of batch b ----
   uint64_t* bar = bars + warp * stages;
   float4* my_meta = meta + warp * stages;
   uint8_t* my_ring = ring + (size_t)warp * stages * S::kStage;
   int page = -1, row = 0;
-  float ks = 0.f, vs = 0.f;
+  float4 scale = make_float4(0.f, 0.f, 0.f, 0.f);
   int n_blk = -1, n_head = 0, n_row = 0;  // of the following batch
   float2 n_scale = make_float2(0.f, 0.f);
   auto look_table = [&](int b) {
@@ -368,8 +419,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   auto next_batch = [&]() {
     page = n_blk >= 0 ? n_blk * a.Hkv + n_head : -1;
     row = n_row;
-    ks = n_scale.x;
-    vs = n_scale.y;
+    // a value scale below 2^-64 counts as 2^-64: what it adds to an output is below 2^-55; of a block of zero
+    // scale only the probabilities count
+    const float v = n_scale.y < kMinScale ? kMinScale : n_scale.y;
+    scale = make_float4(n_scale.x, __log2f(v), __frcp_rn(v), page < 0 ? 0.f : n_scale.y == 0.f ? 2.f : 1.f);
   };
   auto issue = [&](int i, int slot) {
     const int l = i & 31;
@@ -377,8 +430,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     if (l == 0) look_table((i >> 5) + 1);
     if (l == 16) look_scale();
     if (lane == l) {
-      const bool ok = page >= 0;
-      if (ok) {
+      if (page >= 0) {
         mbar_arrive_expect_tx(bar + slot, S::kStage);
         const uint32_t dst = smem_u32(my_ring + (size_t)slot * S::kStage);
 #pragma unroll
@@ -389,10 +441,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       } else {
         mbar_arrive(bar + slot);
       }
-      // a value scale below 2^-64 counts as 2^-64: what it adds to an output is below 2^-55; of a block of
-      // zero scale only the probabilities count. (The warp reads this after a barrier of its own.)
-      const float v = vs < kMinScale ? kMinScale : vs;
-      my_meta[slot] = make_float4(ks, __log2f(v), 1.f / v, !ok ? 0.f : vs == 0.f ? 2.f : 1.f);
+      my_meta[slot] = scale;  // the warp reads it after a barrier of its own
     }
   };
   look_table(0);
@@ -406,13 +455,14 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   // ---- consumer ----
   float acc[NT][S::kMt][4];
   float m[NT][2], l[NT][2], rf[NT][2];
-  constexpr bool kQRegs = NT * S::kHalves <= 4;
+  constexpr bool kQRegs = S::kQRegs;
   uint2 qr[kQRegs ? S::kHalves * 4 : 1][kQRegs ? NT : 1];
   AttnPlace item = {};
   int seg_end = c0, item_first = c0;
   int ctx = 0, nq = 0, q0 = 0, base = 0;
   bool ok = true;
 
+  int qb = 0;
   auto begin_segment = [&](int step) {
     item = attn_locate<ROWS, NW>(batch, step);
     item_first = step - item.s;
@@ -421,53 +471,67 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     q0 = cus[item.r];
     nq = cus[item.r + 1] - q0;
     base = ctx - nq;
-    // q as the B operand: warp w prepares 8-row tile w % NT, half w / NT, ...; 2^-sigma q in fp16, exact
     const bool tree = a.tree && nq <= 32;
-    for (int nt = warp; nt < NT; nt += NW) {
-      const int rho = item.rt * ROWS + nt * 8 + g;
-      const bool live = rho < nq * G;
-      const int t = q0 + rho / G, hq = item.h * G + rho % G;
-      const uint16_t* src = a.q + (live ? t * a.q_stride + (size_t)hq * D + 16 * c : 0);
-      uint4 raw[S::kHalves][2];
-      float amax = 0.f;
+    for (int rr = lane; rr < ROWS; rr += 32) {
+      const int rho = item.rt * ROWS + rr;
+      int2 seen = make_int2(0, 0);
+      if (rho < nq * G)
+        seen = tree ? make_int2(base, (int)(a.tree[q0 + rho / G] & (0xFFFFFFFFu >> (32 - nq))))
+                    : make_int2(base + rho / G + 1, 0);
+      row_seen[rr] = seen;
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    // q as the B operand: 2^-sigma q in fp16, exact, sigma per row
 #pragma unroll
-      for (int hf = 0; hf < S::kHalves; ++hf) {
+    for (int nt = 0; nt < NT; ++nt) {
+      if (kQRegs || nt % NW == warp) {
+        const uint8_t* src = qraw + ((size_t)qb * ROWS + nt * 8 + g) * D * 2 + 32 * c;
+        uint4 raw[S::kHalves][2];
+        float amax = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          raw[hf][k] = live ? *reinterpret_cast<const uint4*>(src + 64 * hf + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {raw[hf][k].x, raw[hf][k].y, raw[hf][k].z, raw[hf][k].w};
+        for (int hf = 0; hf < S::kHalves; ++hf) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+          for (int k = 0; k < 2; ++k) {
+            raw[hf][k] = *reinterpret_cast<const uint4*>(src + 128 * hf + 16 * k);
+            const uint32_t w[4] = {raw[hf][k].x, raw[hf][k].y, raw[hf][k].z, raw[hf][k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+          }
         }
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int sigma = fp16_prescale_exp(amax);
-      const float down = pow2f(-sigma);
-#pragma unroll
-      for (int hf = 0; hf < S::kHalves; ++hf) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint4 u = raw[hf][w >> 1];
-          const uint32_t x = w & 1 ? u.z : u.x, y = w & 1 ? u.w : u.y;
-          qfrag[((hf * 4 + w) * NT + nt) * 32 + lane] =
-              make_uint2(f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down),
-                         f16x2(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xFFFF0000u) * down));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int sigma = fp16_prescale_exp(amax);
+        const float down = pow2f(-sigma), up = a.scale_log2 * pow2f(sigma);
+        if (kQRegs) {
+          rf[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
+          rf[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+        } else if (c == 0) {
+          row_factor[nt * 8 + g] = up;
         }
-      }
-      if (c == 0) {
-        row_factor[nt * 8 + g] = a.scale_log2 * pow2f(sigma);
-        row_limit[nt * 8 + g] = !live ? 0 : tree ? base : base + rho / G + 1;
-        row_bits[nt * 8 + g] = live && tree ? a.tree[t] & (0xFFFFFFFFu >> (32 - nq)) : 0u;
+#pragma unroll
+        for (int hf = 0; hf < S::kHalves; ++hf) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint4 u = raw[hf][w >> 1];
+            const uint32_t x = w & 1 ? u.z : u.x, y = w & 1 ? u.w : u.y;
+            const uint2 f = make_uint2(f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down),
+                                       f16x2(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xFFFF0000u) * down));
+            if (kQRegs)
+              qr[hf * 4 + w][nt] = f;
+            else
+              qfrag[((hf * 4 + w) * NT + nt) * 32 + lane] = f;
+          }
+        }
       }
     }
-    __syncthreads();
+    if (!kQRegs) __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        rf[nt][j] = row_factor[nt * 8 + 2 * c + j];
+        if (!kQRegs) rf[nt][j] = row_factor[nt * 8 + 2 * c + j];
         m[nt][j] = kNoMax;
         l[nt][j] = 0.f;
       }
@@ -475,11 +539,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       for (int mt = 0; mt < S::kMt; ++mt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[nt][mt][j] = 0.f;
-      if (kQRegs) {
-#pragma unroll
-        for (int k = 0; k < S::kHalves * 4; ++k) qr[k][nt] = qfrag[(k * NT + nt) * 32 + lane];
-      }
     }
+    // the other buffer was last read before the barrier above
+    qb ^= 1;
+    if (seg_end < c1) fetch_q(attn_locate<ROWS, NW>(batch, seg_end), qb);
   };
 
   // one unit of 16 tokens whose first is `tok`, landed at `stage`
@@ -530,7 +593,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         for (int j = 0; j < 4; ++j) {
           const int at = tok + (j < 2 ? t0 : t1), rr = nt * 8 + 2 * c + (j & 1);
           const unsigned d = (unsigned)(at - base);
-          const bool seen = at < row_limit[rr] || (d < 32u && (row_bits[rr] >> d & 1u));
+          const int2 lim = row_seen[rr];
+          const bool seen = at < lim.x || (d < 32u && ((unsigned)lim.y >> d & 1u));
           if (!seen) s[nt][j] = -INFINITY;
         }
       }
@@ -761,8 +825,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       begin_segment(c0 + i);
       tok = (item.s * NW + warp) * kUnit;
     }
-    if (ok) ok = mbar_wait(bar + slot, phase, a.err, kErrAttnWait);
-    ok = __all_sync(0xffffffffu, ok);
+    if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar + slot, phase)))
+      ok = __all_sync(0xffffffffu, mbar_wait(bar + slot, phase, a.err, kErrAttnWait));
     if (ok) {
       const float4 mt_ = my_meta[slot];
       if (mt_.w != 0.f) {
@@ -787,8 +851,8 @@ struct AttnLaunch {
 template <int D, int NT, int FMT>
 AttnLaunch attn_smem(int R) {
   using S = AttnShape<D, NT, FMT>;
-  const size_t fixed = S::kBuf + S::kQ + 12 * S::kRows + 8 * S::kWarps * S::kRows + 12 * (size_t)(R + 2);
-  const size_t budget = (size_t)device_max_smem_optin() - 1024 - fixed;
+  const size_t fixed = S::kBuf + S::kQ + S::kRaw + 16 * S::kWarps * S::kRows + 16 * (size_t)(R + 1);
+  const size_t budget = (size_t)device_max_smem_optin() - 2048 - fixed;
   const size_t per = (size_t)S::kWarps * (S::kStage + 24);
   AttnLaunch l;
   l.stages = (int)std::min<size_t>(8, budget / per);
@@ -800,7 +864,7 @@ AttnLaunch attn_smem(int R) {
 // steps of all items, at most (8 rows, 128 tokens); the kernel counts them in 32 bits
 long long attn_most_steps(const AttnArgs& a) {
   const long long tiles = ((long long)a.T * (a.Hq / a.Hkv)) / 8 + 2LL * a.R;
-  return tiles * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128 + 1);
+  return tiles * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128 + 1 + kItemCost);
 }
 
 template <int D, int NT, int FMT>
