@@ -141,7 +141,7 @@ struct AttnShape {
   static constexpr int kMt = D / 16;                   // 16-row tiles of the output's transpose
   static constexpr int kVB = D == 64 ? 8 : 16;         // bytes of a value row that a lane holds
   static constexpr int kStage = 2 * kUnit * D;         // a unit's keys, then its values
-  static constexpr int kPass = kWarps == 16 ? 4 : 8;   // 16 x 8 output tiles that the warps' results are added up of at a time
+  static constexpr int kPass = 8 < NT * kMt ? 8 : NT * kMt;   // 16 x 8 output tiles that the warps' results are added up of at a time
   static constexpr int kBuf = kWarps * kPass * 32 * 16;
   static constexpr bool kQRegs = NT * kHalves <= 4;    // the query fragments stay in registers
   static constexpr int kQ = kQRegs ? 0 : kHalves * 4 * NT * 32 * 8;
@@ -230,6 +230,7 @@ struct AttnPlace {
   int s, steps;   // step within its item, steps of the item
 };
 constexpr int kItemCost = 2;
+constexpr int kWholeSteps = 6;  // items up to this long are not cut: joining the pieces takes longer (4 us)
 template <int NW>
 __device__ __forceinline__ int attn_steps(int ctx) {
   return max(1, (ctx + kUnit * NW - 1) / (kUnit * NW));
@@ -237,6 +238,7 @@ __device__ __forceinline__ int attn_steps(int ctx) {
 // largest r in [0, n) with v[r] <= x
 __device__ __forceinline__ int attn_find(const int* v, int n, int x) {
   int lo = 0, hi = n;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (v[mid] <= x)
@@ -263,8 +265,9 @@ template <int NW>
 __device__ __forceinline__ int attn_step_at(const AttnBatch& b, int x) {
   if (x >= b.cost[b.R]) return b.first[b.R];
   const int r = attn_find(b.cost, b.R, x), steps = attn_steps<NW>(b.ctx[r]);
-  const int rem = x - b.cost[r], item = rem / (steps + kItemCost);
-  return b.first[r] + item * steps + max(0, rem - item * (steps + kItemCost) - kItemCost);
+  const int rem = x - b.cost[r], item = rem / (steps + kItemCost), at = rem - item * (steps + kItemCost);
+  // a short item belongs to the CTA whose share holds its beginning
+  return b.first[r] + item * steps + (steps <= kWholeSteps ? (at ? steps : 0) : max(0, at - kItemCost));
 }
 template <int NW>
 __device__ __forceinline__ int attn_cost_of(const AttnBatch& b, int step) {
@@ -295,12 +298,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   p += S::kQ;
   uint8_t* qraw = p;  // [2][ROWS][D] bf16: this segment's queries and the next one's
   p += S::kRaw;
-  int2* row_seen = reinterpret_cast<int2*>(p) + warp * ROWS;  // tokens below .x are seen, and draft tokens by .y's bits
+  // rows of the item, a copy per warp: tokens below .x are seen, and draft tokens by .y's bits; .z: output row or -1
+  int4* row_info = reinterpret_cast<int4*>(p) + warp * ROWS;
+  p += 16 * NW * ROWS;
+  float2* wstat = reinterpret_cast<float2*>(p);  // [NW][ROWS] maxima and sums
   p += 8 * NW * ROWS;
-  float* wmax = reinterpret_cast<float*>(p);  // [NW][ROWS]
-  p += 4 * NW * ROWS;
-  float* wsum = reinterpret_cast<float*>(p);  // [NW][ROWS]
-  p += 4 * NW * ROWS;
   float4* meta = reinterpret_cast<float4*>(p);  // [NW][stages] key scale, log2 and inverse of the value scale, kind
   p += 16 * NW * stages;
   uint64_t* bars = reinterpret_cast<uint64_t*>(p);  // [NW][stages]
@@ -314,6 +316,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   __shared__ float row_factor[ROWS];
 
   if (lane == 0)
+#pragma unroll 1
     for (int s = 0; s < stages; ++s) mbar_init(bars + warp * stages + s, 1);
   fence_mbar_init();
   pdl_wait();
@@ -327,6 +330,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
     const int most = a.max_blocks * a.bs;
     int2 mine = make_int2(0, 0);  // the host has checked that both stay below 2^31
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       const int q0 = min(max(a.cu_q[r], 0), a.T), q1 = min(max(a.cu_q[r + 1], 0), a.T);
       int ctx = max(0, a.ctx_lens[r]);
@@ -352,11 +356,13 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     if (lane == 31) scan_part[warp] = inc;
     __syncthreads();
     int2 before = make_int2(inc.x - mine.x, inc.y - mine.y), total = make_int2(0, 0);
+#pragma unroll 1
     for (int w = 0; w < NW; ++w) {
       const int2 x = scan_part[w];
       if (w < warp) before.x += x.x, before.y += x.y;
       total.x += x.x, total.y += x.y;
     }
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) first[r] += before.x, cost[r] += before.y;
     if (threadIdx.x == 0) first[a.R] = total.x, cost[a.R] = total.y;
     __syncthreads();
@@ -377,6 +383,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   // the queries of the item that `at` lies in, to buffer `b` (asynchronous)
   auto fetch_q = [&](const AttnPlace& at, int b) {
     const int q_first = cus[at.r], rows = (cus[at.r + 1] - q_first) * G;
+#pragma unroll 1
     for (int i = threadIdx.x; i < ROWS * (D / 8); i += 32 * NW) {
       const int rr = i / (D / 8), rho = at.rt * ROWS + rr;
       const bool live = rho < rows;
@@ -447,10 +454,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   look_table(0);
   look_scale();
   next_batch();
-  {
-    const int k = min(stages, n);
-    for (int i = 0; i < k; ++i) issue(i, i);
-  }
 
   // ---- consumer ----
   float acc[NT][S::kMt][4];
@@ -472,13 +475,17 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     nq = cus[item.r + 1] - q0;
     base = ctx - nq;
     const bool tree = a.tree && nq <= 32;
+#pragma unroll 1
     for (int rr = lane; rr < ROWS; rr += 32) {
       const int rho = item.rt * ROWS + rr;
-      int2 seen = make_int2(0, 0);
-      if (rho < nq * G)
-        seen = tree ? make_int2(base, (int)(a.tree[q0 + rho / G] & (0xFFFFFFFFu >> (32 - nq))))
-                    : make_int2(base + rho / G + 1, 0);
-      row_seen[rr] = seen;
+      int4 info = make_int4(0, 0, -1, 0);
+      if (rho < nq * G) {
+        const int i = rho / G;
+        info.x = tree ? base : base + i + 1;
+        if (tree) info.y = (int)(a.tree[q0 + i] & (0xFFFFFFFFu >> (32 - nq)));
+        info.z = (q0 + i) * a.Hq + item.h * G + rho - i * G;
+      }
+      row_info[rr] = info;
     }
     cp_async_wait_all();
     __syncthreads();
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         for (int j = 0; j < 4; ++j) {
           const int at = tok + (j < 2 ? t0 : t1), rr = nt * 8 + 2 * c + (j & 1);
           const unsigned d = (unsigned)(at - base);
-          const int2 lim = row_seen[rr];
+          const int2 lim = *reinterpret_cast<const int2*>(row_info + rr);
           const bool seen = at < lim.x || (d < 32u && ((unsigned)lim.y >> d & 1u));
           if (!seen) s[nt][j] = -INFINITY;
         }
@@ -670,22 +677,22 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     }
   };
 
-  // result of tile (mt, nt): lane (g, c) holds elements d, d + 1 of rows 2 c, 2 c + 1 as {d r0, d r1, d+1 r0, d+1 r1}
-  auto write_out = [&](int nt, int mt, const float4 o, float l0, float l1) {
+  // result of tile q = nt * kMt + mt: lane (g, c) holds elements d, d + 1 of rows 2 c, 2 c + 1 as
+  // {d r0, d r1, d+1 r0, d+1 r1}; l0, l1 the rows' sums, 0 where no token is seen (the result is 0 then)
+  auto write_out = [&](int q, const float4 o, float l0, float l1) {
+    const int nt = q / S::kMt, mt = q - nt * S::kMt;
     const int d = mt / (S::kVB / 2) * 128 + S::kVB * g + 2 * (mt % (S::kVB / 2));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int rho = item.rt * ROWS + nt * 8 + 2 * c + j;
-      if (rho < nq * G) {
-        const float L = j ? l1 : l0, x = j ? o.y : o.x, y = j ? o.w : o.z;
-        const size_t t = q0 + rho / G, hq = item.h * G + rho % G;
-        // no token seen: 0
-        *reinterpret_cast<uint32_t*>(a.out + (t * a.Hq + hq) * D + d) =
-            L == 0.f ? 0u : f32_to_bf16x2(x / L, y / L);
-      }
+      const int to = row_info[nt * 8 + 2 * c + j].z;
+      const float L = j ? l1 : l0, inv = L == 0.f ? 0.f : __frcp_rn(L);
+      if (to >= 0)
+        *reinterpret_cast<uint32_t*>(a.out + (size_t)to * D + d) =
+            f32_to_bf16x2((j ? o.y : o.x) * inv, (j ? o.w : o.z) * inv);
     }
   };
 
+  constexpr int kTiles = NT * S::kMt;
   auto end_segment = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -694,68 +701,70 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
         l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
         l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
-        if (g == 0) {
-          wmax[warp * ROWS + nt * 8 + 2 * c + j] = m[nt][j];
-          wsum[warp * ROWS + nt * 8 + 2 * c + j] = l[nt][j];
-        }
+        if (g == 0) wstat[warp * ROWS + nt * 8 + 2 * c + j] = make_float2(m[nt][j], l[nt][j]);
       }
     }
     const bool whole = item_first >= c0 && item_first + item.steps <= c1;
-    const int slot = item_first < c0 ? 0 : 1;
     uint8_t* ws = static_cast<uint8_t*>(a.ws) + kAttnCounterBytes;
-    uint8_t* mine = ws + (size_t)(2 * blockIdx.x + slot) * attn_piece_bytes(ROWS, D);
-    float2* stat = reinterpret_cast<float2*>(mine + (size_t)ROWS * D * 4);
+    // a CTA has a piece of at most two items: one begun before its share, one that goes on after it
+    uint8_t* mine = ws + (size_t)(2 * blockIdx.x + (item_first < c0 ? 0 : 1)) * attn_piece_bytes(ROWS, D);
+    float4* stat = reinterpret_cast<float4*>(mine + (size_t)ROWS * D * 4);
     __syncthreads();
-    float down[NT][2];
+    // to the item's maximum
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float mm[2] = {kNoMax, kNoMax};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(wstat + w * ROWS + nt * 8 + 2 * c);
+        mm[0] = fmaxf(mm[0], x.x), mm[1] = fmaxf(mm[1], x.z);
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float mm = kNoMax;
-        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, wmax[w * ROWS + nt * 8 + 2 * c + j]);
-        down[nt][j] = ex2(m[nt][j] - mm);
+        const float f = ex2(m[nt][j] - mm[j]);
+#pragma unroll
+        for (int mt = 0; mt < S::kMt; ++mt) acc[nt][mt][j] *= f, acc[nt][mt][j + 2] *= f;
       }
     }
-    // S::kPass tiles at a time (tile = nt * kMt + mt): all warps' parts into shared memory, then one warp per tile
+    // S::kPass tiles at a time: all warps' parts into shared memory, then a tile per warp is added up
+#pragma unroll 1
+    for (int t0 = 0; t0 < kTiles; t0 += S::kPass) {
 #pragma unroll
-    for (int t0 = 0; t0 < NT * S::kMt; t0 += S::kPass) {
-#pragma unroll
-      for (int k = 0; k < S::kPass; ++k) {
-        const int nt = (t0 + k) / S::kMt, mt = (t0 + k) % S::kMt;
-        buf[(warp * S::kPass + k) * 32 + lane] = make_float4(acc[nt][mt][0] * down[nt][0], acc[nt][mt][1] * down[nt][1],
-                                                             acc[nt][mt][2] * down[nt][0], acc[nt][mt][3] * down[nt][1]);
+      for (int q = 0; q < kTiles; ++q) {
+        if (q / S::kPass * S::kPass == t0)
+          buf[(warp * S::kPass + q % S::kPass) * 32 + lane] =
+              make_float4(acc[q / S::kMt][q % S::kMt][0], acc[q / S::kMt][q % S::kMt][1], acc[q / S::kMt][q % S::kMt][2],
+                          acc[q / S::kMt][q % S::kMt][3]);
       }
       __syncthreads();
       if (warp < S::kPass) {
-        const int nt = (t0 + warp) / S::kMt, mt = (t0 + warp) % S::kMt;
+        const int q = t0 + warp, nt = q / S::kMt, mt = q - nt * S::kMt;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float mm[2] = {kNoMax, kNoMax}, ll[2] = {0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
           const float4 x = buf[(w * S::kPass + warp) * 32 + lane];
           o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) mm[j] = fmaxf(mm[j], wmax[w * ROWS + nt * 8 + 2 * c + j]);
+          const float4 y = *reinterpret_cast<const float4*>(wstat + w * ROWS + nt * 8 + 2 * c);
+          mm[0] = fmaxf(mm[0], y.x), mm[1] = fmaxf(mm[1], y.z);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          for (int w = 0; w < NW; ++w)
-            ll[j] += wsum[w * ROWS + nt * 8 + 2 * c + j] * ex2(wmax[w * ROWS + nt * 8 + 2 * c + j] - mm[j]);
+        for (int w = 0; w < NW; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(wstat + w * ROWS + nt * 8 + 2 * c);
+          ll[0] = fmaf(y.y, ex2(y.x - mm[0]), ll[0]), ll[1] = fmaf(y.w, ex2(y.z - mm[1]), ll[1]);
+        }
         if (whole) {
-          write_out(nt, mt, o, ll[0], ll[1]);
+          write_out(q, o, ll[0], ll[1]);
         } else {
-          reinterpret_cast<float4*>(mine)[(nt * S::kMt + mt) * 32 + lane] = o;
-          if (mt == 0 && g == 0) {
-            stat[nt * 8 + 2 * c] = make_float2(mm[0], ll[0]);
-            stat[nt * 8 + 2 * c + 1] = make_float2(mm[1], ll[1]);
-          }
+          reinterpret_cast<float4*>(mine)[q * 32 + lane] = o;
+          if (mt == 0 && g == 0) stat[nt * 4 + c] = make_float4(mm[0], ll[0], mm[1], ll[1]);
         }
       }
-      __syncthreads();
+      if (t0 + S::kPass < kTiles) __syncthreads();
     }
     if (whole) return;
     // the CTA that brings an item's last piece adds the pieces up, in the order of the CTAs
-    const int f = cta_of(item_first), e = cta_of(item_first + item.steps - 1);
+    const int f = cta_of(item_first), e = cta_of(item_first + item.steps - 1), pieces = e - f + 1;
     unsigned* count = static_cast<unsigned*>(a.ws) + f;
     __threadfence();
     __syncthreads();
@@ -764,23 +773,22 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       if (arrived == (unsigned)(e - f)) *count = 0u;  // the next call finds it as this one did
     }
     __syncthreads();
-    const bool last = arrived == (unsigned)(e - f);
-    __syncthreads();
-    if (!last) return;
+    if (arrived != (unsigned)(e - f)) return;
     __threadfence();
     // factors of the pieces, a row per warp; then a tile per warp (or several warps, each a part of the pieces)
     float* factor = reinterpret_cast<float*>(buf);  // [pieces][ROWS]
     auto piece = [&](int i) {
       return ws + (size_t)(2 * (f + i) + (i == 0 ? 1 : 0)) * attn_piece_bytes(ROWS, D);
     };
-    const int pieces = e - f + 1;
+#pragma unroll 1
     for (int rr = warp; rr < ROWS; rr += NW) {
-      float mm = kNoMax;
+      float mm = kNoMax, ll = 0.f;
+#pragma unroll 2
       for (int i = lane; i < pieces; i += 32)
         mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr).x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-      float ll = 0.f;
+#pragma unroll 2
       for (int i = lane; i < pieces; i += 32) {
         const float2 st = __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr);
         const float x = ex2(st.x - mm);
@@ -788,17 +796,18 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         ll = fmaf(st.y, x, ll);
       }
       ll = warp_sum(ll);
-      if (lane == 0) wsum[rr] = ll;
+      if (lane == 0) wstat[rr].y = ll;
     }
     __syncthreads();
-    constexpr int kTiles = NT * S::kMt, kParts = kTiles < NW ? NW / kTiles : 1;
+    constexpr int kParts = kTiles < NW ? NW / kTiles : 1;
+#pragma unroll 1
     for (int q = warp % kTiles; q < kTiles; q += NW) {
-      const int nt = q / S::kMt, mt = q - nt * S::kMt, part = kParts > 1 ? warp / kTiles : 0;
+      const int part = kParts > 1 ? warp / kTiles : 0, rr = q / S::kMt * 8 + 2 * c;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int i = part; i < pieces; i += kParts) {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(piece(i)) + q * 32 + lane);
-        const float2 fa = *reinterpret_cast<const float2*>(factor + i * ROWS + nt * 8 + 2 * c);
+        const float2 fa = *reinterpret_cast<const float2*>(factor + i * ROWS + rr);
         o.x = fmaf(x.x, fa.x, o.x), o.y = fmaf(x.y, fa.y, o.y);
         o.z = fmaf(x.z, fa.x, o.z), o.w = fmaf(x.w, fa.y, o.w);
       }
@@ -807,39 +816,43 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         buf[warp * 32 + lane] = o;
         __syncthreads();
         if (part) break;
+#pragma unroll 1
         for (int k = 1; k < kParts; ++k) {
           const float4 x = buf[(warp + k * kTiles) * 32 + lane];
           o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
         }
       }
-      write_out(nt, mt, o, wsum[nt * 8 + 2 * c], wsum[nt * 8 + 2 * c + 1]);
+      write_out(q, o, wstat[rr].y, wstat[rr + 1].y);
     }
-    __syncthreads();
   };
 
+  // Iteration i issues step i + stages and consumes step i; the first ones only issue. (Every larger part of the
+  // loop stands in the code once: its size is what a cold start waits for.)
   int slot = 0, tok = 0;
-  uint32_t phase = 0;
-  for (int i = 0; i < n; ++i) {
-    if (c0 + i == seg_end) {
-      if (i > 0) end_segment();
-      begin_segment(c0 + i);
-      tok = (item.s * NW + warp) * kUnit;
-    }
-    if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar + slot, phase)))
-      ok = __all_sync(0xffffffffu, mbar_wait(bar + slot, phase, a.err, kErrAttnWait));
-    if (ok) {
-      const float4 mt_ = my_meta[slot];
-      if (mt_.w != 0.f) {
-        compute(smem_u32(my_ring + (size_t)slot * S::kStage), mt_, tok);
+  uint32_t phase = 1;
+#pragma unroll 1
+  for (int i = -stages;; ++i) {
+    if (i >= 0) {
+      if (i == n || c0 + i == seg_end) {
+        if (i > 0) end_segment();
+        if (i == n) break;
+        begin_segment(c0 + i);
+        tok = (item.s * NW + warp) * kUnit;
       }
-      __syncwarp();
-      if (i + stages < n) issue(i + stages, slot);
+      if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar + slot, phase)))
+        ok = __all_sync(0xffffffffu, mbar_wait(bar + slot, phase, a.err, kErrAttnWait));
+      if (ok) {
+        const float4 mt_ = my_meta[slot];
+        if (mt_.w != 0.f) compute(smem_u32(my_ring + (size_t)slot * S::kStage), mt_, tok);
+        __syncwarp();
+      }
+      tok += NW * kUnit;
     }
-    tok += NW * kUnit;
+    if (ok && i + stages < n) issue(i + stages, slot);
     if (++slot == stages) slot = 0, phase ^= 1u;
   }
-  end_segment();
   if (!ok)  // the copies still in flight land before the shared memory is given up (bounded waits)
+#pragma unroll 1
     for (int s = 0; s < stages; ++s) mbar_wait_n(bar + s, phase, nullptr, 0, 1u << 16);
 }
 
@@ -851,7 +864,7 @@ struct AttnLaunch {
 template <int D, int NT, int FMT>
 AttnLaunch attn_smem(int R) {
   using S = AttnShape<D, NT, FMT>;
-  const size_t fixed = S::kBuf + S::kQ + S::kRaw + 16 * S::kWarps * S::kRows + 16 * (size_t)(R + 1);
+  const size_t fixed = S::kBuf + S::kQ + S::kRaw + 24 * S::kWarps * S::kRows + 16 * (size_t)(R + 1);
   const size_t budget = (size_t)device_max_smem_optin() - 2048 - fixed;
   const size_t per = (size_t)S::kWarps * (S::kStage + 24);
   AttnLaunch l;
