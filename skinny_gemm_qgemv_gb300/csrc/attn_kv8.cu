@@ -133,30 +133,35 @@ __host__ __device__ constexpr size_t attn_piece_bytes(int rows, int D) { return 
 
 template <int D, int NT, int FMT>
 struct AttnShape {
-  static constexpr int kWarps = (D <= 128 && NT == 1) ? 16 : 8;
+  static constexpr int kWarps = 8;
   static constexpr int kRows = 8 * NT;
+  static constexpr int kUps = NT <= 2 && D <= 128 ? 2 : 1;  // units of a warp's step
   static constexpr int kSubs = D > 128 ? D / 128 : 1;  // 128-byte column blocks of a token
   static constexpr int kRowBytes = D > 128 ? 128 : D;
   static constexpr int kHalves = D / 64;               // 64-byte steps of q . k
   static constexpr int kMt = D / 16;                   // 16-row tiles of the output's transpose
-  static constexpr int kVB = D == 64 ? 8 : 16;         // bytes of a value row that a lane holds
-  static constexpr int kStage = 2 * kUnit * D;         // a unit's keys, then its values
-  static constexpr int kPass = 8 < NT * kMt ? 8 : NT * kMt;   // 16 x 8 output tiles that the warps' results are added up of at a time
+  static constexpr int kUnitBytes = kUnit * D;         // a unit's keys (or values)
+  static constexpr int kStage = 2 * kUps * kUnitBytes; // a step's keys, then its values
+  static constexpr int kStepTokens = kUnit * kUps * kWarps;
+  static constexpr int kPass = NT == 1 ? 4 : 8;        // output tiles that the warps' parts are added up of at a time
   static constexpr int kBuf = kWarps * kPass * 32 * 16;
   static constexpr bool kQRegs = NT * kHalves <= 4;    // the query fragments stay in registers
   static constexpr int kQ = kQRegs ? 0 : kHalves * 4 * NT * 32 * 8;
   static constexpr int kRaw = 2 * kRows * D * 2;
 };
 
-// Token of MMA row i of a unit. Rows of the swizzled stage that one shared-memory
+// Order of a unit's tokens. ldmatrix with 8-bit transposition gives lane (g, c)
+// of a 16 x 16 tile the elements d = g (and g + 8) of the tokens of its rows
+// 4 c .. 4 c + 3: the value product's A operand with MMA columns 2 c, 2 c + 1, 2 c + 8,
+// 2 c + 9 = rows 4 c .. 4 c + 3, so MMA row i of the scores' product is row
+// 4 (i % 8 / 2) + i % 2 + 2 (i / 8). Row -> token: rows that one shared-memory
 // phase touches together must differ in the address bits that the swizzle does
-// not already spread: D >= 128 (128-byte rows, chunk ^= row & 7) pairs rows
-// that differ by 4, D = 64 (64-byte rows, chunk ^= row / 2 & 3) pairs odd with even.
+// not already spread: D >= 128 (128-byte rows, chunk ^= row & 7) pairs rows that
+// differ by 4, D = 64 (64-byte rows, chunk ^= row / 2 & 3) odd with even.
 template <int D>
-__device__ __forceinline__ int unit_token(int i) {
-  const int b0 = i & 1, b1 = i >> 1 & 1, b2 = i >> 2 & 1;
-  const int t = D == 64 ? (b2 << 2 | b1 << 1 | (b0 ^ b1)) : ((b0 ^ b2) << 2 | b1 << 1 | b2);
-  return t | (i & 8);
+__device__ __forceinline__ int unit_token(int row) {
+  const int b0 = row & 1, b1 = row >> 1 & 1, b2 = row >> 2 & 1;
+  return D == 64 ? row : (row & 8) | (b0 ^ b2) << 2 | b1 << 1 | b2;
 }
 
 // byte offset of 16-byte chunk `ch` of token row `row` in a swizzled [16][kRowBytes] tile
@@ -177,12 +182,14 @@ __device__ __forceinline__ uint32_t hsub2_1152(uint32_t a) {
 }
 // codes (b0, b1) and (b2, b3) of a word as f16 pairs, exact. int8: b ^ 0x80 =
 // b + 128 under the exponent byte 0x64 is fp16 1024 + 128 + b.
-template <int FMT>
+// RAW: int8 stays 1152 + b (the caller takes 1152 times the other factors' sum off).
+template <int FMT, bool RAW = false>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (FMT == QG_KV_I8) {
     const uint32_t u = w ^ 0x80808080u;
-    lo = hsub2_1152(prmt(u, 0x64646464u, 0x4140u));
-    hi = hsub2_1152(prmt(u, 0x64646464u, 0x4342u));
+    lo = prmt(u, 0x64646464u, 0x4140u);
+    hi = prmt(u, 0x64646464u, 0x4342u);
+    if (!RAW) lo = hsub2_1152(lo), hi = hsub2_1152(hi);
   } else {
     asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
         : "=r"(lo), "=r"(hi)
@@ -201,6 +208,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
+// two 16 x 16 byte tiles, transposed: see unit_token
+__device__ __forceinline__ void ldmatrix_t8(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -214,7 +228,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 // The CTA's view of the batch: requests, their steps and where a step lies.
 // A request has one item per key/value head and tile of kRows query rows, an
-// item has ceil(units / warps) steps. Shares are cut on a scale on which an
+// item has ceil(tokens / tokens of a step) steps. Shares are cut on a scale on which an
 // item also costs kItemCost steps before its first one: what beginning and
 // ending it takes (a batch of 32 requests of 1..8192 tokens, where one CTA can
 // meet 20 short items: 82 -> XX us).
@@ -231,9 +245,9 @@ struct AttnPlace {
 };
 constexpr int kItemCost = 2;
 constexpr int kWholeSteps = 6;  // items up to this long are not cut: joining the pieces takes longer (4 us)
-template <int NW>
+template <int TOK>  // tokens of a step
 __device__ __forceinline__ int attn_steps(int ctx) {
-  return max(1, (ctx + kUnit * NW - 1) / (kUnit * NW));
+  return max(1, (ctx + TOK - 1) / TOK);
 }
 // largest r in [0, n) with v[r] <= x
 __device__ __forceinline__ int attn_find(const int* v, int n, int x) {
@@ -248,11 +262,11 @@ __device__ __forceinline__ int attn_find(const int* v, int n, int x) {
   }
   return lo;
 }
-template <int ROWS, int NW>
+template <int ROWS, int TOK>
 __device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, int step) {
   AttnPlace p;
   p.r = attn_find(b.first, b.R, step);
-  p.steps = attn_steps<NW>(b.ctx[p.r]);
+  p.steps = attn_steps<TOK>(b.ctx[p.r]);
   const int tiles = ((b.cu[p.r + 1] - b.cu[p.r]) * b.G + ROWS - 1) / ROWS;
   const int rem = step - b.first[p.r], item = rem / p.steps;
   p.s = rem - item * p.steps;
@@ -261,17 +275,17 @@ __device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, int step) {
   return p;
 }
 // first step at or after place x of the cost scale, and the place of a step
-template <int NW>
+template <int TOK>
 __device__ __forceinline__ int attn_step_at(const AttnBatch& b, int x) {
   if (x >= b.cost[b.R]) return b.first[b.R];
-  const int r = attn_find(b.cost, b.R, x), steps = attn_steps<NW>(b.ctx[r]);
+  const int r = attn_find(b.cost, b.R, x), steps = attn_steps<TOK>(b.ctx[r]);
   const int rem = x - b.cost[r], item = rem / (steps + kItemCost), at = rem - item * (steps + kItemCost);
   // a short item belongs to the CTA whose share holds its beginning
   return b.first[r] + item * steps + (steps <= kWholeSteps ? (at ? steps : 0) : max(0, at - kItemCost));
 }
-template <int NW>
+template <int TOK>
 __device__ __forceinline__ int attn_cost_of(const AttnBatch& b, int step) {
-  const int r = attn_find(b.first, b.R, step), steps = attn_steps<NW>(b.ctx[r]);
+  const int r = attn_find(b.first, b.R, step), steps = attn_steps<TOK>(b.ctx[r]);
   const int rem = step - b.first[r], item = rem / steps;
   return b.cost[r] + rem + (item + 1) * kItemCost;
 }
@@ -284,9 +298,10 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 template <int D, int NT, int FMT>
 __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     attn_kv8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
-                    int stages, uint32_t ring_offset) {
+                    int stages, uint32_t ring_offset, int wide) {
   using S = AttnShape<D, NT, FMT>;
-  constexpr int NW = S::kWarps, ROWS = S::kRows;
+  constexpr int NW = S::kWarps, ROWS = S::kRows, UPS = S::kUps, TOK = S::kStepTokens;
+  constexpr int SB = 32 / UPS;  // steps whose units the lanes look after
   extern __shared__ __align__(1024) uint8_t smem[];
   // layout: ring | combine buffer | q fragments | rows | warp maxima and sums | meta | barriers | batch
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -303,8 +318,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   p += 16 * NW * ROWS;
   float2* wstat = reinterpret_cast<float2*>(p);  // [NW][ROWS] maxima and sums
   p += 8 * NW * ROWS;
-  float4* meta = reinterpret_cast<float4*>(p);  // [NW][stages] key scale, log2 and inverse of the value scale, kind
-  p += 16 * NW * stages;
+  float4* meta = reinterpret_cast<float4*>(p);  // [NW][stages][UPS] key scale, log2 and inverse of the value scale, kind
+  p += 16 * NW * stages * UPS;
   uint64_t* bars = reinterpret_cast<uint64_t*>(p);  // [NW][stages]
   p += 8 * NW * stages;
   int* first = reinterpret_cast<int*>(p);  // [R + 1]
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   int* ctxs = cus + a.R + 1;               // [R]
   __shared__ int2 scan_part[NW];
   __shared__ unsigned arrived;
-  __shared__ float row_factor[ROWS];
+  __shared__ float2 row_factor[ROWS];
 
   if (lane == 0)
 #pragma unroll 1
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       if (r == a.R - 1) cus[a.R] = q1;
       first[r] = mine.x;
       cost[r] = mine.y;
-      const int items = a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS), steps = attn_steps<NW>(ctx);
+      const int items = a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS), steps = attn_steps<TOK>(ctx);
       mine.x += items * steps;
       mine.y += items * (steps + kItemCost);
     }
@@ -372,11 +387,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   if ((int)blockIdx.x >= A) return;
   const int share = W / A, more = W % A;
   const int x0 = blockIdx.x * share + min((int)blockIdx.x, more);
-  const int c0 = attn_step_at<NW>(batch, x0), c1 = attn_step_at<NW>(batch, x0 + share + ((int)blockIdx.x < more ? 1 : 0));
+  const int c0 = attn_step_at<TOK>(batch, x0), c1 = attn_step_at<TOK>(batch, x0 + share + ((int)blockIdx.x < more ? 1 : 0));
   const int n = c1 - c0;
   if (n == 0) return;
   auto cta_of = [&](int step) {
-    const int x = attn_cost_of<NW>(batch, step), big = more * (share + 1);
+    const int x = attn_cost_of<TOK>(batch, step), big = more * (share + 1);
     return x < big ? x / (share + 1) : more + (x - big) / share;
   };
 
@@ -392,22 +407,22 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       cp_async16(smem_u32(qraw + (size_t)b * ROWS * D * 2 + 16 * i), src, live);
     }
   };
-  fetch_q(attn_locate<ROWS, NW>(batch, c0), 0);
+  fetch_q(attn_locate<ROWS, TOK>(batch, c0), 0);
 
-  // ---- producer side of the warp's ring: lane l looks after step 32 b + l of batch b ----
+  // ---- producer side of the warp's ring: a lane looks after one unit of SB steps ----
   uint64_t* bar = bars + warp * stages;
-  float4* my_meta = meta + warp * stages;
+  float4* my_meta = meta + warp * stages * UPS;
   uint8_t* my_ring = ring + (size_t)warp * stages * S::kStage;
   int page = -1, row = 0;
   float4 scale = make_float4(0.f, 0.f, 0.f, 0.f);
-  int n_blk = -1, n_head = 0, n_row = 0;  // of the following batch
+  int n_blk = -1, n_head = 0, n_row = 0;  // of the following batch of steps
   float2 n_scale = make_float2(0.f, 0.f);
   auto look_table = [&](int b) {
     n_blk = -1;
-    const int step = c0 + 32 * b + lane;
+    const int step = c0 + SB * b + lane / UPS;
     if (step < c1) {
-      const AttnPlace at = attn_locate<ROWS, NW>(batch, step);
-      const int tok = (at.s * NW + warp) * kUnit;
+      const AttnPlace at = attn_locate<ROWS, TOK>(batch, step);
+      const int tok = ((at.s * NW + warp) * UPS + lane % UPS) * kUnit;
       if (tok < ctxs[at.r]) {
         n_blk = __ldg(a.table + (size_t)at.r * a.max_blocks + tok / a.bs);
         n_head = at.h;
@@ -432,23 +447,44 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     scale = make_float4(n_scale.x, __log2f(v), __frcp_rn(v), page < 0 ? 0.f : n_scale.y == 0.f ? 2.f : 1.f);
   };
   auto issue = [&](int i, int slot) {
-    const int l = i & 31;
-    if (l == 0 && i > 0) next_batch();
-    if (l == 0) look_table((i >> 5) + 1);
-    if (l == 16) look_scale();
-    if (lane == l) {
-      if (page >= 0) {
-        mbar_arrive_expect_tx(bar + slot, S::kStage);
-        const uint32_t dst = smem_u32(my_ring + (size_t)slot * S::kStage);
+    const int k = i & (SB - 1);
+    if (k == 0) {
+      if (i > 0) next_batch();
+      look_table(i / SB + 1);
+    }
+    if (k == SB / 2) look_scale();
+    if (lane / UPS == k) my_meta[slot * UPS + lane % UPS] = scale;  // the warp reads it after a barrier of its own
+    int pages[UPS], rows[UPS], units = 0;
 #pragma unroll
-        for (int sub = 0; sub < S::kSubs; ++sub) {
-          tma_load_3d(dst + sub * kUnit * S::kRowBytes, &kmap, sub * 128, row, page, bar + slot);
-          tma_load_3d(dst + kUnit * D + sub * kUnit * S::kRowBytes, &vmap, sub * 128, row, page, bar + slot);
-        }
+    for (int u = 0; u < UPS; ++u) {
+      pages[u] = __shfl_sync(0xffffffffu, page, k * UPS + u);
+      rows[u] = __shfl_sync(0xffffffffu, row, k * UPS + u);
+      units += pages[u] >= 0 ? 1 : 0;
+    }
+    if (lane == 0) {
+      const uint32_t dst = smem_u32(my_ring + (size_t)slot * S::kStage);
+      uint64_t* b = bar + slot;
+      if (units == 0) {
+        mbar_arrive(b);
+      } else if (UPS == 2 && wide) {
+        // both units lie in one block (or the second one past the context, in the block all the same)
+        mbar_arrive_expect_tx(b, S::kStage);
+        tma_load_3d(dst, &kmap, 0, rows[0], pages[0], b);
+        tma_load_3d(dst + UPS * S::kUnitBytes, &vmap, 0, rows[0], pages[0], b);
       } else {
-        mbar_arrive(bar + slot);
+        mbar_arrive_expect_tx(b, 2 * units * S::kUnitBytes);
+#pragma unroll
+        for (int u = 0; u < UPS; ++u) {
+          if (pages[u] >= 0) {
+#pragma unroll
+            for (int sub = 0; sub < S::kSubs; ++sub) {
+              const uint32_t at = dst + u * S::kUnitBytes + sub * kUnit * S::kRowBytes;
+              tma_load_3d(at, &kmap, sub * 128, rows[u], pages[u], b);
+              tma_load_3d(at + UPS * S::kUnitBytes, &vmap, sub * 128, rows[u], pages[u], b);
+            }
+          }
+        }
       }
-      my_meta[slot] = scale;  // the warp reads it after a barrier of its own
     }
   };
   look_table(0);
@@ -458,6 +494,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   // ---- consumer ----
   float acc[NT][S::kMt][4];
   float m[NT][2], l[NT][2], rf[NT][2];
+  float off[NT][2];  // int8: the products start at -1152 times the sum of the row's fp16 queries
   constexpr bool kQRegs = S::kQRegs;
   uint2 qr[kQRegs ? S::kHalves * 4 : 1][kQRegs ? NT : 1];
   AttnPlace item = {};
@@ -467,7 +504,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
 
   int qb = 0;
   auto begin_segment = [&](int step) {
-    item = attn_locate<ROWS, NW>(batch, step);
+    item = attn_locate<ROWS, TOK>(batch, step);
     item_first = step - item.s;
     seg_end = min(c1, item_first + item.steps);
     ctx = ctxs[item.r];
@@ -495,7 +532,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       if (kQRegs || nt % NW == warp) {
         const uint8_t* src = qraw + ((size_t)qb * ROWS + nt * 8 + g) * D * 2 + 32 * c;
         uint4 raw[S::kHalves][2];
-        float amax = 0.f;
+        float amax = 0.f, sum = 0.f;
 #pragma unroll
         for (int hf = 0; hf < S::kHalves; ++hf) {
 #pragma unroll
@@ -503,19 +540,31 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
             raw[hf][k] = *reinterpret_cast<const uint4*>(src + 128 * hf + 16 * k);
             const uint32_t w[4] = {raw[hf][k].x, raw[hf][k].y, raw[hf][k].z, raw[hf][k].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+            for (int j = 0; j < 4; ++j) {
+              const float x = __uint_as_float(w[j] << 16), y = __uint_as_float(w[j] & 0xFFFF0000u);
+              amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+              sum += x + y;
+            }
           }
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int sigma = fp16_prescale_exp(amax);
         const float down = pow2f(-sigma), up = a.scale_log2 * pow2f(sigma);
+        if (FMT == QG_KV_I8) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          sum *= -1152.f * down;
+        }
         if (kQRegs) {
           rf[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
           rf[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+          if (FMT == QG_KV_I8) {
+            off[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+            off[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+          }
         } else if (c == 0) {
-          row_factor[nt * 8 + g] = up;
+          row_factor[nt * 8 + g] = make_float2(up, sum);
         }
 #pragma unroll
         for (int hf = 0; hf < S::kHalves; ++hf) {
@@ -538,7 +587,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (!kQRegs) rf[nt][j] = row_factor[nt * 8 + 2 * c + j];
+        if (!kQRegs) {
+          const float2 x = row_factor[nt * 8 + 2 * c + j];
+          rf[nt][j] = x.x;
+          off[nt][j] = x.y;
+        }
         m[nt][j] = kNoMax;
         l[nt][j] = 0.f;
       }
@@ -549,70 +602,85 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     }
     // the other buffer was last read before the barrier above
     qb ^= 1;
-    if (seg_end < c1) fetch_q(attn_locate<ROWS, NW>(batch, seg_end), qb);
+    if (seg_end < c1) fetch_q(attn_locate<ROWS, TOK>(batch, seg_end), qb);
   };
 
-  // one unit of 16 tokens whose first is `tok`, landed at `stage`
-  auto compute = [&](uint32_t stage, const float4 mt_, int tok) {
-    // two chains of products where there are few, so that they do not wait for each other
-    constexpr int CH = NT <= 2 ? 2 : 1;
-    float sc[CH][NT][4];
+  // lane's places in a swizzled tile: keys (token t0; t0 + 2 is 2 rows on), values (ldmatrix rows)
+  const int t0 = unit_token<D>(4 * (g >> 1) + (g & 1)), t1 = t0 + 2;
+  const uint32_t k_at0 = tile_offset<D>(t0, c), k_at1 = tile_offset<D>(t1, c);
+  const uint32_t v_at = tile_offset<D>(unit_token<D>(lane & 15), lane >> 4);
+
+  // the step's units, landed at `stage`; the first one's first token is `tok`
+  auto compute = [&](uint32_t stage, const float4 (&mu)[UPS], int tok) {
+    float s[UPS][NT][4];
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
+    for (int u = 0; u < UPS; ++u) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[k][nt][j] = 0.f;
-    // S^T = K q^T: lane (g, c) holds tokens g, g + 8 and 16-byte chunk c of each 64 bytes
-    const int t0 = unit_token<D>(g), t1 = t0 + 8;
+        for (int j = 0; j < 4; ++j) s[u][nt][j] = FMT == QG_KV_I8 ? off[nt][j & 1] : 0.f;
+      // S^T = K q^T: lane (g, c) holds tokens t0, t1 and 16-byte chunk c of each 64 bytes
 #pragma unroll
-    for (int hf = 0; hf < S::kHalves; ++hf) {
-      const uint32_t tile = stage + (hf >> 1) * kUnit * S::kRowBytes;
-      const int ch = D == 64 ? c : c + 4 * (hf & 1);
-      const uint4 k0 = lds128(tile + tile_offset<D>(t0, ch)), k1 = lds128(tile + tile_offset<D>(t1, ch));
-      const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+      for (int hf = 0; hf < S::kHalves; ++hf) {
+        const uint32_t tile = stage + u * S::kUnitBytes + (hf >> 1) * kUnit * S::kRowBytes, x = 64 * (hf & 1);
+        const uint4 k0 = lds128((tile + k_at0) ^ x), k1 = lds128((tile + k_at1) ^ x);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t f[4];
-        codes_to_f16<FMT>(w0[w], f[0], f[2]);
-        codes_to_f16<FMT>(w1[w], f[1], f[3]);
+        for (int w = 0; w < 4; ++w) {
+          uint32_t f[4];
+          codes_to_f16<FMT, true>(w0[w], f[0], f[2]);
+          codes_to_f16<FMT, true>(w1[w], f[1], f[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint2 b = kQRegs ? qr[hf * 4 + w][nt] : qfrag[((hf * 4 + w) * NT + nt) * 32 + lane];
-          mma16816(sc[w % CH][nt], f, b.x, b.y);
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 b = kQRegs ? qr[hf * 4 + w][nt] : qfrag[((hf * 4 + w) * NT + nt) * 32 + lane];
+            mma16816(s[u][nt], f, b.x, b.y);
+          }
         }
       }
     }
-    float s[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] = CH == 2 ? sc[0][nt][j] + sc[CH - 1][nt][j] : sc[0][nt][j];
     // t = log2 of (probability times value scale); lane: tokens t0, t1 of rows 2 c, 2 c + 1
-    const bool edge = tok + kUnit > base;  // some row may not see some token
-    bool grow = false;
+    bool grow = false, edge[UPS];
+    uint32_t keep[UPS];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int u = 0; u < UPS; ++u) {
+      const int at0 = tok + u * kUnit;
+      // some row may not see some token, or the unit is absent or has no values
+      edge[u] = at0 + kUnit > base || mu[u].w != 1.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(s[nt][j], mt_.x * rf[nt][j & 1], mt_.y);
-      if (edge) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at = tok + (j < 2 ? t0 : t1), rr = nt * 8 + 2 * c + (j & 1);
-          const unsigned d = (unsigned)(at - base);
-          const int2 lim = *reinterpret_cast<const int2*>(row_info + rr);
-          const bool seen = at < lim.x || (d < 32u && ((unsigned)lim.y >> d & 1u));
-          if (!seen) s[nt][j] = -INFINITY;
+        for (int j = 0; j < 4; ++j) s[u][nt][j] = fmaf(s[u][nt][j], mu[u].x * rf[nt][j & 1], mu[u].y);
+      if (edge[u]) {
+        keep[u] = 0u;  // bytes of the lane's value words that count (slots past the context may hold no numbers)
+        if (mu[u].w == 1.f) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (at0 + unit_token<D>(4 * c + b) < ctx) keep[u] |= 0xFFu << (8 * b);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int at = at0 + (j < 2 ? t0 : t1);
+            const unsigned d = (unsigned)(at - base);
+            const int2 lim = *reinterpret_cast<const int2*>(row_info + nt * 8 + 2 * c + (j & 1));
+            const bool seen = mu[u].w != 0.f && (at < lim.x || (d < 32u && ((unsigned)lim.y >> d & 1u)));
+            if (!seen) s[u][nt][j] = -INFINITY;
+          }
         }
       }
-      grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kSlack || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kSlack;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        grow |= fmaxf(s[u][nt][0], s[u][nt][2]) > m[nt][0] + kSlack ||
+                fmaxf(s[u][nt][1], s[u][nt][3]) > m[nt][1] + kSlack;
     }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float x = fmaxf(s[nt][j], s[nt][j + 2]);
+          float x = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+          if (UPS == 2) x = fmaxf(x, fmaxf(s[UPS - 1][nt][j], s[UPS - 1][nt][j + 2]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -624,71 +692,58 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         }
       }
     }
-    uint32_t pb[NT][2];
+    uint32_t pb[UPS][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float e[4];
+    for (int u = 0; u < UPS; ++u) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] = ex2(s[nt][j] - m[nt][j & 1]);
-      l[nt][0] = fmaf(e[0] + e[2], mt_.z, l[nt][0]);
-      l[nt][1] = fmaf(e[1] + e[3], mt_.z, l[nt][1]);
-      // (token, row) -> (row, token): the B operand of the value product
-      pb[nt][0] = transpose8x8(f16x2(e[0], e[1]));
-      pb[nt][1] = transpose8x8(f16x2(e[2], e[3]));
-    }
-    if (mt_.w == 2.f) return;
-    // O^T += V^T p^T: lane (g, c) holds kVB bytes of the tokens of MMA columns 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-    const int r0 = unit_token<D>(2 * c), r1 = unit_token<D>(2 * c + 1);
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
 #pragma unroll
-    for (int sub = 0; sub < S::kSubs; ++sub) {
-      const uint32_t tile = stage + kUnit * D + sub * kUnit * S::kRowBytes;
-      uint32_t v[4][S::kVB / 4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int rr = (k & 1 ? r1 : r0) + (k & 2 ? 8 : 0);
-        if (D == 64) {
-          const uint2 x = lds64(tile + tile_offset<D>(rr, g >> 1) + 8 * (g & 1));
-          v[k][0] = x.x, v[k][1] = x.y;
-        } else {
-          const uint4 x = lds128(tile + tile_offset<D>(rr, g));
-          v[k][0] = x.x, v[k][1] = x.y, v[k][S::kVB / 4 - 2] = x.z, v[k][S::kVB / 4 - 1] = x.w;
-        }
-        if (FMT == QG_KV_E4M3 && edge && tok + rr >= ctx) {
-          // slots past the context may hold codes that are not numbers
-#pragma unroll
-          for (int w = 0; w < S::kVB / 4; ++w) v[k][w] = 0u;
-        }
+        for (int j = 0; j < 4; ++j) e[j] = ex2(s[u][nt][j] - m[nt][j & 1]);
+        l[nt][0] = fmaf(e[0] + e[2], mu[u].z, l[nt][0]);
+        l[nt][1] = fmaf(e[1] + e[3], mu[u].z, l[nt][1]);
+        // (token, row) -> (row, token): the B operand of the value product
+        pb[u][nt][0] = transpose8x8(f16x2(e[0], e[1]));
+        pb[u][nt][1] = transpose8x8(f16x2(e[2], e[3]));
       }
+    }
+    // O^T += V^T p^T, two 16-element tiles of the head at a time
 #pragma unroll
-      for (int w = 0; w < S::kVB / 4; ++w) {
-        // bytes (2 i, 2 i + 1) of a word: output rows 2 i (MMA row g) and 2 i + 1 (row g + 8) of a tile
-        uint32_t f[2][4];
+    for (int u = 0; u < UPS; ++u) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          codes_to_f16<FMT>(prmt(v[2 * k][w], v[2 * k + 1][w], 0x5140u), f[0][2 * k], f[0][2 * k + 1]);
-          codes_to_f16<FMT>(prmt(v[2 * k][w], v[2 * k + 1][w], 0x7362u), f[1][2 * k], f[1][2 * k + 1]);
+      for (int k = 0; k < S::kMt / 2; ++k) {
+        const uint32_t tile = stage + (UPS + u) * S::kUnitBytes + k / 4 * kUnit * S::kRowBytes;
+        uint32_t v[4];
+        ldmatrix_t8((tile + v_at) ^ (32 * (k % 4)), v);
+        if (edge[u]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] &= keep[u];
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          uint32_t f[4];
+          codes_to_f16<FMT>(v[2 * i], f[0], f[2]);
+          codes_to_f16<FMT>(v[2 * i + 1], f[1], f[3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(acc[nt][sub * (S::kVB / 2) + 2 * w + i], f[i], pb[nt][0], pb[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][2 * k + i], f, pb[u][nt][0], pb[u][nt][1]);
+        }
       }
     }
   };
 
-  // result of tile q = nt * kMt + mt: lane (g, c) holds elements d, d + 1 of rows 2 c, 2 c + 1 as
-  // {d r0, d r1, d+1 r0, d+1 r1}; l0, l1 the rows' sums, 0 where no token is seen (the result is 0 then)
+  // result of tile q = nt * kMt + mt: lane (g, c) holds elements d = 16 mt + g and d + 8 of rows 2 c, 2 c + 1 as
+  // {d r0, d r1, d+8 r0, d+8 r1}; l0, l1 the rows' sums, 0 where no token is seen (the result is 0 then). Lanes of
+  // even and odd g trade a row each, so that a lane writes pairs.
   auto write_out = [&](int q, const float4 o, float l0, float l1) {
-    const int nt = q / S::kMt, mt = q - nt * S::kMt;
-    const int d = mt / (S::kVB / 2) * 128 + S::kVB * g + 2 * (mt % (S::kVB / 2));
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int to = row_info[nt * 8 + 2 * c + j].z;
-      const float L = j ? l1 : l0, inv = L == 0.f ? 0.f : __frcp_rn(L);
-      if (to >= 0)
-        *reinterpret_cast<uint32_t*>(a.out + (size_t)to * D + d) =
-            f32_to_bf16x2((j ? o.y : o.x) * inv, (j ? o.w : o.z) * inv);
+    const int nt = q / S::kMt, mt = q - nt * S::kMt, odd = g & 1;
+    const float i0 = l0 == 0.f ? 0.f : __frcp_rn(l0), i1 = l1 == 0.f ? 0.f : __frcp_rn(l1);
+    const float x0 = o.x * i0, x1 = o.y * i1, y0 = o.z * i0, y1 = o.w * i1;
+    const float x = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 4), y = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 4);
+    const int to = row_info[nt * 8 + 2 * c + odd].z;
+    if (to >= 0) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (size_t)to * D + 16 * mt + (g & 6));
+      dst[0] = odd ? f32_to_bf16x2(x, x1) : f32_to_bf16x2(x0, x);
+      dst[4] = odd ? f32_to_bf16x2(y, y1) : f32_to_bf16x2(y0, y);
     }
   };
 
@@ -837,16 +892,19 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         if (i > 0) end_segment();
         if (i == n) break;
         begin_segment(c0 + i);
-        tok = (item.s * NW + warp) * kUnit;
+        tok = (item.s * NW + warp) * UPS * kUnit;
       }
       if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar + slot, phase)))
         ok = __all_sync(0xffffffffu, mbar_wait(bar + slot, phase, a.err, kErrAttnWait));
       if (ok) {
-        const float4 mt_ = my_meta[slot];
-        if (mt_.w != 0.f) compute(smem_u32(my_ring + (size_t)slot * S::kStage), mt_, tok);
+        float4 mu[UPS];
+        bool any = false;
+#pragma unroll
+        for (int u = 0; u < UPS; ++u) mu[u] = my_meta[slot * UPS + u], any |= mu[u].w != 0.f;
+        if (any) compute(smem_u32(my_ring + (size_t)slot * S::kStage), mu, tok);
         __syncwarp();
       }
-      tok += NW * kUnit;
+      tok += TOK;
     }
     if (ok && i + stages < n) issue(i + stages, slot);
     if (++slot == stages) slot = 0, phase ^= 1u;
@@ -866,7 +924,7 @@ AttnLaunch attn_smem(int R) {
   using S = AttnShape<D, NT, FMT>;
   const size_t fixed = S::kBuf + S::kQ + S::kRaw + 24 * S::kWarps * S::kRows + 16 * (size_t)(R + 1);
   const size_t budget = (size_t)device_max_smem_optin() - 2048 - fixed;
-  const size_t per = (size_t)S::kWarps * (S::kStage + 24);
+  const size_t per = (size_t)S::kWarps * (S::kStage + 16 * S::kUps + 8);
   AttnLaunch l;
   l.stages = (int)std::min<size_t>(8, budget / per);
   l.ring = (uint32_t)((size_t)l.stages * S::kWarps * S::kStage);
@@ -884,17 +942,18 @@ template <int D, int NT, int FMT>
 cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   using S = AttnShape<D, NT, FMT>;
   CUtensorMap km, vm;
+  const int wide = S::kUps == 2 && a.bs % 32 == 0;  // a step's two units in one box
   const auto sw = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   for (int i = 0; i < 2; ++i)
     if (!tmap_3d(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? a.v_cache : a.k_cache, D, a.bs,
-                 (uint64_t)a.num_blocks * a.Hkv, D, (uint64_t)a.bs * D, S::kRowBytes, kUnit, 1, sw))
+                 (uint64_t)a.num_blocks * a.Hkv, D, (uint64_t)a.bs * D, S::kRowBytes, wide ? 2 * kUnit : kUnit, 1, sw))
       return cudaErrorInvalidValue;
   auto k = attn_kv8_kernel<D, NT, FMT>;
   cudaError_t e = allow_max_smem(k);
   if (e != cudaSuccess) return e;
   const AttnLaunch l = attn_smem<D, NT, FMT>(a.R);
   return launch_kernel(k, dim3(std::min(device_sm_count(), kMaxCtas)), dim3(32 * S::kWarps), l.smem, stream, pdl, km, vm, a, l.stages,
-                       l.ring);
+                       l.ring, wide);
 }
 
 // 8-row tiles per item: the least that hold an average request's query rows (more than 32 rows take several
