@@ -29,6 +29,7 @@ constexpr int kPlanThreads = 512;
 struct PlanSums {
   int take, rel;
   long long tok;
+  int flags;  // joined, not summed
 };
 
 // exclusive prefix sums over the CTA; `total` gets the sums of all threads
@@ -41,15 +42,17 @@ __device__ __forceinline__ PlanSums plan_scan(PlanSums v, PlanSums* part, PlanSu
     const long long c = __shfl_up_sync(0xffffffffu, s.tok, o);
     if (lane >= o) s.take += a, s.rel += b, s.tok += c;
   }
+  s.flags = __reduce_or_sync(0xffffffffu, v.flags);
   if (lane == 31) part[warp] = s;
   __syncthreads();
-  PlanSums before = {0, 0, 0};
-  total = {0, 0, 0};
+  PlanSums before = {0, 0, 0, 0};
+  total = {0, 0, 0, 0};
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     if (w < warp) before.take += part[w].take, before.rel += part[w].rel, before.tok += part[w].tok;
     total.take += part[w].take, total.rel += part[w].rel, total.tok += part[w].tok;
+    total.flags |= part[w].flags;
   }
-  return {before.take + s.take - v.take, before.rel + s.rel - v.rel, before.tok + s.tok - v.tok};
+  return {before.take + s.take - v.take, before.rel + s.rel - v.rel, before.tok + s.tok - v.tok, 0};
 }
 
 // largest r in [0, n) with a[r] <= v, for ascending a with a[0] <= v
@@ -67,9 +70,11 @@ __device__ __forceinline__ int last_not_above(const int* a, int n, int v) {
 
 __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
   extern __shared__ int sm[];
-  int* take_ex = sm;              // [R + 1]
-  int* rel_ex = sm + a.R + 1;     // [R + 1]
-  int* tok_ex = sm + 2 * a.R + 2; // [R + 1]
+  int* take_ex = sm;                    // [R + 1] blocks taken before the request
+  int* rel_ex = sm + a.R + 1;           // [R + 1] blocks released before it
+  int* tok_ex = sm + 2 * (a.R + 1);     // [R + 1] new tokens before it
+  int2* blocks = reinterpret_cast<int2*>(sm + (3 * a.R + 4) / 2 * 2);  // [R] blocks held before and after
+  int* olds = reinterpret_cast<int*>(blocks + a.R);                    // [R]
   __shared__ PlanSums part[kPlanThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
@@ -77,66 +82,54 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
   const int per = (a.R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
   const int count = *a.free_count;
-  bool neg = false, outgrown = false;
-  PlanSums mine = {0, 0, 0};
+  PlanSums mine = {0, 0, 0, 0};  // flags 2: a request outgrows the table, 4: a negative length
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) {
     const int o = a.old_lens[r], n = a.new_lens[r];
+    take_ex[r] = mine.take, rel_ex[r] = mine.rel, tok_ex[r] = (int)mine.tok;
+    olds[r] = o;
     if (o < 0 || n < 0) {
-      neg = true;
+      mine.flags |= 4;
     } else if (max(o, n) > a.max_blocks * a.bs) {
-      outgrown = true;
+      mine.flags |= 2;
     } else {
       const int have = (o + a.bs - 1) / a.bs, need = (n + a.bs - 1) / a.bs;
+      blocks[r] = make_int2(have, need);
       mine.take += max(0, need - have);
       mine.rel += max(0, have - need);
       mine.tok += max(0, n - o);
     }
   }
-  const bool any_neg = __syncthreads_or(neg), any_out = __syncthreads_or(outgrown);
   PlanSums total;
-  PlanSums ex = plan_scan(mine, part, total);
+  const PlanSums ex = plan_scan(mine, part, total);
   const int top = count + total.rel;
   int state = 0;
-  if (any_neg || count < 0 || count > a.num_blocks || total.rel > a.num_blocks - count)
+  if ((total.flags & 4) || count < 0 || count > a.num_blocks || total.rel > a.num_blocks - count)
     state = 4;
-  else if (any_out)
+  else if (total.flags & 2)
     state = 2;
   else if (total.tok > a.max_tokens)
     state = 3;
   else if (total.take > top)
     state = 1;
-  if (state) total = {0, 0, 0};
-  if (state == 0) {
-    for (int r = r0; r < r1; ++r) {
-      const int o = a.old_lens[r], n = a.new_lens[r];
-      const int have = (o + a.bs - 1) / a.bs, need = (n + a.bs - 1) / a.bs;
-      take_ex[r] = ex.take, rel_ex[r] = ex.rel, tok_ex[r] = (int)ex.tok;
-      ex.take += max(0, need - have), ex.rel += max(0, have - need), ex.tok += max(0, n - o);
-    }
-    if (tid == 0) take_ex[a.R] = total.take, rel_ex[a.R] = total.rel, tok_ex[a.R] = (int)total.tok;
-  }
+  if (state) total = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) take_ex[r] += ex.take, rel_ex[r] += ex.rel, tok_ex[r] += (int)ex.tok;
+  if (tid == 0) take_ex[a.R] = total.take, rel_ex[a.R] = total.rel, tok_ex[a.R] = (int)total.tok;
   __syncthreads();
   // the block of rank j among those taken
   auto taken = [&](int j) {
     const int p = top - 1 - j;
     if (p < count) return a.free_list[p];
-    const int k = top - 1 - p;  // rank among the released
-    const int r = last_not_above(rel_ex, a.R, k);
-    return a.table[(size_t)r * a.max_blocks + (a.new_lens[r] + a.bs - 1) / a.bs + (k - rel_ex[r])];
+    const int r = last_not_above(rel_ex, a.R, j);  // also the rank among the released
+    return a.table[(size_t)r * a.max_blocks + blocks[r].y + (j - rel_ex[r])];
   };
+  // Three lists of independent writes, each begun at another thread, so that short ones run side by side.
   const int nthreads = gridDim.x * kPlanThreads, gid = blockIdx.x * kPlanThreads + tid;
-  for (int j = gid; j < total.take; j += nthreads) {
-    const int r = last_not_above(take_ex, a.R, j);
-    a.table[(size_t)r * a.max_blocks + (a.old_lens[r] + a.bs - 1) / a.bs + (j - take_ex[r])] = taken(j);
-  }
-  for (int k = gid; k < total.rel; k += nthreads) {
-    const int r = last_not_above(rel_ex, a.R, k);
-    a.free_list[top - 1 - k] =
-        a.table[(size_t)r * a.max_blocks + (a.new_lens[r] + a.bs - 1) / a.bs + (k - rel_ex[r])];
-  }
+  const int tokens = (int)total.tok;
+#pragma unroll 1
   for (int t0 = 4 * gid; t0 < a.max_tokens; t0 += 4 * nthreads) {
     int slot[4], pos[4];
-    const int tokens = (int)total.tok;
     int r = t0 < tokens ? last_not_above(tok_ex, a.R, t0) : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -144,9 +137,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
       slot[i] = pos[i] = -1;
       if (t < tokens) {
         while (tok_ex[r + 1] <= t) ++r;
-        const int old = a.old_lens[r], p = old + t - tok_ex[r], b = p / a.bs, have = (old + a.bs - 1) / a.bs;
+        const int p = olds[r] + t - tok_ex[r], b = p / a.bs, have = blocks[r].x;
         const int blk = b < have ? a.table[(size_t)r * a.max_blocks + b] : taken(take_ex[r] + b - have);
-        slot[i] = blk * a.bs + p % a.bs;
+        slot[i] = blk * a.bs + p - b * a.bs;
         pos[i] = p;
       }
     }
@@ -160,17 +153,35 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
       }
     }
   }
-  if (blockIdx.x == 0) {
+  const int gid_take = gid >= nthreads / 2 ? gid - nthreads / 2 : gid + (nthreads - nthreads / 2);
+#pragma unroll 1
+  for (int j = gid_take; j < total.take; j += nthreads) {
+    const int r = last_not_above(take_ex, a.R, j);
+    a.table[(size_t)r * a.max_blocks + blocks[r].x + (j - take_ex[r])] = taken(j);
+  }
+  const int gid_rel = gid >= nthreads / 4 * 3 ? gid - nthreads / 4 * 3 : gid + (nthreads - nthreads / 4 * 3);
+#pragma unroll 1
+  for (int k = gid_rel; k < total.rel; k += nthreads) {
+    const int r = last_not_above(rel_ex, a.R, k);
+    a.free_list[top - 1 - k] = a.table[(size_t)r * a.max_blocks + blocks[r].y + (k - rel_ex[r])];
+  }
+  if (blockIdx.x == gridDim.x - 1) {
+#pragma unroll 1
     for (int r = tid; r <= a.R; r += kPlanThreads) a.cu_new[r] = state ? 0 : tok_ex[r];
-    if (tid == 0) a.info[0] = (int)total.tok, a.info[1] = total.take, a.info[2] = total.rel, a.info[3] = state;
+    if (tid == 0) *reinterpret_cast<int4*>(a.info) = make_int4(tokens, total.take, total.rel, state);
   }
   // free_count_out may be free_count: the CTA that read it last writes it (no one waits)
   if (tid == 0) {
-    unsigned seen;
-    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.ticket) : "memory");
-    if (seen == gridDim.x - 1) {
-      *a.free_count_out = state ? count : top - total.take;
-      *a.ticket = 0;
+    const int left = state ? count : top - total.take;
+    if (gridDim.x == 1) {
+      *a.free_count_out = left;
+    } else {
+      unsigned seen;
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.ticket) : "memory");
+      if (seen == gridDim.x - 1) {
+        *a.free_count_out = left;
+        *a.ticket = 0;
+      }
     }
   }
 }
@@ -184,10 +195,10 @@ constexpr int kAppendKeep = 8;  // steps of 8 elements kept in registers between
 __device__ __forceinline__ void load8_in(const void* p, int f32, size_t elem, float (&v)[8]) {
   if (f32) {
     const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + elem);
-    const float4 a = __ldg(s), b = __ldg(s + 1);
+    const float4 a = __ldcs(s), b = __ldcs(s + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + elem));
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + elem));
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -198,67 +209,73 @@ __device__ __forceinline__ void load8_in(const void* p, int f32, size_t elem, fl
 }
 
 template <int FMT>
-__device__ __forceinline__ uint2 encode8(const float (&v)[8]) {
-  return make_uint2(kv8_encode4<FMT>(v[0], v[1], v[2], v[3]), kv8_encode4<FMT>(v[4], v[5], v[6], v[7]));
-}
-
-template <int FMT>
 __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a) {
-  __shared__ int run_len;
+  __shared__ int lead[kAppendThreads], leads;
+  __shared__ int part_n[kAppendThreads / 32];
   __shared__ float part[kAppendThreads / 32];
+  const int tid = threadIdx.x;
+  if (tid == 0) leads = 0;
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x;
   const int which = blockIdx.y & 1, head = blockIdx.y >> 1;
   const void* x = which ? a.v : a.k;
   const long long stride = which ? a.v_stride : a.k_stride;
   uint8_t* cache = static_cast<uint8_t*>(which ? a.v_cache : a.k_cache);
   const int d8 = a.D / 8;
-  const int t_end = min(a.T, (int)(blockIdx.x + 1) * a.window);
-  for (int t0 = blockIdx.x * a.window; t0 < t_end; ++t0) {
-    const int slot = __ldg(a.slot_map + t0);
-    if (slot < 0) continue;
-    if (slot >= a.num_blocks * a.bs) {
-      if (tid == 0) report_error(a.err, kErrKvSlot);
-      continue;
+  __syncthreads();
+  {
+    // the first tokens of runs in this CTA's window (slots of a block ascend by one)
+    const int t = blockIdx.x * a.window + tid;
+    if (tid < a.window && t < a.T) {
+      const int slot = __ldg(a.slot_map + t), prev = t > 0 ? __ldg(a.slot_map + t - 1) : -1;
+      if (slot >= a.num_blocks * a.bs)
+        report_error(a.err, kErrKvSlot);
+      else if (slot >= 0 && (slot % a.bs == 0 || prev != slot - 1))
+        lead[atomicAdd(&leads, 1)] = t;
     }
-    const int f = slot % a.bs, blk = slot / a.bs;
-    // the first token of its block in this call? (slots of a block ascend by one)
-    if (f > 0 && t0 > 0 && __ldg(a.slot_map + t0 - 1) == slot - 1) continue;
-    __syncthreads();
-    if (tid == 0) run_len = a.bs - f;
-    __syncthreads();
+  }
+  __syncthreads();
+  for (int k = 0; k < leads; ++k) {
+    const int t0 = lead[k], slot = __ldg(a.slot_map + t0), f = slot % a.bs, blk = slot / a.bs;
+    int n = a.bs - f;  // the run's length: up to the block's end or the first slot that does not follow
     for (int i = tid; i < a.bs - f; i += kAppendThreads)
-      if (t0 + i >= a.T || __ldg(a.slot_map + t0 + i) != slot + i) atomicMin(&run_len, i);
+      if (t0 + i >= a.T || __ldg(a.slot_map + t0 + i) != slot + i) n = min(n, i);
+    n = __reduce_min_sync(0xffffffffu, n);
+    if ((tid & 31) == 0) part_n[tid >> 5] = n;
+    float* sp = a.scales + 2 * ((size_t)blk * a.Hkv + head) + which;
+    const float s0 = f > 0 ? *sp : 0.f;
     __syncthreads();
-    const int chunks = run_len * d8;
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) n = min(n, part_n[w]);
+    const int chunks = n * d8;
+    auto at = [&](int i) { return (t0 + i / d8) * stride + head * a.D + (i % d8) * 8; };
     float keep[kAppendKeep][8];
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < kAppendKeep; ++c) {
       const int i = tid + c * kAppendThreads;
-      if (i < chunks) {
-        load8_in(x, a.f32, (t0 + i / d8) * stride + head * a.D + (i % d8) * 8, keep[c]);
+      if (i < chunks) load8_in(x, a.f32, at(i), keep[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kAppendKeep; ++c) {
+      if (tid + c * kAppendThreads < chunks) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(keep[c][j]));
       }
     }
     for (int i = tid + kAppendKeep * kAppendThreads; i < chunks; i += kAppendThreads) {
       float v[8];
-      load8_in(x, a.f32, (t0 + i / d8) * stride + head * a.D + (i % d8) * 8, v);
+      load8_in(x, a.f32, at(i), v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if ((tid & 31) == 0) part[tid >> 5] = amax;
-    float* sp = a.scales + 2 * ((size_t)blk * a.Hkv + head) + which;
-    const float s0 = f > 0 ? *sp : 0.f;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, part[w]);
-    const float s1 = __fdiv_rn(amax, kv8_qmax<FMT>());
-    const float s = fmaxf(s0, s1);
+    const float s = fmaxf(s0, __fdiv_rn(amax, kv8_qmax<FMT>()));
     if (tid == 0) *sp = s;  // every thread read the old one before the barrier
     uint8_t* page = cache + ((size_t)blk * a.Hkv + head) * a.bs * a.D;
     if (f > 0 && s > s0) {
@@ -272,25 +289,24 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
         kv8_decode4<FMT>(old.y, v[4], v[5], v[6], v[7]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], ratio);
-        *p = encode8<FMT>(v);
+        *p = make_uint2(kv8_encode4<FMT>(v[0], v[1], v[2], v[3]), kv8_encode4<FMT>(v[4], v[5], v[6], v[7]));
       }
     }
     uint2* dst = reinterpret_cast<uint2*>(page + (size_t)f * a.D);
-    auto store = [&](int i, float(&v)[8]) {
+    const float inv = __frcp_rn(s);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = s > 0.f ? __fdiv_rn(v[j], s) : 0.f;
-      dst[i] = encode8<FMT>(v);
-    };
-#pragma unroll
-    for (int c = 0; c < kAppendKeep; ++c)
-      if (tid + c * kAppendThreads < chunks) store(tid + c * kAppendThreads, keep[c]);
+    for (int c = 0; c < kAppendKeep; ++c) {
+      const int i = tid + c * kAppendThreads;
+      if (i < chunks) dst[i] = s > 0.f ? kv8_quantize8<FMT>(keep[c], s, inv) : make_uint2(0u, 0u);
+    }
     for (int i = tid + kAppendKeep * kAppendThreads; i < chunks; i += kAppendThreads) {
       float v[8];
-      load8_in(x, a.f32, (t0 + i / d8) * stride + head * a.D + (i % d8) * 8, v);
-      store(i, v);
+      load8_in(x, a.f32, at(i), v);
+      dst[i] = s > 0.f ? kv8_quantize8<FMT>(v, s, inv) : make_uint2(0u, 0u);
     }
     if (f == 0)
       for (int i = tid + chunks; i < a.bs * d8; i += kAppendThreads) dst[i] = make_uint2(0u, 0u);
+    // (part_n and part are written again only after a barrier that follows their last reads)
   }
 }
 
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(ReadArgs a) {
 
 cudaError_t launch_kv8_plan(const PlanArgs& a, cudaStream_t stream, bool pdl) {
   const int ctas = std::min(device_sm_count(), std::max(1, (a.max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads)));
-  const size_t smem = 3 * sizeof(int) * (a.R + 1);
+  const size_t smem = sizeof(int) * (6 * (size_t)a.R + 8);
   if (smem > 40 << 10) {
     cudaError_t e = allow_max_smem(kv8_plan_kernel);
     if (e != cudaSuccess) return e;
@@ -341,8 +357,9 @@ cudaError_t launch_kv8_plan(const PlanArgs& a, cudaStream_t stream, bool pdl) {
 }
 
 cudaError_t launch_kv8_append(AppendArgs a, int format, cudaStream_t stream, bool pdl) {
-  const long long items = (long long)a.T * a.Hkv * 2;
-  a.window = (int)std::min<long long>(a.bs, std::max<long long>(1, (items + 2431) / 2432));
+  // tokens whose runs one CTA takes: one where that gives up to 1024 CTAs, up to a block of them for a prompt
+  a.window = (int)std::min<long long>(std::min(a.bs, kAppendThreads),
+                                      std::max<long long>(1, (long long)a.T * a.Hkv * 2 / 1024));
   const dim3 grid((a.T + a.window - 1) / a.window, 2 * a.Hkv);
   auto k = format == QG_KV_I8 ? kv8_append_kernel<QG_KV_I8> : kv8_append_kernel<QG_KV_E4M3>;
   return launch_kernel(k, grid, dim3(kAppendThreads), 0, stream, pdl, a);
