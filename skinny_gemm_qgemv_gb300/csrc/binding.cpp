@@ -104,9 +104,9 @@ struct Call {
   at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
     return at::detail::empty_cuda(shape, type, dev, std::nullopt);
   }
-  // the given output, checked, or a new one
+  // the given output, checked, or none yet (Outputs makes those that are missing)
   at::Tensor output(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> shape, const char* name) const {
-    if (o == Py_None) return make(at::IntArrayRef(shape.begin(), shape.size()), type);
+    if (o == Py_None) return at::Tensor();
     const at::Tensor& t = *tensor(o, name);
     need(t, type, shape, name);
     return t;
@@ -117,6 +117,54 @@ struct Call {
     Py_XDECREF(r);
     throw Raised{};
   }
+};
+
+// The outputs that a call makes. Small ones share one allocation (0.8 us each on
+// the host cores, of a call that takes 4); large ones get their own, so that
+// one does not keep another's memory.
+class Outputs {
+ public:
+  explicit Outputs(const Call& c) : c_(c) {}
+  void add(at::Tensor& t, at::ScalarType type, std::initializer_list<int64_t> shape) {
+    if (t.defined()) return;
+    Want& w = wants_[n_++];
+    w.to = &t;
+    w.type = type;
+    w.dims = 0;
+    w.bytes = c10::elementSize(type);
+    for (int64_t d : shape) w.shape[w.dims++] = d, w.bytes *= d;
+  }
+  void make() {
+    size_t total = 0;
+    for (int i = 0; i < n_; ++i) total += (wants_[i].bytes + 255) / 256 * 256;
+    if (n_ < 2 || total > (1u << 20)) {
+      for (int i = 0; i < n_; ++i) *wants_[i].to = c_.make(at::IntArrayRef(wants_[i].shape, wants_[i].dims), wants_[i].type);
+      return;
+    }
+    const at::Tensor base = c_.make({static_cast<int64_t>(total)}, at::kByte);
+    size_t at = 0;
+    for (int i = 0; i < n_; ++i) {
+      const Want& w = wants_[i];
+      auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(base.storage()), base.key_set(),
+                                                      c10::scalarTypeToTypeMeta(w.type));
+      impl->set_storage_offset(static_cast<int64_t>(at / c10::elementSize(w.type)));
+      impl->set_sizes_contiguous(at::IntArrayRef(w.shape, w.dims));
+      *w.to = at::Tensor(std::move(impl));
+      at += (w.bytes + 255) / 256 * 256;
+    }
+  }
+
+ private:
+  struct Want {
+    at::Tensor* to;
+    at::ScalarType type;
+    int64_t shape[4];
+    int dims;
+    size_t bytes;
+  };
+  const Call& c_;
+  Want wants_[5];
+  int n_ = 0;
 };
 
 // A workspace whose counters every call leaves at zero, kept per (use, device,
@@ -205,11 +253,17 @@ PyObject* block_plan(PyObject* const* a) {
   c.need(count, at::kInt, {1}, "free_count");
   const int bs = whole32(a[5], "block_size"), max_tokens = whole32(a[6], "max_tokens");
   if (max_tokens < 0) refuse("max_tokens is negative");
-  const at::Tensor count_out = c.output(a[7], at::kInt, {1}, "free_count_out"),
-                   cu = c.output(a[8], at::kInt, {R + 1}, "cu_new"),
-                   slots = c.output(a[9], at::kInt, {max_tokens}, "slot_map"),
-                   pos = c.output(a[10], at::kInt, {max_tokens}, "positions"),
-                   info = c.output(a[11], at::kInt, {4}, "info");
+  at::Tensor count_out = c.output(a[7], at::kInt, {1}, "free_count_out"),
+             cu = c.output(a[8], at::kInt, {R + 1}, "cu_new"),
+             slots = c.output(a[9], at::kInt, {max_tokens}, "slot_map"),
+             pos = c.output(a[10], at::kInt, {max_tokens}, "positions"), info = c.output(a[11], at::kInt, {4}, "info");
+  Outputs outs(c);
+  outs.add(count_out, at::kInt, {1});
+  outs.add(cu, at::kInt, {R + 1});
+  outs.add(slots, at::kInt, {max_tokens});
+  outs.add(pos, at::kInt, {max_tokens});
+  outs.add(info, at::kInt, {4});
+  outs.make();
   const at::Tensor ws = workspace(c, a[12], "plan", qg_kv8_plan_workspace_size());
   c.done(kv8_block_plan(ptr<int32_t>(old_lens), ptr<int32_t>(new_lens), size32(R, "R"), bs, ptr<int32_t>(table),
                         size32(table.size(1), "max_blocks"), ptr<int32_t>(free_list),
@@ -242,8 +296,12 @@ PyObject* read(PyObject* const* a) {
   const Cache s = cache_of(c, kc, vc, sc);
   const int64_t B = ids.numel();
   c.need(ids, at::kInt, {B}, "block_ids");
-  const at::Tensor k = c.make({B, s.Hkv, s.block_size, s.D}, at::kBFloat16),
-                   v = c.make({B, s.Hkv, s.block_size, s.D}, at::kBFloat16), so = c.make({B, s.Hkv, 2}, at::kFloat);
+  at::Tensor k, v, so;
+  Outputs outs(c);
+  outs.add(k, at::kBFloat16, {B, s.Hkv, s.block_size, s.D});
+  outs.add(v, at::kBFloat16, {B, s.Hkv, s.block_size, s.D});
+  outs.add(so, at::kFloat, {B, s.Hkv, 2});
+  outs.make();
   c.done(kv8_read(ptr<int32_t>(ids), size32(B, "B"), s.Hkv, s.D, s.block_size, s.num_blocks, s.format, ptr<void>(kc),
                   ptr<void>(vc), ptr<float>(sc), ptr<uint16_t>(k), ptr<uint16_t>(v), ptr<float>(so), c.stream));
   return tuple(k, v, so);
@@ -264,7 +322,8 @@ PyObject* attention(PyObject* const* a) {
   c.need(table, at::kInt, {R, -1}, "block_table");
   if (tree) c.need(*tree, at::kInt, {T}, "tree_mask");
   const float scale = a[8] == Py_None ? 1.f / std::sqrt(static_cast<float>(s.D)) : real(a[8]);
-  const at::Tensor out = c.output(a[9], at::kBFloat16, {T, Hq, s.D}, "out");
+  at::Tensor out = c.output(a[9], at::kBFloat16, {T, Hq, s.D}, "out");
+  if (!out.defined()) out = c.make({T, Hq, s.D}, at::kBFloat16);
   const int hq = size32(Hq, "Hq");
   const at::Tensor ws = workspace(c, a[10], "attn", qg_attn_kv8_workspace_size(hq, s.Hkv, s.D));
   c.done(attn_kv8_paged(ptr<uint16_t>(q), stride, ptr<void>(kc), ptr<void>(vc), ptr<float>(sc), ptr<int32_t>(table),
@@ -282,7 +341,7 @@ struct Norm {
 Norm norm_args(const Call& c, const at::Tensor& x, const at::Tensor& w, const at::Tensor* res, PyObject* res_out) {
   c.dense(x, "x");
   if (x.dim() != 2) refuse("x must be [M][K]");
-  Norm n;
+  Norm n = {};
   n.M = size32(x.size(0), "M"), n.K = size32(x.size(1), "K");
   n.xd = dtype_of(x, "x");
   c.need(w, w.scalar_type(), {n.K}, "weight");
@@ -304,8 +363,12 @@ PyObject* norm_bf16(PyObject* const* a) {
   const at::Tensor &x = *tensor(a[0], "x"), &w = *tensor(a[1], "weight");
   const at::Tensor* res = tensor_or_null(a[2], "residual");
   const Call c("rmsnorm_residual", x, a[6]);
-  const Norm n = norm_args(c, x, w, res, a[4]);
-  const at::Tensor out = c.output(a[5], at::kBFloat16, {n.M, n.K}, "out");
+  Norm n = norm_args(c, x, w, res, a[4]);
+  at::Tensor out = c.output(a[5], at::kBFloat16, {n.M, n.K}, "out");
+  Outputs outs(c);
+  outs.add(out, at::kBFloat16, {n.M, n.K});
+  if (res) outs.add(n.res_out, res->scalar_type(), {n.M, n.K});
+  outs.make();
   c.done(rmsnorm_residual(ptr<void>(x), n.xd, ptr<void>(res), n.rd, ptr<void>(w), n.wd, real(a[3]), n.M, n.K,
                           n.res_out.defined() ? ptr<void>(n.res_out) : nullptr, ptr<uint16_t>(out), c.stream));
   return tuple(out, n.res_out);
@@ -315,9 +378,14 @@ PyObject* norm_i8(PyObject* const* a) {
   const at::Tensor &x = *tensor(a[0], "x"), &w = *tensor(a[1], "weight");
   const at::Tensor *res = tensor_or_null(a[2], "residual"), *sb = tensor_or_null(a[3], "sign_bits");
   const Call c("rmsnorm_residual_i8", x, a[8]);
-  const Norm n = norm_args(c, x, w, res, a[5]);
+  Norm n = norm_args(c, x, w, res, a[5]);
   if (sb) c.need(*sb, at::kInt, {n.K / 32}, "sign_bits");
-  const at::Tensor q = c.output(a[6], at::kChar, {n.M, n.K}, "q"), scale = c.output(a[7], at::kFloat, {n.M}, "scale");
+  at::Tensor q = c.output(a[6], at::kChar, {n.M, n.K}, "q"), scale = c.output(a[7], at::kFloat, {n.M}, "scale");
+  Outputs outs(c);
+  outs.add(q, at::kChar, {n.M, n.K});
+  outs.add(scale, at::kFloat, {n.M});
+  if (res) outs.add(n.res_out, res->scalar_type(), {n.M, n.K});
+  outs.make();
   c.done(rmsnorm_residual_i8(ptr<void>(x), n.xd, ptr<void>(res), n.rd, ptr<void>(w), n.wd, real(a[4]),
                              ptr<uint32_t>(sb), n.M, n.K, n.res_out.defined() ? ptr<void>(n.res_out) : nullptr,
                              ptr<int8_t>(q), ptr<float>(scale), c.stream));

@@ -54,30 +54,37 @@ __device__ __forceinline__ uint32_t kv8_encode4(float a, float b, float c, float
   return (uint32_t)lo | (uint32_t)hi << 16;
 }
 
-// Codes of eight values over s > 0: the IEEE quotient v / s to the nearest code.
-// The quotient is taken as v times 1 / s, at most 2 ulp off it; only where that
-// could change the code (next to a border between two codes, about 1 in 5000
-// values) the divisions are made: a division is 8 instructions and a branch.
+// Codes of eight values over s > 0: the IEEE quotient v / s to the nearest code,
+// made without a division (8 instructions and a branch) wherever the code does
+// not depend on the quotient's last bits: v times 1 / s is at most 2 ulp off it.
+// int8: only where that product lies within 1e-4 of a border between two codes
+// are the divisions made; e4m3: only where v times the reciprocals 2^-21 to
+// either side of 1 / s gives two different codes (about 1 in 5000 values each).
 template <int FMT>
 __device__ __forceinline__ uint2 kv8_quantize8(const float (&v)[8], float s, float inv) {
   bool close = !(s > 1e-30f);
+  uint2 codes;
   float q[8];
+  if (FMT == QG_KV_I8) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    q[j] = v[j] * inv;
-    if (FMT == QG_KV_I8) {
+    for (int j = 0; j < 8; ++j) {
+      q[j] = v[j] * inv;
       close |= !(fabsf(q[j] - rintf(q[j])) < 0.4999f);
-    } else {
-      // 20 mantissa bits are rounded off; below 2^-6 it is more
-      const uint32_t u = __float_as_uint(q[j]);
-      close |= (u & 0xFFFFFu) - 0x7FFF0u < 33u || ((u & 0x7FFFFFFFu) - 1u < 0x3C7FFFFFu);
     }
+    codes = make_uint2(kv8_encode4<FMT>(q[0], q[1], q[2], q[3]), kv8_encode4<FMT>(q[4], q[5], q[6], q[7]));
+  } else {
+    const float lo = inv * (1.f - 0x1p-21f), hi = inv * (1.f + 0x1p-21f);
+    codes = make_uint2(kv8_encode4<FMT>(v[0] * lo, v[1] * lo, v[2] * lo, v[3] * lo),
+                       kv8_encode4<FMT>(v[4] * lo, v[5] * lo, v[6] * lo, v[7] * lo));
+    close |= codes.x != kv8_encode4<FMT>(v[0] * hi, v[1] * hi, v[2] * hi, v[3] * hi) ||
+             codes.y != kv8_encode4<FMT>(v[4] * hi, v[5] * hi, v[6] * hi, v[7] * hi);
   }
   if (close) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(v[j], s);
+    codes = make_uint2(kv8_encode4<FMT>(q[0], q[1], q[2], q[3]), kv8_encode4<FMT>(q[4], q[5], q[6], q[7]));
   }
-  return make_uint2(kv8_encode4<FMT>(q[0], q[1], q[2], q[3]), kv8_encode4<FMT>(q[4], q[5], q[6], q[7]));
+  return codes;
 }
 
 }  // namespace qg

@@ -23,6 +23,7 @@
 namespace qg {
 namespace {
 
+
 constexpr int kPlanThreads = 512;
 
 // take and rel are bounded by R * max_blocks < 2^31, the tokens only by their check
@@ -189,8 +190,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
-constexpr int kAppendThreads = 128;
-constexpr int kAppendKeep = 8;  // steps of 8 elements kept in registers between the maximum and the codes
+constexpr int kAppendThreads = 256;
+constexpr int kAppendKeep = 4;  // steps of 8 elements kept in registers between the maximum and the codes
 
 __device__ __forceinline__ void load8_in(const void* p, int f32, size_t elem, float (&v)[8]) {
   if (f32) {
@@ -237,9 +238,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
   __syncthreads();
   for (int k = 0; k < leads; ++k) {
     const int t0 = lead[k], slot = __ldg(a.slot_map + t0), f = slot % a.bs, blk = slot / a.bs;
-    int n = a.bs - f;  // the run's length: up to the block's end or the first slot that does not follow
-    for (int i = tid; i < a.bs - f; i += kAppendThreads)
-      if (t0 + i >= a.T || __ldg(a.slot_map + t0 + i) != slot + i) n = min(n, i);
+    // The run's length: up to the block's end or the first slot that does not follow. The values it can have are
+    // loaded before it is known.
+    const int most = min(a.bs - f, a.T - t0);
+    auto at = [&](int i) { return (t0 + i / d8) * stride + head * a.D + (i % d8) * 8; };
+    float keep[kAppendKeep][8];
+#pragma unroll
+    for (int c = 0; c < kAppendKeep; ++c) {
+      const int i = tid + c * kAppendThreads;
+      if (i < most * d8) load8_in(x, a.f32, at(i), keep[c]);
+    }
+    int n = most;
+    for (int i = tid; i < most; i += kAppendThreads)
+      if (__ldg(a.slot_map + t0 + i) != slot + i) n = min(n, i);
     n = __reduce_min_sync(0xffffffffu, n);
     if ((tid & 31) == 0) part_n[tid >> 5] = n;
     float* sp = a.scales + 2 * ((size_t)blk * a.Hkv + head) + which;
@@ -248,14 +259,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
 #pragma unroll
     for (int w = 0; w < kAppendThreads / 32; ++w) n = min(n, part_n[w]);
     const int chunks = n * d8;
-    auto at = [&](int i) { return (t0 + i / d8) * stride + head * a.D + (i % d8) * 8; };
-    float keep[kAppendKeep][8];
     float amax = 0.f;
-#pragma unroll
-    for (int c = 0; c < kAppendKeep; ++c) {
-      const int i = tid + c * kAppendThreads;
-      if (i < chunks) load8_in(x, a.f32, at(i), keep[c]);
-    }
 #pragma unroll
     for (int c = 0; c < kAppendKeep; ++c) {
       if (tid + c * kAppendThreads < chunks) {
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(ReadArgs a) {
 }  // namespace
 
 cudaError_t launch_kv8_plan(const PlanArgs& a, cudaStream_t stream, bool pdl) {
-  const int ctas = std::min(device_sm_count(), std::max(1, (a.max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads)));
+  const int ctas =
+      std::min(device_sm_count(), std::max(1, (a.max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads)));
   const size_t smem = sizeof(int) * (6 * (size_t)a.R + 8);
   if (smem > 40 << 10) {
     cudaError_t e = allow_max_smem(kv8_plan_kernel);
