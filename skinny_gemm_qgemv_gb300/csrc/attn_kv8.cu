@@ -8,6 +8,7 @@
 
 #include <algorithm>
 
+#include "attn_kv8.cuh"
 #include "kv8.cuh"
 #include "qg_common.cuh"
 #include "qg_internal.h"
@@ -121,16 +122,6 @@ __global__ void __launch_bounds__(32 * kPlainWarps) attn_kv8_plain_kernel(AttnAr
 // ---------------------------------------------------------------------------
 // The tensor-core kernel: D = 64, 128 or 256
 // ---------------------------------------------------------------------------
-constexpr int kUnit = 16;                       // tokens of one ring stage: one block, one scale pair
-constexpr float kNoMax = -1e30f;                // running maximum before any seen token
-constexpr float kSlack = 8.f;                   // log2: probabilities stay below 2^8 (fp16 holds 2^15)
-constexpr float kMinScale = 5.4210109e-20f;     // 2^-64
-constexpr size_t kAttnCounterBytes = 4096;      // one counter per CTA
-constexpr int kMaxCtas = 256;                   // pieces of an item whose factors fit the combine buffer
-
-// bytes of the partial results of one CTA's piece: fp32 outputs, then (max, sum) per row
-__host__ __device__ constexpr size_t attn_piece_bytes(int rows, int D) { return (size_t)rows * (D * 4 + 8); }
-
 template <int D, int NT, int FMT>
 struct AttnShape {
   static constexpr int kWarps = 8;
@@ -170,33 +161,6 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int ch) {
   return D == 64 ? row * 64 + ((ch ^ (row >> 1 & 3)) << 4) : row * 128 + ((ch ^ (row & 7)) << 4);
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return r;
-}
-__device__ __forceinline__ uint32_t hsub2_1152(uint32_t a) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x64806480u));
-  return r;
-}
-// codes (b0, b1) and (b2, b3) of a word as f16 pairs, exact. int8: b ^ 0x80 =
-// b + 128 under the exponent byte 0x64 is fp16 1024 + 128 + b.
-// RAW: int8 stays 1152 + b (the caller takes 1152 times the other factors' sum off).
-template <int FMT, bool RAW = false>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (FMT == QG_KV_I8) {
-    const uint32_t u = w ^ 0x80808080u;
-    lo = prmt(u, 0x64646464u, 0x4140u);
-    hi = prmt(u, 0x64646464u, 0x4342u);
-    if (!RAW) lo = hsub2_1152(lo), hi = hsub2_1152(hi);
-  } else {
-    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  }
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
@@ -215,81 +179,6 @@ __device__ __forceinline__ void ldmatrix_t8(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// The CTA's view of the batch: requests, their steps and where a step lies.
-// A request has one item per key/value head and tile of kRows query rows, an
-// item has ceil(tokens / tokens of a step) steps. Shares are cut on a scale on which an
-// item also costs kItemCost steps before its first one: what beginning and
-// ending it takes (a batch of 32 requests of 1..8192 tokens, where one CTA can
-// meet 20 short items: 82 -> XX us).
-struct AttnBatch {
-  const int* first;  // [R + 1] steps before the request
-  const int* cost;   // [R + 1] the same with every item's kItemCost
-  const int* ctx;    // [R]
-  const int* cu;     // [R + 1]
-  int R, G;
-};
-struct AttnPlace {
-  int r, h, rt;   // request, key/value head, row tile
-  int s, steps;   // step within its item, steps of the item
-};
-constexpr int kItemCost = 2;
-constexpr int kWholeSteps = 6;  // items up to this long are not cut: joining the pieces takes longer (4 us)
-template <int TOK>  // tokens of a step
-__device__ __forceinline__ int attn_steps(int ctx) {
-  return max(1, (ctx + TOK - 1) / TOK);
-}
-// largest r in [0, n) with v[r] <= x
-__device__ __forceinline__ int attn_find(const int* v, int n, int x) {
-  int lo = 0, hi = n;
-#pragma unroll 1
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (v[mid] <= x)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
-template <int ROWS, int TOK>
-__device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, int step) {
-  AttnPlace p;
-  p.r = attn_find(b.first, b.R, step);
-  p.steps = attn_steps<TOK>(b.ctx[p.r]);
-  const int tiles = ((b.cu[p.r + 1] - b.cu[p.r]) * b.G + ROWS - 1) / ROWS;
-  const int rem = step - b.first[p.r], item = rem / p.steps;
-  p.s = rem - item * p.steps;
-  p.h = item / tiles;
-  p.rt = item - p.h * tiles;
-  return p;
-}
-// first step at or after place x of the cost scale, and the place of a step
-template <int TOK>
-__device__ __forceinline__ int attn_step_at(const AttnBatch& b, int x) {
-  if (x >= b.cost[b.R]) return b.first[b.R];
-  const int r = attn_find(b.cost, b.R, x), steps = attn_steps<TOK>(b.ctx[r]);
-  const int rem = x - b.cost[r], item = rem / (steps + kItemCost), at = rem - item * (steps + kItemCost);
-  // a short item belongs to the CTA whose share holds its beginning
-  return b.first[r] + item * steps + (steps <= kWholeSteps ? (at ? steps : 0) : max(0, at - kItemCost));
-}
-template <int TOK>
-__device__ __forceinline__ int attn_cost_of(const AttnBatch& b, int step) {
-  const int r = attn_find(b.first, b.R, step), steps = attn_steps<TOK>(b.ctx[r]);
-  const int rem = step - b.first[r], item = rem / steps;
-  return b.cost[r] + rem + (item + 1) * kItemCost;
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
@@ -337,63 +226,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the batch's steps ----
   const int G = a.Hq / a.Hkv;
-  const AttnBatch batch = {first, cost, ctxs, cus, a.R, G};
-  {
-    const int per = (a.R + 32 * NW - 1) / (32 * NW);
-    const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
-    const int most = a.max_blocks * a.bs;
-    int2 mine = make_int2(0, 0);  // the host has checked that both stay below 2^31
-#pragma unroll 1
-    for (int r = r0; r < r1; ++r) {
-      const int q0 = min(max(a.cu_q[r], 0), a.T), q1 = min(max(a.cu_q[r + 1], 0), a.T);
-      int ctx = max(0, a.ctx_lens[r]);
-      if (ctx > most) {
-        ctx = most;
-        if (blockIdx.x == 0) report_error(a.err, kErrKvLength);
-      }
-      ctxs[r] = ctx;
-      cus[r] = q0;
-      if (r == a.R - 1) cus[a.R] = q1;
-      first[r] = mine.x;
-      cost[r] = mine.y;
-      const int items = a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS), steps = attn_steps<TOK>(ctx);
-      mine.x += items * steps;
-      mine.y += items * (steps + kItemCost);
-    }
-    int2 inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
-      if (lane >= o) inc.x += x, inc.y += y;
-    }
-    if (lane == 31) scan_part[warp] = inc;
-    __syncthreads();
-    int2 before = make_int2(inc.x - mine.x, inc.y - mine.y), total = make_int2(0, 0);
-#pragma unroll 1
-    for (int w = 0; w < NW; ++w) {
-      const int2 x = scan_part[w];
-      if (w < warp) before.x += x.x, before.y += x.y;
-      total.x += x.x, total.y += x.y;
-    }
-#pragma unroll 1
-    for (int r = r0; r < r1; ++r) first[r] += before.x, cost[r] += before.y;
-    if (threadIdx.x == 0) first[a.R] = total.x, cost[a.R] = total.y;
-    __syncthreads();
-  }
-  const int W = cost[a.R];
-  const int A = min((int)gridDim.x, W);  // CTAs with a share: the first W % A take one place more than the others
-  if ((int)blockIdx.x >= A) return;
-  const int share = W / A, more = W % A;
-  const int x0 = blockIdx.x * share + min((int)blockIdx.x, more);
-  const int c0 = attn_step_at<TOK>(batch, x0), c1 = attn_step_at<TOK>(batch, x0 + share + ((int)blockIdx.x < more ? 1 : 0));
-  const int n = c1 - c0;
+  const AttnBatch batch = attn_scan<ROWS, TOK, 32 * NW>(a, first, cost, cus, ctxs, scan_part);
+  const AttnShare mine_of = attn_share<TOK>(batch);
+  const int c0 = mine_of.c0, c1 = mine_of.c1, n = c1 - c0;
   if (n == 0) return;
-  auto cta_of = [&](int step) {
-    const int x = attn_cost_of<TOK>(batch, step), big = more * (share + 1);
-    return x < big ? x / (share + 1) : more + (x - big) / share;
-  };
 
   // the queries of the item that `at` lies in, to buffer `b` (asynchronous)
   auto fetch_q = [&](const AttnPlace& at, int b) {
@@ -819,7 +656,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     }
     if (whole) return;
     // the CTA that brings an item's last piece adds the pieces up, in the order of the CTAs
-    const int f = cta_of(item_first), e = cta_of(item_first + item.steps - 1), pieces = e - f + 1;
+    const int f = attn_cta_of<TOK>(batch, mine_of, item_first),
+              e = attn_cta_of<TOK>(batch, mine_of, item_first + item.steps - 1), pieces = e - f + 1;
     unsigned* count = static_cast<unsigned*>(a.ws) + f;
     __threadfence();
     __syncthreads();
@@ -956,22 +794,20 @@ cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
                        l.ring, wide);
 }
 
-// 8-row tiles per item: the least that hold an average request's query rows (more than 32 rows take several
-// items; D = 256 keeps 16 rows' outputs in registers at most)
+// rows of an average request's item
+int attn_rows(const AttnArgs& a) { return (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv); }
+// more than 16 rows: the tcgen05 kernel (D = 256 keeps to this one, 16 rows at a time: its values as fp16 would take
+// all of the shared memory)
+bool attn_tc_ok(const AttnArgs& a) { return attn_rows(a) > 16 && (a.D == 64 || a.D == 128); }
+
+// 8-row tiles per item: the least that hold an average request's query rows
 template <int FMT>
 cudaError_t launch_by_shape(const AttnArgs& a, cudaStream_t stream, bool pdl) {
-  const int rows = (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv);
-  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  const bool one = attn_rows(a) <= 8;
   switch (a.D) {
-    case 64:
-      return nt == 1   ? launch_mma<64, 1, FMT>(a, stream, pdl)
-             : nt == 2 ? launch_mma<64, 2, FMT>(a, stream, pdl)
-                       : launch_mma<64, 4, FMT>(a, stream, pdl);
-    case 128:
-      return nt == 1   ? launch_mma<128, 1, FMT>(a, stream, pdl)
-             : nt == 2 ? launch_mma<128, 2, FMT>(a, stream, pdl)
-                       : launch_mma<128, 4, FMT>(a, stream, pdl);
-    default: return nt == 1 ? launch_mma<256, 1, FMT>(a, stream, pdl) : launch_mma<256, 2, FMT>(a, stream, pdl);
+    case 64: return one ? launch_mma<64, 1, FMT>(a, stream, pdl) : launch_mma<64, 2, FMT>(a, stream, pdl);
+    case 128: return one ? launch_mma<128, 1, FMT>(a, stream, pdl) : launch_mma<128, 2, FMT>(a, stream, pdl);
+    default: return one ? launch_mma<256, 1, FMT>(a, stream, pdl) : launch_mma<256, 2, FMT>(a, stream, pdl);
   }
 }
 
@@ -981,12 +817,13 @@ bool attn_mma_dim(int D) { return D == 64 || D == 128 || D == 256; }
 
 size_t attn_kv8_workspace_size(int, int, int D) {
   if (!attn_mma_dim(D)) return 0;
-  return kAttnCounterBytes + 2 * (size_t)std::min(device_sm_count(), kMaxCtas) * attn_piece_bytes(D == 256 ? 16 : 32, D);
+  return kAttnCounterBytes + 2 * (size_t)std::min(device_sm_count(), kMaxCtas) * attn_piece_bytes(D == 256 ? 16 : 64, D);
 }
 
 bool attn_kv8_ok(const AttnArgs& a) { return !attn_mma_dim(a.D) || attn_most_steps(a) < (1LL << 31); }
 
 cudaError_t launch_attn_kv8(const AttnArgs& a, int format, cudaStream_t stream, bool pdl) {
+  if (attn_tc_ok(a)) return launch_attn_kv8_tc(a, format, stream, pdl);
   if (attn_mma_dim(a.D))
     return format == QG_KV_I8 ? launch_by_shape<QG_KV_I8>(a, stream, pdl)
                               : launch_by_shape<QG_KV_E4M3>(a, stream, pdl);

@@ -1,0 +1,714 @@
+// Attention over the paged 8-bit cache for many query rows per key/value head
+// (17 and more: drafts of a speculative tree times the heads of a group), on the
+// 5th-generation tensor cores.
+//
+// With 64 rows the products of one cache byte cost what the warp-level kernel of
+// attn_kv8.cu cannot hide: its conversion of a code feeds 32 rows at most and its
+// MMAs run at half of these units' rate or less. Here a step of 128 tokens is
+// converted once for up to 64 rows:
+//   S^T [128 tokens][N rows] = K q^T    A = the keys as fp16 in TMEM (a thread
+//       converts a token's row and stores it to its own lane), B = the queries;
+//   P^T = 2^(S^T ... - m)               a thread per token, half of the rows: what is a
+//       maximum over the tokens becomes a test against the row's m, so no
+//       exchange between threads unless some score outgrows m by 2^8;
+//   O^T [D][N rows] += V^T P^T          A = the values as fp16 in shared memory,
+//       token-major as converted (MN-major operand), B = P^T as written.
+// The value scale of a token's block enters through the exponent and comes off
+// the sum again, as in attn_kv8.cu. Sums, maxima and accumulators are fp32, K, V
+// and q are exact in fp16, p is rounded to fp16.
+//
+// Sixteen warps per CTA, one CTA per SM: 0-3 convert keys, 4-7 and 8-11 softmax of
+// half of the rows each, 12 and 13 convert values, 14 issues the copies, 15 the
+// MMAs (16 warps are what leaves a thread 128 registers). Steps run through two buffers of every kind; S of step i + 1 is
+// issued before O of step i. Shares of the batch, split contexts and the joining
+// of their pieces are those of attn_kv8.cu, with all warps adding pieces up.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "attn_kv8.cuh"
+#include "kv8.cuh"
+#include "qg_common.cuh"
+#include "qg_internal.h"
+
+namespace qg {
+namespace {
+
+constexpr int kTcRows = 64;     // query rows of an item
+constexpr int kTcTok = 128;     // tokens of a step
+constexpr int kTcThreads = 512;
+constexpr int kTcMaxCtas = 152;  // pieces of an item whose factors fit the shared memory of P and q
+
+template <int D>
+struct TcShape {
+  static constexpr int kTile = kTcTok * D;                // a step's keys (or values) as stored
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kV = kTcTok * D * 2;               // a step's values as fp16: [D / 64][128 tokens][64]
+  static constexpr int kP = kTcTok * kTcRows * 2;         // [128 tokens][64 rows] fp16
+  static constexpr int kQ = kTcRows * D * 2;              // [D / 64][64 rows][64] fp16
+  static constexpr int kColK = 0, kColS = 2 * (D / 2), kColO = kColS + 2 * kTcRows;  // TMEM columns
+};
+constexpr uint32_t kTcCols = 512;
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle, version 1. K-major: rows of
+// 64 fp16, `sbo` bytes between groups of 8 rows (lbo unused). MN-major: rows are
+// K, 64 contiguous fp16 of M or N each; sbo between groups of 8 K rows, lbo
+// between blocks of 64 M (N).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// instruction descriptor: fp16 operands, fp32 accumulator
+__device__ __forceinline__ constexpr uint32_t tc_idesc(int M, int N, bool a_mn, bool b_mn) {
+  return 1u << 4 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+      "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// sixteen columns of the thread's lane, to be touched after tmem_wait_ld
+__device__ __forceinline__ void tmem_ld16(uint32_t t, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(t));
+}
+__device__ __forceinline__ void tmem_wait_ld(float* v) {  // orders later uses of v[0..15] after the wait
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+
+template <int COUNT>
+__device__ __forceinline__ void named_barrier(int id) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(COUNT) : "memory");
+}
+template <int COUNT>
+__device__ __forceinline__ bool named_barrier_or(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(p ? 1u : 0u), "r"(id), "n"(COUNT)
+      : "memory");
+  return r != 0;
+}
+
+// fp32 as integers of the same order
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ (i >> 31 & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ (i >> 31 & 0x7FFFFFFF)); }
+
+constexpr int kTcMaxStages = 4;
+
+// the rest of a wait that did not succeed at once; gives up when another role has
+__device__ __noinline__ bool tc_wait_on(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* err) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kMaxPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  report_error(err, kErrAttnWait);
+  *abort_flag = 1u;
+  return false;
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
+                       int box, int stages) {
+  using S = TcShape<D>;
+  constexpr int ROWS = kTcRows, TOK = kTcTok;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, role = warp >> 2, quad = warp & 3;
+  uint8_t* ring = smem;
+  uint8_t* vbuf = ring + stages * S::kStage;
+  uint8_t* pbuf = vbuf + 2 * S::kV;
+  uint8_t* qbuf = pbuf + 2 * S::kP;
+  int* first = reinterpret_cast<int*>(qbuf + S::kQ);
+  int* cost = first + a.R + 1;
+  int* cus = cost + a.R + 1;
+  int* ctxs = cus + a.R + 1;
+  __shared__ __align__(16) float neg_m[ROWS], fall[ROWS], sums[ROWS];
+  __shared__ __align__(16) float wsum[4][ROWS];
+  __shared__ int wmax[4][ROWS];
+  __shared__ int4 row_info[ROWS];  // tokens below .x are seen, and draft tokens by .y's bits; .z: output row or -1
+  __shared__ uint64_t full[kTcMaxStages], empty[kTcMaxStages], k_full[2], s_full[2], s_empty[2], p_full[2], v_full[2], o_done[2];
+  __shared__ int2 scan_part[kTcThreads / 32];
+  __shared__ uint32_t tmem_base;
+  __shared__ unsigned arrived, amax_bits, unset_any[2];
+  __shared__ volatile uint32_t abort_flag;
+
+  if (tid == 0) {
+    for (int i = 0; i < kTcMaxStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 6);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 4);
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, 8);
+      mbar_init(p_full + i, 8);
+      mbar_init(v_full + i, 2);
+      mbar_init(o_done + i, 1);
+    }
+    abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 15) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "r"(kTcCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  tc_before();
+  const AttnBatch batch = attn_scan<ROWS, TOK, kTcThreads>(a, first, cost, cus, ctxs, scan_part);  // has barriers
+  tc_after();
+  const AttnShare share = attn_share<TOK>(batch);
+  const uint32_t tbase = tmem_base;
+  const uint32_t tlane = tbase + ((uint32_t)(quad * 32) << 16);  // the lanes that this warp may touch
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || tc_wait_on(bar, parity, &abort_flag, a.err);
+  };
+  // the same by a whole warp, which goes on together
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+
+  int gi = 0;  // steps of the CTA's earlier segments: buffer gi & 1
+  int st = 0;  // ring stage of a role's next step, and the parity of its passes through the ring
+  uint32_t pass = 0;
+#pragma unroll 1
+  for (int step = share.c0; step < share.c1;) {
+    const AttnPlace item = attn_locate<ROWS, TOK>(batch, step);
+    const int item_first = step - item.s, seg_end = min(share.c1, item_first + item.steps), n = seg_end - step;
+    const int ctx = ctxs[item.r], q0 = cus[item.r], nq = cus[item.r + 1] - q0, base = ctx - nq;
+    const int rows = min(ROWS, nq * batch.G - item.rt * ROWS), nch = (rows + 15) / 16;  // columns in use: 16 nch
+    const int tok0 = item.s * TOK;
+    // ---- the item's queries: 2^-sigma q in fp16 with one sigma for the item (its largest |q| just below 2^15;
+    // what a row 2^20 smaller loses is 2^-40 of the largest scores), K-major, swizzled ----
+    if (tid == 0) amax_bits = 0u;
+    if (tid < ROWS) {
+      const int rho = item.rt * ROWS + tid;
+      int4 info = make_int4(0x7FFFFFFF, 0, -1, 0);
+      if (tid < rows) {
+        const int i = rho / batch.G;
+        const bool tree = a.tree && nq <= 32;
+        info.x = tree ? base : base + i + 1;
+        if (tree) info.y = (int)(a.tree[q0 + i] & (0xFFFFFFFFu >> (32 - nq)));
+        info.z = (q0 + i) * a.Hq + item.h * batch.G + rho - i * batch.G;
+      }
+      row_info[tid] = info;
+      neg_m[tid] = 0.f;
+    }
+    __syncthreads();
+    {
+      constexpr int kPer = D / 8;  // threads of a row: 8 elements each, 512 / kPer rows at a time
+      constexpr int kUse = 512, kTimes = ROWS * kPer / kUse;  // threads that take part
+      uint4 raw[kTimes];
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < kTimes; ++k) {
+        const int rr = (tid + k * kUse) / kPer % ROWS, ch = tid % kPer, to = tid < kUse ? row_info[rr].z : -1;
+        raw[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (to >= 0)
+          raw[k] = *reinterpret_cast<const uint4*>(a.q + (size_t)(to / a.Hq) * a.q_stride + (size_t)(to % a.Hq) * D + 8 * ch);
+        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+      }
+      const unsigned wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+      if (lane == 0) atomicMax(&amax_bits, wm);
+      __syncthreads();
+      const float down = pow2f(-fp16_prescale_exp(__uint_as_float(amax_bits)));
+#pragma unroll
+      for (int k = 0; k < kTimes; ++k) {
+        const int rr = (tid + k * kUse) / kPer, ch = tid % kPer;
+        if (tid >= kUse) break;
+        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          f[j] = f16x2(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
+        sts128(smem_u32(qbuf) + (ch >> 3) * ROWS * 128 + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+               make_uint4(f[0], f[1], f[2], f[3]));
+      }
+      fence_async_smem();
+    }
+    __syncthreads();
+    const float up = a.scale_log2 * pow2f(fp16_prescale_exp(__uint_as_float(amax_bits)));
+
+    if (role == 0) {
+      // ------------------------------------------------ keys: a token's row per thread, fp16 into TMEM
+      const int t = quad * 32 + lane;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int g = gi + i, b = g & 1;
+        if (!wait_warp(full + st, pass)) break;
+        if (g >= 2 && !wait_warp(s_full + b, ((g >> 1) - 1) & 1)) break;  // S of two steps ago has read the buffer
+        tc_after();
+        const uint32_t src = smem_u32(ring + (size_t)st * S::kStage);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t f[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int ch = 4 * h + j;
+            const uint32_t at = D == 64 ? t * 64 + ((ch ^ (t >> 1 & 3)) << 4) : t * 128 + ((ch ^ (t & 7)) << 4);
+            const uint4 w = lds128(src + at);
+            codes_to_f16<FMT>(w.x, f[8 * j], f[8 * j + 1]);
+            codes_to_f16<FMT>(w.y, f[8 * j + 2], f[8 * j + 3]);
+            codes_to_f16<FMT>(w.z, f[8 * j + 4], f[8 * j + 5]);
+            codes_to_f16<FMT>(w.w, f[8 * j + 6], f[8 * j + 7]);
+          }
+          tmem_st32(tlane + S::kColK + b * (D / 2) + 32 * h, f);
+        }
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + st), mbar_arrive(k_full + b);
+        if (++st == stages) st = 0, pass ^= 1u;
+      }
+    } else if (warp == 12 || warp == 13) {
+      // ------------------------------------------------ values: two tokens' rows per thread, fp16 into shared memory
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int g = gi + i, b = g & 1;
+        if (!wait_warp(full + st, pass)) break;
+        if (g >= 2 && !wait_warp(o_done + b, ((g >> 1) - 1) & 1)) break;
+        const uint32_t src = smem_u32(ring + (size_t)st * S::kStage + S::kTile);
+#pragma unroll 1
+        for (int t = (warp - 12) * 32 + lane; t < TOK; t += 64) {
+          const uint32_t dst = smem_u32(vbuf + b * S::kV) + t * 128;
+          const bool none = tok0 + i * TOK + t >= ctx;  // slots past the context may hold codes that are not numbers
+#pragma unroll
+          for (int ch = 0; ch < D / 16; ++ch) {
+            const uint32_t at = D == 64 ? t * 64 + ((ch ^ (t >> 1 & 3)) << 4) : t * 128 + ((ch ^ (t & 7)) << 4);
+            uint4 w = lds128(src + at);
+            if (none) w = make_uint4(0u, 0u, 0u, 0u);
+            uint4 f[2];
+            codes_to_f16<FMT>(w.x, f[0].x, f[0].y);
+            codes_to_f16<FMT>(w.y, f[0].z, f[0].w);
+            codes_to_f16<FMT>(w.z, f[1].x, f[1].y);
+            codes_to_f16<FMT>(w.w, f[1].z, f[1].w);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int c8 = 2 * ch + k;  // 8-element chunk of the row
+              sts128(dst + (c8 >> 3) * TOK * 128 + (((c8 & 7) ^ (t & 7)) << 4), f[k]);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + st), mbar_arrive(v_full + b);
+        if (++st == stages) st = 0, pass ^= 1u;
+      }
+    } else if (warp == 14) {
+      // ------------------------------------------------ copies: `box` tokens of one block at a time
+      const int boxes = TOK / box;
+      auto look = [&](int i) {
+        const int tok = tok0 + i * TOK + lane * box;
+        int blk = -1;
+        if (i < n && lane < boxes && tok < ctx) {
+          blk = __ldg(a.table + (size_t)item.r * a.max_blocks + tok / a.bs);
+          if (blk < 0 || blk >= a.num_blocks) {
+            report_error(a.err, kErrKvBlock);
+            blk = -1;
+          }
+        }
+        return blk;
+      };
+      int next = look(0);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int blk = next;
+        next = look(i + 1);
+        if (gi + i >= stages && !wait_warp(empty + st, pass ^ 1u)) break;
+        if (lane == 0) mbar_arrive_expect_tx(full + st, S::kStage);
+        __syncwarp();
+        if (lane < boxes) {
+          // what is not there is read past the last page: zeros
+          const int page = blk >= 0 ? blk * a.Hkv + item.h : a.num_blocks * a.Hkv;
+          const int row = (tok0 + i * TOK + lane * box) % a.bs;
+          const uint32_t dst = smem_u32(ring + (size_t)st * S::kStage) + lane * box * D;
+          tma_load_3d(dst, &kmap, 0, row, page, full + st);
+          tma_load_3d(dst + S::kTile, &vmap, 0, row, page, full + st);
+        }
+        __syncwarp();
+        if (++st == stages) st = 0, pass ^= 1u;
+      }
+    } else if (warp == 15) {
+      // ------------------------------------------------ MMAs
+      if (lane == 0) {
+        const uint32_t is = tc_idesc(128, 16 * nch, false, false), io = tc_idesc(D, ROWS, true, true);
+        const uint32_t qs = smem_u32(qbuf);
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i <= n && ok; ++i) {
+          if (i < n) {
+            const int g = gi + i, b = g & 1;
+            ok = wait(k_full + b, (g >> 1) & 1) && (g < 2 || wait(s_empty + b, ((g >> 1) - 1) & 1));
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ts(tbase + S::kColS + b * ROWS, tbase + S::kColK + b * (D / 2) + 8 * k,
+                     tc_desc(qs + (k >> 2) * ROWS * 128 + (k & 3) * 32, 16, 1024), is, k > 0);
+            tc_commit(s_full + b);
+          }
+          if (i > 0) {
+            const int g = gi + i - 1, b = g & 1;
+            ok = wait(p_full + b, (g >> 1) & 1) && wait(v_full + b, (g >> 1) & 1);
+            if (!ok) break;
+            tc_after();
+            const uint32_t vs = smem_u32(vbuf + b * S::kV), ps = smem_u32(pbuf + b * S::kP);
+#pragma unroll
+            for (int k = 0; k < TOK / 16; ++k)
+              mma_ss(tbase + S::kColO, tc_desc(vs + k * 2048, TOK * 128, 1024), tc_desc(ps + k * 2048, TOK * 128, 1024), io,
+                     i > 1 || k > 0);
+            tc_commit(o_done + b);
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------ softmax: a token per thread, half of the rows
+      constexpr int HR = ROWS / 2;
+      const int t = quad * 32 + lane, half = role == 1 ? 0 : 1, bar = 1 + half;
+      // this half's columns: hch chunks of 16 from column hc on
+      const int hc = half ? 16 * ((nch + 1) / 2) : 0, hch = half ? nch / 2 : (nch + 1) / 2;
+      const uint32_t t_s = tlane + S::kColS + hc, t_o = tlane + S::kColO + hc;
+      float* nm_of = neg_m + hc;
+      float l[HR];
+#pragma unroll
+      for (int j = 0; j < HR; ++j) l[j] = 0.f;
+      // the token's block of steps ahead, its scales of one step ahead
+      auto look = [&](int i) {
+        const int tok = tok0 + i * TOK + t;
+        if (i >= n || tok >= ctx) return -1;
+        const int blk = __ldg(a.table + (size_t)item.r * a.max_blocks + tok / a.bs);
+        return blk < 0 || blk >= a.num_blocks ? -1 : blk;
+      };
+      auto scales_of = [&](int blk) {
+        return blk < 0 ? make_float2(0.f, -1.f)
+                       : __ldg(reinterpret_cast<const float2*>(a.scales) + (size_t)blk * a.Hkv + item.h);
+      };
+      float2 sc = scales_of(look(0));
+      int blk = look(1);
+      bool unset = true;  // some row has seen no token yet
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int g = gi + i, b = g & 1, tok = tok0 + i * TOK + t;
+        const float2 now = sc;
+        sc = scales_of(blk);
+        blk = look(i + 2);
+        const bool there = now.y >= 0.f || now.y != now.y;
+        const float vs = now.y < kMinScale ? kMinScale : now.y;
+        const float ks = now.x * up, lv = __log2f(vs), inv = __frcp_rn(vs);
+        const bool edge = __any_sync(0xffffffffu, !there || tok >= base);
+        // (After a wait that gave up every later one returns at once: the warps stay in step at their barriers.)
+        wait_warp(s_full + b, (g >> 1) & 1);
+        tc_after();
+        float y[HR];
+#pragma unroll
+        for (int ch = 0; ch < HR / 16; ++ch)
+          if (ch < hch) tmem_ld16(t_s + b * ROWS + 16 * ch, y + 16 * ch);
+#pragma unroll
+        for (int ch = 0; ch < HR / 16; ++ch)
+          if (ch < hch) tmem_wait_ld(y + 16 * ch);
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty + b);
+        bool grow = unset;
+#pragma unroll
+        for (int ch = 0; ch < HR / 16; ++ch) {
+          if (ch < hch) {
+#pragma unroll
+            for (int j = 16 * ch; j < 16 * ch + 16; j += 4) {
+              const float4 nm = *reinterpret_cast<const float4*>(nm_of + j);
+              y[j] = fmaf(y[j], ks, lv + nm.x);
+              y[j + 1] = fmaf(y[j + 1], ks, lv + nm.y);
+              y[j + 2] = fmaf(y[j + 2], ks, lv + nm.z);
+              y[j + 3] = fmaf(y[j + 3], ks, lv + nm.w);
+            }
+          }
+        }
+        if (edge) {
+          const unsigned d = (unsigned)(tok - base);
+#pragma unroll
+          for (int j = 0; j < HR; ++j) {
+            if (j / 16 < hch) {
+              const int2 lim = *reinterpret_cast<const int2*>(row_info + hc + j);
+              const bool seen = there && (tok < lim.x || (d < 32u && ((unsigned)lim.y >> d & 1u)));
+              if (!seen) y[j] = -INFINITY;
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < HR; j += 4)
+          if (j / 16 < hch) grow |= fmaxf(fmaxf(y[j], y[j + 1]), fmaxf(y[j + 2], y[j + 3])) > kSlack;
+        if (g >= 2) wait_warp(o_done + b, ((g >> 1) - 1) & 1);  // P of two steps ago has been read
+        if (named_barrier_or<128>(bar, grow)) {
+          // rows whose m has to rise (or to be set): the largest y over the step's tokens
+#pragma unroll
+          for (int j = 0; j < HR; ++j) {
+            if (j / 16 < hch) {
+              const int top = __reduce_max_sync(0xffffffffu, ordered(y[j]));
+              if (lane == 0) wmax[quad][hc + j] = top;
+            }
+          }
+          if (t == 0) unset_any[half] = 0u;
+          named_barrier<128>(bar);
+          if (t < 16 * hch) {
+            const int j = hc + t;
+            const float top = unordered(max(max(wmax[0][j], wmax[1][j]), max(wmax[2][j], wmax[3][j])));
+            const bool is_set = row_info[j].w != 0;
+            // a first maximum may be below 0, a later one only raises m
+            const float rise = top == -INFINITY ? 0.f : is_set ? fmaxf(top, 0.f) : top;
+            if (!is_set && top != -INFINITY) row_info[j].w = 1;
+            if (!is_set && top == -INFINITY) unset_any[half] = 1u;
+            fall[j] = rise;
+            neg_m[j] -= rise;
+          }
+          named_barrier<128>(bar);
+          unset = unset_any[half] != 0u;
+          if (i > 0) wait_warp(o_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+          tc_after();
+#pragma unroll
+          for (int ch = 0; ch < HR / 16; ++ch) {
+            if (ch < hch) {
+              float o[16];
+              if (i > 0) {
+                tmem_ld16(t_o + 16 * ch, o);
+                tmem_wait_ld(o);
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                // (r < 0 only where m is set for the first time: nothing has been summed yet)
+                const float r = fall[hc + 16 * ch + j], f = ex2(fminf(-r, 0.f));
+                y[16 * ch + j] -= r;
+                l[16 * ch + j] *= f;
+                if (i > 0) o[j] *= f;
+              }
+              if (i > 0) tmem_st16(t_o + 16 * ch, o);
+            }
+          }
+          if (i > 0) tmem_wait_st();
+          tc_before();
+        }
+        // p, its sum without the value scale, and as fp16 in shared memory (of a block of zero scale nothing)
+        const uint32_t dst = smem_u32(pbuf + b * S::kP) + t * 128;
+        const bool zero = now.y == 0.f;
+#pragma unroll
+        for (int c8 = 0; c8 < HR / 8; ++c8) {
+          if (c8 / 2 < hch) {
+            uint32_t f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int j = 8 * c8 + 2 * k;
+              const float e0 = ex2(y[j]), e1 = ex2(y[j + 1]);
+              l[j] = fmaf(e0, inv, l[j]);
+              l[j + 1] = fmaf(e1, inv, l[j + 1]);
+              f[k] = zero ? 0u : f16x2(e0, e1);
+            }
+            sts128(dst + (((c8 + hc / 8) ^ (t & 7)) << 4), make_uint4(f[0], f[1], f[2], f[3]));
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + b);
+      }
+      // the rows' sums over the tokens: per warp, then over the warps
+      {
+        const float x = transposed_warp_sum<HR>(l, lane);
+        const int j = transposed_row<HR>(lane);
+        if (j < 16 * hch) wsum[quad][hc + j] = x;
+      }
+      named_barrier<128>(bar);
+      if (t < 16 * hch) sums[hc + t] = (wsum[0][hc + t] + wsum[1][hc + t]) + (wsum[2][hc + t] + wsum[3][hc + t]);
+      named_barrier<128>(bar);
+      // ---- the segment's results ----
+      const int g = gi + n - 1;
+      if (wait_warp(o_done + (g & 1), (g >> 1) & 1)) {
+        tc_after();
+        const bool whole = item_first >= share.c0 && item_first + item.steps <= share.c1;
+        const int d = D == 128 ? t : quad * 16 + lane;  // D = 64: 16 lanes of each quadrant
+        const bool has = D == 128 || lane < 16;
+        uint8_t* piece = static_cast<uint8_t*>(a.ws) + kAttnCounterBytes +
+                         (size_t)(2 * blockIdx.x + (item_first < share.c0 ? 0 : 1)) * attn_piece_bytes(ROWS, D);
+#pragma unroll 1
+        for (int ch = 0; ch < hch; ++ch) {
+          float o[16];
+          tmem_ld16(t_o + 16 * ch, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int rr = hc + 16 * ch + j, to = row_info[rr].z;
+            if (has && to >= 0) {
+              if (whole) {
+                const float L = sums[rr];
+                const uint32_t v = f32_to_bf16x2(L == 0.f ? 0.f : o[j] * __frcp_rn(L), 0.f);
+                a.out[(size_t)to * D + d] = (uint16_t)v;
+              } else {
+                reinterpret_cast<float*>(piece)[rr * D + d] = o[j];
+              }
+            }
+          }
+        }
+        if (!whole && t < 16 * hch)
+          reinterpret_cast<float2*>(piece + (size_t)ROWS * D * 4)[hc + t] =
+              make_float2(sums[hc + t] > 0.f ? -neg_m[hc + t] : kNoMax, sums[hc + t]);
+        tc_before();
+      }
+    }
+    // ---- end of the segment: all warps ----
+    __threadfence();
+    __syncthreads();
+    if (abort_flag) break;
+    if (!(item_first >= share.c0 && item_first + item.steps <= share.c1)) {
+      // the CTA that brings an item's last piece adds the pieces up, in the order of the CTAs
+      const int f = attn_cta_of<TOK>(batch, share, item_first),
+                e = attn_cta_of<TOK>(batch, share, item_first + item.steps - 1), pieces = e - f + 1;
+      unsigned* count = static_cast<unsigned*>(a.ws) + f;
+      if (tid == 0) {
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(arrived) : "l"(count) : "memory");
+        if (arrived == (unsigned)(e - f)) *count = 0u;  // the next call finds it as this one did
+      }
+      __syncthreads();
+      if (arrived == (unsigned)(e - f)) {
+        __threadfence();
+        const uint8_t* ws = static_cast<const uint8_t*>(a.ws) + kAttnCounterBytes;
+        auto piece = [&](int i) {
+          return ws + (size_t)(2 * (f + i) + (i == 0 ? 1 : 0)) * attn_piece_bytes(ROWS, D);
+        };
+        float* factor = reinterpret_cast<float*>(pbuf);  // [pieces][ROWS]: P and q are done with
+        static_assert(2 * S::kP + S::kQ >= kTcMaxCtas * ROWS * 4, "the factors fit");
+#pragma unroll 1
+        for (int rr = warp; rr < rows; rr += kTcThreads / 32) {
+          float mm = kNoMax, ll = 0.f;
+#pragma unroll 1
+          for (int i = lane; i < pieces; i += 32)
+            mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr).x);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+#pragma unroll 1
+          for (int i = lane; i < pieces; i += 32) {
+            const float2 st = __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr);
+            const float x = ex2(st.x - mm);
+            factor[i * ROWS + rr] = x;
+            ll = fmaf(st.y, x, ll);
+          }
+          ll = warp_sum(ll);
+          if (lane == 0) sums[rr] = ll;
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int x = tid; x < rows * (D / 4); x += kTcThreads) {
+          const int rr = x / (D / 4), d = x % (D / 4) * 4;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int i = 0; i < pieces; ++i) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(i)) + x);
+            const float fa = factor[i * ROWS + rr];
+            o.x = fmaf(v.x, fa, o.x), o.y = fmaf(v.y, fa, o.y), o.z = fmaf(v.z, fa, o.z), o.w = fmaf(v.w, fa, o.w);
+          }
+          const float L = sums[rr], r = L == 0.f ? 0.f : __frcp_rn(L);
+          *reinterpret_cast<uint2*>(a.out + (size_t)row_info[rr].z * D + d) =
+              make_uint2(f32_to_bf16x2(o.x * r, o.y * r), f32_to_bf16x2(o.z * r, o.w * r));
+        }
+      }
+      __syncthreads();
+    }
+    gi += n;
+    step = seg_end;
+  }
+  // After a wait that gave up: what is still in flight lands before the memory is given back (bounded waits).
+  if (abort_flag) {
+    if (warp == 14 && lane == 0)
+      for (int i = 0; i < stages; ++i)
+        for (int ph = 0; ph < 2; ++ph) mbar_wait_n(full + i, ph, nullptr, 0, 1u << 14);
+    if (warp == 15 && lane == 0) {
+      tc_commit(o_done);
+      for (int ph = 0; ph < 2; ++ph) mbar_wait_n(o_done, ph, nullptr, 0, 1u << 14);
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 15) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTcCols));
+  }
+}
+
+template <int D, int FMT>
+cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream, bool pdl) {
+  using S = TcShape<D>;
+  CUtensorMap km, vm;
+  const auto sw = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  // tokens of a copy: the largest part of a step that lies in one block whatever its start
+  const int box = a.bs % 128 == 0 ? 128 : a.bs % 64 == 0 ? 64 : a.bs % 32 == 0 ? 32 : 16;
+  for (int i = 0; i < 2; ++i)
+    if (!tmap_3d(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? a.v_cache : a.k_cache, D, a.bs,
+                 (uint64_t)a.num_blocks * a.Hkv, D, (uint64_t)a.bs * D, D, box, 1, sw))
+      return cudaErrorInvalidValue;
+  auto k = attn_kv8_tc_kernel<D, FMT>;
+  cudaError_t e = allow_max_smem(k);
+  if (e != cudaSuccess) return e;
+  const size_t fixed = 2 * S::kV + 2 * S::kP + S::kQ + 16 * ((size_t)a.R + 1);
+  // three stages; two where the tables of more than 800 requests leave no room
+  const int stages = (int)std::min<size_t>(D == 64 ? 4 : 3, ((size_t)device_max_smem_optin() - 6144 - fixed) / S::kStage);
+  const size_t smem = fixed + stages * S::kStage;
+  return launch_kernel(k, dim3(std::min(device_sm_count(), kTcMaxCtas)), dim3(kTcThreads), smem, stream, pdl, km, vm, a,
+                       box, stages);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_kv8_tc(const AttnArgs& a, int format, cudaStream_t stream, bool pdl) {
+  if (a.D == 64)
+    return format == QG_KV_I8 ? launch_tc<64, QG_KV_I8>(a, stream, pdl) : launch_tc<64, QG_KV_E4M3>(a, stream, pdl);
+  return format == QG_KV_I8 ? launch_tc<128, QG_KV_I8>(a, stream, pdl) : launch_tc<128, QG_KV_E4M3>(a, stream, pdl);
+}
+
+}  // namespace qg
