@@ -21,7 +21,7 @@
 // half of the rows each, 12 and 13 convert values, 14 issues the copies, 15 the
 // MMAs (16 warps are what leaves a thread 128 registers). Steps run through two buffers of every kind; S of step i + 1 is
 // issued before O of step i. Shares of the batch, split contexts and the joining
-// of their pieces are those of attn_kv8.cu, with all warps adding pieces up.
+// their pieces are those of attn_kv8.cu; the pieces are joined by a second kernel.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -143,6 +143,12 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ (i
 
 constexpr int kTcMaxStages = 4;
 
+// one entry per CTA, behind the counters of attn_kv8.cu's pieces
+__device__ __forceinline__ int4* tc_splits(void* ws) {
+  return reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kMaxCtas * 4);
+}
+static_assert(kMaxCtas * 4 + kTcMaxCtas * 16 <= kAttnCounterBytes, "");
+
 // the rest of a wait that did not succeed at once; gives up when another role has
 __device__ __noinline__ bool tc_wait_on(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* err) {
 #pragma unroll 1
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ uint64_t full[kTcMaxStages], empty[kTcMaxStages], k_full[2], s_full[2], s_empty[2], p_full[2], v_full[2], o_done[2];
   __shared__ int2 scan_part[kTcThreads / 32];
   __shared__ uint32_t tmem_base;
-  __shared__ unsigned arrived, amax_bits, unset_any[2];
+  __shared__ unsigned amax_bits, unset_any[2];
   __shared__ volatile uint32_t abort_flag;
 
   if (tid == 0) {
@@ -214,6 +220,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // the same by a whole warp, which goes on together
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
+  int4 split = make_int4(0, 0, 0, 0);  // pieces | rows << 16, first query token, head, row tile
   int gi = 0;  // steps of the CTA's earlier segments: buffer gi & 1
   int st = 0;  // ring stage of a role's next step, and the parity of its passes through the ring
   uint32_t pass = 0;
@@ -351,10 +358,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int blk = -1;
         if (i < n && lane < boxes && tok < ctx) {
           blk = __ldg(a.table + (size_t)item.r * a.max_blocks + tok / a.bs);
-          if (blk < 0 || blk >= a.num_blocks) {
-            report_error(a.err, kErrKvBlock);
-            blk = -1;
-          }
+          if (blk < 0) blk = a.num_blocks;  // bad
         }
         return blk;
       };
@@ -367,8 +371,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(full + st, S::kStage);
         __syncwarp();
         if (lane < boxes) {
+          if (blk >= a.num_blocks) report_error(a.err, kErrKvBlock);
           // what is not there is read past the last page: zeros
-          const int page = blk >= 0 ? blk * a.Hkv + item.h : a.num_blocks * a.Hkv;
+          const int page = blk >= 0 && blk < a.num_blocks ? blk * a.Hkv + item.h : a.num_blocks * a.Hkv;
           const int row = (tok0 + i * TOK + lane * box) % a.bs;
           const uint32_t dst = smem_u32(ring + (size_t)st * S::kStage) + lane * box * D;
           tma_load_3d(dst, &kmap, 0, row, page, full + st);
@@ -426,11 +431,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto look = [&](int i) {
         const int tok = tok0 + i * TOK + t;
         if (i >= n || tok >= ctx) return -1;
-        const int blk = __ldg(a.table + (size_t)item.r * a.max_blocks + tok / a.bs);
-        return blk < 0 || blk >= a.num_blocks ? -1 : blk;
+        return __ldg(a.table + (size_t)item.r * a.max_blocks + tok / a.bs);
       };
       auto scales_of = [&](int blk) {
-        return blk < 0 ? make_float2(0.f, -1.f)
+        return blk < 0 || blk >= a.num_blocks ? make_float2(0.f, -1.f)
                        : __ldg(reinterpret_cast<const float2*>(a.scales) + (size_t)blk * a.Hkv + item.h);
       };
       float2 sc = scales_of(look(0));
@@ -602,66 +606,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     // ---- end of the segment: all warps ----
-    __threadfence();
     __syncthreads();
     if (abort_flag) break;
-    if (!(item_first >= share.c0 && item_first + item.steps <= share.c1)) {
-      // the CTA that brings an item's last piece adds the pieces up, in the order of the CTAs
-      const int f = attn_cta_of<TOK>(batch, share, item_first),
-                e = attn_cta_of<TOK>(batch, share, item_first + item.steps - 1), pieces = e - f + 1;
-      unsigned* count = static_cast<unsigned*>(a.ws) + f;
-      if (tid == 0) {
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(arrived) : "l"(count) : "memory");
-        if (arrived == (unsigned)(e - f)) *count = 0u;  // the next call finds it as this one did
-      }
-      __syncthreads();
-      if (arrived == (unsigned)(e - f)) {
-        __threadfence();
-        const uint8_t* ws = static_cast<const uint8_t*>(a.ws) + kAttnCounterBytes;
-        auto piece = [&](int i) {
-          return ws + (size_t)(2 * (f + i) + (i == 0 ? 1 : 0)) * attn_piece_bytes(ROWS, D);
-        };
-        float* factor = reinterpret_cast<float*>(pbuf);  // [pieces][ROWS]: P and q are done with
-        static_assert(2 * S::kP + S::kQ >= kTcMaxCtas * ROWS * 4, "the factors fit");
-#pragma unroll 1
-        for (int rr = warp; rr < rows; rr += kTcThreads / 32) {
-          float mm = kNoMax, ll = 0.f;
-#pragma unroll 1
-          for (int i = lane; i < pieces; i += 32)
-            mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr).x);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-#pragma unroll 1
-          for (int i = lane; i < pieces; i += 32) {
-            const float2 st = __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr);
-            const float x = ex2(st.x - mm);
-            factor[i * ROWS + rr] = x;
-            ll = fmaf(st.y, x, ll);
-          }
-          ll = warp_sum(ll);
-          if (lane == 0) sums[rr] = ll;
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int x = tid; x < rows * (D / 4); x += kTcThreads) {
-          const int rr = x / (D / 4), d = x % (D / 4) * 4;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int i = 0; i < pieces; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(i)) + x);
-            const float fa = factor[i * ROWS + rr];
-            o.x = fmaf(v.x, fa, o.x), o.y = fmaf(v.y, fa, o.y), o.z = fmaf(v.z, fa, o.z), o.w = fmaf(v.w, fa, o.w);
-          }
-          const float L = sums[rr], r = L == 0.f ? 0.f : __frcp_rn(L);
-          *reinterpret_cast<uint2*>(a.out + (size_t)row_info[rr].z * D + d) =
-              make_uint2(f32_to_bf16x2(o.x * r, o.y * r), f32_to_bf16x2(o.z * r, o.w * r));
-        }
-      }
-      __syncthreads();
+    if (tid == 0 && item_first >= share.c0 && item_first + item.steps > share.c1) {
+      // the item goes on in other shares: their pieces are joined by attn_kv8_join_kernel
+      const int e = attn_cta_of<TOK>(batch, share, item_first + item.steps - 1);
+      split = make_int4((e - (int)blockIdx.x + 1) | rows << 16, q0, item.h, item.rt);
     }
     gi += n;
     step = seg_end;
   }
+  if (tid == 0) tc_splits(a.ws)[blockIdx.x] = abort_flag ? make_int4(0, 0, 0, 0) : split;
   // After a wait that gave up: what is still in flight lands before the memory is given back (bounded waits).
   if (abort_flag) {
     if (warp == 14 && lane == 0)
@@ -679,6 +634,57 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTcCols));
   }
+}
+
+// Adds up the pieces of the items that go over several CTAs' shares, in the order
+// of the CTAs. CTA (b, y): 16 rows of the item that begins in CTA b's share and
+// goes on after it. One CTA adding up an item's 64 rows from 19 pieces took
+// 30 us of 61; here every SM takes part, after the kernel's end.
+constexpr int kJoinRows = 16;
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * D / 4) attn_kv8_join_kernel(AttnArgs a) {
+  __shared__ float factor[kTcMaxCtas][kJoinRows], sums[kJoinRows];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 split = tc_splits(a.ws)[blockIdx.x];
+  const int pieces = split.x & 0xFFFF, r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, (split.x >> 16) - r0);
+  if (pieces < 2 || rows <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.Hq / a.Hkv;
+  const uint8_t* ws = static_cast<const uint8_t*>(a.ws) + kAttnCounterBytes;
+  auto piece = [&](int i) {
+    return ws + (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * attn_piece_bytes(kTcRows, D);
+  };
+#pragma unroll 1
+  for (int rr = warp; rr < rows; rr += kJoinRows * D / 128) {
+    float mm = kNoMax, ll = 0.f;
+    for (int i = lane; i < pieces; i += 32)
+      mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)kTcRows * D * 4) + r0 + rr).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    for (int i = lane; i < pieces; i += 32) {
+      const float2 st = __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)kTcRows * D * 4) + r0 + rr);
+      const float x = ex2(st.x - mm);
+      factor[i][rr] = x;
+      ll = fmaf(st.y, x, ll);
+    }
+    ll = warp_sum(ll);
+    if (lane == 0) sums[rr] = ll;
+  }
+  const int rr = tid / (D / 4), d = tid % (D / 4) * 4;
+  __syncthreads();
+  if (rr >= rows) return;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < pieces; ++i) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(i)) + (r0 + rr) * (D / 4) + d / 4);
+    const float fa = factor[i][rr];
+    o.x = fmaf(v.x, fa, o.x), o.y = fmaf(v.y, fa, o.y), o.z = fmaf(v.z, fa, o.z), o.w = fmaf(v.w, fa, o.w);
+  }
+  const float L = sums[rr], r = L == 0.f ? 0.f : __frcp_rn(L);
+  const int rho = split.w * kTcRows + r0 + rr, qi = rho / G;
+  const size_t to = (size_t)(split.y + qi) * a.Hq + split.z * G + rho - qi * G;
+  *reinterpret_cast<uint2*>(a.out + to * D + d) =
+      make_uint2(f32_to_bf16x2(o.x * r, o.y * r), f32_to_bf16x2(o.z * r, o.w * r));
 }
 
 template <int D, int FMT>
@@ -699,8 +705,11 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   // three stages; two where the tables of more than 800 requests leave no room
   const int stages = (int)std::min<size_t>(D == 64 ? 4 : 3, ((size_t)device_max_smem_optin() - 6144 - fixed) / S::kStage);
   const size_t smem = fixed + stages * S::kStage;
-  return launch_kernel(k, dim3(std::min(device_sm_count(), kTcMaxCtas)), dim3(kTcThreads), smem, stream, pdl, km, vm, a,
-                       box, stages);
+  const int ctas = std::min(device_sm_count(), kTcMaxCtas);
+  e = launch_kernel(k, dim3(ctas), dim3(kTcThreads), smem, stream, pdl, km, vm, a, box, stages);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(attn_kv8_join_kernel<D>, dim3(ctas, kTcRows / kJoinRows), dim3(kJoinRows * D / 4), 0, stream, true,
+                       a);
 }
 
 }  // namespace
