@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ __align__(16) float wsum[4][ROWS];
   __shared__ int wmax[4][ROWS];
   __shared__ int4 row_info[ROWS];  // tokens below .x are seen, and draft tokens by .y's bits; .z: output row or -1
-  __shared__ uint64_t full[kTcMaxStages], empty[kTcMaxStages], k_full[2], s_full[2], s_empty[2], p_full[2], v_full[2], o_done[2];
+  __shared__ uint64_t full[kTcMaxStages], empty[kTcMaxStages], k_full[2], s_full[2], s_empty[2], p_full[2], v_full[2], o_done[2], q_full;
   __shared__ int2 scan_part[kTcThreads / 32];
   __shared__ uint32_t tmem_base;
   __shared__ unsigned amax_bits, unset_any[2];
@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(v_full + i, 2);
       mbar_init(o_done + i, 1);
     }
+    mbar_init(&q_full, 8);
     abort_flag = 0u;
     fence_mbar_init();
   }
@@ -220,79 +221,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // the same by a whole warp, which goes on together
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
+  // A segment: the steps of one item in this CTA's share. Every role walks the segments by itself; buffers and
+  // barriers run on from one to the next (step g of the CTA: buffer g & 1), so the keys and values of a segment are
+  // converted while the last one's results are written.
+  struct Segment {
+    AttnPlace item;
+    int n, g, ctx, q0, nq, base, rows, nch, tok0, item_first, index;  // nch: 16 nch columns are in use
+  };
+  auto first_segment = [&]() {
+    Segment s;
+    s.n = s.g = 0;
+    s.index = -1;
+    return s;
+  };
+  auto next_segment = [&](Segment& s, int& step) {
+    step += s.n;
+    if (step >= share.c1) return false;
+    s.g += s.n;
+    ++s.index;
+    s.item = attn_locate<ROWS, TOK>(batch, step);
+    s.item_first = step - s.item.s;
+    s.n = min(share.c1, s.item_first + s.item.steps) - step;
+    s.ctx = ctxs[s.item.r];
+    s.q0 = cus[s.item.r];
+    s.nq = cus[s.item.r + 1] - s.q0;
+    s.base = s.ctx - s.nq;
+    s.rows = min(ROWS, s.nq * batch.G - s.item.rt * ROWS);
+    s.nch = (s.rows + 15) / 16;
+    s.tok0 = s.item.s * TOK;
+    return true;
+  };
   int4 split = make_int4(0, 0, 0, 0);  // pieces | rows << 16, first query token, head, row tile
-  int gi = 0;  // steps of the CTA's earlier segments: buffer gi & 1
   int st = 0;  // ring stage of a role's next step, and the parity of its passes through the ring
   uint32_t pass = 0;
+  int step = share.c0;
+  Segment sg = first_segment();
+  if (role == 0) {
+    // ------------------------------------------------ keys: a token's row per thread, fp16 into TMEM
+    const int t = quad * 32 + lane;
+    bool ok = true;
+    while (ok && next_segment(sg, step)) {
 #pragma unroll 1
-  for (int step = share.c0; step < share.c1;) {
-    const AttnPlace item = attn_locate<ROWS, TOK>(batch, step);
-    const int item_first = step - item.s, seg_end = min(share.c1, item_first + item.steps), n = seg_end - step;
-    const int ctx = ctxs[item.r], q0 = cus[item.r], nq = cus[item.r + 1] - q0, base = ctx - nq;
-    const int rows = min(ROWS, nq * batch.G - item.rt * ROWS), nch = (rows + 15) / 16;  // columns in use: 16 nch
-    const int tok0 = item.s * TOK;
-    // ---- the item's queries: 2^-sigma q in fp16 with one sigma for the item (its largest |q| just below 2^15;
-    // what a row 2^20 smaller loses is 2^-40 of the largest scores), K-major, swizzled ----
-    if (tid == 0) amax_bits = 0u;
-    if (tid < ROWS) {
-      const int rho = item.rt * ROWS + tid;
-      int4 info = make_int4(0x7FFFFFFF, 0, -1, 0);
-      if (tid < rows) {
-        const int i = rho / batch.G;
-        const bool tree = a.tree && nq <= 32;
-        info.x = tree ? base : base + i + 1;
-        if (tree) info.y = (int)(a.tree[q0 + i] & (0xFFFFFFFFu >> (32 - nq)));
-        info.z = (q0 + i) * a.Hq + item.h * batch.G + rho - i * batch.G;
-      }
-      row_info[tid] = info;
-      neg_m[tid] = 0.f;
-    }
-    __syncthreads();
-    {
-      constexpr int kPer = D / 8;  // threads of a row: 8 elements each, 512 / kPer rows at a time
-      constexpr int kUse = 512, kTimes = ROWS * kPer / kUse;  // threads that take part
-      uint4 raw[kTimes];
-      float amax = 0.f;
-#pragma unroll
-      for (int k = 0; k < kTimes; ++k) {
-        const int rr = (tid + k * kUse) / kPer % ROWS, ch = tid % kPer, to = tid < kUse ? row_info[rr].z : -1;
-        raw[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (to >= 0)
-          raw[k] = *reinterpret_cast<const uint4*>(a.q + (size_t)(to / a.Hq) * a.q_stride + (size_t)(to % a.Hq) * D + 8 * ch);
-        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
-      }
-      const unsigned wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-      if (lane == 0) atomicMax(&amax_bits, wm);
-      __syncthreads();
-      const float down = pow2f(-fp16_prescale_exp(__uint_as_float(amax_bits)));
-#pragma unroll
-      for (int k = 0; k < kTimes; ++k) {
-        const int rr = (tid + k * kUse) / kPer, ch = tid % kPer;
-        if (tid >= kUse) break;
-        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-        uint32_t f[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          f[j] = f16x2(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
-        sts128(smem_u32(qbuf) + (ch >> 3) * ROWS * 128 + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
-               make_uint4(f[0], f[1], f[2], f[3]));
-      }
-      fence_async_smem();
-    }
-    __syncthreads();
-    const float up = a.scale_log2 * pow2f(fp16_prescale_exp(__uint_as_float(amax_bits)));
-
-    if (role == 0) {
-      // ------------------------------------------------ keys: a token's row per thread, fp16 into TMEM
-      const int t = quad * 32 + lane;
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int g = gi + i, b = g & 1;
-        if (!wait_warp(full + st, pass)) break;
-        if (g >= 2 && !wait_warp(s_full + b, ((g >> 1) - 1) & 1)) break;  // S of two steps ago has read the buffer
+      for (int i = 0; i < sg.n; ++i) {
+        const int g = sg.g + i, b = g & 1;
+        ok = wait_warp(full + st, pass) && (g < 2 || wait_warp(s_full + b, ((g >> 1) - 1) & 1));
+        if (!ok) break;  // S of two steps ago has read the buffer
         tc_after();
         const uint32_t src = smem_u32(ring + (size_t)st * S::kStage);
 #pragma unroll
@@ -316,18 +289,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(empty + st), mbar_arrive(k_full + b);
         if (++st == stages) st = 0, pass ^= 1u;
       }
-    } else if (warp == 12 || warp == 13) {
-      // ------------------------------------------------ values: two tokens' rows per thread, fp16 into shared memory
+    }
+  } else if (warp == 12 || warp == 13) {
+    // ------------------------------------------------ values: two tokens' rows per thread, fp16 into shared memory
+    bool ok = true;
+    while (ok && next_segment(sg, step)) {
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int g = gi + i, b = g & 1;
-        if (!wait_warp(full + st, pass)) break;
-        if (g >= 2 && !wait_warp(o_done + b, ((g >> 1) - 1) & 1)) break;
+      for (int i = 0; i < sg.n; ++i) {
+        const int g = sg.g + i, b = g & 1;
+        ok = wait_warp(full + st, pass) && (g < 2 || wait_warp(o_done + b, ((g >> 1) - 1) & 1));
+        if (!ok) break;
         const uint32_t src = smem_u32(ring + (size_t)st * S::kStage + S::kTile);
 #pragma unroll 1
         for (int t = (warp - 12) * 32 + lane; t < TOK; t += 64) {
           const uint32_t dst = smem_u32(vbuf + b * S::kV) + t * 128;
-          const bool none = tok0 + i * TOK + t >= ctx;  // slots past the context may hold codes that are not numbers
+          const bool none = sg.tok0 + i * TOK + t >= sg.ctx;  // slots past the context may hold codes that are not numbers
 #pragma unroll
           for (int ch = 0; ch < D / 16; ++ch) {
             const uint32_t at = D == 64 ? t * 64 + ((ch ^ (t >> 1 & 3)) << 4) : t * 128 + ((ch ^ (t & 7)) << 4);
@@ -350,31 +326,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(empty + st), mbar_arrive(v_full + b);
         if (++st == stages) st = 0, pass ^= 1u;
       }
-    } else if (warp == 14) {
-      // ------------------------------------------------ copies: `box` tokens of one block at a time
-      const int boxes = TOK / box;
+    }
+  } else if (warp == 14) {
+    // ------------------------------------------------ copies: `box` tokens of one block at a time
+    const int boxes = TOK / box;
+    bool ok = true;
+    while (ok && next_segment(sg, step)) {
       auto look = [&](int i) {
-        const int tok = tok0 + i * TOK + lane * box;
+        const int tok = sg.tok0 + i * TOK + lane * box;
         int blk = -1;
-        if (i < n && lane < boxes && tok < ctx) {
-          blk = __ldg(a.table + (size_t)item.r * a.max_blocks + tok / a.bs);
+        if (i < sg.n && lane < boxes && tok < sg.ctx) {
+          blk = __ldg(a.table + (size_t)sg.item.r * a.max_blocks + tok / a.bs);
           if (blk < 0) blk = a.num_blocks;  // bad
         }
         return blk;
       };
       int next = look(0);
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0; i < sg.n; ++i) {
         const int blk = next;
         next = look(i + 1);
-        if (gi + i >= stages && !wait_warp(empty + st, pass ^ 1u)) break;
+        ok = sg.g + i < stages || wait_warp(empty + st, pass ^ 1u);
+        if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(full + st, S::kStage);
         __syncwarp();
         if (lane < boxes) {
           if (blk >= a.num_blocks) report_error(a.err, kErrKvBlock);
           // what is not there is read past the last page: zeros
-          const int page = blk >= 0 && blk < a.num_blocks ? blk * a.Hkv + item.h : a.num_blocks * a.Hkv;
-          const int row = (tok0 + i * TOK + lane * box) % a.bs;
+          const int page = blk >= 0 && blk < a.num_blocks ? blk * a.Hkv + sg.item.h : a.num_blocks * a.Hkv;
+          const int row = (sg.tok0 + i * TOK + lane * box) % a.bs;
           const uint32_t dst = smem_u32(ring + (size_t)st * S::kStage) + lane * box * D;
           tma_load_3d(dst, &kmap, 0, row, page, full + st);
           tma_load_3d(dst + S::kTile, &vmap, 0, row, page, full + st);
@@ -382,12 +362,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (++st == stages) st = 0, pass ^= 1u;
       }
-    } else if (warp == 15) {
-      // ------------------------------------------------ MMAs
-      if (lane == 0) {
-        const uint32_t is = tc_idesc(128, 16 * nch, false, false), io = tc_idesc(D, ROWS, true, true);
-        const uint32_t qs = smem_u32(qbuf);
-        bool ok = true;
+    }
+  } else if (warp == 15) {
+    // ------------------------------------------------ MMAs
+    if (lane == 0) {
+      const uint32_t qs = smem_u32(qbuf), io = tc_idesc(D, ROWS, true, true);
+      bool ok = true;
+      while (ok && next_segment(sg, step)) {
+        const uint32_t is = tc_idesc(128, 16 * sg.nch, false, false);
+        const int n = sg.n, gi = sg.g;
+        ok = wait(&q_full, sg.index & 1);
 #pragma unroll 1
         for (int i = 0; i <= n && ok; ++i) {
           if (i < n) {
@@ -415,11 +399,76 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
-      __syncwarp();
-    } else {
-      // ------------------------------------------------ softmax: a token per thread, half of the rows
-      constexpr int HR = ROWS / 2;
-      const int t = quad * 32 + lane, half = role == 1 ? 0 : 1, bar = 1 + half;
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ softmax: a token per thread, half of the rows
+    constexpr int HR = ROWS / 2;
+    const int t = quad * 32 + lane, half = role == 1 ? 0 : 1, bar = 1 + half;
+    while (next_segment(sg, step)) {
+      const AttnPlace item = sg.item;
+      const int n = sg.n, gi = sg.g, ctx = sg.ctx, base = sg.base, tok0 = sg.tok0, nch = sg.nch, rows = sg.rows;
+      // The item's queries: 2^-sigma q in fp16 with one sigma for the item (its largest |q| just below 2^15; what a
+      // row 2^20 smaller loses is 2^-40 of the largest scores), K-major, swizzled. (The last segment's products have
+      // been waited for.)
+      const int u = half * 128 + t;
+      if (u == 0) amax_bits = 0u;
+      if (u < ROWS) {
+        const int rho = item.rt * ROWS + u;
+        int4 info = make_int4(0x7FFFFFFF, 0, -1, 0);
+        if (u < rows) {
+          const int i = rho / batch.G;
+          const bool tree = a.tree && sg.nq <= 32;
+          info.x = tree ? base : base + i + 1;
+          if (tree) info.y = (int)(a.tree[sg.q0 + i] & (0xFFFFFFFFu >> (32 - sg.nq)));
+          info.z = (sg.q0 + i) * a.Hq + item.h * batch.G + rho - i * batch.G;
+        }
+        row_info[u] = info;
+        neg_m[u] = 0.f;
+      }
+      named_barrier<256>(3);
+      float up;
+      {
+        constexpr int kPer = D / 8, kTimes = ROWS * kPer / 256;  // threads of a row: 8 elements each
+        uint4 raw[kTimes];
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < kTimes; ++k) {
+          const int rr = (u + k * 256) / kPer, ch = u % kPer, to = row_info[rr].z;
+          raw[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (to >= 0) {
+            const int tq = to / a.Hq;
+            raw[k] = *reinterpret_cast<const uint4*>(a.q + (size_t)tq * a.q_stride + (size_t)(to - tq * a.Hq) * D + 8 * ch);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kTimes; ++k) {
+          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+        }
+        const unsigned wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+        if (lane == 0) atomicMax(&amax_bits, wm);
+        named_barrier<256>(3);
+        const int sigma = fp16_prescale_exp(__uint_as_float(amax_bits));
+        const float down = pow2f(-sigma);
+        up = a.scale_log2 * pow2f(sigma);
+#pragma unroll
+        for (int k = 0; k < kTimes; ++k) {
+          const int rr = (u + k * 256) / kPer, ch = u % kPer;
+          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            f[j] = f16x2(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
+          sts128(smem_u32(qbuf) + (ch >> 3) * ROWS * 128 + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                 make_uint4(f[0], f[1], f[2], f[3]));
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
       // this half's columns: hch chunks of 16 from column hc on
       const int hc = half ? 16 * ((nch + 1) / 2) : 0, hch = half ? nch / 2 : (nch + 1) / 2;
       const uint32_t t_s = tlane + S::kColS + hc, t_o = tlane + S::kColO + hc;
@@ -575,6 +624,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int g = gi + n - 1;
       if (wait_warp(o_done + (g & 1), (g >> 1) & 1)) {
         tc_after();
+        const int item_first = sg.item_first;
         const bool whole = item_first >= share.c0 && item_first + item.steps <= share.c1;
         const int d = D == 128 ? t : quad * 16 + lane;  // D = 64: 16 lanes of each quadrant
         const bool has = D == 128 || lane < 16;
@@ -604,20 +654,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               make_float2(sums[hc + t] > 0.f ? -neg_m[hc + t] : kNoMax, sums[hc + t]);
         tc_before();
       }
+      const int item_first = sg.item_first;
+      if (u == 0 && item_first >= share.c0 && item_first + item.steps > share.c1) {
+        // the item goes on in other shares: their pieces are joined by attn_kv8_join_kernel
+        const int e = attn_cta_of<TOK>(batch, share, item_first + item.steps - 1);
+        split = make_int4((e - (int)blockIdx.x + 1) | rows << 16, sg.q0, item.h, item.rt);
+      }
+      named_barrier<256>(3);  // both halves are done with the tables of this segment
     }
-    // ---- end of the segment: all warps ----
-    __syncthreads();
-    if (abort_flag) break;
-    if (tid == 0 && item_first >= share.c0 && item_first + item.steps > share.c1) {
-      // the item goes on in other shares: their pieces are joined by attn_kv8_join_kernel
-      const int e = attn_cta_of<TOK>(batch, share, item_first + item.steps - 1);
-      split = make_int4((e - (int)blockIdx.x + 1) | rows << 16, q0, item.h, item.rt);
-    }
-    gi += n;
-    step = seg_end;
+    if (tid == 128) tc_splits(a.ws)[blockIdx.x] = abort_flag ? make_int4(0, 0, 0, 0) : split;
   }
-  if (tid == 0) tc_splits(a.ws)[blockIdx.x] = abort_flag ? make_int4(0, 0, 0, 0) : split;
   // After a wait that gave up: what is still in flight lands before the memory is given back (bounded waits).
+  __syncthreads();
   if (abort_flag) {
     if (warp == 14 && lane == 0)
       for (int i = 0; i < stages; ++i)
