@@ -122,6 +122,9 @@ __global__ void __launch_bounds__(32 * kPlainWarps) attn_kv8_plain_kernel(AttnAr
 // ---------------------------------------------------------------------------
 // The tensor-core kernel: D = 64, 128 or 256
 // ---------------------------------------------------------------------------
+constexpr int kItemCost = 3;
+constexpr int kWholeSteps = 6;  // joining the pieces takes longer (4 us)
+
 template <int D, int NT, int FMT>
 struct AttnShape {
   static constexpr int kWarps = 8;
@@ -190,6 +193,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
                     int stages, uint32_t ring_offset, int wide) {
   using S = AttnShape<D, NT, FMT>;
   constexpr int NW = S::kWarps, ROWS = S::kRows, UPS = S::kUps, TOK = S::kStepTokens;
+  using Cut = AttnCut<TOK, kItemCost, kWholeSteps>;
   constexpr int SB = 32 / UPS;  // steps whose units the lanes look after
   extern __shared__ __align__(1024) uint8_t smem[];
   // layout: ring | combine buffer | q fragments | rows | warp maxima and sums | meta | barriers | batch
@@ -227,8 +231,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   pdl_launch_dependents();
 
   const int G = a.Hq / a.Hkv;
-  const AttnBatch batch = attn_scan<ROWS, TOK, 32 * NW>(a, first, cost, cus, ctxs, scan_part);
-  const AttnShare mine_of = attn_share<TOK>(batch);
+  const AttnBatch batch = attn_scan<ROWS, Cut, 32 * NW>(a, first, cost, cus, ctxs, scan_part);
+  const AttnShare mine_of = attn_share<Cut>(batch);
   const int c0 = mine_of.c0, c1 = mine_of.c1, n = c1 - c0;
   if (n == 0) return;
 
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       cp_async16(smem_u32(qraw + (size_t)b * ROWS * D * 2 + 16 * i), src, live);
     }
   };
-  fetch_q(attn_locate<ROWS, TOK>(batch, c0), 0);
+  fetch_q(attn_locate<ROWS, Cut>(batch, c0), 0);
 
   // ---- producer side of the warp's ring: a lane looks after one unit of SB steps ----
   uint64_t* bar = bars + warp * stages;
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     n_blk = -1;
     const int step = c0 + SB * b + lane / UPS;
     if (step < c1) {
-      const AttnPlace at = attn_locate<ROWS, TOK>(batch, step);
+      const AttnPlace at = attn_locate<ROWS, Cut>(batch, step);
       const int tok = ((at.s * NW + warp) * UPS + lane % UPS) * kUnit;
       if (tok < ctxs[at.r]) {
         n_blk = __ldg(a.table + (size_t)at.r * a.max_blocks + tok / a.bs);
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
 
   int qb = 0;
   auto begin_segment = [&](int step) {
-    item = attn_locate<ROWS, TOK>(batch, step);
+    item = attn_locate<ROWS, Cut>(batch, step);
     item_first = step - item.s;
     seg_end = min(c1, item_first + item.steps);
     ctx = ctxs[item.r];
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     }
     // the other buffer was last read before the barrier above
     qb ^= 1;
-    if (seg_end < c1) fetch_q(attn_locate<ROWS, TOK>(batch, seg_end), qb);
+    if (seg_end < c1) fetch_q(attn_locate<ROWS, Cut>(batch, seg_end), qb);
   };
 
   // lane's places in a swizzled tile: keys (token t0; t0 + 2 is 2 rows on), values (ldmatrix rows)
@@ -656,8 +660,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     }
     if (whole) return;
     // the CTA that brings an item's last piece adds the pieces up, in the order of the CTAs
-    const int f = attn_cta_of<TOK>(batch, mine_of, item_first),
-              e = attn_cta_of<TOK>(batch, mine_of, item_first + item.steps - 1), pieces = e - f + 1;
+    const int f = attn_cta_of<Cut>(batch, mine_of, item_first),
+              e = attn_cta_of<Cut>(batch, mine_of, item_first + item.steps - 1), pieces = e - f + 1;
     unsigned* count = static_cast<unsigned*>(a.ws) + f;
     __threadfence();
     __syncthreads();
@@ -773,7 +777,7 @@ AttnLaunch attn_smem(int R) {
 // steps of all items, at most (8 rows, 128 tokens); the kernel counts them in 32 bits
 long long attn_most_steps(const AttnArgs& a) {
   const long long tiles = ((long long)a.T * (a.Hq / a.Hkv)) / 8 + 2LL * a.R;
-  return tiles * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128 + 1 + kItemCost);
+  return tiles * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128 + 1 + 8);
 }
 
 template <int D, int NT, int FMT>

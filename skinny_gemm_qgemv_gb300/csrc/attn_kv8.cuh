@@ -61,12 +61,12 @@ __device__ __forceinline__ float ex2(float x) {
 // The CTA's view of the batch: requests, their steps and where a step lies.
 // A request has one item per key/value head and tile of kRows query rows, an
 // item has ceil(tokens / tokens of a step) steps. Shares are cut on a scale on which an
-// item also costs kItemCost steps before its first one: what beginning and
-// ending it takes (a batch of 32 requests of 1..8192 tokens, where one CTA can
+// item also costs some steps before its first one: what beginning and ending it
+// takes (a batch of 32 requests of 1..8192 tokens, where one CTA can
 // meet 20 short items: 82 -> XX us).
 struct AttnBatch {
   const int* first;  // [R + 1] steps before the request
-  const int* cost;   // [R + 1] the same with every item's kItemCost
+  const int* cost;   // [R + 1] the same with every item's cost
   const int* ctx;    // [R]
   const int* cu;     // [R + 1]
   int R, G;
@@ -75,8 +75,12 @@ struct AttnPlace {
   int r, h, rt;   // request, key/value head, row tile
   int s, steps;   // step within its item, steps of the item
 };
-constexpr int kItemCost = 2;
-constexpr int kWholeSteps = 6;  // items up to this long are not cut: joining the pieces takes longer (4 us)
+// How a kernel cuts its items: tokens of a step, steps that an item costs before
+// its first one, and up to how many steps an item is not cut at all.
+template <int TOK, int COST, int WHOLE>
+struct AttnCut {
+  static constexpr int kTok = TOK, kCost = COST, kWhole = WHOLE;
+};
 template <int TOK>  // tokens of a step
 __device__ __forceinline__ int attn_steps(int ctx) {
   return max(1, (ctx + TOK - 1) / TOK);
@@ -94,11 +98,11 @@ __device__ __forceinline__ int attn_find(const int* v, int n, int x) {
   }
   return lo;
 }
-template <int ROWS, int TOK>
+template <int ROWS, class CUT>
 __device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, int step) {
   AttnPlace p;
   p.r = attn_find(b.first, b.R, step);
-  p.steps = attn_steps<TOK>(b.ctx[p.r]);
+  p.steps = attn_steps<CUT::kTok>(b.ctx[p.r]);
   const int tiles = ((b.cu[p.r + 1] - b.cu[p.r]) * b.G + ROWS - 1) / ROWS;
   const int rem = step - b.first[p.r], item = rem / p.steps;
   p.s = rem - item * p.steps;
@@ -107,25 +111,25 @@ __device__ __forceinline__ AttnPlace attn_locate(const AttnBatch& b, int step) {
   return p;
 }
 // first step at or after place x of the cost scale, and the place of a step
-template <int TOK>
+template <class CUT>
 __device__ __forceinline__ int attn_step_at(const AttnBatch& b, int x) {
   if (x >= b.cost[b.R]) return b.first[b.R];
-  const int r = attn_find(b.cost, b.R, x), steps = attn_steps<TOK>(b.ctx[r]);
-  const int rem = x - b.cost[r], item = rem / (steps + kItemCost), at = rem - item * (steps + kItemCost);
+  const int r = attn_find(b.cost, b.R, x), steps = attn_steps<CUT::kTok>(b.ctx[r]);
+  const int rem = x - b.cost[r], item = rem / (steps + CUT::kCost), at = rem - item * (steps + CUT::kCost);
   // a short item belongs to the CTA whose share holds its beginning
-  return b.first[r] + item * steps + (steps <= kWholeSteps ? (at ? steps : 0) : max(0, at - kItemCost));
+  return b.first[r] + item * steps + (steps <= CUT::kWhole ? (at ? steps : 0) : max(0, at - CUT::kCost));
 }
-template <int TOK>
+template <class CUT>
 __device__ __forceinline__ int attn_cost_of(const AttnBatch& b, int step) {
-  const int r = attn_find(b.first, b.R, step), steps = attn_steps<TOK>(b.ctx[r]);
+  const int r = attn_find(b.first, b.R, step), steps = attn_steps<CUT::kTok>(b.ctx[r]);
   const int rem = step - b.first[r], item = rem / steps;
-  return b.cost[r] + rem + (item + 1) * kItemCost;
+  return b.cost[r] + rem + (item + 1) * CUT::kCost;
 }
 
 // The batch's tables in shared memory, formed by all NT threads of a CTA (`part`
 // has NT / 32 entries); returns the batch. The host has checked that the sums
 // stay below 2^31.
-template <int ROWS, int TOK, int NT>
+template <int ROWS, class CUT, int NT>
 __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, int* cost, int* cus, int* ctxs,
                                                int2* part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hkv;
@@ -146,9 +150,9 @@ __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, in
     if (r == a.R - 1) cus[a.R] = q1;
     first[r] = mine.x;
     cost[r] = mine.y;
-    const int items = a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS), steps = attn_steps<TOK>(ctx);
+    const int items = a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS), steps = attn_steps<CUT::kTok>(ctx);
     mine.x += items * steps;
-    mine.y += items * (steps + kItemCost);
+    mine.y += items * (steps + CUT::kCost);
   }
   int2 inc = mine;
 #pragma unroll
@@ -159,7 +163,7 @@ __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, in
   if (lane == 31) part[warp] = inc;
   __syncthreads();
   int2 before = make_int2(inc.x - mine.x, inc.y - mine.y), total = make_int2(0, 0);
-#pragma unroll 1
+#pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     const int2 x = part[w];
     if (w < warp) before.x += x.x, before.y += x.y;
@@ -176,21 +180,21 @@ __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, in
 struct AttnShare {
   int c0, c1, share, more;
 };
-template <int TOK>
+template <class CUT>
 __device__ __forceinline__ AttnShare attn_share(const AttnBatch& b) {
   const int W = b.cost[b.R], A = min((int)gridDim.x, W);  // the first W % A CTAs take one place more than the others
   AttnShare s = {0, 0, 0, 0};
   if ((int)blockIdx.x >= A) return s;
   s.share = W / A, s.more = W % A;
   const int x0 = blockIdx.x * s.share + min((int)blockIdx.x, s.more);
-  s.c0 = attn_step_at<TOK>(b, x0);
-  s.c1 = attn_step_at<TOK>(b, x0 + s.share + ((int)blockIdx.x < s.more ? 1 : 0));
+  s.c0 = attn_step_at<CUT>(b, x0);
+  s.c1 = attn_step_at<CUT>(b, x0 + s.share + ((int)blockIdx.x < s.more ? 1 : 0));
   return s;
 }
 // the CTA whose share holds a step
-template <int TOK>
+template <class CUT>
 __device__ __forceinline__ int attn_cta_of(const AttnBatch& b, const AttnShare& s, int step) {
-  const int x = attn_cost_of<TOK>(b, step), big = s.more * (s.share + 1);
+  const int x = attn_cost_of<CUT>(b, step), big = s.more * (s.share + 1);
   return x < big ? x / (s.share + 1) : s.more + (x - big) / s.share;
 }
 

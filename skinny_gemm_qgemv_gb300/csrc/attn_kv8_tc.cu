@@ -37,6 +37,9 @@ namespace {
 constexpr int kTcRows = 64;     // query rows of an item
 constexpr int kTcTok = 128;     // tokens of a step
 constexpr int kTcThreads = 512;
+// an item costs about 9 us to begin and end, a step 1.5 us; joining is a kernel of its own, so only the shortest items
+// are kept whole
+using TcCut = AttnCut<kTcTok, 5, 2>;
 constexpr int kTcMaxCtas = 152;  // pieces of an item whose factors fit the shared memory of P and q
 
 template <int D>
@@ -134,12 +137,35 @@ __device__ __forceinline__ bool named_barrier_or(int id, bool p) {
   return r != 0;
 }
 
-// fp32 as integers of the same order
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i ^ (i >> 31 & 0x7FFFFFFF);
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ (i >> 31 & 0x7FFFFFFF)); }
+__device__ __forceinline__ uint64_t both(float x) { return pair2(__float_as_uint(x), __float_as_uint(x)); }
+// the larger of R values over the 32 lanes, as transposed_warp_sum: lane L gets that of value transposed_row<R>(L)
+template <int R>
+__device__ __forceinline__ float transposed_warp_max(float (&v)[R], int lane) {
+  int cnt = R;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    if (cnt > 1) {
+      const int half = cnt / 2;
+      const bool upper = lane & o;
+#pragma unroll
+      for (int i = 0; i < R / 2; ++i) {
+        if (i < half) {
+          const float keep = upper ? v[i + half] : v[i], send = upper ? v[i] : v[i + half];
+          v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+      }
+      cnt = half;
+    } else {
+      v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
+  }
+  return v[0];
+}
 
 constexpr int kTcMaxStages = 4;
 
@@ -177,9 +203,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int* cost = first + a.R + 1;
   int* cus = cost + a.R + 1;
   int* ctxs = cus + a.R + 1;
-  __shared__ __align__(16) float neg_m[ROWS], fall[ROWS], sums[ROWS];
+  __shared__ __align__(16) float neg_m[ROWS], fall[ROWS], fade[ROWS], sums[ROWS];
   __shared__ __align__(16) float wsum[4][ROWS];
-  __shared__ int wmax[4][ROWS];
   __shared__ int4 row_info[ROWS];  // tokens below .x are seen, and draft tokens by .y's bits; .z: output row or -1
   __shared__ uint64_t full[kTcMaxStages], empty[kTcMaxStages], k_full[2], s_full[2], s_empty[2], p_full[2], v_full[2], o_done[2], q_full;
   __shared__ int2 scan_part[kTcThreads / 32];
@@ -209,9 +234,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   tc_before();
-  const AttnBatch batch = attn_scan<ROWS, TOK, kTcThreads>(a, first, cost, cus, ctxs, scan_part);  // has barriers
+  const AttnBatch batch = attn_scan<ROWS, TcCut, kTcThreads>(a, first, cost, cus, ctxs, scan_part);  // has barriers
   tc_after();
-  const AttnShare share = attn_share<TOK>(batch);
+  const AttnShare share = attn_share<TcCut>(batch);
   const uint32_t tbase = tmem_base;
   const uint32_t tlane = tbase + ((uint32_t)(quad * 32) << 16);  // the lanes that this warp may touch
 
@@ -239,7 +264,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (step >= share.c1) return false;
     s.g += s.n;
     ++s.index;
-    s.item = attn_locate<ROWS, TOK>(batch, step);
+    s.item = attn_locate<ROWS, TcCut>(batch, step);
     s.item_first = step - s.item.s;
     s.n = min(share.c1, s.item_first + s.item.steps) - step;
     s.ctx = ctxs[s.item.r];
@@ -379,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ok = wait(k_full + b, (g >> 1) & 1) && (g < 2 || wait(s_empty + b, ((g >> 1) - 1) & 1));
             if (!ok) break;
             tc_after();
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 16; ++k)
               mma_ts(tbase + S::kColS + b * ROWS, tbase + S::kColK + b * (D / 2) + 8 * k,
                      tc_desc(qs + (k >> 2) * ROWS * 128 + (k & 3) * 32, 16, 1024), is, k > 0);
@@ -391,7 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) break;
             tc_after();
             const uint32_t vs = smem_u32(vbuf + b * S::kV), ps = smem_u32(pbuf + b * S::kP);
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < TOK / 16; ++k)
               mma_ss(tbase + S::kColO, tc_desc(vs + k * 2048, TOK * 128, 1024), tc_desc(ps + k * 2048, TOK * 128, 1024), io,
                      i > 1 || k > 0);
@@ -473,9 +498,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int hc = half ? 16 * ((nch + 1) / 2) : 0, hch = half ? nch / 2 : (nch + 1) / 2;
       const uint32_t t_s = tlane + S::kColS + hc, t_o = tlane + S::kColO + hc;
       float* nm_of = neg_m + hc;
-      float l[HR];
+      uint64_t l[HR / 2];  // sums of columns 2 j, 2 j + 1
 #pragma unroll
-      for (int j = 0; j < HR; ++j) l[j] = 0.f;
+      for (int j = 0; j < HR / 2; ++j) l[j] = 0ull;
       // the token's block of steps ahead, its scales of one step ahead
       auto look = [&](int i) {
         const int tok = tok0 + i * TOK + t;
@@ -497,7 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         blk = look(i + 2);
         const bool there = now.y >= 0.f || now.y != now.y;
         const float vs = now.y < kMinScale ? kMinScale : now.y;
-        const float ks = now.x * up, lv = __log2f(vs), inv = __frcp_rn(vs);
+        const uint64_t ks2 = both(now.x * up), lv2 = both(__log2f(vs)), inv2 = both(__frcp_rn(vs));
         const bool edge = __any_sync(0xffffffffu, !there || tok >= base);
         // (After a wait that gave up every later one returns at once: the warps stay in step at their barriers.)
         wait_warp(s_full + b, (g >> 1) & 1);
@@ -514,16 +539,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(s_empty + b);
         bool grow = unset;
 #pragma unroll
-        for (int ch = 0; ch < HR / 16; ++ch) {
-          if (ch < hch) {
-#pragma unroll
-            for (int j = 16 * ch; j < 16 * ch + 16; j += 4) {
-              const float4 nm = *reinterpret_cast<const float4*>(nm_of + j);
-              y[j] = fmaf(y[j], ks, lv + nm.x);
-              y[j + 1] = fmaf(y[j + 1], ks, lv + nm.y);
-              y[j + 2] = fmaf(y[j + 2], ks, lv + nm.z);
-              y[j + 3] = fmaf(y[j + 3], ks, lv + nm.w);
-            }
+        for (int j = 0; j < HR; j += 4) {
+          if (j / 16 < hch) {
+            const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(nm_of + j);
+            unpair2(ffma2(pair2(__float_as_uint(y[j]), __float_as_uint(y[j + 1])), ks2, fadd2(lv2, nm.x)), y[j], y[j + 1]);
+            unpair2(ffma2(pair2(__float_as_uint(y[j + 2]), __float_as_uint(y[j + 3])), ks2, fadd2(lv2, nm.y)), y[j + 2],
+                    y[j + 3]);
           }
         }
         if (edge) {
@@ -543,24 +564,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (g >= 2) wait_warp(o_done + b, ((g >> 1) - 1) & 1);  // P of two steps ago has been read
         if (named_barrier_or<128>(bar, grow)) {
           // rows whose m has to rise (or to be set): the largest y over the step's tokens
+          {
+            float top[HR];
 #pragma unroll
-          for (int j = 0; j < HR; ++j) {
-            if (j / 16 < hch) {
-              const int top = __reduce_max_sync(0xffffffffu, ordered(y[j]));
-              if (lane == 0) wmax[quad][hc + j] = top;
-            }
+            for (int j = 0; j < HR; ++j) top[j] = j / 16 < hch ? y[j] : -INFINITY;
+            const float x = transposed_warp_max<HR>(top, lane);
+            const int j = transposed_row<HR>(lane);
+            if (j < 16 * hch) wsum[quad][hc + j] = x;
           }
           if (t == 0) unset_any[half] = 0u;
           named_barrier<128>(bar);
           if (t < 16 * hch) {
             const int j = hc + t;
-            const float top = unordered(max(max(wmax[0][j], wmax[1][j]), max(wmax[2][j], wmax[3][j])));
+            const float top = fmaxf(fmaxf(wsum[0][j], wsum[1][j]), fmaxf(wsum[2][j], wsum[3][j]));
             const bool is_set = row_info[j].w != 0;
-            // a first maximum may be below 0, a later one only raises m
+            // a first maximum may be below 0 (nothing has been summed yet), a later one only raises m
             const float rise = top == -INFINITY ? 0.f : is_set ? fmaxf(top, 0.f) : top;
             if (!is_set && top != -INFINITY) row_info[j].w = 1;
             if (!is_set && top == -INFINITY) unset_any[half] = 1u;
-            fall[j] = rise;
+            fall[j] = -rise;
+            fade[j] = ex2(fminf(-rise, 0.f));
             neg_m[j] -= rise;
           }
           named_barrier<128>(bar);
@@ -568,22 +591,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (i > 0) wait_warp(o_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
           tc_after();
 #pragma unroll
-          for (int ch = 0; ch < HR / 16; ++ch) {
-            if (ch < hch) {
+          for (int j = 0; j < HR; j += 4) {
+            if (j / 16 < hch) {
+              const float4 r = *reinterpret_cast<const float4*>(fall + hc + j);
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fade + hc + j);
+              y[j] += r.x, y[j + 1] += r.y, y[j + 2] += r.z, y[j + 3] += r.w;
+              l[j / 2] = ffma2(l[j / 2], f.x, 0ull);
+              l[j / 2 + 1] = ffma2(l[j / 2 + 1], f.y, 0ull);
+            }
+          }
+          if (i > 0) {
+#pragma unroll 1
+            for (int ch = 0; ch < hch; ++ch) {
               float o[16];
-              if (i > 0) {
-                tmem_ld16(t_o + 16 * ch, o);
-                tmem_wait_ld(o);
-              }
+              tmem_ld16(t_o + 16 * ch, o);
+              tmem_wait_ld(o);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                // (r < 0 only where m is set for the first time: nothing has been summed yet)
-                const float r = fall[hc + 16 * ch + j], f = ex2(fminf(-r, 0.f));
-                y[16 * ch + j] -= r;
-                l[16 * ch + j] *= f;
-                if (i > 0) o[j] *= f;
-              }
-              if (i > 0) tmem_st16(t_o + 16 * ch, o);
+              for (int j = 0; j < 16; ++j) o[j] *= fade[hc + 16 * ch + j];
+              tmem_st16(t_o + 16 * ch, o);
             }
           }
           if (i > 0) tmem_wait_st();
@@ -600,8 +625,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int k = 0; k < 4; ++k) {
               const int j = 8 * c8 + 2 * k;
               const float e0 = ex2(y[j]), e1 = ex2(y[j + 1]);
-              l[j] = fmaf(e0, inv, l[j]);
-              l[j + 1] = fmaf(e1, inv, l[j + 1]);
+              l[j / 2] = ffma2(pair2(__float_as_uint(e0), __float_as_uint(e1)), inv2, l[j / 2]);
               f[k] = zero ? 0u : f16x2(e0, e1);
             }
             sts128(dst + (((c8 + hc / 8) ^ (t & 7)) << 4), make_uint4(f[0], f[1], f[2], f[3]));
@@ -613,23 +637,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       // the rows' sums over the tokens: per warp, then over the warps
       {
-        const float x = transposed_warp_sum<HR>(l, lane);
+        float part[HR];
+#pragma unroll
+        for (int j = 0; j < HR / 2; ++j) unpair2(l[j], part[2 * j], part[2 * j + 1]);
+        const float x = transposed_warp_sum<HR>(part, lane);
         const int j = transposed_row<HR>(lane);
         if (j < 16 * hch) wsum[quad][hc + j] = x;
       }
+      const int item_first = sg.item_first;
+      const bool whole = item_first >= share.c0 && item_first + item.steps <= share.c1;
+      uint8_t* piece = static_cast<uint8_t*>(a.ws) + kAttnCounterBytes +
+                       (size_t)(2 * blockIdx.x + (item_first < share.c0 ? 0 : 1)) * attn_piece_bytes(ROWS, D);
       named_barrier<128>(bar);
-      if (t < 16 * hch) sums[hc + t] = (wsum[0][hc + t] + wsum[1][hc + t]) + (wsum[2][hc + t] + wsum[3][hc + t]);
+      if (t < 16 * hch) {
+        const int j = hc + t;
+        const float L = (wsum[0][j] + wsum[1][j]) + (wsum[2][j] + wsum[3][j]);
+        if (!whole)
+          reinterpret_cast<float2*>(piece + (size_t)ROWS * D * 4)[j] = make_float2(L > 0.f ? -neg_m[j] : kNoMax, L);
+        sums[j] = !whole ? 1.f : L == 0.f ? 0.f : __frcp_rn(L);  // what the outputs are multiplied with
+      }
       named_barrier<128>(bar);
       // ---- the segment's results ----
       const int g = gi + n - 1;
       if (wait_warp(o_done + (g & 1), (g >> 1) & 1)) {
         tc_after();
-        const int item_first = sg.item_first;
-        const bool whole = item_first >= share.c0 && item_first + item.steps <= share.c1;
         const int d = D == 128 ? t : quad * 16 + lane;  // D = 64: 16 lanes of each quadrant
         const bool has = D == 128 || lane < 16;
-        uint8_t* piece = static_cast<uint8_t*>(a.ws) + kAttnCounterBytes +
-                         (size_t)(2 * blockIdx.x + (item_first < share.c0 ? 0 : 1)) * attn_piece_bytes(ROWS, D);
 #pragma unroll 1
         for (int ch = 0; ch < hch; ++ch) {
           float o[16];
@@ -638,26 +671,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int rr = hc + 16 * ch + j, to = row_info[rr].z;
+            const float f = sums[rr], v = f == 0.f ? 0.f : o[j] * f;
             if (has && to >= 0) {
-              if (whole) {
-                const float L = sums[rr];
-                const uint32_t v = f32_to_bf16x2(L == 0.f ? 0.f : o[j] * __frcp_rn(L), 0.f);
-                a.out[(size_t)to * D + d] = (uint16_t)v;
-              } else {
-                reinterpret_cast<float*>(piece)[rr * D + d] = o[j];
-              }
+              if (whole)
+                a.out[(size_t)to * D + d] = (uint16_t)f32_to_bf16x2(v, 0.f);
+              else
+                reinterpret_cast<float*>(piece)[rr * D + d] = v;
             }
           }
         }
-        if (!whole && t < 16 * hch)
-          reinterpret_cast<float2*>(piece + (size_t)ROWS * D * 4)[hc + t] =
-              make_float2(sums[hc + t] > 0.f ? -neg_m[hc + t] : kNoMax, sums[hc + t]);
         tc_before();
       }
-      const int item_first = sg.item_first;
       if (u == 0 && item_first >= share.c0 && item_first + item.steps > share.c1) {
         // the item goes on in other shares: their pieces are joined by attn_kv8_join_kernel
-        const int e = attn_cta_of<TOK>(batch, share, item_first + item.steps - 1);
+        const int e = attn_cta_of<TcCut>(batch, share, item_first + item.steps - 1);
         split = make_int4((e - (int)blockIdx.x + 1) | rows << 16, sg.q0, item.h, item.rt);
       }
       named_barrier<256>(3);  // both halves are done with the tables of this segment
