@@ -287,14 +287,19 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     const float v = n_scale.y < kMinScale ? kMinScale : n_scale.y;
     scale = make_float4(n_scale.x, __log2f(v), __frcp_rn(v), page < 0 ? 0.f : n_scale.y == 0.f ? 2.f : 1.f);
   };
+  // the first batch's pages are known before its scales: the copies of the first steps do not wait for them
+  auto first_batch = [&]() {
+    page = n_blk >= 0 ? n_blk * a.Hkv + n_head : -1;
+    row = n_row;
+  };
   auto issue = [&](int i, int slot) {
     const int k = i & (SB - 1);
-    if (k == 0) {
-      if (i > 0) next_batch();
+    if (k == 0 && i > 0) {
+      next_batch();
       look_table(i / SB + 1);
     }
     if (k == SB / 2) look_scale();
-    if (lane / UPS == k) my_meta[slot * UPS + lane % UPS] = scale;  // the warp reads it after a barrier of its own
+    if (i >= stages && lane / UPS == k) my_meta[slot * UPS + lane % UPS] = scale;  // the warp reads it after a barrier of its own
     int pages[UPS], rows[UPS], units = 0;
 #pragma unroll
     for (int u = 0; u < UPS; ++u) {
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   };
   look_table(0);
   look_scale();
-  next_batch();
+  first_batch();
 
   // ---- consumer ----
   float acc[NT][S::kMt][4];
@@ -605,6 +610,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     // a CTA has a piece of at most two items: one begun before its share, one that goes on after it
     uint8_t* mine = ws + (size_t)(2 * blockIdx.x + (item_first < c0 ? 0 : 1)) * attn_piece_bytes(ROWS, D);
     float4* stat = reinterpret_cast<float4*>(mine + (size_t)ROWS * D * 4);
+    // In the CTA's last segment the ring is free: all tiles at once there, else S::kPass at a time.
+    const bool last = seg_end == c1 && stages * S::kStage * NW >= NW * kTiles * 512;
+    float4* sum_buf = last ? reinterpret_cast<float4*>(ring) : buf;
+    const int per_pass = last ? kTiles : S::kPass;
     __syncthreads();
     // to the item's maximum
 #pragma unroll
@@ -622,24 +631,25 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         for (int mt = 0; mt < S::kMt; ++mt) acc[nt][mt][j] *= f, acc[nt][mt][j + 2] *= f;
       }
     }
-    // S::kPass tiles at a time: all warps' parts into shared memory, then a tile per warp is added up
+    // all warps' parts into shared memory, then a tile per warp is added up
 #pragma unroll 1
-    for (int t0 = 0; t0 < kTiles; t0 += S::kPass) {
+    for (int t0 = 0; t0 < kTiles; t0 += per_pass) {
 #pragma unroll
       for (int q = 0; q < kTiles; ++q) {
-        if (q / S::kPass * S::kPass == t0)
-          buf[(warp * S::kPass + q % S::kPass) * 32 + lane] =
+        if (last || q / S::kPass * S::kPass == t0)
+          sum_buf[(warp * per_pass + q - t0) * 32 + lane] =
               make_float4(acc[q / S::kMt][q % S::kMt][0], acc[q / S::kMt][q % S::kMt][1], acc[q / S::kMt][q % S::kMt][2],
                           acc[q / S::kMt][q % S::kMt][3]);
       }
       __syncthreads();
-      if (warp < S::kPass) {
-        const int q = t0 + warp, nt = q / S::kMt, mt = q - nt * S::kMt;
+#pragma unroll 1
+      for (int q = t0 + warp; q < t0 + per_pass; q += NW) {
+        const int nt = q / S::kMt, mt = q - nt * S::kMt;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float mm[2] = {kNoMax, kNoMax}, ll[2] = {0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          const float4 x = buf[(w * S::kPass + warp) * 32 + lane];
+          const float4 x = sum_buf[(w * per_pass + q - t0) * 32 + lane];
           o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
           const float4 y = *reinterpret_cast<const float4*>(wstat + w * ROWS + nt * 8 + 2 * c);
           mm[0] = fmaxf(mm[0], y.x), mm[1] = fmaxf(mm[1], y.z);
@@ -656,7 +666,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
           if (mt == 0 && g == 0) stat[nt * 4 + c] = make_float4(mm[0], ll[0], mm[1], ll[1]);
         }
       }
-      if (t0 + S::kPass < kTiles) __syncthreads();
+      if (t0 + per_pass < kTiles) __syncthreads();
     }
     if (whole) return;
     // the CTA that brings an item's last piece adds the pieces up, in the order of the CTAs
@@ -733,6 +743,12 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       if (i == n || c0 + i == seg_end) {
         if (i > 0) end_segment();
         if (i == n) break;
+        if (i == 0) {
+          // the first batch's scales have arrived; its first steps' ones go where issue() puts the others'
+          next_batch();
+          if (lane / UPS < stages) my_meta[lane] = scale;
+          look_table(1);
+        }
         begin_segment(c0 + i);
         tok = (item.s * NW + warp) * UPS * kUnit;
       }
@@ -800,9 +816,15 @@ cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
 
 // rows of an average request's item
 int attn_rows(const AttnArgs& a) { return (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv); }
-// more than 16 rows: the tcgen05 kernel (D = 256 keeps to this one, 16 rows at a time: its values as fp16 would take
-// all of the shared memory)
-bool attn_tc_ok(const AttnArgs& a) { return attn_rows(a) > 16 && (a.D == 64 || a.D == 128); }
+// The tcgen05 kernel for many rows of 128 elements. This file's kernel passes over the cache once per 16 rows, at 5 ns
+// per 128 tokens of a head (the HBM rate); that one takes 10 ns per 128 tokens and 64 rows, and 7 us more to begin,
+// end and join (measured: 64 rows, one request: 8192 tokens 23.7 here, 25.4 us there; 32784 tokens 55.5 and 43.5;
+// 32 rows, 32768 tokens: 34.8 and 38.7). The lengths are known to the GPU alone, so their bound decides.
+bool attn_tc_ok(const AttnArgs& a) {
+  if (a.D != 128) return false;
+  const long long rows = attn_rows(a), steps = (long long)a.R * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128);
+  return steps * (5 * ((rows + 15) / 16) - 10 * ((rows + 63) / 64)) >= 7000;
+}
 
 // 8-row tiles per item: the least that hold an average request's query rows
 template <int FMT>

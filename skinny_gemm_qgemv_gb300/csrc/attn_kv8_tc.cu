@@ -1,17 +1,15 @@
-// Attention over the paged 8-bit cache for many query rows per key/value head
-// (17 and more: drafts of a speculative tree times the heads of a group), on the
-// 5th-generation tensor cores.
+// Attention over the paged 8-bit cache for many query rows per key/value head of
+// 128 elements (more than 32: drafts of a speculative tree times the heads of a
+// group), on the 5th-generation tensor cores.
 //
-// With 64 rows the products of one cache byte cost what the warp-level kernel of
-// attn_kv8.cu cannot hide: its conversion of a code feeds 32 rows at most and its
-// MMAs run at half of these units' rate or less. Here a step of 128 tokens is
-// converted once for up to 64 rows:
+// The warp-level kernel of attn_kv8.cu reads the cache once for every 16 rows.
+// Here a step of 128 tokens is read and converted once for up to 64:
 //   S^T [128 tokens][N rows] = K q^T    A = the keys as fp16 in TMEM (a thread
 //       converts a token's row and stores it to its own lane), B = the queries;
 //   P^T = 2^(S^T ... - m)               a thread per token, half of the rows: what is a
 //       maximum over the tokens becomes a test against the row's m, so no
 //       exchange between threads unless some score outgrows m by 2^8;
-//   O^T [D][N rows] += V^T P^T          A = the values as fp16 in shared memory,
+//   O^T [128][N rows] += V^T P^T          A = the values as fp16 in shared memory,
 //       token-major as converted (MN-major operand), B = P^T as written.
 // The value scale of a token's block enters through the exponent and comes off
 // the sum again, as in attn_kv8.cu. Sums, maxima and accumulators are fp32, K, V
@@ -42,13 +40,13 @@ constexpr int kTcThreads = 512;
 using TcCut = AttnCut<kTcTok, 5, 2>;
 constexpr int kTcMaxCtas = 152;  // pieces of an item whose factors fit the shared memory of P and q
 
-template <int D>
+constexpr int D = 128;
 struct TcShape {
   static constexpr int kTile = kTcTok * D;                // a step's keys (or values) as stored
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kV = kTcTok * D * 2;               // a step's values as fp16: [D / 64][128 tokens][64]
+  static constexpr int kV = kTcTok * D * 2;               // a step's values as fp16: [2][128 tokens][64]
   static constexpr int kP = kTcTok * kTcRows * 2;         // [128 tokens][64 rows] fp16
-  static constexpr int kQ = kTcRows * D * 2;              // [D / 64][64 rows][64] fp16
+  static constexpr int kQ = kTcRows * D * 2;              // [2][64 rows][64] fp16
   static constexpr int kColK = 0, kColS = 2 * (D / 2), kColO = kColS + 2 * kTcRows;  // TMEM columns
 };
 constexpr uint32_t kTcCols = 512;
@@ -167,7 +165,7 @@ __device__ __forceinline__ float transposed_warp_max(float (&v)[R], int lane) {
   return v[0];
 }
 
-constexpr int kTcMaxStages = 4;
+constexpr int kTcMaxStages = 3;
 
 // one entry per CTA, behind the counters of attn_kv8.cu's pieces
 __device__ __forceinline__ int4* tc_splits(void* ws) {
@@ -187,11 +185,11 @@ __device__ __noinline__ bool tc_wait_on(uint64_t* bar, uint32_t parity, volatile
   return false;
 }
 
-template <int D, int FMT>
+template <int FMT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
                        int box, int stages) {
-  using S = TcShape<D>;
+  using S = TcShape;
   constexpr int ROWS = kTcRows, TOK = kTcTok;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, role = warp >> 2, quad = warp & 3;
@@ -299,7 +297,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int ch = 4 * h + j;
-            const uint32_t at = D == 64 ? t * 64 + ((ch ^ (t >> 1 & 3)) << 4) : t * 128 + ((ch ^ (t & 7)) << 4);
+            const uint32_t at = t * 128 + ((ch ^ (t & 7)) << 4);
             const uint4 w = lds128(src + at);
             codes_to_f16<FMT>(w.x, f[8 * j], f[8 * j + 1]);
             codes_to_f16<FMT>(w.y, f[8 * j + 2], f[8 * j + 3]);
@@ -331,7 +329,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool none = sg.tok0 + i * TOK + t >= sg.ctx;  // slots past the context may hold codes that are not numbers
 #pragma unroll
           for (int ch = 0; ch < D / 16; ++ch) {
-            const uint32_t at = D == 64 ? t * 64 + ((ch ^ (t >> 1 & 3)) << 4) : t * 128 + ((ch ^ (t & 7)) << 4);
+            const uint32_t at = t * 128 + ((ch ^ (t & 7)) << 4);
             uint4 w = lds128(src + at);
             if (none) w = make_uint4(0u, 0u, 0u, 0u);
             uint4 f[2];
@@ -661,8 +659,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int g = gi + n - 1;
       if (wait_warp(o_done + (g & 1), (g >> 1) & 1)) {
         tc_after();
-        const int d = D == 128 ? t : quad * 16 + lane;  // D = 64: 16 lanes of each quadrant
-        const bool has = D == 128 || lane < 16;
 #pragma unroll 1
         for (int ch = 0; ch < hch; ++ch) {
           float o[16];
@@ -672,11 +668,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int j = 0; j < 16; ++j) {
             const int rr = hc + 16 * ch + j, to = row_info[rr].z;
             const float f = sums[rr], v = f == 0.f ? 0.f : o[j] * f;
-            if (has && to >= 0) {
+            if (to >= 0) {
               if (whole)
-                a.out[(size_t)to * D + d] = (uint16_t)f32_to_bf16x2(v, 0.f);
+                a.out[(size_t)to * D + t] = (uint16_t)f32_to_bf16x2(v, 0.f);
               else
-                reinterpret_cast<float*>(piece)[rr * D + d] = v;
+                reinterpret_cast<float*>(piece)[rr * D + t] = v;
             }
           }
         }
@@ -716,7 +712,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // goes on after it. One CTA adding up an item's 64 rows from 19 pieces took
 // 30 us of 61; here every SM takes part, after the kernel's end.
 constexpr int kJoinRows = 16;
-template <int D>
 __global__ void __launch_bounds__(kJoinRows * D / 4) attn_kv8_join_kernel(AttnArgs a) {
   __shared__ float factor[kTcMaxCtas][kJoinRows], sums[kJoinRows];
   pdl_wait();
@@ -762,37 +757,34 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) attn_kv8_join_kernel(AttnAr
       make_uint2(f32_to_bf16x2(o.x * r, o.y * r), f32_to_bf16x2(o.z * r, o.w * r));
 }
 
-template <int D, int FMT>
+template <int FMT>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream, bool pdl) {
-  using S = TcShape<D>;
+  using S = TcShape;
   CUtensorMap km, vm;
-  const auto sw = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   // tokens of a copy: the largest part of a step that lies in one block whatever its start
   const int box = a.bs % 128 == 0 ? 128 : a.bs % 64 == 0 ? 64 : a.bs % 32 == 0 ? 32 : 16;
   for (int i = 0; i < 2; ++i)
     if (!tmap_3d(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? a.v_cache : a.k_cache, D, a.bs,
-                 (uint64_t)a.num_blocks * a.Hkv, D, (uint64_t)a.bs * D, D, box, 1, sw))
+                 (uint64_t)a.num_blocks * a.Hkv, D, (uint64_t)a.bs * D, D, box, 1))
       return cudaErrorInvalidValue;
-  auto k = attn_kv8_tc_kernel<D, FMT>;
+  auto k = attn_kv8_tc_kernel<FMT>;
   cudaError_t e = allow_max_smem(k);
   if (e != cudaSuccess) return e;
   const size_t fixed = 2 * S::kV + 2 * S::kP + S::kQ + 16 * ((size_t)a.R + 1);
   // three stages; two where the tables of more than 800 requests leave no room
-  const int stages = (int)std::min<size_t>(D == 64 ? 4 : 3, ((size_t)device_max_smem_optin() - 6144 - fixed) / S::kStage);
+  const int stages = (int)std::min<size_t>(3, ((size_t)device_max_smem_optin() - 6144 - fixed) / S::kStage);
   const size_t smem = fixed + stages * S::kStage;
   const int ctas = std::min(device_sm_count(), kTcMaxCtas);
   e = launch_kernel(k, dim3(ctas), dim3(kTcThreads), smem, stream, pdl, km, vm, a, box, stages);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attn_kv8_join_kernel<D>, dim3(ctas, kTcRows / kJoinRows), dim3(kJoinRows * D / 4), 0, stream, true,
+  return launch_kernel(attn_kv8_join_kernel, dim3(ctas, kTcRows / kJoinRows), dim3(kJoinRows * D / 4), 0, stream, true,
                        a);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_kv8_tc(const AttnArgs& a, int format, cudaStream_t stream, bool pdl) {
-  if (a.D == 64)
-    return format == QG_KV_I8 ? launch_tc<64, QG_KV_I8>(a, stream, pdl) : launch_tc<64, QG_KV_E4M3>(a, stream, pdl);
-  return format == QG_KV_I8 ? launch_tc<128, QG_KV_I8>(a, stream, pdl) : launch_tc<128, QG_KV_E4M3>(a, stream, pdl);
+  return format == QG_KV_I8 ? launch_tc<QG_KV_I8>(a, stream, pdl) : launch_tc<QG_KV_E4M3>(a, stream, pdl);
 }
 
 }  // namespace qg
