@@ -689,18 +689,23 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     };
 #pragma unroll 1
     for (int rr = warp; rr < ROWS; rr += NW) {
+      float2 st[kMaxCtas / 32];
       float mm = kNoMax, ll = 0.f;
-#pragma unroll 2
-      for (int i = lane; i < pieces; i += 32)
-        mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr).x);
+#pragma unroll
+      for (int k = 0; k < kMaxCtas / 32; ++k) {
+        const int i = lane + 32 * k;
+        st[k] = i < pieces ? __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr)
+                           : make_float2(kNoMax, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kMaxCtas / 32; ++k) mm = fmaxf(mm, st[k].x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-#pragma unroll 2
-      for (int i = lane; i < pieces; i += 32) {
-        const float2 st = __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)ROWS * D * 4) + rr);
-        const float x = ex2(st.x - mm);
-        factor[i * ROWS + rr] = x;
-        ll = fmaf(st.y, x, ll);
+#pragma unroll
+      for (int k = 0; k < kMaxCtas / 32; ++k) {
+        const float x = ex2(st[k].x - mm);
+        if (lane + 32 * k < pieces) factor[(lane + 32 * k) * ROWS + rr] = x;
+        ll = fmaf(st[k].y, x, ll);
       }
       ll = warp_sum(ll);
       if (lane == 0) wstat[rr].y = ll;
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     for (int q = warp % kTiles; q < kTiles; q += NW) {
       const int part = kParts > 1 ? warp / kTiles : 0, rr = q / S::kMt * 8 + 2 * c;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = part; i < pieces; i += kParts) {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(piece(i)) + q * 32 + lane);
         const float2 fa = *reinterpret_cast<const float2*>(factor + i * ROWS + rr);

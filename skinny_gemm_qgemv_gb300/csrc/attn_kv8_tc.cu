@@ -499,28 +499,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint64_t l[HR / 2];  // sums of columns 2 j, 2 j + 1
 #pragma unroll
       for (int j = 0; j < HR / 2; ++j) l[j] = 0ull;
-      // the token's block of steps ahead, its scales of one step ahead
-      auto look = [&](int i) {
-        const int tok = tok0 + i * TOK + t;
-        if (i >= n || tok >= ctx) return -1;
-        return __ldg(a.table + (size_t)item.r * a.max_blocks + tok / a.bs);
+      // the token's place in the table, its block of steps ahead, its scales of one step ahead
+      const int step_q = TOK / a.bs, step_r = TOK % a.bs;
+      int at_blk = (tok0 + t) / a.bs, at_off = (tok0 + t) - at_blk * a.bs, at_tok = tok0 + t;
+      const int32_t* row_table = a.table + (size_t)item.r * a.max_blocks;
+      const int end_tok = min(ctx, tok0 + n * TOK);
+      auto look = [&]() {  // the next token's entry, -1 past the segment
+        const int blk = at_tok < end_tok ? __ldg(row_table + at_blk) : -1;
+        at_tok += TOK;
+        at_blk += step_q;
+        at_off += step_r;
+        if (at_off >= a.bs) at_off -= a.bs, ++at_blk;
+        return blk;
       };
+      const float2* head_scales = reinterpret_cast<const float2*>(a.scales) + item.h;
       auto scales_of = [&](int blk) {
-        return blk < 0 || blk >= a.num_blocks ? make_float2(0.f, -1.f)
-                       : __ldg(reinterpret_cast<const float2*>(a.scales) + (size_t)blk * a.Hkv + item.h);
+        return blk < 0 || blk >= a.num_blocks ? make_float2(0.f, -1.f) : __ldg(head_scales + (size_t)blk * a.Hkv);
       };
-      float2 sc = scales_of(look(0));
-      int blk = look(1);
+      float2 sc = scales_of(look());
+      int blk = look();
       bool unset = true;  // some row has seen no token yet
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const int g = gi + i, b = g & 1, tok = tok0 + i * TOK + t;
         const float2 now = sc;
         sc = scales_of(blk);
-        blk = look(i + 2);
+        blk = look();
         const bool there = now.y >= 0.f || now.y != now.y;
         const float vs = now.y < kMinScale ? kMinScale : now.y;
-        const uint64_t ks2 = both(now.x * up), lv2 = both(__log2f(vs)), inv2 = both(__frcp_rn(vs));
+        const float lv = __log2f(vs);
+        const uint64_t ks2 = both(now.x * up), lv2 = both(lv), inv2 = both(ex2(-lv));  // (not 1 / vs: what comes off is what went on)
         const bool edge = __any_sync(0xffffffffu, !there || tok >= base);
         // (After a wait that gave up every later one returns at once: the warps stay in step at their barriers.)
         wait_warp(s_full + b, (g >> 1) & 1);
@@ -556,9 +564,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
+        float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < HR; j += 4)
-          if (j / 16 < hch) grow |= fmaxf(fmaxf(y[j], y[j + 1]), fmaxf(y[j + 2], y[j + 3])) > kSlack;
+        for (int j = 0; j < HR; j += 8) {
+          if (j / 16 < hch) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) most[k] = fmaxf(fmaxf(most[k], y[j + k]), y[j + k + 4]);
+          }
+        }
+        grow |= fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kSlack;
         if (g >= 2) wait_warp(o_done + b, ((g >> 1) - 1) & 1);  // P of two steps ago has been read
         if (named_barrier_or<128>(bar, grow)) {
           // rows whose m has to rise (or to be set): the largest y over the step's tokens

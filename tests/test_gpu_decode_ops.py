@@ -473,6 +473,119 @@ def test_decode_ops_back_to_back_with_pdl(q):
 
 
 # --------------------------------------------------------------------------
+# attention, many query rows: a wide block table makes the bound of the lengths large, and with it the tcgen05 kernel
+# runs (more than 32 rows of 128 elements per key/value head)
+# --------------------------------------------------------------------------
+
+def widen(c, tokens=1 << 20):
+    R, maxb = c["table"].shape
+    bs = c["kc"].shape[2]
+    wide = np.full((R, tokens // bs), -1, np.int64)
+    wide[:, :maxb] = c["table"]
+    return dict(c, table=wide)
+
+
+MANY = [
+    # query tokens, context lengths, Hq, Hkv, block, tree
+    ([16], [2063], 32, 8, 64, True),
+    ([16], [16], 32, 8, 16, True),
+    ([12], [128], 32, 8, 16, False),
+    ([9], [129], 4, 1, 16, False),
+    ([16, 1, 32, 7], [16, 1, 32, 200], 8, 2, 16, True),
+    ([11, 0, 16], [1500, 90, 127], 8, 2, 48, False),
+    ([40, 33], [40, 300], 4, 2, 32, True),
+    ([100], [1000], 4, 1, 128, False),
+    ([5, 6, 7], [333, 2500, 64], 48, 4, 32, False),
+    ([64], [4000], 3, 3, 256, False),
+    ([3], [777], 64, 1, 1024, False),
+    ([20] * 9, [(i * 97) % 700 for i in range(9)], 10, 2, 16, False),
+]
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("nq,ctx,Hq,Hkv,bs,tree", MANY)
+def test_attention_many_rows(q, fmt, nq, ctx, Hq, Hkv, bs, tree):
+    rng = np.random.default_rng(sum(ctx) + bs + Hq)
+    c = widen(attn_case(rng, nq, ctx, Hq, Hkv, 128, bs, fmt, tree))
+    out = run_attn(q, c)
+    check_attn(out, c)
+    assert torch.equal(run_attn(q, c), out)  # the same bits again
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_attention_many_rows_masks_and_scales(q, fmt):
+    rng = np.random.default_rng(61)
+    # rows that see nothing, among ones that do
+    c = widen(attn_case(rng, [16, 12], [16, 12], 16, 2, 128, 16, fmt, True))
+    c["masks"][:16] = [0, 1, 0, 0xFFFF0000, 0b1111, 0, 0x80000000, 3, 0, 0, 1 << 9, 0, 0, 0, 0, 0x8000]
+    out = run_attn(q, c)
+    check_attn(out, c)
+    assert not out[0].any() and not out[3].any() and not out[15, :, :].isnan().any() and out[1].any()
+    # a context shorter than the query tokens
+    c = widen(attn_case(rng, [20], [7], 8, 2, 128, 16, fmt, False))
+    out = run_attn(q, c)
+    check_attn(out, c)
+    assert not out[:13].any() and out[13].any()
+    # blocks of zero scale, scales that differ by 2^30, large and tiny queries
+    c = widen(attn_case(rng, [10, 14], [900, 333], 16, 2, 128, 16, fmt, False))
+    c["sc"][::3, :, 1] = 0.0
+    c["sc"][1::3, :, 1] *= np.float32(2.0 ** -30)
+    c["sc"][::5, :, 0] = 0.0
+    c["x"][1] *= 1e-6
+    c["x"][2] *= 40.0
+    check_attn(run_attn(q, c), c)
+    c["sc"][..., 1] = 0.0
+    assert not run_attn(q, c)[:24].any()
+    c["sc"][..., 1] = np.float32(2.0 ** 40)
+    check_attn(run_attn(q, c), c)
+
+
+def test_attention_many_rows_peaked_bad_blocks_and_lengths(q):
+    rng = np.random.default_rng(62)
+    c = widen(attn_case(rng, [14], [2600], 16, 4, 128, 32, "i8", False, qstd=30.0))
+    check_attn(run_attn(q, c), c)
+    check_attn(run_attn(q, c, softmax_scale=1.7), c, 1.7)
+    check_attn(run_attn(q, c, softmax_scale=1e-6), c, 1e-6)
+    c = widen(attn_case(rng, [10, 12], [700, 190], 16, 2, 128, 16, "i8", False))
+    c["table"][0, 3], c["table"][0, 37], c["table"][1, 0] = -1, c["kc"].shape[0], 2 ** 31 - 1
+    c["table"][0, 8:16] = -5                             # a whole step of bad blocks
+    check_attn(run_attn(q, c), c)
+    assert q.device_error(clear=True) == 0x602
+
+
+def test_attention_many_rows_long(q):
+    rng = np.random.default_rng(63)
+    check_attn(run_attn(q, c := widen(attn_case(rng, [9], [40001], 4, 1, 128, 64, "e4m3", False))), c)
+
+
+def test_attention_many_rows_many_requests(q):
+    """More requests than leave room for the third ring stage."""
+    rng = np.random.default_rng(64)
+    c = widen(attn_case(rng, [9] * 1000, [9 + i % 5 for i in range(1000)], 4, 1, 128, 16, "i8", False), 1024)
+    check_attn(run_attn(q, c), c)
+
+
+def test_attention_many_rows_in_a_graph(q):
+    rng = np.random.default_rng(65)
+    c = widen(attn_case(rng, [16, 10], [900, 40], 8, 2, 128, 16, "i8", False))
+    dev = [c["x"].to(DEV), to_cache(c["kc"], "i8"), to_cache(c["vc"], "i8"), torch.from_numpy(c["sc"]).to(DEV),
+           i32(c["table"]), i32(c["ctx"]), i32(c["cu"])]
+    out = torch.full(c["x"].shape, 7.0, device=DEV, dtype=torch.bfloat16)
+    q.attn_kv8_paged(*dev, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.attn_kv8_paged(*dev, out=out)
+    for ctx in ([900, 40], [128, 33], [16, 10]):
+        dev[5].copy_(i32(ctx))
+        for _ in range(2):
+            out.fill_(7.0)
+            g.replay()
+        torch.cuda.synchronize()
+        check_attn(out.cpu(), dict(c, ctx=np.array(ctx)))
+
+
+# --------------------------------------------------------------------------
 # norm
 # --------------------------------------------------------------------------
 
@@ -665,6 +778,17 @@ def test_writes_stay_inside(q):
                          workspace=ws)
         torch.cuda.synchronize()
         assert torch.isfinite(o).all()
+    # attention with many rows
+    kc, vc, sc = random_cache(rng, 9, 2, 16, 128, "i8")
+    x = torch.randn((24, 16, 128), device=DEV).to(torch.bfloat16)
+    table = np.full((2, 65536), -1)
+    table[0, :9], table[1, :9] = np.arange(9), np.arange(9)[::-1]
+    need = q.lib().qg_attn_kv8_workspace_size(16, 2, 128)
+    o = make((24, 16, 128), torch.bfloat16)
+    q.attn_kv8_paged(x, to_cache(kc, "i8"), to_cache(vc, "i8"), torch.from_numpy(sc).to(DEV), i32(table), i32([144, 130]),
+                     i32([0, 10, 24]), out=o, workspace=make((need,), torch.uint8).zero_())
+    torch.cuda.synchronize()
+    assert torch.isfinite(o).all()
     # norm
     for M, K in ((3, 96), (2, 8224)):
         x = torch.randn((M, K), device=DEV)
