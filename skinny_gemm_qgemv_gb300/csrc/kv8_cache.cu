@@ -131,17 +131,35 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
 #pragma unroll 1
   for (int t0 = 4 * gid; t0 < a.max_tokens; t0 += 4 * nthreads) {
     int slot[4], pos[4];
-    int r = t0 < tokens ? last_not_above(tok_ex, a.R, t0) : 0;
+    // the request, its block and the place in it move on from token to token
+    int r = -1, p = 0, end = t0, blk = 0, b = 0, off = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + i;
       slot[i] = pos[i] = -1;
       if (t < tokens) {
-        while (tok_ex[r + 1] <= t) ++r;
-        const int p = olds[r] + t - tok_ex[r], b = p / a.bs, have = blocks[r].x;
-        const int blk = b < have ? a.table[(size_t)r * a.max_blocks + b] : taken(take_ex[r] + b - have);
-        slot[i] = blk * a.bs + p - b * a.bs;
+        bool look = off == a.bs;
+        if (t >= end) {
+          if (r < 0)
+            r = last_not_above(tok_ex, a.R, t);
+          else
+            while (tok_ex[r + 1] <= t) ++r;
+          end = tok_ex[r + 1];
+          p = olds[r] + t - tok_ex[r];
+          b = p / a.bs;
+          off = p - b * a.bs;
+          look = true;
+        } else if (look) {
+          ++b;
+          off = 0;
+        }
+        if (look) {
+          const int have = blocks[r].x;
+          blk = b < have ? a.table[(size_t)r * a.max_blocks + b] : taken(take_ex[r] + b - have);
+        }
+        slot[i] = blk * a.bs + off;
         pos[i] = p;
+        ++off, ++p;
       }
     }
     if (t0 + 4 <= a.max_tokens) {
@@ -351,8 +369,9 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(ReadArgs a) {
 }  // namespace
 
 cudaError_t launch_kv8_plan(const PlanArgs& a, cudaStream_t stream, bool pdl) {
+  // four tokens a thread; each CTA forms the sums anew (a few us, side by side)
   const int ctas =
-      std::min(device_sm_count(), std::max(1, (a.max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads)));
+      std::min(4 * device_sm_count(), std::max(1, (a.max_tokens + 4 * kPlanThreads - 1) / (4 * kPlanThreads)));
   const size_t smem = sizeof(int) * (6 * (size_t)a.R + 8);
   if (smem > 40 << 10) {
     cudaError_t e = allow_max_smem(kv8_plan_kernel);
