@@ -63,7 +63,7 @@ __device__ __forceinline__ float ex2(float x) {
 // item has ceil(tokens / tokens of a step) steps. Shares are cut on a scale on which an
 // item also costs some steps before its first one: what beginning and ending it
 // takes (a batch of 32 requests of 1..8192 tokens, where one CTA can
-// meet 20 short items: 82 -> XX us).
+// meet 20 short items: 82 -> 60 us).
 struct AttnBatch {
   const int* first;  // [R + 1] steps before the request
   const int* cost;   // [R + 1] the same with every item's cost
