@@ -41,12 +41,16 @@ __device__ __forceinline__ void kv8_decode4(uint32_t w, float& a, float& b, floa
   }
 }
 
-// four fp32 to the nearest codes (ties to even, clamped to +-qmax), first in the low byte
+// 1.5 * 2^23: added to |v| < 2^22 it leaves v rounded to the nearest integer (ties to even) in the low bits
+constexpr float kRoundInt = 12582912.f;
+
+// four fp32 to the nearest codes (ties to even), first in the low byte; int8: |v| < 127.5, e4m3 is clamped to +-448
 template <int FMT>
 __device__ __forceinline__ uint32_t kv8_encode4(float a, float b, float c, float d) {
   if (FMT == QG_KV_I8) {
-    auto q = [](float v) { return (uint32_t)(int)fminf(fmaxf(rintf(v), -127.f), 127.f) & 0xFFu; };
-    return q(a) | q(b) << 8 | q(c) << 16 | q(d) << 24;
+    const uint32_t lo = __byte_perm(__float_as_uint(a + kRoundInt), __float_as_uint(b + kRoundInt), 0x0040),
+                   hi = __byte_perm(__float_as_uint(c + kRoundInt), __float_as_uint(d + kRoundInt), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
   }
   uint16_t lo, hi;  // saturates at +-448
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -60,6 +64,8 @@ __device__ __forceinline__ uint32_t kv8_encode4(float a, float b, float c, float
 // int8: only where that product lies within 1e-4 of a border between two codes
 // are the divisions made; e4m3: only where v times the reciprocals 2^-21 to
 // either side of 1 / s gives two different codes (about 1 in 5000 values each).
+// A quotient passes +-127 by a few ulp only, as s is the largest value / 127
+// rounded, except where s is subnormal: the divided ones are clamped.
 template <int FMT>
 __device__ __forceinline__ uint2 kv8_quantize8(const float (&v)[8], float s, float inv) {
   bool close = !(s > 1e-30f);
@@ -69,7 +75,7 @@ __device__ __forceinline__ uint2 kv8_quantize8(const float (&v)[8], float s, flo
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       q[j] = v[j] * inv;
-      close |= !(fabsf(q[j] - rintf(q[j])) < 0.4999f);
+      close |= !(fabsf(q[j] - ((q[j] + kRoundInt) - kRoundInt)) < 0.4999f);
     }
     codes = make_uint2(kv8_encode4<FMT>(q[0], q[1], q[2], q[3]), kv8_encode4<FMT>(q[4], q[5], q[6], q[7]));
   } else {
@@ -81,7 +87,10 @@ __device__ __forceinline__ uint2 kv8_quantize8(const float (&v)[8], float s, flo
   }
   if (close) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(v[j], s);
+    for (int j = 0; j < 8; ++j) {
+      q[j] = __fdiv_rn(v[j], s);
+      if (FMT == QG_KV_I8) q[j] = fminf(fmaxf(q[j], -127.f), 127.f);
+    }
     codes = make_uint2(kv8_encode4<FMT>(q[0], q[1], q[2], q[3]), kv8_encode4<FMT>(q[4], q[5], q[6], q[7]));
   }
   return codes;
