@@ -30,6 +30,15 @@
  *    transform (random sign flips, then a +-1 Hadamard per 32-value block)
  *    spreads outliers, and it is exactly invertible.
  *
+ *  kv8_block_plan / kv8_append / kv8_read / attn_kv8_paged
+ *    The paged key/value cache in 8 bits with a scale per block and head, and
+ *    the attention of decode steps, draft trees and prompt pieces over it: a
+ *    long context is read once per step at half the bytes of bf16.
+ *
+ *  rmsnorm_residual / rmsnorm_residual_i8
+ *    Residual addition and RMS norm in one pass, as the products' bf16 or int8
+ *    activations (with the same randomized Hadamard transform).
+ *
  * Conventions shared by every entry point
  *  - Every array pointer is a DEVICE pointer (global memory of the current
  *    device). The caller allocates and owns all of them; the library never
@@ -550,6 +559,10 @@ QG_API size_t qg_w8a8_hadamard_workspace_size(int M, int K);
  * max_blocks entries; entries past a request's last block are not read.
  * Sizes whose products pass 2^31 are addressed in 64 bits;
  * num_blocks * block_size < 2^31 (slots are int32).
+ *
+ * The kernels of this section are always launched with programmatic dependent
+ * launch, whatever qg_set_pdl says: each touches memory only after the work
+ * before it on the stream has ended, so the order of a stream holds.
  */
 typedef enum { QG_KV_I8 = 0, QG_KV_E4M3 = 1 } qg_kv_format;
 typedef enum { QG_DT_BF16 = 0, QG_DT_F32 = 1 } qg_dtype;
@@ -658,8 +671,8 @@ QG_API qg_status kv8_read(const int32_t *block_ids, int B, int Hkv, int D, int b
  *                sum_j p_j v_j, p = softmax over the seen tokens j of
  *                softmax_scale * q . k_j; 0 where no token is seen. Rows of T
  *                past cu_q[R] are not written.
- *   R 1..1024, T >= 1, D a multiple of 16 in 16..256 (64, 128 and 256 run on
- *   the tensor cores, the others on a plain kernel), Hq <= 1024.
+ *   R 1..1024, T >= 1, D a multiple of 16 in 16..256 (heads are filled
+ *   up with zeros to 64, 128 or 256 on the chip, not in memory), Hq <= 1024.
  *   workspace    qg_attn_kv8_workspace_size(Hq, Hkv, D) bytes, 16-byte aligned,
  *                zero-filled before its first use: its counters are left at
  *                zero by every call, the rest is scratch. Calls that may
@@ -667,6 +680,8 @@ QG_API qg_status kv8_read(const int32_t *block_ids, int B, int Hkv, int D, int b
  * Scores, maxima and sums are fp32, probabilities enter the value product as
  * fp16 (relative rounding 2^-11); the split of a context over the GPU, and so
  * the order of the sums, depends on the shapes and lengths alone.
+ * QG_ERR_UNSUPPORTED: more than 2^31 - 1 steps of 128 tokens, were every table
+ * row full: about Hkv (T (Hq / Hkv) / 8 + 2 R) (max_blocks block_size / 128 + 10).
  */
 QG_API qg_status attn_kv8_paged(const uint16_t *q_bf16, int64_t q_stride, const void *k_cache,
                                 const void *v_cache, const float *scales, const int32_t *block_table,
@@ -718,7 +733,9 @@ typedef enum {
   QG_OP_MOE_MXFP4 = 2,      /* moe_mxfp4_expert_forward */
   QG_OP_HADAMARD_I8 = 3,    /* hadamard32_quant_i8 (none) */
   QG_OP_W8A8_I32 = 4,       /* gemm_w8a8_i32 (none) */
-  QG_OP_W8A8_HADAMARD = 5   /* gemm_w8a8_hadamard */
+  QG_OP_W8A8_HADAMARD = 5,  /* gemm_w8a8_hadamard */
+  QG_OP_KV8_PLAN = 6,       /* kv8_block_plan */
+  QG_OP_ATTN_KV8 = 7        /* attn_kv8_paged: M = Hq, N = Hkv, K = D */
 } qg_op;
 
 QG_API size_t qg_workspace_size(int op, int M, int N, int K, int T, int E, int top_k);

@@ -43,7 +43,8 @@ EXPORTS = [
     "qg_attn_kv8_workspace_size", "rmsnorm_residual", "rmsnorm_residual_i8",
 ]
 
-OP_GEMV_W4A16, OP_SKINNY_W4A16, OP_MOE_MXFP4, OP_HADAMARD_I8, OP_W8A8_I32, OP_W8A8_HADAMARD = range(6)
+(OP_GEMV_W4A16, OP_SKINNY_W4A16, OP_MOE_MXFP4, OP_HADAMARD_I8, OP_W8A8_I32, OP_W8A8_HADAMARD, OP_KV8_PLAN,
+ OP_ATTN_KV8) = range(8)
 
 X_BF16, X_COPY, X_SWIGLU = 0, 1, 2
 

@@ -382,6 +382,8 @@ size_t qg_workspace_size(int op, int M, int N, int K, int T, int E, int top_k) {
     case QG_OP_SKINNY_W4A16: return qg_skinny_workspace_size(M, N, K, 64);
     case QG_OP_MOE_MXFP4: return qg_moe_workspace_size(T, N, K, E, top_k);
     case QG_OP_W8A8_HADAMARD: return qg_w8a8_hadamard_workspace_size(M, K);
+    case QG_OP_KV8_PLAN: return qg_kv8_plan_workspace_size();
+    case QG_OP_ATTN_KV8: return qg_attn_kv8_workspace_size(M, N, K);
     default: return 0;  // the Hadamard quantizer and the int32 W8A8 product need none
   }
 }

@@ -1,9 +1,28 @@
-// Attention of a step's query tokens over the paged 8-bit key/value cache.
+// Attention of a step's query tokens over the paged 8-bit key/value cache, with
+// warp-level matrix instructions: up to 16 query rows (query tokens times the
+// query heads of a group) per pass over the cache.
 //
-// attn_kv8_plain_kernel: one CTA per (query token, query head), four warps that
-// take the context's tokens in turn; a lane holds D / 32 (rounded up to words)
-// elements of q and of the output. One pass with the running maximum and sum of
-// the softmax.
+//   t = (q . k) (ks scale log2 e) + log2(vs)    k, v: codes; ks, vs: the block's scales
+//   p = 2^(t - m),  acc += p v,  l += p / vs,   out = acc / l
+//
+// The value scale enters through the exponent, so codes are multiplied as they
+// are: int8 and e4m3 are exact in fp16, and so is q after an exact power of two
+// per row; p is rounded to fp16 (2^-11 relative), everything else is fp32. The
+// running maximum m moves only when a score passes it by 2^8: p stays below
+// 2^8, far inside fp16, and a step without such a score scales nothing.
+//
+// The cache is read once, so HBM bounds it: the GPU's steps (of 256 tokens of a
+// key/value head) are dealt to one CTA per SM in equal shares, wherever a
+// context begins or ends; each of a CTA's 8 warps takes 32 tokens of a step
+// through a TMA ring of its own (no barrier between warps until an item ends).
+// Keys come out of the swizzled ring as A fragments of S^T = K q^T, values
+// through ldmatrix's byte transposition as A fragments of O^T = V^T P^T: nothing
+// is converted twice and nothing goes back to shared memory. Pieces of a context
+// cut by shares are added up by the CTA that brings the last one.
+// Measured (32 query heads, 8 key/value heads of 128, int8): 131071 tokens 53.6 us,
+// 268 MB at 5.0 TB/s; the streaming itself runs at 6.7 TB/s, and 12 us go to the
+// launch, the first copies and the joining of pieces. 32 requests of 1..8192
+// tokens: 54.4 us, 270 MB. One token over 37 tokens: 6.5 us, all latency.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -16,115 +35,12 @@
 namespace qg {
 namespace {
 
-constexpr int kPlainWarps = 4;
-
-template <int FMT>
-__global__ void __launch_bounds__(32 * kPlainWarps) attn_kv8_plain_kernel(AttnArgs a) {
-  __shared__ float sm_m[kPlainWarps], sm_l[kPlainWarps], sm_o[kPlainWarps][256];
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x, hq = blockIdx.y, h = hq / (a.Hq / a.Hkv);
-  if (t < a.cu_q[0] || t >= a.cu_q[a.R]) return;
-  int r = 0;
-  for (int hi = a.R; hi - r > 1;) {
-    const int mid = (r + hi) >> 1;
-    if (a.cu_q[mid] <= t)
-      r = mid;
-    else
-      hi = mid;
-  }
-  const int n = a.cu_q[r + 1] - a.cu_q[r];
-  int ctx = max(a.ctx_lens[r], 0);
-  if (ctx > a.max_blocks * a.bs) {
-    if (threadIdx.x == 0) report_error(a.err, kErrKvLength);
-    ctx = a.max_blocks * a.bs;
-  }
-  const int base = ctx - n;  // first query token's position
-  const bool tree = a.tree && n <= 32;
-  const uint32_t bits = tree ? a.tree[t] : 0u;
-  const int end = tree ? ctx : min(ctx, base + (t - a.cu_q[r]) + 1);
-  const int words = a.D / 4;
-  float q[2][4] = {}, o[2][4] = {};
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int i = lane + 32 * w;
-    if (i < words) {
-      const uint2 v = *reinterpret_cast<const uint2*>(a.q + t * a.q_stride + (size_t)hq * a.D + 4 * i);
-      q[w][0] = bf16_bits_to_f32(v.x & 0xFFFFu), q[w][1] = bf16_bits_to_f32(v.x >> 16);
-      q[w][2] = bf16_bits_to_f32(v.y & 0xFFFFu), q[w][3] = bf16_bits_to_f32(v.y >> 16);
-    }
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int tok = warp; tok < end; tok += kPlainWarps) {
-    if (tree && tok >= base && !(tok - base < 32 && (bits >> (tok - base) & 1u))) continue;
-    const int blk = a.table[(size_t)r * a.max_blocks + tok / a.bs];
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (lane == 0) report_error(a.err, kErrKvBlock);
-      continue;
-    }
-    const size_t page = (size_t)blk * a.Hkv + h;
-    const size_t at = (page * a.bs + tok % a.bs) * a.D;
-    const float ks = a.scales[2 * page], vs = a.scales[2 * page + 1];
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int i = lane + 32 * w;
-      if (i < words) {
-        float k0, k1, k2, k3;
-        kv8_decode4<FMT>(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.k_cache) + at + 4 * i), k0, k1,
-                         k2, k3);
-        s += q[w][0] * k0 + q[w][1] * k1 + q[w][2] * k2 + q[w][3] * k3;
-      }
-    }
-    s = warp_sum(s) * (ks * a.scale_log2);
-    const float mn = fmaxf(m, s);
-    const float c = mn == -INFINITY ? 1.f : exp2f(m - mn), p = mn == -INFINITY ? 0.f : exp2f(s - mn);
-    m = mn;
-    l = l * c + p;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int i = lane + 32 * w;
-      if (i < words) {
-        float v0, v1, v2, v3;
-        kv8_decode4<FMT>(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v_cache) + at + 4 * i), v0, v1,
-                         v2, v3);
-        const float pv = p * vs;
-        o[w][0] = o[w][0] * c + pv * v0;
-        o[w][1] = o[w][1] * c + pv * v1;
-        o[w][2] = o[w][2] * c + pv * v2;
-        o[w][3] = o[w][3] * c + pv * v3;
-      }
-    }
-  }
-  if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
-#pragma unroll
-  for (int w = 0; w < 2; ++w)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + 32 * w < words) sm_o[warp][4 * (lane + 32 * w) + j] = o[w][j];
-  __syncthreads();
-  float mm = sm_m[0];
-  for (int w = 1; w < kPlainWarps; ++w) mm = fmaxf(mm, sm_m[w]);
-  float ll = 0.f, f[kPlainWarps];
-  for (int w = 0; w < kPlainWarps; ++w) {
-    f[w] = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - mm);
-    ll += sm_l[w] * f[w];
-  }
-  uint32_t* out = reinterpret_cast<uint32_t*>(a.out + ((size_t)t * a.Hq + hq) * a.D);
-  for (int i = threadIdx.x; i < a.D / 2; i += blockDim.x) {
-    float x = 0.f, y = 0.f;
-    for (int w = 0; w < kPlainWarps; ++w) x += f[w] * sm_o[w][2 * i], y += f[w] * sm_o[w][2 * i + 1];
-    const bool none = mm == -INFINITY;  // no token seen
-    out[i] = f32_to_bf16x2(none ? 0.f : x / ll, none ? 0.f : y / ll);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// The tensor-core kernel: D = 64, 128 or 256
-// ---------------------------------------------------------------------------
+// An item costs about as much as 3 steps to begin and end (2.7 us); one of up to 6 steps is not cut: joining its pieces
+// takes longer (4 us) than its steps on one CTA.
 constexpr int kItemCost = 3;
-constexpr int kWholeSteps = 6;  // joining the pieces takes longer (4 us)
+constexpr int kWholeSteps = 6;
 
+// D: elements of a head, filled up with zeros to 64, 128 or 256 as the copies land (a.D is what the arrays have)
 template <int D, int NT, int FMT>
 struct AttnShape {
   static constexpr int kWarps = 8;
@@ -242,9 +158,9 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
 #pragma unroll 1
     for (int i = threadIdx.x; i < ROWS * (D / 8); i += 32 * NW) {
       const int rr = i / (D / 8), rho = at.rt * ROWS + rr;
-      const bool live = rho < rows;
+      const bool live = rho < rows && 8 * (i % (D / 8)) < a.D;
       const uint16_t* src = a.q;
-      if (live) src += (q_first + rho / G) * a.q_stride + (size_t)(at.h * G + rho % G) * D + 8 * (i % (D / 8));
+      if (live) src += (q_first + rho / G) * a.q_stride + (at.h * G + rho % G) * a.D + 8 * (i % (D / 8));
       cp_async16(smem_u32(qraw + (size_t)b * ROWS * D * 2 + 16 * i), src, live);
     }
   };
@@ -586,8 +502,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     const float x0 = o.x * i0, x1 = o.y * i1, y0 = o.z * i0, y1 = o.w * i1;
     const float x = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 4), y = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 4);
     const int to = row_info[nt * 8 + 2 * c + odd].z;
-    if (to >= 0) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (size_t)to * D + 16 * mt + (g & 6));
+    if (to >= 0 && 16 * mt < a.D) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (size_t)to * a.D + 16 * mt + (g & 6));
       dst[0] = odd ? f32_to_bf16x2(x, x1) : f32_to_bf16x2(x0, x);
       dst[4] = odd ? f32_to_bf16x2(y, y1) : f32_to_bf16x2(y0, y);
     }
@@ -808,8 +724,8 @@ cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   const int wide = S::kUps == 2 && a.bs % 32 == 0;  // a step's two units in one box
   const auto sw = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   for (int i = 0; i < 2; ++i)
-    if (!tmap_3d(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? a.v_cache : a.k_cache, D, a.bs,
-                 (uint64_t)a.num_blocks * a.Hkv, D, (uint64_t)a.bs * D, S::kRowBytes, wide ? 2 * kUnit : kUnit, 1, sw))
+    if (!tmap_3d(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? a.v_cache : a.k_cache, a.D, a.bs,
+                 (uint64_t)a.num_blocks * a.Hkv, a.D, (uint64_t)a.bs * a.D, S::kRowBytes, wide ? 2 * kUnit : kUnit, 1, sw))
       return cudaErrorInvalidValue;
   auto k = attn_kv8_kernel<D, NT, FMT>;
   cudaError_t e = allow_max_smem(k);
@@ -819,14 +735,16 @@ cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
                        l.ring, wide);
 }
 
+// the width a head of D elements is filled up to
+int attn_width(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // rows of an average request's item
 int attn_rows(const AttnArgs& a) { return (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv); }
-// The tcgen05 kernel for many rows of 128 elements. This file's kernel passes over the cache once per 16 rows, at 5 ns
+// The tcgen05 kernel for many rows of 128 elements (or fewer, filled up). This file's kernel passes over the cache once per 16 rows, at 5 ns
 // per 128 tokens of a head (the HBM rate); that one takes 10 ns per 128 tokens and 64 rows, and 7 us more to begin,
 // end and join (measured: 64 rows, one request: 8192 tokens 23.7 here, 25.4 us there; 32784 tokens 55.5 and 43.5;
 // 32 rows, 32768 tokens: 34.8 and 38.7). The lengths are known to the GPU alone, so their bound decides.
 bool attn_tc_ok(const AttnArgs& a) {
-  if (a.D != 128) return false;
+  if (attn_width(a.D) != 128) return false;
   const long long rows = attn_rows(a), steps = (long long)a.R * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128);
   return steps * (5 * ((rows + 15) / 16) - 10 * ((rows + 63) / 64)) >= 7000;
 }
@@ -835,31 +753,25 @@ bool attn_tc_ok(const AttnArgs& a) {
 template <int FMT>
 cudaError_t launch_by_shape(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   const bool one = attn_rows(a) <= 8;
-  switch (a.D) {
+  switch (attn_width(a.D)) {
     case 64: return one ? launch_mma<64, 1, FMT>(a, stream, pdl) : launch_mma<64, 2, FMT>(a, stream, pdl);
     case 128: return one ? launch_mma<128, 1, FMT>(a, stream, pdl) : launch_mma<128, 2, FMT>(a, stream, pdl);
     default: return one ? launch_mma<256, 1, FMT>(a, stream, pdl) : launch_mma<256, 2, FMT>(a, stream, pdl);
   }
 }
 
-bool attn_mma_dim(int D) { return D == 64 || D == 128 || D == 256; }
-
 }  // namespace
 
 size_t attn_kv8_workspace_size(int, int, int D) {
-  if (!attn_mma_dim(D)) return 0;
-  return kAttnCounterBytes + 2 * (size_t)std::min(device_sm_count(), kMaxCtas) * attn_piece_bytes(D == 256 ? 16 : 64, D);
+  const int w = attn_width(D);
+  return kAttnCounterBytes + 2 * (size_t)std::min(device_sm_count(), kMaxCtas) * attn_piece_bytes(w == 256 ? 16 : 64, w);
 }
 
-bool attn_kv8_ok(const AttnArgs& a) { return !attn_mma_dim(a.D) || attn_most_steps(a) < (1LL << 31); }
+bool attn_kv8_ok(const AttnArgs& a) { return attn_most_steps(a) < (1LL << 31); }
 
 cudaError_t launch_attn_kv8(const AttnArgs& a, int format, cudaStream_t stream, bool pdl) {
   if (attn_tc_ok(a)) return launch_attn_kv8_tc(a, format, stream, pdl);
-  if (attn_mma_dim(a.D))
-    return format == QG_KV_I8 ? launch_by_shape<QG_KV_I8>(a, stream, pdl)
-                              : launch_by_shape<QG_KV_E4M3>(a, stream, pdl);
-  auto k = format == QG_KV_I8 ? attn_kv8_plain_kernel<QG_KV_I8> : attn_kv8_plain_kernel<QG_KV_E4M3>;
-  return launch_kernel(k, dim3(a.T, a.Hq), dim3(32 * kPlainWarps), 0, stream, pdl, a);
+  return format == QG_KV_I8 ? launch_by_shape<QG_KV_I8>(a, stream, pdl) : launch_by_shape<QG_KV_E4M3>(a, stream, pdl);
 }
 
 }  // namespace qg

@@ -10,12 +10,12 @@
 
 namespace qg {
 
-constexpr int kUnit = 16;                       // tokens of one ring stage: one block, one scale pair
+constexpr int kUnit = 16;                       // tokens that lie in one block, whatever its size: one scale pair
 constexpr float kNoMax = -1e30f;                // running maximum before any seen token
 constexpr float kSlack = 8.f;                   // log2: probabilities stay below 2^8 (fp16 holds 2^15)
 constexpr float kMinScale = 5.4210109e-20f;     // 2^-64
 constexpr size_t kAttnCounterBytes = 4096;      // one counter per CTA
-constexpr int kMaxCtas = 160;                   // pieces of an item whose factors fit the combine buffer
+constexpr int kMaxCtas = 160;                   // CTAs, and so pieces of an item: their factors fit the combine buffer
 
 // bytes of the partial results of one CTA's piece: fp32 outputs, then (max, sum) per row
 __host__ __device__ constexpr size_t attn_piece_bytes(int rows, int D) { return (size_t)rows * (D * 4 + 8); }

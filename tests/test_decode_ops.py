@@ -165,3 +165,11 @@ def test_norm_refusals(L):
 
 def test_device_error_status_names(L):
     assert L.qg_status_string(7).startswith(b"QG_ERR_BAD_INDEX")
+
+
+def test_workspace_query(L):
+    import skinny_gemm_qgemv_gb300 as q
+    assert q.workspace_size(q.OP_KV8_PLAN) == L.qg_kv8_plan_workspace_size() > 0
+    for D in (16, 64, 80, 128, 256):
+        assert q.workspace_size(q.OP_ATTN_KV8, M=8, N=2, K=D) == L.qg_attn_kv8_workspace_size(8, 2, D) > 0
+    assert q.workspace_size(q.OP_ATTN_KV8, M=7, N=2, K=128) == 0

@@ -202,6 +202,29 @@ def test_append_strided_padded_and_zero(q):
     assert not ws[0].any() and not wk[0].any()
 
 
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("ulps", [1, 100, 178, 700, 5000, 200000])
+def test_append_subnormal_scales(q, fmt, ulps):
+    """Values of some 2^-149: the scale is subnormal, so a quotient can pass qmax and is clamped there."""
+    rng = np.random.default_rng(ulps)
+    kc, vc, sc = random_cache(rng, 2, 2, 16, 64, fmt)
+    g = torch.Generator().manual_seed(ulps)
+    k, v = ((torch.randint(-ulps, ulps + 1, (16, 2, 64), generator=g).double() * 2.0 ** -149).float() for _ in range(2))
+    k[3, :, 5], v[4, :, 7] = ulps * 2.0 ** -149, -ulps * 2.0 ** -149
+    check_append(q, fmt, torch.float32, k, v, 16 + np.arange(16), kc, vc, sc, 2, 16)
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_append_largest_values(q, fmt):
+    rng = np.random.default_rng(2)
+    kc, vc, sc = random_cache(rng, 2, 2, 16, 64, fmt)
+    top = torch.finfo(torch.float32).max
+    k = torch.rand((16, 2, 64), generator=torch.Generator().manual_seed(1)) * 2 - 1
+    k = k * top
+    k[2, :, 3] = top
+    check_append(q, fmt, torch.float32, k, -k, np.arange(16), kc, vc, sc, 2, 16)
+
+
 def test_bad_slots_and_blocks_are_skipped_and_reported(q):
     rng = np.random.default_rng(7)
     kc, vc, sc = random_cache(rng, 4, 2, 16, 64, "i8")
@@ -303,6 +326,17 @@ def test_attention(q, fmt, nq, ctx, Hq, Hkv, D, bs, tree):
     out = run_attn(q, c)
     check_attn(out, c)
     assert torch.equal(run_attn(q, c), out)  # the same bits again
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("D", [16, 48, 96, 112, 144, 192, 240])
+@pytest.mark.parametrize("nq", [1, 5])
+def test_attention_head_sizes(q, fmt, D, nq):
+    """Heads between the widths that the kernels are made for, alone in a split context and in a ragged batch."""
+    rng = np.random.default_rng(D + nq)
+    for R, ctx in (([nq], [4000]), ([nq, nq, 1], [nq, 333, 61])):
+        c = attn_case(rng, R, ctx, 6, 2, D, 32, fmt, nq > 1)
+        check_attn(run_attn(q, c), c)
 
 
 def test_attention_masks_that_leave_nothing(q):
@@ -510,6 +544,15 @@ def test_attention_many_rows(q, fmt, nq, ctx, Hq, Hkv, bs, tree):
     out = run_attn(q, c)
     check_attn(out, c)
     assert torch.equal(run_attn(q, c), out)  # the same bits again
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("D", [80, 96, 112])
+def test_attention_many_rows_head_sizes(q, fmt, D):
+    rng = np.random.default_rng(D)
+    for nq, ctx in (([12], [6000]), ([9, 16, 1], [9, 700, 130])):
+        c = widen(attn_case(rng, nq, ctx, 16, 2, D, 48, fmt, True))
+        check_attn(run_attn(q, c), c)
 
 
 @pytest.mark.parametrize("fmt", ["i8", "e4m3"])
