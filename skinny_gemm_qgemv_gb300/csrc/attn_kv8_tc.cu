@@ -77,18 +77,21 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_
 __device__ __forceinline__ constexpr uint32_t tc_idesc(int M, int N, bool a_mn, bool b_mn) {
   return 1u << 4 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Issued where `one` is set (one lane), by code that the whole warp runs: descriptors are then uniform registers.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&v)[32]) {
@@ -394,42 +397,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 15) {
     // ------------------------------------------------ MMAs
-    if (lane == 0) {
-      const uint32_t qs = smem_u32(qbuf), io = tc_idesc(D, ROWS, true, true);
-      bool ok = true;
-      while (ok && next_segment(sg, step)) {
-        const uint32_t is = tc_idesc(128, 16 * sg.nch, false, false);
-        const int n = sg.n, gi = sg.g;
-        ok = wait(&q_full, sg.index & 1);
+    const uint32_t qs = smem_u32(qbuf), io = tc_idesc(D, ROWS, true, true), one = lane == 0;
+    bool ok = true;
+    while (ok && next_segment(sg, step)) {
+      const uint32_t is = tc_idesc(128, 16 * sg.nch, false, false);
+      const int n = sg.n, gi = sg.g;
+      ok = wait_warp(&q_full, sg.index & 1);
 #pragma unroll 1
-        for (int i = 0; i <= n && ok; ++i) {
-          if (i < n) {
-            const int g = gi + i, b = g & 1;
-            ok = wait(k_full + b, (g >> 1) & 1) && (g < 2 || wait(s_empty + b, ((g >> 1) - 1) & 1));
-            if (!ok) break;
-            tc_after();
-#pragma unroll 1
-            for (int k = 0; k < D / 16; ++k)
-              mma_ts(tbase + S::kColS + b * ROWS, tbase + S::kColK + b * (D / 2) + 8 * k,
-                     tc_desc(qs + (k >> 2) * ROWS * 128 + (k & 3) * 32, 16, 1024), is, k > 0);
-            tc_commit(s_full + b);
-          }
-          if (i > 0) {
-            const int g = gi + i - 1, b = g & 1;
-            ok = wait(p_full + b, (g >> 1) & 1) && wait(v_full + b, (g >> 1) & 1);
-            if (!ok) break;
-            tc_after();
-            const uint32_t vs = smem_u32(vbuf + b * S::kV), ps = smem_u32(pbuf + b * S::kP);
-#pragma unroll 1
-            for (int k = 0; k < TOK / 16; ++k)
-              mma_ss(tbase + S::kColO, tc_desc(vs + k * 2048, TOK * 128, 1024), tc_desc(ps + k * 2048, TOK * 128, 1024), io,
-                     i > 1 || k > 0);
-            tc_commit(o_done + b);
-          }
+      for (int i = 0; i <= n && ok; ++i) {
+        if (i < n) {
+          const int g = gi + i, b = g & 1;
+          ok = wait_warp(k_full + b, (g >> 1) & 1) && (g < 2 || wait_warp(s_empty + b, ((g >> 1) - 1) & 1));
+          if (!ok) break;
+          tc_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ts(tbase + S::kColS + b * ROWS, tbase + S::kColK + b * (D / 2) + 8 * k,
+                   tc_desc(qs + (k >> 2) * ROWS * 128 + (k & 3) * 32, 16, 1024), is, k > 0, one);
+          if (one) tc_commit(s_full + b);
+          __syncwarp();
+        }
+        if (i > 0) {
+          const int g = gi + i - 1, b = g & 1;
+          ok = wait_warp(p_full + b, (g >> 1) & 1) && wait_warp(v_full + b, (g >> 1) & 1);
+          if (!ok) break;
+          tc_after();
+          const uint32_t vs = smem_u32(vbuf + b * S::kV), ps = smem_u32(pbuf + b * S::kP);
+#pragma unroll
+          for (int k = 0; k < TOK / 16; ++k)
+            mma_ss(tbase + S::kColO, tc_desc(vs + k * 2048, TOK * 128, 1024), tc_desc(ps + k * 2048, TOK * 128, 1024), io,
+                   k > 0 ? 1u : i > 1, one);
+          if (one) tc_commit(o_done + b);
+          __syncwarp();
         }
       }
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------ softmax: a token per thread, half of the rows
     constexpr int HR = ROWS / 2;
@@ -537,6 +539,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint64_t ks2 = both(now.x * up), lv2 = both(lv), inv2 = both(ex2(-lv));  // (not 1 / vs: what comes off is what went on)
         const bool edge = __any_sync(0xffffffffu, !there || tok >= base);
         // (After a wait that gave up every later one returns at once: the warps stay in step at their barriers.)
+        uint64_t c[HR / 2];  // log2 of the value scale, less the row's m
+#pragma unroll
+        for (int j = 0; j < HR; j += 4) {
+          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(nm_of + j);
+          c[j / 2] = fadd2(lv2, nm.x), c[j / 2 + 1] = fadd2(lv2, nm.y);
+        }
+        // (all of them here: loaded one after the other where they are used they take 0.3 us of a step)
+#pragma unroll
+        for (int j = 0; j < HR / 2; ++j) asm volatile("" : "+l"(c[j]));
         wait_warp(s_full + b, (g >> 1) & 1);
         tc_after();
         float y[HR];
@@ -551,14 +562,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(s_empty + b);
         bool grow = unset;
 #pragma unroll
-        for (int j = 0; j < HR; j += 4) {
-          if (j / 16 < hch) {
-            const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(nm_of + j);
-            unpair2(ffma2(pair2(__float_as_uint(y[j]), __float_as_uint(y[j + 1])), ks2, fadd2(lv2, nm.x)), y[j], y[j + 1]);
-            unpair2(ffma2(pair2(__float_as_uint(y[j + 2]), __float_as_uint(y[j + 3])), ks2, fadd2(lv2, nm.y)), y[j + 2],
-                    y[j + 3]);
-          }
-        }
+        for (int j = 0; j < HR; j += 2)
+          if (j / 16 < hch)
+            unpair2(ffma2(pair2(__float_as_uint(y[j]), __float_as_uint(y[j + 1])), ks2, c[j / 2]), y[j], y[j + 1]);
         if (edge) {
           const unsigned d = (unsigned)(tok - base);
 #pragma unroll
@@ -579,7 +585,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         grow |= fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kSlack;
-        if (g >= 2) wait_warp(o_done + b, ((g >> 1) - 1) & 1);  // P of two steps ago has been read
+        // (P of two steps ago has been read: its product was issued before this step's S, whose end has been waited for)
         if (named_barrier_or<128>(bar, grow)) {
           // rows whose m has to rise (or to be set): the largest y over the step's tokens
           {
