@@ -335,12 +335,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
         for (int t = (warp - 12) * 32 + lane; t < TOK; t += 64) {
           const uint32_t dst = smem_u32(vbuf + b * S::kV) + t * 128;
-          const bool none = sg.tok0 + i * TOK + t >= sg.ctx;  // slots past the context may hold codes that are not numbers
 #pragma unroll
           for (int ch = 0; ch < D / 16; ++ch) {
             const uint32_t at = t * 128 + ((ch ^ (t & 7)) << 4);
-            uint4 w = lds128(src + at);
-            if (none) w = make_uint4(0u, 0u, 0u, 0u);
+            const uint4 w = lds128(src + at);
             uint4 f[2];
             codes_to_f16<FMT>(w.x, f[0].x, f[0].y);
             codes_to_f16<FMT>(w.y, f[0].z, f[0].w);
@@ -351,6 +349,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int c8 = 2 * ch + k;  // 8-element chunk of the row
               sts128(dst + (c8 >> 3) * TOK * 128 + (((c8 & 7) ^ (t & 7)) << 4), f[k]);
             }
+          }
+          // slots past the context may hold codes that are not numbers
+          if (sg.tok0 + i * TOK + t >= sg.ctx) {
+#pragma unroll 1
+            for (int ch = 0; ch < 16; ++ch) sts128(dst + (ch >> 3) * TOK * 128 + ((ch & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
           }
         }
         fence_async_smem();
@@ -566,15 +569,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (j / 16 < hch)
             unpair2(ffma2(pair2(__float_as_uint(y[j]), __float_as_uint(y[j + 1])), ks2, c[j / 2]), y[j], y[j + 1]);
         if (edge) {
+          // which rows see the token (a rolled loop: this code is met once or twice and has to be fetched)
           const unsigned d = (unsigned)(tok - base);
-#pragma unroll
-          for (int j = 0; j < HR; ++j) {
-            if (j / 16 < hch) {
-              const int2 lim = *reinterpret_cast<const int2*>(row_info + hc + j);
-              const bool seen = there && (tok < lim.x || (d < 32u && ((unsigned)lim.y >> d & 1u)));
-              if (!seen) y[j] = -INFINITY;
-            }
+          uint32_t seen = 0u;
+#pragma unroll 2
+          for (int j = 0; j < 16 * hch; ++j) {
+            const int2 lim = *reinterpret_cast<const int2*>(row_info + hc + j);
+            seen |= (tok < lim.x || (d < 32u && ((unsigned)lim.y >> d & 1u)) ? 1u : 0u) << j;
           }
+          if (!there) seen = 0u;
+#pragma unroll
+          for (int j = 0; j < HR; ++j)
+            if (j / 16 < hch) y[j] = seen >> j & 1u ? y[j] : -INFINITY;
         }
         float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -640,7 +646,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         // p, its sum without the value scale, and as fp16 in shared memory (of a block of zero scale nothing)
         const uint32_t dst = smem_u32(pbuf + b * S::kP) + t * 128;
-        const bool zero = now.y == 0.f;
+        const bool zero = now.y == 0.f, some_zero = __any_sync(0xffffffffu, zero);
 #pragma unroll
         for (int c8 = 0; c8 < HR / 8; ++c8) {
           if (c8 / 2 < hch) {
@@ -650,7 +656,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int j = 8 * c8 + 2 * k;
               const float e0 = ex2(y[j]), e1 = ex2(y[j + 1]);
               l[j / 2] = ffma2(pair2(__float_as_uint(e0), __float_as_uint(e1)), inv2, l[j / 2]);
-              f[k] = zero ? 0u : f16x2(e0, e1);
+              f[k] = f16x2(e0, e1);
+            }
+            if (some_zero) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) f[k] = zero ? 0u : f[k];
             }
             sts128(dst + (((c8 + hc / 8) ^ (t & 7)) << 4), make_uint4(f[0], f[1], f[2], f[3]));
           }
@@ -678,7 +688,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float L = (wsum[0][j] + wsum[1][j]) + (wsum[2][j] + wsum[3][j]);
         if (!whole)
           reinterpret_cast<float2*>(piece + (size_t)ROWS * D * 4)[j] = make_float2(L > 0.f ? -neg_m[j] : kNoMax, L);
-        sums[j] = !whole ? 1.f : L == 0.f ? 0.f : __frcp_rn(L);  // what the outputs are multiplied with
+        sums[j] = L == 0.f ? 0.f : __frcp_rn(L);  // what the outputs are multiplied with
       }
       named_barrier<128>(bar);
       // ---- the segment's results ----
@@ -690,15 +700,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           float o[16];
           tmem_ld16(t_o + 16 * ch, o);
           tmem_wait_ld(o);
+          const int j0 = hc + 16 * ch;
+          if (!whole) {
+            float* dst = reinterpret_cast<float*>(piece) + j0 * D + t;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int rr = hc + 16 * ch + j, to = row_info[rr].z;
-            const float f = sums[rr], v = f == 0.f ? 0.f : o[j] * f;
-            if (to >= 0) {
-              if (!whole)
-                reinterpret_cast<float*>(piece)[rr * D + t] = v;
-              else if (t < a.D)
-                a.out[(size_t)to * a.D + t] = (uint16_t)f32_to_bf16x2(v, 0.f);
+            for (int j = 0; j < 16; ++j) dst[j * D] = o[j];  // (rows past the item's are scratch)
+          } else if (t < a.D) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int to = row_info[j0 + j].z;
+              const float f = sums[j0 + j];
+              if (to >= 0) a.out[(size_t)to * a.D + t] = (uint16_t)f32_to_bf16x2(f == 0.f ? 0.f : o[j] * f, 0.f);
             }
           }
         }
@@ -734,53 +746,108 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // Adds up the pieces of the items that go over several CTAs' shares, in the order
-// of the CTAs. CTA (b, y): 16 rows of the item that begins in CTA b's share and
-// goes on after it. One CTA adding up an item's 64 rows from 19 pieces took
-// 30 us of 61; here every SM takes part, after the kernel's end.
-constexpr int kJoinRows = 16;
-__global__ void __launch_bounds__(kJoinRows * D / 4) attn_kv8_join_kernel(AttnArgs a) {
-  __shared__ float factor[kTcMaxCtas][kJoinRows], sums[kJoinRows];
+// of the CTAs. A unit is four rows of an item; the units are dealt over the grid.
+// A row's 128 elements are a warp's, four warps share a row's pieces.
+constexpr int kJoinRows = 4, kJoinParts = 4;
+constexpr int kJoinThreads = 32 * kJoinRows * kJoinParts;
+__global__ void __launch_bounds__(kJoinThreads) attn_kv8_join_kernel(AttnArgs a, int ctas) {
+  __shared__ int4 items[kTcMaxCtas];  // .x: first CTA | rows << 16
+  __shared__ int pieces_of[kTcMaxCtas], unit_end[kTcMaxCtas], found;
+  __shared__ float4 part[kJoinParts][kJoinRows][32];
+  __shared__ float2 stat[kJoinParts][kJoinRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.Hq / a.Hkv;
+  const int row = warp % kJoinRows, mine = warp / kJoinRows;
   pdl_wait();
   pdl_launch_dependents();
-  const int4 split = tc_splits(a.ws)[blockIdx.x];
-  const int pieces = split.x & 0xFFFF, r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, (split.x >> 16) - r0);
-  if (pieces < 2 || rows <= 0) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.Hq / a.Hkv;
-  const uint8_t* ws = static_cast<const uint8_t*>(a.ws) + kAttnCounterBytes;
-  auto piece = [&](int i) {
-    return ws + (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * attn_piece_bytes(kTcRows, D);
-  };
+  if (warp == 0) {  // the items that are in pieces, and their units' prefix sums
+    int n = 0, units = 0;
 #pragma unroll 1
-  for (int rr = warp; rr < rows; rr += kJoinRows * D / 128) {
-    float mm = kNoMax, ll = 0.f;
-    for (int i = lane; i < pieces; i += 32)
-      mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)kTcRows * D * 4) + r0 + rr).x);
+    for (int c0 = 0; c0 < ctas; c0 += 32) {
+      const int4 s = c0 + lane < ctas ? tc_splits(a.ws)[c0 + lane] : make_int4(0, 0, 0, 0);
+      const bool in = (s.x & 0xFFFF) >= 2;
+      const unsigned votes = __ballot_sync(0xffffffffu, in);
+      int u = in ? ((s.x >> 16) + kJoinRows - 1) / kJoinRows : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    for (int i = lane; i < pieces; i += 32) {
-      const float2 st = __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)kTcRows * D * 4) + r0 + rr);
-      const float x = ex2(st.x - mm);
-      factor[i][rr] = x;
-      ll = fmaf(st.y, x, ll);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, u, o);
+        if (lane >= o) u += x;
+      }
+      if (in) {
+        const int at = n + __popc(votes & ((1u << lane) - 1u));
+        items[at] = make_int4((c0 + lane) | (s.x >> 16) << 16, s.y, s.z, s.w);
+        pieces_of[at] = s.x & 0xFFFF;
+        unit_end[at] = units + u;
+      }
+      n += __popc(votes);
+      units += __shfl_sync(0xffffffffu, u, 31);
     }
-    ll = warp_sum(ll);
-    if (lane == 0) sums[rr] = ll;
+    if (lane == 0) found = n;
   }
-  const int rr = tid / (D / 4), d = tid % (D / 4) * 4;
   __syncthreads();
-  if (rr >= rows || d >= a.D) return;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = 0; i < pieces; ++i) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(i)) + (r0 + rr) * (D / 4) + d / 4);
-    const float fa = factor[i][rr];
-    o.x = fmaf(v.x, fa, o.x), o.y = fmaf(v.y, fa, o.y), o.z = fmaf(v.z, fa, o.z), o.w = fmaf(v.w, fa, o.w);
+  const int n = found;
+  const uint8_t* ws = static_cast<const uint8_t*>(a.ws) + kAttnCounterBytes;
+#pragma unroll 1
+  for (int unit = blockIdx.x, it = 0; n > 0 && unit < unit_end[n - 1]; unit += gridDim.x) {
+    while (unit >= unit_end[it]) ++it;
+    const int4 item = items[it];
+    const int first = item.x & 0xFFFF, rows = item.x >> 16, pieces = pieces_of[it];
+    const int rr = (unit - (it > 0 ? unit_end[it - 1] : 0)) * kJoinRows + row;
+    auto piece = [&](int i) {
+      return ws + (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * attn_piece_bytes(kTcRows, D);
+    };
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = kNoMax, l = 0.f;
+    if (rr < rows) {
+      // pieces mine, mine + 4, ..., eight on the way at a time, with a running maximum
+#pragma unroll 1
+      for (int i0 = mine; i0 < pieces; i0 += 8 * kJoinParts) {
+        float2 st[8];
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int i = i0 + k * kJoinParts;
+          if (i < pieces) {
+            st[k] = __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)kTcRows * D * 4) + rr);
+            v[k] = __ldcg(reinterpret_cast<const float4*>(piece(i)) + rr * (D / 4) + lane);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (i0 + k * kJoinParts < pieces) {
+            const float mn = fmaxf(m, st[k].x), f = ex2(m - mn), x = ex2(st[k].x - mn);
+            m = mn;
+            l = fmaf(st[k].y, x, l * f);
+            o.x = fmaf(v[k].x, x, o.x * f), o.y = fmaf(v[k].y, x, o.y * f);
+            o.z = fmaf(v[k].z, x, o.z * f), o.w = fmaf(v[k].w, x, o.w * f);
+          }
+        }
+      }
+    }
+    part[mine][row][lane] = o;
+    if (lane == 0) stat[mine][row] = make_float2(m, l);
+    __syncthreads();
+    if (mine == 0 && rr < rows && 4 * lane < a.D) {
+      float mm = m;
+#pragma unroll
+      for (int p = 1; p < kJoinParts; ++p) mm = fmaxf(mm, stat[p][row].x);
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.f;
+#pragma unroll
+      for (int p = 0; p < kJoinParts; ++p) {
+        const float2 st = stat[p][row];
+        const float4 v = part[p][row][lane];
+        const float x = ex2(st.x - mm);
+        l = fmaf(st.y, x, l);
+        o.x = fmaf(v.x, x, o.x), o.y = fmaf(v.y, x, o.y), o.z = fmaf(v.z, x, o.z), o.w = fmaf(v.w, x, o.w);
+      }
+      const float r = l == 0.f ? 0.f : __frcp_rn(l);
+      const int rho = item.w * kTcRows + rr, qi = rho / G;
+      const size_t to = (size_t)(item.y + qi) * a.Hq + item.z * G + rho - qi * G;
+      *reinterpret_cast<uint2*>(a.out + to * a.D + 4 * lane) =
+          make_uint2(f32_to_bf16x2(o.x * r, o.y * r), f32_to_bf16x2(o.z * r, o.w * r));
+    }
+    __syncthreads();
   }
-  const float L = sums[rr], r = L == 0.f ? 0.f : __frcp_rn(L);
-  const int rho = split.w * kTcRows + r0 + rr, qi = rho / G;
-  const size_t to = (size_t)(split.y + qi) * a.Hq + split.z * G + rho - qi * G;
-  *reinterpret_cast<uint2*>(a.out + to * a.D + d) =
-      make_uint2(f32_to_bf16x2(o.x * r, o.y * r), f32_to_bf16x2(o.z * r, o.w * r));
 }
 
 template <int FMT>
@@ -803,8 +870,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   const int ctas = std::min(device_sm_count(), kTcMaxCtas);
   e = launch_kernel(k, dim3(ctas), dim3(kTcThreads), smem, stream, pdl, km, vm, a, box, stages);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attn_kv8_join_kernel, dim3(ctas, kTcRows / kJoinRows), dim3(kJoinRows * D / 4), 0, stream, true,
-                       a);
+  return launch_kernel(attn_kv8_join_kernel, dim3(ctas), dim3(kJoinThreads), 0, stream, true, a, ctas);
 }
 
 }  // namespace
