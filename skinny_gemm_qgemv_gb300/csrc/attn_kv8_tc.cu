@@ -15,8 +15,8 @@
 // the sum again, as in attn_kv8.cu. Sums, maxima and accumulators are fp32, K, V
 // and q are exact in fp16, p is rounded to fp16.
 //
-// Sixteen warps per CTA, one CTA per SM: 0-3 convert keys, 4-7 and 8-11 softmax of
-// half of the rows each, 12 and 13 convert values, 14 issues the copies, 15 the
+// Sixteen warps per CTA, one CTA per SM: 0-3 convert keys and half of the values,
+// 4-7 and 8-11 softmax of half of the rows each, 12 and 13 the values' other half, 14 issues the copies, 15 the
 // MMAs (16 warps are what leaves a thread 128 registers). Steps run through two
 // buffers of every kind; S of step i + 1 is issued before O of step i. The batch
 // is cut into shares as in attn_kv8.cu; a second kernel joins a context's pieces.
@@ -194,6 +194,28 @@ __device__ __noinline__ bool tc_wait_on(uint64_t* bar, uint32_t parity, volatile
   return false;
 }
 
+// Elements 64 part .. 64 part + 63 of token t's values, from the tile at src to fp16 rows of 64 at dst; zeros where
+// there is no token (slots past the context may hold codes that are not numbers).
+template <int FMT>
+__device__ __forceinline__ void tc_values(uint32_t src, uint32_t dst, int part, int t, bool none) {
+  dst += part * kTcTok * 128 + t * 128;
+  src += t * 128;
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    const uint4 w = lds128(src + (((4 * part + ch) ^ (t & 7)) << 4));
+    uint4 f[2];
+    codes_to_f16<FMT>(w.x, f[0].x, f[0].y);
+    codes_to_f16<FMT>(w.y, f[0].z, f[0].w);
+    codes_to_f16<FMT>(w.z, f[1].x, f[1].y);
+    codes_to_f16<FMT>(w.w, f[1].z, f[1].w);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) sts128(dst + (((2 * ch + k) ^ (t & 7)) << 4), f[k]);
+  }
+  if (none)
+#pragma unroll 1
+    for (int ch = 0; ch < 8; ++ch) sts128(dst + (ch << 4), make_uint4(0u, 0u, 0u, 0u));
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
@@ -213,7 +235,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ __align__(16) float neg_m[ROWS], fall[ROWS], fade[ROWS], sums[ROWS];
   __shared__ __align__(16) float wsum[4][ROWS];
   __shared__ int4 row_info[ROWS];  // tokens below .x are seen, and draft tokens by .y's bits; .z: output row or -1
-  __shared__ uint64_t full[kTcMaxStages], empty[kTcMaxStages], k_full[2], s_full[2], s_empty[2], p_full[2], v_full[2], o_done[2], q_full;
+  __shared__ uint64_t full[kTcMaxStages], empty[kTcMaxStages], s_full[2], o_done[2], q_full;
+  // s_ready: the step's keys are in TMEM and the scores of two steps ago have been read; o_ready: its P and values are there
+  __shared__ uint64_t s_ready[2], o_ready[2];
   __shared__ int2 scan_part[kTcThreads / 32];
   __shared__ uint32_t tmem_base;
   __shared__ unsigned amax_bits, unset_any[2];
@@ -222,11 +246,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kTcMaxStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 6);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 4);
+      mbar_init(s_ready + i, 4 + 8);
       mbar_init(s_full + i, 1);
-      mbar_init(s_empty + i, 8);
-      mbar_init(p_full + i, 8);
-      mbar_init(v_full + i, 2);
+      mbar_init(o_ready + i, 8 + 6);
       mbar_init(o_done + i, 1);
     }
     mbar_init(&q_full, 8);
@@ -247,11 +269,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tbase = tmem_base;
   const uint32_t tlane = tbase + ((uint32_t)(quad * 32) << 16);  // the lanes that this warp may touch
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || tc_wait_on(bar, parity, &abort_flag, a.err);
+  // by a whole warp, which goes on together
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+           __all_sync(0xffffffffu, tc_wait_on(bar, parity, &abort_flag, a.err));
   };
-  // the same by a whole warp, which goes on together
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
   // A segment: the steps of one item in this CTA's share. Every role walks the segments by itself; buffers and
   // barriers run on from one to the next (step g of the CTA: buffer g & 1), so the keys and values of a segment are
@@ -289,7 +311,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int step = share.c0;
   Segment sg = first_segment();
   if (role == 0) {
-    // ------------------------------------------------ keys: a token's row per thread, fp16 into TMEM
+    // ------------------------------------------------ keys: a token's row per thread, fp16 into TMEM; half of its values
     const int t = quad * 32 + lane;
     bool ok = true;
     while (ok && next_segment(sg, step)) {
@@ -318,12 +340,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_wait_st();
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty + st), mbar_arrive(k_full + b);
+        if (lane == 0) mbar_arrive(s_ready + b);
+        // half of the token's values
+        ok = g < 2 || wait_warp(o_done + b, ((g >> 1) - 1) & 1);
+        if (!ok) break;
+        tc_values<FMT>(src + S::kTile, smem_u32(vbuf + b * S::kV), 0, t, sg.tok0 + i * TOK + t >= sg.ctx);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + st), mbar_arrive(o_ready + b);
         if (++st == stages) st = 0, pass ^= 1u;
       }
     }
   } else if (warp == 12 || warp == 13) {
-    // ------------------------------------------------ values: two tokens' rows per thread, fp16 into shared memory
+    // ------------------------------------------------ values: the other half of two tokens' per thread, fp16 into shared memory
     bool ok = true;
     while (ok && next_segment(sg, step)) {
 #pragma unroll 1
@@ -333,32 +362,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         const uint32_t src = smem_u32(ring + (size_t)st * S::kStage + S::kTile);
 #pragma unroll 1
-        for (int t = (warp - 12) * 32 + lane; t < TOK; t += 64) {
-          const uint32_t dst = smem_u32(vbuf + b * S::kV) + t * 128;
-#pragma unroll
-          for (int ch = 0; ch < D / 16; ++ch) {
-            const uint32_t at = t * 128 + ((ch ^ (t & 7)) << 4);
-            const uint4 w = lds128(src + at);
-            uint4 f[2];
-            codes_to_f16<FMT>(w.x, f[0].x, f[0].y);
-            codes_to_f16<FMT>(w.y, f[0].z, f[0].w);
-            codes_to_f16<FMT>(w.z, f[1].x, f[1].y);
-            codes_to_f16<FMT>(w.w, f[1].z, f[1].w);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int c8 = 2 * ch + k;  // 8-element chunk of the row
-              sts128(dst + (c8 >> 3) * TOK * 128 + (((c8 & 7) ^ (t & 7)) << 4), f[k]);
-            }
-          }
-          // slots past the context may hold codes that are not numbers
-          if (sg.tok0 + i * TOK + t >= sg.ctx) {
-#pragma unroll 1
-            for (int ch = 0; ch < 16; ++ch) sts128(dst + (ch >> 3) * TOK * 128 + ((ch & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
-          }
-        }
+        for (int t = (warp - 12) * 32 + lane; t < TOK; t += 64)
+          tc_values<FMT>(src, smem_u32(vbuf + b * S::kV), 1, t, sg.tok0 + i * TOK + t >= sg.ctx);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty + st), mbar_arrive(v_full + b);
+        if (lane == 0) mbar_arrive(empty + st), mbar_arrive(o_ready + b);
         if (++st == stages) st = 0, pass ^= 1u;
       }
     }
@@ -400,35 +408,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 15) {
     // ------------------------------------------------ MMAs
-    const uint32_t qs = smem_u32(qbuf), io = tc_idesc(D, ROWS, true, true), one = lane == 0;
+    // What decides the loops and forms the operands is taken from lane 0, so that all of it stays in uniform registers:
+    // otherwise this warp's instructions bound the step (16 MMAs and their waits 2700 cycles).
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t io = tc_idesc(D, ROWS, true, true), one = lane == 0;
+    const uint32_t tb = uniform(tbase), qs = uniform(smem_u32(qbuf)), vs = uniform(smem_u32(vbuf)), ps = uniform(smem_u32(pbuf));
+    const uint64_t qd = tc_desc(qs, 16, 1024), vd = tc_desc(vs, TOK * 128, 1024), pd = tc_desc(ps, TOK * 128, 1024);
     bool ok = true;
-    while (ok && next_segment(sg, step)) {
-      const uint32_t is = tc_idesc(128, 16 * sg.nch, false, false);
-      const int n = sg.n, gi = sg.g;
-      ok = wait_warp(&q_full, sg.index & 1);
+    while (ok && __all_sync(0xffffffffu, next_segment(sg, step))) {
+      const int n = uniform(sg.n), gi = uniform(sg.g);
+      const uint32_t is = tc_idesc(128, 16 * uniform(sg.nch), false, false);
+      ok = wait_warp(&q_full, uniform(sg.index) & 1);
 #pragma unroll 1
       for (int i = 0; i <= n && ok; ++i) {
         if (i < n) {
-          const int g = gi + i, b = g & 1;
-          ok = wait_warp(k_full + b, (g >> 1) & 1) && (g < 2 || wait_warp(s_empty + b, ((g >> 1) - 1) & 1));
+          const uint32_t g = gi + i, b = g & 1;
+          ok = wait_warp(s_ready + b, (g >> 1) & 1);
           if (!ok) break;
           tc_after();
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ts(tbase + S::kColS + b * ROWS, tbase + S::kColK + b * (D / 2) + 8 * k,
-                   tc_desc(qs + (k >> 2) * ROWS * 128 + (k & 3) * 32, 16, 1024), is, k > 0, one);
+            mma_ts(tb + S::kColS + b * ROWS, tb + S::kColK + b * (D / 2) + 8 * k,
+                   qd + (((k >> 2) * ROWS * 128 + (k & 3) * 32) >> 4), is, k > 0, one);
           if (one) tc_commit(s_full + b);
           __syncwarp();
         }
         if (i > 0) {
-          const int g = gi + i - 1, b = g & 1;
-          ok = wait_warp(p_full + b, (g >> 1) & 1) && wait_warp(v_full + b, (g >> 1) & 1);
+          const uint32_t g = gi + i - 1, b = g & 1;
+          ok = wait_warp(o_ready + b, (g >> 1) & 1);
           if (!ok) break;
           tc_after();
-          const uint32_t vs = smem_u32(vbuf + b * S::kV), ps = smem_u32(pbuf + b * S::kP);
 #pragma unroll
           for (int k = 0; k < TOK / 16; ++k)
-            mma_ss(tbase + S::kColO, tc_desc(vs + k * 2048, TOK * 128, 1024), tc_desc(ps + k * 2048, TOK * 128, 1024), io,
+            mma_ss(tb + S::kColO, vd + ((b * S::kV + k * 2048) >> 4), pd + ((b * S::kP + k * 2048) >> 4), io,
                    k > 0 ? 1u : i > 1, one);
           if (one) tc_commit(o_done + b);
           __syncwarp();
@@ -438,6 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else {
     // ------------------------------------------------ softmax: a token per thread, half of the rows
     constexpr int HR = ROWS / 2;
+    if (lane == 0) mbar_arrive(s_ready), mbar_arrive(s_ready + 1);  // both buffers of S are free
     const int t = quad * 32 + lane, half = role == 1 ? 0 : 1, bar = 1 + half;
     while (next_segment(sg, step)) {
       const AttnPlace item = sg.item;
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (ch < hch) tmem_wait_ld(y + 16 * ch);
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty + b);
+        if (lane == 0) mbar_arrive(s_ready + b);
         bool grow = unset;
 #pragma unroll
         for (int j = 0; j < HR; j += 2)
@@ -667,7 +680,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + b);
+        if (lane == 0) mbar_arrive(o_ready + b);
       }
       // the rows' sums over the tokens: per warp, then over the warps
       {
