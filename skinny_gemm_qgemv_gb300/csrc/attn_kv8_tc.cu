@@ -459,6 +459,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // row 2^20 smaller loses is 2^-40 of the largest scores), K-major, swizzled. (The last segment's products have
       // been waited for.)
       const int u = half * 128 + t;
+      constexpr int kPer = D / 8, kTimes = ROWS * kPer / 256;  // threads of a row: 8 elements each
+      uint4 raw[kTimes];
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < kTimes; ++k) {
+        const int rr = (u + k * 256) / kPer, ch = u % kPer, rho = item.rt * ROWS + rr, i = rho / batch.G;
+        raw[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < rows && 8 * ch < a.D)
+          raw[k] = *reinterpret_cast<const uint4*>(a.q + (size_t)(sg.q0 + i) * a.q_stride +
+                                                   (item.h * batch.G + rho - i * batch.G) * a.D + 8 * ch);
+      }
       if (u == 0) amax_bits = 0u;
       if (u < ROWS) {
         const int rho = item.rt * ROWS + u;
@@ -476,18 +487,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       named_barrier<256>(3);
       float up;
       {
-        constexpr int kPer = D / 8, kTimes = ROWS * kPer / 256;  // threads of a row: 8 elements each
-        uint4 raw[kTimes];
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < kTimes; ++k) {
-          const int rr = (u + k * 256) / kPer, ch = u % kPer, to = row_info[rr].z;
-          raw[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (to >= 0 && 8 * ch < a.D) {
-            const int tq = to / a.Hq;
-            raw[k] = *reinterpret_cast<const uint4*>(a.q + (size_t)tq * a.q_stride + (to - tq * a.Hq) * a.D + 8 * ch);
-          }
-        }
 #pragma unroll
         for (int k = 0; k < kTimes; ++k) {
           const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
@@ -774,9 +773,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv8_join_kernel(AttnArgs a,
   pdl_launch_dependents();
   if (warp == 0) {  // the items that are in pieces, and their units' prefix sums
     int n = 0, units = 0;
-#pragma unroll 1
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const int4 s = c0 + lane < ctas ? tc_splits(a.ws)[c0 + lane] : make_int4(0, 0, 0, 0);
+    constexpr int kTimes = (kTcMaxCtas + 31) / 32;
+    int4 all[kTimes];
+#pragma unroll
+    for (int k = 0; k < kTimes; ++k)
+      all[k] = 32 * k + lane < ctas ? tc_splits(a.ws)[32 * k + lane] : make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < kTimes; ++k) {
+      const int4 s = all[k];
+      const int c0 = 32 * k;
       const bool in = (s.x & 0xFFFF) >= 2;
       const unsigned votes = __ballot_sync(0xffffffffu, in);
       int u = in ? ((s.x >> 16) + kJoinRows - 1) / kJoinRows : 0;
