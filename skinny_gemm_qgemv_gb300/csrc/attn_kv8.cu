@@ -739,14 +739,17 @@ cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
 int attn_width(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // rows of an average request's item
 int attn_rows(const AttnArgs& a) { return (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv); }
-// The tcgen05 kernel for many rows of 128 elements (or fewer, filled up). This file's kernel passes over the cache once per 16 rows, at 5 ns
-// per 128 tokens of a head (the HBM rate); that one takes 10 ns per 128 tokens and 64 rows, and 7 us more to begin,
-// end and join (measured: 64 rows, one request: 8192 tokens 23.7 here, 25.4 us there; 32784 tokens 55.5 and 43.5;
-// 32 rows, 32768 tokens: 34.8 and 38.7). The lengths are known to the GPU alone, so their bound decides.
+// The tcgen05 kernel for many rows of up to 128 elements. This file's kernel passes over the cache once per 16 rows, at
+// 5 ns per 128 tokens of a head (3 ns with heads of 64); that one takes 7 ns per 128 tokens and 64 rows, and about 3 us
+// more to begin, end and join. Measured, here and there: one request, 64 rows, 300 tokens 9.7 and 13.8 us, 2048 tokens
+// 15.8 and 15.2, 8192 tokens 24.2 and 18.5, 32784 tokens 56.0 and 32.5; 32 rows, 8192 tokens 17.3 and 17.2, 32768 tokens
+// 33.5 and 29.4; heads of 64, 64 rows, 65536 tokens 42.3 and 32.7; six requests of 40 rows over 5000 tokens 14.3 and
+// 16.2. The lengths are known to the GPU alone, so their bound decides.
 bool attn_tc_ok(const AttnArgs& a) {
-  if (attn_width(a.D) != 128) return false;
+  const int width = attn_width(a.D);
+  if (width > 128) return false;
   const long long rows = attn_rows(a), steps = (long long)a.R * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128);
-  return steps * (5 * ((rows + 15) / 16) - 10 * ((rows + 63) / 64)) >= 7000;
+  return steps * ((width == 64 ? 3 : 5) * ((rows + 15) / 16) - 7 * ((rows + 63) / 64)) >= 3000;
 }
 
 // 8-row tiles per item: the least that hold an average request's query rows

@@ -1,5 +1,5 @@
 // Attention over the paged 8-bit cache for many query rows per key/value head of
-// up to 128 elements (more than 32 rows: drafts of a speculative tree, or a prompt's
+// up to 128 elements (more than 16 rows: drafts of a speculative tree, or a prompt's
 // piece, times the heads of a group), on the 5th-generation tensor cores.
 //
 // The warp-level kernel of attn_kv8.cu reads the cache once for every 16 rows.
@@ -21,11 +21,12 @@
 // buffers of every kind; S of step i + 1 is issued before O of step i. The batch
 // is cut into shares as in attn_kv8.cu; a second kernel joins a context's pieces.
 //
-// Measured: 64 rows of 8 heads over 32784 int8 tokens 42 us (67 MB at 1.6 TB/s, 34
-// GFLOP at 0.8 PFLOP/s). A step takes 1.8 us against 0.26 us of copies and 0.15 us
-// of MMAs: what bounds it is the softmax warps' chain from one S to its P (TMEM
-// loads, 8192 exponentials on 8 warps, stores). 9 us go to a share's begin and end
-// and 6 us to the joining kernel.
+// Measured: 64 rows of 8 heads over 32784 int8 tokens 32.5 us (67 MB at 2.1 TB/s, 8.6
+// GFLOP), 65568 tokens 51 us. A step takes 1.35 us against 0.6 us of copies (a 152nd of
+// HBM) and 0.3 us of MMAs: it is bound by the chain from one S to its P in the softmax
+// warps and by what the MMA warp waits for and issues, all at about 2500 cycles; no single
+// part taken out makes it more than 8 % faster. 6 us go to the first step, 5 to the last
+// results and their joining.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -41,7 +42,7 @@ namespace {
 constexpr int kTcRows = 64;     // query rows of an item
 constexpr int kTcTok = 128;     // tokens of a step
 constexpr int kTcThreads = 512;
-// an item costs about 9 us to begin and end, a step 1.8 us; joining is a kernel of its own, so only the shortest items
+// an item costs about 7 us to begin and end, a step 1.35 us; joining is a kernel of its own, so only the shortest items
 // are kept whole
 using TcCut = AttnCut<kTcTok, 5, 2>;
 constexpr int kTcMaxCtas = 152;  // CTAs: the join kernel's factors and the table of split items are laid out for it

@@ -547,7 +547,7 @@ def test_attention_many_rows(q, fmt, nq, ctx, Hq, Hkv, bs, tree):
 
 
 @pytest.mark.parametrize("fmt", ["i8", "e4m3"])
-@pytest.mark.parametrize("D", [80, 96, 112])
+@pytest.mark.parametrize("D", [16, 64, 80, 96, 112])
 def test_attention_many_rows_head_sizes(q, fmt, D):
     rng = np.random.default_rng(D)
     for nq, ctx in (([12], [6000]), ([9, 16, 1], [9, 700, 130])):
