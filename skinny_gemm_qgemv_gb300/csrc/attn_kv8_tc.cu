@@ -16,8 +16,9 @@
 // and q are exact in fp16, p is rounded to fp16.
 //
 // Sixteen warps per CTA, one CTA per SM: 0-3 convert keys and half of the values,
-// 4-7 and 8-11 softmax of half of the rows each, 12 and 13 the values' other half, 14 issues the copies, 15 the
-// MMAs (16 warps are what leaves a thread 128 registers). Steps run through two
+// 4-7 and 8-11 softmax of half of the rows each, 12 and 13 the values' other half,
+// 14 issues the copies, 15 the MMAs (16 warps are what leaves a thread 128
+// registers). Steps run through two
 // buffers of every kind; S of step i + 1 is issued before O of step i. The batch
 // is cut into shares as in attn_kv8.cu; a second kernel joins a context's pieces.
 //
