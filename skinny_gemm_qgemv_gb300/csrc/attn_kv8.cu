@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       cp_async16(smem_u32(qraw + (size_t)b * ROWS * D * 2 + 16 * i), src, live);
     }
   };
-  fetch_q(attn_locate<ROWS, Cut>(batch, c0), 0);
+  AttnPlace ahead = attn_locate<ROWS, Cut>(batch, c0);  // of the next segment
+  fetch_q(ahead, 0);
 
   // ---- producer side of the warp's ring: a lane looks after one unit of SB steps ----
   uint64_t* bar = bars + warp * stages;
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
 
   int qb = 0;
   auto begin_segment = [&](int step) {
-    item = attn_locate<ROWS, Cut>(batch, step);
+    item = ahead;
     item_first = step - item.s;
     seg_end = min(c1, item_first + item.steps);
     ctx = ctxs[item.r];
@@ -364,7 +365,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     }
     // the other buffer was last read before the barrier above
     qb ^= 1;
-    if (seg_end < c1) fetch_q(attn_locate<ROWS, Cut>(batch, seg_end), qb);
+    if (seg_end < c1) {
+      ahead = attn_locate<ROWS, Cut>(batch, seg_end);
+      fetch_q(ahead, qb);
+    }
   };
 
   // lane's places in a swizzled tile: keys (token t0; t0 + 2 is 2 rows on), values (ldmatrix rows)
