@@ -606,7 +606,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     auto piece = [&](int i) {
       return ws + (size_t)(2 * (f + i) + (i == 0 ? 1 : 0)) * attn_piece_bytes(ROWS, D);
     };
-    constexpr int kParts = kTiles < NW ? NW / kTiles : 1, kEarly = 8;
+    // (as many as the registers allow without the main loop feeling it: 8192 tokens 12.1 us with 8, 11.6 with 20)
+    constexpr int kParts = kTiles < NW ? NW / kTiles : 1, kEarly = NT == 1 && D <= 128 ? 20 : 8;
     const int part = kParts > 1 ? warp / kTiles : 0;
     float4 early[kEarly];
 #pragma unroll

@@ -186,9 +186,10 @@ __device__ __forceinline__ AttnShare attn_share(const AttnBatch& b) {
   AttnShare s = {0, 0, 0, 0};
   if ((int)blockIdx.x >= A) return s;
   s.share = W / A, s.more = W % A;
-  const int x0 = blockIdx.x * s.share + min((int)blockIdx.x, s.more);
-  s.c0 = attn_step_at<CUT>(b, x0);
-  s.c1 = attn_step_at<CUT>(b, x0 + s.share + ((int)blockIdx.x < s.more ? 1 : 0));
+  // both ends side by side, by the even and the odd lanes
+  const int i = blockIdx.x + (threadIdx.x & 1), step = attn_step_at<CUT>(b, i * s.share + min(i, s.more));
+  s.c0 = __shfl_sync(0xffffffffu, step, 0);
+  s.c1 = __shfl_sync(0xffffffffu, step, 1);
   return s;
 }
 // the CTA whose share holds a step
