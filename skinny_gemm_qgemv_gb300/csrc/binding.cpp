@@ -65,6 +65,7 @@ float real(PyObject* o) {
 struct Call {
   c10::Device dev;
   c10::cuda::OptionalCUDAGuard guard;
+  c10::cuda::OptionalCUDAStreamGuard on;  // a given stream is the current one while outputs are allocated
   void* stream;
   const char* where;
 
@@ -80,6 +81,7 @@ struct Call {
       stream = reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(h));
       Py_DECREF(h);
       if (PyErr_Occurred()) throw Raised{};
+      on.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), dev.index()));
     }
   }
   void on_device(const at::Tensor& t, const char* name) const {

@@ -440,6 +440,24 @@ def test_attention_offsets_past_32_bits(q):
                  ).all())
 
 
+def test_outputs_belong_to_the_given_stream(q):
+    """An output made for another stream does not take memory that the current stream still uses."""
+    s = torch.cuda.Stream()
+    x, w = torch.randn((64, 4096), device=DEV), torch.ones(4096, device=DEV)
+    want, _ = q.rmsnorm_residual(x, w)
+    torch.cuda.synchronize()
+    big = torch.randn((4096, 4096), device=DEV)
+    for _ in range(4):
+        old = torch.empty((64, 4096), device=DEV, dtype=torch.bfloat16)
+        for _ in range(6):
+            big @ big                                    # the current stream is busy
+        old.fill_(3.0)                                   # written late
+        del old                                          # and given back to the current stream's pool
+        got, _ = q.rmsnorm_residual(x, w, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_attention_on_another_stream_and_in_a_graph(q):
     rng = np.random.default_rng(28)
     c = attn_case(rng, [1, 2, 1], [100, 400, 37], 8, 2, 128, 16, "i8", False)
