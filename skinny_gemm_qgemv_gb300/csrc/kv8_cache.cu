@@ -8,10 +8,16 @@
 // and above it a block released in this call, found through the prefix sums in
 // the releasing request's row, which nothing overwrites either.
 //
-// kv8_append_kernel. One CTA per run of slots, head and cache (keys or values):
-// the run's maximum decides the block's scale, the earlier codes of the block
-// are rounded to a grown scale, the run is quantized. All IEEE fp32 operations
-// on single values, so the codes do not depend on the work's order.
+// kv8_append_kernel. One CTA per window of tokens, head and cache (keys or values); it finds the runs that begin there.
+// A run's maximum decides the block's scale, the earlier codes of the block are
+// rounded to a grown scale, the run is quantized. All IEEE fp32 operations on
+// single values, so the codes do not depend on the work's order. A run is read
+// once (kept in registers between the maximum and the codes) and is a chain of
+// slot map -> values -> maximum -> codes, so what bounds it is how many runs an SM
+// holds: 4093 tokens of 8 heads of 128 from fp32, 33.5 MB, 12 us (2.8 TB/s).
+//
+// kv8_read_kernel. One CTA per block, head and cache, 8-byte loads and 16-byte
+// stores: 8.4 MB of codes to 16.8 MB of bf16 in 5 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -208,8 +214,6 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_plan_kernel(PlanArgs a) {
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
-constexpr int kAppendThreads = 256;
-constexpr int kAppendKeep = 4;  // steps of 8 elements kept in registers between the maximum and the codes
 
 __device__ __forceinline__ void load8_in(const void* p, int f32, size_t elem, float (&v)[8]) {
   if (f32) {
@@ -227,11 +231,12 @@ __device__ __forceinline__ void load8_in(const void* p, int f32, size_t elem, fl
   }
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a) {
-  __shared__ int lead[kAppendThreads], leads;
-  __shared__ int part_n[kAppendThreads / 32];
-  __shared__ float part[kAppendThreads / 32];
+// KEEP: steps of 8 elements that a thread keeps between the maximum and the codes (what is more is read again)
+template <int FMT, int THREADS, int KEEP>
+__global__ void __launch_bounds__(THREADS, KEEP == 1 ? 2048 / THREADS : KEEP == 2 ? 1280 / THREADS : 1024 / THREADS) kv8_append_kernel(AppendArgs a) {
+  __shared__ int lead[THREADS], leads;
+  __shared__ int part_n[THREADS / 32];
+  __shared__ float part[THREADS / 32];
   const int tid = threadIdx.x;
   if (tid == 0) leads = 0;
   pdl_wait();
@@ -260,14 +265,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
     // loaded before it is known.
     const int most = min(a.bs - f, a.T - t0);
     auto at = [&](int i) { return (t0 + i / d8) * stride + head * a.D + (i % d8) * 8; };
-    float keep[kAppendKeep][8];
+    float keep[KEEP][8];
 #pragma unroll
-    for (int c = 0; c < kAppendKeep; ++c) {
-      const int i = tid + c * kAppendThreads;
+    for (int c = 0; c < KEEP; ++c) {
+      const int i = tid + c * THREADS;
       if (i < most * d8) load8_in(x, a.f32, at(i), keep[c]);
     }
     int n = most;
-    for (int i = tid; i < most; i += kAppendThreads)
+    for (int i = tid; i < most; i += THREADS)
       if (__ldg(a.slot_map + t0 + i) != slot + i) n = min(n, i);
     n = __reduce_min_sync(0xffffffffu, n);
     if ((tid & 31) == 0) part_n[tid >> 5] = n;
@@ -275,17 +280,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
     const float s0 = f > 0 ? *sp : 0.f;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) n = min(n, part_n[w]);
+    for (int w = 0; w < THREADS / 32; ++w) n = min(n, part_n[w]);
     const int chunks = n * d8;
     float amax = 0.f;
 #pragma unroll
-    for (int c = 0; c < kAppendKeep; ++c) {
-      if (tid + c * kAppendThreads < chunks) {
+    for (int c = 0; c < KEEP; ++c) {
+      if (tid + c * THREADS < chunks) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(keep[c][j]));
       }
     }
-    for (int i = tid + kAppendKeep * kAppendThreads; i < chunks; i += kAppendThreads) {
+    for (int i = tid + KEEP * THREADS; i < chunks; i += THREADS) {
       float v[8];
       load8_in(x, a.f32, at(i), v);
 #pragma unroll
@@ -296,14 +301,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
     if ((tid & 31) == 0) part[tid >> 5] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, part[w]);
+    for (int w = 0; w < THREADS / 32; ++w) amax = fmaxf(amax, part[w]);
     const float s = fmaxf(s0, __fdiv_rn(amax, kv8_qmax<FMT>()));
     if (tid == 0) *sp = s;  // every thread read the old one before the barrier
     uint8_t* page = cache + ((size_t)blk * a.Hkv + head) * a.bs * a.D;
     if (f > 0 && s > s0) {
       // the earlier codes, rounded to the grown scale
       const float ratio = __fdiv_rn(s0, s);
-      for (int i = tid; i < f * d8; i += kAppendThreads) {
+      for (int i = tid; i < f * d8; i += THREADS) {
         uint2* p = reinterpret_cast<uint2*>(page) + i;
         const uint2 old = *p;
         float v[8];
@@ -317,17 +322,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
     uint2* dst = reinterpret_cast<uint2*>(page + (size_t)f * a.D);
     const float inv = __frcp_rn(s);
 #pragma unroll
-    for (int c = 0; c < kAppendKeep; ++c) {
-      const int i = tid + c * kAppendThreads;
+    for (int c = 0; c < KEEP; ++c) {
+      const int i = tid + c * THREADS;
       if (i < chunks) dst[i] = s > 0.f ? kv8_quantize8<FMT>(keep[c], s, inv) : make_uint2(0u, 0u);
     }
-    for (int i = tid + kAppendKeep * kAppendThreads; i < chunks; i += kAppendThreads) {
+    for (int i = tid + KEEP * THREADS; i < chunks; i += THREADS) {
       float v[8];
       load8_in(x, a.f32, at(i), v);
       dst[i] = s > 0.f ? kv8_quantize8<FMT>(v, s, inv) : make_uint2(0u, 0u);
     }
     if (f == 0)
-      for (int i = tid + chunks; i < a.bs * d8; i += kAppendThreads) dst[i] = make_uint2(0u, 0u);
+      for (int i = tid + chunks; i < a.bs * d8; i += THREADS) dst[i] = make_uint2(0u, 0u);
     // (part_n and part are written again only after a barrier that follows their last reads)
   }
 }
@@ -381,13 +386,22 @@ cudaError_t launch_kv8_plan(const PlanArgs& a, cudaStream_t stream, bool pdl) {
 }
 
 cudaError_t launch_kv8_append(AppendArgs a, int format, cudaStream_t stream, bool pdl) {
-  // Tokens whose runs one CTA takes: one where that gives up to 2048 CTAs, up to a block of them for a long prompt
-  // (4093 tokens in blocks of 64, with the read-back: 18.5 us at 1024, 16.4 at 2048, 18.8 at 4096).
-  a.window = (int)std::min<long long>(std::min(a.bs, kAppendThreads),
-                                      std::max<long long>(1, (long long)a.T * a.Hkv * 2 / 2048));
+  // Tokens whose runs one CTA takes: one where that gives up to eight CTAs an SM, up to a block of them (and no more
+  // than a CTA has threads) for a long prompt.
+  a.window = (int)std::min<long long>(std::min(a.bs, 128),
+                                      std::max<long long>(1, (long long)a.T * a.Hkv * 2 / (8 * device_sm_count())));
   const dim3 grid((a.T + a.window - 1) / a.window, 2 * a.Hkv);
-  auto k = format == QG_KV_I8 ? kv8_append_kernel<QG_KV_I8> : kv8_append_kernel<QG_KV_E4M3>;
-  return launch_kernel(k, grid, dim3(kAppendThreads), 0, stream, pdl, a);
+  auto launch = [&](auto i8, auto e4m3, int threads) {
+    return launch_kernel(format == QG_KV_I8 ? i8 : e4m3, grid, dim3(threads), 0, stream, pdl, a);
+  };
+  // By the elements of a run: no more registers and threads than it needs, for the more runs are on the way per SM.
+  // With the read-back, 4093 tokens of 8 heads of 128: blocks of 16 30.0 us in the widest form, 22.4 with 256 threads and
+  // one step, 21.2 as here; blocks of 32 23.2 and 20.1; blocks of 64 (fp32) 16.5, 19.4 with 512 threads.
+  const int elems = a.bs * a.D;
+  if (elems <= 1024) return launch(kv8_append_kernel<QG_KV_I8, 128, 1>, kv8_append_kernel<QG_KV_E4M3, 128, 1>, 128);
+  if (elems <= 2048) return launch(kv8_append_kernel<QG_KV_I8, 128, 2>, kv8_append_kernel<QG_KV_E4M3, 128, 2>, 128);
+  if (elems <= 4096) return launch(kv8_append_kernel<QG_KV_I8, 256, 2>, kv8_append_kernel<QG_KV_E4M3, 256, 2>, 256);
+  return launch(kv8_append_kernel<QG_KV_I8, 256, 4>, kv8_append_kernel<QG_KV_E4M3, 256, 4>, 256);
 }
 
 cudaError_t launch_kv8_read(const ReadArgs& a, int format, cudaStream_t stream, bool pdl) {
