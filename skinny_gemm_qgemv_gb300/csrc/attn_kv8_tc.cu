@@ -177,6 +177,9 @@ __device__ __forceinline__ float transposed_warp_max(float (&v)[R], int lane) {
 }
 
 constexpr int kTcMaxStages = 3;
+// Slots of the scales of a step: when step h's are written the values of step h - 3 have been converted, and before them
+// the P of step h - 5 was read: the softmax is at step h - 4 or later.
+constexpr int kTcSlots = 8;
 
 // one entry per CTA, behind the counters of attn_kv8.cu's pieces
 __device__ __forceinline__ int4* tc_splits(void* ws) {
@@ -240,6 +243,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ uint64_t full[kTcMaxStages], empty[kTcMaxStages], s_full[2], o_done[2], q_full;
   // s_ready: the step's keys are in TMEM and the scores of two steps ago have been read; o_ready: its P and values are there
   __shared__ uint64_t s_ready[2], o_ready[2];
+  __shared__ uint64_t scaled[kTcSlots];  // the step's scales have been written
+  __shared__ float4 unit_scales[kTcSlots][TOK / kUnit];
   __shared__ int2 scan_part[kTcThreads / 32];
   __shared__ uint32_t tmem_base;
   __shared__ unsigned amax_bits, unset_any[2];
@@ -254,6 +259,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(o_done + i, 1);
     }
     mbar_init(&q_full, 8);
+    for (int i = 0; i < kTcSlots; ++i) mbar_init(scaled + i, 1);
     abort_flag = 0u;
     fence_mbar_init();
   }
@@ -374,37 +380,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 14) {
     // ------------------------------------------------ copies: `box` tokens of one block at a time
-    const int boxes = TOK / box;
+    // A lane looks after a unit of 16 tokens: its block, and what the softmax needs of the block's scales (one warp
+    // works it out; two more warps of every quarter would otherwise look up each token: 1 of their 9 instructions).
+    const int boxes = TOK / box, per_box = box / kUnit;
+    const float2* scales = reinterpret_cast<const float2*>(a.scales);
     bool ok = true;
     while (ok && next_segment(sg, step)) {
       auto look = [&](int i) {
-        const int tok = sg.tok0 + i * TOK + lane * box;
+        const int tok = sg.tok0 + i * TOK + lane * kUnit;
         int blk = -1;
-        if (i < sg.n && lane < boxes && tok < sg.ctx) {
+        if (i < sg.n && lane < TOK / kUnit && tok < sg.ctx) {
           blk = __ldg(a.table + (size_t)sg.item.r * a.max_blocks + tok / a.bs);
           if (blk < 0) blk = a.num_blocks;  // bad
         }
         return blk;
       };
-      int next = look(0);
+      auto scales_of = [&](int blk) {
+        return blk >= 0 && blk < a.num_blocks ? __ldg(scales + (size_t)blk * a.Hkv + sg.item.h) : make_float2(0.f, -1.f);
+      };
+      int blk = look(0), next = look(1);
+      float2 sc = scales_of(blk);
 #pragma unroll 1
       for (int i = 0; i < sg.n; ++i) {
-        const int blk = next;
-        next = look(i + 1);
-        ok = sg.g + i < stages || wait_warp(empty + st, pass ^ 1u);
+        const int g = sg.g + i, mine = __shfl_sync(0xffffffffu, blk, lane * per_box & 31);
+        ok = g < stages || wait_warp(empty + st, pass ^ 1u);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(full + st, S::kStage);
         __syncwarp();
         if (lane < boxes) {
-          if (blk >= a.num_blocks) report_error(a.err, kErrKvBlock);
+          if (mine >= a.num_blocks) report_error(a.err, kErrKvBlock);
           // what is not there is read past the last page: zeros
-          const int page = blk >= 0 && blk < a.num_blocks ? blk * a.Hkv + sg.item.h : a.num_blocks * a.Hkv;
+          const int page = mine >= 0 && mine < a.num_blocks ? mine * a.Hkv + sg.item.h : a.num_blocks * a.Hkv;
           const int row = (sg.tok0 + i * TOK + lane * box) % a.bs;
           const uint32_t dst = smem_u32(ring + (size_t)st * S::kStage) + lane * box * D;
           tma_load_3d(dst, &kmap, 0, row, page, full + st);
           tma_load_3d(dst + S::kTile, &vmap, 0, row, page, full + st);
         }
+        if (lane < TOK / kUnit) {
+          // key scale, log2 of the value scale and 2^-that (not its inverse: what comes off is what went on), kind
+          const float lv = __log2f(sc.y < kMinScale ? kMinScale : sc.y);
+          unit_scales[g % kTcSlots][lane] =
+              make_float4(sc.x, lv, ex2(-lv), sc.y == 0.f ? 2.f : sc.y > 0.f || sc.y != sc.y ? 1.f : 0.f);
+        }
         __syncwarp();
+        if (lane == 0) mbar_arrive(scaled + g % kTcSlots);
+        blk = next;
+        next = look(i + 2);
+        sc = scales_of(blk);
         if (++st == stages) st = 0, pass ^= 1u;
       }
     }
@@ -456,7 +478,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int t = quad * 32 + lane, half = role == 1 ? 0 : 1, bar = 1 + half;
     while (next_segment(sg, step)) {
       const AttnPlace item = sg.item;
-      const int n = sg.n, gi = sg.g, ctx = sg.ctx, base = sg.base, tok0 = sg.tok0, nch = sg.nch, rows = sg.rows;
+      const int n = sg.n, gi = sg.g, base = sg.base, tok0 = sg.tok0, nch = sg.nch, rows = sg.rows;
       // The item's queries: 2^-sigma q in fp16 with one sigma for the item (its largest |q| just below 2^15; what a
       // row 2^20 smaller loses is 2^-40 of the largest scores), K-major, swizzled. (The last segment's products have
       // been waited for.)
@@ -524,37 +546,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint64_t l[HR / 2];  // sums of columns 2 j, 2 j + 1
 #pragma unroll
       for (int j = 0; j < HR / 2; ++j) l[j] = 0ull;
-      // the token's place in the table, its block of steps ahead, its scales of one step ahead
-      const int step_q = TOK / a.bs, step_r = TOK % a.bs;
-      int at_blk = (tok0 + t) / a.bs, at_off = (tok0 + t) - at_blk * a.bs, at_tok = tok0 + t;
-      const int32_t* row_table = a.table + (size_t)item.r * a.max_blocks;
-      const int end_tok = min(ctx, tok0 + n * TOK);
-      auto look = [&]() {  // the next token's entry, -1 past the segment
-        const int blk = at_tok < end_tok ? __ldg(row_table + at_blk) : -1;
-        at_tok += TOK;
-        at_blk += step_q;
-        at_off += step_r;
-        if (at_off >= a.bs) at_off -= a.bs, ++at_blk;
-        return blk;
-      };
-      const float2* head_scales = reinterpret_cast<const float2*>(a.scales) + item.h;
-      auto scales_of = [&](int blk) {
-        return blk < 0 || blk >= a.num_blocks ? make_float2(0.f, -1.f) : __ldg(head_scales + (size_t)blk * a.Hkv);
-      };
-      float2 sc = scales_of(look());
-      int blk = look();
       bool unset = true;  // some row has seen no token yet
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const int g = gi + i, b = g & 1, tok = tok0 + i * TOK + t;
-        const float2 now = sc;
-        sc = scales_of(blk);
-        blk = look();
-        const bool there = now.y >= 0.f || now.y != now.y;
-        const float vs = now.y < kMinScale ? kMinScale : now.y;
-        const float lv = __log2f(vs);
-        const uint64_t ks2 = both(now.x * up), lv2 = both(lv), inv2 = both(ex2(-lv));  // (not 1 / vs: what comes off is what went on)
-        const bool edge = __any_sync(0xffffffffu, !there || tok >= base);
+        wait_warp(scaled + g % kTcSlots, g / kTcSlots & 1);
+        const float4 sc = unit_scales[g % kTcSlots][t / kUnit];
+        const uint64_t ks2 = both(sc.x * up), lv2 = both(sc.y), inv2 = both(sc.z);
+        const bool there = sc.w != 0.f, zero = sc.w == 2.f, edge = __any_sync(0xffffffffu, !there || tok >= base);
         // (After a wait that gave up every later one returns at once: the warps stay in step at their barriers.)
         uint64_t c[HR / 2];  // log2 of the value scale, less the row's m
 #pragma unroll
@@ -660,7 +659,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         // p, its sum without the value scale, and as fp16 in shared memory (of a block of zero scale nothing)
         const uint32_t dst = smem_u32(pbuf + b * S::kP) + t * 128;
-        const bool zero = now.y == 0.f, some_zero = __any_sync(0xffffffffu, zero);
+        const bool some_zero = __any_sync(0xffffffffu, zero);
 #pragma unroll
         for (int c8 = 0; c8 < HR / 8; ++c8) {
           if (c8 / 2 < hch) {
