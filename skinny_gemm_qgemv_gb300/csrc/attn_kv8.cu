@@ -728,9 +728,10 @@ AttnLaunch attn_smem(int R) {
   const size_t budget = (size_t)device_max_smem_optin() - 2048 - fixed;
   const size_t per = (size_t)S::kWarps * (S::kStage + 16 * S::kUps + 8);
   AttnLaunch l;
-  // Three are enough to stream at HBM's rate; more only queue up there, and CTAs end further apart (heads of 64, 32
-  // requests of 1..8192 tokens: 44.7 us with as many as fit, 43.6 with three).
-  l.stages = (int)std::min<size_t>(3, budget / per);
+  // Two steps ahead (128 KB an SM) are enough to stream at HBM's rate; more only queue up there, and CTAs end further
+  // apart (131071 tokens 52.0 us with three, 50.7 with two; e4m3 51.9 and 49.6; heads of 256, 65536 tokens 55.0 and 52.8;
+  // 32 ragged requests 55.5 and 55.0; only with e4m3 in blocks of 16 the other way, 53.4 and 54.0).
+  l.stages = (int)std::min<size_t>(2, budget / per);
   l.ring = (uint32_t)((size_t)l.stages * S::kWarps * S::kStage);
   l.smem = fixed + per * l.stages;
   return l;
