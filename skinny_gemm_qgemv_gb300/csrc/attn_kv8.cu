@@ -19,10 +19,10 @@
 // through ldmatrix's byte transposition as A fragments of O^T = V^T P^T: nothing
 // is converted twice and nothing goes back to shared memory. Pieces of a context
 // cut by shares are added up by the CTA that brings the last one.
-// Measured (32 query heads, 8 key/value heads of 128, int8): 131071 tokens 52.0 us,
-// 268 MB at 5.2 TB/s; the streaming itself runs at 6.7 TB/s, and 12 us go to the
+// Measured (32 query heads, 8 key/value heads of 128, int8): 131071 tokens 50.5 us,
+// 268 MB at 5.3 TB/s; the streaming itself runs at 6.7 TB/s, and 12 us go to the
 // launch, the first copies and the joining of pieces. 32 requests of 1..8192
-// tokens: 53.2 us, 270 MB. One token over 37 tokens: 6.4 us, all latency.
+// tokens: 54.1 us, 270 MB. One token over 37 tokens: 6.3 us, all latency.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -768,7 +768,7 @@ int attn_rows(const AttnArgs& a) { return (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv)
 // The tcgen05 kernel for many rows of up to 128 elements. This file's kernel passes over the cache once per 16 rows, at
 // 5 ns per 128 tokens of a head (3 ns with heads of 64); that one takes 7 ns per 128 tokens and 64 rows, and about 3 us
 // more to begin, end and join. Measured, here and there: one request, 64 rows, 300 tokens 9.7 and 13.8 us, 2048 tokens
-// 15.8 and 15.2, 8192 tokens 24.2 and 18.5, 32784 tokens 56.0 and 32.5; 32 rows, 8192 tokens 17.3 and 17.2, 32768 tokens
+// 15.8 and 15.2, 8192 tokens 24.2 and 17.6, 32784 tokens 56.0 and 30.4; 32 rows, 8192 tokens 17.3 and 17.2, 32768 tokens
 // 33.5 and 29.4; heads of 64, 64 rows, 65536 tokens 42.3 and 32.7; six requests of 40 rows over 5000 tokens 14.3 and
 // 16.2. The lengths are known to the GPU alone, so their bound decides.
 bool attn_tc_ok(const AttnArgs& a) {

@@ -22,10 +22,10 @@
 // buffers of every kind; S of step i + 1 is issued before O of step i. The batch
 // is cut into shares as in attn_kv8.cu; a second kernel joins a context's pieces.
 //
-// Measured: 64 rows of 8 heads over 32784 int8 tokens 32.5 us (67 MB at 2.1 TB/s, 8.6
-// GFLOP), 65568 tokens 51 us. A step takes 1.35 us against 0.6 us of copies (a 152nd of
+// Measured: 64 rows of 8 heads over 32784 int8 tokens 30.4 us (67 MB at 2.2 TB/s, 8.6
+// GFLOP), 65568 tokens 47 us. A step takes 1.25 us against 0.6 us of copies (a 152nd of
 // HBM) and 0.3 us of MMAs: it is bound by the chain from one S to its P in the softmax
-// warps and by what the MMA warp waits for and issues, all at about 2500 cycles; no single
+// warps and by what the MMA warp waits for and issues, all at about 2300 cycles; no single
 // part taken out makes it more than 8 % faster. 6 us go to the first step, 5 to the last
 // results and their joining.
 #include <cuda_runtime.h>
@@ -43,7 +43,7 @@ namespace {
 constexpr int kTcRows = 64;     // query rows of an item
 constexpr int kTcTok = 128;     // tokens of a step
 constexpr int kTcThreads = 512;
-// an item costs about 7 us to begin and end, a step 1.35 us; joining is a kernel of its own, so only the shortest items
+// an item costs about 7 us to begin and end, a step 1.25 us; joining is a kernel of its own, so only the shortest items
 // are kept whole
 using TcCut = AttnCut<kTcTok, 5, 2>;
 constexpr int kTcMaxCtas = 152;  // CTAs: the join kernel's factors and the table of split items are laid out for it
