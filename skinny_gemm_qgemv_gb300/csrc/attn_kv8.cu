@@ -22,7 +22,7 @@
 // Measured (32 query heads, 8 key/value heads of 128, int8): 131071 tokens 50.5 us,
 // 268 MB at 5.3 TB/s; the streaming itself runs at 6.7 TB/s, and 12 us go to the
 // launch, the first copies and the joining of pieces. 32 requests of 1..8192
-// tokens: 54.1 us, 270 MB. One token over 37 tokens: 6.3 us, all latency.
+// tokens: 52.8 us, 270 MB. One token over 37 tokens: 6.3 us, all latency.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,10 +35,11 @@
 namespace qg {
 namespace {
 
-// An item costs about as much as 3 steps to begin and end (2.7 us); one of up to 6 steps is not cut: joining its pieces
-// takes longer (4 us) than its steps on one CTA.
-constexpr int kItemCost = 3;
-constexpr int kWholeSteps = 6;
+// An item costs about as much as 2 steps to begin and end; one of up to 3 steps is not cut: joining its pieces takes
+// longer than its steps on one CTA. With (2, 3), (3, 6) and (1, 3): 32 ragged requests of four drafts 63.2, 66.6 and
+// 73.4 us, of one token 52.8, 54.2 and 56.9; one of 1024 tokens 8.9, 10.3 and 8.9; 16 of 1..1024 tokens 11.3, 11.0, 15.3.
+constexpr int kItemCost = 2;
+constexpr int kWholeSteps = 3;
 
 // D: elements of a head, filled up with zeros to 64, 128 or 256 as the copies land (a.D is what the arrays have)
 template <int D, int NT, int FMT>
