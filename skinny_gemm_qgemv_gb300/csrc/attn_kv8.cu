@@ -19,10 +19,10 @@
 // through ldmatrix's byte transposition as A fragments of O^T = V^T P^T: nothing
 // is converted twice and nothing goes back to shared memory. Pieces of a context
 // cut by shares are added up by the CTA that brings the last one.
-// Measured (32 query heads, 8 key/value heads of 128, int8): 131071 tokens 50.5 us,
-// 268 MB at 5.3 TB/s; the streaming itself runs at 6.7 TB/s, and 12 us go to the
+// Measured (32 query heads, 8 key/value heads of 128, int8): 131071 tokens 50.1 us,
+// 268 MB at 5.4 TB/s; the streaming itself runs at 6.7 TB/s, and 10 us go to the
 // launch, the first copies and the joining of pieces. 32 requests of 1..8192
-// tokens: 52.8 us, 270 MB. One token over 37 tokens: 6.3 us, all latency.
+// tokens: 52.8 us, 270 MB. One token over 37 tokens: 6.2 us, all latency.
 #include <cuda_runtime.h>
 
 #include <algorithm>

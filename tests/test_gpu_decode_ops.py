@@ -526,7 +526,7 @@ def test_decode_ops_back_to_back_with_pdl(q):
 
 # --------------------------------------------------------------------------
 # attention, many query rows: a wide block table makes the bound of the lengths large, and with it the tcgen05 kernel
-# runs (more than 32 rows of 128 elements per key/value head)
+# runs (more than 16 rows of up to 128 elements per key/value head)
 # --------------------------------------------------------------------------
 
 def widen(c, tokens=1 << 20):
