@@ -46,6 +46,7 @@ template <int D, int NT, int FMT>
 struct AttnShape {
   static constexpr int kWarps = 8;
   static constexpr int kRows = 8 * NT;
+  static_assert(kRows <= kMmaRows, "the workspace's pieces");
   static constexpr int kUps = NT <= 2 && D <= 128 ? 2 : 1;  // units of a warp's step
   static constexpr int kSubs = D > 128 ? D / 128 : 1;  // 128-byte column blocks of a token
   static constexpr int kRowBytes = D > 128 ? 128 : D;
@@ -774,7 +775,7 @@ int attn_rows(const AttnArgs& a) { return (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv)
 // 16.2. The lengths are known to the GPU alone, so their bound decides.
 bool attn_tc_ok(const AttnArgs& a) {
   const int width = attn_width(a.D);
-  if (width > 128) return false;
+  if (width > kTcHead) return false;
   const long long rows = attn_rows(a), steps = (long long)a.R * a.Hkv * (((long long)a.max_blocks * a.bs + 127) / 128);
   return steps * ((width == 64 ? 3 : 5) * ((rows + 15) / 16) - 7 * ((rows + 63) / 64)) >= 3000;
 }
@@ -793,8 +794,10 @@ cudaError_t launch_by_shape(const AttnArgs& a, cudaStream_t stream, bool pdl) {
 }  // namespace
 
 size_t attn_kv8_workspace_size(int, int, int D) {
-  const int w = attn_width(D);
-  return kAttnCounterBytes + 2 * (size_t)std::min(device_sm_count(), kMaxCtas) * attn_piece_bytes(w == 256 ? 16 : 64, w);
+  // which kernel runs depends on the call: the larger pieces of those that may
+  size_t piece = attn_piece_bytes(kMmaRows, attn_width(D));
+  if (attn_width(D) <= kTcHead) piece = std::max(piece, attn_piece_bytes(kTcRows, kTcHead));
+  return kAttnCounterBytes + 2 * (size_t)std::min(device_sm_count(), kMaxCtas) * piece;
 }
 
 bool attn_kv8_ok(const AttnArgs& a) { return attn_most_steps(a) < (1LL << 31); }

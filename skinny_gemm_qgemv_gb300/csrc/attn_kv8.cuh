@@ -17,6 +17,10 @@ constexpr float kMinScale = 5.4210109e-20f;     // 2^-64
 constexpr size_t kAttnCounterBytes = 4096;      // one counter per CTA
 constexpr int kMaxCtas = 160;                   // CTAs, and so pieces of an item: their factors fit the combine buffer
 
+constexpr int kMmaRows = 16;                    // query rows of an item of the warp-level kernel, at most
+constexpr int kTcRows = 64;                     // query rows of an item of the tcgen05 kernel
+constexpr int kTcHead = 128;                    // elements that it fills every head up to
+
 // bytes of the partial results of one CTA's piece: fp32 outputs, then (max, sum) per row
 __host__ __device__ constexpr size_t attn_piece_bytes(int rows, int D) { return (size_t)rows * (D * 4 + 8); }
 

@@ -40,7 +40,6 @@
 namespace qg {
 namespace {
 
-constexpr int kTcRows = 64;     // query rows of an item
 constexpr int kTcTok = 128;     // tokens of a step
 constexpr int kTcThreads = 512;
 // an item costs about 7 us to begin and end, a step 1.25 us; joining is a kernel of its own, so only the shortest items
@@ -48,7 +47,7 @@ constexpr int kTcThreads = 512;
 using TcCut = AttnCut<kTcTok, 5, 2>;
 constexpr int kTcMaxCtas = 152;  // CTAs: the join kernel's factors and the table of split items are laid out for it
 
-constexpr int D = 128;  // elements of a head; fewer (a.D) are filled up with zeros as the copies land
+constexpr int D = kTcHead;  // elements of a head; fewer (a.D) are filled up with zeros as the copies land
 struct TcShape {
   static constexpr int kTile = kTcTok * D;                // a step's keys (or values) as stored
   static constexpr int kStage = 2 * kTile;
@@ -186,6 +185,7 @@ __device__ __forceinline__ int4* tc_splits(void* ws) {
   return reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kMaxCtas * 4);
 }
 static_assert(kMaxCtas * 4 + kTcMaxCtas * 16 <= kAttnCounterBytes, "");
+static_assert(kTcMaxCtas <= kMaxCtas, "the workspace has pieces for kMaxCtas");
 
 // the rest of a wait that did not succeed at once; gives up when another role has
 __device__ __noinline__ bool tc_wait_on(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* err) {

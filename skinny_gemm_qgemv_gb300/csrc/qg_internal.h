@@ -291,7 +291,7 @@ size_t attn_kv8_workspace_size(int Hq, int Hkv, int D);
 // false: more work than the kernel counts (2^31 steps of 128 tokens and 8 rows)
 bool attn_kv8_ok(const AttnArgs& a);
 cudaError_t launch_attn_kv8(const AttnArgs& a, int format, cudaStream_t stream, bool pdl);
-cudaError_t launch_attn_kv8_tc(const AttnArgs& a, int format, cudaStream_t stream, bool pdl);  // D = 128
+cudaError_t launch_attn_kv8_tc(const AttnArgs& a, int format, cudaStream_t stream, bool pdl);  // D <= 128
 cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t stream, bool pdl);
 
 // MXFP4 MoE (moe_mxfp4.cu, moe_mx_mma.cu)

@@ -173,3 +173,14 @@ def test_workspace_query(L):
     for D in (16, 64, 80, 128, 256):
         assert q.workspace_size(q.OP_ATTN_KV8, M=8, N=2, K=D) == L.qg_attn_kv8_workspace_size(8, 2, D) > 0
     assert q.workspace_size(q.OP_ATTN_KV8, M=7, N=2, K=128) == 0
+
+
+def test_attention_workspace_holds_the_widest_pieces(L):
+    """The many-row kernel fills heads of up to 128 elements up to 128: its pieces of a split context, 64 rows of 128
+    fp32 values with a maximum and a sum each and two of them a CTA, have that size whatever D is."""
+    full = L.qg_attn_kv8_workspace_size(8, 2, 128)
+    for D in range(16, 129, 16):
+        assert L.qg_attn_kv8_workspace_size(8, 2, D) == full, D
+    # without a device the query answers for one CTA; a device has more
+    assert full >= 4096 + 2 * 64 * (128 * 4 + 8)
+    assert L.qg_attn_kv8_workspace_size(8, 2, 256) >= 4096 + 2 * 16 * (256 * 4 + 8)

@@ -860,3 +860,21 @@ def test_writes_stay_inside(q):
                               scale=make((M,), torch.float32))
     torch.cuda.synchronize()
     assert all(intact(b) for b in bands)
+
+
+@pytest.mark.parametrize("D", [16, 64, 96, 128, 256])
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_pieces_stay_in_the_queried_workspace(q, D, wide):
+    """Contexts split over all CTAs (every CTA has a piece of two items) with a workspace of exactly the queried size,
+    16 MB of a fixed pattern behind it; with a wide table heads of up to 128 run on the tcgen05 kernel."""
+    rng = np.random.default_rng(71 + D)
+    Hq, Hkv = 20, 4
+    c = attn_case(rng, [9, 12, 5], [9000, 4100, 6007], Hq, Hkv, D, 64, "i8", False)
+    if wide:
+        c = widen(c)
+    need, behind = q.lib().qg_attn_kv8_workspace_size(Hq, Hkv, D), 16 << 20
+    buf = torch.full((BAND + need + behind,), 0xA5, device=DEV, dtype=torch.uint8)
+    ws = buf[BAND:BAND + need].zero_()
+    for _ in range(2):
+        check_attn(run_attn(q, c, workspace=ws), c)
+        assert intact((buf, need))
