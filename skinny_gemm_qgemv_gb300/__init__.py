@@ -567,7 +567,8 @@ def kv8_block_plan(old_lens, new_lens, block_table, free_list, free_count, block
     [num_blocks] are updated in place. Returns (free_count_out, cu_new,
     slot_map, positions, info); info = [new tokens, taken, released, state],
     state 0 unless nothing was done (see the header). free_count_out may be
-    free_count. The zeroed workspace is kept per (device, stream)."""
+    free_count. The zeroed workspace is kept per (device, stream); a stream
+    capture has one of its own."""
     return (_bind or _binding()).block_plan(old_lens, new_lens, block_table, free_list, free_count, block_size,
                                             max_tokens, free_count_out, cu_new, slot_map, positions, info, workspace,
                                             stream)
@@ -593,8 +594,8 @@ def attn_kv8_paged(q, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tre
     paged cache: request r's queries are rows cu_q[r] .. cu_q[r + 1] - 1, the
     last of its ctx_lens[r] tokens; causal, or by tree_mask (int32 [T], bit j:
     query token j of the request is seen). softmax_scale defaults to D ** -0.5.
-    Returns out, bf16 [T][Hq][D]. The zeroed workspace is kept per (device,
-    stream)."""
+    Returns out, bf16 [T][Hq][D]; rows past cu_q[R] are not written. The zeroed
+    workspace is kept per (device, stream); a stream capture has one of its own."""
     return (_bind or _binding()).attention(q, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tree_mask,
                                            softmax_scale, out, workspace, stream)
 

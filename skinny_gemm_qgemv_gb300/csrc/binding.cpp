@@ -170,20 +170,39 @@ class Outputs {
 };
 
 // A workspace whose counters every call leaves at zero, kept per (use, device,
-// stream): calls on one stream are ordered, so they may share it. In a stream
-// capture a new one is made (its zero fill is captured too) and not kept.
+// stream): calls on one stream are ordered, so they may share it. A stream that
+// is being captured has one per capture instead, zeroed within the graph and of
+// the graph's own memory: a graph may be replayed on any stream, next to eager
+// calls on the captured one, and outlives what is kept for those. (It is held
+// until the stream's next call that is not of that capture, so that one zero fill
+// serves all of the graph's calls.)
 at::Tensor zeroed_workspace(const Call& c, const char* use, size_t bytes) {
-  static auto* kept = new std::map<std::tuple<std::string, int, void*>, at::Tensor>;  // outlives the interpreter's end
-  const auto key = std::make_tuple(std::string(use), static_cast<int>(c.dev.index()), c.stream);
-  auto it = kept->find(key);
-  if (it != kept->end() && it->second.nbytes() >= bytes) return it->second;
+  using Key = std::tuple<std::string, int, void*>;
+  static auto* kept = new std::map<Key, at::Tensor>;  // both outlive the interpreter's end
+  static auto* captured = new std::map<Key, std::pair<unsigned long long, at::Tensor>>;
+  const Key key(use, static_cast<int>(c.dev.index()), c.stream);
   const auto st = static_cast<cudaStream_t>(c.stream);
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) cudaGetLastError();
-  c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(st, c.dev.index()));
-  at::Tensor ws = at::zeros({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(c.dev));
-  if (capturing == cudaStreamCaptureStatusNone) (*kept)[key] = ws;
-  return ws;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(st, &capturing, &id) != cudaSuccess) {
+    cudaGetLastError();
+    capturing = cudaStreamCaptureStatusNone;
+  }
+  auto make = [&]() {
+    c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(st, c.dev.index()));
+    return at::zeros({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(c.dev));
+  };
+  if (capturing != cudaStreamCaptureStatusNone) {
+    auto it = captured->find(key);
+    if (it != captured->end() && it->second.first == id && it->second.second.nbytes() >= bytes) return it->second.second;
+    const at::Tensor ws = make();
+    (*captured)[key] = {id, ws};
+    return ws;
+  }
+  if (!captured->empty()) captured->erase(key);
+  auto it = kept->find(key);
+  if (it != kept->end() && it->second.nbytes() >= bytes) return it->second;
+  return (*kept)[key] = make();
 }
 
 at::Tensor workspace(const Call& c, PyObject* given, const char* use, size_t bytes) {

@@ -878,3 +878,124 @@ def test_attention_pieces_stay_in_the_queried_workspace(q, D, wide):
     for _ in range(2):
         check_attn(run_attn(q, c, workspace=ws), c)
         assert intact((buf, need))
+
+
+# --------------------------------------------------------------------------
+# workspaces and stream captures
+# --------------------------------------------------------------------------
+
+def on_device(c):
+    return [c["x"].to(DEV), to_cache(c["kc"], c["fmt"]), to_cache(c["vc"], c["fmt"]), torch.from_numpy(c["sc"]).to(DEV),
+            i32(c["table"]), i32(c["ctx"]), i32(c["cu"])]
+
+
+def captured(st, calls):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        calls()
+    return g
+
+
+def test_a_capture_has_a_workspace_of_its_own(q):
+    """Also where the captured stream has had an eager call: the graph's own memory holds the workspace."""
+    rng = np.random.default_rng(81)
+    c = attn_case(rng, [1, 2], [3000, 400], 8, 2, 128, 16, "i8", False)
+    dev, out = on_device(c), torch.full(c["x"].shape, 7.0, device=DEV, dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        q.attn_kv8_paged(*dev, out=out)                  # a workspace is kept for the stream
+    st.synchronize()
+    g = captured(st, lambda: (q.attn_kv8_paged(*dev, out=out), q.attn_kv8_paged(*dev, out=out)))
+    need = q.lib().qg_attn_kv8_workspace_size(8, 2, 128)
+    own = sum(s["total_size"] for s in torch.cuda.memory_snapshot() if tuple(s["segment_pool_id"]) == tuple(g.pool()))
+    assert own >= need
+    for _ in range(3):
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        check_attn(out.cpu(), c)
+
+
+def test_a_graph_outlives_the_kept_workspace(q):
+    """An eager call that needs a larger workspace on the captured stream replaces the kept one; what then gets its
+    memory is not written by replays."""
+    rng = np.random.default_rng(82)
+    small = attn_case(rng, [2, 1], [5000, 700], 8, 2, 256, 32, "i8", False)
+    large = attn_case(rng, [1, 1], [4000, 60], 8, 2, 128, 32, "i8", False)
+    st = torch.cuda.Stream()
+    ds, dl = on_device(small), on_device(large)
+    outs = [torch.full(c["x"].shape, 7.0, device=DEV, dtype=torch.bfloat16) for c in (small, large)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        q.attn_kv8_paged(*ds, out=outs[0])
+    g = captured(st, lambda: q.attn_kv8_paged(*ds, out=outs[0]))
+    with torch.cuda.stream(st):
+        q.attn_kv8_paged(*dl, out=outs[1])
+        fill = [torch.full((4 << 20,), 0x5A, device=DEV, dtype=torch.uint8) for _ in range(8)]
+        outs[0].fill_(7.0)
+        for _ in range(3):
+            g.replay()
+            q.attn_kv8_paged(*dl, out=outs[1])
+    st.synchronize()
+    assert all(bool((f == 0x5A).all()) for f in fill)
+    check_attn(outs[0].cpu(), small)
+    check_attn(outs[1].cpu(), large)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_graphs_of_one_stream_replayed_side_by_side(q, wide):
+    """Two graphs captured on a stream that has had eager calls, replayed on two streams next to further eager ones."""
+    rng = np.random.default_rng(83)
+    cases = [attn_case(rng, [9, 2], [6000, 500], 16, 2, 128, 16, "i8", False) for _ in range(3)]
+    if wide:
+        cases = [widen(c) for c in cases]
+    dev = [on_device(c) for c in cases]
+    outs = [torch.full(c["x"].shape, 7.0, device=DEV, dtype=torch.bfloat16) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    with torch.cuda.stream(streams[0]):
+        q.attn_kv8_paged(*dev[0], out=outs[0])
+    graphs = [captured(streams[0], lambda i=i: q.attn_kv8_paged(*dev[i], out=outs[i])) for i in (1, 2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                if i == 0:
+                    q.attn_kv8_paged(*dev[0], out=outs[0])
+                else:
+                    graphs[i - 1].replay()
+    torch.cuda.synchronize()
+    for c, out in zip(cases, outs):
+        check_attn(out.cpu(), c)
+
+
+def test_plans_captured_on_one_stream_replayed_side_by_side(q):
+    """The plan's ticket too: several CTAs a call, the count written by the last."""
+    rng = np.random.default_rng(84)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    states = [plan_state(rng, 300, 16, 90, 60, 5) for _ in range(3)]
+    tokens = [int(np.maximum(n - o, 0).sum()) for o, n, *_ in states]
+    args = [[i32(o), i32(n), i32(t), i32(f), i32([c])] for o, n, t, f, c in states]
+    outs = [dict(free_count_out=i32([-9]), cu_new=i32([0] * 301), slot_map=i32([0] * t), positions=i32([0] * t),
+                 info=i32([9] * 4)) for t in tokens]
+    calls = [lambda i=i: q.kv8_block_plan(*args[i], 16, tokens[i], **outs[i]) for i in range(3)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(streams[0]):
+        calls[0]()
+    graphs = [captured(streams[0], c) for c in calls[1:]]
+    torch.cuda.synchronize()
+    want = [od.block_plan(o, n, t, f, c, 16, k) for (o, n, t, f, c), k in zip(states, tokens)]
+    for _ in range(10):
+        for i, (o, n, t, f, c) in enumerate(states):     # as they were
+            args[i][2].copy_(i32(t)), args[i][3].copy_(i32(f)), outs[i]["free_count_out"].fill_(-9)
+        torch.cuda.synchronize()
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                calls[0]() if i == 0 else graphs[i - 1].replay()
+        torch.cuda.synchronize()
+        for i in range(3):
+            got = [args[i][2], args[i][3]] + [outs[i][k] for k in ("free_count_out", "cu_new", "slot_map", "positions",
+                                                                     "info")]
+            for g, w in zip(got, want[i]):
+                assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
