@@ -197,8 +197,8 @@ def stack_io(mats, dev, M, seed=1):
 
 
 def prime_skinny_workspace(q, mats, M, dev, stream):
-    """Allocate (outside any capture) the zero-filled skinny workspace every
-    projection of the stack will share on `stream`."""
+    """Allocate the zero-filled skinny workspace that the eager calls of every
+    projection of the stack share on `stream` (a capture has its own)."""
     need = max(q.lib().qg_skinny_workspace_size(M, N, K, 64) for (_, N, K, *_r) in mats)
     if need:
         q.skinny_workspace(need, dev, stream)

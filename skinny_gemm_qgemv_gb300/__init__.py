@@ -258,26 +258,24 @@ def qgemv_w8a16(wq, scales, x, y=None, stream=None):
     return y
 
 
-_WS = {}
+def _workspace(use, nbytes, device, stream):
+    """A workspace that every call leaves zero-filled, from the compiled half
+    of the binding: kept per (use, device, stream); a stream capture has its
+    own, zeroed within the graph."""
+    device = torch.device(device)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    return (_bind or _binding()).workspace(use, nbytes, index, stream.cuda_stream)
 
 
 def skinny_workspace(nbytes, device, stream=None):
-    """A zero-filled workspace for qgemm_w4a16_skinny, cached per (device,
+    """A zero-filled workspace for qgemm_w4a16_skinny, kept per (device,
     stream) and reused (every call leaves it zero-filled): calls on one stream
     are ordered, so they may share it, and calls on different streams get
-    different ones. Inside a stream capture a fresh one is made (the zero fill
-    is captured too) and not cached."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    key = (str(device), stream.cuda_stream)
-    ws = _WS.get(key)
-    if ws is not None and ws.numel() >= nbytes:
-        return ws
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, device=device, dtype=torch.uint8)
-    ws = torch.zeros(max(nbytes, 1 << 20), device=device, dtype=torch.uint8)
-    _WS[key] = ws
-    return ws
+    different ones. The calls of a stream capture share one of their own, of
+    the graph's memory and zeroed within the graph."""
+    return _workspace("skinny", max(nbytes, 1 << 20), device, stream)
 
 
 def qgemm_w4a16_skinny(wq, scales, biases, x, y=None, workspace=None, stream=None):
@@ -484,15 +482,12 @@ def hadamard32_quant_i8(x, sign_bits, q=None, scale=None, stream=None):
     return q, scale
 
 
-_W8WS = {}
-
-
 def gemm_w8a8_hadamard(x, sign_bits, w, sw, y=None, workspace=None, stream=None):
     """y[m][n] = C[m][n] s_a[m] s_w[n] / 32 in one launch: x bf16 [M][K] is
     transformed and quantized like hadamard32_quant_i8 (bit-exact), C = q_a w^T
     exactly; w int8 [N][K] and sw fp32 [N] are the weights quantized the same
-    way. The zero-filled workspace is cached per (device, stream) (every call
-    leaves it zeroed)."""
+    way. The zero-filled workspace is kept per (device, stream) (every call
+    leaves it zeroed); a stream capture has one of its own."""
     M, K = x.shape
     N = w.shape[0]
     for t, b, n in ((x, 2, "x"), (sign_bits, 4, "sign_bits"), (w, 1, "w"), (sw, 4, "sw")):
@@ -501,15 +496,7 @@ def gemm_w8a8_hadamard(x, sign_bits, w, sw, y=None, workspace=None, stream=None)
         y = torch.empty(M, N, device=x.device, dtype=torch.float32)
     need = lib().qg_w8a8_hadamard_workspace_size(M, K)
     if workspace is None:
-        st = stream if stream is not None else torch.cuda.current_stream(x.device)
-        key = (str(x.device), st.cuda_stream)
-        workspace = _W8WS.get(key)
-        if workspace is None or workspace.numel() < need:
-            if torch.cuda.is_current_stream_capturing():
-                workspace = torch.zeros(need, device=x.device, dtype=torch.uint8)
-            else:
-                workspace = torch.zeros(max(need, 1 << 16), device=x.device, dtype=torch.uint8)
-                _W8WS[key] = workspace
+        workspace = _workspace("w8a8", max(need, 1 << 16), x.device, stream)
     _check(lib().gemm_w8a8_hadamard(_p(x), _p(sign_bits), _p(w), _p(sw), _p(y), M, N, K, _p(workspace),
                                     workspace.numel(), _stream(stream)), "gemm_w8a8_hadamard")
     return y

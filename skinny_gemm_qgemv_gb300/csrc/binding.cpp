@@ -176,12 +176,11 @@ class Outputs {
 // calls on the captured one, and outlives what is kept for those. (It is held
 // until the stream's next call that is not of that capture, so that one zero fill
 // serves all of the graph's calls.)
-at::Tensor zeroed_workspace(const Call& c, const char* use, size_t bytes) {
+at::Tensor zeroed_workspace(c10::Device dev, cudaStream_t st, const char* use, size_t bytes) {
   using Key = std::tuple<std::string, int, void*>;
   static auto* kept = new std::map<Key, at::Tensor>;  // both outlive the interpreter's end
   static auto* captured = new std::map<Key, std::pair<unsigned long long, at::Tensor>>;
-  const Key key(use, static_cast<int>(c.dev.index()), c.stream);
-  const auto st = static_cast<cudaStream_t>(c.stream);
+  const Key key(use, static_cast<int>(dev.index()), st);
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
   unsigned long long id = 0;
   if (cudaStreamGetCaptureInfo(st, &capturing, &id) != cudaSuccess) {
@@ -189,8 +188,8 @@ at::Tensor zeroed_workspace(const Call& c, const char* use, size_t bytes) {
     capturing = cudaStreamCaptureStatusNone;
   }
   auto make = [&]() {
-    c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(st, c.dev.index()));
-    return at::zeros({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(c.dev));
+    c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(st, dev.index()));
+    return at::zeros({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(dev));
   };
   if (capturing != cudaStreamCaptureStatusNone) {
     auto it = captured->find(key);
@@ -206,7 +205,8 @@ at::Tensor zeroed_workspace(const Call& c, const char* use, size_t bytes) {
 }
 
 at::Tensor workspace(const Call& c, PyObject* given, const char* use, size_t bytes) {
-  if (given == Py_None) return bytes ? zeroed_workspace(c, use, bytes) : at::Tensor();
+  if (given == Py_None)
+    return bytes ? zeroed_workspace(c.dev, static_cast<cudaStream_t>(c.stream), use, bytes) : at::Tensor();
   const at::Tensor& t = *tensor(given, "workspace");
   c.dense(t, "workspace");
   return t;
@@ -413,6 +413,19 @@ PyObject* norm_i8(PyObject* const* a) {
   return tuple(q, scale, n.res_out);
 }
 
+// (use, bytes, device index, stream handle): the workspace, for the calls that are marshalled in Python
+PyObject* make_workspace(PyObject* const* a) {
+  const char* use = PyUnicode_AsUTF8(a[0]);
+  if (!use) throw Raised{};
+  const int bytes = whole32(a[1], "bytes"), index = whole32(a[2], "device");
+  const auto st = reinterpret_cast<cudaStream_t>(PyLong_AsUnsignedLongLong(a[3]));
+  if (PyErr_Occurred()) throw Raised{};
+  if (bytes < 0) refuse("bytes is negative");
+  const c10::Device dev(c10::kCUDA, static_cast<c10::DeviceIndex>(index));
+  const c10::cuda::CUDAGuard guard(dev);
+  return wrap(zeroed_workspace(dev, st, use, static_cast<size_t>(bytes)));
+}
+
 // no C++ exception passes into Python
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -441,6 +454,7 @@ PyMethodDef kMethods[] = {
     {"block_plan", QG_FAST(block_plan, 14), nullptr}, {"append", QG_FAST(append, 7), nullptr},
     {"read", QG_FAST(read, 5), nullptr},              {"attention", QG_FAST(attention, 12), nullptr},
     {"norm_bf16", QG_FAST(norm_bf16, 7), nullptr},    {"norm_i8", QG_FAST(norm_i8, 9), nullptr},
+    {"workspace", QG_FAST(make_workspace, 4), nullptr},
     {"set_raise", set_raise, METH_O, nullptr},        {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_qgbind", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -999,3 +999,38 @@ def test_plans_captured_on_one_stream_replayed_side_by_side(q):
                                                                      "info")]
             for g, w in zip(got, want[i]):
                 assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+
+
+def test_captured_products_have_workspaces_of_their_own(q):
+    """The skinny product and the fused int8 product likewise, and a workspace first made for a given stream is zeroed
+    there."""
+    w4 = synth.w4_weights(512, 1024, seed=5, slot=0, device=DEV)
+    x = synth.bf16_normal((16, 1024), seed=5, slot=1, device=DEV)
+    sb = synth.sign_bits(1024, 5, 2).to(DEV)
+    w8, s8 = q.hadamard32_quant_i8(synth.bf16_normal((256, 1024), seed=5, slot=3, device=DEV), sb)
+    assert q.lib().qg_skinny_workspace_size(16, 512, 1024, 64) + q.lib().qg_w8a8_hadamard_workspace_size(16, 1024) > 0
+    want = q.qgemm_w4a16_skinny(*w4, x), q.gemm_w8a8_hadamard(x, sb, w8, s8)
+    outs = [torch.empty_like(y) for y in want]
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    kept = [q.skinny_workspace(1, DEV, st), q._workspace("w8a8", 1 << 16, DEV, st)]
+
+    def calls():
+        q.qgemm_w4a16_skinny(*w4, x, y=outs[0], stream=st)
+        q.gemm_w8a8_hadamard(x, sb, w8, s8, y=outs[1], stream=st)
+
+    calls()
+    st.synchronize()
+    inside = []
+    g = captured(st, lambda: (inside.extend((q.skinny_workspace(1, DEV), q._workspace("w8a8", 1 << 16, DEV, None))), calls()))
+    assert q.skinny_workspace(1, DEV, st).data_ptr() == kept[0].data_ptr()
+    pool = [s for s in torch.cuda.memory_snapshot() if tuple(s["segment_pool_id"]) == tuple(g.pool())]
+    for ws in inside:
+        assert any(s["address"] <= ws.data_ptr() < s["address"] + s["total_size"] for s in pool)
+    for _ in range(2):
+        for o in outs:
+            o.fill_(3.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
