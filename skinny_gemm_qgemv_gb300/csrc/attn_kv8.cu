@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   int* ctxs = cus + a.R + 1;               // [R]
   __shared__ int2 scan_part[NW];
   __shared__ unsigned arrived;
-  __shared__ float2 row_factor[ROWS];
+  __shared__ float row_factor[ROWS];
 
   if (lane == 0)
 #pragma unroll 1
@@ -259,7 +259,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   // ---- consumer ----
   float acc[NT][S::kMt][4];
   float m[NT][2], l[NT][2], rf[NT][2];
-  float off[NT][2];  // int8: the products start at -1152 times the sum of the row's fp16 queries
   constexpr bool kQRegs = S::kQRegs;
   uint2 qr[kQRegs ? S::kHalves * 4 : 1][kQRegs ? NT : 1];
   AttnPlace item = {};
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       if (kQRegs || nt % NW == warp) {
         const uint8_t* src = qraw + ((size_t)qb * ROWS + nt * 8 + g) * D * 2 + 32 * c;
         uint4 raw[S::kHalves][2];
-        float amax = 0.f, sum = 0.f;
+        float amax = 0.f;
 #pragma unroll
         for (int hf = 0; hf < S::kHalves; ++hf) {
 #pragma unroll
@@ -308,7 +307,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
             for (int j = 0; j < 4; ++j) {
               const float x = __uint_as_float(w[j] << 16), y = __uint_as_float(w[j] & 0xFFFF0000u);
               amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
-              sum += x + y;
             }
           }
         }
@@ -316,20 +314,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int sigma = fp16_prescale_exp(amax);
         const float down = pow2f(-sigma), up = a.scale_log2 * pow2f(sigma);
-        if (FMT == QG_KV_I8) {
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          sum *= -1152.f * down;
-        }
         if (kQRegs) {
           rf[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
           rf[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
-          if (FMT == QG_KV_I8) {
-            off[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-            off[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
-          }
         } else if (c == 0) {
-          row_factor[nt * 8 + g] = make_float2(up, sum);
+          row_factor[nt * 8 + g] = up;
         }
 #pragma unroll
         for (int hf = 0; hf < S::kHalves; ++hf) {
@@ -352,11 +341,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (!kQRegs) {
-          const float2 x = row_factor[nt * 8 + 2 * c + j];
-          rf[nt][j] = x.x;
-          off[nt][j] = x.y;
-        }
+        if (!kQRegs) rf[nt][j] = row_factor[nt * 8 + 2 * c + j];
         m[nt][j] = kNoMax;
         l[nt][j] = 0.f;
       }
@@ -386,7 +371,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[u][nt][j] = FMT == QG_KV_I8 ? off[nt][j & 1] : 0.f;
+        for (int j = 0; j < 4; ++j) s[u][nt][j] = 0.f;
       // S^T = K q^T: lane (g, c) holds tokens t0, t1 and 16-byte chunk c of each 64 bytes
 #pragma unroll
       for (int hf = 0; hf < S::kHalves; ++hf) {
@@ -396,8 +381,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t f[4];
-          codes_to_f16<FMT, true>(w0[w], f[0], f[2]);
-          codes_to_f16<FMT, true>(w1[w], f[1], f[3]);
+          codes_to_f16<FMT>(w0[w], f[0], f[2]);
+          codes_to_f16<FMT>(w1[w], f[1], f[3]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 b = kQRegs ? qr[hf * 4 + w][nt] : qfrag[((hf * 4 + w) * NT + nt) * 32 + lane];

@@ -1034,3 +1034,31 @@ def test_captured_products_have_workspaces_of_their_own(q):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+# --------------------------------------------------------------------------
+# attention: scores
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 10])
+def test_attention_scores_of_small_codes(q, D, fmt, G):
+    """Keys of codes +-1 under positive queries: the score's error goes by sum |q k|, not by the queries' sum. Both
+    tokens of a context have the same score (the query's halves are equal, the second key has its halves exchanged) and
+    opposite values, so what the result differs from 0 by is the scores' error."""
+    rng = np.random.default_rng(91 + D)
+    R, Hkv, bs = 64, 8, 16
+    c = attn_case(rng, [1] * R, [2] * R, G * Hkv, Hkv, D, bs, fmt, False)
+    one = {"i8": (1, 255), "e4m3": (0x38, 0xB8)}[fmt]
+    for r in range(R):
+        b = c["table"][r, 0]
+        k = np.where(rng.random((Hkv, D)) < 0.5, *one).astype(np.uint8)
+        c["kc"][b, :, 0], c["kc"][b, :, 1] = k, np.roll(k, D // 2, -1)
+        c["vc"][b, :, 0] = {"i8": 100, "e4m3": 0x6C}[fmt]
+        c["vc"][b, :, 1] = {"i8": 256 - 100, "e4m3": 0xEC}[fmt]
+    half = np.exp(rng.standard_normal(tuple(c["x"].shape[:2]) + (D // 2,)))
+    c["x"] = torch.from_numpy(np.concatenate((half, half), -1)).to(torch.bfloat16)
+    c["sc"][..., 0] = 1.0
+    scale = 0.01 / ((D + 8) * 2.0 ** -23 * float(c["x"].double().sum(-1).max()))
+    check_attn(run_attn(q, c, softmax_scale=scale), c, scale)
