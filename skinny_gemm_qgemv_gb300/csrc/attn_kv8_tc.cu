@@ -175,6 +175,7 @@ __device__ __forceinline__ float transposed_warp_max(float (&v)[R], int lane) {
   return v[0];
 }
 
+constexpr unsigned kRowSpan = 16u << 23;  // rows' queries that differ by 2^16, on the bits of fp32, do not share a scale
 constexpr int kTcMaxStages = 3;
 // Slots of the scales of a step: when step h's are written the values of step h - 3 have been converted, and before them
 // the P of step h - 5 was read: the softmax is at step h - 4 or later.
@@ -247,7 +248,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ float4 unit_scales[kTcSlots][TOK / kUnit];
   __shared__ int2 scan_part[kTcThreads / 32];
   __shared__ uint32_t tmem_base;
-  __shared__ unsigned amax_bits, unset_any[2];
+  __shared__ __align__(16) float row_scale[ROWS];  // factors of scores, where the rows' queries differ in scale
+  __shared__ unsigned amax_bits, amin_bits;  // the rows' largest finite |q|: the largest and the smallest above 0
+  __shared__ unsigned unset_any[2];
   __shared__ volatile uint32_t abort_flag;
 
   if (tid == 0) {
@@ -479,54 +482,70 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     while (next_segment(sg, step)) {
       const AttnPlace item = sg.item;
       const int n = sg.n, gi = sg.g, base = sg.base, tok0 = sg.tok0, nch = sg.nch, rows = sg.rows;
-      // The item's queries: 2^-sigma q in fp16 with one sigma for the item (its largest |q| just below 2^15; what a
-      // row 2^20 smaller loses is 2^-40 of the largest scores), K-major, swizzled. (The last segment's products have
-      // been waited for.)
+      // The item's queries: 2^-sigma q in fp16, K-major, swizzled; four threads a row. One sigma serves the item's rows
+      // (its largest finite |q| just below 2^15) down to rows 2^-16 of that, whose values keep 2^-24 of the row's
+      // largest; a smaller row gets a sigma of its own and its scores a factor. What is not finite stays so, in its own
+      // row's products. (The last segment's products have been waited for.)
       const int u = half * 128 + t;
-      constexpr int kPer = D / 8, kTimes = ROWS * kPer / 256;  // threads of a row: 8 elements each
-      uint4 raw[kTimes];
-      float amax = 0.f;
-#pragma unroll
-      for (int k = 0; k < kTimes; ++k) {
-        const int rr = (u + k * 256) / kPer, ch = u % kPer, rho = item.rt * ROWS + rr, i = rho / batch.G;
-        raw[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < rows && 8 * ch < a.D)
-          raw[k] = *reinterpret_cast<const uint4*>(a.q + (size_t)(sg.q0 + i) * a.q_stride +
-                                                   (item.h * batch.G + rho - i * batch.G) * a.D + 8 * ch);
-      }
-      if (u == 0) amax_bits = 0u;
-      if (u < ROWS) {
-        const int rho = item.rt * ROWS + u;
-        int4 info = make_int4(0x7FFFFFFF, 0, -1, 0);
-        if (u < rows) {
-          const int i = rho / batch.G;
-          const bool tree = a.tree && sg.nq <= 32;
-          info.x = tree ? base : base + i + 1;
-          if (tree) info.y = (int)(a.tree[sg.q0 + i] & (0xFFFFFFFFu >> (32 - sg.nq)));
-          info.z = (sg.q0 + i) * a.Hq + item.h * batch.G + rho - i * batch.G;
-        }
-        row_info[u] = info;
-        neg_m[u] = 0.f;
-      }
-      named_barrier<256>(3);
       float up;
+      auto rows_differ = [&]() {  // some row has a sigma of its own
+        return amin_bits < amax_bits && amax_bits - amin_bits > kRowSpan;
+      };
       {
+        constexpr int kPer = 256 / ROWS, kTimes = D / 8 / kPer;  // threads of a row, 8 elements at a time
+        const int rr = u / kPer, c0 = u % kPer, rho = item.rt * ROWS + rr, qi = rho / batch.G;
+        const int head = item.h * batch.G + rho - qi * batch.G;
+        uint4 raw[kTimes];
+        const uint16_t* src = a.q + (size_t)(sg.q0 + qi) * a.q_stride + head * a.D;
+#pragma unroll
+        for (int k = 0; k < kTimes; ++k) {
+          const int ch = c0 + k * kPer;
+          raw[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < rows && 8 * ch < a.D) raw[k] = *reinterpret_cast<const uint4*>(src + 8 * ch);
+        }
+        if (u == 0) amax_bits = 0u, amin_bits = 0xFFFFFFFFu;
+        if (c0 == 0) {
+          int4 info = make_int4(0x7FFFFFFF, 0, -1, 0);
+          if (rr < rows) {
+            const bool tree = a.tree && sg.nq <= 32;
+            info.x = tree ? base : base + qi + 1;
+            if (tree) info.y = (int)(a.tree[sg.q0 + qi] & (0xFFFFFFFFu >> (32 - sg.nq)));
+            info.z = (sg.q0 + qi) * a.Hq + head;
+          }
+          row_info[rr] = info;
+          neg_m[rr] = 0.f;
+        }
+        named_barrier<256>(3);
+        unsigned row_max = 0u;  // largest finite |q| as the bits of an fp32
 #pragma unroll
         for (int k = 0; k < kTimes; ++k) {
           const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+          for (int j = 0; j < 4; ++j) {
+            const unsigned lo = w[j] << 16 & 0x7FFF0000u, hi = w[j] & 0x7FFF0000u;
+            row_max = max(row_max, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+          }
         }
-        const unsigned wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-        if (lane == 0) atomicMax(&amax_bits, wm);
+#pragma unroll
+        for (int o = 1; o < kPer; o <<= 1) row_max = max(row_max, __shfl_xor_sync(0xffffffffu, row_max, o));
+        const unsigned most = __reduce_max_sync(0xffffffffu, row_max),
+                       least = __reduce_min_sync(0xffffffffu, row_max ? row_max : 0xFFFFFFFFu);
+        if (lane == 0) atomicMax(&amax_bits, most), atomicMin(&amin_bits, least);
         named_barrier<256>(3);
-        const int sigma = fp16_prescale_exp(__uint_as_float(amax_bits));
-        const float down = pow2f(-sigma);
+        int sigma = fp16_prescale_exp(__uint_as_float(amax_bits));
         up = a.scale_log2 * pow2f(sigma);
+        const bool differ = rows_differ();
+        if (differ) {
+          int own = sigma;
+          if (row_max && amax_bits - row_max > kRowSpan)
+            own = max(fp16_prescale_exp(__uint_as_float(row_max)), sigma - 126);
+          if (c0 == 0) row_scale[rr] = pow2f(own - sigma);
+          sigma = own;
+        }
+        const float down = pow2f(-sigma);
 #pragma unroll
         for (int k = 0; k < kTimes; ++k) {
-          const int rr = (u + k * 256) / kPer, ch = u % kPer;
+          const int ch = c0 + k * kPer;
           const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
           uint32_t f[4];
 #pragma unroll
@@ -538,6 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full);
+        if (differ) named_barrier<256>(3);
       }
       // this half's columns: hch chunks of 16 from column hc on
       const int hc = half ? 16 * ((nch + 1) / 2) : 0, hch = half ? nch / 2 : (nch + 1) / 2;
@@ -606,6 +626,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         grow |= fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kSlack;
         // (P of two steps ago has been read: its product was issued before this step's S, whose end has been waited for)
         if (named_barrier_or<128>(bar, grow)) {
+          // rows with a sigma of their own: the factor for what the scores put on top of c (here, where such items come
+          // in every step, and not where scores are read: the loop has no register to spare, 64 rows over 65568 tokens
+          // took 57 us instead of 48)
+          if (rows_differ()) {
+#pragma unroll
+            for (int j = 0; j < HR; ++j) {
+              if (j / 16 < hch) {
+                const float cj = sc.y + nm_of[j];
+                y[j] = fmaf(row_scale[hc + j], y[j] - cj, cj);
+              }
+            }
+          }
           // rows whose m has to rise (or to be set): the largest y over the step's tokens
           {
             float top[HR];
@@ -630,7 +662,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             neg_m[j] -= rise;
           }
           named_barrier<128>(bar);
-          unset = unset_any[half] != 0u;
+          unset = unset_any[half] != 0u || rows_differ();
           if (i > 0) wait_warp(o_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
           tc_after();
 #pragma unroll

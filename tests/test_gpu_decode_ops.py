@@ -1062,3 +1062,28 @@ def test_attention_scores_of_small_codes(q, D, fmt, G):
     c["sc"][..., 0] = 1.0
     scale = 0.01 / ((D + 8) * 2.0 ** -23 * float(c["x"].double().sum(-1).max()))
     check_attn(run_attn(q, c, softmax_scale=scale), c, scale)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attention_rows_do_not_touch_one_another(q, wide, tree):
+    """Infinite and NaN query elements stay in their own rows, and rows of very different sizes keep their precision,
+    also where many rows share a pass over the cache."""
+    rng = np.random.default_rng(95)
+    c = attn_case(rng, [14, 9], [1500, 333], 16, 4, 128, 32, "i8", tree, qstd=1.5)
+    if wide:
+        c = widen(c)
+    for (t, h), f in {(1, 2): 2.0 ** 30, (3, 5): 2.0 ** -17, (4, 5): 2.0 ** 17, (6, 9): 2.0 ** 100, (7, 9): 0.0,
+                      (16, 15): 2.0 ** 20, (17, 3): 2.0 ** -100}.items():
+        c["x"][t, h] = (c["x"][t, h].float() * f).to(torch.bfloat16)
+    check_attn(run_attn(q, c), c)
+    bad = [(0, 1), (2, 5), (5, 6), (18, 0), (22, 15)]
+    clean = dict(c, x=c["x"].clone())
+    for i, (t, h) in enumerate(bad):
+        clean["x"][t, h] = 0.0
+        c["x"][t, h, 7 * i] = (math.inf, math.nan, -math.inf)[i % 3]
+    out = run_attn(q, c)
+    for t, h in bad:
+        assert bool(out[t, h].isnan().any())
+        out[t, h] = run_attn(q, clean)[t, h]
+    check_attn(out, clean)
