@@ -11,7 +11,7 @@
 namespace qg {
 
 constexpr int kUnit = 16;                       // tokens that lie in one block, whatever its size: one scale pair
-constexpr float kNoMax = -1e30f;                // running maximum before any seen token
+constexpr float kNoMax = -3.402823466e+38f;     // running maximum before any seen token: no finite score is below it
 constexpr float kSlack = 8.f;                   // log2: probabilities stay below 2^8 (fp16 holds 2^15)
 constexpr float kMinScale = 5.4210109e-20f;     // 2^-64
 constexpr size_t kAttnCounterBytes = 4096;      // one counter per CTA

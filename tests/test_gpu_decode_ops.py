@@ -1087,3 +1087,16 @@ def test_attention_rows_do_not_touch_one_another(q, wide, tree):
         assert bool(out[t, h].isnan().any())
         out[t, h] = run_attn(q, clean)[t, h]
     check_attn(out, clean)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq,ctx,wide", [(1, 1, False), (1, 3000, False), (16, 16, True), (16, 3000, True)])
+def test_attention_scores_far_below_zero(q, D, nq, ctx, wide):
+    """Every seen score is some -1e31: values that are all alike come out, whatever the weights."""
+    c = attn_case(np.random.default_rng(97), [nq], [ctx], 8, 2, D, 16, "i8", False)
+    if wide:
+        c = widen(c)
+    c["x"][:] = -1e30
+    c["kc"][:], c["vc"][:], c["sc"][:] = 1, 100, 1.0
+    out = run_attn(q, c)[:nq].float()
+    assert bool(((out - 100.0).abs() <= 100 * 2.0 ** -8).all())
