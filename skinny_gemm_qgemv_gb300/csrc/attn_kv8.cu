@@ -424,8 +424,9 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        grow |= fmaxf(s[u][nt][0], s[u][nt][2]) > m[nt][0] + kSlack ||
-                fmaxf(s[u][nt][1], s[u][nt][3]) > m[nt][1] + kSlack;
+        // (the difference, which is exact where it is small: m + kSlack may round up to a score whose p passes fp16)
+        grow |= fmaxf(s[u][nt][0], s[u][nt][2]) - m[nt][0] > kSlack ||
+                fmaxf(s[u][nt][1], s[u][nt][3]) - m[nt][1] > kSlack;
     }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll

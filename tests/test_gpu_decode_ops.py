@@ -1100,3 +1100,24 @@ def test_attention_scores_far_below_zero(q, D, nq, ctx, wide):
     c["kc"][:], c["vc"][:], c["sc"][:] = 1, 100, 1.0
     out = run_attn(q, c)[:nq].float()
     assert bool(((out - 100.0).abs() <= 100 * 2.0 ** -8).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_scores_past_the_steps_of_fp32(q, D):
+    """Scores of 2^27, where fp32 has steps of 16: a later token one step above the largest so far takes all weight."""
+    rng = np.random.default_rng(98)
+    apart = 128 if D == 256 else 256                      # tokens of a step: one warp takes these, one after the other
+    c = attn_case(rng, [1], [2 * apart + 80], 8, 2, D, 16, "i8", False)
+    c["kc"][:] = 0
+    c["sc"][:] = 1.0
+    c["x"][:] = 0.0
+    c["x"][..., 0], c["x"][..., 1] = 2.0 ** 27, 16.0
+    scale = float(np.float32(np.log(2.0)))               # the scores are q . k in units of log 2
+    assert np.float32(scale) * np.float32(np.log2(np.e)) == 1
+    for j in (1, 2, 3):
+        tok = 3 + (j - 1) * apart
+        b = c["table"][0, tok // 16]
+        c["kc"][b, :, tok % 16, 0], c["kc"][b, :, tok % 16, 1] = 1, j
+    want = torch.from_numpy(c["vc"][b, :, tok % 16].view(np.int8).astype(np.float32)).repeat_interleave(4, 0)
+    out = run_attn(q, c, softmax_scale=scale)[0].float()
+    assert bool(((out - want).abs() <= want.abs() * 2.0 ** -8 + 2.0 ** -16 * 256).all())
