@@ -655,7 +655,8 @@ QG_API qg_status kv8_read(const int32_t *block_ids, int B, int Hkv, int D, int b
  *   q_bf16       bf16 [T][Hq][D], token t at element t * q_stride (>= Hq * D,
  *                a multiple of 8).
  *   cu_q         int32 [R + 1]: request r's query tokens are cu_q[r] ..
- *                cu_q[r+1] - 1 (none is allowed); 0 <= cu_q <= T, ascending.
+ *                cu_q[r+1] - 1 (none is allowed); 0 <= cu_q <= T, ascending
+ *                (otherwise nothing is written, and it is reported).
  *   ctx_lens     int32 [R]: tokens of request r in the cache, its n query
  *                tokens (the last n) among them; at most max_blocks *
  *                block_size (longer ones are cut there and reported).
@@ -754,7 +755,8 @@ QG_API void qg_set_pdl(int enable);
  * qg_device_error -- the sticky device-side error word of the current device:
  * 0 when no kernel has given up a bounded wait, otherwise a nonzero code
  * naming where it gave up (0x6xx: where a kernel of the paged cache met a slot
- * or block id outside the cache, or a length past its table, and skipped it).
+ * or block id outside the cache, a length past its table or query bounds
+ * that do not ascend, and skipped it).
  * Synchronizes the device. With clear != 0 the word is reset to 0. Returns
  * QG_ERR_DEVICE_TIMEOUT when the word was nonzero, QG_ERR_BAD_INDEX for 0x6xx.
  */

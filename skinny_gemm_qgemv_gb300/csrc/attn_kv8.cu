@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
 
   const int G = a.Hq / a.Hkv;
   const AttnBatch batch = attn_scan<ROWS, Cut, 32 * NW>(a, first, cost, cus, ctxs, scan_part);
-  const AttnShare mine_of = attn_share<Cut>(batch);
+  const AttnShare mine_of = attn_share<Cut>(batch, a.err);
   const int c0 = mine_of.c0, c1 = mine_of.c1, n = c1 - c0;
   if (n == 0) return;
 

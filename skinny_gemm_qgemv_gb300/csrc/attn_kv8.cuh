@@ -133,7 +133,8 @@ __device__ __forceinline__ int attn_cost_of(const AttnBatch& b, int step) {
 
 // The batch's tables in shared memory, formed by all NT threads of a CTA (`part`
 // has NT / 32 entries); returns the batch. The host has checked that the sums
-// stay below 2^31.
+// stay below 2^31 for query tokens that ascend within T; if they do not, the
+// batch's cost is -1.
 template <int ROWS, class CUT, int NT>
 __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, int* cost, int* cus, int* ctxs,
                                                int2* part) {
@@ -142,9 +143,11 @@ __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, in
   const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
   const int most = a.max_blocks * a.bs;
   int2 mine = make_int2(0, 0);
+  bool bad = false;
 #pragma unroll 1
   for (int r = r0; r < r1; ++r) {
-    const int q0 = min(max(a.cu_q[r], 0), a.T), q1 = min(max(a.cu_q[r + 1], 0), a.T);
+    const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1];
+    bad |= q0 < 0 || q0 > q1 || q1 > a.T;
     int ctx = max(0, a.ctx_lens[r]);
     if (ctx > most) {
       ctx = most;
@@ -155,7 +158,7 @@ __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, in
     if (r == a.R - 1) cus[a.R] = q1;
     first[r] = mine.x;
     cost[r] = mine.y;
-    const int items = a.Hkv * ((max(0, q1 - q0) * G + ROWS - 1) / ROWS), steps = attn_steps<CUT::kTok>(ctx);
+    const int items = a.Hkv * (((q1 - q0) * G + ROWS - 1) / ROWS), steps = attn_steps<CUT::kTok>(ctx);
     mine.x += items * steps;
     mine.y += items * (steps + CUT::kCost);
   }
@@ -165,18 +168,21 @@ __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, in
     const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
     if (lane >= o) inc.x += x, inc.y += y;
   }
-  if (lane == 31) part[warp] = inc;
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 31) part[warp] = make_int2(inc.x, bad ? -1 : inc.y);
   __syncthreads();
   int2 before = make_int2(inc.x - mine.x, inc.y - mine.y), total = make_int2(0, 0);
+  int marks = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     const int2 x = part[w];
     if (w < warp) before.x += x.x, before.y += x.y;
     total.x += x.x, total.y += x.y;
+    marks |= x.y;
   }
 #pragma unroll 1
   for (int r = r0; r < r1; ++r) first[r] += before.x, cost[r] += before.y;
-  if (threadIdx.x == 0) first[a.R] = total.x, cost[a.R] = total.y;
+  if (threadIdx.x == 0) first[a.R] = total.x, cost[a.R] = marks < 0 ? -1 : total.y;
   __syncthreads();
   return {first, cost, ctxs, cus, a.R, G};
 }
@@ -186,10 +192,13 @@ struct AttnShare {
   int c0, c1, share, more;
 };
 template <class CUT>
-__device__ __forceinline__ AttnShare attn_share(const AttnBatch& b) {
+__device__ __forceinline__ AttnShare attn_share(const AttnBatch& b, uint32_t* err) {
   const int W = b.cost[b.R], A = min((int)gridDim.x, W);  // the first W % A CTAs take one place more than the others
   AttnShare s = {0, 0, 0, 0};
-  if ((int)blockIdx.x >= A) return s;
+  if ((int)blockIdx.x >= A) {
+    if (W < 0 && blockIdx.x == 0 && threadIdx.x == 0) report_error(err, kErrKvQueries);
+    return s;
+  }
   s.share = W / A, s.more = W % A;
   // both ends side by side, by the even and the odd lanes
   const int i = blockIdx.x + (threadIdx.x & 1), step = attn_step_at<CUT>(b, i * s.share + min(i, s.more));

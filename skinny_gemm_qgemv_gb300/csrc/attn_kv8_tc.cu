@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_before();
   const AttnBatch batch = attn_scan<ROWS, TcCut, kTcThreads>(a, first, cost, cus, ctxs, scan_part);  // has barriers
   tc_after();
-  const AttnShare share = attn_share<TcCut>(batch);
+  const AttnShare share = attn_share<TcCut>(batch, a.err);
   const uint32_t tbase = tmem_base;
   const uint32_t tlane = tbase + ((uint32_t)(quad * 32) << 16);  // the lanes that this warp may touch
 

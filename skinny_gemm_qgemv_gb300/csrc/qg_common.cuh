@@ -35,6 +35,7 @@ enum DeviceError : uint32_t {
   kErrKvSlot = 0x601,    // 0x6xx: an index outside the paged cache, skipped
   kErrKvBlock = 0x602,
   kErrKvLength = 0x603,
+  kErrKvQueries = 0x604,
   kErrAttnWait = 0x701,
 };
 

@@ -1121,3 +1121,18 @@ def test_attention_scores_past_the_steps_of_fp32(q, D):
     want = torch.from_numpy(c["vc"][b, :, tok % 16].view(np.int8).astype(np.float32)).repeat_interleave(4, 0)
     out = run_attn(q, c, softmax_scale=scale)[0].float()
     assert bool(((out - want).abs() <= want.abs() * 2.0 ** -8 + 2.0 ** -16 * 256).all())
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("cu", [[0, 12, 9, 20], [0, 12, 16, 24], [-1, 12, 16, 20], [3, 2, 1, 0]])
+def test_attention_query_bounds_that_do_not_ascend(q, cu, wide):
+    """Reported, and nothing is written."""
+    c = attn_case(np.random.default_rng(99), [8, 8, 4], [300, 40, 20], 8, 2, 128, 16, "i8", False)
+    c["x"] = c["x"][:20]
+    if wide:
+        c = widen(c)
+    c["cu"] = np.array(cu)
+    assert bool((run_attn(q, c) == 7.0).all())
+    assert q.device_error(clear=True) == 0x604
+    c["cu"] = np.array([0, 8, 8, 20])
+    check_attn(run_attn(q, c), c)
