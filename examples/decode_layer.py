@@ -63,10 +63,11 @@ class PagedCache:
         self.block_size = block_size
 
     def resize(self, new_lens, max_tokens):
-        """Grow or shrink the requests to new_lens: (cu_new, slots, positions, info) of the new tokens."""
+        """Grow or shrink the requests to new_lens: (cu_new, slots, positions, info) of the new tokens. A plan that is
+        refused (info[3] is not 0: too few blocks, say) changes nothing, so the lengths stay as they were too."""
         out = lib.kv8_block_plan(self.lens, new_lens, self.table, self.free, self.count, self.block_size, max_tokens,
                                  free_count_out=self.count)
-        self.lens = new_lens
+        self.lens = torch.where(out[4][3:] == 0, new_lens, self.lens)
         return out[1:]
 
 
@@ -86,7 +87,8 @@ class DecodeLayer:
 
     def step(self, x, residual, cache, new_lens, tree=None):
         """x, residual fp32 [M][hidden]: the last layer's output and the residual stream (updated in place). Returns
-        this layer's output and everything in between by name."""
+        this layer's output and everything in between by name. Where the plan was refused (t["info"][3] is not 0) nothing
+        was stored and no row attended: the output and the residual stream of that step are to be dropped."""
         M = x.shape[0]
         t = dict(x=x, old_residual=residual.clone())
         t["h1"], _ = lib.rmsnorm_residual(x, self.norm1, residual=residual, residual_out=residual)
@@ -131,7 +133,9 @@ def main():
 
     # prompts of 5, 7, 9 and 11 tokens as one step of 32 rows
     y, t = layer.step(*rows(32), cache, lens(5, 7, 9, 11))
-    print("prompts:", t["info"].tolist(), "output", tuple(y.shape))
+    info = t["info"].tolist()
+    assert info[3] == 0, "the plan was refused"           # read once here; a server looks at it where it samples
+    print("prompts:", info, "output", tuple(y.shape))
     # decode: one token of every request
     n = [5, 7, 9, 11]
     for _ in range(3):

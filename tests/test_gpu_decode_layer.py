@@ -104,3 +104,27 @@ def test_decode_layer_steps(ex):
 def test_example_runs(ex, capsys):
     ex.main()
     assert "free blocks" in capsys.readouterr().out
+
+
+def test_a_refused_plan_leaves_the_cache_as_it_was(ex):
+    """More tokens than the pool has blocks for: lengths, table and stack stay, and the next steps are sound."""
+    layer = ex.DecodeLayer(512, heads=4, kv_heads=2, head_dim=64, intermediate=512, seed=4)
+    cache = ex.PagedCache(2, num_blocks=3, max_blocks=8, Hkv=2, D=64)
+    lens = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def step(*new):
+        M = max(1, sum(new) - int(cache.lens.sum()))
+        return layer.step(torch.randn(M, 512, device="cuda"), torch.randn(M, 512, device="cuda"), cache, lens(*new))
+
+    _, t = step(14, 10)
+    assert t["info"].tolist() == [24, 2, 0, 0] and cache.lens.tolist() == [14, 10]
+    before = cache.table.clone(), cache.free.clone(), cache.count.clone(), cache.k.clone(), cache.scales.clone()
+    _, t = step(20, 20)
+    assert t["info"].tolist() == [0, 0, 0, 1] and cache.lens.tolist() == [14, 10]
+    for a, b in zip(before, (cache.table, cache.free, cache.count, cache.k, cache.scales)):
+        assert torch.equal(a, b)
+    y, t = step(17, 11)
+    assert t["info"].tolist() == [4, 1, 0, 0] and bool(torch.isfinite(y).all())
+    *_, info = cache.resize(lens(0, 0), 1)
+    assert info.tolist() == [0, 0, 3, 0]
+    assert cache.count.item() == 3 and sorted(cache.free.tolist()) == [0, 1, 2]
