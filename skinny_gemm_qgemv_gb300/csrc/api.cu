@@ -464,7 +464,10 @@ const char* qg_last_cuda_error_string(void) { return cudaGetErrorString(t_last_c
 
 // The decode step's operators always launch with programmatic dependent launch:
 // their kernels touch nothing in memory before the dependency wait, so only the
-// launch itself overlaps the previous kernel (qg_set_pdl has no say in it).
+// launch itself overlaps the previous kernel (qg_set_pdl has no say in it). They
+// begin while the kernel before them still writes, so what that one may write is
+// read by plain loads: the read-only path (ld.global.nc) is for memory that no
+// one writes from a kernel's beginning on.
 
 // The paged 8-bit cache: sizes shared by its entry points
 static qg_status check_kv8(int Hkv, int D, int block_size, int num_blocks, int format) {

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
       const AttnPlace at = attn_locate<ROWS, Cut>(batch, step);
       const int tok = ((at.s * NW + warp) * UPS + lane % UPS) * kUnit;
       if (tok < ctxs[at.r]) {
-        n_blk = __ldg(a.table + (size_t)at.r * a.max_blocks + tok / a.bs);
+        n_blk = a.table[(size_t)at.r * a.max_blocks + tok / a.bs];
         n_head = at.h;
         n_row = tok % a.bs;
         if (n_blk < 0 || n_blk >= a.num_blocks) {
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, NT, FMT>::kWarps, 1)
   };
   auto look_scale = [&]() {
     if (n_blk >= 0)
-      n_scale = __ldg(reinterpret_cast<const float2*>(a.scales) + (size_t)n_blk * a.Hkv + n_head);
+      n_scale = reinterpret_cast<const float2*>(a.scales)[(size_t)n_blk * a.Hkv + n_head];
   };
   auto next_batch = [&]() {
     page = n_blk >= 0 ? n_blk * a.Hkv + n_head : -1;

@@ -393,13 +393,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int tok = sg.tok0 + i * TOK + lane * kUnit;
         int blk = -1;
         if (i < sg.n && lane < TOK / kUnit && tok < sg.ctx) {
-          blk = __ldg(a.table + (size_t)sg.item.r * a.max_blocks + tok / a.bs);
+          blk = a.table[(size_t)sg.item.r * a.max_blocks + tok / a.bs];
           if (blk < 0) blk = a.num_blocks;  // bad
         }
         return blk;
       };
       auto scales_of = [&](int blk) {
-        return blk >= 0 && blk < a.num_blocks ? __ldg(scales + (size_t)blk * a.Hkv + sg.item.h) : make_float2(0.f, -1.f);
+        return blk >= 0 && blk < a.num_blocks ? scales[(size_t)blk * a.Hkv + sg.item.h] : make_float2(0.f, -1.f);
       };
       int blk = look(0), next = look(1);
       float2 sc = scales_of(blk);

@@ -31,7 +31,6 @@
 namespace qg {
 namespace {
 
-
 constexpr int kPlanThreads = 512;
 
 // take and rel are bounded by R * max_blocks < 2^31, the tokens only by their check
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, KEEP == 1 ? 2048 / THREADS : KEEP == 
     // the first tokens of runs in this CTA's window (slots of a block ascend by one)
     const int t = blockIdx.x * a.window + tid;
     if (tid < a.window && t < a.T) {
-      const int slot = __ldg(a.slot_map + t), prev = t > 0 ? __ldg(a.slot_map + t - 1) : -1;
+      const int slot = a.slot_map[t], prev = t > 0 ? a.slot_map[t - 1] : -1;
       if (slot >= a.num_blocks * a.bs)
         report_error(a.err, kErrKvSlot);
       else if (slot >= 0 && (slot % a.bs == 0 || prev != slot - 1))
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, KEEP == 1 ? 2048 / THREADS : KEEP == 
   }
   __syncthreads();
   for (int k = 0; k < leads; ++k) {
-    const int t0 = lead[k], slot = __ldg(a.slot_map + t0), f = slot % a.bs, blk = slot / a.bs;
+    const int t0 = lead[k], slot = a.slot_map[t0], f = slot % a.bs, blk = slot / a.bs;
     // The run's length: up to the block's end or the first slot that does not follow. The values it can have are
     // loaded before it is known.
     const int most = min(a.bs - f, a.T - t0);
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(THREADS, KEEP == 1 ? 2048 / THREADS : KEEP == 
     }
     int n = most;
     for (int i = tid; i < most; i += THREADS)
-      if (__ldg(a.slot_map + t0 + i) != slot + i) n = min(n, i);
+      if (a.slot_map[t0 + i] != slot + i) n = min(n, i);
     n = __reduce_min_sync(0xffffffffu, n);
     if ((tid & 31) == 0) part_n[tid >> 5] = n;
     float* sp = a.scales + 2 * ((size_t)blk * a.Hkv + head) + which;
@@ -348,19 +347,19 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(ReadArgs a) {
   pdl_launch_dependents();
   const int which = blockIdx.z, head = blockIdx.y;
   const int per = a.bs * a.D / 8;
-  const int id = __ldg(a.ids + blockIdx.x);
+  const int id = a.ids[blockIdx.x];
   const bool ok = id >= 0 && id < a.num_blocks;
   if (!ok && threadIdx.x == 0) report_error(a.err, kErrKvBlock);
   const size_t page = ((size_t)(ok ? id : 0) * a.Hkv + head);
   const size_t dst = ((size_t)blockIdx.x * a.Hkv + head);
-  const float s = ok ? __ldg(a.scales + 2 * page + which) : 0.f;
+  const float s = ok ? a.scales[2 * page + which] : 0.f;
   if (threadIdx.x == 0) a.scales_out[2 * dst + which] = s;
   const uint2* src = reinterpret_cast<const uint2*>(which ? a.v_cache : a.k_cache) + page * per;
   uint4* out = reinterpret_cast<uint4*>(which ? a.v : a.k) + dst * per;
   for (int i = threadIdx.x; i < per; i += blockDim.x) {
     uint4 o = make_uint4(0u, 0u, 0u, 0u);
     if (ok) {
-      const uint2 c = __ldg(src + i);
+      const uint2 c = src[i];
       float v[8];
       kv8_decode4<FMT>(c.x, v[0], v[1], v[2], v[3]);
       kv8_decode4<FMT>(c.y, v[4], v[5], v[6], v[7]);

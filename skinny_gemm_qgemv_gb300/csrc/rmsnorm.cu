@@ -71,7 +71,7 @@ __device__ __forceinline__ float cta_reduce(float v, float* part) {
 // stored (residual_out may be residual, so the compiler cannot move a load over
 // a store by itself).
 template <int C, int THREADS, bool I8, bool XF, bool RF>
-__global__ void __launch_bounds__(THREADS) rmsnorm_kernel(const void* __restrict__ x, const void* res,
+__global__ void __launch_bounds__(THREADS) rmsnorm_kernel(const void* x, const void* res,
                                                           const void* __restrict__ w, int w_f32, float eps,
                                                           const uint32_t* __restrict__ sign_bits, int K, void* res_out,
                                                           void* __restrict__ out, float* __restrict__ scale) {
