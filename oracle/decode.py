@@ -118,11 +118,10 @@ def append(x, slots, cache, scales, fmt, num_blocks, bs):
 
 
 def attention(q, k_cache, v_cache, scales, table, ctx_lens, cu_q, fmt, softmax_scale, tree=None):
-    """float64 attention of q [T][Hq][D] over uint8-pattern caches. Returns (out
-    [T][Hq][D], bound [T][Hq][D]): bound = sum p |v| with, per row, the largest
-    sum |q k| of a seen token in the second array's companion below.
-    The third value is [T][Hq]: max over seen tokens of sum |q_d k_d| *
-    softmax_scale; the fourth the number of seen tokens; the fifth max |v|."""
+    """float64 attention of q [T][Hq][D] over uint8-pattern caches. Returns
+    five arrays: out [T][Hq][D]; sum p |v| [T][Hq][D]; and [T][Hq] each: the
+    largest sum |q_d k_d| * softmax_scale of a seen token, the number of seen
+    tokens, the largest |v|."""
     T, Hq, D = q.shape
     nb, Hkv, bs, _ = k_cache.shape
     G = Hq // Hkv

@@ -1136,3 +1136,22 @@ def test_attention_query_bounds_that_do_not_ascend(q, cu, wide):
     assert q.device_error(clear=True) == 0x604
     c["cu"] = np.array([0, 8, 8, 20])
     check_attn(run_attn(q, c), c)
+
+
+# --------------------------------------------------------------------------
+# norm of many rows: several steps a thread, and rows of more than 8192 elements
+# --------------------------------------------------------------------------
+
+NORM_MANY = [(700, 7168, "bf16", "bf16", "bf16"), (611, 8192, "f32", "f32", "f32"), (640, 4128, "f32", "bf16", "bf16"),
+             (609, 4096, "bf16", "f32", "f32"), (615, 5152, "bf16", None, "bf16"), (612, 12288, "f32", "f32", "bf16")]
+
+
+@pytest.mark.parametrize("M,K,xd,rd,wd", NORM_MANY)
+def test_norm_bf16_of_many_rows(q, M, K, xd, rd, wd):
+    test_norm_bf16(q, M, K, xd, rd, wd)
+
+
+@pytest.mark.parametrize("had", [False, True])
+@pytest.mark.parametrize("M,K,xd,rd,wd", NORM_MANY)
+def test_norm_i8_of_many_rows(q, M, K, xd, rd, wd, had):
+    test_norm_i8(q, M, K, xd, rd, wd, had)
