@@ -620,7 +620,7 @@ QG_API size_t qg_kv8_plan_workspace_size(void);
  *                the cache is skipped and reported (qg_device_error). The
  *                slots of one block are consecutive in T and ascending by 1
  *                (as kv8_block_plan gives them): a run.
- *   T >= 1, 1 <= Hkv <= 1024, D a multiple of 16 in 16..256.
+ *   1 <= T <= 2^30, 1 <= Hkv <= 1024, D a multiple of 16 in 16..256.
  * Per run (first slot f of its block), head and cache, in fp32 with IEEE
  * rounding, qmax = 127 (int8) or 448 (e4m3):
  *   s0 = f > 0 ? scale : 0;  s = max(s0, max|x| / qmax)  becomes the scale;

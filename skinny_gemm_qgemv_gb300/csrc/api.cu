@@ -509,7 +509,7 @@ qg_status kv8_append(const void* k, const void* v, int dtype, int64_t k_stride, 
                      const int32_t* slot_map, int T, int Hkv, int D, int block_size, int num_blocks, int format,
                      void* k_cache, void* v_cache, float* scales, void* stream) {
   if (!k || !v || !slot_map || !k_cache || !v_cache || !scales) return QG_ERR_INVALID_ARG;
-  if (T < 1 || (dtype != QG_DT_BF16 && dtype != QG_DT_F32)) return QG_ERR_INVALID_ARG;
+  if (T < 1 || T > (1 << 30) || (dtype != QG_DT_BF16 && dtype != QG_DT_F32)) return QG_ERR_INVALID_ARG;
   qg_status st = check_kv8(Hkv, D, block_size, num_blocks, format);
   if (st != QG_OK) return st;
   if (k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D || k_stride % 8 != 0 || v_stride % 8 != 0)

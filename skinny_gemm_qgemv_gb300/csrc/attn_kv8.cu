@@ -752,7 +752,7 @@ cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream, bool pdl) {
 // the width a head of D elements is filled up to
 int attn_width(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // rows of an average request's item
-int attn_rows(const AttnArgs& a) { return (a.T + a.R - 1) / a.R * (a.Hq / a.Hkv); }
+int attn_rows(const AttnArgs& a) { return (int)(((long long)a.T + a.R - 1) / a.R) * (a.Hq / a.Hkv); }
 // The tcgen05 kernel for many rows of up to 128 elements. This file's kernel passes over the cache once per 16 rows, at
 // 5 ns per 128 tokens of a head (3 ns with heads of 64); that one takes 7 ns per 128 tokens and 64 rows, and about 3 us
 // more to begin, end and join. Measured, here and there: one request, 64 rows, 300 tokens 9.7 and 13.8 us, 2048 tokens

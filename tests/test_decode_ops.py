@@ -184,3 +184,8 @@ def test_attention_workspace_holds_the_widest_pieces(L):
     # without a device the query answers for one CTA; a device has more
     assert full >= 4096 + 2 * 64 * (128 * 4 + 8)
     assert L.qg_attn_kv8_workspace_size(8, 2, 256) >= 4096 + 2 * 16 * (256 * 4 + 8)
+
+
+def test_append_refuses_more_tokens_than_it_counts(L):
+    for T in ((1 << 30) + 1, 2 ** 31 - 1):
+        assert L.kv8_append(P(A), P(A), 0, 16, 16, P(A), T, 1, 16, 16, 8, 0, P(A), P(A), P(A), None) == 1
