@@ -19,7 +19,8 @@ the drafts of a speculative tree) goes through
 
 Weights are random; the point is how the calls fit together: all lengths,
 tables and slots stay on the GPU, and rejected drafts are given back by a plan
-with smaller lengths.
+with smaller lengths. (Accepted drafts that are not the first ones of their
+tree are appended again in their order after such a plan.)
 """
 from __future__ import annotations
 
@@ -141,7 +142,7 @@ def main():
     for _ in range(3):
         n = [a + 1 for a in n]
         y, t = layer.step(*rows(R), cache, lens(*n))
-    # speculative verification: six drafts of a tree for every request, two of them accepted
+    # speculative verification: six drafts of a tree for every request, its first two accepted (one below the other)
     parents = [-1, 0, 0, 1, 2, 4]
     words = tree_words(parents).repeat(R)
     y, t = layer.step(*rows(6 * R), cache, lens(*[a + 6 for a in n]), tree=words)

@@ -629,7 +629,12 @@ QG_API size_t qg_kv8_plan_workspace_size(void);
  *   f = 0 (a new block): the slots after the run are set to 0.
  *   s = 0 (all values 0) gives codes 0. Other slots keep their codes. So a
  *   block's scale only grows while it fills, and each growth rounds its earlier
- *   codes once more (by at most half a step of the new scale).
+ *   codes once more (by at most half a step of the new scale). Tokens given
+ *   back (a plan with smaller lengths) do not take a grown scale back: codes
+ *   rounded to a rejected draft's scale stay so until their block is begun
+ *   anew. An accepted path of a draft tree that is not its first tokens is
+ *   appended again: shrink to the tokens before the drafts, grow by the
+ *   accepted ones, append their keys and values in their order.
  * Results are exact functions of the inputs (no sums are formed).
  */
 QG_API qg_status kv8_append(const void *k, const void *v, int dtype, int64_t k_stride, int64_t v_stride,
@@ -678,9 +683,12 @@ QG_API qg_status kv8_read(const int32_t *block_ids, int B, int Hkv, int D, int b
  *                zero-filled before its first use: its counters are left at
  *                zero by every call, the rest is scratch. Calls that may
  *                overlap need separate workspaces.
- * Scores, maxima and sums are fp32, probabilities enter the value product as
- * fp16 (relative rounding 2^-11); the split of a context over the GPU, and so
- * the order of the sums, depends on the shapes and lengths alone.
+ * Codes are multiplied exactly; scores, maxima and sums are fp32;
+ * probabilities enter the value product, times their block's value scale, as
+ * fp16: rounded by 2^-11 of themselves, or by 2^-25 of the row's largest where
+ * that is more. A row does not depend on what other rows of q hold, infinities
+ * and NaN included. The split of a context over the GPU, and so the order of
+ * the sums, depends on the shapes and lengths alone.
  * QG_ERR_UNSUPPORTED: more than 2^31 - 1 steps of 128 tokens, were every table
  * row full: about Hkv (T (Hq / Hkv) / 8 + 2 R) (max_blocks block_size / 128 + 10).
  */

@@ -11,6 +11,11 @@ Entry points (same names as the C ABI):
   SkinnyGroup qgemm_w4a16_skinny_group_*. The decode step around the products:
   kv8_block_plan, kv8_append, kv8_read, attn_kv8_paged (the paged 8-bit
   key/value cache), rmsnorm_residual, rmsnorm_residual_i8
+
+A call is enqueued on `stream`, torch's current one by default. With a stream
+given, the caller orders it after what made the inputs and keeps the inputs
+until it is through (or marks them with Tensor.record_stream), as for any work
+on a stream that is not their own.
 """
 from __future__ import annotations
 

@@ -19,10 +19,10 @@
 // through ldmatrix's byte transposition as A fragments of O^T = V^T P^T: nothing
 // is converted twice and nothing goes back to shared memory. Pieces of a context
 // cut by shares are added up by the CTA that brings the last one.
-// Measured (32 query heads, 8 key/value heads of 128, int8): 131071 tokens 50.1 us,
-// 268 MB at 5.4 TB/s; the streaming itself runs at 6.7 TB/s, and 10 us go to the
+// Measured (32 query heads, 8 key/value heads of 128, int8): 131071 tokens 50.5 us,
+// 268 MB at 5.3 TB/s; the streaming itself runs at 6.7 TB/s, and 10 us go to the
 // launch, the first copies and the joining of pieces. 32 requests of 1..8192
-// tokens: 52.8 us, 270 MB. One token over 37 tokens: 6.2 us, all latency.
+// tokens (e4m3): 52.8 us, 270 MB. One token over 37 tokens: 6.4 us, all latency.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -36,8 +36,8 @@ namespace qg {
 namespace {
 
 // An item costs about as much as 2 steps to begin and end; one of up to 3 steps is not cut: joining its pieces takes
-// longer than its steps on one CTA. With (2, 3), (3, 6) and (1, 3): 32 ragged requests of four drafts 63.2, 66.6 and
-// 73.4 us, of one token 52.8, 54.2 and 56.9; one of 1024 tokens 8.9, 10.3 and 8.9; 16 of 1..1024 tokens 11.3, 11.0, 15.3.
+// longer than its steps on one CTA. With (2, 3), (3, 6) and (1, 3): 32 ragged requests of four drafts 65.1, 68.3 and
+// 73.7 us, of one token 52.8, 54.2 and 56.6; one of 1024 tokens 8.9, 10.3 and 8.8; 16 of 1..1024 tokens 11.3, 11.1, 15.5.
 constexpr int kItemCost = 2;
 constexpr int kWholeSteps = 3;
 
@@ -717,8 +717,8 @@ AttnLaunch attn_smem(int R) {
   const size_t per = (size_t)S::kWarps * (S::kStage + 16 * S::kUps + 8);
   AttnLaunch l;
   // Two steps ahead (128 KB an SM) are enough to stream at HBM's rate; more only queue up there, and CTAs end further
-  // apart (131071 tokens 52.0 us with three, 50.7 with two; e4m3 51.9 and 49.6; heads of 256, 65536 tokens 55.0 and 52.8;
-  // 32 ragged requests 55.5 and 55.0; only with e4m3 in blocks of 16 the other way, 53.4 and 54.0).
+  // apart (131071 tokens 51.7 us with three, 50.6 with two; e4m3 51.3 and 49.8; heads of 256, 65536 tokens 54.7 and 53.8;
+  // 32 ragged requests 57.8 and 57.0; only with e4m3 in blocks of 16 the other way, 52.3 and 52.8).
   l.stages = (int)std::min<size_t>(2, budget / per);
   l.ring = (uint32_t)((size_t)l.stages * S::kWarps * S::kStage);
   l.smem = fixed + per * l.stages;
@@ -755,10 +755,11 @@ int attn_width(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 int attn_rows(const AttnArgs& a) { return (int)(((long long)a.T + a.R - 1) / a.R) * (a.Hq / a.Hkv); }
 // The tcgen05 kernel for many rows of up to 128 elements. This file's kernel passes over the cache once per 16 rows, at
 // 5 ns per 128 tokens of a head (3 ns with heads of 64); that one takes 7 ns per 128 tokens and 64 rows, and about 3 us
-// more to begin, end and join. Measured, here and there: one request, 64 rows, 300 tokens 9.7 and 13.8 us, 2048 tokens
-// 15.8 and 15.2, 8192 tokens 24.2 and 17.6, 32784 tokens 56.0 and 30.4; 32 rows, 8192 tokens 17.3 and 17.2, 32768 tokens
-// 33.5 and 29.4; heads of 64, 64 rows, 65536 tokens 42.3 and 32.7; six requests of 40 rows over 5000 tokens 14.3 and
-// 16.2. The lengths are known to the GPU alone, so their bound decides.
+// more to begin, end and join. Measured, here and there: one request, 64 rows, 300 tokens 9.5 and 14.0 us, 2048 tokens
+// 14.5 and 15.0, 8192 tokens 23.9 and 18.1, 32784 tokens 57.2 and 30.8; 32 rows, 8192 tokens 16.7 and 16.9, 32768 tokens
+// 34.3 and 28.2; heads of 64, 64 rows, 65536 tokens 41.4 and 30.7; six requests of 40 rows over 5000 tokens 11.8 and
+// 15.8. The lengths are known to the GPU alone, so their bound decides: short contexts of a table made for long ones
+// take the longer time.
 bool attn_tc_ok(const AttnArgs& a) {
   const int width = attn_width(a.D);
   if (width > kTcHead) return false;

@@ -22,8 +22,8 @@
 // buffers of every kind; S of step i + 1 is issued before O of step i. The batch
 // is cut into shares as in attn_kv8.cu; a second kernel joins a context's pieces.
 //
-// Measured: 64 rows of 8 heads over 32784 int8 tokens 30.4 us (67 MB at 2.2 TB/s, 8.6
-// GFLOP), 65568 tokens 47 us. A step takes 1.25 us against 0.6 us of copies (a 152nd of
+// Measured: 64 rows of 8 heads over 32784 int8 tokens 30.8 us (67 MB at 2.2 TB/s, 8.6
+// GFLOP), 65568 tokens 48 us. A step takes 1.26 us against 0.6 us of copies (a 152nd of
 // HBM) and 0.3 us of MMAs: it is bound by the chain from one S to its P in the softmax
 // warps and by what the MMA warp waits for and issues, all at about 2300 cycles; no single
 // part taken out makes it more than 8 % faster. 6 us go to the first step, 5 to the last

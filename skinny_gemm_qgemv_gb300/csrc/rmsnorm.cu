@@ -10,7 +10,7 @@
 // algorithmic one. A 32-block of the transform is four neighbouring lanes: the
 // butterflies of span 1, 2, 4 stay in a thread, 8 and 16 are two shuffles.
 // Many rows are bound by HBM (4096 rows of 7168, bf16 to int8 codes: 205 MB in
-// 35 us, 5.9 TB/s), few rows by the launch and one trip through load, two
+// 37 us, 5.6 TB/s; to bf16 235 MB in 35 us), few rows by the launch and one trip through load, two
 // reductions and store (one row of 4096: 3.7 us).
 #include <cuda_runtime.h>
 
@@ -211,7 +211,7 @@ cudaError_t launch(const NormArgs& a, cudaStream_t stream, bool pdl) {
   auto threads = [&](int c) { return ((n8 + c - 1) / c + 31) / 32 * 32; };
   // Few rows: as many threads as a row has steps, for latency. Many rows (four CTAs an SM and more) of up to 8192
   // elements: several steps per thread, so that more bytes are on the way per SM (4096 rows of 7168 bf16, int8 codes:
-  // 57 -> 35 us).
+  // 57 -> 37 us).
   if (n8 <= 1024 && a.M >= 4 * device_sm_count())
     return n8 <= 512 ? launch_types<2, 256, I8>(a, threads(2), stream, pdl)
                      : launch_types<4, 256, I8>(a, threads(4), stream, pdl);
