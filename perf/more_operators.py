@@ -80,8 +80,8 @@ def draw(rng):
         plain = (1 << 28) // ((n + alone) * q * Hq)              # the plain form's scores
         ctx = _log(rng, q, max(q, min(1024, plain, (1 << 25) // ((n + alone) * Hkv * D))))
         return dict(op=op, groups=",".join(map(str, groups)), alone=alone, q=q,
-                    prefix=_log(rng, 16, max(17, min(top, plain))), ctx=ctx, tree=q > 1 and rng.random() < 0.5, Hq=Hq, Hkv=Hkv, D=D, bs=rng.choice([16, 32, 48, 64, 128]),
-                    fmt=rng.choice(["i8", "e4m3"]))
+                    prefix=_log(rng, 16, max(17, min(top, plain))), ctx=ctx, tree=q > 1 and rng.random() < 0.5, Hq=Hq,
+                    Hkv=Hkv, D=D, bs=rng.choice([16, 32, 48, 64, 128]), fmt=rng.choice(["i8", "e4m3"]))
     if op == "rope":
         D, Hkv = rng.choice([64, 80, 96, 128, 128, 256]), rng.choice([1, 2, 4, 8])
         Hq = Hkv * rng.choice([1, 2, 4, 5, 8])
