@@ -728,6 +728,45 @@ QG_API qg_status rmsnorm_residual_i8(const void *x, int x_dtype, const void *res
                                      int K, void *residual_out, int8_t *q, float *scale, void *stream);
 
 /*
+ * qk_norm_rope -- the norms of queries and keys for each head and the position
+ * rotation (rotary embedding), in one pass: what stands between the q, k
+ * projections and kv8_append / attn_kv8_paged.
+ *
+ *   q, k         [T][Hq][D], [T][Hkv][D], bf16 or fp32 (x_dtype), token t at
+ *                element t * q_stride (k_stride) (>= H * D, a multiple of 8):
+ *                also slices of a fused q/k/v row.
+ *   positions    int32 [axes][T]: a token's position on each axis, 1 <= axes <=
+ *                4 (a text's position; time, height and width of an image's or
+ *                a video's patch). A token whose position on axis 0 is negative
+ *                (the padding of kv8_block_plan) is left out: its rows of the
+ *                outputs stay as they were.
+ *   inv_freq     double [rotary_dim / 2]: radians that pair i turns per
+ *                position (base^(-2i / rotary_dim), or a scaled form of it).
+ *   pair_axis    HOST array, uint8 [rotary_dim / 2]: the axis, below axes, that
+ *                pair i turns by (in sections, alternating, any order); read
+ *                before the call returns. NULL: axis 0 (axes = 1 only).
+ *   rotary_dim   a multiple of 8, 8..D: the first rotary_dim elements of a head
+ *                turn, the others are only normed.
+ *   interleaved  0: pair i is (i, i + rotary_dim / 2); otherwise (2i, 2i + 1).
+ *   q_weight, k_weight  [D], bf16 or fp32 (w_dtype); NULL: no norm of the
+ *                queries (keys).
+ *   y = (x * rsqrt(mean(x^2) + eps)) * weight over a head's D elements, then a
+ *   pair (u, v) by a = position * inv_freq: (u cos a - v sin a, v cos a +
+ *   u sin a), all in fp32; the angle is reduced in 64 bits (off by less than
+ *   2^-52 of itself before that).
+ *   q_out_bf16   bf16 [T][Hq][D], k_out [T][Hkv][D], bf16 or fp32 (k_out_dtype)
+ *                (outputs), rounded to nearest even. fp32 keys go into
+ *                kv8_append without a rounding on the way.
+ *   1 <= T <= 2^30, Hq and Hkv 1..1024, D a multiple of 16 in 16..256, eps >= 0.
+ * One launch; capturable in a CUDA graph.
+ */
+QG_API qg_status qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int x_dtype,
+                              const int32_t *positions, int axes, const double *inv_freq, int rotary_dim,
+                              const uint8_t *pair_axis, int interleaved, const void *q_weight,
+                              const void *k_weight, int w_dtype, float eps, int T, int Hq, int Hkv, int D,
+                              uint16_t *q_out_bf16, void *k_out, int k_out_dtype, void *stream);
+
+/*
  * qg_workspace_size -- the single workspace query of the boundary: device
  * bytes the operation `op` needs for the given shape, group size 64 where
  * the operation has one (M, N, K for the W4A16 and W8A8 products; T, E,

@@ -10,7 +10,7 @@ Entry points (same names as the C ABI):
   hadamard32_quant_i8, gemm_w8a8_i32; GemvGroup wraps qgemv_w4a16_group_* and
   SkinnyGroup qgemm_w4a16_skinny_group_*. The decode step around the products:
   kv8_block_plan, kv8_append, kv8_read, attn_kv8_paged (the paged 8-bit
-  key/value cache), rmsnorm_residual, rmsnorm_residual_i8
+  key/value cache), rmsnorm_residual, rmsnorm_residual_i8, qk_norm_rope
 
 A call is enqueued on `stream`, torch's current one by default. With a stream
 given, the caller orders it after what made the inputs and keeps the inputs
@@ -46,6 +46,7 @@ EXPORTS = [
     "gemm_w8a8_hadamard", "qg_w8a8_hadamard_workspace_size", "qg_workspace_size",
     "kv8_block_plan", "qg_kv8_plan_workspace_size", "kv8_append", "kv8_read", "attn_kv8_paged",
     "qg_attn_kv8_workspace_size", "rmsnorm_residual", "rmsnorm_residual_i8",
+    "qk_norm_rope",
 ]
 
 (OP_GEMV_W4A16, OP_SKINNY_W4A16, OP_MOE_MXFP4, OP_HADAMARD_I8, OP_W8A8_I32, OP_W8A8_HADAMARD, OP_KV8_PLAN,
@@ -177,6 +178,8 @@ def lib() -> ctypes.CDLL:
         L.rmsnorm_residual.argtypes = [P, I, P, I, P, I, F, I, I, P, P, P]
         L.rmsnorm_residual_i8.restype = I
         L.rmsnorm_residual_i8.argtypes = [P, I, P, I, P, I, F, P, I, I, P, P, P, P]
+        L.qk_norm_rope.restype = I
+        L.qk_norm_rope.argtypes = [P, I64, P, I64, I, P, I, P, I, P, I, P, P, I, F, I, I, I, I, P, P, I, P]
         _lib = L
     return _lib
 
@@ -605,3 +608,19 @@ def rmsnorm_residual_i8(x, weight, residual=None, sign_bits=None, eps=1e-6, resi
     the randomized Hadamard transform when sign_bits (int32 [K/32]) are given:
     returns (q int8 [M][K], scale fp32 [M], h)."""
     return (_bind or _binding()).norm_i8(x, weight, residual, sign_bits, eps, residual_out, q, scale, stream)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, pair_axis=None,
+                 q_out=None, k_out=None, stream=None):
+    """Per-head RMS norms of q [T][Hq][D] and k [T][Hkv][D] (bf16 or fp32, tokens
+    dense, any token stride; no norm without a weight [D]) and the rotation of
+    their pairs by position * inv_freq (float64 [pairs]; the first 2 * pairs
+    elements of a head turn). positions int32 [T] or [axes][T]; with several axes
+    pair_axis (bytes or whole numbers, one a pair) says which axis a pair turns
+    by. interleaved: pairs (2i, 2i + 1) instead of (i, i + pairs). Tokens whose
+    (first) position is negative are left out. Returns (q bf16, k in its own type,
+    or k_out's: bf16 or fp32)."""
+    if pair_axis is not None and not isinstance(pair_axis, bytes):
+        pair_axis = bytes(pair_axis)
+    return (_bind or _binding()).qk_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, pair_axis,
+                                         q_out, k_out, stream)

@@ -607,6 +607,33 @@ qg_status rmsnorm_residual_i8(const void* x, int x_dtype, const void* residual, 
   return from_cuda(qg::launch_rmsnorm(a, static_cast<cudaStream_t>(stream), true));
 }
 
+qg_status qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int x_dtype,
+                       const int32_t* positions, int axes, const double* inv_freq, int rotary_dim,
+                       const uint8_t* pair_axis, int interleaved, const void* q_weight, const void* k_weight,
+                       int w_dtype, float eps, int T, int Hq, int Hkv, int D, uint16_t* q_out_bf16, void* k_out,
+                       int k_out_dtype, void* stream) {
+  if (!q || !k || !positions || !inv_freq || !q_out_bf16 || !k_out) return QG_ERR_INVALID_ARG;
+  for (int dt : {x_dtype, w_dtype, k_out_dtype})
+    if (dt != QG_DT_BF16 && dt != QG_DT_F32) return QG_ERR_INVALID_ARG;
+  if (T < 1 || T > (1 << 30) || Hq < 1 || Hq > 1024 || Hkv < 1 || Hkv > 1024) return QG_ERR_INVALID_ARG;
+  if (D < 16 || D > 256 || D % 16 != 0 || rotary_dim < 8 || rotary_dim > D || rotary_dim % 8 != 0)
+    return QG_ERR_INVALID_ARG;
+  if (axes < 1 || axes > 4 || (axes > 1 && !pair_axis) || !(eps >= 0.f)) return QG_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)Hq * D || q_stride % 8 != 0 || k_stride < (int64_t)Hkv * D || k_stride % 8 != 0)
+    return QG_ERR_INVALID_ARG;
+  qg::RopeArgs a = {q, k, x_dtype == QG_DT_F32, q_stride, k_stride, positions, inv_freq, {}, rotary_dim,
+                    interleaved != 0, q_weight, k_weight, w_dtype == QG_DT_F32, eps, T, Hq, Hkv, D, q_out_bf16, k_out,
+                    k_out_dtype == QG_DT_F32};
+  for (int i = 0; pair_axis && i < rotary_dim / 2; ++i) {
+    if (pair_axis[i] >= axes) return QG_ERR_INVALID_ARG;
+    a.axis_bits[i / 16] |= (uint32_t)pair_axis[i] << (2 * (i % 16));
+  }
+  if (!aligned16(q) || !aligned16(k) || !aligned16(positions) || !aligned16(inv_freq) || !aligned16(q_weight) ||
+      !aligned16(k_weight) || !aligned16(q_out_bf16) || !aligned16(k_out))
+    return QG_ERR_MISALIGNED;
+  return from_cuda(qg::launch_qk_rope(a, static_cast<cudaStream_t>(stream), true));
+}
+
 qg_status qg_device_error(uint32_t* code, int clear) {
   uint32_t* p = err_word();
   if (!p) return QG_ERR_CUDA;

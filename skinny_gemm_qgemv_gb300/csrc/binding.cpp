@@ -413,6 +413,53 @@ PyObject* norm_i8(PyObject* const* a) {
   return tuple(q, scale, n.res_out);
 }
 
+PyObject* qk_rope(PyObject* const* a) {
+  const at::Tensor &q = *tensor(a[0], "q"), &k = *tensor(a[1], "k"), &pos = *tensor(a[2], "positions"),
+                   &freq = *tensor(a[3], "inv_freq");
+  const at::Tensor *qw = tensor_or_null(a[4], "q_weight"), *kw = tensor_or_null(a[5], "k_weight");
+  const Call c("qk_norm_rope", q, a[11]);
+  const int64_t qs = token_stride(c, q, "q"), ks = token_stride(c, k, "k");
+  const int64_t T = q.size(0), Hq = q.size(1), Hkv = k.size(1), D = q.size(2);
+  if (k.size(0) != T || k.size(2) != D || k.scalar_type() != q.scalar_type())
+    refuse("q and k must have one type, T and D");
+  const int xd = dtype_of(q, "q");
+  const int64_t axes = pos.dim() == 2 ? pos.size(0) : 1;
+  if (pos.dim() == 2)
+    c.need(pos, at::kInt, {axes, T}, "positions");
+  else
+    c.need(pos, at::kInt, {T}, "positions");
+  c.need(freq, at::kDouble, {-1}, "inv_freq");
+  int wd = QG_DT_F32;
+  if (qw) c.need(*qw, qw->scalar_type(), {D}, "q_weight"), wd = dtype_of(*qw, "q_weight");
+  if (kw) c.need(*kw, kw->scalar_type(), {D}, "k_weight"), wd = dtype_of(*kw, "k_weight");
+  if (qw && kw && qw->scalar_type() != kw->scalar_type()) refuse("q_weight and k_weight must have one type");
+  const int inter = PyObject_IsTrue(a[7]);
+  if (inter < 0) throw Raised{};
+  const uint8_t* pair_axis = nullptr;
+  if (a[8] != Py_None) {
+    if (!PyBytes_Check(a[8]) || PyBytes_GET_SIZE(a[8]) != freq.numel())
+      refuse("pair_axis must have one entry for each of inv_freq");
+    pair_axis = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(a[8]));
+  } else if (axes > 1) {
+    refuse("positions on several axes need pair_axis");
+  }
+  at::Tensor qo = c.output(a[9], at::kBFloat16, {T, Hq, D}, "q_out"), ko;
+  if (a[10] != Py_None) {
+    ko = *tensor(a[10], "k_out");
+    dtype_of(ko, "k_out");
+    c.need(ko, ko.scalar_type(), {T, Hkv, D}, "k_out");
+  }
+  Outputs outs(c);
+  outs.add(qo, at::kBFloat16, {T, Hq, D});
+  outs.add(ko, k.scalar_type(), {T, Hkv, D});
+  outs.make();
+  c.done(qk_norm_rope(ptr<void>(q), qs, ptr<void>(k), ks, xd, ptr<int32_t>(pos), size32(axes, "axes"),
+                      ptr<double>(freq), size32(2 * freq.numel(), "rotary_dim"), pair_axis, inter, ptr<void>(qw),
+                      ptr<void>(kw), wd, real(a[6]), size32(T, "T"), size32(Hq, "Hq"), size32(Hkv, "Hkv"),
+                      size32(D, "D"), ptr<uint16_t>(qo), ptr<void>(ko), dtype_of(ko, "k_out"), c.stream));
+  return tuple(qo, ko);
+}
+
 // (use, bytes, device index, stream handle): the workspace, for the calls that are marshalled in Python
 PyObject* make_workspace(PyObject* const* a) {
   const char* use = PyUnicode_AsUTF8(a[0]);
@@ -454,6 +501,7 @@ PyMethodDef kMethods[] = {
     {"block_plan", QG_FAST(block_plan, 14), nullptr}, {"append", QG_FAST(append, 7), nullptr},
     {"read", QG_FAST(read, 5), nullptr},              {"attention", QG_FAST(attention, 12), nullptr},
     {"norm_bf16", QG_FAST(norm_bf16, 7), nullptr},    {"norm_i8", QG_FAST(norm_i8, 9), nullptr},
+    {"qk_rope", QG_FAST(qk_rope, 12), nullptr},
     {"workspace", QG_FAST(make_workspace, 4), nullptr},
     {"set_raise", set_raise, METH_O, nullptr},        {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_qgbind", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

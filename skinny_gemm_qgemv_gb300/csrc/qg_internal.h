@@ -223,7 +223,8 @@ cudaError_t launch_w8a16_gemv(const int8_t* wq, const float* scales, const uint1
                               cudaStream_t stream, bool pdl);
 
 // The decode step around the products: paged 8-bit key/value cache
-// (kv8_cache.cu), attention over it (attn_kv8.cu), residual RMS norm (rmsnorm.cu)
+// (kv8_cache.cu), attention over it (attn_kv8.cu), residual RMS norm (rmsnorm.cu), norms of
+// queries and keys with the position rotation (qk_rope.cu)
 struct PlanArgs {
   const int32_t *old_lens, *new_lens;
   int R, bs;
@@ -284,6 +285,22 @@ struct NormArgs {
   void* out;
   float* scale;  // null: bf16 output
 };
+struct RopeArgs {
+  const void *q, *k;
+  int x_f32;
+  long long q_stride, k_stride;
+  const int32_t* pos;        // [axes][T]
+  const double* inv_freq;    // [rot / 2]
+  uint32_t axis_bits[8];     // two bits a pair
+  int rot, interleaved;
+  const void *q_w, *k_w;     // null: no norm
+  int w_f32;
+  float eps;
+  int T, Hq, Hkv, D;
+  uint16_t* q_out;
+  void* k_out;
+  int k_out_f32;
+};
 cudaError_t launch_kv8_plan(const PlanArgs& a, cudaStream_t stream, bool pdl);
 cudaError_t launch_kv8_append(AppendArgs a, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_kv8_read(const ReadArgs& a, int format, cudaStream_t stream, bool pdl);
@@ -293,6 +310,7 @@ bool attn_kv8_ok(const AttnArgs& a);
 cudaError_t launch_attn_kv8(const AttnArgs& a, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_attn_kv8_tc(const AttnArgs& a, int format, cudaStream_t stream, bool pdl);  // D <= 128
 cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t stream, bool pdl);
+cudaError_t launch_qk_rope(const RopeArgs& a, cudaStream_t stream, bool pdl);
 
 // MXFP4 MoE (moe_mxfp4.cu, moe_mx_mma.cu)
 constexpr int kMxTC = 8;                // pairs of one virtual expert: the N = 8 columns of one MMA
