@@ -4,11 +4,13 @@
 //   pair i of the first `rot` elements turns by a = position[axis(i)] inv_freq[i]:
 //   (u, v) -> (u cos a - v sin a, v cos a + u sin a).
 //
-// GB300 mapping: a head is 16 or 32 lanes' with four consecutive elements a lane
-// (eight for heads of more than 128), so it stays in registers from one load to one
-// store: HBM bounds many tokens, launch and one trip of loads a few. The sines of a
-// token are formed once for all of its heads, by one thread a pair, into one of two
-// tables in shared memory (one barrier a token).
+// GB300 mapping: a head is 8 to 32 lanes' with two runs of four elements a lane, the
+// two that turn against each other where pairs are split over halves: a head stays in
+// registers from one load to one store, pairs need no exchange, and a warp has two
+// heads' (or pairs of heads') loads on the way. HBM bounds many tokens, launch and one
+// trip of loads a few. The sines of a token are formed once for all of its heads, by a thread a pair
+// and for up to eight tokens at once, into one of two tables in shared memory (one
+// barrier a round).
 //
 // Angles: a / 2 pi counts whole turns, so the fraction of a turn that a position
 // adds is kept as a 64-bit fixed-point number per thread and multiplied by the
@@ -26,210 +28,194 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kUnroll = 2, kCtas = 4;
 
-// four consecutive elements as loaded, and as fp32
+// four consecutive elements as loaded
 template <bool F32>
 struct Quad {
-  uint4 v;  // bf16: .x, .y
+  uint32_t w[F32 ? 4 : 2];
+  __device__ __forceinline__ void load(const void* p) {
+    if (F32) {
+      const uint4 v = *static_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[F32 ? 2 : 0] = v.z, w[F32 ? 3 : 1] = v.w;
+    } else {
+      const uint2 v = *static_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void values(float* f) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      f[j] = __uint_as_float(F32 ? w[F32 ? j : 0] : j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+  }
 };
-template <bool F32>
-__device__ __forceinline__ Quad<F32> load_quad(const void* p, long long i) {
-  Quad<F32> r;
-  if (F32) {
-    r.v = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-    r.v = make_uint4(w.x, w.y, 0u, 0u);
-  }
-  return r;
-}
-template <bool F32>
-__device__ __forceinline__ void to_f32(const Quad<F32>& r, float (&f)[4]) {
-  if (F32) {
-    f[0] = __uint_as_float(r.v.x), f[1] = __uint_as_float(r.v.y);
-    f[2] = __uint_as_float(r.v.z), f[3] = __uint_as_float(r.v.w);
-  } else {
-    f[0] = __uint_as_float(r.v.x << 16), f[1] = __uint_as_float(r.v.x & 0xFFFF0000u);
-    f[2] = __uint_as_float(r.v.y << 16), f[3] = __uint_as_float(r.v.y & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void weights4(const void* w, int f32, int at, float (&f)[4]) {
-  if (f32) {
-    to_f32<true>(load_quad<true>(w, at), f);
-  } else {
-    to_f32<false>(load_quad<false>(w, at), f);
-  }
-}
 
-// L: lanes of a head; C: runs of four elements a lane has, 4 L apart; F32: the type of x; UN: heads of a warp at a time
-template <bool F32, int L, int C, int UN>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(RopeArgs a) {
-  __shared__ float2 turn[2][128];  // (cos, sin) of the token's pairs
+// L: lanes of a head, each with two of its quads of elements; F32: the type of x
+template <bool F32, int L>
+__global__ void __launch_bounds__(kThreads, kCtas) qk_rope_kernel(RopeArgs a, int lead, int lead_log) {
+  constexpr int HW = 32 / L;              // heads of a warp's load
+  constexpr int kSize = F32 ? 4 : 2;      // bytes of an element
+  __shared__ float2 turn[2][kThreads];    // (cos, sin) of the pairs of a round's tokens
+  __shared__ __align__(16) float weight[2][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int HW = 32 / L;  // heads of a warp's load
   const int ql = lane % L, half = a.rot / 2;
+  // A lane's quads begin at e[0] and e[1]: where halves turn against each other the elements of a pair are the same
+  // ones of its two quads; else, and past the turning elements, its quads are neighbours.
+  const bool split = !a.interleaved && 4 * ql < half;
+  const int e[2] = {split ? 4 * ql : 8 * ql, split ? 4 * ql + half : 8 * ql + 4};
+  const bool in = e[0] < a.D, turns = e[0] < a.rot;
   pdl_wait();
   pdl_launch_dependents();
 
-  // the pair that this thread looks after: the fraction of a turn per position, times 2^64
+  // A round is kThreads / lead tokens; a thread forms the sines of one pair of one of them. The fraction of a turn per
+  // position, times 2^64:
+  const int pair = threadIdx.x & (lead - 1), my_token = threadIdx.x >> lead_log, tokens = kThreads >> lead_log;
   unsigned long long step = 0;
-  int axis = 0;
-  if (threadIdx.x < half) {
-    const double t = a.inv_freq[threadIdx.x] * 0.15915494309189533577;  // 1 / (2 pi)
+  const int32_t* my_pos = a.pos;
+  if (pair < half) {
+    const double t = a.inv_freq[pair] * 0.15915494309189533577;  // 1 / (2 pi)
     step = 2ull * (unsigned long long)__double2ll_rn((t - rint(t)) * 9223372036854775808.0);
-    axis = a.axis_bits[threadIdx.x >> 4] >> (2 * (threadIdx.x & 15)) & 3u;
+    my_pos += (long long)(a.axis_bits[pair >> 4] >> (2 * (pair & 15)) & 3u) * a.T;
   }
-  // this lane's weights; its elements past the head count as 0
-  float wq[C][4], wk[C][4];
-  bool in[C], turns[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int e = 4 * (ql + L * c);
-    in[c] = e < a.D, turns[c] = e < a.rot;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) wq[c][j] = wk[c][j] = 1.f;
-    if (in[c] && a.q_w) weights4(a.q_w, a.w_f32, e, wq[c]);
-    if (in[c] && a.k_w) weights4(a.k_w, a.w_f32, e, wk[c]);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < 2 * a.D; i += kThreads) {
+    const int k = i >= a.D, e = i - k * a.D;
+    const void* w = k ? a.k_w : a.q_w;
+    weight[k][e] = !w ? 1.f : a.w_f32 ? static_cast<const float*>(w)[e] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[e]);
   }
   const int heads = a.Hq + a.Hkv, units = (heads + HW - 1) / HW;
-  const int u0 = blockIdx.y * kWarps + warp, du = gridDim.y * kWarps;
+  // a token's units go to kWarps / tokens warps (one round's tokens at most kWarps) of gridDim.y CTAs
+  const int t_of = warp & (tokens - 1), per = kWarps / tokens;
+  const int u0 = blockIdx.y * per + warp / tokens, du = gridDim.y * per;
   const float inv_d = 1.f / (float)a.D;
-  const int shift = half / 4;  // quads between the elements of a pair (split halves)
+  const bool normed = a.q_w || a.k_w;
 
   int b = 0;
 #pragma unroll 1
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    if (a.pos[t] < 0) continue;  // padding (the same for all threads)
-    auto head_of = [&](int u) { return u * HW + lane / L; };
-    Quad<F32> raw[UN][C];
+  for (int t0 = blockIdx.x * tokens; t0 < a.T; t0 += gridDim.x * tokens, b ^= 1) {
+    const int t = t0 + t_of;
+    const bool live = t < a.T && a.pos[min(t, a.T - 1)] >= 0;  // (the same for a warp)
+    // rows of the token; the keys' so that they too are indexed by the head's number among all
+    const char* q_in = static_cast<const char*>(a.q) + t * a.q_stride * kSize;
+    const char* k_in = static_cast<const char*>(a.k) + (t * a.k_stride - a.Hq * a.D) * kSize;
+    Quad<F32> raw[kUnroll][2];
     auto fetch = [&](int u) {
 #pragma unroll
-      for (int n = 0; n < UN; ++n) {
-        const int h = head_of(u + n * du);
+      for (int n = 0; n < kUnroll; ++n) {
+        const int h = (u + n * du) * HW + lane / L;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          raw[n][c].v = make_uint4(0u, 0u, 0u, 0u);
-          if (h < heads && in[c]) {
-            const int e = 4 * (ql + L * c);
-            raw[n][c] = h < a.Hq ? load_quad<F32>(a.q, t * a.q_stride + h * a.D + e)
-                                 : load_quad<F32>(a.k, t * a.k_stride + (h - a.Hq) * a.D + e);
-          }
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int j = 0; j < kSize; ++j) raw[n][c].w[j] = 0u;
+        }
+        if (live && h < heads && in) {
+          const char* src = h < a.Hq ? q_in : k_in;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) raw[n][c].load(src + (h * a.D + e[c]) * kSize);
         }
       }
     };
     fetch(u0);  // on the way while the sines are formed
-    if (threadIdx.x < half) {
-      const long long p = a.pos[(long long)axis * a.T + t];
+    if (pair < half && t0 + my_token < a.T) {
+      const long long p = my_pos[t0 + my_token];
       const float half_turns = (float)(long long)(step * (unsigned long long)p) * 0x1p-63f;  // in [-1, 1]
       float s, c;
       sincospif(half_turns, &s, &c);
       turn[b][threadIdx.x] = make_float2(c, s);
     }
-    __syncthreads();  // (a table is read right after its barrier, and written again past the next token's)
-    // y = x cs + (its partner) sn
-    float cs[C][4], sn[C][4];
+    __syncthreads();  // (a table is written again two rounds later, past the next round's barrier)
+    if (!live) continue;
+    // split halves: four pairs (x[0][j], x[1][j]); else pairs (x[c][j], x[c][j + 1]), j even
+    float cs[4], sn[4];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = 4 * (ql + L * c);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        cs[c][j] = 1.f, sn[c][j] = 0.f;
-        if (turns[c]) {
-          const bool lo = a.interleaved ? j % 2 == 0 : e < half;
-          const float2 x = turn[b][a.interleaved ? (e + j) / 2 : lo ? e + j : e + j - half];
-          cs[c][j] = x.x, sn[c][j] = lo ? -x.y : x.y;
-        }
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int at = !turns ? 0 : split ? e[0] + j : e[0] / 2 + j;
+      const float2 x = turn[b][t_of * lead + at];
+      cs[j] = turns ? x.x : 1.f, sn[j] = turns ? x.y : 0.f;
     }
 #pragma unroll 1
-    for (int u = u0; u < units; u += UN * du) {
+    for (int u = u0; u < units; u += kUnroll * du) {
       if (u != u0) fetch(u);
 #pragma unroll
-      for (int n = 0; n < UN; ++n) {
-        const int h = head_of(u + n * du);
+      for (int n = 0; n < kUnroll; ++n) {
+        if (u + n * du >= units) break;
+        const int h = (u + n * du) * HW + lane / L;
         const bool is_q = h < a.Hq;
-        float x[C][4];
-        float ss = 0.f;
+        float x[8];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          to_f32<F32>(raw[n][c], x[c]);
+        for (int c = 0; c < 2; ++c) raw[n][c].values(x + 4 * c);
+        if (normed) {
+          float ss = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) ss = fmaf(x[c][j], x[c][j], ss);
-        }
-        if (a.q_w || a.k_w) {
+          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
           for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
-          const bool normed = is_q ? a.q_w != nullptr : a.k_w != nullptr;
+          const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+          if (in && (is_q ? a.q_w != nullptr : a.k_w != nullptr)) {
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (normed) x[c][j] = x[c][j] * r * (is_q ? wq[c][j] : wk[c][j]);
-        }
-        float y[C][4];
-        if (a.interleaved) {
-#pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[c][j] = turns[c] ? fmaf(x[c][j], cs[c][j], x[c][j ^ 1] * sn[c][j]) : x[c][j];
-        } else {
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const int at = ql + L * c, from = turns[c] ? (at < shift ? at + shift : at - shift) : at;
-            const int src = (lane & ~(L - 1)) | (from & (L - 1));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float p = __shfl_sync(0xffffffffu, x[0][j], src);
-              if (C == 2) {
-                const float p1 = __shfl_sync(0xffffffffu, x[C - 1][j], src);
-                if (from >= L) p = p1;
-              }
-              y[c][j] = turns[c] ? fmaf(x[c][j], cs[c][j], p * sn[c][j]) : x[c][j];
+            for (int c = 0; c < 2; ++c) {
+              const float4 g = *reinterpret_cast<const float4*>(weight[is_q ? 0 : 1] + e[c]);
+              x[4 * c] = x[4 * c] * r * g.x, x[4 * c + 1] = x[4 * c + 1] * r * g.y;
+              x[4 * c + 2] = x[4 * c + 2] * r * g.z, x[4 * c + 3] = x[4 * c + 3] * r * g.w;
             }
           }
         }
-        if (h < heads) {
+        if (turns) {
+          if (split) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            if (!in[c]) continue;
-            const int e = 4 * (ql + L * c);
-            const uint2 packed = make_uint2(f32_to_bf16x2(y[c][0], y[c][1]), f32_to_bf16x2(y[c][2], y[c][3]));
-            if (is_q) {
-              *reinterpret_cast<uint2*>(a.q_out + ((long long)t * a.Hq + h) * a.D + e) = packed;
-            } else {
-              const long long to = ((long long)t * a.Hkv + h - a.Hq) * a.D + e;
-              if (a.k_out_f32)
-                *reinterpret_cast<float4*>(static_cast<float*>(a.k_out) + to) = make_float4(y[c][0], y[c][1], y[c][2], y[c][3]);
-              else
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.k_out) + to) = packed;
+            for (int j = 0; j < 4; ++j) {
+              const float v = x[j], w = x[4 + j];
+              x[j] = fmaf(v, cs[j], -w * sn[j]), x[4 + j] = fmaf(w, cs[j], v * sn[j]);
             }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float v = x[2 * j], w = x[2 * j + 1];
+              x[2 * j] = fmaf(v, cs[j], -w * sn[j]), x[2 * j + 1] = fmaf(w, cs[j], v * sn[j]);
+            }
+          }
+        }
+        if (h < heads && in) {
+          const long long row = is_q ? (long long)t * a.Hq + h : (long long)t * a.Hkv + h - a.Hq;
+          if (!is_q && a.k_out_f32) {
+            float* dst = static_cast<float*>(a.k_out) + row * a.D;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<float4*>(dst + e[c]) = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          } else {
+            uint16_t* dst = (is_q ? a.q_out : static_cast<uint16_t*>(a.k_out)) + row * a.D;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<uint2*>(dst + e[c]) =
+                  make_uint2(f32_to_bf16x2(x[4 * c], x[4 * c + 1]), f32_to_bf16x2(x[4 * c + 2], x[4 * c + 3]));
           }
         }
       }
     }
-    b ^= 1;
   }
 }
 
-template <bool F32, int L, int C>
+template <bool F32, int L>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream, bool pdl) {
-  const int sms = device_sm_count();
-  const int units = (a.Hq + a.Hkv + 32 / L - 1) / (32 / L), per = (units + kWarps - 1) / kWarps;
-  // few tokens: their heads over several CTAs, a head a warp
-  const int split = std::min(per, std::max(1, 2 * sms / a.T));
-  const int grid = std::min(a.T, 8 * sms);
-  auto k = qk_rope_kernel<F32, L, C, 2>;
-  return launch_kernel(k, dim3(grid, split), dim3(kThreads), 0, stream, pdl, a);
+  const int sms = device_sm_count(), units = (a.Hq + a.Hkv + 32 / L - 1) / (32 / L);
+  // Threads per token of a round: its pairs, filled up to a power of two. A round takes as many tokens as keep the SMs
+  // busy, eight at most (a warp each); few tokens: one a round, its heads over several CTAs, one to a warp.
+  int lead_log = 5;
+  while (1 << lead_log < a.rot / 2) ++lead_log;
+  while (lead_log < 8 && (a.T + (kThreads >> lead_log) - 1) / (kThreads >> lead_log) < kCtas * sms) ++lead_log;
+  const int tokens = kThreads >> lead_log, rounds = (a.T + tokens - 1) / tokens;
+  const int parts = tokens > 1 ? 1 : std::min((units + kWarps - 1) / kWarps, std::max(1, 2 * sms / rounds));
+  auto k = qk_rope_kernel<F32, L>;
+  return launch_kernel(k, dim3(std::min(rounds, kCtas * sms), parts), dim3(kThreads), 0, stream, pdl, a, 1 << lead_log,
+                       lead_log);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_rope(const RopeArgs& a, cudaStream_t stream, bool pdl) {
-  if (a.D <= 64) return a.x_f32 ? launch<true, 16, 1>(a, stream, pdl) : launch<false, 16, 1>(a, stream, pdl);
-  if (a.D <= 128) return a.x_f32 ? launch<true, 32, 1>(a, stream, pdl) : launch<false, 32, 1>(a, stream, pdl);
-  return a.x_f32 ? launch<true, 32, 2>(a, stream, pdl) : launch<false, 32, 2>(a, stream, pdl);
+  if (a.D <= 64) return a.x_f32 ? launch<true, 8>(a, stream, pdl) : launch<false, 8>(a, stream, pdl);
+  if (a.D <= 128) return a.x_f32 ? launch<true, 16>(a, stream, pdl) : launch<false, 16>(a, stream, pdl);
+  return a.x_f32 ? launch<true, 32>(a, stream, pdl) : launch<false, 32>(a, stream, pdl);
 }
 
 }  // namespace qg
