@@ -701,6 +701,44 @@ QG_API qg_status attn_kv8_paged(const uint16_t *q_bf16, int64_t q_stride, const 
 QG_API size_t qg_attn_kv8_workspace_size(int Hq, int Hkv, int D);
 
 /*
+ * attn_kv8_shared -- attn_kv8_paged for a batch whose requests begin, in groups,
+ * with the same tokens (a system prompt, a document that several answers are
+ * drawn about): a group's prefix lies in the cache once and is read once for all
+ * of the group's query tokens.
+ *
+ *   cu_req       int32 [groups + 1]: group g's requests are cu_req[g] ..
+ *                cu_req[g+1] - 1 (none is allowed); 0 <= cu_req <= R, ascending
+ *                (otherwise nothing is written, and it is reported). Requests
+ *                before cu_req[0] and from cu_req[groups] on have no prefix.
+ *   prefix_table int32 [groups][max_prefix_blocks], prefix_lens int32 [groups]:
+ *                the blocks and the number of tokens of each group's prefix (0
+ *                is allowed, and any length: the last block may be partly
+ *                filled). For example the rows of requests of their own in
+ *                kv8_block_plan's table, which hold the prefixes.
+ *   block_table, ctx_lens, cu_q, tree_mask  as in attn_kv8_paged, for what
+ *                comes after the prefix: ctx_lens[r] counts request r's own
+ *                tokens, its query tokens among them. (Its positions, for the
+ *                rotation of queries and keys, count the prefix too.)
+ *   out_bf16     as in attn_kv8_paged, over the prefix's tokens, all of which
+ *                every query token of the group sees, and the request's own.
+ *   1 <= groups <= 1024; everything else as in attn_kv8_paged, its remarks on
+ *   accuracy included; the partial results of prefix and own tokens join in fp32.
+ *   workspace    qg_attn_kv8_shared_workspace_size(T, Hq, Hkv, D) bytes, 16-byte
+ *                aligned, zero-filled before its first use: its counters (the
+ *                first 4096 bytes) are left at zero by every call, the rest is
+ *                scratch. Calls that may overlap need separate workspaces.
+ * Three launches, capturable in a CUDA graph.
+ */
+QG_API qg_status attn_kv8_shared(const uint16_t *q_bf16, int64_t q_stride, const void *k_cache,
+                                 const void *v_cache, const float *scales, const int32_t *prefix_table,
+                                 const int32_t *prefix_lens, const int32_t *cu_req, const int32_t *block_table,
+                                 const int32_t *ctx_lens, const int32_t *cu_q, const uint32_t *tree_mask,
+                                 int groups, int R, int T, int Hq, int Hkv, int D, int block_size, int num_blocks,
+                                 int max_prefix_blocks, int max_blocks, int format, float softmax_scale,
+                                 uint16_t *out_bf16, void *workspace, size_t ws_bytes, void *stream);
+QG_API size_t qg_attn_kv8_shared_workspace_size(int T, int Hq, int Hkv, int D);
+
+/*
  * rmsnorm_residual / rmsnorm_residual_i8 -- the residual addition and the RMS
  * norm before a product, as bf16 (the W4A16 products) or as int8 codes with a
  * scale per row (the W8A8 products).
@@ -783,7 +821,8 @@ typedef enum {
   QG_OP_W8A8_I32 = 4,       /* gemm_w8a8_i32 (none) */
   QG_OP_W8A8_HADAMARD = 5,  /* gemm_w8a8_hadamard */
   QG_OP_KV8_PLAN = 6,       /* kv8_block_plan */
-  QG_OP_ATTN_KV8 = 7        /* attn_kv8_paged: M = Hq, N = Hkv, K = D */
+  QG_OP_ATTN_KV8 = 7,       /* attn_kv8_paged: M = Hq, N = Hkv, K = D */
+  QG_OP_ATTN_KV8_SHARED = 8 /* attn_kv8_shared: T, M = Hq, N = Hkv, K = D */
 } qg_op;
 
 QG_API size_t qg_workspace_size(int op, int M, int N, int K, int T, int E, int top_k);

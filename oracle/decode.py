@@ -161,6 +161,63 @@ def attention(q, k_cache, v_cache, scales, table, ctx_lens, cu_q, fmt, softmax_s
     return out, mag, qk, seen_n, vmax
 
 
+def attention_shared(q, k_cache, v_cache, scales, ptable, plens, cu_req, table, ctx_lens, cu_q, fmt, softmax_scale,
+                     tree=None):
+    """As attention, for requests that see the tokens of their group's prefix
+    (ptable, plens; group g has the requests cu_req[g] .. cu_req[g + 1] - 1) before
+    their own."""
+    T, Hq, D = q.shape
+    nb, Hkv, bs, _ = k_cache.shape
+    G = Hq // Hkv
+    out, mag = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    qk, seen_n, vmax = np.zeros((T, Hq)), np.zeros((T, Hq)), np.zeros((T, Hq))
+    group_of = {r: g for g in range(len(plens)) for r in range(int(cu_req[g]), int(cu_req[g + 1]))}
+
+    def tokens(row, n):
+        tok = np.arange(n)
+        blk = row[tok // bs].astype(np.int64)
+        return np.where((blk >= 0) & (blk < nb), blk, -1), tok % bs
+
+    for r in range(len(ctx_lens)):
+        n = int(cu_q[r + 1] - cu_q[r])
+        ctx = min(max(int(ctx_lens[r]), 0), table.shape[1] * bs)
+        pre = min(max(int(plens[group_of[r]]), 0), ptable.shape[1] * bs) if r in group_of else 0
+        blk, slot = tokens(table[r], ctx)
+        if pre:
+            pb, ps = tokens(ptable[group_of[r]], pre)
+            blk, slot = np.concatenate((pb, blk)), np.concatenate((ps, slot))
+        good, safe = blk >= 0, np.where(blk >= 0, blk, 0)
+        tok, base = np.arange(pre + ctx), pre + ctx - n
+        if n == 0 or pre + ctx == 0:
+            continue
+        see = np.zeros((n, pre + ctx), bool)
+        for i in range(n):
+            if tree is not None and n <= 32:
+                bits = (int(tree[int(cu_q[r]) + i]) >> np.clip(tok - base, 0, 31)) & 1
+                see[i] = good & ((tok < base) | (tok < pre) | (bits == 1))
+            else:
+                see[i] = good & ((tok <= base + i) | (tok < pre))
+        live = see.any(1)
+        at = int(cu_q[r]) + np.arange(n)[live]
+        if not live.any():
+            continue
+        for h in range(Hkv):
+            K = decode(k_cache[safe, h, slot], fmt) * scales[safe, h, 0].astype(np.float64)[:, None]
+            V = decode(v_cache[safe, h, slot], fmt) * scales[safe, h, 1].astype(np.float64)[:, None]
+            used = see.any(0)
+            V = np.where(used[:, None], V, 0.0)
+            for hq in range(h * G, (h + 1) * G):
+                qq = q[at, hq].astype(np.float64)
+                s = np.where(see[live], qq @ K.T * softmax_scale, -np.inf)
+                p = np.exp(s - s.max(1, keepdims=True))
+                p /= p.sum(1, keepdims=True)
+                out[at, hq], mag[at, hq] = p @ V, p @ np.abs(V)
+                qk[at, hq] = np.where(see[live], np.abs(qq) @ np.abs(K).T, 0).max(1) * softmax_scale
+                seen_n[at, hq] = see[live].sum(1)
+                vmax[at, hq] = np.where(see[live], np.abs(V).max(1), 0).max(1)
+    return out, mag, qk, seen_n, vmax
+
+
 def rmsnorm(h, weight, eps, sign_bits=None):
     """float64 y (or its randomized Hadamard transform) of the stored rows h;
     also sum |y| of each value's 32-block (or |y| itself)."""

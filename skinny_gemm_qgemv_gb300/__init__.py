@@ -9,8 +9,8 @@ Entry points (same names as the C ABI):
   qgemv_w4a16, qgemm_w4a16_skinny, moe_mxfp4_expert_forward,
   hadamard32_quant_i8, gemm_w8a8_i32; GemvGroup wraps qgemv_w4a16_group_* and
   SkinnyGroup qgemm_w4a16_skinny_group_*. The decode step around the products:
-  kv8_block_plan, kv8_append, kv8_read, attn_kv8_paged (the paged 8-bit
-  key/value cache), rmsnorm_residual, rmsnorm_residual_i8, qk_norm_rope
+  kv8_block_plan, kv8_append, kv8_read, attn_kv8_paged, attn_kv8_shared (the
+  paged 8-bit key/value cache), rmsnorm_residual, rmsnorm_residual_i8, qk_norm_rope
 
 A call is enqueued on `stream`, torch's current one by default. With a stream
 given, the caller orders it after what made the inputs and keeps the inputs
@@ -46,11 +46,11 @@ EXPORTS = [
     "gemm_w8a8_hadamard", "qg_w8a8_hadamard_workspace_size", "qg_workspace_size",
     "kv8_block_plan", "qg_kv8_plan_workspace_size", "kv8_append", "kv8_read", "attn_kv8_paged",
     "qg_attn_kv8_workspace_size", "rmsnorm_residual", "rmsnorm_residual_i8",
-    "qk_norm_rope",
+    "qk_norm_rope", "attn_kv8_shared", "qg_attn_kv8_shared_workspace_size",
 ]
 
 (OP_GEMV_W4A16, OP_SKINNY_W4A16, OP_MOE_MXFP4, OP_HADAMARD_I8, OP_W8A8_I32, OP_W8A8_HADAMARD, OP_KV8_PLAN,
- OP_ATTN_KV8) = range(8)
+ OP_ATTN_KV8, OP_ATTN_KV8_SHARED) = range(9)
 
 X_BF16, X_COPY, X_SWIGLU = 0, 1, 2
 
@@ -178,6 +178,10 @@ def lib() -> ctypes.CDLL:
         L.rmsnorm_residual.argtypes = [P, I, P, I, P, I, F, I, I, P, P, P]
         L.rmsnorm_residual_i8.restype = I
         L.rmsnorm_residual_i8.argtypes = [P, I, P, I, P, I, F, P, I, I, P, P, P, P]
+        L.attn_kv8_shared.restype = I
+        L.attn_kv8_shared.argtypes = [P, I64] + [P] * 10 + [I] * 11 + [F, P, P, Z, P]
+        L.qg_attn_kv8_shared_workspace_size.restype = Z
+        L.qg_attn_kv8_shared_workspace_size.argtypes = [I, I, I, I]
         L.qk_norm_rope.restype = I
         L.qk_norm_rope.argtypes = [P, I64, P, I64, I, P, I, P, I, P, I, P, P, I, F, I, I, I, I, P, P, I, P]
         _lib = L
@@ -593,6 +597,20 @@ def attn_kv8_paged(q, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tre
     workspace is kept per (device, stream); a stream capture has one of its own."""
     return (_bind or _binding()).attention(q, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tree_mask,
                                            softmax_scale, out, workspace, stream)
+
+
+def attn_kv8_shared(q, k_cache, v_cache, scales, prefix_table, prefix_lens, cu_req, block_table, ctx_lens, cu_q,
+                    tree_mask=None, softmax_scale=None, out=None, workspace=None, stream=None):
+    """attn_kv8_paged for requests that begin, in groups, with the same tokens:
+    group g's requests cu_req[g] .. cu_req[g + 1] - 1 (int32 [groups + 1]; requests
+    outside all groups have no prefix) see the prefix_lens[g] tokens of
+    prefix_table[g] (int32 [groups][max_prefix_blocks]) before their own;
+    block_table, ctx_lens, cu_q and tree_mask are of their own tokens alone. A
+    prefix is read once for all of its group. The zeroed workspace is kept per
+    (device, stream) and grows with T; a stream capture has one of its own."""
+    return (_bind or _binding()).attention_shared(q, k_cache, v_cache, scales, prefix_table, prefix_lens, cu_req,
+                                                  block_table, ctx_lens, cu_q, tree_mask, softmax_scale, out, workspace,
+                                                  stream)
 
 
 def rmsnorm_residual(x, weight, residual=None, eps=1e-6, residual_out=None, out=None, stream=None):

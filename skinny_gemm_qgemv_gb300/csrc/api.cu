@@ -384,6 +384,7 @@ size_t qg_workspace_size(int op, int M, int N, int K, int T, int E, int top_k) {
     case QG_OP_W8A8_HADAMARD: return qg_w8a8_hadamard_workspace_size(M, K);
     case QG_OP_KV8_PLAN: return qg_kv8_plan_workspace_size();
     case QG_OP_ATTN_KV8: return qg_attn_kv8_workspace_size(M, N, K);
+    case QG_OP_ATTN_KV8_SHARED: return qg_attn_kv8_shared_workspace_size(T, M, N, K);
     default: return 0;  // the Hadamard quantizer and the int32 W8A8 product need none
   }
 }
@@ -545,6 +546,16 @@ size_t qg_attn_kv8_workspace_size(int Hq, int Hkv, int D) {
   return qg::attn_kv8_workspace_size(Hq, Hkv, D);
 }
 
+static qg_status check_attn(int R, int T, int Hq, int Hkv, int D, int block_size, int max_blocks, int64_t q_stride,
+                            float softmax_scale) {
+  if (R < 1 || R > 1024 || T < 1 || Hq < 1 || Hq > 1024 || Hq % Hkv != 0 || max_blocks < 1) return QG_ERR_INVALID_ARG;
+  if ((long long)max_blocks * block_size > (1LL << 31) - 2048 || (long long)T * Hq >= (1LL << 31))
+    return QG_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)Hq * D || q_stride % 8 != 0) return QG_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f)) return QG_ERR_INVALID_ARG;
+  return QG_OK;
+}
+
 qg_status attn_kv8_paged(const uint16_t* q_bf16, int64_t q_stride, const void* k_cache, const void* v_cache,
                          const float* scales, const int32_t* block_table, const int32_t* ctx_lens,
                          const int32_t* cu_q, const uint32_t* tree_mask, int R, int T, int Hq, int Hkv, int D,
@@ -554,11 +565,8 @@ qg_status attn_kv8_paged(const uint16_t* q_bf16, int64_t q_stride, const void* k
     return QG_ERR_INVALID_ARG;
   qg_status st = check_kv8(Hkv, D, block_size, num_blocks, format);
   if (st != QG_OK) return st;
-  if (R < 1 || R > 1024 || T < 1 || Hq < 1 || Hq > 1024 || Hq % Hkv != 0 || max_blocks < 1) return QG_ERR_INVALID_ARG;
-  if ((long long)max_blocks * block_size > (1LL << 31) - 2048 || (long long)T * Hq >= (1LL << 31))
-    return QG_ERR_INVALID_ARG;
-  if (q_stride < (int64_t)Hq * D || q_stride % 8 != 0) return QG_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f)) return QG_ERR_INVALID_ARG;
+  st = check_attn(R, T, Hq, Hkv, D, block_size, max_blocks, q_stride, softmax_scale);
+  if (st != QG_OK) return st;
   if (!aligned16(q_bf16) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(scales) ||
       !aligned16(block_table) || !aligned16(ctx_lens) || !aligned16(cu_q) || !aligned16(tree_mask) ||
       !aligned16(out_bf16) || !aligned16(workspace))
@@ -572,6 +580,44 @@ qg_status attn_kv8_paged(const uint16_t* q_bf16, int64_t q_stride, const void* k
                           out_bf16, workspace, err};
   if (!qg::attn_kv8_ok(a)) return QG_ERR_UNSUPPORTED;
   return from_cuda(qg::launch_attn_kv8(a, format, static_cast<cudaStream_t>(stream), true));
+}
+
+size_t qg_attn_kv8_shared_workspace_size(int T, int Hq, int Hkv, int D) {
+  if (T < 1 || (long long)T * Hq >= (1LL << 31) || qg_attn_kv8_workspace_size(Hq, Hkv, D) == 0) return 0;
+  return qg::attn_kv8_shared_workspace_size(T, Hq, Hkv, D);
+}
+
+qg_status attn_kv8_shared(const uint16_t* q_bf16, int64_t q_stride, const void* k_cache, const void* v_cache,
+                          const float* scales, const int32_t* prefix_table, const int32_t* prefix_lens,
+                          const int32_t* cu_req, const int32_t* block_table, const int32_t* ctx_lens,
+                          const int32_t* cu_q, const uint32_t* tree_mask, int groups, int R, int T, int Hq, int Hkv,
+                          int D, int block_size, int num_blocks, int max_prefix_blocks, int max_blocks, int format,
+                          float softmax_scale, uint16_t* out_bf16, void* workspace, size_t ws_bytes, void* stream) {
+  if (!q_bf16 || !k_cache || !v_cache || !scales || !prefix_table || !prefix_lens || !cu_req || !block_table ||
+      !ctx_lens || !cu_q || !out_bf16)
+    return QG_ERR_INVALID_ARG;
+  qg_status st = check_kv8(Hkv, D, block_size, num_blocks, format);
+  if (st != QG_OK) return st;
+  st = check_attn(R, T, Hq, Hkv, D, block_size, max_blocks, q_stride, softmax_scale);
+  if (st != QG_OK) return st;
+  st = check_attn(groups, T, Hq, Hkv, D, block_size, max_prefix_blocks, q_stride, softmax_scale);
+  if (st != QG_OK) return st;
+  if (!aligned16(q_bf16) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(scales) ||
+      !aligned16(prefix_table) || !aligned16(prefix_lens) || !aligned16(cu_req) || !aligned16(block_table) ||
+      !aligned16(ctx_lens) || !aligned16(cu_q) || !aligned16(tree_mask) || !aligned16(out_bf16) || !aligned16(workspace))
+    return QG_ERR_MISALIGNED;
+  const size_t need = qg_attn_kv8_shared_workspace_size(T, Hq, Hkv, D);
+  if (ws_bytes < need || !workspace) return QG_ERR_WORKSPACE;
+  qg::AttnArgs own = {q_bf16, q_stride, k_cache, v_cache, scales, block_table, ctx_lens, cu_q, tree_mask, R, T,
+                      Hq, Hkv, D, block_size, num_blocks, max_blocks, softmax_scale * 1.4426950408889634f,
+                      out_bf16, workspace, nullptr};
+  qg::AttnArgs pre = own;
+  pre.table = prefix_table, pre.ctx_lens = prefix_lens, pre.R = groups, pre.max_blocks = max_prefix_blocks;
+  pre.tree = nullptr, pre.cu_req = cu_req, pre.requests = R;
+  if (!qg::attn_kv8_ok(own) || !qg::attn_kv8_ok(pre)) return QG_ERR_UNSUPPORTED;
+  own.err = pre.err = err_word();
+  if (!own.err) return QG_ERR_CUDA;
+  return from_cuda(qg::launch_attn_kv8_shared(own, pre, format, static_cast<cudaStream_t>(stream), true));
 }
 
 static qg_status check_norm(const qg::NormArgs& a, int x_dtype, int res_dtype, int w_dtype) {

@@ -134,8 +134,9 @@ __device__ __forceinline__ int attn_cost_of(const AttnBatch& b, int step) {
 // The batch's tables in shared memory, formed by all NT threads of a CTA (`part`
 // has NT / 32 entries); returns the batch. The host has checked that the sums
 // stay below 2^31 for query tokens that ascend within T; if they do not, the
-// batch's cost is -1.
-template <int ROWS, class CUT, int NT>
+// batch's cost is -1. GROUPS: with a.cu_req a context is a group's, its query
+// tokens those of its requests.
+template <int ROWS, class CUT, int NT, bool GROUPS = false>
 __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, int* cost, int* cus, int* ctxs,
                                                int2* part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hkv;
@@ -146,7 +147,13 @@ __device__ __forceinline__ AttnBatch attn_scan(const AttnArgs& a, int* first, in
   bool bad = false;
 #pragma unroll 1
   for (int r = r0; r < r1; ++r) {
-    const int q0 = a.cu_q[r], q1 = a.cu_q[r + 1];
+    int i0 = r, i1 = r + 1;
+    if (GROUPS && a.cu_req) {
+      i0 = a.cu_req[r], i1 = a.cu_req[r + 1];
+      bad |= i0 < 0 || i0 > i1 || i1 > a.requests;
+      i0 = min(max(i0, 0), a.requests), i1 = min(max(i1, 0), a.requests);
+    }
+    const int q0 = a.cu_q[i0], q1 = a.cu_q[i1];
     bad |= q0 < 0 || q0 > q1 || q1 > a.T;
     int ctx = max(0, a.ctx_lens[r]);
     if (ctx > most) {

@@ -355,6 +355,39 @@ PyObject* attention(PyObject* const* a) {
   return wrap(out);
 }
 
+PyObject* attention_shared(PyObject* const* a) {
+  const at::Tensor &q = *tensor(a[0], "q"), &kc = *tensor(a[1], "k_cache"), &vc = *tensor(a[2], "v_cache"),
+                   &sc = *tensor(a[3], "scales"), &ptable = *tensor(a[4], "prefix_table"),
+                   &plens = *tensor(a[5], "prefix_lens"), &cu_req = *tensor(a[6], "cu_req"),
+                   &table = *tensor(a[7], "block_table"), &ctx = *tensor(a[8], "ctx_lens"),
+                   &cu = *tensor(a[9], "cu_q");
+  const at::Tensor* tree = tensor_or_null(a[10], "tree_mask");
+  const Call c("attn_kv8_shared", q, a[14]);
+  const Cache s = cache_of(c, kc, vc, sc);
+  const int64_t stride = token_stride(c, q, "q");
+  const int64_t T = q.size(0), Hq = q.size(1), R = ctx.numel(), G = plens.numel();
+  if (q.scalar_type() != at::kBFloat16 || q.size(2) != s.D) refuse("q must be bfloat16 [T][Hq][D] with the cache's D");
+  c.need(plens, at::kInt, {G}, "prefix_lens");
+  c.need(cu_req, at::kInt, {G + 1}, "cu_req");
+  c.need(ptable, at::kInt, {G, -1}, "prefix_table");
+  c.need(ctx, at::kInt, {R}, "ctx_lens");
+  c.need(cu, at::kInt, {R + 1}, "cu_q");
+  c.need(table, at::kInt, {R, -1}, "block_table");
+  if (tree) c.need(*tree, at::kInt, {T}, "tree_mask");
+  const float scale = a[11] == Py_None ? 1.f / std::sqrt(static_cast<float>(s.D)) : real(a[11]);
+  at::Tensor out = c.output(a[12], at::kBFloat16, {T, Hq, s.D}, "out");
+  if (!out.defined()) out = c.make({T, Hq, s.D}, at::kBFloat16);
+  const int hq = size32(Hq, "Hq"), t = size32(T, "T");
+  const at::Tensor ws = workspace(c, a[13], "attn_shared", qg_attn_kv8_shared_workspace_size(t, hq, s.Hkv, s.D));
+  c.done(attn_kv8_shared(ptr<uint16_t>(q), stride, ptr<void>(kc), ptr<void>(vc), ptr<float>(sc), ptr<int32_t>(ptable),
+                         ptr<int32_t>(plens), ptr<int32_t>(cu_req), ptr<int32_t>(table), ptr<int32_t>(ctx),
+                         ptr<int32_t>(cu), ptr<uint32_t>(tree), size32(G, "groups"), size32(R, "R"), t, hq, s.Hkv, s.D,
+                         s.block_size, s.num_blocks, size32(ptable.size(1), "max_prefix_blocks"),
+                         size32(table.size(1), "max_blocks"), s.format, scale, ptr<uint16_t>(out),
+                         ws.defined() ? ptr<void>(ws) : nullptr, ws.defined() ? ws.nbytes() : 0, c.stream));
+  return wrap(out);
+}
+
 struct Norm {
   int M, K, xd, rd, wd;
   at::Tensor res_out;
@@ -500,6 +533,7 @@ PyObject* set_raise(PyObject*, PyObject* f) {
 PyMethodDef kMethods[] = {
     {"block_plan", QG_FAST(block_plan, 14), nullptr}, {"append", QG_FAST(append, 7), nullptr},
     {"read", QG_FAST(read, 5), nullptr},              {"attention", QG_FAST(attention, 12), nullptr},
+    {"attention_shared", QG_FAST(attention_shared, 15), nullptr},
     {"norm_bf16", QG_FAST(norm_bf16, 7), nullptr},    {"norm_i8", QG_FAST(norm_i8, 9), nullptr},
     {"qk_rope", QG_FAST(qk_rope, 12), nullptr},
     {"workspace", QG_FAST(make_workspace, 4), nullptr},

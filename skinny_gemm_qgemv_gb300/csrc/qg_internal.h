@@ -270,6 +270,12 @@ struct AttnArgs {
   uint16_t* out;
   void* ws;
   uint32_t* err;
+  // of attn_kv8_shared.cu's passes: R counts groups whose requests, of `requests`, cu_req [R + 1] bounds, or is null;
+  // partial results: fp32 [T * Hq][D] and (maximum, sum) [T * Hq]
+  const int32_t* cu_req;
+  int requests;
+  float* part_o;
+  float2* part_ml;
 };
 struct NormArgs {
   const void* x;
@@ -309,6 +315,10 @@ size_t attn_kv8_workspace_size(int Hq, int Hkv, int D);
 bool attn_kv8_ok(const AttnArgs& a);
 cudaError_t launch_attn_kv8(const AttnArgs& a, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_attn_kv8_tc(const AttnArgs& a, int format, cudaStream_t stream, bool pdl);  // D <= 128
+// attention of requests whose groups share a prefix (attn_kv8_shared.cu): own has every request's own context, pre every
+// group's prefix (R, table, ctx_lens, max_blocks, cu_req)
+size_t attn_kv8_shared_workspace_size(int T, int Hq, int Hkv, int D);
+cudaError_t launch_attn_kv8_shared(const AttnArgs& own, const AttnArgs& pre, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t stream, bool pdl);
 cudaError_t launch_qk_rope(const RopeArgs& a, cudaStream_t stream, bool pdl);
 

@@ -8,14 +8,23 @@ Tolerances (fixed before the first run):
     sine and cosine by another 2 units: a pair (u, v) comes out within
     2^-19 (|u| + |v|), and 2^-51 of the whole angle times that; a bf16 result
     within 2^-8 of itself more.
+  * attention with a shared prefix: |o - ref| <= 2^-8 |ref| (the bf16 result) +
+    (2^-11 + 2 d + n 2^-24 + 2^-20) sum p|v| + n 2^-25 max|v|, n the seen tokens:
+    the probabilities' fp16 rounding, the scores' fp32 error d = (D + 8) 2^-23 max
+    sum|q k| in both numerator and denominator, the fp32 sums, the joining of
+    partial results, and probabilities below fp16's normal range.
 """
 import numpy as np
 import pytest
 import torch
 
+from oracle import decode as od
+
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+FMT = {"i8": od.I8, "e4m3": od.E4M3}
+DT = {"i8": torch.int8, "e4m3": torch.float8_e4m3fn}
 
 
 @pytest.fixture(scope="module")
@@ -160,3 +169,240 @@ def test_rope_refusals(q):
         q.qk_norm_rope(x, k, pos[None].expand(2, 3).contiguous(), f, pair_axis=[2] + [0] * 31)
     with pytest.raises(q.QGError):
         q.qk_norm_rope(x, k, pos, f[:30])
+
+
+# --------------------------------------------------------------------------
+# attention with a shared prefix
+# --------------------------------------------------------------------------
+
+def i32(x):
+    a = np.asarray(x, dtype=np.int64)
+    return torch.from_numpy(a.astype(np.uint32).view(np.int32).copy()).to(DEV)
+
+
+class Shared:
+    """A batch: groups [(prefix length, requests)], `before` and `after` requests without a prefix; lens, nq: own
+    tokens and query tokens of all requests in order."""
+
+    def __init__(self, seed, fmt, groups, before, after, lens, nq, Hq, Hkv, D, bs, tree=False, spare_rows=0, q_size=1.5):
+        rng = np.random.default_rng(seed)
+        self.fmt, self.D = fmt, D
+        self.plens, R = [p for p, _ in groups], before + after + sum(n for _, n in groups)
+        assert len(lens) == len(nq) == R
+        self.lens, self.cu = list(lens), np.concatenate(([0], np.cumsum(nq)))
+        self.cu_req = before + np.concatenate(([0], np.cumsum([n for _, n in groups])))
+        need = [-(-n // bs) for n in self.plens + self.lens]
+        nb = sum(need) + 3
+        c = rng.integers(0, 256, (2, nb, Hkv, bs, D), dtype=np.uint8)
+        if fmt == "i8":
+            c[c == 128] = 7
+        else:
+            c[(c & 0x7F) == 0x7F] ^= 0x10
+        self.k, self.v = c
+        self.scales = (rng.random((nb, Hkv, 2)) * 2.0 / float(od.QMAX[FMT[fmt]]) + 1e-4).astype(np.float32)
+        ids, at = rng.permutation(nb), 0
+        tables = []
+        for part in (need[:len(groups)], need[len(groups):]):
+            t = np.full((len(part), max(1, max(part)) + 1), -1)
+            for r, n in enumerate(part):
+                t[r, :n] = ids[at:at + n]
+                at += n
+            tables.append(t)
+        self.ptable, self.table = tables
+        T = int(self.cu[-1]) + spare_rows
+        # the fill-up of D elements keeps scores of some size
+        self.q = torch.from_numpy(rng.standard_normal((T, Hq, D)) * q_size).to(torch.bfloat16)
+        self.tree = None
+        if tree:
+            self.tree = np.zeros(T, np.int64)
+            for r in range(R):
+                for i in range(nq[r]):
+                    p = rng.integers(-1, i) if i else -1
+                    t = self.cu[r] + i
+                    self.tree[t] = ((self.tree[self.cu[r] + p] if p >= 0 else 0) | 1 << min(i, 31)) & 0xFFFFFFFF
+
+    def args(self):
+        cache = [torch.from_numpy(x.copy()).to(DEV).view(DT[self.fmt]) for x in (self.k, self.v)]
+        return dict(q=self.q.to(DEV), k_cache=cache[0], v_cache=cache[1], scales=torch.from_numpy(self.scales).to(DEV),
+                    prefix_table=i32(self.ptable), prefix_lens=i32(self.plens), cu_req=i32(self.cu_req),
+                    block_table=i32(self.table), ctx_lens=i32(self.lens), cu_q=i32(self.cu),
+                    tree_mask=None if self.tree is None else i32(self.tree))
+
+    def check(self, out, scale=None, rows=None):
+        scale = self.D ** -0.5 if scale is None else scale
+        ref, mag, qk, n, vmax = od.attention_shared(
+            self.q.double().numpy(), self.k, self.v, self.scales, self.ptable, self.plens, self.cu_req, self.table,
+            self.lens, self.cu, FMT[self.fmt], scale, self.tree)
+        qk, n, vmax = qk[..., None], n[..., None], vmax[..., None]
+        tol = 2.0 ** -8 * np.abs(ref) + \
+            (2.0 ** -11 + 2 * (self.D + 8) * 2.0 ** -23 * qk + n * 2.0 ** -24 + 2.0 ** -20) * mag + n * 2.0 ** -25 * vmax
+        T = int(self.cu[-1])
+        rows = np.arange(T) if rows is None else rows
+        err = (np.abs(out.double().cpu().numpy() - ref) - tol)[rows]
+        assert np.all(err <= 0), (err.max(), np.unravel_index(err.argmax(), err.shape))
+
+
+SHARED = {
+    "one": dict(groups=[(1, 1)], before=0, after=0, lens=[1], nq=[1], Hq=1, Hkv=1, D=128, bs=16),
+    "two": dict(groups=[(37, 2)], before=0, after=0, lens=[1, 5], nq=[1, 1], Hq=8, Hkv=2, D=128, bs=16),
+    "ends": dict(groups=[(129, 3), (0, 2), (16, 0), (127, 1)], before=1, after=2, lens=[3, 1, 40, 16, 2, 7, 9, 33, 5],
+                 nq=[1, 1, 2, 1, 1, 3, 1, 0, 1], Hq=8, Hkv=2, D=128, bs=32),
+    "rows129": dict(groups=[(700, 43)], before=0, after=0, lens=[1 + i % 9 for i in range(43)], nq=[1] * 43, Hq=6, Hkv=2,
+                    D=128, bs=64),
+    "rows300": dict(groups=[(3000, 75), (2000, 70)], before=0, after=0, lens=[1 + i % 40 for i in range(145)],
+                    nq=[1] * 145, Hq=4, Hkv=1, D=128, bs=48),
+    "long": dict(groups=[(9000, 3)], before=0, after=1, lens=[500, 1, 130, 300], nq=[1, 1, 1, 1], Hq=8, Hkv=2, D=128,
+                 bs=128),
+    "drafts": dict(groups=[(600, 4), (90, 3)], before=1, after=1, lens=[9, 6, 30, 17, 6, 60, 8, 6, 25], nq=[6] * 9, Hq=16,
+                   Hkv=2, D=64, bs=16, tree=True),
+    "many drafts": dict(groups=[(300, 3)], before=0, after=0, lens=[40, 33, 64], nq=[40, 32, 33], Hq=4, Hkv=2, D=64, bs=32,
+                        tree=True),
+    "prompt": dict(groups=[(513, 2)], before=0, after=0, lens=[200, 131], nq=[200, 131], Hq=8, Hkv=2, D=128, bs=64),
+    "small heads": dict(groups=[(200, 5)], before=0, after=0, lens=[1, 2, 3, 4, 5], nq=[1] * 5, Hq=10, Hkv=2, D=16, bs=16),
+    "heads of 80": dict(groups=[(333, 9)], before=1, after=0, lens=list(range(1, 11)), nq=[1] * 10, Hq=4, Hkv=1, D=80,
+                        bs=16),
+    "heads of 96": dict(groups=[(1500, 40)], before=0, after=0, lens=[3] * 40, nq=[1] * 40, Hq=8, Hkv=2, D=96, bs=80),
+    "heads of 208": dict(groups=[(400, 7)], before=0, after=1, lens=[11] * 8, nq=[1] * 8, Hq=6, Hkv=3, D=208, bs=32),
+    "heads of 256": dict(groups=[(1000, 20), (50, 2)], before=0, after=0, lens=[5] * 22, nq=[2] * 22, Hq=4, Hkv=2, D=256,
+                         bs=16),
+    "many groups": dict(groups=[(10 + 7 * i, 1 + i % 3) for i in range(60)], before=0, after=0, lens=[2] * 120,
+                        nq=[1] * 120, Hq=4, Hkv=2, D=64, bs=16),
+}
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("name", SHARED)
+def test_shared_attention(q, name, fmt):
+    b = Shared(len(name), fmt, **SHARED[name])
+    a = b.args()
+    b.check(q.attn_kv8_shared(**a))
+    b.check(q.attn_kv8_shared(**a, softmax_scale=0.5 * b.D ** -0.5), scale=0.5 * b.D ** -0.5)
+
+
+def test_shared_attention_rows_that_see_nothing(q):
+    """No prefix tokens and no own ones, or a tree's word of none: zeros; rows behind the last request stay."""
+    b = Shared(1, "i8", [(0, 2), (5, 1)], 1, 0, [0, 0, 3, 0], [1, 1, 2, 1], 4, 2, 128, 16, tree=True, spare_rows=3)
+    b.tree[1:4] = 0
+    a = b.args()
+    out = torch.full((8, 4, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+    got = q.attn_kv8_shared(**a, out=out)
+    assert got.data_ptr() == out.data_ptr()
+    b.check(out[:5].clone() if b.q.shape[0] == 5 else torch.cat((out[:5], torch.zeros((3, 4, 128), device=DEV))))
+    assert not out[:2].any() and (out[5:] == 9.0).all()
+    # request 2 has one own token before its two drafts, which see it alone; request 3 sees the prefix alone
+    assert out[2:5].any()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_shared_attention_garbage_behind_the_ends(q, D):
+    """Slots past a prefix's or a context's end hold NaN codes; one query row is NaN, one infinite, one huge."""
+    b = Shared(2, "e4m3", [(100, 6)], 0, 1, [5, 1, 17, 2, 2, 2, 40], [1] * 7, 4, 2, D, 64)
+    for row, n in [(b.ptable[0], 100)] + list(zip(b.table, b.lens)):
+        blk = row[n // 64] if n % 64 else -1
+        if blk >= 0:
+            b.k[blk][:, n % 64:] = 0x7F
+            b.v[blk][:, n % 64:] = 0xFF
+    b.q[1, 0, 3] = float("nan")
+    b.q[2, 1, 0] = float("inf")
+    b.q[3, 2] *= 1e30
+    a = b.args()
+    out = q.attn_kv8_shared(**a)
+    clean = b.q.clone()
+    clean[1, 0, 3] = clean[2, 1, 0] = 0
+    clean[3, 2] = 0
+    assert out[1, 0].isnan().all() and out[2, 1].isnan().all()
+    b.q, full = clean, b.q
+    ref = out.clone()
+    ref[1, 0], ref[2, 1], ref[3, 2] = 0, 0, 0
+    want = q.attn_kv8_shared(**{**a, "q": clean.to(DEV)})
+    b.check(want)
+    for t in range(7):
+        for h in range(4):
+            if (t, h) not in ((1, 0), (2, 1), (3, 2)):
+                assert torch.equal(out[t, h], want[t, h]), (t, h)
+
+
+def test_shared_attention_is_attention_over_both(q):
+    """A prefix of whole blocks against attn_kv8_paged over the joined block lists, and no groups' requests at all."""
+    b = Shared(3, "i8", [(512, 9)], 0, 0, [1 + 3 * i for i in range(9)], [1] * 9, 8, 2, 128, 16)
+    a = b.args()
+    table = i32(np.concatenate((np.repeat(b.ptable[:, :32], 9, 0), b.table), 1))
+    both = q.attn_kv8_paged(a["q"], a["k_cache"], a["v_cache"], a["scales"], table, i32(np.array(b.lens) + 512), a["cu_q"])
+    got = q.attn_kv8_shared(**a)
+    assert (both.float() - got.float()).abs().max() <= 2.0 ** -6 * both.float().abs().max()
+    none = q.attn_kv8_shared(**{**a, "cu_req": i32([9, 9])})
+    alone = q.attn_kv8_paged(a["q"], a["k_cache"], a["v_cache"], a["scales"], a["block_table"], a["ctx_lens"], a["cu_q"])
+    assert (none.float() - alone.float()).abs().max() <= 2.0 ** -8 * alone.float().abs().max()
+
+
+def test_shared_attention_strides_streams_and_capture(q):
+    b = Shared(4, "e4m3", [(700, 30), (90, 4)], 1, 1, [1 + i for i in range(36)], [1] * 36, 8, 2, 128, 16)
+    a = b.args()
+    want = q.attn_kv8_shared(**a)
+    b.check(want)
+    # a slice of a fused row, on a stream of its own
+    row = torch.zeros((36, 12 * 128 + 8), dtype=torch.bfloat16, device=DEV)
+    row[:, 128:9 * 128] = a["q"].flatten(1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = q.attn_kv8_shared(**{**a, "q": row[:, 128:9 * 128].unflatten(1, (8, 128))}, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    # two graphs on one stream, replayed on others beside one another and an eager call
+    graphs, outs = [], []
+    for _ in range(2):
+        out = torch.empty_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q.attn_kv8_shared(**a, out=out)
+        graphs.append(g), outs.append(out)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        eager = q.attn_kv8_shared(**a)
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want) and torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+def test_shared_attention_reports(q):
+    """Block ids outside the cache count as unseen; lengths past the table are cut; bounds that do not ascend write nothing."""
+    b = Shared(5, "i8", [(300, 5)], 0, 1, [4] * 6, [1] * 6, 4, 2, 128, 16)
+    b.ptable[0, 3], b.ptable[0, 7], b.table[2, 0] = -5, 10 ** 6, 10 ** 6
+    a = b.args()
+    b.check(q.attn_kv8_shared(**a))
+    assert q.device_error(clear=True) >> 8 == 6
+    b = Shared(5, "i8", [(300, 5)], 0, 1, [4] * 6, [1] * 6, 4, 2, 128, 16)
+    b.plens = [10 ** 6]
+    for row in b.ptable:
+        row[row < 0] = 0
+    b.check(q.attn_kv8_shared(**b.args()))
+    assert q.device_error(clear=True) == 0x603
+    b = Shared(5, "i8", [(300, 2), (40, 3)], 0, 1, [4] * 6, [1] * 6, 4, 2, 128, 16)
+    a = b.args()
+    for bad in (dict(cu_req=i32([0, 3, 2])), dict(cu_req=i32([-1, 2, 5])), dict(cu_req=i32([0, 2, 7])),
+                dict(cu_q=i32([0, 1, 2, 1, 4, 5, 6])), dict(cu_q=i32([0, 1, 2, 3, 4, 5, 7]))):
+        out = torch.full((6, 4, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+        q.attn_kv8_shared(**{**a, **bad}, out=out)
+        assert (out == 9.0).all()
+        assert q.device_error(clear=True) == 0x604
+    b.check(q.attn_kv8_shared(**a))
+
+
+def test_shared_attention_refusals(q):
+    b = Shared(6, "i8", [(30, 2)], 0, 0, [4] * 2, [1] * 2, 4, 2, 128, 16)
+    a = b.args()
+    for bad in (dict(q=a["q"].float()), dict(q=a["q"][..., :64]), dict(prefix_table=a["prefix_table"].long()),
+                dict(prefix_lens=i32([3, 4])), dict(cu_req=i32([0])), dict(ctx_lens=i32([1])), dict(cu_q=i32([0, 1])),
+                dict(tree_mask=i32([1])), dict(out=torch.zeros((2, 4, 128), device=DEV)),
+                dict(block_table=a["block_table"][:1]), dict(prefix_lens=a["prefix_lens"].cpu())):
+        with pytest.raises(ValueError):
+            q.attn_kv8_shared(**{**a, **bad})
+    with pytest.raises(q.QGError):
+        q.attn_kv8_shared(**a, workspace=torch.zeros(4096, dtype=torch.uint8, device=DEV))
+    with pytest.raises(q.QGError):
+        q.attn_kv8_shared(**a, softmax_scale=-1.0)
