@@ -1,0 +1,563 @@
+// Attention of the query rows of whole groups over their shared prefixes in the
+// paged 8-bit cache, heads of up to 128 elements, on the 5th-generation tensor cores.
+//
+//   S [128 rows][128 tokens] = q K^T   A = the queries, B = the keys, both fp16 in
+//                                      shared memory (codes and queries are exact)
+//   P = 2^(S ks f + log2 vs - m)       a thread per query row: f the row's scale,
+//                                      ks, vs the scales of the token's block
+//   O [128 rows][D] += P V             A = P as fp16 in tensor memory, over the S that
+//                                      it came from; B = the values, token-major
+// There is no mask but the prefix's end: a step's tokens are seen by all rows, so
+// rows stand across a CTA's lanes (S^T, as in attn_kv8_tc.cu, would need a vote
+// on maxima across threads). m moves only where a score outgrows it by 2^8.
+//
+// An item is up to 256 rows of a key/value head; its steps go through two streams of
+// MMAs and softmax warps that take turns on the tensor cores. With more than 128
+// rows a stream is half of the rows, and both use a step's converted keys and
+// values; with fewer the streams take every other step for the same rows and are
+// added up at the end (one stream alone would wait for its own softmax half of the
+// time).
+//
+// Warps: 0-3 and 4-7 softmax of the streams, 8-11 copy and convert, 12 looks up
+// blocks and scales, 13 issues the MMAs. Codes go from global memory through
+// registers to fp16 tiles: staged by TMA they would cross shared memory twice more
+// (64 of 320 KB a step, whose 128 bytes a cycle the MMAs' operands need).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "attn_kv8.cuh"
+#include "attn_prefix.cuh"
+#include "attn_tc.cuh"
+#include "kv8.cuh"
+#include "qg_common.cuh"
+#include "qg_internal.h"
+
+namespace qg {
+namespace {
+
+constexpr int kThreads = 448;
+constexpr int kSlots = 8;       // steps whose blocks and scales are kept
+constexpr int kRowsTile = 128;  // rows of a stream's MMAs
+constexpr int kUnits = kPrefixTok / kUnit;
+constexpr int TOK = kPrefixTok;
+
+// DP: elements that a head is filled up to (64 or 128)
+template <int DP>
+struct PrefixShape {
+  static constexpr int kHalves = DP / 64;            // 64-element blocks of a tile's rows
+  static constexpr int kTile = TOK * DP * 2;         // 128 rows (tokens or queries) as fp16
+  static constexpr int kBlock = TOK * 128;           // one 64-element block of them
+  static constexpr int kTokens = 32 / kHalves;       // tokens of a load of all converters
+  static constexpr int kLoads = TOK / kTokens;
+  static constexpr int kSmem = 6 * kTile;            // two of queries, keys and values each
+  static constexpr uint32_t kColS = 0, kColO = 256;  // tensor memory columns: S0, S1, O0, O1, 128 apart
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(t));
+}
+// two waits' worth of operands: orders later uses of v[0..31] after the loads
+__device__ __forceinline__ void tmem_wait_ld32(float* v) {
+  tmem_wait_ld(v);
+  tmem_wait_ld(v + 16);
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t t, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+template <int FMT, int DP>
+__global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a, uint8_t* pieces) {
+  using S = PrefixShape<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3;
+  uint8_t* qbuf = smem;
+  uint8_t* kbuf = qbuf + 2 * S::kTile;
+  uint8_t* vbuf = kbuf + 2 * S::kTile;
+  int* first = reinterpret_cast<int*>(vbuf + 2 * S::kTile);
+  int* cost = first + a.R + 1;
+  int* cus = cost + a.R + 1;
+  int* ctxs = cus + a.R + 1;
+  __shared__ long long unit_at[kSlots][kUnits];     // element of the unit's first token in the cache, -1: not there
+  __shared__ float4 unit_scales[kSlots][kUnits];    // key scale, log2 of the value scale, 2^-that, kind
+  __shared__ uint64_t found[kSlots], spent[kSlots];  // a step's slot has been written; its values have been multiplied
+  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], s_full[2], p_ready[2], q_full, o_done;
+  __shared__ int2 scan_part[kThreads / 32];
+  __shared__ float2 other[kRowsTile];  // the second stream's maxima and sums
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile uint32_t abort_flag;
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(found + i, 1), mbar_init(spent + i, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 4), mbar_init(v_full + i, 4);
+      mbar_init(k_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + i, 4);
+    }
+    mbar_init(&q_full, 8);
+    mbar_init(&o_done, 1);
+    abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  tc_before();
+  const AttnBatch batch = attn_scan<kPrefixRows, PrefixCut, kThreads, true>(a, first, cost, cus, ctxs, scan_part);
+  tc_after();
+  const AttnShare share = attn_share<PrefixCut>(batch, a.err);
+  const uint32_t tbase = tmem_base;
+
+  // by a whole warp, which goes on together
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+           __all_sync(0xffffffffu, tc_wait_on(bar, parity, &abort_flag, a.err));
+  };
+  // A segment: the steps of one item in this CTA's share. Every role walks the segments by itself; the steps of the CTA
+  // are counted through (step g: buffers g & 1, slot g % kSlots).
+  struct Segment {
+    AttnPlace item;
+    int n, g, rows, tok0, index;
+  };
+  auto first_segment = [&]() {
+    Segment s;
+    s.n = s.g = 0;
+    s.index = -1;
+    return s;
+  };
+  auto next_segment = [&](Segment& s, int& step) {
+    step += s.n;
+    if (step >= share.c1) return false;
+    s.g += s.n;
+    ++s.index;
+    s.item = attn_locate<kPrefixRows, PrefixCut>(batch, step);
+    s.n = min(share.c1, step - s.item.s + s.item.steps) - step;
+    s.rows = min(kPrefixRows, (cus[s.item.r + 1] - cus[s.item.r]) * batch.G - s.item.rt * kPrefixRows);
+    s.tok0 = s.item.s * TOK;
+    return true;
+  };
+  int step = share.c0;
+  Segment sg = first_segment();
+
+  if (warp < 8) {
+    // ------------------------------------------------ softmax: a row per thread
+    const int stream = warp >> 2, r = quad * 32 + lane;
+    const uint32_t tlane = tbase + ((uint32_t)(quad * 32) << 16);
+    const uint32_t ts = tlane + S::kColS + 128 * stream, to = tlane + S::kColO + 128 * stream;
+    uint32_t passes = 0;  // of s_full[stream]
+    while (next_segment(sg, step)) {
+      const bool two = sg.rows > kRowsTile;
+      const int ctx = ctxs[sg.item.r], q0 = cus[sg.item.r];
+      const int rr = (two ? kRowsTile * stream : 0) + r;
+      const int rho = sg.item.rt * kPrefixRows + rr, qi = rho / batch.G;
+      const bool live = rr < sg.rows;
+      const size_t out_row = (size_t)(q0 + qi) * a.Hq + sg.item.h * batch.G + rho - qi * batch.G;
+      // the row as 2^-sigma q in fp16, exact, sigma from its largest finite element
+      float rf;
+      {
+        uint4 raw[DP / 8];
+        const uint16_t* src =
+            a.q + (size_t)(q0 + qi) * a.q_stride + (size_t)(sg.item.h * batch.G + rho - qi * batch.G) * a.D;
+        unsigned most = 0u;
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+          raw[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (live && 8 * j < a.D) raw[j] = *reinterpret_cast<const uint4*>(src + 8 * j);
+        }
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const unsigned lo = w[k] << 16 & 0x7FFF0000u, hi = w[k] & 0x7FFF0000u;
+            most = max(most, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+          }
+        }
+        const int sigma = fp16_prescale_exp(__uint_as_float(most));
+        const float down = pow2f(-sigma);
+        rf = a.scale_log2 * pow2f(sigma);
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            f[k] = f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          sts128(smem_u32(qbuf) + stream * S::kTile + (j >> 3) * S::kBlock + r * 128 + (((j & 7) ^ (r & 7)) << 4),
+                 make_uint4(f[0], f[1], f[2], f[3]));
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
+      float m = kNoMax, l = 0.f;
+      bool begun = false;
+#pragma unroll 1
+      for (int i = two ? 0 : stream; i < sg.n; i += two ? 1 : 2) {
+        const int g = sg.g + i, slot = g % kSlots;
+        wait_warp(found + slot, g / kSlots & 1);
+        wait_warp(s_full + stream, passes & 1);
+        ++passes;
+        tc_after();
+        const int seen = ctx - (sg.tok0 + i * TOK);  // tokens of the step, if not all
+        const float4* us = unit_scales[slot];
+        // the step's largest score
+        float top = kNoMax;
+#pragma unroll
+        for (int c = 0; c < TOK / 32; ++c) {
+          float s[32];
+          tmem_ld32(ts + 32 * c, s);
+          tmem_wait_ld32(s);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float4 sc = us[2 * c + u];
+            float x[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
+            if (seen < 32 * c + 16 * u + 16) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (32 * c + 16 * u + j < seen) x[j & 3] = fmaxf(x[j & 3], s[16 * u + j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j & 3] = fmaxf(x[j & 3], s[16 * u + j]);
+            }
+            if (sc.w != 0.f) {
+              const float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+              if (y != kNoMax) top = fmaxf(top, fmaf(y, sc.x * rf, sc.y));
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, top - m > kSlack)) {
+          const float mn = fmaxf(m, top), f = ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (begun) {  // (the stream's last product has been waited for with this S)
+#pragma unroll 1
+            for (int c = 0; c < DP / 32; ++c) {
+              float o[32];
+              tmem_ld32(to + 32 * c, o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= f;
+              tmem_st16(to + 32 * c, *reinterpret_cast<float(*)[16]>(o));
+              tmem_st16(to + 32 * c + 16, *reinterpret_cast<float(*)[16]>(o + 16));
+            }
+          }
+        }
+        begun = true;
+        // p, its sum without the value scale, and as fp16 where the scores were (the first half of them has been read by
+        // then)
+#pragma unroll
+        for (int c = 0; c < TOK / 32; ++c) {
+          float s[32];
+          uint32_t p[16];
+          tmem_ld32(ts + 32 * c, s);
+          tmem_wait_ld32(s);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float4 sc = us[2 * c + u];
+            const uint64_t f2 = both(sc.x * rf), b2 = both(sc.y - m);
+            uint64_t sum = 0ull;
+            const bool edge = seen < 32 * c + 16 * u + 16 || sc.w == 0.f;
+            float e[16];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              float y0, y1;
+              unpair2(ffma2(pair2(__float_as_uint(s[16 * u + j]), __float_as_uint(s[16 * u + j + 1])), f2, b2), y0, y1);
+              e[j] = ex2(y0), e[j + 1] = ex2(y1);
+            }
+            if (edge) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (sc.w == 0.f || 32 * c + 16 * u + j >= seen) e[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              sum = fadd2(sum, pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])));
+              p[8 * u + j / 2] = f16x2(e[j], e[j + 1]);
+            }
+            if (sc.w == 2.f) {  // a block of zero scale: only the probabilities count
+#pragma unroll
+              for (int j = 0; j < 8; ++j) p[8 * u + j] = 0u;
+            }
+            float s0, s1;
+            unpair2(sum, s0, s1);
+            l = fmaf(s0 + s1, sc.z, l);
+          }
+          tmem_st16u(ts + 16 * c, p);
+        }
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready + stream);
+      }
+      // ---- the segment's results ----
+      wait_warp(&o_done, sg.index & 1);
+      tc_after();
+      float w0 = 1.f, w1 = 0.f;  // weights of the streams' outputs
+      if (!two) {
+        if (stream == 1) other[r] = make_float2(m, l);
+        named_barrier<256>(1);
+        if (stream == 0) {
+          const float2 x = other[r];
+          const float mn = fmaxf(m, x.x);
+          w0 = ex2(m - mn), w1 = ex2(x.x - mn);
+          l = fmaf(x.y, w1, l * w0);
+          m = mn;
+        }
+      }
+      const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+      w0 *= inv, w1 *= inv;
+      const bool second = !two && sg.n > 1;  // (the streams' outputs are sums from their first step on)
+      if (two || stream == 0) {
+        const int item_first = step - sg.item.s;
+        const bool whole = item_first >= share.c0 && item_first + sg.item.steps <= share.c1;
+        uint8_t* piece = prefix_piece(pieces, blockIdx.x, item_first < share.c0 ? 0 : 1, a.D);
+        float* dst = whole ? a.part_o + out_row * a.D : reinterpret_cast<float*>(piece) + (size_t)rr * a.D;
+        if (live) {
+          float2* ml = whole ? a.part_ml + out_row : reinterpret_cast<float2*>(piece + (size_t)kPrefixRows * a.D * 4) + rr;
+          *ml = make_float2(m, l);
+        }
+#pragma unroll 1
+        for (int c = 0; c < DP / 16; ++c) {
+          float o[16];
+          tmem_ld16(to + 16 * c, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = inv == 0.f ? 0.f : o[j] * w0;
+          if (second) {
+            float x[16];
+            tmem_ld16(to + 128 + 16 * c, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = fmaf(x[j], w1, o[j]);
+          }
+          if (live && 16 * c < a.D) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              *reinterpret_cast<float4*>(dst + 16 * c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+        }
+      }
+      tc_before();
+      named_barrier<256>(1);  // both streams' outputs and `other` have been read
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------ keys and values: 16 codes a thread and load, as fp16 tiles
+    const int t = tid - 256, ch = t & 3, tk = t >> 2 & (S::kTokens - 1), half = S::kHalves == 2 ? t >> 6 : 0;
+    const int e = half * 64 + ch * 16;
+    const bool in = e < a.D;
+    const uint8_t *kc = static_cast<const uint8_t*>(a.k_cache), *vc = static_cast<const uint8_t*>(a.v_cache);
+    uint4 kr[S::kLoads], vr[S::kLoads];
+    // (a slot's addresses, then the loads: what is not there counts as zeros)
+    auto fetch = [&](const uint8_t* cache, uint4(&raw)[S::kLoads], int g, int seen) {
+      const long long* at = unit_at[g % kSlots];
+#pragma unroll
+      for (int k = 0; k < S::kLoads; ++k) {
+        const int tok = k * S::kTokens + tk;
+        const long long base = at[tok / kUnit];
+        raw[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (base >= 0 && in && tok < seen)
+          raw[k] = *reinterpret_cast<const uint4*>(cache + base + (tok % kUnit) * a.D + e);
+      }
+    };
+    // rows of 64 elements, 16-byte chunks swizzled; neighbouring lanes are the four chunk pairs of two tokens: no conflicts
+    auto store = [&](uint8_t* tile, const uint4(&raw)[S::kLoads]) {
+      const uint32_t dst = smem_u32(tile) + half * S::kBlock;
+#pragma unroll
+      for (int k = 0; k < S::kLoads; ++k) {
+        const int tok = k * S::kTokens + tk;
+        uint4 f[2];
+        codes_to_f16<FMT>(raw[k].x, f[0].x, f[0].y);
+        codes_to_f16<FMT>(raw[k].y, f[0].z, f[0].w);
+        codes_to_f16<FMT>(raw[k].z, f[1].x, f[1].y);
+        codes_to_f16<FMT>(raw[k].w, f[1].z, f[1].w);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sts128(dst + tok * 128 + (((2 * ch + j) ^ (tok & 7)) << 4), f[j]);
+      }
+      fence_async_smem();
+      __syncwarp();
+    };
+    // the walk of the loads, a step ahead of the stores
+    Segment ahead = first_segment();
+    int ahead_step = share.c0, ai = 0, ag = 0, aseen = 0;
+    bool more = next_segment(ahead, ahead_step), ok = true;
+    auto look = [&]() {  // the next step to load: its number and tokens
+      ag = ahead.g + ai;
+      aseen = ctxs[ahead.item.r] - (ahead.tok0 + ai * TOK);
+      return wait_warp(found + ag % kSlots, ag / kSlots & 1);
+    };
+    auto advance = [&]() {
+      if (++ai == ahead.n) ai = 0, more = next_segment(ahead, ahead_step);
+    };
+    if (more) {
+      ok = look();
+      if (ok) fetch(kc, kr, ag, aseen), fetch(vc, vr, ag, aseen);
+      advance();
+    }
+    for (int g = 0, left = share.c1 - share.c0; ok && g < left; ++g) {
+      const int b = g & 1;
+      const bool next = more;
+      ok = g < 2 || wait_warp(k_empty + b, ((g >> 1) - 1) & 1);
+      if (!ok) break;
+      store(kbuf + b * S::kTile, kr);
+      if (lane == 0) mbar_arrive(k_full + b);
+      if (next) {
+        ok = look();
+        if (!ok) break;
+        fetch(kc, kr, ag, aseen);
+      }
+      ok = g < 2 || wait_warp(spent + (g - 2) % kSlots, (g - 2) / kSlots & 1);
+      if (!ok) break;
+      store(vbuf + b * S::kTile, vr);
+      if (lane == 0) mbar_arrive(v_full + b);
+      if (next) {
+        fetch(vc, vr, ag, aseen);
+        advance();
+      }
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------ a lane per unit of 16 tokens: its block and the block's scales
+    const float2* scales = reinterpret_cast<const float2*>(a.scales);
+    bool ok = true;
+    while (ok && next_segment(sg, step)) {
+      const int ctx = ctxs[sg.item.r];
+      auto look = [&](int i) {
+        const int tok = sg.tok0 + i * TOK + lane * kUnit;
+        int blk = -1;
+        if (i < sg.n && lane < kUnits && tok < ctx) {
+          blk = a.table[(size_t)sg.item.r * a.max_blocks + tok / a.bs];
+          if (blk < 0 || blk >= a.num_blocks) {
+            report_error(a.err, kErrKvBlock);
+            blk = -1;
+          }
+        }
+        return blk;
+      };
+      auto scales_of = [&](int blk) {
+        return blk >= 0 ? scales[(size_t)blk * a.Hkv + sg.item.h] : make_float2(0.f, 1.f);
+      };
+      int blk = look(0), next = look(1);
+      float2 sc = scales_of(blk);
+#pragma unroll 1
+      for (int i = 0; i < sg.n; ++i) {
+        const int g = sg.g + i, slot = g % kSlots;
+        ok = g < kSlots || wait_warp(spent + slot, (g / kSlots - 1) & 1);
+        if (!ok) break;
+        if (lane < kUnits) {
+          const int row = (sg.tok0 + i * TOK + lane * kUnit) % a.bs;
+          unit_at[slot][lane] = blk < 0 ? -1 : (((long long)blk * a.Hkv + sg.item.h) * a.bs + row) * a.D;
+          // a value scale below 2^-64 counts as 2^-64; what comes off the sum is what went on
+          const float lv = __log2f(sc.y < kMinScale ? kMinScale : sc.y);
+          unit_scales[slot][lane] = make_float4(sc.x, lv, ex2(-lv), blk < 0 ? 0.f : sc.y == 0.f ? 2.f : 1.f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(found + slot);
+        blk = next;
+        next = look(i + 2);
+        sc = scales_of(blk);
+      }
+    }
+  } else {
+    // ------------------------------------------------ MMAs
+    // What decides the loops and forms the operands is taken from lane 0, so that it stays in uniform registers.
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t one = lane == 0, is = tc_idesc(128, TOK, false, false), io = tc_idesc(128, DP, false, true);
+    const uint32_t tb = uniform(tbase);
+    const uint64_t qd = tc_desc(uniform(smem_u32(qbuf)), 16, 1024), kd = tc_desc(uniform(smem_u32(kbuf)), 16, 1024),
+                   vd = tc_desc(uniform(smem_u32(vbuf)), S::kBlock, 1024);
+    uint32_t passes[2] = {0u, 0u};  // of p_ready
+    bool ok = true;
+    while (ok && __all_sync(0xffffffffu, next_segment(sg, step))) {
+      const int n = uniform(sg.n), gi = uniform(sg.g), two = uniform(sg.rows > kRowsTile);
+      const int events = two ? 2 * n : n;  // event x: stream x & 1, of step x / 2 or x
+      auto issue_s = [&](int x) {
+        const int t = x & 1, g = gi + (two ? x >> 1 : x), b = g & 1;
+        if (!wait_warp(k_full + b, (g >> 1) & 1)) return false;
+        tc_after();
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t at = ((k >> 2) * S::kBlock + (k & 3) * 32) >> 4;
+          mma_ss(tb + S::kColS + 128 * t, qd + at + (t * S::kTile >> 4), kd + at + (b * S::kTile >> 4), is, k > 0, one);
+        }
+        if (one) {
+          tc_commit(s_full + t);
+          if (!two || t == 1) tc_commit(k_empty + b);
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = wait_warp(&q_full, uniform(sg.index) & 1);
+      if (!ok) break;
+      tc_after();
+      ok = issue_s(0) && (events < 2 || issue_s(1));
+#pragma unroll 1
+      for (int x = 0; ok && x < events; ++x) {
+        const int t = x & 1, g = gi + (two ? x >> 1 : x), b = g & 1;
+        ok = wait_warp(p_ready + t, passes[t] & 1) && wait_warp(v_full + b, (g >> 1) & 1);
+        if (!ok) break;
+        ++passes[t];
+        tc_after();
+#pragma unroll
+        for (int k = 0; k < TOK / 16; ++k)
+          mma_ts(tb + S::kColO + 128 * t, tb + S::kColS + 128 * t + 8 * k, vd + ((b * S::kTile + k * 2048) >> 4), io,
+                 k > 0 ? 1u : x > 1, one);
+        if (one && (!two || t == 1)) tc_commit(spent + g % kSlots);
+        __syncwarp();
+        if (x + 2 < events) ok = issue_s(x + 2);
+      }
+      if (one) tc_commit(&o_done);
+      __syncwarp();
+    }
+  }
+  // After a wait that gave up: the products in flight end before the memory is given back (a bounded wait).
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 13) {
+    if (abort_flag) {
+      if (lane == 0) {
+        tc_commit(&o_done);
+        for (int ph = 0; ph < 2; ++ph) mbar_wait_n(&o_done, ph, nullptr, 0, 1u << 14);
+      }
+      __syncwarp();
+    }
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512u));
+  }
+}
+
+template <int FMT, int DP>
+cudaError_t launch(const AttnArgs& a, uint8_t* pieces, int ctas, cudaStream_t stream, bool pdl) {
+  auto k = attn_kv8_prefix_kernel<FMT, DP>;
+  const cudaError_t e = allow_max_smem(k);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(k, dim3(ctas), dim3(kThreads), PrefixShape<DP>::kSmem + 16 * ((size_t)a.R + 1), stream, pdl, a,
+                       pieces);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_kv8_prefix(const AttnArgs& a, int format, uint8_t* pieces, int ctas, cudaStream_t stream,
+                                   bool pdl) {
+  if (format == QG_KV_I8)
+    return a.D <= 64 ? launch<QG_KV_I8, 64>(a, pieces, ctas, stream, pdl) : launch<QG_KV_I8, 128>(a, pieces, ctas, stream, pdl);
+  return a.D <= 64 ? launch<QG_KV_E4M3, 64>(a, pieces, ctas, stream, pdl)
+                   : launch<QG_KV_E4M3, 128>(a, pieces, ctas, stream, pdl);
+}
+
+}  // namespace qg

@@ -318,6 +318,9 @@ cudaError_t launch_attn_kv8_tc(const AttnArgs& a, int format, cudaStream_t strea
 // attention of requests whose groups share a prefix (attn_kv8_shared.cu): own has every request's own context, pre every
 // group's prefix (R, table, ctx_lens, max_blocks, cu_req)
 size_t attn_kv8_shared_workspace_size(int T, int Hq, int Hkv, int D);
+// the prefixes' part for heads of up to 128, on tcgen05; pieces of what several CTAs share: attn_prefix.cuh
+cudaError_t launch_attn_kv8_prefix(const AttnArgs& a, int format, uint8_t* pieces, int ctas, cudaStream_t stream,
+                                   bool pdl);
 cudaError_t launch_attn_kv8_shared(const AttnArgs& own, const AttnArgs& pre, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t stream, bool pdl);
 cudaError_t launch_qk_rope(const RopeArgs& a, cudaStream_t stream, bool pdl);
