@@ -69,16 +69,10 @@ __device__ __forceinline__ void tmem_wait_ld32(float* v) {
   tmem_wait_ld(v);
   tmem_wait_ld(v + 16);
 }
-__device__ __forceinline__ void tmem_st16u(uint32_t t, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
+constexpr float kMostMass = 256.f;  // sum of a step's p up to which its maximum stays: fp16 holds 2^15
 
 template <int FMT, int DP>
-__global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a, uint8_t* pieces) {
+__global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a, uint8_t* pieces, int2* source) {
   using S = PrefixShape<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3;
@@ -91,7 +85,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
   int* ctxs = cus + a.R + 1;
   __shared__ long long unit_at[kSlots][kUnits];     // element of the unit's first token in the cache, -1: not there
   __shared__ float4 unit_scales[kSlots][kUnits];    // key scale, log2 of the value scale, 2^-that, kind
-  __shared__ uint64_t found[kSlots], spent[kSlots];  // a step's slot has been written; its values have been multiplied
+  // a step's blocks, its scales have been written; its values have been multiplied
+  __shared__ uint64_t found[kSlots], scaled[kSlots], spent[kSlots];
   __shared__ uint64_t k_full[2], k_empty[2], v_full[2], s_full[2], p_ready[2], q_full, o_done;
   __shared__ int2 scan_part[kThreads / 32];
   __shared__ float2 other[kRowsTile];  // the second stream's maxima and sums
@@ -99,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
   __shared__ volatile uint32_t abort_flag;
 
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(found + i, 1), mbar_init(spent + i, 1);
+    for (int i = 0; i < kSlots; ++i) mbar_init(found + i, 1), mbar_init(scaled + i, 1), mbar_init(spent + i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4), mbar_init(v_full + i, 4);
       mbar_init(k_empty + i, 1);
@@ -211,96 +206,97 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
 #pragma unroll 1
       for (int i = two ? 0 : stream; i < sg.n; i += two ? 1 : 2) {
         const int g = sg.g + i, slot = g % kSlots;
-        wait_warp(found + slot, g / kSlots & 1);
+        wait_warp(scaled + slot, g / kSlots & 1);
         wait_warp(s_full + stream, passes & 1);
         ++passes;
         tc_after();
         const int seen = ctx - (sg.tok0 + i * TOK);  // tokens of the step, if not all
         const float4* us = unit_scales[slot];
-        // the step's largest score
-        float top = kNoMax;
+        uint32_t p[TOK / 2];
+        // p of the step against the maximum so far, and its sum without the value scale
+        auto probabilities = [&](float& mass) {
+          float part = 0.f;
+          mass = 0.f;
 #pragma unroll
-        for (int c = 0; c < TOK / 32; ++c) {
-          float s[32];
-          tmem_ld32(ts + 32 * c, s);
-          tmem_wait_ld32(s);
+          for (int h = 0; h < 2; ++h) {
+            float s[64];
+            tmem_ld32(ts + 64 * h, s);
+            tmem_ld32(ts + 64 * h + 32, s + 32);
+            tmem_wait_ld32(s);
+            tmem_wait_ld32(s + 32);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float4 sc = us[2 * c + u];
-            float x[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
-            if (seen < 32 * c + 16 * u + 16) {
+            for (int v = 0; v < 4; ++v) {
+              const int u = 4 * h + v;
+              const float4 sc = us[u];
+              const uint64_t f2 = both(sc.x * rf), b2 = both(sc.y - m);
+              uint64_t sum = 0ull;
+              float* e = s + 16 * v;
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (32 * c + 16 * u + j < seen) x[j & 3] = fmaxf(x[j & 3], s[16 * u + j]);
-            } else {
+              for (int j = 0; j < 16; j += 2) {
+                float y0, y1;
+                unpair2(ffma2(pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])), f2, b2), y0, y1);
+                e[j] = ex2(y0), e[j + 1] = ex2(y1);
+              }
+              if (seen < 16 * u + 16 || sc.w == 0.f) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) x[j & 3] = fmaxf(x[j & 3], s[16 * u + j]);
-            }
-            if (sc.w != 0.f) {
-              const float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-              if (y != kNoMax) top = fmaxf(top, fmaf(y, sc.x * rf, sc.y));
+                for (int j = 0; j < 16; ++j)
+                  if (sc.w == 0.f || 16 * u + j >= seen) e[j] = 0.f;
+              }
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                sum = fadd2(sum, pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])));
+                p[8 * u + j / 2] = f16x2(e[j], e[j + 1]);
+              }
+              if (sc.w == 2.f) {  // a block of zero scale: only the probabilities count
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[8 * u + j] = 0u;
+              }
+              float s0, s1;
+              unpair2(sum, s0, s1);
+              mass += s0 + s1;
+              part = fmaf(s0 + s1, sc.z, part);
             }
           }
-        }
-        if (__any_sync(0xffffffffu, top - m > kSlack)) {
+          return part;
+        };
+        // Where the step's sum is at most 2^8 so is every p, and m stays (a pass over the scores for their maximum, in
+        // every step, took as long as the exponentials). Otherwise m rises to the largest score, and p is formed anew.
+        float mass, part = probabilities(mass);
+        if (__any_sync(0xffffffffu, mass > kMostMass)) {
+          float top = kNoMax;
+#pragma unroll 1
+          for (int u = 0; u < kUnits; ++u) {
+            const float4 sc = us[u];
+            float s[16];
+            tmem_ld16(ts + 16 * u, s);
+            tmem_wait_ld(s);
+            float x = kNoMax;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (16 * u + j < seen) x = fmaxf(x, s[j]);
+            if (sc.w != 0.f && x != kNoMax) top = fmaxf(top, fmaf(x, sc.x * rf, sc.y));
+          }
           const float mn = fmaxf(m, top), f = ex2(m - mn);
           m = mn;
           l *= f;
           if (begun) {  // (the stream's last product has been waited for with this S)
 #pragma unroll 1
-            for (int c = 0; c < DP / 32; ++c) {
-              float o[32];
-              tmem_ld32(to + 32 * c, o);
-              tmem_wait_ld32(o);
+            for (int c = 0; c < DP / 16; ++c) {
+              float o[16];
+              tmem_ld16(to + 16 * c, o);
+              tmem_wait_ld(o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] *= f;
-              tmem_st16(to + 32 * c, *reinterpret_cast<float(*)[16]>(o));
-              tmem_st16(to + 32 * c + 16, *reinterpret_cast<float(*)[16]>(o + 16));
+              for (int j = 0; j < 16; ++j) o[j] *= f;
+              tmem_st16(to + 16 * c, o);
             }
           }
+          part = probabilities(mass);
         }
         begun = true;
-        // p, its sum without the value scale, and as fp16 where the scores were (the first half of them has been read by
-        // then)
-#pragma unroll
-        for (int c = 0; c < TOK / 32; ++c) {
-          float s[32];
-          uint32_t p[16];
-          tmem_ld32(ts + 32 * c, s);
-          tmem_wait_ld32(s);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float4 sc = us[2 * c + u];
-            const uint64_t f2 = both(sc.x * rf), b2 = both(sc.y - m);
-            uint64_t sum = 0ull;
-            const bool edge = seen < 32 * c + 16 * u + 16 || sc.w == 0.f;
-            float e[16];
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              float y0, y1;
-              unpair2(ffma2(pair2(__float_as_uint(s[16 * u + j]), __float_as_uint(s[16 * u + j + 1])), f2, b2), y0, y1);
-              e[j] = ex2(y0), e[j + 1] = ex2(y1);
-            }
-            if (edge) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (sc.w == 0.f || 32 * c + 16 * u + j >= seen) e[j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              sum = fadd2(sum, pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])));
-              p[8 * u + j / 2] = f16x2(e[j], e[j + 1]);
-            }
-            if (sc.w == 2.f) {  // a block of zero scale: only the probabilities count
-#pragma unroll
-              for (int j = 0; j < 8; ++j) p[8 * u + j] = 0u;
-            }
-            float s0, s1;
-            unpair2(sum, s0, s1);
-            l = fmaf(s0 + s1, sc.z, l);
-          }
-          tmem_st16u(ts + 16 * c, p);
-        }
+        l += part;
+        // over the first half of the scores
+        tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(p));
+        tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(p + 32));
         tmem_wait_st();
         tc_before();
         __syncwarp();
@@ -327,31 +323,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       if (two || stream == 0) {
         const int item_first = step - sg.item.s;
         const bool whole = item_first >= share.c0 && item_first + sg.item.steps <= share.c1;
+        const int last = whole ? 0 : attn_cta_of<PrefixCut>(batch, share, item_first + sg.item.steps - 1);
         uint8_t* piece = prefix_piece(pieces, blockIdx.x, item_first < share.c0 ? 0 : 1, a.D);
-        float* dst = whole ? a.part_o + out_row * a.D : reinterpret_cast<float*>(piece) + (size_t)rr * a.D;
         if (live) {
           float2* ml = whole ? a.part_ml + out_row : reinterpret_cast<float2*>(piece + (size_t)kPrefixRows * a.D * 4) + rr;
           *ml = make_float2(m, l);
+          if (item_first >= share.c0)  // the CTA that has the item's beginning says how many pieces it is in
+            source[out_row] = make_int2(blockIdx.x << 8 | rr, whole ? 1 : last - (int)blockIdx.x + 1);
         }
+        // 32 rows and elements of a warp at a time through the queries' place (their products are done), so that a row's
+        // 128 bytes are stored together
+        const uint32_t stage = smem_u32(qbuf) + warp * 4096;
+        const size_t first_row = (size_t)q0 * a.Hq + sg.item.h * batch.G;  // of the item's query rows, as out_row
 #pragma unroll 1
-        for (int c = 0; c < DP / 16; ++c) {
-          float o[16];
-          tmem_ld16(to + 16 * c, o);
-          tmem_wait_ld(o);
+        for (int c = 0; c < DP / 32; ++c) {
+          float o[32];
+          tmem_ld32(to + 32 * c, o);
+          tmem_wait_ld32(o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = inv == 0.f ? 0.f : o[j] * w0;
+          for (int j = 0; j < 32; ++j) o[j] = inv == 0.f ? 0.f : o[j] * w0;
           if (second) {
-            float x[16];
-            tmem_ld16(to + 128 + 16 * c, x);
-            tmem_wait_ld(x);
+            float x[32];
+            tmem_ld32(to + 128 + 32 * c, x);
+            tmem_wait_ld32(x);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = fmaf(x[j], w1, o[j]);
+            for (int j = 0; j < 32; ++j) o[j] = fmaf(x[j], w1, o[j]);
           }
-          if (live && 16 * c < a.D) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              *reinterpret_cast<float4*>(dst + 16 * c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          for (int j = 0; j < 8; ++j)
+            sts128(stage + lane * 128 + ((j ^ (lane & 7)) << 4),
+                   make_uint4(__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]), __float_as_uint(o[4 * j + 2]),
+                              __float_as_uint(o[4 * j + 3])));
+          __syncwarp();
+          const int e = 32 * c + 4 * (lane & 7);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int k = 4 * j + (lane >> 3), row = rr - lane + k;
+            const uint4 v = lds128(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
+            if (row < sg.rows && e < a.D) {
+              const int rho_k = sg.item.rt * kPrefixRows + row, qk = rho_k / batch.G;
+              float* dst = whole ? a.part_o + (first_row + (size_t)qk * a.Hq + rho_k - qk * batch.G) * a.D
+                                 : reinterpret_cast<float*>(piece) + (size_t)row * a.D;
+              *reinterpret_cast<uint4*>(dst + e) = v;
+            }
           }
+          __syncwarp();
         }
       }
       tc_before();
@@ -452,8 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       auto scales_of = [&](int blk) {
         return blk >= 0 ? scales[(size_t)blk * a.Hkv + sg.item.h] : make_float2(0.f, 1.f);
       };
-      int blk = look(0), next = look(1);
-      float2 sc = scales_of(blk);
+      int blk = look(0);
 #pragma unroll 1
       for (int i = 0; i < sg.n; ++i) {
         const int g = sg.g + i, slot = g % kSlots;
@@ -462,15 +477,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
         if (lane < kUnits) {
           const int row = (sg.tok0 + i * TOK + lane * kUnit) % a.bs;
           unit_at[slot][lane] = blk < 0 ? -1 : (((long long)blk * a.Hkv + sg.item.h) * a.bs + row) * a.D;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(found + slot);
+        const float2 sc = scales_of(blk);
+        const int next = look(i + 1);
+        if (lane < kUnits) {
           // a value scale below 2^-64 counts as 2^-64; what comes off the sum is what went on
           const float lv = __log2f(sc.y < kMinScale ? kMinScale : sc.y);
           unit_scales[slot][lane] = make_float4(sc.x, lv, ex2(-lv), blk < 0 ? 0.f : sc.y == 0.f ? 2.f : 1.f);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(found + slot);
+        if (lane == 0) mbar_arrive(scaled + slot);
         blk = next;
-        next = look(i + 2);
-        sc = scales_of(blk);
       }
     }
   } else {
@@ -542,22 +561,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
 }
 
 template <int FMT, int DP>
-cudaError_t launch(const AttnArgs& a, uint8_t* pieces, int ctas, cudaStream_t stream, bool pdl) {
+cudaError_t launch(const AttnArgs& a, uint8_t* pieces, int2* source, int ctas, cudaStream_t stream, bool pdl) {
   auto k = attn_kv8_prefix_kernel<FMT, DP>;
   const cudaError_t e = allow_max_smem(k);
   if (e != cudaSuccess) return e;
   return launch_kernel(k, dim3(ctas), dim3(kThreads), PrefixShape<DP>::kSmem + 16 * ((size_t)a.R + 1), stream, pdl, a,
-                       pieces);
+                       pieces, source);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_kv8_prefix(const AttnArgs& a, int format, uint8_t* pieces, int ctas, cudaStream_t stream,
-                                   bool pdl) {
+cudaError_t launch_attn_kv8_prefix(const AttnArgs& a, int format, uint8_t* pieces, int2* source, int ctas,
+                                   cudaStream_t stream, bool pdl) {
   if (format == QG_KV_I8)
-    return a.D <= 64 ? launch<QG_KV_I8, 64>(a, pieces, ctas, stream, pdl) : launch<QG_KV_I8, 128>(a, pieces, ctas, stream, pdl);
-  return a.D <= 64 ? launch<QG_KV_E4M3, 64>(a, pieces, ctas, stream, pdl)
-                   : launch<QG_KV_E4M3, 128>(a, pieces, ctas, stream, pdl);
+    return a.D <= 64 ? launch<QG_KV_I8, 64>(a, pieces, source, ctas, stream, pdl)
+                     : launch<QG_KV_I8, 128>(a, pieces, source, ctas, stream, pdl);
+  return a.D <= 64 ? launch<QG_KV_E4M3, 64>(a, pieces, source, ctas, stream, pdl)
+                   : launch<QG_KV_E4M3, 128>(a, pieces, source, ctas, stream, pdl);
 }
 
 }  // namespace qg

@@ -20,9 +20,13 @@ namespace qg {
 namespace {
 
 struct JoinArgs {
-  AttnArgs own, pre;
-  const uint8_t* pieces;  // null: the prefix pass leaves every row's result in pre.part_o
-  int ctas;               // of the prefix pass
+  const int32_t *cu_q, *cu_req;
+  int R, groups, T, Hq, D;
+  const float *own_o, *pre_o;
+  const float2 *own_ml, *pre_ml;
+  const int2* source;     // null: every row's prefix result is in pre_o
+  const uint8_t* pieces;
+  uint16_t* out;
 };
 
 constexpr int kJoinThreads = 256;
@@ -37,56 +41,44 @@ __device__ bool bounds_bad(const int32_t* cu, int n, int top) {
 
 // A row per warp. Its parts: the request's own tokens; where its group has a prefix, that one's result or, if the
 // prefix's steps went over several CTAs, their pieces, in the order of the CTAs.
-__global__ void __launch_bounds__(kJoinThreads) attn_shared_join_kernel(const __grid_constant__ JoinArgs j) {
-  extern __shared__ int tables[];
-  __shared__ int2 scan_part[kJoinThreads / 32];
-  const AttnArgs& a = j.own;
+__global__ void __launch_bounds__(kJoinThreads) attn_shared_join_kernel(JoinArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  if (bounds_bad(a.cu_q, a.R, a.T) || bounds_bad(j.pre.cu_req, j.pre.R, a.R)) return;
-  const int t0 = a.cu_q[0], t1 = a.cu_q[a.R], G = a.Hq / a.Hkv, groups = j.pre.R;
-  AttnBatch batch = {};
-  int *first = tables, *cost = first + groups + 1, *cus = cost + groups + 1, *ctxs = cus + groups + 1;
-  AttnShare share = {0, 0, 0, 0};
-  if (j.pieces) {
-    batch = attn_scan<kPrefixRows, PrefixCut, kJoinThreads, true>(j.pre, first, cost, cus, ctxs, scan_part);
-    const int W = cost[groups], A = min(j.ctas, W);  // as attn_share
-    if (A > 0) share.share = W / A, share.more = W % A;
-  }
-  const int g0 = a.cu_q[j.pre.cu_req[0]], g1 = a.cu_q[j.pre.cu_req[groups]];
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)(t1 - t0) * a.Hq;
+  const bool bad = bounds_bad(a.cu_q, a.R, a.T);
+  if (bounds_bad(a.cu_req, a.groups, a.R) || bad) return;
+  const int r0 = a.cu_q[0] * a.Hq, r1 = a.cu_q[a.R] * a.Hq;
+  const int g0 = a.cu_q[a.cu_req[0]] * a.Hq, g1 = a.cu_q[a.cu_req[a.groups]] * a.Hq;
+  const int lane = threadIdx.x & 31, stride = gridDim.x * (kJoinThreads / 32);
+  // (a sum that is no number makes the row none, as it would alone)
+  auto weight = [&](float2 s, float m) { return s.y > 0.f ? s.y * ex2(s.x - m) : s.y; };
 #pragma unroll 1
-  for (long long i = (long long)blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; i < rows;
-       i += (long long)gridDim.x * (kJoinThreads / 32)) {
-    const int t = t0 + (int)(i / a.Hq), hq = (int)(i % a.Hq);
-    const long long row = (long long)t0 * a.Hq + i;
-    const float2 own = a.part_ml[row];
-    const bool shared = t >= g0 && t < g1;
-    int f = 0, pieces = shared ? 1 : 0, rr = 0;
-    const float* pre_o = j.pre.part_o + row * a.D;
-    const float2* pre_ml = j.pre.part_ml + row;
-    if (shared && j.pieces) {
-      const int g = attn_find(cus, groups, t);  // the last group that begins here: one with query tokens
-      const int rho = (t - cus[g]) * G + hq % G, tiles = ((cus[g + 1] - cus[g]) * G + kPrefixRows - 1) / kPrefixRows;
-      const int steps = attn_steps<kPrefixTok>(ctxs[g]), at = first[g] + ((hq / G) * tiles + rho / kPrefixRows) * steps;
-      f = attn_cta_of<PrefixCut>(batch, share, at);
-      pieces = attn_cta_of<PrefixCut>(batch, share, at + steps - 1) - f + 1;
-      rr = rho % kPrefixRows;
+  for (int row = r0 + blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; row < r1; row += stride) {
+    const bool shared = row >= g0 && row < g1;
+    const float2 own = a.own_ml[row], none = make_float2(kNoMax, 0.f);
+    float2 pre = none;
+    int2 from = make_int2(0, shared ? 1 : 0);
+    if (shared) {
+      if (a.source) from = a.source[row];
+      pre = a.pre_ml[row];  // (not written where the prefix is in pieces)
     }
+    const int pieces = from.y;
     // the first piece is the second one of its CTA, as its item goes on after it; the others begin theirs
-    auto piece = [&](int p) { return j.pieces + (size_t)(2 * (f + p) + (p == 0 ? 1 : 0)) * prefix_piece_bytes(a.D); };
-    auto stat = [&](int p) {
-      return pieces == 1 ? *pre_ml : reinterpret_cast<const float2*>(piece(p) + (size_t)kPrefixRows * a.D * 4)[rr];
+    auto piece = [&](int p) {
+      return a.pieces + (size_t)(2 * ((from.x >> 8) + p) + (p == 0 ? 1 : 0)) * prefix_piece_bytes(a.D);
     };
-    // (a sum that is no number makes the row none, as it would alone)
-    auto weight = [&](float2 s, float m) { return s.y > 0.f ? s.y * ex2(s.x - m) : s.y; };
-    float m = own.x, all;
-    for (int p = lane; p < pieces; p += 32) m = fmaxf(m, stat(p).x);
+    auto stat = [&](int p) {
+      return p >= pieces ? none : pieces == 1 ? pre
+                                              : reinterpret_cast<const float2*>(piece(p) + (size_t)kPrefixRows * a.D * 4)[from.x & 255];
+    };
+    float2 mine = stat(lane);  // of piece `lane`; further ones are read again
+    float m = fmaxf(own.x, mine.x);
+#pragma unroll 1
+    for (int p = lane + 32; p < pieces; p += 32) m = fmaxf(m, stat(p).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    all = lane == 0 ? weight(own, m) : 0.f;
-    for (int p = lane; p < pieces; p += 32) all += weight(stat(p), m);
+    float all = weight(mine, m) + (lane == 0 ? weight(own, m) : 0.f);
+#pragma unroll 1
+    for (int p = lane + 32; p < pieces; p += 32) all += weight(stat(p), m);
     all = warp_sum(all);
     const float inv = all == 0.f ? 0.f : 1.f / all;
 #pragma unroll 1
@@ -99,16 +91,22 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join_kernel(const __
           o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
         }
       };
-      add(weight(own, m) * inv, a.part_o + row * a.D);
-      if (pieces == 1) {
-        add(weight(*pre_ml, m) * inv, pre_o);
-      } else {
-#pragma unroll 4
-        for (int p = 0; p < pieces; ++p)
-          add(weight(stat(p), m) * inv, reinterpret_cast<const float*>(piece(p)) + (size_t)rr * a.D);
+      add(weight(own, m) * inv, a.own_o + (size_t)row * a.D);
+      if (pieces == 1) add(weight(pre, m) * inv, a.pre_o + (size_t)row * a.D);
+      if (pieces > 1) {
+#pragma unroll 1
+        for (int p0 = 0; p0 < pieces; p0 += 32) {
+          const float w = weight(p0 ? stat(p0 + lane) : mine, m) * inv;
+#pragma unroll 8
+          for (int k = 0; k < min(32, pieces - p0); ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            add(wk, reinterpret_cast<const float*>(piece(p0 + k)) + (size_t)(from.x & 255) * a.D);
+          }
+        }
       }
       if (in)
-        *reinterpret_cast<uint2*>(a.out + row * a.D + e) = make_uint2(f32_to_bf16x2(o.x, o.y), f32_to_bf16x2(o.z, o.w));
+        *reinterpret_cast<uint2*>(a.out + (size_t)row * a.D + e) =
+            make_uint2(f32_to_bf16x2(o.x, o.y), f32_to_bf16x2(o.z, o.w));
     }
   }
 }
@@ -117,7 +115,7 @@ size_t up(size_t n) { return (n + 1023) / 1024 * 1024; }
 
 // the workspace: what the passes use (counters first), then the partial results of both
 struct SharedLayout {
-  size_t own_o, own_ml, pre_o, pre_ml, pieces, total;
+  size_t own_o, own_ml, pre_o, pre_ml, source, pieces, total;
 };
 // the prefix pass by attn_kv8_prefix.cu; its CTAs
 bool prefix_tc_ok(int D) { return D <= 128; }
@@ -129,7 +127,8 @@ SharedLayout layout(int T, int Hq, int Hkv, int D) {
   l.own_ml = l.own_o + up(rows * D * 4);
   l.pre_o = l.own_ml + up(rows * 8);
   l.pre_ml = l.pre_o + up(rows * D * 4);
-  l.pieces = l.pre_ml + up(rows * 8);
+  l.source = l.pre_ml + up(rows * 8);
+  l.pieces = l.source + (prefix_tc_ok(D) ? up(rows * 8) : 0);
   l.total = l.pieces + (prefix_tc_ok(D) ? up(2 * prefix_ctas() * prefix_piece_bytes(D)) : 0);
   return l;
 }
@@ -151,12 +150,14 @@ cudaError_t launch_attn_kv8_shared(const AttnArgs& own, const AttnArgs& pre, int
   };
   cudaError_t e = warp_level(s);
   if (e != cudaSuccess) return e;
-  e = tc ? launch_attn_kv8_prefix(p, format, ws + l.pieces, prefix_ctas(), stream, pdl) : warp_level(p);
+  int2* source = tc ? reinterpret_cast<int2*>(ws + l.source) : nullptr;
+  e = tc ? launch_attn_kv8_prefix(p, format, ws + l.pieces, source, prefix_ctas(), stream, pdl) : warp_level(p);
   if (e != cudaSuccess) return e;
-  const JoinArgs j = {s, p, tc ? ws + l.pieces : nullptr, prefix_ctas()};
+  const JoinArgs j = {own.cu_q, pre.cu_req, own.R, pre.R, own.T, own.Hq, own.D, s.part_o, p.part_o, s.part_ml, p.part_ml,
+                      source, ws + l.pieces, own.out};
   const long long rows = (long long)own.T * own.Hq, per = kJoinThreads / 32;
   const int grid = (int)std::min<long long>((rows + per - 1) / per, 8LL * device_sm_count());
-  return launch_kernel(attn_shared_join_kernel, dim3(grid), dim3(kJoinThreads), 16 * ((size_t)pre.R + 1), stream, pdl, j);
+  return launch_kernel(attn_shared_join_kernel, dim3(grid), dim3(kJoinThreads), 0, stream, pdl, j);
 }
 
 }  // namespace qg

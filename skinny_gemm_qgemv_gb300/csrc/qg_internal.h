@@ -318,9 +318,10 @@ cudaError_t launch_attn_kv8_tc(const AttnArgs& a, int format, cudaStream_t strea
 // attention of requests whose groups share a prefix (attn_kv8_shared.cu): own has every request's own context, pre every
 // group's prefix (R, table, ctx_lens, max_blocks, cu_req)
 size_t attn_kv8_shared_workspace_size(int T, int Hq, int Hkv, int D);
-// the prefixes' part for heads of up to 128, on tcgen05; pieces of what several CTAs share: attn_prefix.cuh
-cudaError_t launch_attn_kv8_prefix(const AttnArgs& a, int format, uint8_t* pieces, int ctas, cudaStream_t stream,
-                                   bool pdl);
+// the prefixes' part for heads of up to 128, on tcgen05: a row's result is in part_o and part_ml where source[row].y = 1,
+// else in source[row].y pieces, the first one row source[row].x & 255 of CTA source[row].x >> 8's (attn_prefix.cuh)
+cudaError_t launch_attn_kv8_prefix(const AttnArgs& a, int format, uint8_t* pieces, int2* source, int ctas,
+                                   cudaStream_t stream, bool pdl);
 cudaError_t launch_attn_kv8_shared(const AttnArgs& own, const AttnArgs& pre, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t stream, bool pdl);
 cudaError_t launch_qk_rope(const RopeArgs& a, cudaStream_t stream, bool pdl);
