@@ -18,8 +18,8 @@
 // added up at the end (one stream alone would wait for its own softmax half of the
 // time).
 //
-// Warps: 0-3 and 4-7 softmax of the streams, 8-11 copy and convert, 12 looks up
-// blocks and scales, 13 issues the MMAs. Codes go from global memory through
+// Warps: 0-3 and 4-7 softmax of the streams, 8-11 copy and convert keys, 12-15
+// values, 16 looks up blocks and scales, 17 issues the MMAs. Codes go from global memory through
 // registers to fp16 tiles: staged by TMA they would cross shared memory twice more
 // (64 of 320 KB a step, whose 128 bytes a cycle the MMAs' operands need).
 #include <cuda_runtime.h>
@@ -36,7 +36,7 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 576;
 constexpr int kSlots = 8;       // steps whose blocks and scales are kept
 constexpr int kRowsTile = 128;  // rows of a stream's MMAs
 constexpr int kUnits = kPrefixTok / kUnit;
@@ -69,7 +69,24 @@ __device__ __forceinline__ void tmem_wait_ld32(float* v) {
   tmem_wait_ld(v);
   tmem_wait_ld(v + 16);
 }
-constexpr float kMostMass = 256.f;  // sum of a step's p up to which its maximum stays: fp16 holds 2^15
+constexpr float kMostMass = 256.f;  // sum of some p up to which their maximum stays: fp16 holds 2^15
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 16 bytes of global memory, zeros where `there` is not set; no branch
+__device__ __forceinline__ uint4 load_if(const void* p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((unsigned)there)
+      : "memory");
+  return v;
+}
 
 template <int FMT, int DP>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a, uint8_t* pieces, int2* source) {
@@ -106,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
     abort_flag = 0u;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == 17) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
                  "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -166,18 +183,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       // the row as 2^-sigma q in fp16, exact, sigma from its largest finite element
       float rf;
       {
-        uint4 raw[DP / 8];
         const uint16_t* src =
             a.q + (size_t)(q0 + qi) * a.q_stride + (size_t)(sg.item.h * batch.G + rho - qi * batch.G) * a.D;
+        auto load = [&](int j) {
+          return live && 8 * j < a.D ? *reinterpret_cast<const uint4*>(src + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+        };
         unsigned most = 0u;
-#pragma unroll
+#pragma unroll 8
         for (int j = 0; j < DP / 8; ++j) {
-          raw[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (live && 8 * j < a.D) raw[j] = *reinterpret_cast<const uint4*>(src + 8 * j);
-        }
-#pragma unroll
-        for (int j = 0; j < DP / 8; ++j) {
-          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+          const uint4 raw = load(j);
+          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const unsigned lo = w[k] << 16 & 0x7FFF0000u, hi = w[k] & 0x7FFF0000u;
@@ -187,9 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
         const int sigma = fp16_prescale_exp(__uint_as_float(most));
         const float down = pow2f(-sigma);
         rf = a.scale_log2 * pow2f(sigma);
-#pragma unroll
-        for (int j = 0; j < DP / 8; ++j) {
-          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll 4
+        for (int j = 0; j < DP / 8; ++j) {  // (read again: a row kept would take 64 registers)
+          const uint4 raw = load(j);
+          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
           uint32_t f[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -212,91 +228,96 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
         tc_after();
         const int seen = ctx - (sg.tok0 + i * TOK);  // tokens of the step, if not all
         const float4* us = unit_scales[slot];
-        uint32_t p[TOK / 2];
-        // p of the step against the maximum so far, and its sum without the value scale
-        auto probabilities = [&](float& mass) {
-          float part = 0.f;
-          mass = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float s[64];
-            tmem_ld32(ts + 64 * h, s);
-            tmem_ld32(ts + 64 * h + 32, s + 32);
+        // Two units at a time: p against the maximum so far, its sum without the value scale, and as fp16 over the scores
+        // read before. Where the sum is at most 2^8 so is every p, and m stays (a pass over the scores for their maximum
+        // took as long as the exponentials); otherwise m rises to a whole number above the largest, by which what the
+        // step has written already is scaled exactly. (Unrolled, the loop ran slower: three roles' code passes through
+        // an SM's instruction caches in every step.)
+#pragma unroll 1
+        for (int c = 0; c < TOK / 32; ++c) {
+          const float4 sc[2] = {us[2 * c], us[2 * c + 1]};
+          const int here = seen - 32 * c;
+          const bool edge = here < 32 || sc[0].w == 0.f || sc[1].w == 0.f;
+          uint32_t p[16];
+          float s[32], part = 0.f;
+          // (twice at most: above a whole number that no score passes there is no second rise)
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            tmem_ld32(ts + 32 * c, s);
             tmem_wait_ld32(s);
-            tmem_wait_ld32(s + 32);
+            float mass = 0.f;
+            part = 0.f;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const int u = 4 * h + v;
-              const float4 sc = us[u];
-              const uint64_t f2 = both(sc.x * rf), b2 = both(sc.y - m);
+            for (int u = 0; u < 2; ++u) {
+              const uint64_t f2 = both(sc[u].x * rf), b2 = both(sc[u].y), m2 = both(-m);
               uint64_t sum = 0ull;
-              float* e = s + 16 * v;
+              float* e = s + 16 * u;
 #pragma unroll
               for (int j = 0; j < 16; j += 2) {
                 float y0, y1;
-                unpair2(ffma2(pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])), f2, b2), y0, y1);
+                // (the score as it is compared with m, then the difference: a sum with -m in one step may lie above 0 by a
+                // rounding of large scores)
+                unpair2(fadd2(ffma2(pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])), f2, b2), m2), y0, y1);
                 e[j] = ex2(y0), e[j + 1] = ex2(y1);
               }
-              if (seen < 16 * u + 16 || sc.w == 0.f) {
+              if (edge) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                  if (sc.w == 0.f || 16 * u + j >= seen) e[j] = 0.f;
+                  if (sc[u].w == 0.f || 16 * u + j >= here) e[j] = 0.f;
               }
 #pragma unroll
               for (int j = 0; j < 16; j += 2) {
                 sum = fadd2(sum, pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])));
                 p[8 * u + j / 2] = f16x2(e[j], e[j + 1]);
               }
-              if (sc.w == 2.f) {  // a block of zero scale: only the probabilities count
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[8 * u + j] = 0u;
-              }
               float s0, s1;
               unpair2(sum, s0, s1);
               mass += s0 + s1;
-              part = fmaf(s0 + s1, sc.z, part);
+              part = fmaf(s0 + s1, sc[u].z, part);
+            }
+            if (pass == 1 || !__any_sync(0xffffffffu, mass > kMostMass)) break;
+            tmem_ld32(ts + 32 * c, s);
+            tmem_wait_ld32(s);
+            float top = kNoMax;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float4 x = sc[j / 16];
+              if (j < here && x.w != 0.f) top = fmaxf(top, fmaf(s[j], x.x * rf, x.y));
+            }
+            const float mn = top > m ? ceilf(top) : m, f = ex2(m - mn);
+            const uint32_t f16 = f16x2(f, f);
+            m = mn;
+            l *= f;
+#pragma unroll 1
+            for (int k = 0; k < c; ++k) {
+              uint32_t x[16];
+              tmem_ld16(ts + 16 * k, reinterpret_cast<float*>(x));
+              tmem_wait_ld(reinterpret_cast<float*>(x));
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = hmul2(x[j], f16);
+              tmem_st16(ts + 16 * k, *reinterpret_cast<float(*)[16]>(x));
+            }
+            if (begun) {  // (the stream's last product has been waited for with this S)
+#pragma unroll 1
+              for (int k = 0; k < DP / 16; ++k) {
+                float o[16];
+                tmem_ld16(to + 16 * k, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] *= f;
+                tmem_st16(to + 16 * k, o);
+              }
             }
           }
-          return part;
-        };
-        // Where the step's sum is at most 2^8 so is every p, and m stays (a pass over the scores for their maximum, in
-        // every step, took as long as the exponentials). Otherwise m rises to the largest score, and p is formed anew.
-        float mass, part = probabilities(mass);
-        if (__any_sync(0xffffffffu, mass > kMostMass)) {
-          float top = kNoMax;
-#pragma unroll 1
-          for (int u = 0; u < kUnits; ++u) {
-            const float4 sc = us[u];
-            float s[16];
-            tmem_ld16(ts + 16 * u, s);
-            tmem_wait_ld(s);
-            float x = kNoMax;
+          l += part;
+          if (sc[0].w == 2.f || sc[1].w == 2.f) {  // of a block of zero scale only the probabilities count
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              if (16 * u + j < seen) x = fmaxf(x, s[j]);
-            if (sc.w != 0.f && x != kNoMax) top = fmaxf(top, fmaf(x, sc.x * rf, sc.y));
+              if (sc[j / 8].w == 2.f) p[j] = 0u;
           }
-          const float mn = fmaxf(m, top), f = ex2(m - mn);
-          m = mn;
-          l *= f;
-          if (begun) {  // (the stream's last product has been waited for with this S)
-#pragma unroll 1
-            for (int c = 0; c < DP / 16; ++c) {
-              float o[16];
-              tmem_ld16(to + 16 * c, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] *= f;
-              tmem_st16(to + 16 * c, o);
-            }
-          }
-          part = probabilities(mass);
+          tmem_st16(ts + 16 * c, *reinterpret_cast<float(*)[16]>(p));
         }
         begun = true;
-        l += part;
-        // over the first half of the scores
-        tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(p));
-        tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(p + 32));
         tmem_wait_st();
         tc_before();
         __syncwarp();
@@ -334,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
         // 32 rows and elements of a warp at a time through the queries' place (their products are done), so that a row's
         // 128 bytes are stored together
         const uint32_t stage = smem_u32(qbuf) + warp * 4096;
-        const size_t first_row = (size_t)q0 * a.Hq + sg.item.h * batch.G;  // of the item's query rows, as out_row
+        float* dst = whole ? a.part_o : reinterpret_cast<float*>(piece);
+        const int my_row = !live ? -1 : whole ? (int)out_row : rr;
 #pragma unroll 1
         for (int c = 0; c < DP / 32; ++c) {
           float o[32];
@@ -358,14 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
           const int e = 32 * c + 4 * (lane & 7);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int k = 4 * j + (lane >> 3), row = rr - lane + k;
+            const int k = 4 * j + (lane >> 3), row = __shfl_sync(0xffffffffu, my_row, k);
             const uint4 v = lds128(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
-            if (row < sg.rows && e < a.D) {
-              const int rho_k = sg.item.rt * kPrefixRows + row, qk = rho_k / batch.G;
-              float* dst = whole ? a.part_o + (first_row + (size_t)qk * a.Hq + rho_k - qk * batch.G) * a.D
-                                 : reinterpret_cast<float*>(piece) + (size_t)row * a.D;
-              *reinterpret_cast<uint4*>(dst + e) = v;
-            }
+            if (row >= 0 && e < a.D) *reinterpret_cast<uint4*>(dst + (size_t)row * a.D + e) = v;
           }
           __syncwarp();
         }
@@ -373,28 +390,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       tc_before();
       named_barrier<256>(1);  // both streams' outputs and `other` have been read
     }
-  } else if (warp < 12) {
-    // ------------------------------------------------ keys and values: 16 codes a thread and load, as fp16 tiles
-    const int t = tid - 256, ch = t & 3, tk = t >> 2 & (S::kTokens - 1), half = S::kHalves == 2 ? t >> 6 : 0;
+  } else if (warp < 16) {
+    // ------------------------------------------------ keys (warps 8-11) and values (12-15): 16 codes a thread and load,
+    // as fp16 tiles
+    const int t = tid & 127, ch = t & 3, tk = t >> 2 & (S::kTokens - 1), half = S::kHalves == 2 ? t >> 6 : 0;
     const int e = half * 64 + ch * 16;
-    const bool in = e < a.D;
-    const uint8_t *kc = static_cast<const uint8_t*>(a.k_cache), *vc = static_cast<const uint8_t*>(a.v_cache);
-    uint4 kr[S::kLoads], vr[S::kLoads];
-    // (a slot's addresses, then the loads: what is not there counts as zeros)
-    auto fetch = [&](const uint8_t* cache, uint4(&raw)[S::kLoads], int g, int seen) {
-      const long long* at = unit_at[g % kSlots];
+    const bool in = e < a.D, values = warp >= 12;
+    const uint8_t* cache = static_cast<const uint8_t*>(values ? a.v_cache : a.k_cache) + e;
+    uint64_t* full = values ? v_full : k_full;
+    uint4 raw[S::kLoads];
+    // the next step's loads, what is not there as zeros; they are on the way while this step's MMAs run
+    int i = 0;
+    bool more = next_segment(sg, step);
+    auto fetch = [&]() {
+      const int slot = (sg.g + i) % kSlots, seen = in ? ctxs[sg.item.r] - (sg.tok0 + i * TOK) : 0;
+      if (!wait_warp(found + slot, (sg.g + i) / kSlots & 1)) return false;
 #pragma unroll
       for (int k = 0; k < S::kLoads; ++k) {
         const int tok = k * S::kTokens + tk;
-        const long long base = at[tok / kUnit];
-        raw[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (base >= 0 && in && tok < seen)
-          raw[k] = *reinterpret_cast<const uint4*>(cache + base + (tok % kUnit) * a.D + e);
+        const long long base = unit_at[slot][tok / kUnit];
+        raw[k] = load_if(cache + base + (tok % kUnit) * a.D, base >= 0 && tok < seen);
       }
+      if (++i == sg.n) i = 0, more = next_segment(sg, step);
+      return true;
     };
-    // rows of 64 elements, 16-byte chunks swizzled; neighbouring lanes are the four chunk pairs of two tokens: no conflicts
-    auto store = [&](uint8_t* tile, const uint4(&raw)[S::kLoads]) {
-      const uint32_t dst = smem_u32(tile) + half * S::kBlock;
+    bool ok = !more || fetch();
+    uint8_t* tiles = (values ? vbuf : kbuf) + half * S::kBlock;
+#pragma unroll 1
+    for (int g = 0; ok && g < share.c1 - share.c0; ++g) {
+      const int b = g & 1;
+      // the products of two steps ago have read the tile
+      ok = g < 2 || (values ? wait_warp(spent + (g - 2) % kSlots, (g - 2) / kSlots & 1)
+                            : wait_warp(k_empty + b, ((g >> 1) - 1) & 1));
+      if (!ok) break;
+      // rows of 64 elements, 16-byte chunks swizzled; eight lanes are the four chunk pairs of two tokens: no conflicts
+      const uint32_t dst = smem_u32(tiles) + b * S::kTile;
 #pragma unroll
       for (int k = 0; k < S::kLoads; ++k) {
         const int tok = k * S::kTokens + tk;
@@ -408,46 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       }
       fence_async_smem();
       __syncwarp();
-    };
-    // the walk of the loads, a step ahead of the stores
-    Segment ahead = first_segment();
-    int ahead_step = share.c0, ai = 0, ag = 0, aseen = 0;
-    bool more = next_segment(ahead, ahead_step), ok = true;
-    auto look = [&]() {  // the next step to load: its number and tokens
-      ag = ahead.g + ai;
-      aseen = ctxs[ahead.item.r] - (ahead.tok0 + ai * TOK);
-      return wait_warp(found + ag % kSlots, ag / kSlots & 1);
-    };
-    auto advance = [&]() {
-      if (++ai == ahead.n) ai = 0, more = next_segment(ahead, ahead_step);
-    };
-    if (more) {
-      ok = look();
-      if (ok) fetch(kc, kr, ag, aseen), fetch(vc, vr, ag, aseen);
-      advance();
+      if (lane == 0) mbar_arrive(full + b);
+      if (more) ok = fetch();
     }
-    for (int g = 0, left = share.c1 - share.c0; ok && g < left; ++g) {
-      const int b = g & 1;
-      const bool next = more;
-      ok = g < 2 || wait_warp(k_empty + b, ((g >> 1) - 1) & 1);
-      if (!ok) break;
-      store(kbuf + b * S::kTile, kr);
-      if (lane == 0) mbar_arrive(k_full + b);
-      if (next) {
-        ok = look();
-        if (!ok) break;
-        fetch(kc, kr, ag, aseen);
-      }
-      ok = g < 2 || wait_warp(spent + (g - 2) % kSlots, (g - 2) / kSlots & 1);
-      if (!ok) break;
-      store(vbuf + b * S::kTile, vr);
-      if (lane == 0) mbar_arrive(v_full + b);
-      if (next) {
-        fetch(vc, vr, ag, aseen);
-        advance();
-      }
-    }
-  } else if (warp == 12) {
+  } else if (warp == 16) {
     // ------------------------------------------------ a lane per unit of 16 tokens: its block and the block's scales
     const float2* scales = reinterpret_cast<const float2*>(a.scales);
     bool ok = true;
@@ -548,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 13) {
+  if (warp == 17) {
     if (abort_flag) {
       if (lane == 0) {
         tc_commit(&o_done);
