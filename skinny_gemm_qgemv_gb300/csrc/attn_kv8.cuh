@@ -63,6 +63,11 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The CTA's view of the batch: requests, their steps and where a step lies.
 // A request has one item per key/value head and tile of kRows query rows, an
 // item has ceil(tokens / tokens of a step) steps. Shares are cut on a scale on which an

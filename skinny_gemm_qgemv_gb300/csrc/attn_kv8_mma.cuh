@@ -79,11 +79,6 @@ __device__ __forceinline__ void ldmatrix_t8(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // PART: results are partial ones for attn_kv8_shared.cu (fp32 outputs and each row's maximum and sum), and with a.cu_req
 // a context is a group's prefix, every token of which is seen by every query token of the group's requests
 template <int D, int NT, int FMT, bool PART>

@@ -183,15 +183,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       // the row as 2^-sigma q in fp16, exact, sigma from its largest finite element
       float rf;
       {
-        const uint16_t* src =
-            a.q + (size_t)(q0 + qi) * a.q_stride + (size_t)(sg.item.h * batch.G + rho - qi * batch.G) * a.D;
-        auto load = [&](int j) {
-          return live && 8 * j < a.D ? *reinterpret_cast<const uint4*>(src + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
-        };
+        // copied as they are to their place, a warp's 32 rows by that warp, then converted there
+        const long long at = (long long)(q0 + qi) * a.q_stride + (long long)(sg.item.h * batch.G + rho - qi * batch.G) * a.D;
+        const uint32_t rows = smem_u32(qbuf) + stream * S::kTile + quad * 32 * 128;
+        auto chunk = [&](int row, int j) { return rows + (j >> 3) * S::kBlock + row * 128 + (((j & 7) ^ (row & 7)) << 4); };
+        constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows of a copy
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) {
+          const int k = i * kAtOnce + lane / kLanes, j = lane % kLanes;
+          const long long from = __shfl_sync(0xffffffffu, live ? at : -1ll, k);
+          cp_async16(chunk(k, j), a.q + (from < 0 ? 0 : from + 8 * j), from >= 0 && 8 * j < a.D);
+        }
+        cp_async_wait_all();
+        __syncwarp();
         unsigned most = 0u;
-#pragma unroll 8
+#pragma unroll 4
         for (int j = 0; j < DP / 8; ++j) {
-          const uint4 raw = load(j);
+          const uint4 raw = lds128(chunk(lane, j));
           const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -203,15 +211,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
         const float down = pow2f(-sigma);
         rf = a.scale_log2 * pow2f(sigma);
 #pragma unroll 4
-        for (int j = 0; j < DP / 8; ++j) {  // (read again: a row kept would take 64 registers)
-          const uint4 raw = load(j);
+        for (int j = 0; j < DP / 8; ++j) {
+          const uint4 raw = lds128(chunk(lane, j));
           const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
           uint32_t f[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             f[k] = f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          sts128(smem_u32(qbuf) + stream * S::kTile + (j >> 3) * S::kBlock + r * 128 + (((j & 7) ^ (r & 7)) << 4),
-                 make_uint4(f[0], f[1], f[2], f[3]));
+          sts128(chunk(lane, j), make_uint4(f[0], f[1], f[2], f[3]));
         }
         fence_async_smem();
         __syncwarp();
