@@ -128,7 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
                  "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  pdl_wait();
+  // The kernel before is the one over the requests' own tokens, of whose results nothing is read here: its CTAs all
+  // waited for what came before them (the cache, the lengths, the last call's joining), so this one need not wait for
+  // it but at its end, before the joining begins.
   pdl_launch_dependents();
   tc_before();
   const AttnBatch batch = attn_scan<kPrefixRows, PrefixCut, kThreads, true>(a, first, cost, cus, ctxs, scan_part);
@@ -545,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       __syncwarp();
     }
   }
+  if (tid == 0) pdl_wait();
   // After a wait that gave up: the products in flight end before the memory is given back (a bounded wait).
   tc_before();
   __syncthreads();
