@@ -805,6 +805,44 @@ QG_API qg_status qk_norm_rope(const void *q, int64_t q_stride, const void *k, in
                               uint16_t *q_out_bf16, void *k_out, int k_out_dtype, void *stream);
 
 /*
+ * sample_logits -- a token per row of the output head's logits (qgemv_w8a16,
+ * qgemm_w4a16_skinny), drawn with a given random number.
+ *
+ *   logits       [M][V], bf16 or fp32 (dtype), row m at element m * stride (>= V;
+ *                any, rows need not be aligned). NaN counts as -infinity, which
+ *                is never drawn, +infinity as the type's largest number.
+ *   u            fp32 [M]: uniform in [0, 1) (below 0 and NaN count as 0, 1 and
+ *                above as the largest number below 1).
+ *   temperature  fp32 [M] or NULL (1 everywhere). 0, negative or NaN: greedy, the
+ *                first of the largest logits, probability 1.
+ *   top_k        int32 or int64 (top_k_bytes 4 or 8) [M] or NULL; 0, negative, or
+ *                V and more: no such cut.
+ *   top_p        fp32 [M] or NULL; 1 and more, or NaN: no such cut.
+ *   min_p        fp32 [M] or NULL; 0, negative or NaN: no such cut; above 1
+ *                counts as 1.
+ *   A row's tokens in descending order of their logits, the lower index first
+ *   among equal ones, have weights w_j = exp((x_j - x_max) / temperature), sums
+ *   C_n = w_1 + .. + w_n. Of them are kept the top_k first; of these the fewest
+ *   first n with C_n >= top_p C_k (one at least); of these the ones with
+ *   w_j >= min_p w_1. With C the sum of the kept, the token is the first one whose
+ *   C_i is above u C.
+ *   tokens       int32 [M] (output): its index; -1 if no logit is above -infinity.
+ *   probs        fp32 [M] (output) or NULL: w_i / C, with which it was drawn; 0 for
+ *                token -1.
+ *   1 <= M <= 2^20, 1 <= V <= QG_SAMPLE_MAX_V (more: QG_ERR_UNSUPPORTED).
+ * Weights and their sums are whole numbers of 2^-43 of the largest weight, each
+ * weight to 2^-23 of itself or better: results do not depend on any order of
+ * summation, and differ from the definition's where u C or top_p C_k lies within
+ * 2^-22 C of a sum C_i. Rows whose cuts end, or whose draw falls, among more than
+ * 1024 tokens of nearly equal logits take ten times as long. One launch, no
+ * workspace; capturable in a CUDA graph.
+ */
+#define QG_SAMPLE_MAX_V 393216
+QG_API qg_status sample_logits(const void *logits, int dtype, int64_t stride, int M, int V, const float *u,
+                               const float *temperature, const void *top_k, int top_k_bytes,
+                               const float *top_p, const float *min_p, int32_t *tokens, float *probs, void *stream);
+
+/*
  * qg_workspace_size -- the single workspace query of the boundary: device
  * bytes the operation `op` needs for the given shape, group size 64 where
  * the operation has one (M, N, K for the W4A16 and W8A8 products; T, E,

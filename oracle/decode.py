@@ -232,3 +232,25 @@ def rmsnorm(h, weight, eps, sign_bits=None):
     H = np.array([[(-1.0) ** bin(a & b).count("1") for b in i] for a in i])
     mag = np.broadcast_to(np.abs(z).sum(-1, keepdims=True), z.shape)
     return (z @ H).reshape(M, K), mag.reshape(M, K)
+
+
+def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """One row of the sampler in float64: (order: the tokens above -infinity as
+    they rank, C: their summed weights, kept: how many stay, place: of the drawn
+    one in the order). x fp32 or bf16 values, finite largest number 3.4e38."""
+    x = np.where(np.isnan(x), -np.inf, np.minimum(np.asarray(x, np.float64), np.float64(np.finfo(np.float32).max)))
+    order = np.lexsort((np.arange(len(x)), -x))
+    order = order[x[order] > -np.inf]
+    if len(order) == 0:
+        return order, np.zeros(0), 0, -1
+    d = x[order] - x[order[0]]
+    if not temperature > 0:
+        return order, np.ones(len(order)), 1, 0
+    C = np.cumsum(np.exp(d / min(float(temperature), 1e30)))
+    n = len(order) if not 0 < top_k < len(x) else min(int(top_k), len(order))
+    if top_p < 1:
+        n = min(n, int((C[:n] < float(top_p) * C[n - 1]).sum()) + 1)
+    if min_p > 0:
+        n = min(n, int((d >= float(temperature) * np.log(min(1.0, float(min_p)))).sum()))
+    u = min(max(float(u), 0.0), 1 - 2.0 ** -24) if u == u else 0.0
+    return order, C, n, min(int((C[:n] <= u * C[n - 1]).sum()), n - 1)

@@ -10,7 +10,8 @@ Entry points (same names as the C ABI):
   hadamard32_quant_i8, gemm_w8a8_i32; GemvGroup wraps qgemv_w4a16_group_* and
   SkinnyGroup qgemm_w4a16_skinny_group_*. The decode step around the products:
   kv8_block_plan, kv8_append, kv8_read, attn_kv8_paged, attn_kv8_shared (the
-  paged 8-bit key/value cache), rmsnorm_residual, rmsnorm_residual_i8, qk_norm_rope
+  paged 8-bit key/value cache), rmsnorm_residual, rmsnorm_residual_i8, qk_norm_rope,
+  sample_logits
 
 A call is enqueued on `stream`, torch's current one by default. With a stream
 given, the caller orders it after what made the inputs and keeps the inputs
@@ -47,6 +48,7 @@ EXPORTS = [
     "kv8_block_plan", "qg_kv8_plan_workspace_size", "kv8_append", "kv8_read", "attn_kv8_paged",
     "qg_attn_kv8_workspace_size", "rmsnorm_residual", "rmsnorm_residual_i8",
     "qk_norm_rope", "attn_kv8_shared", "qg_attn_kv8_shared_workspace_size",
+    "sample_logits",
 ]
 
 (OP_GEMV_W4A16, OP_SKINNY_W4A16, OP_MOE_MXFP4, OP_HADAMARD_I8, OP_W8A8_I32, OP_W8A8_HADAMARD, OP_KV8_PLAN,
@@ -182,6 +184,8 @@ def lib() -> ctypes.CDLL:
         L.attn_kv8_shared.argtypes = [P, I64] + [P] * 10 + [I] * 11 + [F, P, P, Z, P]
         L.qg_attn_kv8_shared_workspace_size.restype = Z
         L.qg_attn_kv8_shared_workspace_size.argtypes = [I, I, I, I]
+        L.sample_logits.restype = I
+        L.sample_logits.argtypes = [P, I, I64, I, I, P, P, P, I] + [P] * 5
         L.qk_norm_rope.restype = I
         L.qk_norm_rope.argtypes = [P, I64, P, I64, I, P, I, P, I, P, I, P, P, I, F, I, I, I, I, P, P, I, P]
         _lib = L
@@ -642,3 +646,14 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
         pair_axis = bytes(pair_axis)
     return (_bind or _binding()).qk_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, pair_axis,
                                          q_out, k_out, stream)
+
+
+def sample_logits(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, stream=None):
+    """A token per row of logits (bf16 or fp32 [M][V], rows dense, any row
+    stride), drawn with the given uniform numbers u (fp32 [M]) from the softmax at
+    `temperature`, cut to the top_k first tokens, then to the fewest of share
+    top_p, then to those of at least min_p times the first one's probability; the
+    settings are tensors [M] (top_k int32 or int64, the others fp32) or None. temperature 0
+    is greedy. Returns (tokens int32 [M], probs fp32 [M]: the probability that the
+    token was drawn with)."""
+    return (_bind or _binding()).sample(logits, u, temperature, top_k, top_p, min_p, tokens, probs, stream)

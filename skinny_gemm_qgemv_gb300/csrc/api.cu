@@ -680,6 +680,23 @@ qg_status qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k
   return from_cuda(qg::launch_qk_rope(a, static_cast<cudaStream_t>(stream), true));
 }
 
+qg_status sample_logits(const void* logits, int dtype, int64_t stride, int M, int V, const float* u,
+                        const float* temperature, const void* top_k, int top_k_bytes, const float* top_p,
+                        const float* min_p, int32_t* tokens, float* probs, void* stream) {
+  if (!logits || !u || !tokens || (dtype != QG_DT_BF16 && dtype != QG_DT_F32)) return QG_ERR_INVALID_ARG;
+  if (top_k && top_k_bytes != 4 && top_k_bytes != 8) return QG_ERR_INVALID_ARG;
+  if (M < 1 || M > (1 << 20) || V < 1 || stride < V) return QG_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(u) || !aligned16(temperature) || !aligned16(top_k) || !aligned16(top_p) ||
+      !aligned16(min_p) || !aligned16(tokens) || !aligned16(probs))
+    return QG_ERR_MISALIGNED;
+  if (V > QG_SAMPLE_MAX_V) return QG_ERR_UNSUPPORTED;
+  uint32_t* err = err_word();
+  if (!err) return QG_ERR_CUDA;
+  const qg::SampleArgs a = {logits, dtype == QG_DT_F32, stride, M, V, u, temperature, top_k, top_k_bytes == 8, top_p,
+                            min_p, tokens, probs, err};
+  return from_cuda(qg::launch_sample(a, static_cast<cudaStream_t>(stream), true));
+}
+
 qg_status qg_device_error(uint32_t* code, int clear) {
   uint32_t* p = err_word();
   if (!p) return QG_ERR_CUDA;

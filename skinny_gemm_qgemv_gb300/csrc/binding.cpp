@@ -493,6 +493,30 @@ PyObject* qk_rope(PyObject* const* a) {
   return tuple(qo, ko);
 }
 
+PyObject* sample(PyObject* const* a) {
+  const at::Tensor &x = *tensor(a[0], "logits"), &u = *tensor(a[1], "u");
+  const at::Tensor *temp = tensor_or_null(a[2], "temperature"), *k = tensor_or_null(a[3], "top_k"),
+                   *p = tensor_or_null(a[4], "top_p"), *mp = tensor_or_null(a[5], "min_p");
+  const Call c("sample_logits", x, a[8]);
+  if (x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1)) refuse("logits must be [M][V] with dense rows");
+  const int64_t M = x.size(0), V = x.size(1), stride = M > 1 ? x.stride(0) : V;
+  const int dt = dtype_of(x, "logits");
+  c.need(u, at::kFloat, {M}, "u");
+  if (temp) c.need(*temp, at::kFloat, {M}, "temperature");
+  if (k) c.need(*k, k->scalar_type() == at::kLong ? at::kLong : at::kInt, {M}, "top_k");
+  if (p) c.need(*p, at::kFloat, {M}, "top_p");
+  if (mp) c.need(*mp, at::kFloat, {M}, "min_p");
+  at::Tensor tokens = c.output(a[6], at::kInt, {M}, "tokens"), probs = c.output(a[7], at::kFloat, {M}, "probs");
+  Outputs outs(c);
+  outs.add(tokens, at::kInt, {M});
+  outs.add(probs, at::kFloat, {M});
+  outs.make();
+  c.done(sample_logits(ptr<void>(x), dt, stride, size32(M, "M"), size32(V, "V"), ptr<float>(u), ptr<float>(temp),
+                       ptr<void>(k), k ? static_cast<int>(k->element_size()) : 0, ptr<float>(p), ptr<float>(mp), ptr<int32_t>(tokens), ptr<float>(probs),
+                       c.stream));
+  return tuple(tokens, probs);
+}
+
 // (use, bytes, device index, stream handle): the workspace, for the calls that are marshalled in Python
 PyObject* make_workspace(PyObject* const* a) {
   const char* use = PyUnicode_AsUTF8(a[0]);
@@ -536,6 +560,7 @@ PyMethodDef kMethods[] = {
     {"attention_shared", QG_FAST(attention_shared, 15), nullptr},
     {"norm_bf16", QG_FAST(norm_bf16, 7), nullptr},    {"norm_i8", QG_FAST(norm_i8, 9), nullptr},
     {"qk_rope", QG_FAST(qk_rope, 12), nullptr},
+    {"sample", QG_FAST(sample, 9), nullptr},
     {"workspace", QG_FAST(make_workspace, 4), nullptr},
     {"set_raise", set_raise, METH_O, nullptr},        {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_qgbind", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -37,6 +37,7 @@ enum DeviceError : uint32_t {
   kErrKvLength = 0x603,
   kErrKvQueries = 0x604,
   kErrAttnWait = 0x701,
+  kErrSampleWait = 0x801,
 };
 
 // Upper bound on polls of one mbarrier phase before a kernel reports a timeout

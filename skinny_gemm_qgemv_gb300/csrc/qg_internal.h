@@ -224,7 +224,7 @@ cudaError_t launch_w8a16_gemv(const int8_t* wq, const float* scales, const uint1
 
 // The decode step around the products: paged 8-bit key/value cache
 // (kv8_cache.cu), attention over it (attn_kv8.cu), residual RMS norm (rmsnorm.cu), norms of
-// queries and keys with the position rotation (qk_rope.cu)
+// queries and keys with the position rotation (qk_rope.cu), sampling (sample.cu)
 struct PlanArgs {
   const int32_t *old_lens, *new_lens;
   int R, bs;
@@ -291,6 +291,19 @@ struct NormArgs {
   void* out;
   float* scale;  // null: bf16 output
 };
+struct SampleArgs {
+  const void* logits;
+  int f32;
+  long long stride;
+  int M, V;
+  const float *u, *temperature;
+  const void* top_k;  // int32, or int64 with k64
+  int k64;
+  const float *top_p, *min_p;
+  int32_t* tokens;
+  float* probs;
+  uint32_t* err;
+};
 struct RopeArgs {
   const void *q, *k;
   int x_f32;
@@ -324,6 +337,7 @@ cudaError_t launch_attn_kv8_prefix(const AttnArgs& a, int format, uint8_t* piece
                                    cudaStream_t stream, bool pdl);
 cudaError_t launch_attn_kv8_shared(const AttnArgs& own, const AttnArgs& pre, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t stream, bool pdl);
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream, bool pdl);
 cudaError_t launch_qk_rope(const RopeArgs& a, cudaStream_t stream, bool pdl);
 
 // MXFP4 MoE (moe_mxfp4.cu, moe_mx_mma.cu)

@@ -1,0 +1,770 @@
+// A token per row of logits, drawn from the softmax cut by temperature, top-k,
+// top-p and min-p, with one given random number a row.
+//
+// The tokens of a row in descending order of their logits (the lower index first
+// among equal ones) have weights w_j = exp((x_j - x_max) / T) and sums C_n = w_1 + ..
+// + w_n. What is kept is always a beginning of that order: the k first, then the
+// fewest n with C_n >= p C_k, then those with x - x_max >= T ln(min_p). The token is
+// the first one with C_i > u C_n.
+//
+// No row is sorted. A cluster of CTAs holds the row in its shared memory (a bulk
+// copy each: HBM is read once), takes the maximum, and counts the tokens in 2047
+// bins of equal width below it; what a cut or the draw needs of the order lies in
+// one bin, or for small cuts in the first few: those tokens alone are gathered and
+// sorted by one CTA.
+//
+// Sums are whole numbers, in units of 2^-43 of the largest weight, so no order of
+// atomics or of threads changes them. A bin's sum is its count times the weight of
+// its middle less the sum of its tokens' deviations from it: both are 32-bit atomics
+// in shared memory, and a deviation, below 2^-7.5 of the weight, keeps 2^-22 of it
+// there (a token's weight alone 2^-31). Distances from the maximum are formed
+// without error from two fp32.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qg_common.cuh"
+#include "qg_internal.h"
+
+namespace qg {
+namespace {
+
+typedef unsigned long long u64;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 2048;     // the last one takes what lies below the others
+constexpr int kOver = kBins - 1;
+constexpr int kList = 1024;     // tokens that are gathered and sorted, at most
+constexpr int kFewK = 768;      // top-k up to which the bins only count
+constexpr float kFewScale = 90.f;      // their number per unit of a logit
+constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: leaves the nearest whole number in the low bits of a sum
+constexpr int kMaxCluster = 8;
+
+struct Found {  // a bin: the tokens and the weight before it, the tokens in it
+  int bin, n, count, pad;
+  u64 mass;
+};
+struct Row {  // what the CTAs of a cluster tell one another
+  float max[kMaxCluster];
+  int lowest[kMaxCluster];
+  int count[kMaxCluster], over[kMaxCluster], listed[kMaxCluster], landed[kMaxCluster];
+  u64 mass[kMaxCluster], tail[kMaxCluster], sum[2][kMaxCluster];
+  Found found[2];    // of two searches in turn
+  u64 result[2];  // of a walk through a sorted list: the sum at its end, the place
+};
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+__device__ __forceinline__ void put32(const void* p, int rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void put64(const void* p, int rank, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t get32(const void* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ u64 get64(const void* p, int rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// fp32 as unsigned numbers of the same order; -0 is 0
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+template <class T, class OP>
+__device__ __forceinline__ T warp_all(T v, OP op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+// over the CTA, for all threads; `part` [kWarps] is free again after the caller's next barrier
+template <class T, class OP>
+__device__ __forceinline__ T cta_all(T v, OP op, T* part) {
+  v = warp_all(v, op);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) v = op(v, part[w]);
+  return v;
+}
+struct Add {
+  template <class T>
+  __device__ T operator()(T a, T b) const { return a + b; }
+};
+struct Max {
+  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Min {
+  __device__ int operator()(int a, int b) const { return min(a, b); }
+};
+
+// The weight of a distance from the maximum, as described above: bins of 1 / S octaves, S = 64 << sj.
+struct Scale {
+  float max, ch, cl;  // ch + cl = S log2(e) / T
+  float per;          // ln 2 / S
+  int sj;
+};
+__device__ __forceinline__ int bin_of(float a, float c) {
+  return __float_as_int(fminf(a * c, (float)kOver) + kMagic) & 0xFFF;
+}
+// 1 - 2^(-r / S) for the distance of a from the middle of bin b, |r| <= 1/2 or little more
+__device__ __forceinline__ float deviation(const Scale& s, float x, float a, float b) {
+  const float t = a - s.max, e = (s.max - (a - t)) + (-x - t);  // a + e = max - x
+  const float r = fmaf(a, s.ch, -b) + fmaf(a, s.cl, e * s.ch), y = r * s.per;
+  return y * fmaf(y, fmaf(y, 1.f / 6.f, -0.5f), 1.f);
+}
+// 2^(-b / S) in units of 2^-63, from the powers of 2^(-1/64) and 2^(-1/4096)
+__device__ __forceinline__ u64 middle(const u64 (*pow)[64], int b, int sj) {
+  const int octave = b >> (6 + sj);
+  const u64 w = __umul64hi(pow[0][b >> sj & 63], pow[1][(b & ((1 << sj) - 1)) << (6 - sj)]) << 1;
+  return octave > 63 ? 0ull : w >> octave;
+}
+__device__ __forceinline__ u64 weight_of(const Scale& s, const u64 (*pow)[64], float x) {
+  const float a = s.max - x, th = a * s.ch;
+  if (!(th < 1048576.f)) return 0ull;
+  const float bf = rintf(th);
+  const long long dev = (long long)(deviation(s, x, a, bf) * 17592186044416.f);  // 2^44
+  return __umul64hi(middle(pow, (int)bf, s.sj), (u64)((1ll << 44) - dev));
+}
+
+template <bool F32>
+struct Elem {
+  static constexpr int kPer = F32 ? 4 : 8;  // of 16 bytes
+};
+template <bool F32>
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[Elem<F32>::kPer]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < Elem<F32>::kPer; ++j)
+    x[j] = __uint_as_float(F32 ? w[j % 4] : j & 1 ? w[j / 2 % 4] & 0xFFFF0000u : w[j / 2 % 4] << 16);
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int cluster) {
+  using E = Elem<F32>;
+  constexpr int PER = E::kPer;
+  extern __shared__ __align__(16) uint8_t smem[];
+  // layout: bins' counts | their deviations | sums before this CTA's bins | tokens before them | the slice
+  int* cnt = reinterpret_cast<int*>(smem);
+  int* dev = cnt + kBins;
+  const int own_bins = kBins / cluster;
+  u64* before_m = reinterpret_cast<u64*>(dev + kBins);
+  int* before_n = reinterpret_cast<int*>(before_m + own_bins);
+  uint4* slice = reinterpret_cast<uint4*>(before_n + own_bins);
+  // a gathered list over the counts, its sorted whole (in CTA 0) over the deviations
+  u64* list = reinterpret_cast<u64*>(cnt);
+  u64* sorted = reinterpret_cast<u64*>(dev);
+  __shared__ Row row;
+  __shared__ u64 pow[2][64];
+  __shared__ u64 part64[kWarps];
+  __shared__ int part32[kWarps];
+  __shared__ float partf[kWarps];
+  __shared__ uint64_t bar;
+  __shared__ int taken;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int m = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+  const int size = F32 ? 4 : 2;
+
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+  }
+  if (tid < 128) pow[tid >> 6][tid & 63] = (u64)(exp2(-(double)(tid & 63) / (tid < 64 ? 64. : 4096.)) * 9223372036854775808.);
+#pragma unroll 1
+  for (int i = tid; i < 2 * kBins; i += kThreads) cnt[i] = 0;
+  cluster_arrive();  // every CTA of the cluster runs once this is through: its memory may be written
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+
+  // ---- the slice: 16-byte units of the row from its first 16-byte boundary on; what lies before that and after the last
+  // whole unit fills up a unit of the first and of the last CTA, with -infinity around it
+  const char* base = static_cast<const char*>(a.logits) + m * a.stride * size;
+  const int head = (int)((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / size;
+  const int lead = min(head, a.V), units = (a.V - lead) / PER, rest = a.V - lead - units * PER;
+  const int u0 = (int)((long long)units * rank / cluster), u1 = (int)((long long)units * (rank + 1) / cluster);
+  const int front = rank == 0 && lead ? 1 : 0, back = rank == cluster - 1 && rest ? 1 : 0;
+  const int n = front + (u1 - u0) + back;                    // units in shared memory
+  const int first = lead + (u0 - front) * PER;               // index of the first one's first element
+  if (tid == 0) {
+    const uint32_t bytes = (uint32_t)(u1 - u0) * 16u;
+    mbar_arrive_expect_tx(&bar, bytes);
+    constexpr uint32_t kPiece = 32768u;
+    const char* src = base + (size_t)(lead + u0 * PER) * size;
+#pragma unroll 1
+    for (uint32_t at = 0; at < bytes; at += kPiece)
+      bulk_g2s(reinterpret_cast<uint8_t*>(slice + front) + at, src + at, min(kPiece, bytes - at), &bar);
+  }
+  if (tid < 2 * PER) {
+    const int j = tid % PER, which = tid / PER;               // 0: the front unit, 1: the back one
+    const int e = which ? lead + units * PER + j : lead - PER + j;
+    const bool in = which ? j < rest : e >= 0;
+    if (which ? back : front) {
+      uint4* to = which ? slice + n - 1 : slice;
+      if (F32)
+        reinterpret_cast<uint32_t*>(to)[j] = in ? reinterpret_cast<const uint32_t*>(base)[e] : 0xFF800000u;
+      else
+        reinterpret_cast<uint16_t*>(to)[j] = in ? reinterpret_cast<const uint16_t*>(base)[e] : (uint16_t)0xFF80u;
+    }
+  }
+  const float u_raw = a.u[m];
+  const float u = u_raw >= 0.f ? fminf(u_raw, 0.99999994f) : 0.f;
+  const float temp = a.temperature ? a.temperature[m] : 1.f;
+  const bool greedy = !(temp > 0.f);
+  const float T = fminf(fmaxf(temp, 1e-30f), 1e30f);
+  long long k_raw = 0;
+  if (a.top_k) k_raw = a.k64 ? static_cast<const long long*>(a.top_k)[m] : static_cast<const int*>(a.top_k)[m];
+  const float p_raw = a.top_p ? a.top_p[m] : 1.f, mp_raw = a.min_p ? a.min_p[m] : 0.f;
+  const int k = k_raw > 0 && k_raw < a.V ? (int)k_raw : 0;   // 0: all
+  const bool has_p = p_raw < 1.f, has_m = mp_raw > 0.f;
+  __syncthreads();
+  bool landed = __syncthreads_and(mbar_wait(&bar, 0, a.err, kErrSampleWait));
+
+  auto index_of = [&](int i, int j) { return first + i * PER + j; };
+  // f(x, unit, element) of all of the thread's elements
+  auto sweep = [&](auto&& f) {
+#pragma unroll 2
+    for (int i = tid; i < n; i += kThreads) {
+      float x[PER];
+      unpack<F32>(slice[i], x);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) f(x[j], i, j);
+    }
+  };
+
+  // ---- the maximum; NaN counts as -infinity, +infinity as the type's largest number
+  constexpr float kMost = 3.402823466e+38f;
+  float top = -INFINITY;
+  bool odd = false;
+  sweep([&](float x, int, int) {
+    top = fmaxf(top, x);
+    odd |= !(x <= kMost);
+  });
+  if (__syncthreads_or(odd)) {
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) {
+      if (F32) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(slice + i);
+#pragma unroll 1
+        for (int j = 0; j < PER; ++j) {
+          const float x = __uint_as_float(w[j]);
+          if (!(x <= kMost)) w[j] = x != x ? 0xFF800000u : 0x7F7FFFFFu;
+        }
+      } else {
+        uint16_t* w = reinterpret_cast<uint16_t*>(slice + i);
+#pragma unroll 1
+        for (int j = 0; j < PER; ++j) {
+          const float x = bf16_bits_to_f32(w[j]);
+          if (!(x <= kMost)) w[j] = x != x ? (uint16_t)0xFF80u : (uint16_t)0x7F7Fu;
+        }
+      }
+    }
+    top = fminf(top, F32 ? kMost : __uint_as_float(0x7F7F0000u));
+    __syncthreads();
+  }
+  top = cta_all(top, Max(), partf);
+  cluster_wait();
+  if (tid < cluster) {
+    put32(&row.max[rank], tid, __float_as_uint(top));
+    put32(&row.landed[rank], tid, landed);
+  }
+  cluster_sync();
+  for (int c = 0; c < cluster; ++c) top = fmaxf(top, row.max[c]), landed &= row.landed[c] != 0;
+
+  // the whole cluster's sum; `which` alternates between calls, so that one's numbers are read before they are written again
+  int turn = 0;
+  auto cluster_sum = [&](u64 v) {
+    v = cta_all(v, Add(), part64);
+    turn ^= 1;
+    if (tid < cluster) put64(&row.sum[turn][rank], tid, v);
+    cluster_sync();
+    v = 0;
+    for (int c = 0; c < cluster; ++c) v += row.sum[turn][c];
+    return v;
+  };
+
+  int token = -1;
+  float prob = 0.f;
+  if (top == -INFINITY || !landed) {
+    // nothing to draw
+  } else if (greedy) {
+    int at = 0x7FFFFFFF;
+    sweep([&](float x, int i, int j) {
+      if (x == top) at = min(at, index_of(i, j));
+    });
+    at = cta_all(at, Min(), part32);
+    if (tid < cluster) put32(&row.lowest[rank], tid, (uint32_t)at);
+    cluster_sync();
+    for (int c = 0; c < cluster; ++c) at = min(at, row.lowest[c]);
+    token = at;
+    prob = 1.f;
+  } else {
+    Scale s;
+    s.max = top;
+    s.sj = 0;
+    while (s.sj < 6 && T > (float)(1 << s.sj)) ++s.sj;
+    const double c = 1.4426950408889634 * (64 << s.sj) / (double)T;
+    s.ch = (float)c, s.cl = (float)(c - (double)s.ch);
+    s.per = 0.69314718f / (float)(64 << s.sj);
+    // x passes min_p from here on
+    const float least = has_m ? __double2float_ru((double)top + (double)T * log((double)fminf(mp_raw, 1.f))) : -INFINITY;
+    const double p64 = (double)p_raw, u64_ = (double)u;
+    auto share = [](double f, u64 z) { return (u64)ceil(f * (double)z); };  // of a sum, for C >= share
+    auto past = [](double f, u64 z) { return (u64)(f * (double)z) + 1; };   // for C > f z
+
+    u64 Z = 0, drawn_of = 0;  // all weights; the kept ones
+    int finite = 0;           // tokens above -infinity
+    bool few = k > 0 && k <= kFewK;  // the bins only count, and are of the logits' scale
+    bool done = false;
+    float c_bin = 0.f;
+
+    // ---- the bins and what lies before each of this CTA's own
+    auto histogram = [&]() {
+      c_bin = few ? kFewScale : s.ch;
+      int over = 0;
+      float tail = 0.f;
+      if (few) {
+        sweep([&](float x, int, int) {
+          const int b = bin_of(top - x, c_bin);
+          if (b < kOver)
+            atomicAdd(cnt + b, 1);
+          else
+            over += x > -INFINITY;
+        });
+      } else {
+        const float unit = (float)(4194304 << s.sj), inv_s = -1.f / (float)(64 << s.sj);
+        sweep([&](float x, int, int) {
+          const float d = top - x, th = d * s.ch, bm = fminf(th, (float)kOver) + kMagic;
+          const int b = __float_as_int(bm) & 0xFFF;
+          if (b < kOver) {
+            const float q = fmaf(deviation(s, x, d, bm - kMagic), unit, kMagic);
+            atomicAdd(cnt + b, 1);
+            atomicAdd(dev + b, __float_as_int(q) - 0x4B400000);
+          } else {
+            over += x > -INFINITY;
+            tail += ex2(th * inv_s);
+          }
+        });
+      }
+      over = cta_all(over, Add(), part32);
+      const u64 tail_sum = cta_all((u64)(tail * 8796093022208.f), Add(), part64);  // 2^43
+      cluster_sync();  // all counts are there
+      // this CTA's bins, over the cluster: four or fewer consecutive ones a thread
+      const int per = (own_bins + kThreads - 1) / kThreads, b0 = tid * per;
+      int mine_n = 0;
+      u64 mine_m = 0;
+#pragma unroll 1
+      for (int i = b0; i < min(b0 + per, own_bins); ++i) {
+        const int b = rank * own_bins + i;
+        int count = 0;
+        long long deviate = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          if (r < cluster) {
+            count += (int)get32(cnt + b, r);
+            if (!few) deviate += (int)get32(dev + b, r);
+          }
+        }
+        before_n[i] = mine_n;
+        before_m[i] = mine_m;
+        mine_n += count;
+        if (!few && count)
+          mine_m += __umul64hi(middle(pow, b, s.sj), ((u64)count << 44) - (u64)(deviate * (1ll << (22 - s.sj))));
+      }
+      // exclusive sums over the threads
+      int inc_n = mine_n;
+      u64 inc_m = mine_m;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc_n, o);
+        const u64 y = __shfl_up_sync(0xffffffffu, inc_m, o);
+        if (lane >= o) inc_n += x, inc_m += y;
+      }
+      __syncthreads();
+      if (lane == 31) part32[warp] = inc_n, part64[warp] = inc_m;
+      __syncthreads();
+      int base_n = inc_n - mine_n, total_n = 0;
+      u64 base_m = inc_m - mine_m, total_m = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) base_n += part32[w], base_m += part64[w];
+        total_n += part32[w], total_m += part64[w];
+      }
+      if (tid < cluster) {
+        put32(&row.count[rank], tid, (uint32_t)total_n);
+        put64(&row.mass[rank], tid, total_m);
+        put32(&row.over[rank], tid, (uint32_t)over);
+        put64(&row.tail[rank], tid, tail_sum);
+      }
+      cluster_sync();  // (and all have read the counts: a list may take their place)
+      finite = 0, Z = 0;
+      for (int r = 0; r < cluster; ++r) {
+        if (r < rank) base_n += row.count[r], base_m += row.mass[r];
+        finite += row.count[r] + row.over[r];
+        Z += row.mass[r] + row.tail[r];
+      }
+#pragma unroll 1
+      for (int i = b0; i < min(b0 + per, own_bins); ++i) before_n[i] += base_n, before_m[i] += base_m;
+      __syncthreads();
+    };
+    // tokens, weight before the overflow bin
+    auto inner_n = [&]() {
+      int x = 0;
+      for (int r = 0; r < cluster; ++r) x += row.count[r];
+      return x;
+    };
+    auto inner_m = [&]() {
+      u64 x = 0;
+      for (int r = 0; r < cluster; ++r) x += row.mass[r];
+      return x;
+    };
+    auto end_n = [&](int i) {  // after this CTA's bin i
+      int x = 0;
+      if (i + 1 < own_bins) return before_n[i + 1];
+      for (int r = 0; r <= rank; ++r) x += row.count[r];
+      return x;
+    };
+    auto end_m = [&](int i) {
+      u64 x = 0;
+      if (i + 1 < own_bins) return before_m[i + 1];
+      for (int r = 0; r <= rank; ++r) x += row.mass[r];
+      return x;
+    };
+    int search_turn = 0;
+    // what this CTA knows of its bin i to the whole cluster
+    auto tell = [&](int i) {
+#pragma unroll 1
+      for (int r = 0; r < cluster; ++r) {
+        Found* f = &row.found[search_turn];
+        put32(&f->bin, r, (uint32_t)(rank * own_bins + i));
+        put32(&f->n, r, (uint32_t)before_n[i]);
+        put32(&f->count, r, (uint32_t)(end_n(i) - before_n[i]));
+        put64(&f->mass, r, before_m[i]);
+      }
+    };
+    // the bin in which the count (which 0) or the sum (1) reaches `want`; kOver where none of the inner ones does
+    auto find = [&](int which, u64 want) {
+      search_turn ^= 1;
+#pragma unroll 1
+      for (int i = tid; i < own_bins; i += kThreads) {
+        const u64 lo = which ? before_m[i] : (u64)before_n[i], hi = which ? end_m(i) : (u64)end_n(i);
+        if (lo < want && want <= hi) tell(i);
+      }
+      cluster_sync();
+      Found f = row.found[search_turn];
+      if (want > (which ? inner_m() : (u64)inner_n())) f.bin = kOver, f.n = inner_n(), f.count = finite - f.n, f.mass = inner_m();
+      return f;
+    };
+    auto of_bin = [&](int b) {
+      search_turn ^= 1;
+      if (b / own_bins == rank && tid == b % own_bins % kThreads) tell(b % own_bins);
+      cluster_sync();
+      return row.found[search_turn];
+    };
+    // The tokens of bins lo .. hi, no more than kList of them, sorted in CTA 0: keys in descending order with
+    // the complement of the index below.
+    auto gather = [&](int lo, int hi) {
+      if (tid == 0) taken = 0;
+      __syncthreads();
+      sweep([&](float x, int i, int j) {
+        const int b = bin_of(top - x, c_bin);
+        if (b >= lo && b <= hi && x > -INFINITY) {
+          const int at = atomicAdd(&taken, 1);
+          if (at < kList) list[at] = (u64)key_of(x) << 32 | (uint32_t)~index_of(i, j);
+        }
+      });
+      __syncthreads();
+      if (tid == 0) put32(&row.listed[rank], 0, (uint32_t)min(taken, kList));
+      cluster_sync();
+      int count = 0;
+      if (rank == 0) {
+#pragma unroll 1
+        for (int r = 0; r < cluster; ++r) {
+          const int some = min(row.listed[r], kList - count);
+#pragma unroll 1
+          for (int i = tid; i < some; i += kThreads) sorted[count + i] = get64(list + i, r);
+          count += some;
+        }
+        int width = 32;
+        while (width < count) width <<= 1;
+#pragma unroll 1
+        for (int i = count + tid; i < width; i += kThreads) sorted[i] = 0ull;
+        __syncthreads();
+#pragma unroll 1
+        for (int span = 2; span <= width; span <<= 1) {
+#pragma unroll 1
+          for (int step = span >> 1; step > 0; step >>= 1) {
+#pragma unroll 1
+            for (int i = tid; i < width / 2; i += kThreads) {
+              const int x = 2 * i - (i & (step - 1)), y = x + step;
+              const u64 p = sorted[x], q = sorted[y];
+              if ((p < q) == ((x & span) == 0)) sorted[x] = q, sorted[y] = p;
+            }
+            __syncthreads();
+          }
+        }
+      }
+      return count;
+    };
+    // In CTA 0, of a sorted list: the sums of the weights up to each of the thread's two places 2 tid, 2 tid + 1
+    auto prefix = [&](int count, u64 (&sum)[2]) {
+      u64 w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = 2 * tid + j;
+        w[j] = i < count ? weight_of(s, pow, value_of((uint32_t)(sorted[i] >> 32))) : 0ull;
+      }
+      u64 inc = w[0] + w[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      __syncthreads();
+      if (lane == 31) part64[warp] = inc;
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v)
+        if (v < warp) inc += part64[v];
+      sum[0] = inc - w[1], sum[1] = inc;
+    };
+    // smallest place of a list's `count` at which base + its sum reaches `want` (count if none does): for CTA 0's threads
+    auto reach = [&](const u64 (&sum)[2], int count, u64 base, u64 want) {
+      int at = count;
+#pragma unroll
+      for (int j = 1; j >= 0; --j)
+        if (2 * tid + j < count && base + sum[j] >= want) at = 2 * tid + j;
+      return cta_all(at, Min(), part32);
+    };
+    auto sum_at = [&](const u64 (&sum)[2], int i) {  // the sum at place i, for all threads of CTA 0
+      __syncthreads();
+      if (tid == i >> 1) row.result[0] = sum[i & 1];
+      __syncthreads();
+      return row.result[0];
+    };
+
+    // ---- where a bin holds more than a list does, or the target lies below the bins: by halving the numbers that the
+    // order's keys, then the indexes of equal ones, may be (slow, for rows of many equal logits, or very flat ones)
+    auto mass_from = [&](uint32_t key) {
+      u64 w = 0;
+      sweep([&](float x, int, int) {
+        if (key_of(x) >= key) w += weight_of(s, pow, x);
+      });
+      return cluster_sum(w);
+    };
+    auto count_from = [&](uint32_t key) {
+      u64 w = 0;
+      sweep([&](float x, int, int) { w += key_of(x) >= key && x > -INFINITY; });
+      return cluster_sum(w);
+    };
+    // the sum at the place where the count (which 0) or the sum reaches `want`, and that place's key and number among its
+    // equals
+    struct Place {
+      u64 sum;
+      uint32_t key;
+      u64 nth;
+    };
+    auto search = [&](int which, u64 want) {
+      uint32_t lo = key_of(-kMost), hi = key_of(top);  // the largest key from which on it is reached lies here
+#pragma unroll 1
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        if ((which ? mass_from(mid) : count_from(mid)) >= want)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      Place r;
+      r.key = lo;
+      const u64 w = weight_of(s, pow, value_of(lo)), m_above = lo == 0xFFFFFFFFu ? 0 : mass_from(lo + 1),
+                n_above = lo == 0xFFFFFFFFu ? 0 : count_from(lo + 1), equal = count_from(lo) - n_above;
+      r.nth = which ? (w ? (want - min(want, m_above) + w - 1) / w : 1ull) : want - min(want, n_above);
+      r.nth = max(1ull, min(r.nth, equal));
+      r.sum = m_above + r.nth * w;
+      return r;
+    };
+    auto index_of_nth = [&](uint32_t key, u64 nth) {
+      int lo = 0, hi = a.V - 1;
+#pragma unroll 1
+      while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        u64 w = 0;
+        sweep([&](float x, int i, int j) { w += key_of(x) == key && index_of(i, j) <= mid; });
+        if (cluster_sum(w) >= nth)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      return lo;
+    };
+    float drawn = 0.f;  // the token's logit
+
+    // ---- small cuts: all that may be kept in one list
+    histogram();
+    Found kth = {};
+    if (k && k < finite) kth = find(0, (u64)k);
+    if (few && (k >= finite || kth.bin == kOver || kth.n + kth.count > kList)) {
+      // the k-th does not lie in a list's reach: bins of weights
+      few = false;
+      cluster_sync();
+#pragma unroll 1
+      for (int i = tid; i < 2 * kBins; i += kThreads) cnt[i] = 0;
+      __syncthreads();
+      histogram();
+      if (k && k < finite) kth = find(0, (u64)k);
+    }
+    const bool has_k = k && k < finite;
+    int last = kOver, upto = kList + 1;  // a bin that holds the end of what is kept, and the tokens up to its end
+    if (has_k) {
+      last = kth.bin, upto = kth.n + kth.count;
+    } else if (has_p) {
+      // (a little further: the sums of the bins and of single tokens differ in their last digits)
+      const Found f = find(1, min(Z, max(1ull, share(p64, Z) + (Z >> 20))));
+      last = f.bin, upto = f.n + f.count;
+    }
+    if (has_m && !(has_k && has_p)) {  // (top-p after top-k needs the k first)
+      const int b = bin_of(top - fmaxf(least, -kMost), c_bin) + 1;
+      if (b < kOver && b < last) {
+        const Found f = of_bin(b);
+        last = b, upto = f.n + f.count;
+      }
+    }
+    if (last != kOver && upto <= kList) {
+      const int count = gather(0, last);
+      if (rank == 0) {
+        u64 sum[2];
+        prefix(count, sum);
+        int keep = has_k ? min(k, count) : count;
+        if (has_p) {
+          const u64 z = has_k ? sum_at(sum, keep - 1) : Z;
+          keep = min(keep, reach(sum, keep, 0, max(1ull, share(p64, z))) + 1);
+        }
+        if (has_m) {
+          int pass = 0;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            pass += 2 * tid + j < count && value_of((uint32_t)(sorted[2 * tid + j] >> 32)) >= least;
+          keep = min(keep, cta_all(pass, Add(), part32));
+        }
+        keep = max(keep, 1);
+        drawn_of = sum_at(sum, keep - 1);
+        const int at = min(reach(sum, keep, 0, past(u64_, drawn_of)), keep - 1);
+        token = (int)~(uint32_t)sorted[at];
+        drawn = value_of((uint32_t)(sorted[at] >> 32));
+      }
+      done = true;
+    }
+    if (!done) {
+      // ---- large cuts, or none: each one's end lies in one bin
+      drawn_of = Z;
+      auto end_of = [&](int which, const Found& f, u64 want) {  // the sum at the place where it reaches `want`
+        if (f.bin == kOver || f.count > kList) return search(which, want).sum;
+        const int count = gather(f.bin, f.bin);
+        if (rank == 0) {
+          u64 sum[2];
+          prefix(count, sum);
+          int at = which ? reach(sum, count, f.mass, want) : (int)(want - f.n) - 1;
+          at = min(max(at, 0), count - 1);
+          const u64 z = f.mass + sum_at(sum, at);
+          if (tid < cluster) put64(&row.result[1], tid, z);
+        }
+        cluster_sync();
+        return row.result[1];
+      };
+      if (has_k) drawn_of = end_of(0, kth, (u64)k);
+      if (has_p) {
+        const u64 want = max(1ull, share(p64, drawn_of));
+        const Found f = find(1, want);
+        drawn_of = min(drawn_of, end_of(1, f, want));
+      }
+      if (has_m) drawn_of = min(drawn_of, mass_from(key_of(fmaxf(least, -kMost))));
+      const u64 want = past(u64_, drawn_of);
+      const Found f = find(1, want);
+      if (f.bin == kOver || f.count > kList) {
+        const Place at = search(1, min(want, mass_from(key_of(-kMost))));
+        token = index_of_nth(at.key, at.nth);
+        drawn = value_of(at.key);
+      } else {
+        const int count = gather(f.bin, f.bin);
+        if (rank == 0) {
+          u64 sum[2];
+          prefix(count, sum);
+          const int at = min(reach(sum, count, f.mass, want), count - 1);
+          token = (int)~(uint32_t)sorted[at];
+          drawn = value_of((uint32_t)(sorted[at] >> 32));
+        }
+      }
+    }
+    if (rank == 0 && tid == 0)
+      prob = (float)(exp(((double)drawn - (double)top) / (double)T) * 8796093022208. / (double)drawn_of);
+  }
+  if (rank == 0 && tid == 0) {
+    a.tokens[m] = token;
+    if (a.probs) a.probs[m] = prob;
+  }
+  cluster_sync();  // no CTA leaves while another reads its memory
+  if (!landed) mbar_wait_n(&bar, 0, nullptr, 0, 1u << 16);  // nor before its copies have landed (a bounded wait)
+}
+
+template <bool F32>
+cudaError_t launch(const SampleArgs& a, cudaStream_t stream, bool pdl) {
+  auto k = sample_kernel<F32>;
+  cudaError_t e = allow_max_smem(k);
+  if (e != cudaSuccess) return e;
+  const int cluster = a.V <= 8192 ? 1 : a.V <= 16384 ? 2 : a.V <= 32768 ? 4 : 8;
+  const int own = kBins / cluster, per = F32 ? 4 : 8;
+  const size_t smem = 2 * kBins * 4 + own * 12 + 16 * ((size_t)(a.V / per + cluster - 1) / cluster + 3);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.M * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, a, cluster);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream, bool pdl) {
+  return a.f32 ? launch<true>(a, stream, pdl) : launch<false>(a, stream, pdl);
+}
+
+}  // namespace qg

@@ -13,6 +13,10 @@ Tolerances (fixed before the first run):
     the probabilities' fp16 rounding, the scores' fp32 error d = (D + 8) 2^-23 max
     sum|q k| in both numerator and denominator, the fp32 sums, the joining of
     partial results, and probabilities below fp16's normal range.
+  * sampling: the token is the definition's; where u C, or top_p times its sum,
+    lies within 2^-22 of the whole sum from a border, the one across it may come
+    too (weights are held to 2^-23 of themselves). The probability within 2^-21 of
+    itself: two such sums and the fp32 result.
 """
 import numpy as np
 import pytest
@@ -406,3 +410,214 @@ def test_shared_attention_refusals(q):
         q.attn_kv8_shared(**a, workspace=torch.zeros(4096, dtype=torch.uint8, device=DEV))
     with pytest.raises(q.QGError):
         q.attn_kv8_shared(**a, softmax_scale=-1.0)
+
+
+# --------------------------------------------------------------------------
+# sampling
+# --------------------------------------------------------------------------
+
+EPS = 2.0 ** -22
+
+
+def check_row(x, u, token, prob, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    order, C, n, i = od.sample(x, u, temperature, top_k, top_p, min_p)
+    if i < 0:
+        assert token == -1 and prob == 0
+        return
+    # what may be kept: with top_p a little less or more, where its border is near
+    kept = {n}
+    if top_p < 1 and temperature > 0:
+        kept |= {od.sample(x, u, temperature, top_k, top_p * (1 + f) + g * EPS, min_p)[2] for f, g in ((EPS, 1), (-EPS, -1))}
+    u = min(max(u, 0.0), 1 - 2.0 ** -24) if u == u else 0.0
+    probs = []
+    j = int(np.nonzero(order == token)[0][0])
+    for n in kept:
+        lo, hi = (min(int((C[:n] <= (u + f) * C[n - 1]).sum()), n - 1) for f in (-EPS, EPS))
+        if lo <= j <= hi:  # the definition's, or one across borders that are near
+            d = min(float(x[token]), 3.5e38) - min(float(x[order[0]]), 3.5e38)
+            probs.append(np.exp(d / min(float(temperature), 1e30)) / C[n - 1] if temperature > 0 else 1.0)
+    assert probs, (token, order[i], n, len(order))
+    assert any(abs(prob - p) <= 2.0 ** -21 * p + 2.0 ** -149 for p in probs), (prob, probs)
+
+
+def run_rows(q, x, u, passed=None, **settings):
+    """x: CPU tensor; settings: per-row lists or None."""
+    M = x.shape[0]
+    t = {n: None if v is None else torch.tensor(v, dtype=torch.int32 if n == "top_k" else torch.float32, device=DEV)
+         for n, v in settings.items()}
+    tokens, probs = q.sample_logits(x.to(DEV) if passed is None else passed,
+                                    torch.tensor(u, dtype=torch.float32, device=DEV), **t)
+    tokens, probs = tokens.cpu().numpy(), probs.double().cpu().numpy()
+    rows = x.float().numpy()
+    for m in range(M):
+        own = {n: (np.float32(v[m]) if n != "top_k" else int(v[m])) for n, v in settings.items() if v is not None}
+        check_row(rows[m], float(np.float32(u[m])), int(tokens[m]), float(probs[m]), **own)
+    return tokens, probs
+
+
+def settings_mix(rng, M, V):
+    return dict(temperature=rng.choice([0.0, 0.3, 0.7, 1.0, 1.3, 3.0, 20.0], M).tolist(),
+                top_k=rng.choice([0, 1, 5, 50, 400, 1500, V - 1, V, 10 * V], M).tolist(),
+                top_p=rng.choice([1.0, 0.9, 0.5, 0.99, 0.0, 1e-6, 2.0], M).tolist(),
+                min_p=rng.choice([0.0, 0.0, 0.1, 0.01, 1.0, 3.0], M).tolist())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 8, 9, 31, 100, 1000, 4097, 8192, 8193, 16385, 32771, 50021])
+def test_sample(q, V, dtype):
+    rng = np.random.default_rng(V)
+    M = 40
+    x = torch.from_numpy(rng.standard_normal((M, V)) * rng.choice([0.3, 2.0, 6.0], (M, 1))).to(dtype)
+    u = rng.random(M).tolist()
+    u[0], u[1], u[2], u[3] = 0.0, 1 - 2.0 ** -24, 1.0, float("nan")
+    run_rows(q, x, u)
+    mix = settings_mix(rng, M, V)
+    run_rows(q, x, u, **mix)
+    for name in mix:
+        run_rows(q, x, u, **{name: mix[name]})
+    run_rows(q, x, u, top_k=mix["top_k"], top_p=mix["top_p"])
+    d = x.to(DEV), torch.tensor(u, device=DEV)
+    long = torch.tensor(mix["top_k"], device=DEV) * (1 << 33)   # above 32 bits: no cut
+    for k in (long, long.sign() * 3):
+        assert all(map(torch.equal, q.sample_logits(*d, top_k=k), q.sample_logits(*d, top_k=k.clamp(max=1 << 30).int())))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [131075, 151936, 262147, 393216])
+def test_sample_large(q, V, dtype):
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy(rng.standard_normal((8, V)) * 2).to(dtype)
+    x[::2, rng.integers(0, V, 30)] += 9
+    u = rng.random(8).tolist()
+    run_rows(q, x, u)
+    run_rows(q, x, u, temperature=[0.7] * 8, top_k=[50] * 8, top_p=[0.95] * 8)
+    run_rows(q, x, u, **settings_mix(rng, 8, V))
+    run_rows(q, x, u, temperature=[0.8, 1.0, 1.5, 2.5] * 2, top_p=[0.5, 0.9, 0.99, 0.9999] * 2)
+
+
+@pytest.mark.parametrize("V", [50, 3000, 20000])
+def test_sample_strided_rows(q, V):
+    """Rows that begin at any place, of both types."""
+    rng = np.random.default_rng(V)
+    for dtype in (torch.float32, torch.bfloat16):
+        for pad in (1, 2, 3, 5, 7):
+            big = torch.full((9, V + pad), float("nan"), dtype=dtype)
+            big[:, :V] = torch.from_numpy(rng.standard_normal((9, V)) * 3).to(dtype)
+            dev = big.to(DEV)
+            run_rows(q, big[:, :V], rng.random(9).tolist(), passed=dev[:, :V], top_p=[0.9] * 9)
+            run_rows(q, big[:, :V], rng.random(9).tolist(), passed=dev[:, :V], temperature=[0.0] * 9)
+
+
+def test_sample_inverts_the_distribution(q):
+    """Evenly spaced numbers give every token its share of them."""
+    rng = np.random.default_rng(1)
+    x = torch.from_numpy(rng.standard_normal(50)).float()
+    M = 4096
+    u = ((np.arange(M) + 0.5) / M).tolist()
+    tokens, probs = run_rows(q, x.expand(M, 50).contiguous(), u)
+    p = torch.softmax(x.double(), 0).numpy()
+    counts = np.bincount(tokens, minlength=50)
+    assert np.abs(counts - p * M).max() <= 1.0 + 1e-3
+
+
+@pytest.mark.parametrize("V", [40, 1500, 9000, 70000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample_equal_logits(q, V, dtype):
+    """All logits equal, or of three values: the lower index comes first, cuts fall among equal ones."""
+    rng = np.random.default_rng(V)
+    M = 10
+    u = rng.random(M).tolist()
+    x = torch.full((M, V), 1.5, dtype=dtype)
+    run_rows(q, x, u)
+    run_rows(q, x, u, top_k=[7, 1, 0, V - 1, V // 2, V // 3, 20, 30, 2, 5])
+    run_rows(q, x, u, top_p=[0.5, 0.1, 0.9, 1.0, 0.25, 0.75, 0.3, 0.6, 0.7, 0.8])
+    assert run_rows(q, x, u, temperature=[0.0] * M)[0].tolist() == [0] * M
+    x = torch.tensor([3.0, 2.0, -0.0, 0.0])[torch.from_numpy(rng.integers(0, 4, (M, V)))].to(dtype)
+    run_rows(q, x, u, top_k=[V // 2] * 5 + [V // 5] * 5, top_p=[0.9, 0.5] * 5, min_p=[0.0, 0.2] * 5)
+    run_rows(q, x, u, temperature=[2.0] * M)
+
+
+def test_sample_masks_and_numbers_that_are_none(q):
+    rng = np.random.default_rng(2)
+    V, inf, nan = 9000, float("inf"), float("nan")
+    for dtype in (torch.float32, torch.bfloat16):
+        most = torch.finfo(dtype).max
+        x = torch.from_numpy(rng.standard_normal((12, V)) * 2).to(dtype)
+        x[0] = -inf                                  # nothing to draw
+        x[1] = nan
+        x[2] = -inf
+        x[2, 777] = -5.0                             # one token
+        x[3, ::2] = -inf                             # a mask
+        x[4, 100:8000] = nan
+        x[5, 17] = inf                               # counts as the largest number: drawn
+        x[6, [40, 3000]] = inf
+        x[7] = -most                                 # a mask of the type's lowest value, everywhere
+        x[8] = -most
+        x[8, 5:9] = 1.0
+        x[9] = most
+        x[10, :4000] = -inf
+        x[10, 8999] = most
+        u = rng.random(12).tolist()
+        for setting in (dict(), dict(top_k=[50] * 12), dict(top_p=[0.9] * 12), dict(min_p=[0.1] * 12),
+                        dict(temperature=[0.0] * 12), dict(temperature=[1e-38, 1e-20, 0.01, 0.1, 1e9, inf] * 2),
+                        dict(temperature=[5.0] * 12, top_k=[20] * 12, top_p=[0.8] * 12)):
+            y = x.float().clamp(max=most).to(dtype) if dtype == torch.bfloat16 else x
+            tokens, probs = run_rows(q, y, u, passed=x.to(DEV), **setting)
+            assert tokens[:2].tolist() == [-1, -1] and tokens[2] == 777 and tokens[5] == 17 and tokens[6] in (40, 3000)
+            assert tokens[8] in (5, 6, 7, 8) or (setting.get("temperature") or [0])[0] == 1e-38
+    # a temperature that is no number is greedy; negative settings are none
+    x = torch.from_numpy(rng.standard_normal((3, 100))).float()
+    t, p = q.sample_logits(x.to(DEV), torch.full((3,), 0.7, device=DEV), temperature=torch.tensor([nan, -1.0, -inf], device=DEV))
+    assert torch.equal(t.cpu().long(), x.argmax(1)) and (p == 1).all()
+    run_rows(q, x, [0.7] * 3, top_k=[-1, -100, 0], min_p=[-1.0, 0.0, -0.5])
+    t, _ = q.sample_logits(x.to(DEV), torch.full((3,), 0.7, device=DEV), top_p=torch.full((3,), nan, device=DEV),
+                           min_p=torch.full((3,), nan, device=DEV))
+    assert torch.equal(t, q.sample_logits(x.to(DEV), torch.full((3,), 0.7, device=DEV))[0])
+
+
+def test_sample_far_tails(q):
+    """Draws and cuts below the bins: a lone head far above a bulk that has most of the mass, cold and hot rows."""
+    rng = np.random.default_rng(4)
+    V = 30000
+    x = torch.from_numpy(rng.standard_normal((8, V))).float()
+    x[:, 11] += torch.tensor([20.0, 40.0, 10.0, 25.0, 30.0, 60.0, 100.0, 15.0])
+    u = rng.random(8).tolist()
+    run_rows(q, x, u, temperature=[5.0, 8.0, 2.0, 6.0, 10.0, 20.0, 30.0, 64.0])
+    run_rows(q, x, u, temperature=[5.0, 8.0, 2.0, 6.0, 10.0, 20.0, 30.0, 64.0], top_p=[0.999] * 4 + [0.5] * 4)
+    run_rows(q, x, u, temperature=[4.0] * 8, top_k=[300, 3000, 20000, 29999] * 2)
+    run_rows(q, x, u, temperature=[0.02] * 8, top_k=[300, 3000] * 4)
+    run_rows(q, x, [0.9999999] * 8, temperature=[1.0] * 8)
+
+
+def test_sample_streams_and_capture(q):
+    rng = np.random.default_rng(5)
+    x = torch.from_numpy(rng.standard_normal((20, 60000)) * 2).float()
+    d, u = x.to(DEV), torch.rand(20, generator=gen(1)).to(DEV)
+    kw = dict(temperature=torch.full((20,), 0.8, device=DEV), top_k=torch.full((20,), 40, dtype=torch.int32, device=DEV))
+    want, wp = q.sample_logits(d, u, **kw)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    tokens, probs = torch.empty_like(want), torch.empty_like(wp)
+    got = q.sample_logits(d, u, **kw, tokens=tokens, probs=probs, stream=s)
+    s.synchronize()
+    assert torch.equal(tokens, want) and torch.equal(probs, wp) and got[0].data_ptr() == tokens.data_ptr()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a, b = q.sample_logits(d, u, **kw)
+    for _ in range(3):
+        u.copy_(torch.rand(20, generator=gen(7)).to(DEV))
+        g.replay()
+        torch.cuda.synchronize()
+        e, f = q.sample_logits(d, u, **kw)
+        assert torch.equal(a, e) and torch.equal(b, f)
+
+
+def test_sample_refusals(q):
+    x, u = torch.zeros((3, 100), device=DEV), torch.zeros(3, device=DEV)
+    for bad in (dict(logits=x.double()), dict(logits=x.half()), dict(logits=x[0]), dict(logits=x.t()), dict(u=u[:2]),
+                dict(u=u.double()), dict(u=u.cpu()), dict(temperature=u[:1]), dict(top_k=u), dict(top_p=u.double()),
+                dict(min_p=u.int()), dict(tokens=u), dict(probs=u.int())):
+        with pytest.raises(ValueError):
+            q.sample_logits(**{**dict(logits=x, u=u), **bad})
+    with pytest.raises(q.QGError):
+        q.sample_logits(torch.zeros((1, 400000), device=DEV), u[:1])

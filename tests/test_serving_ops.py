@@ -79,3 +79,32 @@ def test_shared_attention_refusals(L):
     assert call(wsb=need - 1) == 4 and call(off=dict(ws=None)) == 4
     assert call(R=1024, T=1 << 20, mb=1 << 26, wsb=1 << 40) == 3
     assert call(groups=1024, T=1 << 20, mpb=1 << 26, wsb=1 << 40) == 3
+
+
+def test_sample_oracle_by_hand():
+    x = np.log([0.1, 0.4, 0.1, 0.2, 0.2])
+    for u, want in ((0.0, 1), (0.39, 1), (0.41, 3), (0.59, 3), (0.61, 4), (0.81, 0), (0.91, 2), (0.9999, 2)):
+        order, C, n, i = od.sample(x, u)
+        assert order.tolist() == [1, 3, 4, 0, 2] and n == 5 and order[i] == want
+    assert od.sample(x, 0.99, top_k=2)[2] == 2 and od.sample(x, 0.99, top_p=0.61)[2] == 3
+    assert od.sample(x, 0.99, top_k=3, top_p=0.7)[2] == 2          # 0.6 of 0.8 is 0.75
+    assert od.sample(x, 0.99, min_p=0.4)[2] == 3 and od.sample(x, 0.99, top_p=0.0)[2] == 1
+    assert od.sample(x, 0.99, temperature=0.0)[2:] == (1, 0)
+    assert od.sample(np.full(3, -np.inf), 0.5)[3] == -1
+    order, _, n, i = od.sample(np.array([np.nan, 1.0, np.inf, np.inf, -np.inf]), 0.6)
+    assert order.tolist() == [2, 3, 1] and order[i] == 3
+
+
+def test_sample_refusals(L):
+    names = ("x", "u", "t", "k", "p", "mp", "tok", "pr")
+
+    def call(dt=1, stride=100, M=2, V=100, kb=4, off={}):
+        a = {n: P(off.get(n, A)) for n in names}
+        return L.sample_logits(a["x"], dt, stride, M, V, a["u"], a["t"], a["k"], kb, a["p"], a["mp"], a["tok"], a["pr"], None)
+    for n in names:
+        assert call(off={n: A + 8}) == 2, n
+    for n in ("x", "u", "tok"):
+        assert call(off={n: None}) == 1, n
+    for bad in (dict(dt=2), dict(stride=99), dict(M=0), dict(M=(1 << 20) + 1), dict(V=0), dict(kb=2)):
+        assert call(**bad) == 1, bad
+    assert call(V=393217, stride=393217) == 3
