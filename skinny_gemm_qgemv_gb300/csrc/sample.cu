@@ -11,7 +11,8 @@
 // copy each: HBM is read once), takes the maximum, and counts the tokens in 2047
 // bins of equal width below it; what a cut or the draw needs of the order lies in
 // one bin, or for small cuts in the first few: those tokens alone are gathered and
-// sorted by one CTA.
+// sorted by one CTA. For cuts that keep a few hundred tokens a sample tells where
+// they begin, and nothing is counted.
 //
 // Sums are whole numbers, in units of 2^-43 of the largest weight, so no order of
 // atomics or of threads changes them. A bin's sum is its count times the weight of
@@ -48,6 +49,8 @@ struct Row {  // what the CTAs of a cluster tell one another
   float max[kMaxCluster];
   int lowest[kMaxCluster];
   int count[kMaxCluster], over[kMaxCluster], listed[kMaxCluster], landed[kMaxCluster];
+  float bound[kMaxCluster];
+  int done;
   u64 mass[kMaxCluster], tail[kMaxCluster], sum[2][kMaxCluster];
   Found found[2];    // of two searches in turn
   u64 result[2];  // of a walk through a sorted list: the sum at its end, the place
@@ -202,8 +205,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     fence_mbar_init();
   }
   if (tid < 128) pow[tid >> 6][tid & 63] = (u64)(exp2(-(double)(tid & 63) / (tid < 64 ? 64. : 4096.)) * 9223372036854775808.);
-#pragma unroll 1
-  for (int i = tid; i < 2 * kBins; i += kThreads) cnt[i] = 0;
   cluster_arrive();  // every CTA of the cluster runs once this is through: its memory may be written
   pdl_wait();
   pdl_launch_dependents();
@@ -349,10 +350,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     bool few = k > 0 && k <= kFewK;  // the bins only count, and are of the logits' scale
     bool done = false;
     float c_bin = 0.f;
+    float drawn = 0.f;  // the token's logit
 
     // ---- the bins and what lies before each of this CTA's own
     auto histogram = [&]() {
       c_bin = few ? kFewScale : s.ch;
+#pragma unroll 1
+      for (int i = tid; i < 2 * kBins; i += kThreads) cnt[i] = 0;
+      __syncthreads();
       int over = 0;
       float tail = 0.f;
       if (few) {
@@ -493,6 +498,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       cluster_sync();
       return row.found[search_turn];
     };
+    // `count` keys of sorted[] in descending order, equal ones in any (there are none): exchanges within 32 places by
+    // shuffles, wider ones in shared memory
+    auto sort = [&](int count) {
+      int width = 32;
+      while (width < count) width <<= 1;
+#pragma unroll 1
+      for (int i = count + tid; i < width; i += kThreads) sorted[i] = 0ull;
+      __syncthreads();
+      auto within = [&](int from, int to) {  // the steps of up to 16 places of the spans from .. to
+#pragma unroll 1
+        for (int i = tid; i < width; i += kThreads) {
+          u64 v = sorted[i];
+#pragma unroll 1
+          for (int span = from; span <= to; span <<= 1) {
+            const bool up = (i & span) == 0;
+#pragma unroll 1
+            for (int step = min(span >> 1, 16); step > 0; step >>= 1) {
+              const u64 q = __shfl_xor_sync(0xffffffffu, v, step);
+              v = ((i & step) == 0) == up ? max(v, q) : min(v, q);
+            }
+          }
+          sorted[i] = v;
+        }
+        __syncthreads();
+      };
+      within(2, 32);
+#pragma unroll 1
+      for (int span = 64; span <= width; span <<= 1) {
+#pragma unroll 1
+        for (int step = span >> 1; step >= 32; step >>= 1) {
+#pragma unroll 1
+          for (int i = tid; i < width / 2; i += kThreads) {
+            const int x = 2 * i - (i & (step - 1)), y = x + step;
+            const u64 p = sorted[x], q = sorted[y];
+            if ((p < q) == ((x & span) == 0)) sorted[x] = q, sorted[y] = p;
+          }
+          __syncthreads();
+        }
+        within(span, span);
+      }
+    };
+    // the CTAs' lists, of which row.listed tells, sorted in CTA 0; their number
+    auto collect = [&]() {
+      int count = 0;
+#pragma unroll 1
+      for (int r = 0; r < cluster; ++r) {
+        const int some = min(row.listed[r], kList - count);
+#pragma unroll 1
+        for (int i = tid; i < some; i += kThreads) sorted[count + i] = get64(list + i, r);
+        count += some;
+      }
+      sort(count);
+      return count;
+    };
+    auto put_in_list = [&](float x, int i, int j) {
+      const int at = atomicAdd(&taken, 1);
+      if (at < kList) list[at] = (u64)key_of(x) << 32 | (uint32_t)~index_of(i, j);
+    };
     // The tokens of bins lo .. hi, no more than kList of them, sorted in CTA 0: keys in descending order with
     // the complement of the index below.
     auto gather = [&](int lo, int hi) {
@@ -500,43 +563,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       __syncthreads();
       sweep([&](float x, int i, int j) {
         const int b = bin_of(top - x, c_bin);
-        if (b >= lo && b <= hi && x > -INFINITY) {
-          const int at = atomicAdd(&taken, 1);
-          if (at < kList) list[at] = (u64)key_of(x) << 32 | (uint32_t)~index_of(i, j);
-        }
+        if (b >= lo && b <= hi && x > -INFINITY) put_in_list(x, i, j);
       });
       __syncthreads();
       if (tid == 0) put32(&row.listed[rank], 0, (uint32_t)min(taken, kList));
       cluster_sync();
-      int count = 0;
-      if (rank == 0) {
-#pragma unroll 1
-        for (int r = 0; r < cluster; ++r) {
-          const int some = min(row.listed[r], kList - count);
-#pragma unroll 1
-          for (int i = tid; i < some; i += kThreads) sorted[count + i] = get64(list + i, r);
-          count += some;
-        }
-        int width = 32;
-        while (width < count) width <<= 1;
-#pragma unroll 1
-        for (int i = count + tid; i < width; i += kThreads) sorted[i] = 0ull;
-        __syncthreads();
-#pragma unroll 1
-        for (int span = 2; span <= width; span <<= 1) {
-#pragma unroll 1
-          for (int step = span >> 1; step > 0; step >>= 1) {
-#pragma unroll 1
-            for (int i = tid; i < width / 2; i += kThreads) {
-              const int x = 2 * i - (i & (step - 1)), y = x + step;
-              const u64 p = sorted[x], q = sorted[y];
-              if ((p < q) == ((x & span) == 0)) sorted[x] = q, sorted[y] = p;
-            }
-            __syncthreads();
-          }
-        }
-      }
-      return count;
+      return rank == 0 ? collect() : 0;
     };
     // In CTA 0, of a sorted list: the sums of the weights up to each of the thread's two places 2 tid, 2 tid + 1
     auto prefix = [&](int count, u64 (&sum)[2]) {
@@ -573,6 +605,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       if (tid == i >> 1) row.result[0] = sum[i & 1];
       __syncthreads();
       return row.result[0];
+    };
+
+    // In CTA 0, the token of a list that begins with all that is kept (of the k first where `by_k`); false: it does not
+    // (unless it is sure to), its tokens have too little of the mass for top-p
+    auto draw = [&](int count, bool by_k, bool sure) {
+      u64 sum[2];
+      prefix(count, sum);
+      int keep = by_k ? min(k, count) : count, pass = count;
+      if (has_m) {
+        pass = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          pass += 2 * tid + j < count && value_of((uint32_t)(sorted[2 * tid + j] >> 32)) >= least;
+        pass = cta_all(pass, Add(), part32);
+      }
+      if (has_p) {
+        const u64 z = by_k ? sum_at(sum, keep - 1) : Z;
+        const int at = reach(sum, keep, 0, max(1ull, share(p64, z)));
+        if (at == keep && !sure && !by_k && pass == count && sum_at(sum, count - 1) < Z - (Z >> 20)) return false;
+        keep = min(keep, at + 1);
+      }
+      keep = min(keep, pass);
+      keep = max(keep, 1);
+      drawn_of = sum_at(sum, keep - 1);
+      const int at = min(reach(sum, keep, 0, past(u64_, drawn_of)), keep - 1);
+      token = (int)~(uint32_t)sorted[at];
+      drawn = value_of((uint32_t)(sorted[at] >> 32));
+      return true;
     };
 
     // ---- where a bin holds more than a list does, or the target lies below the bins: by halving the numbers that the
@@ -629,23 +689,106 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       }
       return lo;
     };
-    float drawn = 0.f;  // the token's logit
+
+    // ---- Short of counting all tokens: a bound below which a few hundred lie above is guessed from a sample, and what
+    // lies above it gathered, with the sum of all weights where top-p needs that. If what is kept proves to reach further
+    // (or the bound to be far off), the bins below decide.
+    const bool every = a.V <= kList;  // a list holds the whole row
+    if (every || (k ? k <= kList / 2 : has_p || has_m)) {
+      float bound = -kMost;
+      if (!every && !k && !has_p) {
+        bound = fmaxf(least, -kMost);
+      } else if (!every) {
+        // The r-th largest of the warps' largest sampled logits: of 16 warps' samples together about the
+        // 16 (1 / 16 + .. + 1 / (17 - r))-th largest. A thread samples one unit.
+        float best = -INFINITY;
+        const int i = n > kThreads ? (int)((long long)tid * n / kThreads) : tid;
+        if (i < n) {
+          float x[PER];
+          unpack<F32>(slice[i], x);
+#pragma unroll
+          for (int j = 0; j < PER; ++j) best = fmaxf(best, x[j]);
+        }
+        best = warp_all(best, Max());
+        __syncthreads();
+        if (lane == 0) partf[warp] = best;
+        __syncthreads();
+        const float want = (float)min(600, max(250, 4 * k)) / (float)cluster * (float)kThreads / (float)max(n, kThreads);
+        int r = 0;
+        for (float at = 0.f; r < kWarps && at < want; ++r) at += 16.f / (float)(kWarps - r);
+        r = max(r, 1);
+        const float mine = partf[lane & (kWarps - 1)];
+        int above = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) above += partf[w] > mine || (partf[w] == mine && w < (lane & (kWarps - 1)));
+        const unsigned it = __ballot_sync(0xffffffffu, above == r - 1);
+        bound = __shfl_sync(0xffffffffu, mine, __ffs(it) - 1);
+        // the middle one of the CTAs'
+        if (tid < cluster) put32(&row.bound[rank], tid, __float_as_uint(bound));
+        cluster_sync();
+        float middle_one = bound;
+        for (int q = 0; q < cluster; ++q) {
+          int more = 0;
+          for (int o = 0; o < cluster; ++o) more += row.bound[o] > row.bound[q] || (row.bound[o] == row.bound[q] && o < q);
+          if (more == cluster / 2) middle_one = row.bound[q];
+        }
+        bound = fmaxf(middle_one, -kMost);
+      }
+      if (tid == 0) taken = 0;
+      __syncthreads();
+      float mass = 0.f;
+      const float c1 = -s.ch / (float)(64 << s.sj), c2 = -s.cl / (float)(64 << s.sj);
+      const bool need_z = has_p && !k && !every;
+      sweep([&](float x, int i, int j) {
+        if (x >= bound) put_in_list(x, i, j);
+        if (need_z) {
+          const float d = top - x;
+          mass += ex2(fmaxf(fmaf(d, c1, d * c2), -200.f));  // (of -infinity that sum is no number)
+        }
+      });
+      const u64 mine = need_z ? cta_all((u64)(mass * 8796093022208.f), Add(), part64) : 0ull;
+      __syncthreads();
+      if (tid < cluster) {
+        put32(&row.listed[rank], tid, (uint32_t)taken);
+        put64(&row.mass[rank], tid, mine);
+      }
+      cluster_sync();
+      int count = 0;
+      for (int r = 0; r < cluster; ++r) count += row.listed[r], Z += row.mass[r];
+      if (count > 0 && count <= kList && (count >= k || every)) {
+        bool ok = true;
+        if (rank == 0) {
+          count = collect();
+          if (every) {  // (all weights, and k as if there were no more than that)
+            u64 sum[2];
+            prefix(count, sum);
+            Z = sum_at(sum, count - 1);
+          }
+          ok = draw(count, k > 0, false);
+        }
+        if (need_z) {
+          if (tid < cluster && rank == 0) put32(&row.done, tid, ok);
+          cluster_sync();
+          ok = row.done != 0;
+        }
+        done = ok;
+      }
+      if (!done) Z = 0;
+    }
 
     // ---- small cuts: all that may be kept in one list
-    histogram();
     Found kth = {};
+    bool has_k = false;
+    if (!done) {
+    histogram();
     if (k && k < finite) kth = find(0, (u64)k);
     if (few && (k >= finite || kth.bin == kOver || kth.n + kth.count > kList)) {
       // the k-th does not lie in a list's reach: bins of weights
       few = false;
-      cluster_sync();
-#pragma unroll 1
-      for (int i = tid; i < 2 * kBins; i += kThreads) cnt[i] = 0;
-      __syncthreads();
       histogram();
       if (k && k < finite) kth = find(0, (u64)k);
     }
-    const bool has_k = k && k < finite;
+    has_k = k && k < finite;
     int last = kOver, upto = kList + 1;  // a bin that holds the end of what is kept, and the tokens up to its end
     if (has_k) {
       last = kth.bin, upto = kth.n + kth.count;
@@ -663,28 +806,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     }
     if (last != kOver && upto <= kList) {
       const int count = gather(0, last);
-      if (rank == 0) {
-        u64 sum[2];
-        prefix(count, sum);
-        int keep = has_k ? min(k, count) : count;
-        if (has_p) {
-          const u64 z = has_k ? sum_at(sum, keep - 1) : Z;
-          keep = min(keep, reach(sum, keep, 0, max(1ull, share(p64, z))) + 1);
-        }
-        if (has_m) {
-          int pass = 0;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            pass += 2 * tid + j < count && value_of((uint32_t)(sorted[2 * tid + j] >> 32)) >= least;
-          keep = min(keep, cta_all(pass, Add(), part32));
-        }
-        keep = max(keep, 1);
-        drawn_of = sum_at(sum, keep - 1);
-        const int at = min(reach(sum, keep, 0, past(u64_, drawn_of)), keep - 1);
-        token = (int)~(uint32_t)sorted[at];
-        drawn = value_of((uint32_t)(sorted[at] >> 32));
-      }
+      if (rank == 0) draw(count, has_k, true);
       done = true;
+    }
     }
     if (!done) {
       // ---- large cuts, or none: each one's end lies in one bin
