@@ -148,11 +148,64 @@ __device__ __forceinline__ float deviation(const Scale& s, float x, float a, flo
   const float r = fmaf(a, s.ch, -b) + fmaf(a, s.cl, e * s.ch), y = r * s.per;
   return y * fmaf(y, fmaf(y, 1.f / 6.f, -0.5f), 1.f);
 }
-// 2^(-b / S) in units of 2^-63, from the powers of 2^(-1/64) and 2^(-1/4096)
+// 2^(-i / 64) and 2^(-i / 4096), i = 0 .. 63, in units of 2^-63, rounded to nearest
+__constant__ u64 kPow[2][64] = {
+    {
+     0x8000000000000000ull, 0x7e9f06067a4360baull, 0x7d41d96db915019dull, 0x7be86fb985689ddcull,
+     0x7a92be8a92436616ull, 0x7940bb9e2cffd89dull, 0x77f25ccdee6d7ae6ull, 0x76a7980f6cca15c2ull,
+     0x75606373ee921c97ull, 0x741cb5281e25ee34ull, 0x72dc8373be41a454ull, 0x719fc4b95f452d29ull,
+     0x70666f76154a7089ull, 0x6f307a412f074892ull, 0x6dfddbcbed791babull, 0x6cce8ae13c57ebdbull,
+     0x6ba27e656b4eb57aull, 0x6a79ad55e7f6fd10ull, 0x69540ec8f895722dull, 0x683199ed779592caull,
+     0x6712460a8fc24072ull, 0x65f60a7f79393e2eull, 0x64dcdec3371793d1ull, 0x63c6ba6455dcd8aeull,
+     0x62b39508aa836d6full, 0x61a3666d124bb204ull, 0x6096266533384a2bull, 0x5f8bccdb3d398841ull,
+     0x5e8451cfac061b5full, 0x5d7fad59099f22feull, 0x5c7dd7a3b17dcf75ull, 0x5b7ec8f19468bbc9ull,
+     0x5a827999fcef3242ull, 0x5988e20954889245ull, 0x5891fac0e95612c8ull, 0x579dbc56b48521baull,
+     0x56ac1f752150a563ull, 0x55bd1cdad49f699cull, 0x54d0ad5a753e077cull, 0x53e6c9da74b29ab5ull,
+     0x52ff6b54d8a89c75ull, 0x521a8ad704f3404full, 0x513821818624b40cull, 0x50582887dcb8a7e1ull,
+     0x4f7a993048d088d7ull, 0x4e9f6cd3967fdba8ull, 0x4dc69cdceaa72a9cull, 0x4cf022c9905bfd32ull,
+     0x4c1bf828c6dc54b8ull, 0x4b4a169b900c2d00ull, 0x4a7a77d47f7b84b1ull, 0x49ad159789f37496ull,
+     0x48e1e9b9d588e19bull, 0x4818ee218a3358eeull, 0x47521cc5a2e6a9e0ull, 0x468d6fadbf2dd4f3ull,
+     0x45cae0f1f545eb73ull, 0x450a6abaa4b77ecdull, 0x444c0740496d4294ull, 0x438fb0cb4f468808ull,
+     0x42d561b3e6243d8aull, 0x421d1461d66f2023ull, 0x4166c34c5615d0ecull, 0x40b268f9de0183baull,
+    },
+    {
+     0x8000000000000000ull, 0x7ffa748dff8dc61full, 0x7ff4e9597bed93abull, 0x7fef5e6272758c21ull,
+     0x7fe9d3a8e07bf086ull, 0x7fe4492cc3571f68ull, 0x7fdebeee185d94ddull, 0x7fd934ecdce5ea7dull,
+     0x7fd3ab290e46d769ull, 0x7fce21a2a9d73041ull, 0x7fc89859acede72aull, 0x7fc30f4e14e20bc6ull,
+     0x7fbd867fdf0acb3bull, 0x7fb7fdef08bf7027ull, 0x7fb2759b8f5762aaull, 0x7faced85702a285dull,
+     0x7fa765aca88f6453ull, 0x7fa1de1135ded717ull, 0x7f9c56b315705eaeull, 0x7f96cf92449bf692ull,
+     0x7f9148aec0b9b7b1ull, 0x7f8bc2088721d86full, 0x7f863b9f952caca0ull, 0x7f80b573e832a58bull,
+     0x7f7b2f857d8c51e5ull, 0x7f75a9d452925dd4ull, 0x7f702460649d92eaull, 0x7f6a9f29b106d825ull,
+     0x7f651a30352731eeull, 0x7f5f9573ee57c218ull, 0x7f5a10f4d9f1c7ddull, 0x7f548cb2f54e9fdfull,
+     0x7f4f08ae3dc7c426ull, 0x7f4984e6b0b6cc1dull, 0x7f44015c4b756c94ull, 0x7f3e7e0f0b5d77bcull,
+     0x7f38fafeedc8dd26ull, 0x7f33782bf011a9c2ull, 0x7f2df5960f9207e1ull, 0x7f28733d49a43f2dull,
+     0x7f22f1219ba2b4aeull, 0x7f1d6f4302e7eac6ull, 0x7f17eda17cce812eull, 0x7f126c3d06b134faull,
+     0x7f0ceb159deae091ull, 0x7f076a2b3fd67bb2ull, 0x7f01e97de9cf1b6eull, 0x7efc690d992ff22aull,
+     0x7ef6e8da4b544f9aull, 0x7ef168e3fd97a0c6ull, 0x7eebe92aad557001ull, 0x7ee669ae57e964edull,
+     0x7ee0ea6efaaf4479ull, 0x7edb6b6c9302f0dfull, 0x7ed5eca71e4069a1ull, 0x7ed06e1e99c3cb8bull,
+     0x7ecaefd302e950afull, 0x7ec571c4570d5067ull, 0x7ebff3f2938c3f4full, 0x7eba765db5c2af49ull,
+     0x7eb4f905bb0d4f78ull, 0x7eaf7beaa0c8ec3eull, 0x7ea9ff0c64526f40ull, 0x7ea4826b0306df5full,
+    },
+};
+// f z for an fp32 f in [0, 1), rounded up or down: exact (64-bit floating-point instructions, of which GB300 issues two
+// lanes a cycle and SM, would take longer than the sweeps)
+__device__ __forceinline__ u64 times(float f, u64 z, bool up) {
+  const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+  const u64 m = e ? (bits & 0x7FFFFFu) | 0x800000u : bits & 0x7FFFFFu;  // f = m 2^-shift
+  const int shift = 150 - (e ? (int)e : 1);                            // 24 or more
+  const u64 lo = z * m, hi = __umul64hi(z, m);
+  if (shift >= 88) return up && (lo | hi);
+  const u64 whole = shift >= 64 ? hi >> (shift - 64) : hi << (64 - shift) | lo >> shift;
+  const bool left = shift >= 64 ? (hi & ((1ull << (shift - 64)) - 1)) | lo : lo & ((1ull << shift) - 1);
+  return whole + (up && left);
+}
+// 2^(-b / S) in units of 2^-63 for bins below the octave, and the octave
+__device__ __forceinline__ u64 mantissa(const u64 (*pow)[64], int b, int sj) {
+  return __umul64hi(pow[0][b >> sj & 63], pow[1][(b & ((1 << sj) - 1)) << (6 - sj)]) << 1;
+}
 __device__ __forceinline__ u64 middle(const u64 (*pow)[64], int b, int sj) {
   const int octave = b >> (6 + sj);
-  const u64 w = __umul64hi(pow[0][b >> sj & 63], pow[1][(b & ((1 << sj) - 1)) << (6 - sj)]) << 1;
-  return octave > 63 ? 0ull : w >> octave;
+  return octave > 63 ? 0ull : mantissa(pow, b, sj) >> octave;
 }
 __device__ __forceinline__ u64 weight_of(const Scale& s, const u64 (*pow)[64], float x) {
   const float a = s.max - x, th = a * s.ch;
@@ -160,6 +213,16 @@ __device__ __forceinline__ u64 weight_of(const Scale& s, const u64 (*pow)[64], f
   const float bf = rintf(th);
   const long long dev = (long long)(deviation(s, x, a, bf) * 17592186044416.f);  // 2^44
   return __umul64hi(middle(pow, (int)bf, s.sj), (u64)((1ll << 44) - dev));
+}
+
+// weight_of / total as fp32, whatever the weight is
+__device__ __forceinline__ float share_of(const Scale& s, const u64 (*pow)[64], float x, u64 total) {
+  const float a = s.max - x, th = a * s.ch;
+  if (!(th < 1048576.f)) return 0.f;
+  const float bf = rintf(th);
+  const int b = (int)bf, octave = b >> (6 + s.sj);
+  const u64 w = __umul64hi(mantissa(pow, b, s.sj), (u64)((1ll << 44) - (long long)(deviation(s, x, a, bf) * 17592186044416.f)));
+  return octave > 200 ? 0.f : (float)((double)w / (double)total * __hiloint2double((1023 - octave) << 20, 0));
 }
 
 template <bool F32>
@@ -196,6 +259,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   __shared__ float partf[kWarps];
   __shared__ uint64_t bar;
   __shared__ int taken;
+  __shared__ float step_of[2];      // the scale's ch, cl
+  __shared__ double least_of;       // T ln(min_p)
+  __shared__ float least_at;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int m = blockIdx.x / cluster, rank = blockIdx.x % cluster;
   const int size = F32 ? 4 : 2;
@@ -204,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     mbar_init(&bar, 1);
     fence_mbar_init();
   }
-  if (tid < 128) pow[tid >> 6][tid & 63] = (u64)(exp2(-(double)(tid & 63) / (tid < 64 ? 64. : 4096.)) * 9223372036854775808.);
+  if (tid < 128) pow[tid >> 6][tid & 63] = kPow[tid >> 6][tid & 63];
   cluster_arrive();  // every CTA of the cluster runs once this is through: its memory may be written
   pdl_wait();
   pdl_launch_dependents();
@@ -250,6 +316,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   const float p_raw = a.top_p ? a.top_p[m] : 1.f, mp_raw = a.min_p ? a.min_p[m] : 0.f;
   const int k = k_raw > 0 && k_raw < a.V ? (int)k_raw : 0;   // 0: all
   const bool has_p = p_raw < 1.f, has_m = mp_raw > 0.f;
+  int sj = 0;
+  while (sj < 6 && T > (float)(1 << sj)) ++sj;
+  // (by one warp: GB300 has two lanes an SM for 64-bit floating point)
+  if (warp == 1 && !greedy) {
+    const double c = 1.4426950408889634 * (64 << sj) / (double)T, at = has_m ? (double)T * log((double)fminf(mp_raw, 1.f)) : 0.;
+    if (lane == 0) step_of[0] = (float)c, step_of[1] = (float)(c - (double)(float)c), least_of = at;
+  }
   __syncthreads();
   bool landed = __syncthreads_and(mbar_wait(&bar, 0, a.err, kErrSampleWait));
 
@@ -334,16 +407,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   } else {
     Scale s;
     s.max = top;
-    s.sj = 0;
-    while (s.sj < 6 && T > (float)(1 << s.sj)) ++s.sj;
-    const double c = 1.4426950408889634 * (64 << s.sj) / (double)T;
-    s.ch = (float)c, s.cl = (float)(c - (double)s.ch);
+    s.sj = sj;
+    s.ch = step_of[0], s.cl = step_of[1];
     s.per = 0.69314718f / (float)(64 << s.sj);
     // x passes min_p from here on
-    const float least = has_m ? __double2float_ru((double)top + (double)T * log((double)fminf(mp_raw, 1.f))) : -INFINITY;
-    const double p64 = (double)p_raw, u64_ = (double)u;
-    auto share = [](double f, u64 z) { return (u64)ceil(f * (double)z); };  // of a sum, for C >= share
-    auto past = [](double f, u64 z) { return (u64)(f * (double)z) + 1; };   // for C > f z
+    if (has_m) {
+      if (tid == 0) least_at = __double2float_ru((double)top + least_of);
+      __syncthreads();
+    }
+    const float least = has_m ? least_at : -INFINITY, p_share = fmaxf(p_raw, 0.f);
+    auto share = [](float f, u64 z) { return times(f, z, true); };      // of a sum, for C >= share
+    auto past = [](float f, u64 z) { return times(f, z, false) + 1; };  // for C > f z
 
     u64 Z = 0, drawn_of = 0;  // all weights; the kept ones
     int finite = 0;           // tokens above -infinity
@@ -541,13 +615,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     };
     // the CTAs' lists, of which row.listed tells, sorted in CTA 0; their number
     auto collect = [&]() {
-      int count = 0;
+      int ends[kMaxCluster], count = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r < cluster) count += row.listed[r];
+        ends[r] = count;
+      }
+      count = min(count, kList);
 #pragma unroll 1
-      for (int r = 0; r < cluster; ++r) {
-        const int some = min(row.listed[r], kList - count);
-#pragma unroll 1
-        for (int i = tid; i < some; i += kThreads) sorted[count + i] = get64(list + i, r);
-        count += some;
+      for (int i = tid; i < count; i += kThreads) {  // all on the way at once
+        int r = 0, begin = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster - 1; ++q)
+          if (i >= ends[q]) r = q + 1, begin = ends[q];
+        sorted[i] = get64(list + i - begin, r);
       }
       sort(count);
       return count;
@@ -622,14 +703,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       }
       if (has_p) {
         const u64 z = by_k ? sum_at(sum, keep - 1) : Z;
-        const int at = reach(sum, keep, 0, max(1ull, share(p64, z)));
+        const int at = reach(sum, keep, 0, max(1ull, share(p_share, z)));
         if (at == keep && !sure && !by_k && pass == count && sum_at(sum, count - 1) < Z - (Z >> 20)) return false;
         keep = min(keep, at + 1);
       }
       keep = min(keep, pass);
       keep = max(keep, 1);
       drawn_of = sum_at(sum, keep - 1);
-      const int at = min(reach(sum, keep, 0, past(u64_, drawn_of)), keep - 1);
+      const int at = min(reach(sum, keep, 0, past(u, drawn_of)), keep - 1);
       token = (int)~(uint32_t)sorted[at];
       drawn = value_of((uint32_t)(sorted[at] >> 32));
       return true;
@@ -713,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         __syncthreads();
         if (lane == 0) partf[warp] = best;
         __syncthreads();
-        const float want = (float)min(600, max(250, 4 * k)) / (float)cluster * (float)kThreads / (float)max(n, kThreads);
+        const float want = (float)(k ? max(160, 3 * k) : 300) / (float)cluster * (float)kThreads / (float)max(n, kThreads);
         int r = 0;
         for (float at = 0.f; r < kWarps && at < want; ++r) at += 16.f / (float)(kWarps - r);
         r = max(r, 1);
@@ -794,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       last = kth.bin, upto = kth.n + kth.count;
     } else if (has_p) {
       // (a little further: the sums of the bins and of single tokens differ in their last digits)
-      const Found f = find(1, min(Z, max(1ull, share(p64, Z) + (Z >> 20))));
+      const Found f = find(1, min(Z, max(1ull, share(p_share, Z) + (Z >> 20))));
       last = f.bin, upto = f.n + f.count;
     }
     if (has_m && !(has_k && has_p)) {  // (top-p after top-k needs the k first)
@@ -829,12 +910,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       };
       if (has_k) drawn_of = end_of(0, kth, (u64)k);
       if (has_p) {
-        const u64 want = max(1ull, share(p64, drawn_of));
+        const u64 want = max(1ull, share(p_share, drawn_of));
         const Found f = find(1, want);
         drawn_of = min(drawn_of, end_of(1, f, want));
       }
       if (has_m) drawn_of = min(drawn_of, mass_from(key_of(fmaxf(least, -kMost))));
-      const u64 want = past(u64_, drawn_of);
+      const u64 want = past(u, drawn_of);
       const Found f = find(1, want);
       if (f.bin == kOver || f.count > kList) {
         const Place at = search(1, min(want, mass_from(key_of(-kMost))));
@@ -852,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       }
     }
     if (rank == 0 && tid == 0)
-      prob = (float)(exp(((double)drawn - (double)top) / (double)T) * 8796093022208. / (double)drawn_of);
+      prob = share_of(s, pow, drawn, drawn_of);
   }
   if (rank == 0 && tid == 0) {
     a.tokens[m] = token;
