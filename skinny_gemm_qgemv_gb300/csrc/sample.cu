@@ -225,22 +225,22 @@ __device__ __forceinline__ float share_of(const Scale& s, const u64 (*pow)[64], 
   return octave > 200 ? 0.f : (float)((double)w / (double)total * __hiloint2double((1023 - octave) << 20, 0));
 }
 
+// four consecutive elements
 template <bool F32>
-struct Elem {
-  static constexpr int kPer = F32 ? 4 : 8;  // of 16 bytes
-};
-template <bool F32>
-__device__ __forceinline__ void unpack(const uint4& v, float (&x)[Elem<F32>::kPer]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < Elem<F32>::kPer; ++j)
-    x[j] = __uint_as_float(F32 ? w[j % 4] : j & 1 ? w[j / 2 % 4] & 0xFFFF0000u : w[j / 2 % 4] << 16);
+__device__ __forceinline__ void quad(const uint8_t* slice, int i, float (&x)[4]) {
+  if (F32) {
+    const float4 v = reinterpret_cast<const float4*>(slice)[i];
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = reinterpret_cast<const uint2*>(slice)[i];
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int cluster) {
-  using E = Elem<F32>;
-  constexpr int PER = E::kPer;
+  constexpr int PER = F32 ? 4 : 8;  // elements of 16 bytes
   extern __shared__ __align__(16) uint8_t smem[];
   // layout: bins' counts | their deviations | sums before this CTA's bins | tokens before them | the slice
   int* cnt = reinterpret_cast<int*>(smem);
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   const int own_bins = kBins / cluster;
   u64* before_m = reinterpret_cast<u64*>(dev + kBins);
   int* before_n = reinterpret_cast<int*>(before_m + own_bins);
-  uint4* slice = reinterpret_cast<uint4*>(before_n + own_bins);
+  uint8_t* slice = reinterpret_cast<uint8_t*>(before_n + own_bins);
   // a gathered list over the counts, its sorted whole (in CTA 0) over the deviations
   u64* list = reinterpret_cast<u64*>(cnt);
   u64* sorted = reinterpret_cast<u64*>(dev);
@@ -292,14 +292,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     const char* src = base + (size_t)(lead + u0 * PER) * size;
 #pragma unroll 1
     for (uint32_t at = 0; at < bytes; at += kPiece)
-      bulk_g2s(reinterpret_cast<uint8_t*>(slice + front) + at, src + at, min(kPiece, bytes - at), &bar);
+      bulk_g2s(slice + 16 * front + at, src + at, min(kPiece, bytes - at), &bar);
   }
   if (tid < 2 * PER) {
     const int j = tid % PER, which = tid / PER;               // 0: the front unit, 1: the back one
     const int e = which ? lead + units * PER + j : lead - PER + j;
     const bool in = which ? j < rest : e >= 0;
     if (which ? back : front) {
-      uint4* to = which ? slice + n - 1 : slice;
+      uint8_t* to = which ? slice + 16 * (n - 1) : slice;
       if (F32)
         reinterpret_cast<uint32_t*>(to)[j] = in ? reinterpret_cast<const uint32_t*>(base)[e] : 0xFF800000u;
       else
@@ -326,15 +326,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   __syncthreads();
   bool landed = __syncthreads_and(mbar_wait(&bar, 0, a.err, kErrSampleWait));
 
-  auto index_of = [&](int i, int j) { return first + i * PER + j; };
-  // f(x, unit, element) of all of the thread's elements
+  const int quads = n * (PER / 4);
+  auto index_of = [&](int i, int j) { return first + 4 * i + j; };
+  // f(x, i, j) of element j of quad i, of all of the thread's (no further unrolled: much of this code runs once a row, and
+  // a row's time is that of fetching it)
   auto sweep = [&](auto&& f) {
-#pragma unroll 2
-    for (int i = tid; i < n; i += kThreads) {
-      float x[PER];
-      unpack<F32>(slice[i], x);
+#pragma unroll 1
+    for (int i = tid; i < quads; i += kThreads) {
+      float x[4];
+      quad<F32>(slice, i, x);
 #pragma unroll
-      for (int j = 0; j < PER; ++j) f(x[j], i, j);
+      for (int j = 0; j < 4; ++j) f(x[j], i, j);
     }
   };
 
@@ -348,21 +350,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   });
   if (__syncthreads_or(odd)) {
 #pragma unroll 1
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < 4 * quads; i += kThreads) {
       if (F32) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(slice + i);
-#pragma unroll 1
-        for (int j = 0; j < PER; ++j) {
-          const float x = __uint_as_float(w[j]);
-          if (!(x <= kMost)) w[j] = x != x ? 0xFF800000u : 0x7F7FFFFFu;
-        }
+        float& x = reinterpret_cast<float*>(slice)[i];
+        if (!(x <= kMost)) x = x != x ? -INFINITY : kMost;
       } else {
-        uint16_t* w = reinterpret_cast<uint16_t*>(slice + i);
-#pragma unroll 1
-        for (int j = 0; j < PER; ++j) {
-          const float x = bf16_bits_to_f32(w[j]);
-          if (!(x <= kMost)) w[j] = x != x ? (uint16_t)0xFF80u : (uint16_t)0x7F7Fu;
-        }
+        uint16_t& w = reinterpret_cast<uint16_t*>(slice)[i];
+        const float x = bf16_bits_to_f32(w);
+        if (!(x <= kMost)) w = x != x ? (uint16_t)0xFF80u : (uint16_t)0x7F7Fu;
       }
     }
     top = fminf(top, F32 ? kMost : __uint_as_float(0x7F7F0000u));
@@ -781,20 +776,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         bound = fmaxf(least, -kMost);
       } else if (!every) {
         // The r-th largest of the warps' largest sampled logits: of 16 warps' samples together about the
-        // 16 (1 / 16 + .. + 1 / (17 - r))-th largest. A thread samples one unit.
+        // 16 (1 / 16 + .. + 1 / (17 - r))-th largest. A thread samples one quad.
         float best = -INFINITY;
-        const int i = n > kThreads ? (int)((long long)tid * n / kThreads) : tid;
-        if (i < n) {
-          float x[PER];
-          unpack<F32>(slice[i], x);
-#pragma unroll
-          for (int j = 0; j < PER; ++j) best = fmaxf(best, x[j]);
+        const int i = quads > kThreads ? (int)((long long)tid * quads / kThreads) : tid;
+        if (i < quads) {
+          float x[4];
+          quad<F32>(slice, i, x);
+          best = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         }
         best = warp_all(best, Max());
         __syncthreads();
         if (lane == 0) partf[warp] = best;
         __syncthreads();
-        const float want = (float)(k ? max(160, 3 * k) : 300) / (float)cluster * (float)kThreads / (float)max(n, kThreads);
+        const float want = (float)(k ? max(160, 3 * k) : 300) / (float)cluster * (float)kThreads / (float)max(quads, kThreads);
         int r = 0;
         for (float at = 0.f; r < kWarps && at < want; ++r) at += 16.f / (float)(kWarps - r);
         r = max(r, 1);
@@ -807,12 +801,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         // the middle one of the CTAs'
         if (tid < cluster) put32(&row.bound[rank], tid, __float_as_uint(bound));
         cluster_sync();
-        float middle_one = bound;
-        for (int q = 0; q < cluster; ++q) {
-          int more = 0;
-          for (int o = 0; o < cluster; ++o) more += row.bound[o] > row.bound[q] || (row.bound[o] == row.bound[q] && o < q);
-          if (more == cluster / 2) middle_one = row.bound[q];
+        const float theirs = row.bound[lane & (cluster - 1)];
+        int more = 0;
+        for (int o = 0; o < cluster; ++o) {
+          const float x = __shfl_sync(0xffffffffu, theirs, o);
+          more += x > theirs || (x == theirs && o < (lane & (cluster - 1)));
         }
+        const float middle_one = __shfl_sync(0xffffffffu, theirs, __ffs(__ballot_sync(0xffffffffu, more == cluster / 2)) - 1);
         bound = fmaxf(middle_one, -kMost);
       }
       if (tid == 0) taken = 0;
