@@ -48,7 +48,7 @@ struct Found {  // a bin: the tokens and the weight before it, the tokens in it
 struct Row {  // what the CTAs of a cluster tell one another
   float max[kMaxCluster];
   int lowest[kMaxCluster];
-  int count[kMaxCluster], over[kMaxCluster], listed[kMaxCluster], landed[kMaxCluster];
+  int count[kMaxCluster], listed[kMaxCluster], landed[kMaxCluster], over;
   float bound[kMaxCluster];
   int done;
   u64 mass[kMaxCluster], tail[kMaxCluster], sum[2][kMaxCluster];
@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   __shared__ float partf[kWarps];
   __shared__ uint64_t bar;
   __shared__ int taken;
+  __shared__ u64 tail_of;           // what lies below the bins
   __shared__ float step_of[2];      // the scale's ch, cl
   __shared__ double least_of;       // T ln(min_p)
   __shared__ float least_at;
@@ -425,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     auto histogram = [&]() {
       c_bin = few ? kFewScale : s.ch;
 #pragma unroll 1
-      for (int i = tid; i < 2 * kBins; i += kThreads) cnt[i] = 0;
+      for (int i = tid; i < 2 * kBins / 4; i += kThreads) reinterpret_cast<int4*>(cnt)[i] = make_int4(0, 0, 0, 0);
+      if (tid == 0) tail_of = 0;
       __syncthreads();
       int over = 0;
       float tail = 0.f;
@@ -452,8 +454,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
           }
         });
       }
-      over = cta_all(over, Add(), part32);
-      const u64 tail_sum = cta_all((u64)(tail * 8796093022208.f), Add(), part64);  // 2^43
+      over = warp_all(over, Add());
+      const u64 tail_part = warp_all((u64)(tail * 8796093022208.f), Add());  // 2^43
+      if (lane == 0 && over) {
+        atomicAdd(cnt + kOver, over);
+        atomicAdd(&tail_of, tail_part);
+      }
       cluster_sync();  // all counts are there
       // this CTA's bins, over the cluster: four or fewer consecutive ones a thread
       const int per = (own_bins + kThreads - 1) / kThreads, b0 = tid * per;
@@ -473,11 +479,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         }
         before_n[i] = mine_n;
         before_m[i] = mine_m;
+        if (b == kOver) {
+          over = count;
+          break;
+        }
         mine_n += count;
         if (!few && count)
           mine_m += __umul64hi(middle(pow, b, s.sj), ((u64)count << 44) - (u64)(deviate * (1ll << (22 - s.sj))));
       }
       // exclusive sums over the threads
+      if (b0 + per >= own_bins && b0 < own_bins && rank == cluster - 1)
+        for (int r = 0; r < cluster; ++r) put32(&row.over, r, (uint32_t)over);
       int inc_n = mine_n;
       u64 inc_m = mine_m;
 #pragma unroll
@@ -499,14 +511,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       if (tid < cluster) {
         put32(&row.count[rank], tid, (uint32_t)total_n);
         put64(&row.mass[rank], tid, total_m);
-        put32(&row.over[rank], tid, (uint32_t)over);
-        put64(&row.tail[rank], tid, tail_sum);
+        put64(&row.tail[rank], tid, tail_of);
       }
       cluster_sync();  // (and all have read the counts: a list may take their place)
-      finite = 0, Z = 0;
+      finite = row.over, Z = 0;
       for (int r = 0; r < cluster; ++r) {
         if (r < rank) base_n += row.count[r], base_m += row.mass[r];
-        finite += row.count[r] + row.over[r];
+        finite += row.count[r];
         Z += row.mass[r] + row.tail[r];
       }
 #pragma unroll 1
