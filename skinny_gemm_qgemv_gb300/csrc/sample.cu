@@ -238,15 +238,19 @@ __device__ __forceinline__ void quad(const uint8_t* slice, int i, float (&x)[4])
   }
 }
 
-template <bool F32>
+// HELD: a cluster per row, which it holds in shared memory; else a CTA per row, which reads it again from L2 in every
+// sweep
+template <bool F32, bool HELD>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int cluster) {
   constexpr int PER = F32 ? 4 : 8;  // elements of 16 bytes
   extern __shared__ __align__(16) uint8_t smem[];
-  // layout: bins' counts | their deviations | sums before this CTA's bins | tokens before them | the slice
+  // layout: bins' counts | their deviations (| both again, of the warps of odd number) | sums before this CTA's bins |
+  // tokens before them | the slice
+  constexpr int kCopies = HELD ? 1 : 2;
   int* cnt = reinterpret_cast<int*>(smem);
   int* dev = cnt + kBins;
-  const int own_bins = kBins / cluster;
-  u64* before_m = reinterpret_cast<u64*>(dev + kBins);
+  const int own_bins = HELD ? kBins / cluster : kBins;
+  u64* before_m = reinterpret_cast<u64*>(cnt + 2 * kCopies * kBins);
   int* before_n = reinterpret_cast<int*>(before_m + own_bins);
   uint8_t* slice = reinterpret_cast<uint8_t*>(before_n + own_bins);
   // a gathered list over the counts, its sorted whole (in CTA 0) over the deviations
@@ -264,7 +268,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   __shared__ double least_of;       // T ln(min_p)
   __shared__ float least_at;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int m = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+  const int m = HELD ? blockIdx.x / cluster : blockIdx.x, rank = HELD ? blockIdx.x % cluster : 0;
+  if (!HELD) cluster = 1;
+  int* my_cnt = cnt + (HELD ? 0 : (warp & 1) * 2 * kBins);
+  int* my_dev = my_cnt + kBins;
   const int size = F32 ? 4 : 2;
 
   if (tid == 0) {
@@ -272,7 +279,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     fence_mbar_init();
   }
   if (tid < 128) pow[tid >> 6][tid & 63] = kPow[tid >> 6][tid & 63];
-  cluster_arrive();  // every CTA of the cluster runs once this is through: its memory may be written
+  if (HELD) cluster_arrive();  // every CTA of the cluster runs once this is through: its memory may be written
+  // of the cluster, or of the CTA alone
+  auto all_sync = [&]() {
+    if (HELD)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
+  auto tell32 = [&](const void* at, int r, uint32_t v) {
+    if (HELD)
+      put32(at, r, v);
+    else
+      *reinterpret_cast<volatile uint32_t*>(const_cast<void*>(at)) = v;
+  };
+  auto tell64 = [&](const void* at, int r, u64 v) {
+    if (HELD)
+      put64(at, r, v);
+    else
+      *reinterpret_cast<volatile u64*>(const_cast<void*>(at)) = v;
+  };
+  auto ask32 = [&](const void* at, int r) { return HELD ? get32(at, r) : *static_cast<const uint32_t*>(at); };
+  auto ask64 = [&](const void* at, int r) { return HELD ? get64(at, r) : *static_cast<const u64*>(at); };
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
@@ -286,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   const int front = rank == 0 && lead ? 1 : 0, back = rank == cluster - 1 && rest ? 1 : 0;
   const int n = front + (u1 - u0) + back;                    // units in shared memory
   const int first = lead + (u0 - front) * PER;               // index of the first one's first element
-  if (tid == 0) {
+  if (HELD && tid == 0) {
     const uint32_t bytes = (uint32_t)(u1 - u0) * 16u;
     mbar_arrive_expect_tx(&bar, bytes);
     constexpr uint32_t kPiece = 32768u;
@@ -295,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     for (uint32_t at = 0; at < bytes; at += kPiece)
       bulk_g2s(slice + 16 * front + at, src + at, min(kPiece, bytes - at), &bar);
   }
-  if (tid < 2 * PER) {
+  if (HELD && tid < 2 * PER) {
     const int j = tid % PER, which = tid / PER;               // 0: the front unit, 1: the back one
     const int e = which ? lead + units * PER + j : lead - PER + j;
     const bool in = which ? j < rest : e >= 0;
@@ -325,31 +353,77 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     if (lane == 0) step_of[0] = (float)c, step_of[1] = (float)(c - (double)(float)c), least_of = at;
   }
   __syncthreads();
-  bool landed = __syncthreads_and(mbar_wait(&bar, 0, a.err, kErrSampleWait));
+  bool landed = !HELD || __syncthreads_and(mbar_wait(&bar, 0, a.err, kErrSampleWait));
 
+  constexpr float kMost = 3.402823466e+38f;
+  const float largest = F32 ? kMost : __uint_as_float(0x7F7F0000u);
   const int quads = n * (PER / 4);
   auto index_of = [&](int i, int j) { return first + 4 * i + j; };
-  // f(x, i, j) of element j of quad i, of all of the thread's (no further unrolled: much of this code runs once a row, and
-  // a row's time is that of fetching it)
-  auto sweep = [&](auto&& f) {
+  auto load = [&](int i, float (&x)[4]) {
+    if (HELD) {
+      quad<F32>(slice, i, x);
+      return;
+    }
+    const int e = first + 4 * i;
+    if (e >= 0 && e + 4 <= a.V) {
+      quad<F32>(reinterpret_cast<const uint8_t*>(base) + (long long)e * size, 0, x);
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        float v = -INFINITY;
+        if (e + j >= 0 && e + j < a.V)
+          v = F32 ? reinterpret_cast<const float*>(base)[e + j] : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(base)[e + j]);
+        x[0] = j == 0 ? v : x[0], x[1] = j == 1 ? v : x[1], x[2] = j == 2 ? v : x[2], x[3] = j == 3 ? v : x[3];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = fminf(fmaxf(x[j], -INFINITY), largest);
+  };
+  // f(x, i, j) of element j of quad i, of all of the thread's. Held rows: no further unrolled (much of this code runs once
+  // a row, and a short row's time is that of fetching it); others: four loads on the way. `slow`: what rarely runs.
+  auto sweep_slow = [&](auto&& f) {
 #pragma unroll 1
     for (int i = tid; i < quads; i += kThreads) {
       float x[4];
-      quad<F32>(slice, i, x);
+      load(i, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f(x[j], i, j);
+    }
+  };
+  auto sweep = [&](auto&& f) {
+    if (HELD) {
+      sweep_slow(f);
+      return;
+    }
+    constexpr int kDeep = 4;
+    int i = tid;
+#pragma unroll 1
+    for (; i + (kDeep - 1) * kThreads < quads; i += kDeep * kThreads) {
+      float x[kDeep][4];
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) load(i + k * kThreads, x[k]);
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f(x[k][j], i + k * kThreads, j);
+    }
+#pragma unroll 1
+    for (; i < quads; i += kThreads) {
+      float x[4];
+      load(i, x);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f(x[j], i, j);
     }
   };
 
   // ---- the maximum; NaN counts as -infinity, +infinity as the type's largest number
-  constexpr float kMost = 3.402823466e+38f;
   float top = -INFINITY;
   bool odd = false;
   sweep([&](float x, int, int) {
     top = fmaxf(top, x);
     odd |= !(x <= kMost);
   });
-  if (__syncthreads_or(odd)) {
+  if (HELD && __syncthreads_or(odd)) {
 #pragma unroll 1
     for (int i = tid; i < 4 * quads; i += kThreads) {
       if (F32) {
@@ -361,16 +435,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         if (!(x <= kMost)) w = x != x ? (uint16_t)0xFF80u : (uint16_t)0x7F7Fu;
       }
     }
-    top = fminf(top, F32 ? kMost : __uint_as_float(0x7F7F0000u));
+    top = fminf(top, largest);
     __syncthreads();
   }
   top = cta_all(top, Max(), partf);
-  cluster_wait();
+  if (HELD) cluster_wait();
   if (tid < cluster) {
-    put32(&row.max[rank], tid, __float_as_uint(top));
-    put32(&row.landed[rank], tid, landed);
+    tell32(&row.max[rank], tid, __float_as_uint(top));
+    tell32(&row.landed[rank], tid, landed);
   }
-  cluster_sync();
+  all_sync();
   for (int c = 0; c < cluster; ++c) top = fmaxf(top, row.max[c]), landed &= row.landed[c] != 0;
 
   // the whole cluster's sum; `which` alternates between calls, so that one's numbers are read before they are written again
@@ -378,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   auto cluster_sum = [&](u64 v) {
     v = cta_all(v, Add(), part64);
     turn ^= 1;
-    if (tid < cluster) put64(&row.sum[turn][rank], tid, v);
-    cluster_sync();
+    if (tid < cluster) tell64(&row.sum[turn][rank], tid, v);
+    all_sync();
     v = 0;
     for (int c = 0; c < cluster; ++c) v += row.sum[turn][c];
     return v;
@@ -391,12 +465,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     // nothing to draw
   } else if (greedy) {
     int at = 0x7FFFFFFF;
-    sweep([&](float x, int i, int j) {
+    sweep_slow([&](float x, int i, int j) {
       if (x == top) at = min(at, index_of(i, j));
     });
     at = cta_all(at, Min(), part32);
-    if (tid < cluster) put32(&row.lowest[rank], tid, (uint32_t)at);
-    cluster_sync();
+    if (tid < cluster) tell32(&row.lowest[rank], tid, (uint32_t)at);
+    all_sync();
     for (int c = 0; c < cluster; ++c) at = min(at, row.lowest[c]);
     token = at;
     prob = 1.f;
@@ -426,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     auto histogram = [&]() {
       c_bin = few ? kFewScale : s.ch;
 #pragma unroll 1
-      for (int i = tid; i < 2 * kBins / 4; i += kThreads) reinterpret_cast<int4*>(cnt)[i] = make_int4(0, 0, 0, 0);
+      for (int i = tid; i < kCopies * 2 * kBins / 4; i += kThreads) reinterpret_cast<int4*>(cnt)[i] = make_int4(0, 0, 0, 0);
       if (tid == 0) tail_of = 0;
       __syncthreads();
       int over = 0;
@@ -435,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         sweep([&](float x, int, int) {
           const int b = bin_of(top - x, c_bin);
           if (b < kOver)
-            atomicAdd(cnt + b, 1);
+            atomicAdd(my_cnt + b, 1);
           else
             over += x > -INFINITY;
         });
@@ -446,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
           const int b = __float_as_int(bm) & 0xFFF;
           if (b < kOver) {
             const float q = fmaf(deviation(s, x, d, bm - kMagic), unit, kMagic);
-            atomicAdd(cnt + b, 1);
-            atomicAdd(dev + b, __float_as_int(q) - 0x4B400000);
+            atomicAdd(my_cnt + b, 1);
+            atomicAdd(my_dev + b, __float_as_int(q) - 0x4B400000);
           } else {
             over += x > -INFINITY;
             tail += ex2(th * inv_s);
@@ -460,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         atomicAdd(cnt + kOver, over);
         atomicAdd(&tail_of, tail_part);
       }
-      cluster_sync();  // all counts are there
+      all_sync();  // all counts are there
       // this CTA's bins, over the cluster: four or fewer consecutive ones a thread
       const int per = (own_bins + kThreads - 1) / kThreads, b0 = tid * per;
       int mine_n = 0;
@@ -470,11 +544,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         const int b = rank * own_bins + i;
         int count = 0;
         long long deviate = 0;
+        if (!HELD) count = cnt[2 * kBins + b], deviate = dev[2 * kBins + b];
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
+        for (int r = 0; r < (HELD ? kMaxCluster : 1); ++r) {
           if (r < cluster) {
-            count += (int)get32(cnt + b, r);
-            if (!few) deviate += (int)get32(dev + b, r);
+            count += (int)ask32(cnt + b, r);
+            if (!few) deviate += (int)ask32(dev + b, r);
           }
         }
         before_n[i] = mine_n;
@@ -489,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       }
       // exclusive sums over the threads
       if (b0 + per >= own_bins && b0 < own_bins && rank == cluster - 1)
-        for (int r = 0; r < cluster; ++r) put32(&row.over, r, (uint32_t)over);
+        for (int r = 0; r < cluster; ++r) tell32(&row.over, r, (uint32_t)over);
       int inc_n = mine_n;
       u64 inc_m = mine_m;
 #pragma unroll
@@ -509,11 +584,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         total_n += part32[w], total_m += part64[w];
       }
       if (tid < cluster) {
-        put32(&row.count[rank], tid, (uint32_t)total_n);
-        put64(&row.mass[rank], tid, total_m);
-        put64(&row.tail[rank], tid, tail_of);
+        tell32(&row.count[rank], tid, (uint32_t)total_n);
+        tell64(&row.mass[rank], tid, total_m);
+        tell64(&row.tail[rank], tid, tail_of);
       }
-      cluster_sync();  // (and all have read the counts: a list may take their place)
+      all_sync();  // (and all have read the counts: a list may take their place)
       finite = row.over, Z = 0;
       for (int r = 0; r < cluster; ++r) {
         if (r < rank) base_n += row.count[r], base_m += row.mass[r];
@@ -553,10 +628,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
 #pragma unroll 1
       for (int r = 0; r < cluster; ++r) {
         Found* f = &row.found[search_turn];
-        put32(&f->bin, r, (uint32_t)(rank * own_bins + i));
-        put32(&f->n, r, (uint32_t)before_n[i]);
-        put32(&f->count, r, (uint32_t)(end_n(i) - before_n[i]));
-        put64(&f->mass, r, before_m[i]);
+        tell32(&f->bin, r, (uint32_t)(rank * own_bins + i));
+        tell32(&f->n, r, (uint32_t)before_n[i]);
+        tell32(&f->count, r, (uint32_t)(end_n(i) - before_n[i]));
+        tell64(&f->mass, r, before_m[i]);
       }
     };
     // the bin in which the count (which 0) or the sum (1) reaches `want`; kOver where none of the inner ones does
@@ -567,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         const u64 lo = which ? before_m[i] : (u64)before_n[i], hi = which ? end_m(i) : (u64)end_n(i);
         if (lo < want && want <= hi) tell(i);
       }
-      cluster_sync();
+      all_sync();
       Found f = row.found[search_turn];
       if (want > (which ? inner_m() : (u64)inner_n())) f.bin = kOver, f.n = inner_n(), f.count = finite - f.n, f.mass = inner_m();
       return f;
@@ -575,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     auto of_bin = [&](int b) {
       search_turn ^= 1;
       if (b / own_bins == rank && tid == b % own_bins % kThreads) tell(b % own_bins);
-      cluster_sync();
+      all_sync();
       return row.found[search_turn];
     };
     // `count` keys of sorted[] in descending order, equal ones in any (there are none): exchanges within 32 places by
@@ -634,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
 #pragma unroll
         for (int q = 0; q < kMaxCluster - 1; ++q)
           if (i >= ends[q]) r = q + 1, begin = ends[q];
-        sorted[i] = get64(list + i - begin, r);
+        sorted[i] = ask64(list + i - begin, r);
       }
       sort(count);
       return count;
@@ -653,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         if (b >= lo && b <= hi && x > -INFINITY) put_in_list(x, i, j);
       });
       __syncthreads();
-      if (tid == 0) put32(&row.listed[rank], 0, (uint32_t)min(taken, kList));
-      cluster_sync();
+      if (tid == 0) tell32(&row.listed[rank], 0, (uint32_t)min(taken, kList));
+      all_sync();
       return rank == 0 ? collect() : 0;
     };
     // In CTA 0, of a sorted list: the sums of the weights up to each of the thread's two places 2 tid, 2 tid + 1
@@ -726,14 +801,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     // order's keys, then the indexes of equal ones, may be (slow, for rows of many equal logits, or very flat ones)
     auto mass_from = [&](uint32_t key) {
       u64 w = 0;
-      sweep([&](float x, int, int) {
+      sweep_slow([&](float x, int, int) {
         if (key_of(x) >= key) w += weight_of(s, pow, x);
       });
       return cluster_sum(w);
     };
     auto count_from = [&](uint32_t key) {
       u64 w = 0;
-      sweep([&](float x, int, int) { w += key_of(x) >= key && x > -INFINITY; });
+      sweep_slow([&](float x, int, int) { w += key_of(x) >= key && x > -INFINITY; });
       return cluster_sum(w);
     };
     // the sum at the place where the count (which 0) or the sum reaches `want`, and that place's key and number among its
@@ -768,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       while (lo < hi) {
         const int mid = lo + (hi - lo) / 2;
         u64 w = 0;
-        sweep([&](float x, int i, int j) { w += key_of(x) == key && index_of(i, j) <= mid; });
+        sweep_slow([&](float x, int i, int j) { w += key_of(x) == key && index_of(i, j) <= mid; });
         if (cluster_sum(w) >= nth)
           hi = mid;
         else
@@ -792,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         const int i = quads > kThreads ? (int)((long long)tid * quads / kThreads) : tid;
         if (i < quads) {
           float x[4];
-          quad<F32>(slice, i, x);
+          load(i, x);
           best = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         }
         best = warp_all(best, Max());
@@ -810,8 +885,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         const unsigned it = __ballot_sync(0xffffffffu, above == r - 1);
         bound = __shfl_sync(0xffffffffu, mine, __ffs(it) - 1);
         // the middle one of the CTAs'
-        if (tid < cluster) put32(&row.bound[rank], tid, __float_as_uint(bound));
-        cluster_sync();
+        if (tid < cluster) tell32(&row.bound[rank], tid, __float_as_uint(bound));
+        all_sync();
         const float theirs = row.bound[lane & (cluster - 1)];
         int more = 0;
         for (int o = 0; o < cluster; ++o) {
@@ -836,10 +911,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       const u64 mine = need_z ? cta_all((u64)(mass * 8796093022208.f), Add(), part64) : 0ull;
       __syncthreads();
       if (tid < cluster) {
-        put32(&row.listed[rank], tid, (uint32_t)taken);
-        put64(&row.mass[rank], tid, mine);
+        tell32(&row.listed[rank], tid, (uint32_t)taken);
+        tell64(&row.mass[rank], tid, mine);
       }
-      cluster_sync();
+      all_sync();
       int count = 0;
       for (int r = 0; r < cluster; ++r) count += row.listed[r], Z += row.mass[r];
       if (count > 0 && count <= kList && (count >= k || every)) {
@@ -854,8 +929,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
           ok = draw(count, k > 0, false);
         }
         if (need_z) {
-          if (tid < cluster && rank == 0) put32(&row.done, tid, ok);
-          cluster_sync();
+          if (tid < cluster && rank == 0) tell32(&row.done, tid, ok);
+          all_sync();
           ok = row.done != 0;
         }
         done = ok;
@@ -909,9 +984,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
           int at = which ? reach(sum, count, f.mass, want) : (int)(want - f.n) - 1;
           at = min(max(at, 0), count - 1);
           const u64 z = f.mass + sum_at(sum, at);
-          if (tid < cluster) put64(&row.result[1], tid, z);
+          if (tid < cluster) tell64(&row.result[1], tid, z);
         }
-        cluster_sync();
+        all_sync();
         return row.result[1];
       };
       if (has_k) drawn_of = end_of(0, kth, (u64)k);
@@ -945,16 +1020,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     a.tokens[m] = token;
     if (a.probs) a.probs[m] = prob;
   }
-  cluster_sync();  // no CTA leaves while another reads its memory
+  all_sync();  // no CTA leaves while another reads its memory
   if (!landed) mbar_wait_n(&bar, 0, nullptr, 0, 1u << 16);  // nor before its copies have landed (a bounded wait)
+}
+
+// Where a CTA per row pays: the clusters' rows follow one another through the SMs, 2 SMs / cluster at a time and some 20 us
+// each, mostly waiting for their own barriers; a CTA per row takes 8 us and 0.43 ns a logit, but the GPU holds two an SM.
+// Clusters and CTAs, plain softmax: 76 rows of 20001 logits 27.3 and 17.7 us, of 50021 47.8 and 30.9, of 151936 63.4 and
+// 71.8; 152 rows of 151936 110 and 72, 512 rows 344 and 254. (The counts of one of the two copies of the bins stay below
+// 2^31 / 22780 = 94270, that a bin's deviations fit 32 bits.)
+bool row_per_cta(long long M, int V, int cluster) {
+  return V <= 180000 && 152 * M * cluster > (long long)device_sm_count() * (120 + V / 154);
 }
 
 template <bool F32>
 cudaError_t launch(const SampleArgs& a, cudaStream_t stream, bool pdl) {
-  auto k = sample_kernel<F32>;
+  const int cluster = a.V <= 8192 ? 1 : a.V <= 16384 ? 2 : a.V <= 32768 ? 4 : 8;
+  const bool held = cluster == 1 || !row_per_cta(a.M, a.V, cluster);
+  auto k = held ? sample_kernel<F32, true> : sample_kernel<F32, false>;
   cudaError_t e = allow_max_smem(k);
   if (e != cudaSuccess) return e;
-  const int cluster = a.V <= 8192 ? 1 : a.V <= 16384 ? 2 : a.V <= 32768 ? 4 : 8;
+  if (!held) return launch_kernel(k, dim3(a.M), dim3(kThreads), 4 * kBins * 4 + kBins * 12, stream, pdl, a, 1);
   const int own = kBins / cluster, per = F32 ? 4 : 8;
   const size_t smem = 2 * kBins * 4 + own * 12 + 16 * ((size_t)(a.V / per + cluster - 1) / cluster + 3);
   cudaLaunchConfig_t cfg = {};

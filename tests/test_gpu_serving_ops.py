@@ -508,6 +508,23 @@ def test_sample_strided_rows(q, V):
             run_rows(q, big[:, :V], rng.random(9).tolist(), passed=dev[:, :V], temperature=[0.0] * 9)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,V", [(130, 50021), (470, 8195), (240, 20001)])
+def test_sample_many_rows(q, M, V, dtype):
+    """More rows than are held at once; rows that begin anywhere; equal logits, masks and numbers that are none among them."""
+    rng = np.random.default_rng(M)
+    big = torch.full((M, V + 3), float("nan"), dtype=dtype)
+    x = big[:, :V]
+    x.copy_(torch.from_numpy(rng.standard_normal((M, V)) * rng.choice([0.3, 2.0, 6.0], (M, 1))))
+    x[3], x[4], x[5, ::2], x[6, 100:] = 1.5, float("-inf"), float("nan"), float("-inf")
+    x[7, 9], x[8], x[9, 5:] = float("inf"), -torch.finfo(dtype).max, 0.25
+    clean = x.float().clamp(max=torch.finfo(dtype).max).to(dtype) if dtype == torch.bfloat16 else x
+    dev, u = big.to(DEV)[:, :V], rng.random(M).tolist()
+    run_rows(q, clean, u, passed=dev)
+    run_rows(q, clean, u, passed=dev, **settings_mix(rng, M, V))
+    run_rows(q, clean, u, passed=dev, temperature=[0.8] * M, top_p=rng.choice([0.5, 0.9, 0.99], M).tolist())
+
+
 def test_sample_inverts_the_distribution(q):
     """Evenly spaced numbers give every token its share of them."""
     rng = np.random.default_rng(1)
