@@ -7,15 +7,22 @@ the drafts of a speculative tree) goes through
 
     rmsnorm_residual        -> bf16 rows
     qgemm_w4a16_skinny      -> q, k, v (fp32)
-    (rotary embedding, torch)
     kv8_block_plan          -> pages and slots of the step's tokens
+    qk_norm_rope            -> norms of queries and keys, position rotation
     kv8_append              -> keys and values into the paged 8-bit cache
     attn_kv8_paged          -> attention of the step's rows over the cache
+    (attn_kv8_shared)          ... where requests begin with the same tokens
     qgemm_w4a16_skinny      -> output projection
     rmsnorm_residual_i8     -> int8 rows after the randomized Hadamard transform
     gemm_w8a8_i32           -> gate and up
     (SwiGLU, torch)
     qgemm_w4a16_skinny      -> down projection, the next layer's input
+
+and behind the last layer
+
+    rmsnorm_residual        -> bf16 rows
+    qgemm_w4a16_skinny      -> logits
+    sample_logits           -> the next tokens
 
 Weights are random; the point is how the calls fit together: all lengths,
 tables and slots stay on the GPU, and rejected drafts are given back by a plan
@@ -36,16 +43,6 @@ if ROOT not in sys.path:
 
 import skinny_gemm_qgemv_gb300 as lib  # noqa: E402
 import synth  # noqa: E402
-
-
-def rotate(x, positions, base=10000.0):
-    """Rotary embedding of x fp32 [M][heads][D] at positions int32 [M] (angles in float64: far positions)."""
-    D = x.shape[-1]
-    freq = base ** (-torch.arange(0, D, 2, device=x.device, dtype=torch.float64) / D)
-    angle = positions.clamp(min=0).double()[:, None] * freq
-    c, s = angle.cos().float()[:, None], angle.sin().float()[:, None]
-    a, b = x[..., 0::2], x[..., 1::2]
-    return torch.stack((a * c - b * s, a * s + b * c), -1).flatten(-2)
 
 
 class PagedCache:
@@ -81,13 +78,19 @@ class DecodeLayer:
         self.wdown = w4(hidden, intermediate, 4)
         self.norm1 = 1 + synth.normal_f32((hidden,), 0.1, seed, 5, device)
         self.norm2 = 1 + synth.normal_f32((hidden,), 0.1, seed, 6, device)
+        self.qnorm, self.knorm = (1 + synth.normal_f32((head_dim,), 0.1, seed, s, device) for s in (9, 10))
+        self.inv_freq = 10000.0 ** (-torch.arange(0, head_dim, 2, device=device, dtype=torch.float64) / head_dim)
         self.sign_bits = synth.sign_bits(hidden, seed, 7).to(device)
         # gate and up as one int8 matrix, its rows transformed and quantized like the activations
         w = synth.normal_f32((2 * intermediate, hidden), 0.02, seed, 8, device).to(torch.bfloat16)
         self.w8, self.s8 = lib.hadamard32_quant_i8(w, self.sign_bits)
 
-    def step(self, x, residual, cache, new_lens, tree=None):
-        """x, residual fp32 [M][hidden]: the last layer's output and the residual stream (updated in place). Returns
+    def step(self, x, residual, cache, new_lens, tree=None, shared=None):
+        """shared: (cu_req int32 [G + 1], offset int32 [requests]): the requests cu_req[g] .. cu_req[g + 1] - 1 begin
+        with the tokens of request g, a prefix that is held once and does not grow; offset is each request's prefix length,
+        which its positions count too.
+
+        x, residual fp32 [M][hidden]: the last layer's output and the residual stream (updated in place). Returns
         this layer's output and everything in between by name. Where the plan was refused (t["info"][3] is not 0) nothing
         was stored and no row attended: the output and the residual stream of that step are to be dropped."""
         M = x.shape[0]
@@ -96,11 +99,23 @@ class DecodeLayer:
         q, k, v = (lib.qgemm_w4a16_skinny(*w, t["h1"]).unflatten(1, (-1, self.head_dim))
                    for w in (self.wq, self.wk, self.wv))
         t["cu"], t["slots"], t["positions"], t["info"] = cache.resize(new_lens, M)
-        t["q"] = rotate(q, t["positions"]).to(torch.bfloat16)
-        t["k"], t["v"] = rotate(k, t["positions"]), v
+        if shared is not None:
+            cu_req, offset = shared
+            owner = torch.searchsorted(t["cu"][1:], torch.arange(M, device=x.device, dtype=torch.int32), right=True)
+            owner = owner.clamp(max=offset.numel() - 1)
+            t["positions"] = torch.where(t["positions"] < 0, t["positions"], t["positions"] + offset[owner])
+        t["raw_q"], t["raw_k"] = q, k
+        t["q"], t["k"] = lib.qk_norm_rope(q, k, t["positions"], self.inv_freq, q_weight=self.qnorm, k_weight=self.knorm,
+                                          interleaved=True)
+        t["v"] = v
         lib.kv8_append(t["k"], t["v"], t["slots"], cache.k, cache.v, cache.scales)
-        t["attn"] = lib.attn_kv8_paged(t["q"], cache.k, cache.v, cache.scales, cache.table, cache.lens, t["cu"],
-                                       tree_mask=tree)
+        pages = cache.k, cache.v, cache.scales
+        if shared is None:
+            t["attn"] = lib.attn_kv8_paged(t["q"], *pages, cache.table, cache.lens, t["cu"], tree_mask=tree)
+        else:
+            G = cu_req.numel() - 1
+            t["attn"] = lib.attn_kv8_shared(t["q"], *pages, cache.table[:G], cache.lens[:G], cu_req, cache.table, cache.lens,
+                                            t["cu"], tree_mask=tree)
         t["o"] = lib.qgemm_w4a16_skinny(*self.wo, t["attn"].flatten(1))
         t["residual1"] = residual.clone()
         t["h8"], t["s"], _ = lib.rmsnorm_residual_i8(t["o"], self.norm2, residual=residual, sign_bits=self.sign_bits,
@@ -111,6 +126,20 @@ class DecodeLayer:
         t["act"] = (torch.nn.functional.silu(gate) * up).to(torch.bfloat16).contiguous()
         t["y"] = lib.qgemm_w4a16_skinny(*self.wdown, t["act"])
         return t["y"], t
+
+
+class Head:
+    """The last norm, the output head and the sampler."""
+
+    def __init__(self, hidden=1024, vocabulary=4096, seed=0, device="cuda"):
+        self.w = synth.w4_weights(vocabulary, hidden, seed=seed, slot=20, device=device)
+        self.norm = 1 + synth.normal_f32((hidden,), 0.1, seed, 21, device)
+
+    def step(self, y, residual, u, temperature=None, top_k=None, top_p=None, min_p=None):
+        """Tokens and their probabilities for rows y, residual fp32 [M][hidden], u fp32 [M] in [0, 1)."""
+        h, _ = lib.rmsnorm_residual(y, self.norm, residual=residual)
+        logits = lib.qgemm_w4a16_skinny(*self.w, h)
+        return (*lib.sample_logits(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p), logits)
 
 
 def tree_words(parents, device="cuda"):
@@ -157,6 +186,19 @@ def main():
     torch.cuda.synchronize()
     print(f"{(time.perf_counter() - began) / steps * 1e6:.0f} us a layer step of {R} requests, contexts", n)
     assert torch.isfinite(y).all() and lib.device_error() == 0
+
+    # three answers to one prompt: request 0 holds the prompt, requests 1 .. 3 begin with it and go their own ways
+    cache = PagedCache(4, num_blocks=64, max_blocks=16, Hkv=layer.kv_heads, D=layer.head_dim)
+    y, t = layer.step(*rows(29), cache, lens(29, 0, 0, 0))
+    head, shared = Head(hidden), (lens(1, 4), lens(0, 29, 29, 29))
+    settings = dict(temperature=torch.full((3,), 0.8, device="cuda"), top_k=lens(50, 50, 50),
+                    top_p=torch.full((3,), 0.95, device="cuda"))
+    for i in range(1, 4):
+        x, residual = rows(3)
+        y, t = layer.step(x, residual, cache, lens(29, i, i, i), shared=shared)
+        tokens, probs, _ = head.step(y, residual, torch.rand(3, device="cuda"), **settings)
+        print("tokens", tokens.tolist(), "drawn with", [round(p, 4) for p in probs.tolist()])
+    assert lib.device_error() == 0
 
 
 if __name__ == "__main__":
