@@ -36,7 +36,7 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 576;
+constexpr int kThreads = 640;  // five warpgroups, the last with two warps at work
 constexpr int kSlots = 8;       // steps whose blocks and scales are kept
 constexpr int kRowsTile = 128;  // rows of a stream's MMAs
 constexpr int kUnits = kPrefixTok / kUnit;
@@ -88,6 +88,18 @@ __device__ __forceinline__ uint4 load_if(const void* p, bool there) {
   return v;
 }
 
+// A warpgroup's share of the registers that the CTA was launched with: 96 a thread, of which the softmax gets more
+// (256 x 128 + 384 x 72 <= 640 x 96).
+constexpr int kSoftmaxRegs = 128, kOtherRegs = 72;
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int FMT, int DP>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a, uint8_t* pieces, int2* source) {
   using S = PrefixShape<DP>;
@@ -101,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
   int* cus = cost + a.R + 1;
   int* ctxs = cus + a.R + 1;
   __shared__ long long unit_at[kSlots][kUnits];     // element of the unit's first token in the cache, -1: not there
+  __shared__ bool plain[kSlots];                    // all of the slot's units are of kind 1
   __shared__ float4 unit_scales[kSlots][kUnits];    // key scale, log2 of the value scale, 2^-that, kind
   // a step's blocks, its scales have been written; its values have been multiplied
   __shared__ uint64_t found[kSlots], scaled[kSlots], spent[kSlots];
@@ -140,8 +153,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
 
   // by a whole warp, which goes on together
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
-           __all_sync(0xffffffffu, tc_wait_on(bar, parity, &abort_flag, a.err));
+    // (in line: around a call ptxas finds no registers for setmaxnreg's shares)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    bool ok = false;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kMaxPolls && !ok; ++i) {
+      ok = mbar_try_wait(bar, parity);
+      if (!ok && abort_flag) break;
+      if (!ok && i == kMaxPolls - 1) {
+        report_error(a.err, kErrAttnWait);
+        abort_flag = 1u;
+      }
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
   };
   // A segment: the steps of one item in this CTA's share. Every role walks the segments by itself; the steps of the CTA
   // are counted through (step g: buffers g & 1, slot g % kSlots).
@@ -170,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
   Segment sg = first_segment();
 
   if (warp < 8) {
+    registers_up<kSoftmaxRegs>();
     // ------------------------------------------------ softmax: a row per thread
     const int stream = warp >> 2, r = quad * 32 + lane;
     const uint32_t tlane = tbase + ((uint32_t)(quad * 32) << 16);
@@ -227,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
         if (lane == 0) mbar_arrive(&q_full);
       }
       float m = kNoMax, l = 0.f;
-      bool begun = false;
+      bool begun = false, fresh = true, large = false;  // fresh: no maximum yet
 #pragma unroll 1
       for (int i = two ? 0 : stream; i < sg.n; i += two ? 1 : 2) {
         const int g = sg.g + i, slot = g % kSlots;
@@ -237,13 +262,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
         tc_after();
         const int seen = ctx - (sg.tok0 + i * TOK);  // tokens of the step, if not all
         const float4* us = unit_scales[slot];
-        // Two units at a time: p against the maximum so far, its sum without the value scale, and as fp16 over the scores
-        // read before. Where the sum is at most 2^8 so is every p, and m stays (a pass over the scores for their maximum
-        // took as long as the exponentials); otherwise m rises to a whole number above the largest, by which what the
-        // step has written already is scaled exactly. (Unrolled, the loop ran slower: three roles' code passes through
-        // an SM's instruction caches in every step.)
+        // Two units (32 columns) at a time: p against the maximum so far, its sum without the value scale, and as fp16 over
+        // the scores read before. Where the sum is at most 2^8 so is every p, and m stays (a pass over the scores for their
+        // maximum took as long as the exponentials).
+        int c = 0;
+        if (!fresh && !large && plain[slot] && seen >= TOK) {
+          // nothing to mask: the next scores are on the way while these are worked on
+          float s[2][32];
+          auto half = [&](float(&e)[32], int c) {
+            const float4 sc[2] = {us[2 * c], us[2 * c + 1]};
+            uint32_t p[16];
+            float mass = 0.f, part = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint64_t f2 = both(sc[u].x * rf), b2 = both(sc[u].y - m);
+              uint64_t sum = 0ull;
+#pragma unroll
+              for (int j = 16 * u; j < 16 * u + 16; j += 2) {
+                float y0, y1;
+                unpair2(ffma2(pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])), f2, b2), y0, y1);
+                y0 = ex2(y0), y1 = ex2(y1);
+                sum = fadd2(sum, pair2(__float_as_uint(y0), __float_as_uint(y1)));
+                p[j / 2] = f16x2(y0, y1);
+              }
+              float s0, s1;
+              unpair2(sum, s0, s1);
+              mass += s0 + s1;
+              part = fmaf(s0 + s1, sc[u].z, part);
+            }
+            if (__any_sync(0xffffffffu, mass > kMostMass)) return false;
+            l += part;
+            tmem_st16(ts + 16 * c, *reinterpret_cast<float(*)[16]>(p));
+            return true;
+          };
+          tmem_ld32(ts, s[0]);
 #pragma unroll 1
-        for (int c = 0; c < TOK / 32; ++c) {
+          for (; c < TOK / 32; c += 2) {
+            tmem_wait_ld32(s[0]);
+            tmem_ld32(ts + 32 * c + 32, s[1]);
+            const bool first = half(s[0], c);
+            tmem_wait_ld32(s[1]);
+            if (!first) break;
+            if (c == 0) tmem_ld32(ts + 64, s[0]);
+            if (!half(s[1], c + 1)) {
+              ++c;
+              break;
+            }
+          }
+          tmem_wait_ld32(s[0]);
+        }
+        // The general form: m rises to a whole number above the largest score, by which what the step has written already
+        // is scaled exactly.
+#pragma unroll 1
+        for (; c < TOK / 32; ++c) {
           const float4 sc[2] = {us[2 * c], us[2 * c + 1]};
           const int here = seen - 32 * c;
           const bool edge = here < 32 || sc[0].w == 0.f || sc[1].w == 0.f;
@@ -254,39 +325,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
           for (int pass = 0; pass < 2; ++pass) {
             tmem_ld32(ts + 32 * c, s);
             tmem_wait_ld32(s);
-            float mass = 0.f;
-            part = 0.f;
+            if (!fresh) {
+              float mass = 0.f;
+              part = 0.f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint64_t f2 = both(sc[u].x * rf), b2 = both(sc[u].y), m2 = both(-m);
-              uint64_t sum = 0ull;
-              float* e = s + 16 * u;
+              for (int u = 0; u < 2; ++u) {
+                const uint64_t f2 = both(sc[u].x * rf), b2 = both(large ? sc[u].y : sc[u].y - m), m2 = both(-m);
+                uint64_t sum = 0ull;
+                float* e = s + 16 * u;
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float y0, y1;
-                // (the score as it is compared with m, then the difference: a sum with -m in one step may lie above 0 by a
-                // rounding of large scores)
-                unpair2(fadd2(ffma2(pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])), f2, b2), m2), y0, y1);
-                e[j] = ex2(y0), e[j + 1] = ex2(y1);
+                for (int j = 0; j < 16; j += 2) {
+                  float y0, y1;
+                  // (large scores: as they are compared with m, then the difference; in one step it may lie above 0 by their
+                  // rounding)
+                  uint64_t y = ffma2(pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])), f2, b2);
+                  if (large) y = fadd2(y, m2);
+                  unpair2(y, y0, y1);
+                  e[j] = ex2(y0), e[j + 1] = ex2(y1);
+                }
+                if (edge) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    if (sc[u].w == 0.f || 16 * u + j >= here) e[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  sum = fadd2(sum, pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])));
+                  p[8 * u + j / 2] = f16x2(e[j], e[j + 1]);
+                }
+                float s0, s1;
+                unpair2(sum, s0, s1);
+                mass += s0 + s1;
+                part = fmaf(s0 + s1, sc[u].z, part);
               }
-              if (edge) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (sc[u].w == 0.f || 16 * u + j >= here) e[j] = 0.f;
-              }
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                sum = fadd2(sum, pair2(__float_as_uint(e[j]), __float_as_uint(e[j + 1])));
-                p[8 * u + j / 2] = f16x2(e[j], e[j + 1]);
-              }
-              float s0, s1;
-              unpair2(sum, s0, s1);
-              mass += s0 + s1;
-              part = fmaf(s0 + s1, sc[u].z, part);
+              if (pass == 1 || !__any_sync(0xffffffffu, mass > kMostMass)) break;
+              tmem_ld32(ts + 32 * c, s);
+              tmem_wait_ld32(s);
             }
-            if (pass == 1 || !__any_sync(0xffffffffu, mass > kMostMass)) break;
-            tmem_ld32(ts + 32 * c, s);
-            tmem_wait_ld32(s);
+            fresh = false;
             float top = kNoMax;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -296,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
             const float mn = top > m ? ceilf(top) : m, f = ex2(m - mn);
             const uint32_t f16 = f16x2(f, f);
             m = mn;
+            large = __any_sync(0xffffffffu, fabsf(m) > 65536.f && m != kNoMax);
             l *= f;
 #pragma unroll 1
             for (int k = 0; k < c; ++k) {
@@ -400,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       named_barrier<256>(1);  // both streams' outputs and `other` have been read
     }
   } else if (warp < 16) {
+    registers_down<kOtherRegs>();
     // ------------------------------------------------ keys (warps 8-11) and values (12-15): 16 codes a thread and load,
     // as fp16 tiles
     const int t = tid & 127, ch = t & 3, tk = t >> 2 & (S::kTokens - 1), half = S::kHalves == 2 ? t >> 6 : 0;
@@ -451,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
       if (more) ok = fetch();
     }
   } else if (warp == 16) {
+    registers_down<kOtherRegs>();
     // ------------------------------------------------ a lane per unit of 16 tokens: its block and the block's scales
     const float2* scales = reinterpret_cast<const float2*>(a.scales);
     bool ok = true;
@@ -490,12 +569,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
           const float lv = __log2f(sc.y < kMinScale ? kMinScale : sc.y);
           unit_scales[slot][lane] = make_float4(sc.x, lv, ex2(-lv), blk < 0 ? 0.f : sc.y == 0.f ? 2.f : 1.f);
         }
+        const bool usual = __all_sync(0xffffffffu, lane >= kUnits || (blk >= 0 && sc.y != 0.f));
+        if (lane == 0) plain[slot] = usual;
         __syncwarp();
         if (lane == 0) mbar_arrive(scaled + slot);
         blk = next;
       }
     }
+  } else if (warp > 17) {
+    registers_down<kOtherRegs>();
   } else {
+    registers_down<kOtherRegs>();
     // ------------------------------------------------ MMAs
     // What decides the loops and forms the operands is taken from lane 0, so that it stays in uniform registers.
     auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
