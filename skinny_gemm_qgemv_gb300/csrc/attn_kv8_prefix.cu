@@ -587,15 +587,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
     const uint32_t tb = uniform(tbase);
     const uint64_t qd = tc_desc(uniform(smem_u32(qbuf)), 16, 1024), kd = tc_desc(uniform(smem_u32(kbuf)), 16, 1024),
                    vd = tc_desc(uniform(smem_u32(vbuf)), S::kBlock, 1024);
-    uint32_t passes[2] = {0u, 0u};  // of p_ready
+    uint32_t passes0 = 0, passes1 = 0;  // of p_ready
     bool ok = true;
     while (ok && __all_sync(0xffffffffu, next_segment(sg, step))) {
       const int n = uniform(sg.n), gi = uniform(sg.g), two = uniform(sg.rows > kRowsTile);
       const int events = two ? 2 * n : n;  // event x: stream x & 1, of step x / 2 or x
+      // (a wait costs this warp some 200 cycles of the 1450 that an event's products take: each is made once, where it is
+      // not in the way)
+      auto keys_there = [&](int x) {
+        const int g = gi + (two ? x >> 1 : x), b = g & 1;
+        return (two && (x & 1)) || wait_warp(k_full + b, (g >> 1) & 1);
+      };
       auto issue_s = [&](int x) {
         const int t = x & 1, g = gi + (two ? x >> 1 : x), b = g & 1;
-        if (!wait_warp(k_full + b, (g >> 1) & 1)) return false;
-        tc_after();
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint32_t at = ((k >> 2) * S::kBlock + (k & 3) * 32) >> 4;
@@ -606,18 +610,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
           if (!two || t == 1) tc_commit(k_empty + b);
         }
         __syncwarp();
-        return true;
       };
       ok = wait_warp(&q_full, uniform(sg.index) & 1);
+      ok = ok && keys_there(0) && (events < 2 || two || keys_there(1));
       if (!ok) break;
       tc_after();
-      ok = issue_s(0) && (events < 2 || issue_s(1));
+      issue_s(0);
+      if (events > 1) issue_s(1);
 #pragma unroll 1
       for (int x = 0; ok && x < events; ++x) {
         const int t = x & 1, g = gi + (two ? x >> 1 : x), b = g & 1;
-        ok = wait_warp(p_ready + t, passes[t] & 1) && wait_warp(v_full + b, (g >> 1) & 1);
+        ok = ((two && t) || wait_warp(v_full + b, (g >> 1) & 1)) && (x + 2 >= events || keys_there(x + 2)) &&
+             wait_warp(p_ready + t, (t ? passes1 : passes0) & 1);
         if (!ok) break;
-        ++passes[t];
+        (t ? passes1 : passes0) += 1;
         tc_after();
 #pragma unroll
         for (int k = 0; k < TOK / 16; ++k)
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
                  k > 0 ? 1u : x > 1, one);
         if (one && (!two || t == 1)) tc_commit(spent + g % kSlots);
         __syncwarp();
-        if (x + 2 < events) ok = issue_s(x + 2);
+        if (x + 2 < events) issue_s(x + 2);
       }
       if (one) tc_commit(&o_done);
       __syncwarp();
