@@ -34,7 +34,8 @@ constexpr int kThreads = 256, kWarps = kThreads / 32, kUnroll = 2, kCtas = 4;
 template <bool F32>
 struct Quad {
   uint32_t w[F32 ? 4 : 2];
-  __device__ __forceinline__ void load(const void* p) {
+  __device__ __forceinline__ void load(const void* p, bool there) {
+    if (!there) return;  // (the values are not used)
     if (F32) {
       const uint4 v = *static_cast<const uint4*>(p);
       w[0] = v.x, w[1] = v.y, w[F32 ? 2 : 0] = v.z, w[F32 ? 3 : 1] = v.w;
@@ -83,39 +84,33 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_rope_kernel(RopeArgs a, in
     const void* w = k ? a.k_w : a.q_w;
     weight[k][e] = !w ? 1.f : a.w_f32 ? static_cast<const float*>(w)[e] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[e]);
   }
-  const int heads = a.Hq + a.Hkv, units = (heads + HW - 1) / HW;
-  // a token's units go to kWarps / tokens warps (one round's tokens at most kWarps) of gridDim.y CTAs
+  const int units_q = (a.Hq + HW - 1) / HW, units_k = (a.Hkv + HW - 1) / HW;
+  // a token's units go to kWarps / tokens warps (one round's tokens at most kWarps) of gridDim.y CTAs, the queries' first
   const int t_of = warp & (tokens - 1), per = kWarps / tokens;
-  const int u0 = blockIdx.y * per + warp / tokens, du = gridDim.y * per;
+  const int w0 = blockIdx.y * per + warp / tokens, du = gridDim.y * per;
+  const int k0 = (w0 - units_q % du + du) % du;
   const float inv_d = 1.f / (float)a.D;
-  const bool normed = a.q_w || a.k_w;
+  const int at0 = (lane / L) * a.D + e[0], gap = e[1] - e[0], step_u = du * HW * a.D;
 
   int b = 0;
 #pragma unroll 1
   for (int t0 = blockIdx.x * tokens; t0 < a.T; t0 += gridDim.x * tokens, b ^= 1) {
     const int t = t0 + t_of;
     const bool live = t < a.T && a.pos[min(t, a.T - 1)] >= 0;  // (the same for a warp)
-    // rows of the token; the keys' so that they too are indexed by the head's number among all
     const char* q_in = static_cast<const char*>(a.q) + t * a.q_stride * kSize;
-    const char* k_in = static_cast<const char*>(a.k) + (t * a.k_stride - a.Hq * a.D) * kSize;
+    const char* k_in = static_cast<const char*>(a.k) + t * a.k_stride * kSize;
     Quad<F32> raw[kUnroll][2];
-    auto fetch = [&](int u) {
+    // the warp's unit u of H heads and the kUnroll - 1 after it; a lane that has no head there reads the first one's
+    auto fetch = [&](const char* src, int u, int H) {
 #pragma unroll
       for (int n = 0; n < kUnroll; ++n) {
-        const int h = (u + n * du) * HW + lane / L;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int j = 0; j < kSize; ++j) raw[n][c].w[j] = 0u;
-        }
-        if (live && h < heads && in) {
-          const char* src = h < a.Hq ? q_in : k_in;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) raw[n][c].load(src + (h * a.D + e[c]) * kSize);
-        }
+        const bool there = live && in && (u + n * du) * HW + lane / L < H;
+        const int at = there ? u * HW * a.D + n * step_u + at0 : 0;
+        raw[n][0].load(src + at * kSize, live);
+        raw[n][1].load(src + (there ? at + gap : 0) * kSize, live);
       }
     };
-    fetch(u0);  // on the way while the sines are formed
+    fetch(q_in, w0, a.Hq);  // on the way while the sines are formed
     if (pair < half && t0 + my_token < a.T) {
       const long long p = my_pos[t0 + my_token];
       const float half_turns = (float)(long long)(step * (unsigned long long)p) * 0x1p-63f;  // in [-1, 1]
@@ -125,69 +120,79 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_rope_kernel(RopeArgs a, in
     }
     __syncthreads();  // (a table is written again two rounds later, past the next round's barrier)
     if (!live) continue;
-    // split halves: four pairs (x[0][j], x[1][j]); else pairs (x[c][j], x[c][j + 1]), j even
-    float cs[4], sn[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = !turns ? 0 : split ? e[0] + j : e[0] / 2 + j;
-      const float2 x = turn[b][t_of * lead + at];
-      cs[j] = turns ? x.x : 1.f, sn[j] = turns ? x.y : 0.f;
-    }
+    // Pair j of the lane's four is (x[0][j], x[1][j]) where halves are split, else x[j / 2][j % 2 * 2] and the next one:
+    // (u, v) -> (u a - v b, v c + u d), with the weights in the factors.
 #pragma unroll 1
-    for (int u = u0; u < units; u += kUnroll * du) {
-      if (u != u0) fetch(u);
+    for (int side = 0; side < 2; ++side) {
+      const int H = side ? a.Hkv : a.Hq, units = side ? units_k : units_q, first = side ? k0 : w0;
+      const bool normed = side ? a.k_w != nullptr : a.q_w != nullptr;
+      const char* src = side ? k_in : q_in;
+      if (first >= units) continue;
+      if (side) fetch(src, first, H);
+      float ca[4], cb[4], cc[4], cd[4];
+      {
+        const float4 w0_ = *reinterpret_cast<const float4*>(weight[side] + (in ? e[0] : 0)),
+                     w1_ = *reinterpret_cast<const float4*>(weight[side] + (in ? e[1] : 0));
+        const float w[8] = {w0_.x, w0_.y, w0_.z, w0_.w, w1_.x, w1_.y, w1_.z, w1_.w};
 #pragma unroll
-      for (int n = 0; n < kUnroll; ++n) {
-        if (u + n * du >= units) break;
-        const int h = (u + n * du) * HW + lane / L;
-        const bool is_q = h < a.Hq;
-        float x[8];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) raw[n][c].values(x + 4 * c);
-        if (normed) {
-          float ss = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-          for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-          if (in && (is_q ? a.q_w != nullptr : a.k_w != nullptr)) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float4 g = *reinterpret_cast<const float4*>(weight[is_q ? 0 : 1] + e[c]);
-              x[4 * c] = x[4 * c] * r * g.x, x[4 * c + 1] = x[4 * c + 1] * r * g.y;
-              x[4 * c + 2] = x[4 * c + 2] * r * g.z, x[4 * c + 3] = x[4 * c + 3] * r * g.w;
-            }
-          }
+        for (int j = 0; j < 4; ++j) {
+          const int at = !turns ? 0 : split ? e[0] + j : e[0] / 2 + j;
+          const float2 x = turn[b][t_of * lead + at];
+          const float c = turns ? x.x : 1.f, s = turns ? x.y : 0.f, wu = split ? w[j] : w[2 * j], wv = split ? w[4 + j] : w[2 * j + 1];
+          ca[j] = c * wu, cb[j] = s * wv, cc[j] = c * wv, cd[j] = s * wu;
         }
-        if (turns) {
+      }
+      const long long row = (long long)t * H * a.D;
+      uint16_t* out16 = (side ? static_cast<uint16_t*>(a.k_out) : a.q_out) + row;
+      float* out32 = static_cast<float*>(a.k_out) + row;
+      const bool wide = side && a.k_out_f32;
+#pragma unroll 1
+      for (int u = first; u < units; u += kUnroll * du) {
+        if (u != first) fetch(src, u, H);
+#pragma unroll
+        for (int n = 0; n < kUnroll; ++n) {
+          if (u + n * du >= units) break;
+          float x[8];
+          raw[n][0].values(x);
+          raw[n][1].values(x + 4);
+          float r = 1.f;
+          if (normed) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+            ss = in ? ss : 0.f;
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            r = rsqrtf(fmaf(ss, inv_d, a.eps));
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] *= r;
+          float y[8];
           if (split) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float v = x[j], w = x[4 + j];
-              x[j] = fmaf(v, cs[j], -w * sn[j]), x[4 + j] = fmaf(w, cs[j], v * sn[j]);
+              y[j] = fmaf(x[j], ca[j], -x[4 + j] * cb[j]);
+              y[4 + j] = fmaf(x[4 + j], cc[j], x[j] * cd[j]);
             }
-          } else {
+          } else if (turns) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float v = x[2 * j], w = x[2 * j + 1];
-              x[2 * j] = fmaf(v, cs[j], -w * sn[j]), x[2 * j + 1] = fmaf(w, cs[j], v * sn[j]);
+              y[2 * j] = fmaf(x[2 * j], ca[j], -x[2 * j + 1] * cb[j]);
+              y[2 * j + 1] = fmaf(x[2 * j + 1], cc[j], x[2 * j] * cd[j]);
             }
-          }
-        }
-        if (h < heads && in) {
-          const long long row = is_q ? (long long)t * a.Hq + h : (long long)t * a.Hkv + h - a.Hq;
-          if (!is_q && a.k_out_f32) {
-            float* dst = static_cast<float*>(a.k_out) + row * a.D;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              *reinterpret_cast<float4*>(dst + e[c]) = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
           } else {
-            uint16_t* dst = (is_q ? a.q_out : static_cast<uint16_t*>(a.k_out)) + row * a.D;
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              *reinterpret_cast<uint2*>(dst + e[c]) =
-                  make_uint2(f32_to_bf16x2(x[4 * c], x[4 * c + 1]), f32_to_bf16x2(x[4 * c + 2], x[4 * c + 3]));
+            for (int j = 0; j < 4; ++j) y[2 * j] = x[2 * j] * ca[j], y[2 * j + 1] = x[2 * j + 1] * cc[j];
+          }
+          if (in && (u + n * du) * HW + lane / L < H) {
+            const int at = u * HW * a.D + n * step_u + at0;
+            if (wide) {
+              *reinterpret_cast<float4*>(out32 + at) = make_float4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<float4*>(out32 + at + gap) = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+              *reinterpret_cast<uint2*>(out16 + at) = make_uint2(f32_to_bf16x2(y[0], y[1]), f32_to_bf16x2(y[2], y[3]));
+              *reinterpret_cast<uint2*>(out16 + at + gap) = make_uint2(f32_to_bf16x2(y[4], y[5]), f32_to_bf16x2(y[6], y[7]));
+            }
           }
         }
       }
@@ -197,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_rope_kernel(RopeArgs a, in
 
 template <bool F32, int L>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream, bool pdl) {
-  const int sms = device_sm_count(), units = (a.Hq + a.Hkv + 32 / L - 1) / (32 / L);
+  const int sms = device_sm_count(), units = (a.Hq + 32 / L - 1) / (32 / L) + (a.Hkv + 32 / L - 1) / (32 / L);
   // Threads per token of a round: its pairs, filled up to a power of two. A round takes as many tokens as keep the SMs
   // busy, eight at most (a warp each); few tokens: one a round, its heads over several CTAs, one to a warp.
   int lead_log = 5;
