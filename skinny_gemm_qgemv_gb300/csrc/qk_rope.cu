@@ -28,7 +28,7 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kUnroll = 2, kCtas = 4;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kUnroll = 2, kCtas = 3;
 
 // four consecutive elements as loaded
 template <bool F32>
@@ -99,18 +99,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_rope_kernel(RopeArgs a, in
     const bool live = t < a.T && a.pos[min(t, a.T - 1)] >= 0;  // (the same for a warp)
     const char* q_in = static_cast<const char*>(a.q) + t * a.q_stride * kSize;
     const char* k_in = static_cast<const char*>(a.k) + t * a.k_stride * kSize;
-    Quad<F32> raw[kUnroll][2];
+    Quad<F32> next[kUnroll][2];  // the loads on the way: a group of units ahead of what is worked on
     // the warp's unit u of H heads and the kUnroll - 1 after it; a lane that has no head there reads the first one's
     auto fetch = [&](const char* src, int u, int H) {
 #pragma unroll
       for (int n = 0; n < kUnroll; ++n) {
         const bool there = live && in && (u + n * du) * HW + lane / L < H;
         const int at = there ? u * HW * a.D + n * step_u + at0 : 0;
-        raw[n][0].load(src + at * kSize, live);
-        raw[n][1].load(src + (there ? at + gap : 0) * kSize, live);
+        next[n][0].load(src + at * kSize, live);
+        next[n][1].load(src + (there ? at + gap : 0) * kSize, live);
       }
     };
-    fetch(q_in, w0, a.Hq);  // on the way while the sines are formed
+    const bool no_q = w0 >= units_q;
+    fetch(no_q ? k_in : q_in, no_q ? k0 : w0, no_q ? a.Hkv : a.Hq);  // on the way while the sines are formed
     if (pair < half && t0 + my_token < a.T) {
       const long long p = my_pos[t0 + my_token];
       const float half_turns = (float)(long long)(step * (unsigned long long)p) * 0x1p-63f;  // in [-1, 1]
@@ -128,7 +129,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_rope_kernel(RopeArgs a, in
       const bool normed = side ? a.k_w != nullptr : a.q_w != nullptr;
       const char* src = side ? k_in : q_in;
       if (first >= units) continue;
-      if (side) fetch(src, first, H);
       float ca[4], cb[4], cc[4], cd[4];
       {
         const float4 w0_ = *reinterpret_cast<const float4*>(weight[side] + (in ? e[0] : 0)),
@@ -148,7 +148,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_rope_kernel(RopeArgs a, in
       const bool wide = side && a.k_out_f32;
 #pragma unroll 1
       for (int u = first; u < units; u += kUnroll * du) {
-        if (u != first) fetch(src, u, H);
+        Quad<F32> raw[kUnroll][2];
+#pragma unroll
+        for (int n = 0; n < kUnroll; ++n) raw[n][0] = next[n][0], raw[n][1] = next[n][1];
+        if (u + kUnroll * du < units)
+          fetch(src, u + kUnroll * du, H);
+        else if (side == 0 && k0 < units_k)
+          fetch(k_in, k0, a.Hkv);
 #pragma unroll
         for (int n = 0; n < kUnroll; ++n) {
           if (u + n * du >= units) break;
