@@ -49,7 +49,7 @@ struct Row {  // what the CTAs of a cluster tell one another
   float max[kMaxCluster];
   int lowest[kMaxCluster];
   int count[kMaxCluster], listed[kMaxCluster], landed[kMaxCluster], over;
-  float bound[kMaxCluster];
+  float bound[kMaxCluster], below[kMaxCluster];
   int done;
   u64 mass[kMaxCluster], tail[kMaxCluster], sum[2][kMaxCluster];
   Found found[2];    // of two searches in turn
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   __shared__ u64 pow[2][64];
   __shared__ u64 part64[kWarps];
   __shared__ int part32[kWarps];
-  __shared__ float partf[kWarps];
+  __shared__ float partf[kWarps], part_below[kWarps];
   __shared__ uint64_t bar;
   __shared__ int taken;
   __shared__ u64 tail_of;           // what lies below the bins
@@ -857,16 +857,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     // (or the bound to be far off), the bins below decide.
     const bool every = a.V <= kList;  // a list holds the whole row
     if (every || (k ? k <= kList / 2 : has_p || has_m)) {
+      bool hopeless = false;
       float bound = -kMost;
       if (!every && !k && !has_p) {
         bound = fmaxf(least, -kMost);
       } else if (!every) {
         // The r-th largest of the warps' largest sampled logits: of 16 warps' samples together about the
         // 16 (1 / 16 + .. + 1 / (17 - r))-th largest. A thread samples one quad.
-        float best = -INFINITY;
+        float best = -INFINITY, x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         const int i = quads > kThreads ? (int)((long long)tid * quads / kThreads) : tid;
         if (i < quads) {
-          float x[4];
           load(i, x);
           best = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         }
@@ -884,8 +884,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         for (int w = 0; w < kWarps; ++w) above += partf[w] > mine || (partf[w] == mine && w < (lane & (kWarps - 1)));
         const unsigned it = __ballot_sync(0xffffffffu, above == r - 1);
         bound = __shfl_sync(0xffffffffu, mine, __ffs(it) - 1);
+        // With top-p alone, the weights below the bound as the sample has them: where they outweigh some 250 of the largest
+        // (1 - p) / p times what lies above is too little.
+        float below = 0.f;
+        if (has_p && !k) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) below += x[j] < bound ? ex2((x[j] - top) * s.ch / (float)(64 << s.sj)) : 0.f;
+          below = cta_all(below, Add(), part_below) * (float)max(quads, kThreads) / (float)kThreads;
+        }
         // the middle one of the CTAs'
-        if (tid < cluster) tell32(&row.bound[rank], tid, __float_as_uint(bound));
+        if (tid < cluster) {
+          tell32(&row.bound[rank], tid, __float_as_uint(bound));
+          tell32(&row.below[rank], tid, __float_as_uint(below));
+        }
         all_sync();
         const float theirs = row.bound[lane & (cluster - 1)];
         int more = 0;
@@ -895,45 +906,50 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         }
         const float middle_one = __shfl_sync(0xffffffffu, theirs, __ffs(__ballot_sync(0xffffffffu, more == cluster / 2)) - 1);
         bound = fmaxf(middle_one, -kMost);
+        below = 0.f;
+        for (int o = 0; o < cluster; ++o) below += row.below[o];
+        hopeless = below * p_share > 250.f * (1.f - p_share) && !has_m;
       }
-      if (tid == 0) taken = 0;
-      __syncthreads();
-      float mass = 0.f;
-      const float c1 = -s.ch / (float)(64 << s.sj), c2 = -s.cl / (float)(64 << s.sj);
-      const bool need_z = has_p && !k && !every;
-      sweep([&](float x, int i, int j) {
-        if (x >= bound) put_in_list(x, i, j);
-        if (need_z) {
-          const float d = top - x;
-          mass += ex2(fmaxf(fmaf(d, c1, d * c2), -200.f));  // (of -infinity that sum is no number)
-        }
-      });
-      const u64 mine = need_z ? cta_all((u64)(mass * 8796093022208.f), Add(), part64) : 0ull;
-      __syncthreads();
-      if (tid < cluster) {
-        tell32(&row.listed[rank], tid, (uint32_t)taken);
-        tell64(&row.mass[rank], tid, mine);
-      }
-      all_sync();
-      int count = 0;
-      for (int r = 0; r < cluster; ++r) count += row.listed[r], Z += row.mass[r];
-      if (count > 0 && count <= kList && (count >= k || every)) {
-        bool ok = true;
-        if (rank == 0) {
-          count = collect();
-          if (every) {  // (all weights, and k as if there were no more than that)
-            u64 sum[2];
-            prefix(count, sum);
-            Z = sum_at(sum, count - 1);
+      if (!hopeless) {
+        if (tid == 0) taken = 0;
+        __syncthreads();
+        float mass = 0.f;
+        const float c1 = -s.ch / (float)(64 << s.sj), c2 = -s.cl / (float)(64 << s.sj);
+        const bool need_z = has_p && !k && !every;
+        sweep([&](float x, int i, int j) {
+          if (x >= bound) put_in_list(x, i, j);
+          if (need_z) {
+            const float d = top - x;
+            mass += ex2(fmaxf(fmaf(d, c1, d * c2), -200.f));  // (of -infinity that sum is no number)
           }
-          ok = draw(count, k > 0, false);
+        });
+        const u64 mine = need_z ? cta_all((u64)(mass * 8796093022208.f), Add(), part64) : 0ull;
+        __syncthreads();
+        if (tid < cluster) {
+          tell32(&row.listed[rank], tid, (uint32_t)taken);
+          tell64(&row.mass[rank], tid, mine);
         }
-        if (need_z) {
-          if (tid < cluster && rank == 0) tell32(&row.done, tid, ok);
-          all_sync();
-          ok = row.done != 0;
+        all_sync();
+        int count = 0;
+        for (int r = 0; r < cluster; ++r) count += row.listed[r], Z += row.mass[r];
+        if (count > 0 && count <= kList && (count >= k || every)) {
+          bool ok = true;
+          if (rank == 0) {
+            count = collect();
+            if (every) {  // (all weights, and k as if there were no more than that)
+              u64 sum[2];
+              prefix(count, sum);
+              Z = sum_at(sum, count - 1);
+            }
+            ok = draw(count, k > 0, false);
+          }
+          if (need_z) {
+            if (tid < cluster && rank == 0) tell32(&row.done, tid, ok);
+            all_sync();
+            ok = row.done != 0;
+          }
+          done = ok;
         }
-        done = ok;
       }
       if (!done) Z = 0;
     }
@@ -1033,16 +1049,28 @@ bool row_per_cta(long long M, int V, int cluster) {
   return V <= 180000 && 152 * M * cluster > (long long)device_sm_count() * (120 + V / 154);
 }
 
+size_t sample_smem(bool f32, int V, int cluster) {
+  return 2 * kBins * 4 + kBins / cluster * 12 + 16 * ((size_t)(V / (f32 ? 4 : 8) + cluster - 1) / cluster + 3);
+}
+
 template <bool F32>
 cudaError_t launch(const SampleArgs& a, cudaStream_t stream, bool pdl) {
-  const int cluster = a.V <= 8192 ? 1 : a.V <= 16384 ? 2 : a.V <= 32768 ? 4 : 8;
-  const bool held = cluster == 1 || !row_per_cta(a.M, a.V, cluster);
+  const int sms = device_sm_count(), most = a.V <= 8192 ? 1 : a.V <= 16384 ? 2 : a.V <= 32768 ? 4 : 8;
+  // the largest cluster with which all rows are held at once, a CTA an SM, if there is one (plain softmax, 76 rows of 50021
+  // logits: clusters of 8, 4, 2, a CTA per row that reads it from L2: 48, 34, 21, 31 us; with 1024 threads a CTA 23)
+  int cluster = most;
+  auto ctas = [&](int c) {
+    const size_t bytes = sample_smem(F32, a.V, c) + 3072;
+    return bytes <= (size_t)device_max_smem_optin() && a.V / c <= 94000 ? sms : 0;
+  };
+  while (cluster > 1 && (long long)a.M * cluster > ctas(cluster)) cluster /= 2;
+  bool held = (long long)a.M * cluster <= ctas(cluster);
+  if (!held) cluster = most, held = cluster == 1 || !row_per_cta(a.M, a.V, cluster);
   auto k = held ? sample_kernel<F32, true> : sample_kernel<F32, false>;
   cudaError_t e = allow_max_smem(k);
   if (e != cudaSuccess) return e;
   if (!held) return launch_kernel(k, dim3(a.M), dim3(kThreads), 4 * kBins * 4 + kBins * 12, stream, pdl, a, 1);
-  const int own = kBins / cluster, per = F32 ? 4 : 8;
-  const size_t smem = 2 * kBins * 4 + own * 12 + 16 * ((size_t)(a.V / per + cluster - 1) / cluster + 3);
+  const size_t smem = sample_smem(F32, a.V, cluster);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.M * cluster);
   cfg.blockDim = dim3(kThreads);
