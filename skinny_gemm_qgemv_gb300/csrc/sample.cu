@@ -32,7 +32,6 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;     // the last one takes what lies below the others
 constexpr int kOver = kBins - 1;
 constexpr int kList = 1024;     // tokens that are gathered and sorted, at most
@@ -110,16 +109,16 @@ __device__ __forceinline__ T warp_all(T v, OP op) {
   for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-// over the CTA, for all threads; `part` [kWarps] is free again after the caller's next barrier
-template <class T, class OP>
-__device__ __forceinline__ T cta_all(T v, OP op, T* part) {
+// over the CTA, for all threads; `part` [warps] is free again after the caller's next barrier
+template <int WARPS, class T, class OP>
+__device__ __forceinline__ T cta_all_of(T v, OP op, T* part) {
   v = warp_all(v, op);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = part[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) v = op(v, part[w]);
+  for (int w = 1; w < WARPS; ++w) v = op(v, part[w]);
   return v;
 }
 struct Add {
@@ -240,9 +239,11 @@ __device__ __forceinline__ void quad(const uint8_t* slice, int i, float (&x)[4])
 
 // HELD: a cluster per row, which it holds in shared memory; else a CTA per row, which reads it again from L2 in every
 // sweep
-template <bool F32, bool HELD>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int cluster) {
+template <bool F32, bool HELD, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(SampleArgs a, int cluster) {
   constexpr int PER = F32 ? 4 : 8;  // elements of 16 bytes
+  constexpr int kWarps = kThreads / 32, kPlaces = kList / kThreads;  // places of a list that a thread has
+  auto cta_all = [](auto v, auto op, auto* part) { return cta_all_of<kWarps>(v, op, part); };
   extern __shared__ __align__(16) uint8_t smem[];
   // layout: bins' counts | their deviations (| both again, of the warps of odd number) | sums before this CTA's bins |
   // tokens before them | the slice
@@ -359,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
   const float largest = F32 ? kMost : __uint_as_float(0x7F7F0000u);
   const int quads = n * (PER / 4);
   auto index_of = [&](int i, int j) { return first + 4 * i + j; };
+  bool clean = true;  // no logit is NaN or +infinity, as far as is known
   auto load = [&](int i, float (&x)[4]) {
     if (HELD) {
       quad<F32>(slice, i, x);
@@ -376,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         x[0] = j == 0 ? v : x[0], x[1] = j == 1 ? v : x[1], x[2] = j == 2 ? v : x[2], x[3] = j == 3 ? v : x[3];
       }
     }
+    if (clean) return;  // (the same for all threads)
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = fminf(fmaxf(x[j], -INFINITY), largest);
   };
@@ -423,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
     top = fmaxf(top, x);
     odd |= !(x <= kMost);
   });
-  if (HELD && __syncthreads_or(odd)) {
+  clean = !__syncthreads_or(odd);
+  if (HELD && !clean) {
 #pragma unroll 1
     for (int i = tid; i < 4 * quads; i += kThreads) {
       if (F32) {
@@ -435,9 +439,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         if (!(x <= kMost)) w = x != x ? (uint16_t)0xFF80u : (uint16_t)0x7F7Fu;
       }
     }
-    top = fminf(top, largest);
     __syncthreads();
   }
+  top = fminf(top, largest);
   top = cta_all(top, Max(), partf);
   if (HELD) cluster_wait();
   if (tid < cluster) {
@@ -732,15 +736,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       all_sync();
       return rank == 0 ? collect() : 0;
     };
-    // In CTA 0, of a sorted list: the sums of the weights up to each of the thread's two places 2 tid, 2 tid + 1
-    auto prefix = [&](int count, u64 (&sum)[2]) {
-      u64 w[2];
+    // In CTA 0, of a sorted list: the sums of the weights up to each of the thread's places, kPlaces tid and on
+    struct Sums {
+      u64 at[kPlaces];
+    };
+    auto prefix = [&](int count) {
+      Sums sum;
+      u64 inc = 0;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * tid + j;
-        w[j] = i < count ? weight_of(s, pow, value_of((uint32_t)(sorted[i] >> 32))) : 0ull;
+      for (int j = 0; j < kPlaces; ++j) {
+        const int i = kPlaces * tid + j;
+        inc += i < count ? weight_of(s, pow, value_of((uint32_t)(sorted[i] >> 32))) : 0ull;
+        sum.at[j] = inc;
       }
-      u64 inc = w[0] + w[1];
+      const u64 own = inc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -749,37 +758,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       __syncthreads();
       if (lane == 31) part64[warp] = inc;
       __syncthreads();
+      inc -= own;
 #pragma unroll
       for (int v = 0; v < kWarps; ++v)
         if (v < warp) inc += part64[v];
-      sum[0] = inc - w[1], sum[1] = inc;
+#pragma unroll
+      for (int j = 0; j < kPlaces; ++j) sum.at[j] += inc;
+      return sum;
     };
     // smallest place of a list's `count` at which base + its sum reaches `want` (count if none does): for CTA 0's threads
-    auto reach = [&](const u64 (&sum)[2], int count, u64 base, u64 want) {
+    auto reach = [&](const Sums& sum, int count, u64 base, u64 want) {
       int at = count;
 #pragma unroll
-      for (int j = 1; j >= 0; --j)
-        if (2 * tid + j < count && base + sum[j] >= want) at = 2 * tid + j;
+      for (int j = kPlaces - 1; j >= 0; --j)
+        if (kPlaces * tid + j < count && base + sum.at[j] >= want) at = kPlaces * tid + j;
       return cta_all(at, Min(), part32);
     };
-    auto sum_at = [&](const u64 (&sum)[2], int i) {  // the sum at place i, for all threads of CTA 0
+    auto sum_at = [&](const Sums& sum, int i) {  // the sum at place i, for all threads of CTA 0
       __syncthreads();
-      if (tid == i >> 1) row.result[0] = sum[i & 1];
+#pragma unroll
+      for (int j = 0; j < kPlaces; ++j)
+        if (kPlaces * tid + j == i) row.result[0] = sum.at[j];
       __syncthreads();
       return row.result[0];
     };
-
     // In CTA 0, the token of a list that begins with all that is kept (of the k first where `by_k`); false: it does not
     // (unless it is sure to), its tokens have too little of the mass for top-p
     auto draw = [&](int count, bool by_k, bool sure) {
-      u64 sum[2];
-      prefix(count, sum);
+      const Sums sum = prefix(count);
       int keep = by_k ? min(k, count) : count, pass = count;
       if (has_m) {
         pass = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          pass += 2 * tid + j < count && value_of((uint32_t)(sorted[2 * tid + j] >> 32)) >= least;
+        for (int j = 0; j < kPlaces; ++j)
+          pass += kPlaces * tid + j < count && value_of((uint32_t)(sorted[kPlaces * tid + j] >> 32)) >= least;
         pass = cta_all(pass, Add(), part32);
       }
       if (has_p) {
@@ -863,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         bound = fmaxf(least, -kMost);
       } else if (!every) {
         // The r-th largest of the warps' largest sampled logits: of 16 warps' samples together about the
-        // 16 (1 / 16 + .. + 1 / (17 - r))-th largest. A thread samples one quad.
+        // 16 (1 / 16 + .. + 1 / (17 - r))-th largest (and so with 32). A thread samples one quad.
         float best = -INFINITY, x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         const int i = quads > kThreads ? (int)((long long)tid * quads / kThreads) : tid;
         if (i < quads) {
@@ -876,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         __syncthreads();
         const float want = (float)(k ? max(160, 3 * k) : 300) / (float)cluster * (float)kThreads / (float)max(quads, kThreads);
         int r = 0;
-        for (float at = 0.f; r < kWarps && at < want; ++r) at += 16.f / (float)(kWarps - r);
+        for (float at = 0.f; r < kWarps && at < want; ++r) at += (float)kWarps / (float)(kWarps - r);
         r = max(r, 1);
         const float mine = partf[lane & (kWarps - 1)];
         int above = 0;
@@ -937,8 +949,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
           if (rank == 0) {
             count = collect();
             if (every) {  // (all weights, and k as if there were no more than that)
-              u64 sum[2];
-              prefix(count, sum);
+              const Sums sum = prefix(count);
               Z = sum_at(sum, count - 1);
             }
             ok = draw(count, k > 0, false);
@@ -995,8 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
         if (f.bin == kOver || f.count > kList) return search(which, want).sum;
         const int count = gather(f.bin, f.bin);
         if (rank == 0) {
-          u64 sum[2];
-          prefix(count, sum);
+          const Sums sum = prefix(count);
           int at = which ? reach(sum, count, f.mass, want) : (int)(want - f.n) - 1;
           at = min(max(at, 0), count - 1);
           const u64 z = f.mass + sum_at(sum, at);
@@ -1021,8 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int c
       } else {
         const int count = gather(f.bin, f.bin);
         if (rank == 0) {
-          u64 sum[2];
-          prefix(count, sum);
+          const Sums sum = prefix(count);
           const int at = min(reach(sum, count, f.mass, want), count - 1);
           token = (int)~(uint32_t)sorted[at];
           drawn = value_of((uint32_t)(sorted[at] >> 32));
@@ -1066,14 +1075,18 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream, bool pdl) {
   while (cluster > 1 && (long long)a.M * cluster > ctas(cluster)) cluster /= 2;
   bool held = (long long)a.M * cluster <= ctas(cluster);
   if (!held) cluster = most, held = cluster == 1 || !row_per_cta(a.M, a.V, cluster);
-  auto k = held ? sample_kernel<F32, true> : sample_kernel<F32, false>;
+  // Two CTAs an SM; where their rows together would not stay in L2, one of 1024 threads (512 rows of 151936 fp32 logits,
+  // top-k 50: 179 and 149 us; of 50021: 55 and 83).
+  const bool much = 2ll * sms * a.V * (F32 ? 4 : 2) > 96ll << 20;
+  const int threads = !held && much ? 1024 : 512;
+  auto k = held ? sample_kernel<F32, true, 512> : much ? sample_kernel<F32, false, 1024> : sample_kernel<F32, false, 512>;
   cudaError_t e = allow_max_smem(k);
   if (e != cudaSuccess) return e;
-  if (!held) return launch_kernel(k, dim3(a.M), dim3(kThreads), 4 * kBins * 4 + kBins * 12, stream, pdl, a, 1);
+  if (!held) return launch_kernel(k, dim3(a.M), dim3(threads), 4 * kBins * 4 + kBins * 12, stream, pdl, a, 1);
   const size_t smem = sample_smem(F32, a.V, cluster);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.M * cluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

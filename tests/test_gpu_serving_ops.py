@@ -509,7 +509,7 @@ def test_sample_strided_rows(q, V):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("M,V", [(130, 50021), (470, 8195), (240, 20001)])
+@pytest.mark.parametrize("M,V", [(130, 50021), (470, 8195), (240, 20001), (160, 90001)])
 def test_sample_many_rows(q, M, V, dtype):
     """More rows than are held at once; rows that begin anywhere; equal logits, masks and numbers that are none among them."""
     rng = np.random.default_rng(M)
