@@ -131,7 +131,7 @@ size_t up(size_t n) { return (n + 1023) / 1024 * 1024; }
 struct SharedLayout {
   size_t own_o, own_ml, pre_o, pre_ml, source, pieces, total;
 };
-// the prefix pass by attn_kv8_prefix.cu; its CTAs
+// heads that attn_kv8_prefix.cu takes; its CTAs
 bool prefix_tc_ok(int D) { return D <= 128; }
 int prefix_ctas() { return device_sm_count(); }
 SharedLayout layout(int T, int Hq, int Hkv, int D) {
@@ -157,7 +157,11 @@ cudaError_t launch_attn_kv8_shared(const AttnArgs& own, const AttnArgs& pre, int
   AttnArgs s = own, p = pre;
   s.part_o = reinterpret_cast<float*>(ws + l.own_o), s.part_ml = reinterpret_cast<float2*>(ws + l.own_ml);
   p.part_o = reinterpret_cast<float*>(ws + l.pre_o), p.part_ml = reinterpret_cast<float2*>(ws + l.pre_ml);
-  const bool tc = prefix_tc_ok(own.D);
+  // Up to 16 rows a group of a prefix that may be long, the warp-level kernel reads it at the copy rate, where that of
+  // attn_kv8_prefix.cu takes as long for 128 rows as for one. Measured, here and there (32/8 heads of 128): 16 rows, 600
+  // tokens 20.0 and 21.9 us, 4096 tokens 27.1 and 23.5, 65536 tokens 65 and 51; 32 rows, 65536 tokens 68 and 71, 64 rows 69
+  // and 113.
+  const bool tc = prefix_tc_ok(own.D) && !(attn_rows(pre) <= 16 && (long long)pre.max_blocks * pre.bs >= 2048);
   auto warp_level = [&](const AttnArgs& a) {
     return format == QG_KV_I8 ? launch_by_shape<QG_KV_I8, true>(a, stream, pdl)
                               : launch_by_shape<QG_KV_E4M3, true>(a, stream, pdl);
