@@ -724,8 +724,8 @@ QG_API size_t qg_attn_kv8_workspace_size(int Hq, int Hkv, int D);
  *   1 <= groups <= 1024; everything else as in attn_kv8_paged, its remarks on
  *   accuracy included; the partial results of prefix and own tokens join in fp32.
  *   workspace    qg_attn_kv8_shared_workspace_size(T, Hq, Hkv, D) bytes, 16-byte
- *                aligned, zero-filled before its first use: its counters (the
- *                first 4096 bytes) are left at zero by every call, the rest is
+ *                aligned, its first 4096 bytes zero-filled before its first use:
+ *                they are counters, left at zero by every call; the rest is
  *                scratch. Calls that may overlap need separate workspaces.
  * Three launches, capturable in a CUDA graph.
  */

@@ -142,8 +142,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_prefix_kernel(AttnArgs a
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   // The kernel before is the one over the requests' own tokens, of whose results nothing is read here: its CTAs all
-  // waited for what came before them (the cache, the lengths, the last call's joining), so this one need not wait for
-  // it but at its end, before the joining begins.
+  // waited for what came before them (the cache, the lengths, the last call's joining) before they let this one begin, so
+  // it need not wait for it but at its end, before the joining begins. What is read below was complete by then; the fence
+  // keeps loads from what an SM's L1 may hold of older contents.
+  __threadfence();
   pdl_launch_dependents();
   tc_before();
   const AttnBatch batch = attn_scan<kPrefixRows, PrefixCut, kThreads, true>(a, first, cost, cus, ctxs, scan_part);

@@ -175,8 +175,8 @@ class Outputs {
 // the graph's own memory: a graph may be replayed on any stream, next to eager
 // calls on the captured one, and outlives what is kept for those. (It is held
 // until the stream's next call that is not of that capture, so that one zero fill
-// serves all of the graph's calls.)
-at::Tensor zeroed_workspace(c10::Device dev, cudaStream_t st, const char* use, size_t bytes) {
+// serves all of the graph's calls.) Only its first `zeros` bytes are zeroed, all of them by default.
+at::Tensor zeroed_workspace(c10::Device dev, cudaStream_t st, const char* use, size_t bytes, size_t zeros = ~size_t{0}) {
   using Key = std::tuple<std::string, int, void*>;
   static auto* kept = new std::map<Key, at::Tensor>;  // both outlive the interpreter's end
   static auto* captured = new std::map<Key, std::pair<unsigned long long, at::Tensor>>;
@@ -189,7 +189,10 @@ at::Tensor zeroed_workspace(c10::Device dev, cudaStream_t st, const char* use, s
   }
   auto make = [&]() {
     c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(st, dev.index()));
-    return at::zeros({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(dev));
+    if (zeros >= bytes) return at::zeros({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(dev));
+    const at::Tensor ws = at::detail::empty_cuda({static_cast<int64_t>(bytes)}, at::kByte, dev, std::nullopt);
+    ws.narrow(0, 0, static_cast<int64_t>(zeros)).zero_();
+    return ws;
   };
   if (capturing != cudaStreamCaptureStatusNone) {
     auto it = captured->find(key);
@@ -204,9 +207,9 @@ at::Tensor zeroed_workspace(c10::Device dev, cudaStream_t st, const char* use, s
   return (*kept)[key] = make();
 }
 
-at::Tensor workspace(const Call& c, PyObject* given, const char* use, size_t bytes) {
+at::Tensor workspace(const Call& c, PyObject* given, const char* use, size_t bytes, size_t zeros = ~size_t{0}) {
   if (given == Py_None)
-    return bytes ? zeroed_workspace(c.dev, static_cast<cudaStream_t>(c.stream), use, bytes) : at::Tensor();
+    return bytes ? zeroed_workspace(c.dev, static_cast<cudaStream_t>(c.stream), use, bytes, zeros) : at::Tensor();
   const at::Tensor& t = *tensor(given, "workspace");
   c.dense(t, "workspace");
   return t;
@@ -378,7 +381,7 @@ PyObject* attention_shared(PyObject* const* a) {
   at::Tensor out = c.output(a[12], at::kBFloat16, {T, Hq, s.D}, "out");
   if (!out.defined()) out = c.make({T, Hq, s.D}, at::kBFloat16);
   const int hq = size32(Hq, "Hq"), t = size32(T, "T");
-  const at::Tensor ws = workspace(c, a[13], "attn_shared", qg_attn_kv8_shared_workspace_size(t, hq, s.Hkv, s.D));
+  const at::Tensor ws = workspace(c, a[13], "attn_shared", qg_attn_kv8_shared_workspace_size(t, hq, s.Hkv, s.D), 4096);
   c.done(attn_kv8_shared(ptr<uint16_t>(q), stride, ptr<void>(kc), ptr<void>(vc), ptr<float>(sc), ptr<int32_t>(ptable),
                          ptr<int32_t>(plens), ptr<int32_t>(cu_req), ptr<int32_t>(table), ptr<int32_t>(ctx),
                          ptr<int32_t>(cu), ptr<uint32_t>(tree), size32(G, "groups"), size32(R, "R"), t, hq, s.Hkv, s.D,

@@ -373,6 +373,19 @@ def test_shared_attention_strides_streams_and_capture(q):
         assert torch.equal(eager, want) and torch.equal(outs[0], want) and torch.equal(outs[1], want)
 
 
+def test_shared_attention_workspace(q):
+    """A given workspace of which only the counters are zeroed, used by calls of several sizes in turn."""
+    batches = [Shared(7 + i, "i8", [(n, r)], 0, 1, [3] * (r + 1), [1] * (r + 1), 8, 2, D, 32)
+               for i, (n, r, D) in enumerate(((500, 40, 128), (3000, 2, 128), (70, 5, 256), (900, 33, 64)))]
+    size = max(q.workspace_size(q.OP_ATTN_KV8_SHARED, M=8, N=2, K=b.D, T=b.q.shape[0]) for b in batches)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    ws[:4096] = 0
+    for _ in range(2):
+        for b in batches:
+            b.check(q.attn_kv8_shared(**b.args(), workspace=ws))
+            assert not ws[:4096].any()
+
+
 def test_shared_attention_reports(q):
     """Block ids outside the cache count as unseen; lengths past the table are cut; bounds that do not ascend write nothing."""
     b = Shared(5, "i8", [(300, 5)], 0, 1, [4] * 6, [1] * 6, 4, 2, 128, 16)
