@@ -39,6 +39,12 @@
  *    Residual addition and RMS norm in one pass, as the products' bf16 or int8
  *    activations (with the same randomized Hadamard transform).
  *
+ *  qk_norm_rope / attn_kv8_shared / sample_logits
+ *    The rest of a serving step: norms of queries and keys with the position
+ *    rotation, the attention of requests whose groups share a prefix of the
+ *    cache (read once for all of them), and the next token drawn from the
+ *    output head's logits.
+ *
  * Conventions shared by every entry point
  *  - Every array pointer is a DEVICE pointer (global memory of the current
  *    device). The caller allocates and owns all of them; the library never

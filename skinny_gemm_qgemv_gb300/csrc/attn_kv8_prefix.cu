@@ -22,6 +22,13 @@
 // values, 16 looks up blocks and scales, 17 issues the MMAs. Codes go from global memory through
 // registers to fp16 tiles: staged by TMA they would cross shared memory twice more
 // (64 of 320 KB a step, whose 128 bytes a cycle the MMAs' operands need).
+//
+// Measured (32/8 heads of 128, int8): 64 requests over 65529 shared tokens, own tokens and join included, 106 us (16.8
+// million scores a key/value head: 36 us at the library product's rate, 23 us for the bytes). A step of 256 rows and
+// 128 tokens takes some 4100 cycles: each stream's chain of scores from tensor memory, exponentials and P back to it
+// takes 2000, the MMAs of both 2900 in the tensor pipe's one order; it is busy for 24 % of a short run's cycles and the
+// softmax warps issue in 39 %. With up to 128 rows a step takes 2500. Beginning and end cost 15 us: first codes, blocks'
+// places and queries 6, results 3, the rest launch.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -17,6 +17,11 @@
 // position modulo 2^64: off by 2^-52 of the turns made (the rounding of
 // inv_freq / 2 pi), with no 64-bit floating-point instruction per token (GB300
 // issues two of those a cycle and SM).
+//
+// Measured (32/8 heads of 128): 16384 tokens of bf16 rows 66 us for 336 MB (5.1 TB/s; the bytes' floor is 50): 54 M warp
+// instructions, an issue in 70 % of the cycles, two thirds of them conversions, products and the rounding of elements.
+// 4093 fp32 tokens of 16/8 heads with three axes 20.4 us (84 MB), one token 4.2. Three CTAs an SM of 80 registers; the
+// next heads' loads are issued before the present ones are worked on (77 us without).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -20,6 +20,11 @@
 // in shared memory, and a deviation, below 2^-7.5 of the weight, keeps 2^-22 of it
 // there (a token's weight alone 2^-31). Distances from the maximum are formed
 // without error from two fp32.
+//
+// Measured (fp32 logits unless said): one row of 151936 14.5 us, 32 rows 21, each some twenty phases between barriers of
+// a cluster (latency: a warp waits 7 of 8 cycles, 5 of them for a barrier); 61 bf16 rows of 50021 without
+// top-k 45, which count all tokens and gather two bins; 512 rows of 151936 drawn from the whole softmax 251 (46
+// us for the bytes), 0.34 M warp instructions a row issued in 63 % of the cycles, four waves of rows.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -1069,7 +1074,7 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream, bool pdl) {
   // logits: clusters of 8, 4, 2, a CTA per row that reads it from L2: 48, 34, 21, 31 us; with 1024 threads a CTA 23)
   int cluster = most;
   auto ctas = [&](int c) {
-    const size_t bytes = sample_smem(F32, a.V, c) + 3072;
+    const size_t bytes = sample_smem(F32, a.V, c) + 3 * 1024;
     return bytes <= (size_t)device_max_smem_optin() && a.V / c <= 94000 ? sms : 0;
   };
   while (cluster > 1 && (long long)a.M * cluster > ctas(cluster)) cluster /= 2;
