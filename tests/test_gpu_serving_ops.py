@@ -155,6 +155,19 @@ def test_rope_at_zero_is_the_norm_and_turns_compose(q):
     assert (once - two).abs().max() <= 2.0 ** -16 * x.abs().max()  # three turns, 2^-19 of |u| + |v| each
 
 
+def test_rope_offsets_past_32_bits(q):
+    """Rows whose elements begin past 2^31: as the same tokens in a call of their own."""
+    T, Hq, D = 8300, 1024, 256
+    x = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=DEV)
+    x[:2], x[-3:] = 1.0, torch.randn((3, Hq, D), generator=gen(5)).to(DEV)
+    pos = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    pos[:2], pos[-3:] = 7, torch.tensor([0, 77, 12345], dtype=torch.int32, device=DEV)
+    f, w = freqs(D // 2).to(DEV), torch.ones(D, device=DEV)
+    a, b = q.qk_norm_rope(x, x, pos, f, q_weight=w)
+    c, d = q.qk_norm_rope(x[-3:], x[-3:], pos[-3:].clone(), f, q_weight=w)
+    assert torch.equal(a[-3:], c) and torch.equal(b[-3:], d)
+
+
 def test_rope_refusals(q):
     x, k = torch.zeros((3, 4, 64), device=DEV), torch.zeros((3, 2, 64), device=DEV)
     pos, f = torch.zeros(3, dtype=torch.int32, device=DEV), freqs(32).to(DEV)
@@ -384,6 +397,37 @@ def test_shared_attention_workspace(q):
         for b in batches:
             b.check(q.attn_kv8_shared(**b.args(), workspace=ws))
             assert not ws[:4096].any()
+
+
+@pytest.mark.parametrize("prefix,requests", [(700, 40), (2500, 3)])
+def test_shared_attention_far_blocks(q, prefix, requests):
+    """Blocks whose codes begin past 2^32, for either of the prefixes' kernels."""
+    n = requests + 1
+    b = Shared(12, "i8", [(prefix, requests)], 0, 1, [1 + i for i in range(n)], [1] * n, 8, 2, 128, 64)
+    a = b.args()
+    want = q.attn_kv8_shared(**a)
+    b.check(want)
+    nb, per = b.k.shape[1] if b.k.ndim == 5 else b.k.shape[0], 2 * 64 * 128
+    far = (1 << 32) // per + 5
+    big = {}
+    for name in ("k_cache", "v_cache"):
+        t = torch.empty((far + nb, 2, 64, 128), dtype=torch.int8, device=DEV)
+        t[far:] = a[name]
+        big[name] = t
+    scales = torch.zeros((far + nb, 2, 2), device=DEV)
+    scales[far:] = a["scales"]
+    move = lambda t: torch.where(t < 0, t, t + far)  # noqa: E731
+    got = q.attn_kv8_shared(**{**a, **big, "scales": scales, "prefix_table": move(a["prefix_table"]),
+                               "block_table": move(a["block_table"])})
+    assert torch.equal(got, want)
+
+
+def test_shared_attention_most_groups(q):
+    """1024 groups of a request each, every third one without a prefix, every fifth without a query."""
+    nq = [0 if i % 5 == 4 else 1 for i in range(1024)]
+    b = Shared(13, "e4m3", [(0 if i % 3 == 2 else 1 + i % 150, 1) for i in range(1024)], 0, 0, [1 + i % 20 for i in range(1024)],
+               nq, 4, 2, 128, 16)
+    b.check(q.attn_kv8_shared(**b.args()))
 
 
 def test_shared_attention_reports(q):
@@ -640,6 +684,22 @@ def test_sample_streams_and_capture(q):
         torch.cuda.synchronize()
         e, f = q.sample_logits(d, u, **kw)
         assert torch.equal(a, e) and torch.equal(b, f)
+
+
+def test_sample_offsets_past_32_bits(q):
+    """A row that begins past 2^32 bytes, of the cluster's form and of a CTA's."""
+    V = 50021
+    for M in (3, 300):
+        stride = (1 << 31) // (M - 1) + 7
+        whole = torch.empty((M - 1) * stride + V, dtype=torch.bfloat16, device=DEV)
+        x = whole.as_strided((M, V), (stride, 1))
+        rows = torch.randn((M, V), generator=gen(M)).mul(2).to(torch.bfloat16).to(DEV)
+        x.copy_(rows)
+        u = torch.rand(M, generator=gen(M + 1)).to(DEV)
+        for kw in ({}, dict(top_k=torch.full((M,), 40, dtype=torch.int32, device=DEV))):
+            a, b = q.sample_logits(x, u, **kw)
+            c, d = q.sample_logits(rows, u, **kw)
+            assert torch.equal(a, c) and torch.equal(b, d)
 
 
 def test_sample_refusals(q):
