@@ -45,9 +45,9 @@ constexpr float kFewScale = 90.f;      // their number per unit of a logit
 constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: leaves the nearest whole number in the low bits of a sum
 constexpr int kMaxCluster = 8;
 
-struct Found {  // a bin: the tokens and the weight before it, the tokens in it
+struct Found {  // a bin: the tokens and the weight before it, the tokens in it, the weight up to its end
   int bin, n, count, pad;
-  u64 mass;
+  u64 mass, after;
 };
 struct Row {  // what the CTAs of a cluster tell one another
   float max[kMaxCluster];
@@ -264,6 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
   u64* sorted = reinterpret_cast<u64*>(dev);
   __shared__ Row row;
   __shared__ u64 pow[2][64];
+  __shared__ __align__(16) u64 splitter[32];  // of a sort
+  __shared__ int part_size[33], part_begin[34];
+  __shared__ uint8_t part_of[kList];
   __shared__ u64 part64[kWarps];
   __shared__ int part32[kWarps];
   __shared__ float partf[kWarps], part_below[kWarps];
@@ -641,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         tell32(&f->n, r, (uint32_t)before_n[i]);
         tell32(&f->count, r, (uint32_t)(end_n(i) - before_n[i]));
         tell64(&f->mass, r, before_m[i]);
+        tell64(&f->after, r, end_m(i));
       }
     };
     // the bin in which the count (which 0) or the sum (1) reaches `want`; kOver where none of the inner ones does
@@ -653,7 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       }
       all_sync();
       Found f = row.found[search_turn];
-      if (want > (which ? inner_m() : (u64)inner_n())) f.bin = kOver, f.n = inner_n(), f.count = finite - f.n, f.mass = inner_m();
+      if (want > (which ? inner_m() : (u64)inner_n())) f.bin = kOver, f.n = inner_n(), f.count = finite - f.n, f.mass = inner_m(),
+        f.after = Z;
       return f;
     };
     auto of_bin = [&](int b) {
@@ -662,46 +667,73 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       all_sync();
       return row.found[search_turn];
     };
-    // `count` keys of sorted[] in descending order, equal ones in any (there are none): exchanges within 32 places by
-    // shuffles, wider ones in shared memory
-    auto sort = [&](int count) {
-      int width = 32;
-      while (width < count) width <<= 1;
-#pragma unroll 1
-      for (int i = count + tid; i < width; i += kThreads) sorted[i] = 0ull;
-      __syncthreads();
-      auto within = [&](int from, int to) {  // the steps of up to 16 places of the spans from .. to
-#pragma unroll 1
-        for (int i = tid; i < width; i += kThreads) {
-          u64 v = sorted[i];
-#pragma unroll 1
-          for (int span = from; span <= to; span <<= 1) {
-            const bool up = (i & span) == 0;
-#pragma unroll 1
-            for (int step = min(span >> 1, 16); step > 0; step >>= 1) {
-              const u64 q = __shfl_xor_sync(0xffffffffu, v, step);
-              v = ((i & step) == 0) == up ? max(v, q) : min(v, q);
-            }
-          }
-          sorted[i] = v;
-        }
-        __syncthreads();
-      };
-      within(2, 32);
-#pragma unroll 1
-      for (int span = 64; span <= width; span <<= 1) {
-#pragma unroll 1
-        for (int step = span >> 1; step >= 32; step >>= 1) {
-#pragma unroll 1
-          for (int i = tid; i < width / 2; i += kThreads) {
-            const int x = 2 * i - (i & (step - 1)), y = x + step;
-            const u64 p = sorted[x], q = sorted[y];
-            if ((p < q) == ((x & span) == 0)) sorted[x] = q, sorted[y] = p;
-          }
-          __syncthreads();
-        }
-        within(span, span);
+    // The first `count` of kList keys, place 32 (kPlaces warp + p) + lane of them in v[p], no two alike, into sorted[] in
+    // descending order: parted by up to 32 of them (a key's part: how many of those are above it), then each one's place is
+    // its part's beginning and the number of larger ones there. Whatever the parts are, the order is the same. (253 keys
+    // 3.0, 622 6.9 thousand cycles; by a bitonic network 5.3 and 10.3, and unrolled no less: code that runs once is slow.)
+    auto sort = [&](const u64 (&v)[kPlaces], int count) {
+      const float scale = fminf(32.f / (float)count, 1.f);
+      const int at = 32 * kPlaces * warp + lane;
+#pragma unroll
+      for (int p = 0; p < kPlaces; ++p) {
+        const int i = at + 32 * p, k = (int)((float)i * scale);
+        if (i < count && (i == 0 || (int)((float)(i - 1) * scale) < k)) splitter[k] = v[p];
       }
+      if (tid >= count && tid < 32) splitter[tid] = 0ull;
+      if (tid < 33) part_size[tid] = 0;
+      __syncthreads();
+      int part[kPlaces], nth[kPlaces];
+#pragma unroll
+      for (int p = 0; p < kPlaces; ++p) part[p] = 0;
+      if (at < count) {
+#pragma unroll 4
+        for (int k = 0; k < 32; k += 2) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(splitter + k);
+#pragma unroll
+          for (int p = 0; p < kPlaces; ++p) part[p] += (x.x > v[p]) + (x.y > v[p]);
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < kPlaces; ++p)
+        if (at + 32 * p < count) nth[p] = atomicAdd(part_size + part[p], 1);
+      __syncthreads();
+      int upto = part_size[lane];
+      const int own = upto;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (warp == 0) {
+        part_begin[lane] = upto - own;
+        if (lane == 31) part_begin[32] = upto, part_begin[33] = count;
+      }
+#pragma unroll
+      for (int p = 0; p < kPlaces; ++p) {
+        const int before = __shfl_sync(0xffffffffu, upto, max(part[p] - 1, 0));
+        if (at + 32 * p < count) {
+          const int to = nth[p] + (part[p] ? before : 0);
+          list[to] = v[p];
+          part_of[to] = (uint8_t)part[p];
+        }
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int i = tid; i < count; i += kThreads) {
+        const u64 key = list[i];
+        const int from = part_begin[part_of[i]], to = part_begin[part_of[i] + 1];
+        int place = from;
+#pragma unroll 1
+        for (int q = from; q < to; q += 4) {  // (a list's end is followed by sorted[])
+          u64 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = list[q + k];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) place += q + k < to && x[k] > key;
+        }
+        sorted[place] = key;
+      }
+      __syncthreads();
     };
     // the CTAs' lists, of which row.listed tells, sorted in CTA 0; their number
     auto collect = [&]() {
@@ -712,29 +744,31 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         ends[r] = count;
       }
       count = min(count, kList);
-#pragma unroll 1
-      for (int i = tid; i < count; i += kThreads) {  // all on the way at once
+      u64 v[kPlaces];
+#pragma unroll
+      for (int p = 0; p < kPlaces; ++p) {  // all on the way at once
+        const int i = 32 * (kPlaces * warp + p) + lane;
         int r = 0, begin = 0;
 #pragma unroll
         for (int q = 0; q < kMaxCluster - 1; ++q)
           if (i >= ends[q]) r = q + 1, begin = ends[q];
-        sorted[i] = ask64(list + i - begin, r);
+        v[p] = i < count ? ask64(list + i - begin, r) : 0ull;
       }
-      sort(count);
+      sort(v, count);
       return count;
     };
     auto put_in_list = [&](float x, int i, int j) {
       const int at = atomicAdd(&taken, 1);
       if (at < kList) list[at] = (u64)key_of(x) << 32 | (uint32_t)~index_of(i, j);
     };
-    // The tokens of bins lo .. hi, no more than kList of them, sorted in CTA 0: keys in descending order with
-    // the complement of the index below.
-    auto gather = [&](int lo, int hi) {
+    // The tokens of bins lo .. hi and of bin `too`, no more than kList of them, sorted in CTA 0: keys in descending order
+    // with the complement of the index below.
+    auto gather = [&](int lo, int hi, int too) {
       if (tid == 0) taken = 0;
       __syncthreads();
       sweep([&](float x, int i, int j) {
         const int b = bin_of(top - x, c_bin);
-        if (b >= lo && b <= hi && x > -INFINITY) put_in_list(x, i, j);
+        if (((b >= lo && b <= hi) || b == too) && x > -INFINITY) put_in_list(x, i, j);
       });
       __syncthreads();
       if (tid == 0) tell32(&row.listed[rank], 0, (uint32_t)min(taken, kList));
@@ -771,14 +805,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       for (int j = 0; j < kPlaces; ++j) sum.at[j] += inc;
       return sum;
     };
-    // smallest place of a list's `count` at which base + its sum reaches `want` (count if none does): for CTA 0's threads
-    auto reach = [&](const Sums& sum, int count, u64 base, u64 want) {
+    // smallest place from .. count - 1 of a list at which base + its sum reaches `want` (count if none does): for CTA 0's
+    // threads
+    auto reach_from = [&](const Sums& sum, int from, int count, u64 base, u64 want) {
       int at = count;
 #pragma unroll
       for (int j = kPlaces - 1; j >= 0; --j)
-        if (kPlaces * tid + j < count && base + sum.at[j] >= want) at = kPlaces * tid + j;
+        if (kPlaces * tid + j >= from && kPlaces * tid + j < count && base + sum.at[j] >= want) at = kPlaces * tid + j;
       return cta_all(at, Min(), part32);
     };
+    auto reach = [&](const Sums& sum, int count, u64 base, u64 want) { return reach_from(sum, 0, count, base, want); };
     auto sum_at = [&](const Sums& sum, int i) {  // the sum at place i, for all threads of CTA 0
       __syncthreads();
 #pragma unroll
@@ -930,26 +966,32 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       if (!hopeless) {
         if (tid == 0) taken = 0;
         __syncthreads();
-        float mass = 0.f;
+        float mass = 0.f, above = 0.f;
         const float c1 = -s.ch / (float)(64 << s.sj), c2 = -s.cl / (float)(64 << s.sj);
         const bool need_z = has_p && !k && !every;
         sweep([&](float x, int i, int j) {
           if (x >= bound) put_in_list(x, i, j);
           if (need_z) {
-            const float d = top - x;
-            mass += ex2(fmaxf(fmaf(d, c1, d * c2), -200.f));  // (of -infinity that sum is no number)
+            const float d = top - x, w = ex2(fmaxf(fmaf(d, c1, d * c2), -200.f));  // (of -infinity that sum is no number)
+            mass += w;
+            above += x >= bound ? w : 0.f;
           }
         });
         const u64 mine = need_z ? cta_all((u64)(mass * 8796093022208.f), Add(), part64) : 0ull;
+        const u64 listed = need_z ? cta_all((u64)(above * 8796093022208.f), Add(), part64) : 0ull;
         __syncthreads();
         if (tid < cluster) {
           tell32(&row.listed[rank], tid, (uint32_t)taken);
           tell64(&row.mass[rank], tid, mine);
+          tell64(&row.tail[rank], tid, listed);
         }
         all_sync();
         int count = 0;
-        for (int r = 0; r < cluster; ++r) count += row.listed[r], Z += row.mass[r];
-        if (count > 0 && count <= kList && (count >= k || every)) {
+        u64 in_list = 0;
+        for (int r = 0; r < cluster; ++r) count += row.listed[r], Z += row.mass[r], in_list += row.tail[r];
+        // (a list that ends before top-p and min_p do is not worth sorting)
+        const bool far = !need_z || (has_m && least >= bound) || in_list + (Z >> 10) >= share(p_share, Z);
+        if (far && count > 0 && count <= kList && (count >= k || every)) {
           bool ok = true;
           if (rank == 0) {
             count = collect();
@@ -971,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     }
 
     // ---- small cuts: all that may be kept in one list
-    Found kth = {};
+    Found kth = {}, pth = {};
     bool has_k = false;
     if (!done) {
     histogram();
@@ -988,8 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       last = kth.bin, upto = kth.n + kth.count;
     } else if (has_p) {
       // (a little further: the sums of the bins and of single tokens differ in their last digits)
-      const Found f = find(1, min(Z, max(1ull, share(p_share, Z) + (Z >> 20))));
-      last = f.bin, upto = f.n + f.count;
+      pth = find(1, min(Z, max(1ull, share(p_share, Z) + (Z >> 20))));
+      last = pth.bin, upto = pth.n + pth.count;
     }
     if (has_m && !(has_k && has_p)) {  // (top-p after top-k needs the k first)
       const int b = bin_of(top - fmaxf(least, -kMost), c_bin) + 1;
@@ -999,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       }
     }
     if (last != kOver && upto <= kList) {
-      const int count = gather(0, last);
+      const int count = gather(0, last, 0);
       if (rank == 0) draw(count, has_k, true);
       done = true;
     }
@@ -1009,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       drawn_of = Z;
       auto end_of = [&](int which, const Found& f, u64 want) {  // the sum at the place where it reaches `want`
         if (f.bin == kOver || f.count > kList) return search(which, want).sum;
-        const int count = gather(f.bin, f.bin);
+        const int count = gather(f.bin, f.bin, f.bin);
         if (rank == 0) {
           const Sums sum = prefix(count);
           int at = which ? reach(sum, count, f.mass, want) : (int)(want - f.n) - 1;
@@ -1023,23 +1065,46 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       if (has_k) drawn_of = end_of(0, kth, (u64)k);
       if (has_p) {
         const u64 want = max(1ull, share(p_share, drawn_of));
-        const Found f = find(1, want);
-        drawn_of = min(drawn_of, end_of(1, f, want));
+        const Found f = pth.mass < want && want <= pth.after ? pth : find(1, want);
+        // Wherever in its bin top-p ends, the draw ends in one bin or a few: they are gathered at once (a flat row of 50021
+        // bf16 logits one sweep and sort less: 61 of them 35 -> 28 us).
+        const bool at_once = !has_m && f.bin != kOver;
+        const u64 most = past(u, min(drawn_of, f.after + (Z >> 20)));
+        const Found d = at_once ? find(1, past(u, min(drawn_of, want))) : f,
+                    e = at_once && most > d.after ? find(1, most) : d;
+        const int ahead = e.bin < f.bin ? e.n + e.count - d.n : f.n - d.n;  // tokens listed before those of top-p's bin
+        if (at_once && d.bin <= f.bin && ahead + f.count <= kList) {
+          const int count = gather(d.bin, min(e.bin, f.bin), f.bin);
+          if (rank == 0) {
+            const Sums sum = prefix(count);
+            const u64 base = f.mass - (ahead ? sum_at(sum, ahead - 1) : 0ull);
+            const int end = min(reach_from(sum, ahead, count, base, want), count - 1);
+            drawn_of = min(drawn_of, base + sum_at(sum, end));
+            const int upto = e.bin < f.bin ? ahead : count, at = min(reach(sum, upto, d.mass, past(u, drawn_of)), upto - 1);
+            token = (int)~(uint32_t)sorted[at];
+            drawn = value_of((uint32_t)(sorted[at] >> 32));
+          }
+          done = true;
+        } else {
+          drawn_of = min(drawn_of, end_of(1, f, want));
+        }
       }
-      if (has_m) drawn_of = min(drawn_of, mass_from(key_of(fmaxf(least, -kMost))));
-      const u64 want = past(u, drawn_of);
-      const Found f = find(1, want);
-      if (f.bin == kOver || f.count > kList) {
-        const Place at = search(1, min(want, mass_from(key_of(-kMost))));
-        token = index_of_nth(at.key, at.nth);
-        drawn = value_of(at.key);
-      } else {
-        const int count = gather(f.bin, f.bin);
-        if (rank == 0) {
-          const Sums sum = prefix(count);
-          const int at = min(reach(sum, count, f.mass, want), count - 1);
-          token = (int)~(uint32_t)sorted[at];
-          drawn = value_of((uint32_t)(sorted[at] >> 32));
+      if (!done) {
+        if (has_m) drawn_of = min(drawn_of, mass_from(key_of(fmaxf(least, -kMost))));
+        const u64 want = past(u, drawn_of);
+        const Found f = find(1, want);
+        if (f.bin == kOver || f.count > kList) {
+          const Place at = search(1, min(want, mass_from(key_of(-kMost))));
+          token = index_of_nth(at.key, at.nth);
+          drawn = value_of(at.key);
+        } else {
+          const int count = gather(f.bin, f.bin, f.bin);
+          if (rank == 0) {
+            const Sums sum = prefix(count);
+            const int at = min(reach(sum, count, f.mass, want), count - 1);
+            token = (int)~(uint32_t)sorted[at];
+            drawn = value_of((uint32_t)(sorted[at] >> 32));
+          }
         }
       }
     }
@@ -1074,7 +1139,7 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream, bool pdl) {
   // logits: clusters of 8, 4, 2, a CTA per row that reads it from L2: 48, 34, 21, 31 us; with 1024 threads a CTA 23)
   int cluster = most;
   auto ctas = [&](int c) {
-    const size_t bytes = sample_smem(F32, a.V, c) + 3 * 1024;
+    const size_t bytes = sample_smem(F32, a.V, c) + 4 * 1024;
     return bytes <= (size_t)device_max_smem_optin() && a.V / c <= 94000 ? sms : 0;
   };
   while (cluster > 1 && (long long)a.M * cluster > ctas(cluster)) cluster /= 2;
