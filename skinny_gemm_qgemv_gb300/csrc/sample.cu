@@ -21,10 +21,11 @@
 // there (a token's weight alone 2^-31). Distances from the maximum are formed
 // without error from two fp32.
 //
-// Measured (fp32 logits unless said): one row of 151936 14.5 us, 32 rows 21, each some twenty phases between barriers of
-// a cluster (latency: a warp waits 7 of 8 cycles, 5 of them for a barrier); 61 bf16 rows of 50021 without
-// top-k 45, which count all tokens and gather two bins; 512 rows of 151936 drawn from the whole softmax 251 (46
-// us for the bytes), 0.34 M warp instructions a row issued in 63 % of the cycles, four waves of rows.
+// Measured (fp32 logits unless said): one row of 151936 13.5 us, 32 rows 18.6, each some twenty phases between barriers of
+// a cluster, of 500 to 5000 cycles (a warp issues in one of 18; code that runs once a row is slow to fetch too); 61 bf16
+// rows of 50021 without top-k 35, the slowest of which try a list, count all tokens and gather two bins; 512 rows of 151936
+// drawn from the whole softmax 249 (46 us for the bytes): four waves of rows, each 16 us for the maximum and 15 for the
+// list at the copy rate and 33 for the count, whose two shared atomics a token bound it.
 #include <cuda_runtime.h>
 
 #include <algorithm>
