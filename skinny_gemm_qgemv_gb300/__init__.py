@@ -643,7 +643,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     (first) position is negative are left out. Returns (q bf16, k in its own type,
     or k_out's: bf16 or fp32)."""
     if pair_axis is not None and not isinstance(pair_axis, bytes):
-        pair_axis = bytes(pair_axis)
+        pair_axis = bytes(list(pair_axis))  # (a number alone, or an array's memory, would pass as bytes too)
     return (_bind or _binding()).qk_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, pair_axis,
                                          q_out, k_out, stream)
 

@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import decode as od
 
@@ -108,3 +109,14 @@ def test_sample_refusals(L):
     for bad in (dict(dt=2), dict(stride=99), dict(M=0), dict(M=(1 << 20) + 1), dict(V=0), dict(kb=2)):
         assert call(**bad) == 1, bad
     assert call(V=393217, stride=393217) == 3
+
+
+def test_rope_pair_axis_is_a_sequence():
+    """A number alone is no list of axes; arrays of any whole type are."""
+    import skinny_gemm_qgemv_gb300 as q
+    x, pos, f = torch.zeros((3, 4, 64)), torch.zeros((2, 3), dtype=torch.int32), torch.ones(32, dtype=torch.float64)
+    with pytest.raises(TypeError):
+        q.qk_norm_rope(x, x, pos, f, pair_axis=32)
+    for axes in (np.zeros(32, np.int64), torch.zeros(32, dtype=torch.int64), [0] * 32):
+        with pytest.raises(ValueError, match="CUDA|cuda|device"):  # (as far as the tensors' place)
+            q.qk_norm_rope(x, x, pos, f, pair_axis=axes)
