@@ -14,12 +14,14 @@
 // sorted by one CTA. For cuts that keep a few hundred tokens a sample tells where
 // they begin, and nothing is counted.
 //
-// Sums are whole numbers, in units of 2^-43 of the largest weight, so no order of
-// atomics or of threads changes them. A bin's sum is its count times the weight of
-// its middle less the sum of its tokens' deviations from it: both are 32-bit atomics
-// in shared memory, and a deviation, below 2^-7.5 of the weight, keeps 2^-22 of it
-// there (a token's weight alone 2^-31). Distances from the maximum are formed
-// without error from two fp32.
+// Weights are whole numbers, in units of 2^-43 of the largest one: the weight of the
+// middle of the token's bin less its deviation from that, which is a multiple of a
+// power of two that the bin has (half of it is at most 2^-22 of the weight). A bin's
+// sum is then its count times its middle's weight less the sum of its tokens'
+// deviations, by 32-bit atomics in shared memory, and the same to the last digit as
+// the sum of its tokens' weights one by one: neither an order of atomics or threads
+// nor the way by which a row's token is found changes a result. Distances from the
+// maximum are formed without error from two fp32.
 //
 // Measured (fp32 logits unless said): one row of 151936 13.5 us, 32 rows 18.6, each some twenty phases between barriers of
 // a cluster, of 500 to 5000 cycles (a warp issues in one of 18; code that runs once a row is slow to fetch too); 61 bf16
@@ -142,6 +144,8 @@ struct Min {
 struct Scale {
   float max, ch, cl;  // ch + cl = S log2(e) / T
   float per;          // ln 2 / S
+  float inv;          // -1 / S
+  float end;          // bins from here on, 45 octaves down, weigh less than half a unit
   int sj;
 };
 __device__ __forceinline__ int bin_of(float a, float c) {
@@ -208,16 +212,32 @@ __device__ __forceinline__ u64 times(float f, u64 z, bool up) {
 __device__ __forceinline__ u64 mantissa(const u64 (*pow)[64], int b, int sj) {
   return __umul64hi(pow[0][b >> sj & 63], pow[1][(b & ((1 << sj) - 1)) << (6 - sj)]) << 1;
 }
-__device__ __forceinline__ u64 middle(const u64 (*pow)[64], int b, int sj) {
-  const int octave = b >> (6 + sj);
-  return octave > 63 ? 0ull : mantissa(pow, b, sj) >> octave;
+// The middle of bin b (a whole number) as fp32, units of 2^-43; and as the factor of a deviation in that bin's steps of
+// 2^shift units: from 2^(21 + sj) up to, but not, twice that where the middle is so large (deviations are then below 22780
+// steps, whatever sj), and the middle itself, with steps of a unit, where it is less.
+__device__ __forceinline__ float middle_f32(const Scale& s, float b) { return ex2(fmaf(b, s.inv, 43.f)); }
+__device__ __forceinline__ float steps_of(const Scale& s, float middle, int& shift) {
+  const uint32_t bits = __float_as_uint(middle), top = (uint32_t)(127 + 21 + s.sj) << 23, e = bits & 0x7F800000u;
+  const uint32_t over = e - min(e, top);
+  shift = (int)(over >> 23);
+  return __uint_as_float(bits - over);
+}
+// the middle in whole units: small ones from fp32, off by less than one unit
+__device__ __forceinline__ u64 middle_of(const u64 (*pow)[64], float middle, int b, int sj) {
+  if (middle < 2097152.f) return (u64)__float2uint_rn(middle);
+  return ((mantissa(pow, b, sj) >> (19 + (b >> (6 + sj)))) + 1) >> 1;
+}
+// steps by which x at distance a, of bin b and its factor, weighs less than the bin's middle
+__device__ __forceinline__ int steps_below(const Scale& s, float x, float a, float b, float factor) {
+  return __float_as_int(fmaf(deviation(s, x, a, b), factor, kMagic)) - 0x4B400000;
 }
 __device__ __forceinline__ u64 weight_of(const Scale& s, const u64 (*pow)[64], float x) {
   const float a = s.max - x, th = a * s.ch;
-  if (!(th < 1048576.f)) return 0ull;
-  const float bf = rintf(th);
-  const long long dev = (long long)(deviation(s, x, a, bf) * 17592186044416.f);  // 2^44
-  return __umul64hi(middle(pow, (int)bf, s.sj), (u64)((1ll << 44) - dev));
+  if (!(th < s.end)) return 0ull;
+  const float b = rintf(th), middle = middle_f32(s, b);
+  int shift;
+  const float factor = steps_of(s, middle, shift);
+  return middle_of(pow, middle, (int)b, s.sj) - (u64)(steps_below(s, x, a, b, factor) * (1ll << shift));
 }
 
 // weight_of / total as fp32, whatever the weight is
@@ -496,6 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     s.sj = sj;
     s.ch = step_of[0], s.cl = step_of[1];
     s.per = 0.69314718f / (float)(64 << s.sj);
+    s.inv = -1.f / (float)(64 << s.sj);
+    s.end = (float)(45 * 64 << s.sj);
     // x passes min_p from here on
     if (has_m) {
       if (tid == 0) least_at = __double2float_ru((double)top + least_of);
@@ -520,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       if (tid == 0) tail_of = 0;
       __syncthreads();
       int over = 0;
-      float tail = 0.f;
+      u64 tail = 0;
       if (few) {
         sweep([&](float x, int, int) {
           const int b = bin_of(top - x, c_bin);
@@ -530,22 +552,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
             over += x > -INFINITY;
         });
       } else {
-        const float unit = (float)(4194304 << s.sj), inv_s = -1.f / (float)(64 << s.sj);
         sweep([&](float x, int, int) {
           const float d = top - x, th = d * s.ch, bm = fminf(th, (float)kOver) + kMagic;
           const int b = __float_as_int(bm) & 0xFFF;
           if (b < kOver) {
-            const float q = fmaf(deviation(s, x, d, bm - kMagic), unit, kMagic);
+            int shift;
+            const float middle = bm - kMagic, factor = steps_of(s, middle_f32(s, middle), shift);
             atomicAdd(my_cnt + b, 1);
-            atomicAdd(my_dev + b, __float_as_int(q) - 0x4B400000);
+            atomicAdd(my_dev + b, steps_below(s, x, d, middle, factor));
           } else {
             over += x > -INFINITY;
-            tail += ex2(th * inv_s);
+            tail += weight_of(s, pow, x);
           }
         });
       }
       over = warp_all(over, Add());
-      const u64 tail_part = warp_all((u64)(tail * 8796093022208.f), Add());  // 2^43
+      const u64 tail_part = warp_all(tail, Add());
       if (lane == 0 && over) {
         atomicAdd(cnt + kOver, over);
         atomicAdd(&tail_of, tail_part);
@@ -575,8 +597,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
           break;
         }
         mine_n += count;
-        if (!few && count)
-          mine_m += __umul64hi(middle(pow, b, s.sj), ((u64)count << 44) - (u64)(deviate * (1ll << (22 - s.sj))));
+        if (!few && count) {
+          int shift;
+          const float middle = middle_f32(s, (float)b);
+          steps_of(s, middle, shift);
+          mine_m += (u64)count * middle_of(pow, middle, b, s.sj) - (u64)(deviate * (1ll << shift));
+        }
       }
       // exclusive sums over the threads
       if (b0 + per >= own_bins && b0 < own_bins && rank == cluster - 1)
@@ -1033,8 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     if (has_k) {
       last = kth.bin, upto = kth.n + kth.count;
     } else if (has_p) {
-      // (a little further: the sums of the bins and of single tokens differ in their last digits)
-      pth = find(1, min(Z, max(1ull, share(p_share, Z) + (Z >> 20))));
+      pth = find(1, max(1ull, share(p_share, Z)));
       last = pth.bin, upto = pth.n + pth.count;
     }
     if (has_m && !(has_k && has_p)) {  // (top-p after top-k needs the k first)
@@ -1073,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         // Wherever in its bin top-p ends, the draw ends in one bin or a few: they are gathered at once (a flat row of 50021
         // bf16 logits one sweep and sort less: 61 of them 35 -> 28 us).
         const bool at_once = !has_m && f.bin != kOver;
-        const u64 most = past(u, min(drawn_of, f.after + (Z >> 20)));
+        const u64 most = past(u, min(drawn_of, f.after));
         const Found d = at_once ? find(1, past(u, min(drawn_of, want))) : f,
                     e = at_once && most > d.after ? find(1, most) : d;
         const int ahead = e.bin < f.bin ? e.n + e.count - d.n : f.n - d.n;  // tokens listed before those of top-p's bin
@@ -1098,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         const u64 want = past(u, drawn_of);
         const Found f = find(1, want);
         if (f.bin == kOver || f.count > kList) {
-          const Place at = search(1, min(want, mass_from(key_of(-kMost))));
+          const Place at = search(1, want);
           token = index_of_nth(at.key, at.nth);
           drawn = value_of(at.key);
         } else {

@@ -56,6 +56,71 @@ class Ranked:
         assert ok, (u, p, token, prob, int(j), self.kept(p), self.order[min(self.kept(p), len(self.C)) - 1])
 
 
+def in_batches(q, x, row, settings, batches):
+    """Case i is row `row[i]` of x with the i-th settings; the cases in calls of M rows each, for all M of `batches`:
+    equal in all of them. Returns the first one's tokens and probabilities."""
+    d, row, n, first = x.to(DEV), torch.tensor(row), len(row), None
+    t = {k: torch.tensor(np.asarray(v), dtype=torch.int32 if k == "top_k" else torch.float32) for k, v in settings.items()}
+    for M in batches:
+        tokens, probs = [], []
+        for i in range(0, n, M):
+            at = torch.arange(i, i + M) % n
+            a, b = q.sample_logits(d[row[at].to(DEV)], **{k: v[at].to(DEV) for k, v in t.items()})
+            keep = min(M, n - i)
+            tokens.append(a[:keep].cpu().numpy()), probs.append(b[:keep].cpu().numpy())
+        got = np.concatenate(tokens), np.concatenate(probs)
+        first = first or got
+        assert np.array_equal(got[0], first[0]), (M, np.nonzero(got[0] != first[0])[0][:5])
+        assert np.array_equal(got[1].view(np.int32), first[1].view(np.int32)), \
+            (M, np.nonzero(got[1] != first[1])[0][:5], got[1][got[1] != first[1]][:3], first[1][got[1] != first[1]][:3])
+    return first
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("temperature,gap", [(8.0, 25.0), (64.0, 40.0), (3.9, 45.0)])
+def test_a_bulk_below_the_bins(q, dtype, temperature, gap):
+    """One token far above a bulk of one value, hot rows: most of the mass lies below the bins."""
+    V, x, rows = 151936, [], []
+    for i in range(4):
+        y = torch.full((V,), -gap - 0.37 * i).to(dtype)
+        y[77 + i] = 1.0
+        x.append(y)
+        rows.append(Ranked(y.float().numpy(), temperature))
+    row, u, p = [], [], []
+    for i in range(4):
+        for k, v in enumerate((1e-5, 0.3, 0.71, LAST_U)):
+            row.append(i), u.append(v), p.append((1.0, 0.9, 1 - 2.0 ** -22)[(i + k) % 3])
+    T = [temperature] * len(row)
+    tokens, probs = in_batches(q, torch.stack(x), row, dict(u=u, top_p=p, temperature=T), (16, 3, 32, 160))
+    for i in range(len(row)):
+        rows[row[i]].check(u[i], p[i], int(tokens[i]), float(probs[i]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [20001, 151936])
+def test_a_row_gives_the_same_in_every_batch(q, V, dtype):
+    """All settings; rows of few values, where cuts end among thousands of nearly equal tokens, among them."""
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy(rng.standard_normal((24, V)) * rng.choice([0.5, 2.0, 4.0], (24, 1)))
+    for i in range(0, 24, 3):
+        x[i] = (x[i] * 3).round() / 3 + 1e-4 * torch.from_numpy(rng.standard_normal(V))
+    x[1::4, rng.choice(V, 150, replace=False)] += 8
+    n = 192
+    settings = dict(u=rng.random(n), temperature=rng.choice([0.4, 0.8, 1.0, 1.7, 20.0], n),
+                    top_k=rng.choice([0, 0, 20, 300, 500, 3000], n), top_p=rng.choice([1.0, 0.5, 0.9, 0.99, 0.999], n),
+                    min_p=rng.choice([0.0, 0.0, 0.05, 1e-3], n))
+    row = [i % 24 for i in range(n)]
+    tokens, probs = in_batches(q, x.to(dtype), row, settings, (n, 1, 32, 100, 600))
+    f32 = x.to(dtype).float().numpy()
+    for i in range(0, n, 5):
+        own = {k: (int(v[i]) if k == "top_k" else np.float32(v[i])) for k, v in settings.items()}
+        u = own.pop("u")
+        order, C, kept, at = od.sample(f32[row[i]], u, **own)
+        if order[at] == tokens[i]:  # (borders within EPS are the other tests')
+            want = np.exp((float(f32[row[i]][order[at]]) - float(f32[row[i]][order[0]])) / float(own["temperature"])) / C[kept - 1]
+            assert abs(probs[i] - want) <= 2.0 ** -21 * want or own["top_p"] < 1, (i, own, probs[i], want)
+
+
 def test_temperatures_just_above_one(q):
     """A few tokens far above a broad bulk that has some of the mass: 22 logits below the maximum are within the bins at
     any temperature, and a temperature of 1.2 takes about as long as one of 0.99 (a row that ends below them takes twenty
