@@ -853,9 +853,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       __syncthreads();
       return row.result[0];
     };
-    // In CTA 0, the token of a list that begins with all that is kept (of the k first where `by_k`); false: it does not
-    // (unless it is sure to), its tokens have too little of the mass for top-p
-    auto draw = [&](int count, bool by_k, bool sure) {
+    // In CTA 0, the token of a list that begins with all that is kept (of the k first where `by_k`). Where Z is known but
+    // to `slack`, false unless top-p's end lies in the list and is the same for all that Z may be (or min_p's comes first).
+    auto draw = [&](int count, bool by_k, u64 slack) {
       const Sums sum = prefix(count);
       int keep = by_k ? min(k, count) : count, pass = count;
       if (has_m) {
@@ -866,9 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         pass = cta_all(pass, Add(), part32);
       }
       if (has_p) {
-        const u64 z = by_k ? sum_at(sum, keep - 1) : Z;
+        const u64 z = by_k ? sum_at(sum, keep - 1) : Z - slack;
         const int at = reach(sum, keep, 0, max(1ull, share(p_share, z)));
-        if (at == keep && !sure && !by_k && pass == count && sum_at(sum, count - 1) < Z - (Z >> 20)) return false;
+        if (slack && (pass == count || at < pass) && (at == count || sum_at(sum, at) < share(p_share, Z + slack))) return false;
         keep = min(keep, at + 1);
       }
       keep = min(keep, pass);
@@ -936,8 +936,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     };
 
     // ---- Short of counting all tokens: a bound below which a few hundred lie above is guessed from a sample, and what
-    // lies above it gathered, with the sum of all weights where top-p needs that. If what is kept proves to reach further
-    // (or the bound to be far off), the bins below decide.
+    // lies above it gathered, with about the sum of all weights where top-p needs that. If what is kept proves to reach
+    // further, if it would end elsewhere with a little more or less of that sum, or if the bound is far off, the bins below
+    // decide.
     const bool every = a.V <= kList;  // a list holds the whole row
     if (every || (k ? k <= kList / 2 : has_p || has_m)) {
       bool hopeless = false;
@@ -996,18 +997,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       if (!hopeless) {
         if (tid == 0) taken = 0;
         __syncthreads();
-        float mass = 0.f, above = 0.f;
+        u64 mass = 0;
+        float four = 0.f, above = 0.f;
         const float c1 = -s.ch / (float)(64 << s.sj), c2 = -s.cl / (float)(64 << s.sj);
         const bool need_z = has_p && !k && !every;
         sweep([&](float x, int i, int j) {
           if (x >= bound) put_in_list(x, i, j);
           if (need_z) {
             const float d = top - x, w = ex2(fmaxf(fmaf(d, c1, d * c2), -200.f));  // (of -infinity that sum is no number)
-            mass += w;
+            // (By fours as whole numbers: whatever the row, Z is off by less than 2^-18 of itself. w's exponent is rounded twice
+            // to 2^-24 of itself: a octaves below the maximum that is 2^-23.5 a of w, and what lies there weighs at most
+            // 2^(18.6 - a), so of Z it is 2^-19.7 at most; ex2 adds 2^-22, three additions 2^-22.4, units cut off 2^-25.)
+            four = j ? four + w : w;
+            if (j == 3) mass += (u64)(four * 8796093022208.f);  // 2^43
             above += x >= bound ? w : 0.f;
           }
         });
-        const u64 mine = need_z ? cta_all((u64)(mass * 8796093022208.f), Add(), part64) : 0ull;
+        const u64 mine = need_z ? cta_all(mass, Add(), part64) : 0ull;
         const u64 listed = need_z ? cta_all((u64)(above * 8796093022208.f), Add(), part64) : 0ull;
         __syncthreads();
         if (tid < cluster) {
@@ -1029,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
               const Sums sum = prefix(count);
               Z = sum_at(sum, count - 1);
             }
-            ok = draw(count, k > 0, false);
+            ok = draw(count, k > 0, need_z ? Z >> 18 : 0ull);
           }
           if (need_z) {
             if (tid < cluster && rank == 0) tell32(&row.done, tid, ok);
@@ -1071,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     }
     if (last != kOver && upto <= kList) {
       const int count = gather(0, last, 0);
-      if (rank == 0) draw(count, has_k, true);
+      if (rank == 0) draw(count, has_k, 0);
       done = true;
     }
     }

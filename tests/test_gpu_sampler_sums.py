@@ -77,6 +77,52 @@ def in_batches(q, x, row, settings, batches):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_top_p_over_a_bulk_of_one_value(q, dtype):
+    """700 tokens above a bulk that has about half of the mass; top-p ends among the first ones, next to a border."""
+    rng = np.random.default_rng(11)
+    V, x, rows = 151936, [], []
+    for i in range(12):
+        y = np.full(V, -5.2 - 0.11 * i)
+        y[rng.choice(V, 700, replace=False)] = 0.5 - rng.random(700) * 2.5
+        x.append(torch.from_numpy(y).to(dtype))
+        rows.append(Ranked(x[-1].float().numpy()))
+    row, u, p = [], [], []
+    for i, r in enumerate(rows):
+        for j, f in enumerate((-10, -5, -2.5, -1.25, 1.25, 2.5, 5, 10)):
+            n = 60 + 9 * j + i
+            while r.x[r.order[n]] == r.x[r.order[n - 1]] and n < 300:  # (bf16: to the end of equal ones)
+                n += 1
+            row.append(i), u.append(LAST_U), p.append(np.float32(r.C[n - 1] / r.C[-1] + f * EPS))
+    tokens, probs = in_batches(q, torch.stack(x), row, dict(u=u, top_p=p), (96, 8, 32, 512))
+    for i in range(len(row)):
+        rows[row[i]].check(u[i], p[i], int(tokens[i]), float(probs[i]))
+
+
+def test_top_p_near_one(q):
+    """250 tokens have all but 3.5 to 4 * 2^-22 of the mass, some hundred more a little, a bulk of one value the rest: what
+    the definition keeps of it is drawn."""
+    rng = np.random.default_rng(12)
+    V, x, rows = 50021, [], []
+    for i in range(6):
+        at = rng.permutation(V)
+        y = np.empty(V)
+        y[at[:250]] = -17 * rng.random(250)
+        y[at[0]] = 0.0
+        y[at[250:850]] = -20.5 - rng.random(600)
+        y[at[850:]] = np.log(np.exp(y[at[:250]]).sum() * (3.55 + 0.06 * i) * EPS / (V - 850))
+        x.append(torch.from_numpy(y).float())
+        rows.append(Ranked(x[-1].numpy()))
+    row, u, p = [], [], []
+    for i in range(6):
+        for top_p in (1 - 2.0 ** -24, 1 - 2.0 ** -23, 1 - 2.0 ** -22, 1 - 2.0 ** -21, 1 - 2.0 ** -20, 1 - 2.0 ** -18):
+            for v in (LAST_U, 1 - 2.0 ** -22, 0.5):
+                row.append(i), u.append(v), p.append(top_p)
+    tokens, probs = in_batches(q, torch.stack(x), row, dict(u=u, top_p=p), (108, 6, 32, 512))
+    for i in range(len(row)):
+        rows[row[i]].check(u[i], p[i], int(tokens[i]), float(probs[i]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("temperature,gap", [(8.0, 25.0), (64.0, 40.0), (3.9, 45.0)])
 def test_a_bulk_below_the_bins(q, dtype, temperature, gap):
     """One token far above a bulk of one value, hot rows: most of the mass lies below the bins."""
