@@ -167,6 +167,37 @@ def test_a_row_gives_the_same_in_every_batch(q, V, dtype):
             assert abs(probs[i] - want) <= 2.0 ** -21 * want or own["top_p"] < 1, (i, own, probs[i], want)
 
 
+@pytest.mark.parametrize("M,V,dtype", [
+    (160, 170001, torch.bfloat16), (160, 180000, torch.bfloat16), (160, 180000, torch.float32), (170, 180001, torch.bfloat16),
+    (48, 151936, torch.float32), (100, 151936, torch.float32), (139, 151936, torch.bfloat16), (64, 262147, torch.float32),
+    (21, 393216, torch.float32)])
+def test_launch_forms(q, M, V, dtype):
+    """Rows of one value; rows that all lie at one or the other end of one bin (the largest sums of deviations); masked
+    rows of fewer tokens than top-k; ordinary ones. Clusters in waves and CTAs per row, at the widest rows of each."""
+    rng = np.random.default_rng(M + V)
+    kinds = torch.empty((8, V), dtype=torch.float64)
+    kinds[0] = 1.25
+    kinds[1] = -(300 + 0.4998) / (64 * 1.4426950408889634)
+    kinds[2] = -(300 - 0.4998) / (64 * 1.4426950408889634)
+    kinds[1:3, 5] = 0.0
+    kinds[3] = float("-inf")
+    kinds[3, rng.choice(V, 7, replace=False)] = torch.from_numpy(rng.standard_normal(7))
+    kinds[4:] = torch.from_numpy(rng.standard_normal((4, V)) * 2)
+    kinds[5, rng.choice(V, 100, replace=False)] += 9
+    kinds = kinds.to(dtype)
+    u, p = rng.random(M), np.where(np.arange(M) // 8 % 2, 0.9, 1.0)
+    k = np.where(np.arange(M) % 8 == 3, 50, 0)
+    got = []
+    for top_k in (None, torch.from_numpy(k).to(DEV)):
+        a, b = q.sample_logits(kinds[torch.arange(M) % 8].to(DEV), torch.from_numpy(u).float().to(DEV), top_k=top_k,
+                               top_p=torch.from_numpy(p).float().to(DEV))
+        got.append((a.cpu().numpy(), b.cpu().numpy()))
+    assert all(np.array_equal(x, y) for x, y in zip(*got))
+    rows = [Ranked(y.float().numpy()) for y in kinds]
+    for m in list(range(min(M, 16))) + list(range(max(16, M - 16), M)):
+        rows[m % 8].check(u[m], p[m], int(got[0][0][m]), float(got[0][1][m]))
+
+
 def test_temperatures_just_above_one(q):
     """A few tokens far above a broad bulk that has some of the mass: 22 logits below the maximum are within the bins at
     any temperature, and a temperature of 1.2 takes about as long as one of 0.99 (a row that ends below them takes twenty
