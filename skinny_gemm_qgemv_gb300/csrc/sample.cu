@@ -375,11 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
   const float p_raw = a.top_p ? a.top_p[m] : 1.f, mp_raw = a.min_p ? a.min_p[m] : 0.f;
   const int k = k_raw > 0 && k_raw < a.V ? (int)k_raw : 0;   // 0: all
   const bool has_p = p_raw < 1.f, has_m = mp_raw > 0.f;
-  // The bins reach 22 T / 2^sj logits below the maximum, 22 at least (with T up to 2^sj they ended 11 below it for a T just
-  // above 1, and a row whose bulk has some of the mass there was searched by halving: 512 rows of 151936 at 0.6 to 1.2 with
-  // top-p 2.4 and 0.31 ms).
+  // The bins reach 22 T / 2^sj logits below the maximum: 22 at least, so that they hold the bulk below a high head too (with
+  // 11, 512 rows of 151936 at temperatures of 0.6 to 1.2 and top-p took 2.4 ms instead of 0.31, searched by halving). Where
+  // a bin of that width, 0.0108 T / 2^sj logits, would hold more tokens of a broad row than a list, they have half of it
+  // (152 broad rows of 262144 at a temperature of 1.4 0.86 and 0.26 ms).
   int sj = 0;
   while (sj < 6 && T >= (float)(2 << sj)) ++sj;
+  if (sj < 6 && T > (float)(1 << sj) && (float)a.V * T > 350000.f * (float)(1 << sj)) ++sj;
   // (by one warp: GB300 has two lanes an SM for 64-bit floating point)
   if (warp == 1 && !greedy) {
     const double c = 1.4426950408889634 * (64 << sj) / (double)T, at = has_m ? (double)T * log((double)fminf(mp_raw, 1.f)) : 0.;
