@@ -231,10 +231,15 @@ __device__ __forceinline__ u64 middle_of(const u64 (*pow)[64], float middle, int
 __device__ __forceinline__ int steps_below(const Scale& s, float x, float a, float b, float factor) {
   return __float_as_int(fmaf(deviation(s, x, a, b), factor, kMagic)) - 0x4B400000;
 }
+// The weight below the bins, th bins down. With S = 64 that is less than 2^11 units, and fp32 gives them to 2^-8 of one.
+__device__ __forceinline__ uint32_t weight_below(const Scale& s, float th) {
+  return __float_as_uint(ex2(fmaf(th, s.inv, 43.f)) + kMagic) - 0x4B400000u;
+}
 __device__ __forceinline__ u64 weight_of(const Scale& s, const u64 (*pow)[64], float x) {
   const float a = s.max - x, th = a * s.ch;
   if (!(th < s.end)) return 0ull;
   const float b = rintf(th), middle = middle_f32(s, b);
+  if (s.sj == 0 && b >= (float)kOver) return weight_below(s, th);
   int shift;
   const float factor = steps_of(s, middle, shift);
   return middle_of(pow, middle, (int)b, s.sj) - (u64)(steps_below(s, x, a, b, factor) * (1ll << shift));
@@ -544,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       if (tid == 0) tail_of = 0;
       __syncthreads();
       int over = 0;
+      uint32_t below = 0;
       u64 tail = 0;
       if (few) {
         sweep([&](float x, int, int) {
@@ -564,9 +570,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
             atomicAdd(my_dev + b, steps_below(s, x, d, middle, factor));
           } else {
             over += x > -INFINITY;
-            tail += weight_of(s, pow, x);
+            below += weight_below(s, th);
           }
         });
+        tail = below;
+        if (s.sj > 0 && over) {  // (apart: in the sweep, this code slowed it down where it does not run)
+          tail = 0;
+          sweep_slow([&](float x, int, int) {
+            if ((top - x) * s.ch > (float)kOver - 0.5f) tail += weight_of(s, pow, x);
+          });
+        }
       }
       over = warp_all(over, Add());
       const u64 tail_part = warp_all(tail, Add());
