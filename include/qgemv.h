@@ -797,7 +797,7 @@ QG_API qg_status rmsnorm_residual_i8(const void *x, int x_dtype, const void *res
  *   y = (x * rsqrt(mean(x^2) + eps)) * weight over a head's D elements, then a
  *   pair (u, v) by a = position * inv_freq: (u cos a - v sin a, v cos a +
  *   u sin a), all in fp32; the angle is reduced in 64 bits (off by less than
- *   2^-52 of itself before that).
+ *   2^-52 of itself and, at position p, |p| 2^-64 turns before that).
  *   q_out_bf16   bf16 [T][Hq][D], k_out [T][Hkv][D], bf16 or fp32 (k_out_dtype)
  *                (outputs), rounded to nearest even. fp32 keys go into
  *                kv8_append without a rounding on the way.
