@@ -42,8 +42,8 @@
  *  qk_norm_rope / attn_kv8_shared / sample_logits
  *    The rest of a serving step: norms of queries and keys with the position
  *    rotation, the attention of requests whose groups share a prefix of the
- *    cache (read once for all of them), and the next token drawn from the
- *    output head's logits.
+ *    cache (read for all of a group together), and the next token drawn from
+ *    the output head's logits.
  *
  * Conventions shared by every entry point
  *  - Every array pointer is a DEVICE pointer (global memory of the current
@@ -709,8 +709,13 @@ QG_API size_t qg_attn_kv8_workspace_size(int Hq, int Hkv, int D);
 /*
  * attn_kv8_shared -- attn_kv8_paged for a batch whose requests begin, in groups,
  * with the same tokens (a system prompt, a document that several answers are
- * drawn about): a group's prefix lies in the cache once and is read once for all
- * of the group's query tokens.
+ * drawn about): a group's prefix lies in the cache once and is read for all of the
+ * group's rows (query tokens times the query heads of a key/value head) together:
+ * heads of up to 128 once per 256 rows; heads above 128 once per 16 rows, and
+ * others too where the batch has at most 16 rows a group on average (T / groups
+ * query tokens, those without a prefix counted in) and the prefix table holds
+ * 2048 tokens and more. A request's own tokens are read once per 16 of its rows
+ * (attn_kv8_paged may read them once per 64).
  *
  *   cu_req       int32 [groups + 1]: group g's requests are cu_req[g] ..
  *                cu_req[g+1] - 1 (none is allowed); 0 <= cu_req <= R, ascending
@@ -732,7 +737,8 @@ QG_API size_t qg_attn_kv8_workspace_size(int Hq, int Hkv, int D);
  *   workspace    qg_attn_kv8_shared_workspace_size(T, Hq, Hkv, D) bytes, 16-byte
  *                aligned, its first 4096 bytes zero-filled before its first use:
  *                they are counters, left at zero by every call; the rest is
- *                scratch. Calls that may overlap need separate workspaces.
+ *                scratch: up to 8 D + 24 bytes for each of T * Hq rows, and some
+ *                MB. Calls that may overlap need separate workspaces.
  * Three launches, capturable in a CUDA graph.
  */
 QG_API qg_status attn_kv8_shared(const uint16_t *q_bf16, int64_t q_stride, const void *k_cache,

@@ -610,8 +610,10 @@ def attn_kv8_shared(q, k_cache, v_cache, scales, prefix_table, prefix_lens, cu_r
     outside all groups have no prefix) see the prefix_lens[g] tokens of
     prefix_table[g] (int32 [groups][max_prefix_blocks]) before their own;
     block_table, ctx_lens, cu_q and tree_mask are of their own tokens alone. A
-    prefix is read once for all of its group. The workspace is kept per (device,
-    stream) and grows with T; a stream capture has one of its own."""
+    prefix is read for all of its group together. The workspace is kept per (device,
+    stream) and grows to the largest T (8 D + 24 bytes for each of T * Hq rows: 0.55 GB
+    for 16384 tokens of 32 heads of 128), unless one is given; a stream capture has
+    one of its own."""
     return (_bind or _binding()).attention_shared(q, k_cache, v_cache, scales, prefix_table, prefix_lens, cu_req,
                                                   block_table, ctx_lens, cu_q, tree_mask, softmax_scale, out, workspace,
                                                   stream)

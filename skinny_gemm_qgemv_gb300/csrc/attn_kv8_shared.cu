@@ -4,14 +4,17 @@
 // request's own tokens S join as
 //   m = max(m_P, m_S), out = (2^(m_P - m) l_P o_P + 2^(m_S - m) l_S o_S) /
 //                            (2^(m_P - m) l_P + 2^(m_S - m) l_S),
-// so the prefix is read once for all query rows of its group instead of once per
-// request. Three launches: every request over its own tokens, every group over its
+// so the prefix is read for all query rows of its group together instead of once
+// per request. Three launches: every request over its own tokens, every group over its
 // prefix (no mask: all of it is seen), both leaving a row's maximum, sum and fp32
 // output in the workspace, and the joining.
 //
 // Measured (32/8 heads of 128): four requests of up to 37 own tokens over 600 shared ones 19 us, 34 of up to 1024 over
-// 8200 43 us, 64 of up to 300 over 65529 106 us, of which the own tokens' pass takes 14 to 22 (as attn_kv8_paged would)
-// and the joining 6 to 8; the prefix's kernel begins while the own tokens' one ends.
+// 8200 43 us, 64 of up to 300 over 65529 106 us, of which the own tokens' pass takes 14 to 22
+// and the joining 6 to 8; the prefix's kernel begins while the own tokens' one ends. The own tokens always go to the
+// warp-level kernel, a pass per 16 rows: more rows a request over many own tokens take longer than by attn_kv8_paged, whose
+// tcgen05 kernel leaves no partial results (64 requests of eight drafts, 8 heads a group, up to 1000 own tokens over 8192
+// shared ones 319 us; attn_kv8_paged over the own tokens alone 71).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -161,7 +164,8 @@ cudaError_t launch_attn_kv8_shared(const AttnArgs& own, const AttnArgs& pre, int
   AttnArgs s = own, p = pre;
   s.part_o = reinterpret_cast<float*>(ws + l.own_o), s.part_ml = reinterpret_cast<float2*>(ws + l.own_ml);
   p.part_o = reinterpret_cast<float*>(ws + l.pre_o), p.part_ml = reinterpret_cast<float2*>(ws + l.pre_ml);
-  // Up to 16 rows a group of a prefix that may be long, the warp-level kernel reads it at the copy rate, where that of
+  // Up to 16 rows a group, on the average of the batch (the groups' own rows are known to the GPU alone; a group of 64 beside
+  // 19 of one, two heads a group, goes to the warp-level kernel with the others), of a prefix that may be long, the warp-level kernel reads it at the copy rate, where that of
   // attn_kv8_prefix.cu takes as long for 128 rows as for one. Measured, here and there (32/8 heads of 128): 16 rows, 600
   // tokens 20.0 and 21.9 us, 4096 tokens 27.1 and 23.5, 65536 tokens 65 and 51; 32 rows, 65536 tokens 68 and 71, 64 rows 69
   // and 113.
