@@ -821,7 +821,7 @@ QG_API qg_status qk_norm_rope(const void *q, int64_t q_stride, const void *k, in
  * qgemm_w4a16_skinny), drawn with a given random number.
  *
  *   logits       [M][V], bf16 or fp32 (dtype), row m at element m * stride (>= V;
- *                any, rows need not be aligned). NaN counts as -infinity, which
+ *                any: rows after the first need not be aligned). NaN counts as -infinity, which
  *                is never drawn, +infinity as the type's largest number.
  *   u            fp32 [M]: uniform in [0, 1) (below 0 and NaN count as 0, 1 and
  *                above as the largest number below 1).
@@ -842,12 +842,15 @@ QG_API qg_status qk_norm_rope(const void *q, int64_t q_stride, const void *k, in
  *   probs        fp32 [M] (output) or NULL: w_i / C, with which it was drawn; 0 for
  *                token -1.
  *   1 <= M <= 2^20, 1 <= V <= QG_SAMPLE_MAX_V (more: QG_ERR_UNSUPPORTED).
- * Weights and their sums are whole numbers of 2^-43 of the largest weight, each
- * weight to 2^-23 of itself or better: results do not depend on any order of
- * summation, and differ from the definition's where u C or top_p C_k lies within
- * 2^-22 C of a sum C_i. Rows whose cuts end, or whose draw falls, among more than
- * 1024 tokens of nearly equal logits take ten times as long. One launch, no
- * workspace; capturable in a CUDA graph.
+ * Weights are whole numbers of 2^-43 of the largest one, each to 2^-22 of itself or
+ * to 2^-43, and so are their sums: a row's token and probability depend on neither
+ * an order of summation nor the other rows of the call, the probability is off by
+ * less than 2^-21 of itself, and the token differs from the definition's only where
+ * u C or top_p C_k lies within 2^-22 C of a sum C_i. Rows whose cuts end, or whose
+ * draw falls, among more than 1024 tokens of nearly equal logits, or at temperatures
+ * above 1 more than 22 logits below the largest (with V above 175000 at some
+ * temperatures 11), take ten to fifty times as long. One launch, no workspace;
+ * capturable in a CUDA graph.
  */
 #define QG_SAMPLE_MAX_V 393216
 QG_API qg_status sample_logits(const void *logits, int dtype, int64_t stride, int M, int V, const float *u,

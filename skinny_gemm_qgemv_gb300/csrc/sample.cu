@@ -23,11 +23,12 @@
 // nor the way by which a row's token is found changes a result. Distances from the
 // maximum are formed without error from two fp32.
 //
-// Measured (fp32 logits unless said): one row of 151936 13.5 us, 32 rows 18.6, each some twenty phases between barriers of
+// Measured (fp32 logits unless said): one row of 151936 13 us, 32 rows 18 to 20, each some twenty phases between barriers of
 // a cluster, of 500 to 5000 cycles (a warp issues in one of 18; code that runs once a row is slow to fetch too); 61 bf16
-// rows of 50021 without top-k 35, the slowest of which try a list, count all tokens and gather two bins; 512 rows of 151936
-// drawn from the whole softmax 249 (46 us for the bytes): four waves of rows, each 16 us for the maximum and 15 for the
-// list at the copy rate and 33 for the count, whose two shared atomics a token bound it.
+// rows of 50021 without top-k 34 to 36, the slowest of which try a list, count all tokens and gather two bins; 512 rows of
+// 151936 drawn from the whole softmax 250 (46 us for the bytes): four waves of rows, each 16 us for the maximum and 15 for
+// the list at the copy rate and 33 for the count, whose two shared atomics a token bound it. Rows that are searched by
+// halving: one of equal logits 0.4 ms, 152 of them 2.5.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -1116,8 +1117,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
       if (has_p) {
         const u64 want = max(1ull, share(p_share, drawn_of));
         const Found f = pth.mass < want && want <= pth.after ? pth : find(1, want);
-        // Wherever in its bin top-p ends, the draw ends in one bin or a few: they are gathered at once (a flat row of 50021
-        // bf16 logits one sweep and sort less: 61 of them 35 -> 28 us).
+        // Wherever in its bin top-p ends, the draw ends in one bin or a few: they are gathered at once (a sweep and a sort
+        // less).
         const bool at_once = !has_m && f.bin != kOver;
         const u64 most = past(u, min(drawn_of, f.after));
         const Found d = at_once ? find(1, past(u, min(drawn_of, want))) : f,
@@ -1171,8 +1172,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
 
 // Where a CTA per row pays: the clusters' rows follow one another through the SMs, 2 SMs / cluster at a time and some 20 us
 // each, mostly waiting for their own barriers; a CTA per row takes 8 us and 0.43 ns a logit, but the GPU holds two an SM.
-// Clusters and CTAs, plain softmax: 76 rows of 20001 logits 27.3 and 17.7 us, of 50021 47.8 and 30.9, of 151936 63.4 and
-// 71.8; 152 rows of 151936 110 and 72, 512 rows 344 and 254. (The counts of one of the two copies of the bins stay below
+// Clusters of 8 and CTAs of 512 threads, plain softmax, fp32: 76 rows of 20001 logits 46.5 and 20.5 us, of 50021 50.8 and
+// 32.9, of 151936 65.5 and 72.1; 128 rows of 151936 98.7 and 72.6, 152 rows 113 and 73, 512 rows 354 and 252. (The counts of one of the two copies of the bins stay below
 // 2^31 / 22780 = 94270, that a bin's deviations fit 32 bits.)
 bool row_per_cta(long long M, int V, int cluster) {
   return V <= 180000 && 152 * M * cluster > (long long)device_sm_count() * (120 + V / 154);
@@ -1186,7 +1187,7 @@ template <bool F32>
 cudaError_t launch(const SampleArgs& a, cudaStream_t stream, bool pdl) {
   const int sms = device_sm_count(), most = a.V <= 8192 ? 1 : a.V <= 16384 ? 2 : a.V <= 32768 ? 4 : 8;
   // the largest cluster with which all rows are held at once, a CTA an SM, if there is one (plain softmax, 76 rows of 50021
-  // logits: clusters of 8, 4, 2, a CTA per row that reads it from L2: 48, 34, 21, 31 us; with 1024 threads a CTA 23)
+  // logits: clusters of 8, 4, 2, a CTA per row that reads it from L2: 51, 35, 22, 33 us; with 1024 threads a CTA 30)
   int cluster = most;
   auto ctas = [&](int c) {
     const size_t bytes = sample_smem(F32, a.V, c) + 4 * 1024;
@@ -1195,8 +1196,9 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream, bool pdl) {
   while (cluster > 1 && (long long)a.M * cluster > ctas(cluster)) cluster /= 2;
   bool held = (long long)a.M * cluster <= ctas(cluster);
   if (!held) cluster = most, held = cluster == 1 || !row_per_cta(a.M, a.V, cluster);
-  // Two CTAs an SM; where their rows together would not stay in L2, one of 1024 threads (512 rows of 151936 fp32 logits,
-  // top-k 50: 179 and 149 us; of 50021: 55 and 83).
+  // Two CTAs an SM; where their rows together would not stay in L2, one of 1024 threads (512 rows of 50021 fp32 logits:
+  // two of 512 threads an SM 90.6 us, one of 1024 118; 76 rows of 151936 72.1 and 59.6, 152 rows 72.9 and 63.5, 512 rows
+  // 252 and 253, with top-k 50 152 rows 76.8 and 33.7).
   const bool much = 2ll * sms * a.V * (F32 ? 4 : 2) > 96ll << 20;
   const int threads = !held && much ? 1024 : 512;
   auto k = held ? sample_kernel<F32, true, 512> : much ? sample_kernel<F32, false, 1024> : sample_kernel<F32, false, 512>;
