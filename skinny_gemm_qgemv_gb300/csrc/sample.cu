@@ -1173,8 +1173,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
 // Where a CTA per row pays: the clusters' rows follow one another through the SMs, 2 SMs / cluster at a time and some 20 us
 // each, mostly waiting for their own barriers; a CTA per row takes 8 us and 0.43 ns a logit, but the GPU holds two an SM.
 // Clusters of 8 and CTAs of 512 threads, plain softmax, fp32: 76 rows of 20001 logits 46.5 and 20.5 us, of 50021 50.8 and
-// 32.9, of 151936 65.5 and 72.1; 128 rows of 151936 98.7 and 72.6, 152 rows 113 and 73, 512 rows 354 and 252. (The counts of one of the two copies of the bins stay below
-// 2^31 / 22780 = 94270, that a bin's deviations fit 32 bits.)
+// 32.9, of 151936 65.5 and 72.1; 128 rows of 151936 98.7 and 72.6, 152 rows 113 and 73, 512 rows 354 and 252. (The counts
+// of one of the two copies of the bins stay below 2^31 / 22780 = 94270, that a bin's deviations fit 32 bits.)
 bool row_per_cta(long long M, int V, int cluster) {
   return V <= 180000 && 152 * M * cluster > (long long)device_sm_count() * (120 + V / 154);
 }
