@@ -847,10 +847,11 @@ QG_API qg_status qk_norm_rope(const void *q, int64_t q_stride, const void *k, in
  * an order of summation nor the other rows of the call, the probability is off by
  * less than 2^-21 of itself, and the token differs from the definition's only where
  * u C or top_p C_k lies within 2^-22 C of a sum C_i. Rows whose cuts end, or whose
- * draw falls, among more than 1024 tokens of nearly equal logits, or at temperatures
- * above 1 more than 22 logits below the largest (with V above 175000 at some
- * temperatures 11), take ten to fifty times as long. One launch, no workspace;
- * capturable in a CUDA graph.
+ * draw falls, among more than 1024 tokens of nearly equal logits or far below the
+ * largest one take ten to fifty times as long: below 22 logits (at temperatures up
+ * to 1, 22 times the temperature, where hardly any weight is; with V above 175000 at
+ * some temperatures above 1, 11). One launch, no workspace; capturable in a CUDA
+ * graph.
  */
 #define QG_SAMPLE_MAX_V 393216
 QG_API qg_status sample_logits(const void *logits, int dtype, int64_t stride, int M, int V, const float *u,
